@@ -506,6 +506,88 @@ int32_t lora_grad_x(const void *dY, const void *W, const uint8_t *keep_mask, int
 int32_t lora_transpose(const void *src, void *dst, int32_t rows, int32_t cols, int32_t dtype,
                        void *stream);
 
+/* ---------------------------------------------------- 8-bit base weight
+ * The layer over a frozen base weight held in 8-bit floating point: half the
+ * bytes of the decode stream, twice the matrix rate of a prefill, and the
+ * backward over the same weight ([S-LoRA] 批处理: the base product is shared
+ * by the batch and frozen; [LoRAFusion] 解决什么真问题: only A and B train.
+ * The pages do not give an 8-bit form).
+ * Codes are OCP e4m3 (4 exponent bits, 3 mantissa bits, largest value 448),
+ * with one power-of-two scale per block: 128 consecutive columns of a row of
+ * X or dY, a 128 x 128 block of W (so the codes of W and W^T are the same).
+ * For a block whose largest magnitude is amax:
+ *   e     = the smallest integer >= -126 with amax <= 448 . 2^e
+ *   code  = x . 2^-e rounded once to e4m3 (nearest even, subnormals kept)
+ *   scale = the byte e + 127; a code stands for its value times 2^e
+ * A block that holds an infinity or a NaN has scale byte 255 and NaN codes:
+ * every result it enters is NaN.  The last block of a row (or column) covers
+ * what is left of it; codes past the end are zero.
+ * Layout: a row of d codes is lora_quantised_row_bytes(d) bytes (d rounded up
+ * to 128), a row of scales lora_quantised_scale_bytes(d) bytes (ceil(d / 128)
+ * rounded up to 4, zeros past the last block).  Buffers 16-byte aligned. */
+typedef struct {
+  int32_t d_in, d_out;
+  uint8_t *q_t;               /* [d_out][row_bytes(d_in)]  codes of W_t           */
+  uint8_t *scale;             /* [ceil(d_out/128)][scale_bytes(d_in)]             */
+  uint8_t *q;                 /* [d_in][row_bytes(d_out)]  codes of W, or NULL    */
+  uint8_t *scale_t;           /* [ceil(d_in/128)][scale_bytes(d_out)], or NULL    */
+} lora_quantised_weight;      /* host struct, device pointers; q and scale_t are
+                                 needed by lora_grad_x_quantised only            */
+int64_t lora_quantised_row_bytes(int32_t d);
+int64_t lora_quantised_scale_bytes(int32_t d);
+/* Rows of X [T][d] (dtype) into codes and scales of the row layout above.
+ * Errors: INVALID_ARG (null, aliasing, T < 0 or above 2^20, bad dtype),
+ * UNSUPPORTED (d not a multiple of 64), DEVICE. */
+int32_t lora_quantise_rows(const void *X, int32_t dtype, int32_t T, int32_t d, uint8_t *codes,
+                           uint8_t *scale, void *stream);
+/* W_t [d_out][d_in] (dtype, nn.Linear layout) into w's buffers, both
+ * orientations when q and scale_t are given (both or neither).  Once per
+ * frozen weight, and again after a merge.
+ * Errors: INVALID_ARG (null, aliasing, bad dtype), UNSUPPORTED (widths not
+ * multiples of 64), DEVICE. */
+int32_t lora_quantise_weight(const void *W_t, int32_t dtype, const lora_quantised_weight *w,
+                             void *stream);
+/* lora_apply over a quantised weight: with X^ the rows of X quantised by the
+ * call and W^ the weight's values,
+ *   Y[t][n] = round( sum_i X^[t][i].W^[n][i] + sum_{p of t} sum_j U[u_off[p]+j].B_a[j][n] )
+ * and U as in lora_apply, from X itself: the LoRA branch is not quantised.
+ * Arguments as for lora_apply, W in place of W_t; the pool's dtype is that of
+ * X and Y.  bf16 layers sum on the scaled 8-bit MFMA, whose alignment inside
+ * one instruction costs up to about 6e-5 of the result's norm; fp32 layers
+ * sum the same codes with fp32 accuracy on the bf16 MFMA.
+ *   ws >= lora_apply_quantised_workspace_bytes(...); U stays in it where
+ *   lora_apply_u_offset says, so that lora_grad takes (ws, ws_bytes) as its
+ *   apply workspace.
+ * Rows without an active slot equal the base product alone.
+ * Errors: those of lora_apply, INVALID_ARG when W's widths are not the pool's. */
+size_t lora_apply_quantised_workspace_bytes(int32_t T, int32_t K, int32_t d_in, int32_t d_out,
+                                            int32_t max_rank, int32_t dtype);
+int32_t lora_apply_quantised(const void *X, const lora_quantised_weight *W, void *Y, int32_t T,
+                             int32_t K, const float *gates, const uint8_t *keep_mask,
+                             float keep_scale, const lora_pool_desc *pool, const void *plan, void *ws,
+                             size_t ws_bytes, void *stream);
+/* lora_plan then lora_apply_quantised for one batch, as one call (plan, U and
+ * Y as those two give them, bit for bit).  Arguments as for lora_forward. */
+int32_t lora_forward_quantised(const int32_t *ids, const float *gates, int32_t T, int32_t K,
+                               const void *X, const lora_quantised_weight *W, void *Y,
+                               const uint8_t *keep_mask, float keep_scale,
+                               const lora_pool_desc *pool, void *plan, size_t plan_bytes, void *ws,
+                               size_t ws_bytes, void *stream);
+/* lora_grad_x over the quantised weight: with dY^ the rows of dY quantised by
+ * the call (128 columns of d_out per scale) and W^ the same values the forward
+ * used,
+ *   dX[t][i] = round( sum_n dY^[t][n].W^[n][i] + m[t][i] . sum_{p of t} sum_j G[u_off[p]+j].A_a[i][j] )
+ * Arguments as for lora_grad_x, W (its q and scale_t) in place of the
+ * transposed weight.  ws >= lora_grad_x_quantised_workspace_bytes(...).
+ * Errors: those of lora_grad_x, INVALID_ARG when W has no q or scale_t or its
+ * widths are not the pool's. */
+size_t lora_grad_x_quantised_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out, int32_t dtype);
+int32_t lora_grad_x_quantised(const void *dY, const lora_quantised_weight *W,
+                              const uint8_t *keep_mask, int32_t T, int32_t K,
+                              const lora_pool_desc *pool, const void *plan, const void *grad_ws,
+                              size_t grad_ws_bytes, int32_t max_rank, void *dX, void *ws,
+                              size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

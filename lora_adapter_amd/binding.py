@@ -37,6 +37,9 @@ EXPORTS = (
     "lora_residency_destroy", "lora_residency_prepare", "lora_residency_finish",
     "lora_residency_stats", "lora_residency_page_table", "lora_tsqr_workspace_bytes", "lora_tsqr",
     "lora_compress_workspace_bytes", "lora_compress",
+    "lora_quantised_row_bytes", "lora_quantised_scale_bytes", "lora_quantise_rows",
+    "lora_quantise_weight", "lora_apply_quantised_workspace_bytes", "lora_apply_quantised",
+    "lora_forward_quantised", "lora_grad_x_quantised_workspace_bytes", "lora_grad_x_quantised",
 )
 
 
@@ -64,6 +67,11 @@ class PageCopy(ctypes.Structure):
                 ("count", ctypes.c_int32)]
 
 
+class QuantisedWeightDesc(ctypes.Structure):
+    _fields_ = [("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32), ("q_t", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("q", ctypes.c_void_p), ("scale_t", ctypes.c_void_p)]
+
+
 class ResidencyConfig(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32),
                 ("n_adapters", ctypes.c_int32), ("n_pages", ctypes.c_int64),
@@ -77,6 +85,7 @@ class ResidencyConfig(ctypes.Structure):
 _lib = None
 _I32, _I64, _SZ, _VP, _F32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float
 _PD = ctypes.POINTER(PoolDesc)
+_QW = ctypes.POINTER(QuantisedWeightDesc)
 
 _PROTOS = {
     "lora_abi_version": (_I32, []),
@@ -130,6 +139,17 @@ _PROTOS = {
     "lora_compress_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32]),
     "lora_compress": (_I32, [_PD, _VP, _I32, _I32, _I32, _F32, _F32, _I32, _VP, _VP, _VP, _VP, _VP,
                              _SZ, _VP]),
+    "lora_quantised_row_bytes": (_I64, [_I32]),
+    "lora_quantised_scale_bytes": (_I64, [_I32]),
+    "lora_quantise_rows": (_I32, [_VP, _I32, _I32, _I32, _VP, _VP, _VP]),
+    "lora_quantise_weight": (_I32, [_VP, _I32, _QW, _VP]),
+    "lora_apply_quantised_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32]),
+    "lora_apply_quantised": (_I32, [_VP, _QW, _VP, _I32, _I32, _VP, _VP, _F32, _PD, _VP, _VP, _SZ, _VP]),
+    "lora_forward_quantised": (_I32, [_VP, _VP, _I32, _I32, _VP, _QW, _VP, _VP, _F32, _PD, _VP, _SZ,
+                                      _VP, _SZ, _VP]),
+    "lora_grad_x_quantised_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32]),
+    "lora_grad_x_quantised": (_I32, [_VP, _QW, _VP, _I32, _I32, _PD, _VP, _VP, _SZ, _I32, _VP, _VP,
+                                     _SZ, _VP]),
 }
 
 
@@ -492,4 +512,85 @@ def lora_compress(pool: Pool, adapters, M: int, n: int, policy: int, ratio: floa
     _check("lora_compress", lib().lora_compress(
         pool.ref, _ptr(adapters), M, n, policy, float(ratio), float(energy), floor_rank,
         _ptr(out_a), _ptr(out_b), _ptr(out_rank), _ptr(out_sigma), _ptr(ws),
+        ws.numel() * ws.element_size(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- 8-bit base weight
+
+def lora_quantised_row_bytes(d: int) -> int:
+    return int(lib().lora_quantised_row_bytes(d))
+
+
+def lora_quantised_scale_bytes(d: int) -> int:
+    return int(lib().lora_quantised_scale_bytes(d))
+
+
+class QuantisedWeight:
+    """Device tensors of one weight's e4m3 codes and scale bytes (layouts in
+    include/lora.h) and the matching C descriptor.  `q` and `scale_t` (the
+    codes of W for the input gradient) may be None."""
+
+    def __init__(self, d_out: int, d_in: int, q_t, scale, q=None, scale_t=None):
+        rb, sb, nb = lora_quantised_row_bytes, lora_quantised_scale_bytes, lambda d: (d + 127) // 128
+        for t, rows, row in ((q_t, d_out, rb(d_in)), (scale, nb(d_out), sb(d_in)),
+                             (q, d_in, rb(d_out)), (scale_t, nb(d_in), sb(d_out))):
+            if t is not None and (tuple(t.shape) != (rows, row) or t.element_size() != 1
+                                  or not t.is_contiguous()):
+                raise ValueError(f"expected a contiguous 1-byte tensor [{rows}][{row}], got {tuple(t.shape)}")
+        self.d_out, self.d_in = d_out, d_in
+        self.q_t, self.scale, self.q, self.scale_t = q_t, scale, q, scale_t
+        self.desc = QuantisedWeightDesc(d_in, d_out, _ptr(q_t), _ptr(scale), _ptr(q), _ptr(scale_t))
+
+    @classmethod
+    def empty(cls, d_out: int, d_in: int, device="cuda", both: bool = True):
+        """Unfilled buffers for lora_quantise_weight (`both`: W too)."""
+        import torch
+        rb, sb, nb = lora_quantised_row_bytes, lora_quantised_scale_bytes, lambda d: (d + 127) // 128
+        e = lambda *s: torch.empty(s, dtype=torch.uint8, device=device)
+        return cls(d_out, d_in, e(d_out, rb(d_in)), e(nb(d_out), sb(d_in)),
+                   e(d_in, rb(d_out)) if both else None, e(nb(d_in), sb(d_out)) if both else None)
+
+    @property
+    def ref(self):
+        return ctypes.byref(self.desc)
+
+
+def lora_quantise_rows(X, dtype: int, T: int, d: int, codes, scale, stream=None):
+    _check("lora_quantise_rows", lib().lora_quantise_rows(_ptr(X), dtype, T, d, _ptr(codes),
+                                                          _ptr(scale), _stream(stream)))
+
+
+def lora_quantise_weight(W_t, dtype: int, w: QuantisedWeight, stream=None):
+    _check("lora_quantise_weight", lib().lora_quantise_weight(_ptr(W_t), dtype, w.ref, _stream(stream)))
+
+
+def lora_apply_quantised_workspace_bytes(T: int, K: int, d_in: int, d_out: int, max_rank: int,
+                                         dtype: int) -> int:
+    return int(lib().lora_apply_quantised_workspace_bytes(T, K, d_in, d_out, max_rank, dtype))
+
+
+def lora_apply_quantised(X, W: QuantisedWeight, Y, T: int, K: int, gates, keep_mask,
+                         keep_scale: float, pool: Pool, plan, ws, stream=None):
+    _check("lora_apply_quantised", lib().lora_apply_quantised(
+        _ptr(X), W.ref, _ptr(Y), T, K, _ptr(gates), _ptr(keep_mask), float(keep_scale), pool.ref,
+        _ptr(plan), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def lora_forward_quantised(ids, gates, T: int, K: int, X, W: QuantisedWeight, Y, keep_mask,
+                           keep_scale: float, pool: Pool, plan, ws, stream=None):
+    _check("lora_forward_quantised", lib().lora_forward_quantised(
+        _ptr(ids), _ptr(gates), T, K, _ptr(X), W.ref, _ptr(Y), _ptr(keep_mask), float(keep_scale),
+        pool.ref, _ptr(plan), plan.numel() * plan.element_size(), _ptr(ws),
+        ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def lora_grad_x_quantised_workspace_bytes(T: int, d_in: int, d_out: int, dtype: int) -> int:
+    return int(lib().lora_grad_x_quantised_workspace_bytes(T, d_in, d_out, dtype))
+
+
+def lora_grad_x_quantised(dY, W: QuantisedWeight, keep_mask, T: int, K: int, pool: Pool, plan,
+                          grad_ws, max_rank: int, dX, ws, stream=None):
+    _check("lora_grad_x_quantised", lib().lora_grad_x_quantised(
+        _ptr(dY), W.ref, _ptr(keep_mask), T, K, pool.ref, _ptr(plan), _ptr(grad_ws),
+        grad_ws.numel() * grad_ws.element_size(), int(max_rank), _ptr(dX), _ptr(ws),
         ws.numel() * ws.element_size(), _stream(stream)))

@@ -3,6 +3,7 @@
 #include <string.h>
 
 #include "lora_internal.h"
+#include "quantise.h"
 
 using namespace lora;
 
@@ -678,6 +679,204 @@ int32_t lora_compress(const lora_pool_desc *pool, const int32_t *adapters, int32
   if (ws_bytes < lora_compress_workspace_bytes(M, pool->d_in, pool->d_out, n)) return LORA_ERR_CAPACITY;
   return dev(launch_compress(pool_view(pool), adapters, M, n, policy, ratio, energy, floor_rank,
                              out_a, out_b, out_rank, out_sigma, ws, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------ 8-bit base weight
+
+namespace {
+
+int32_t check_weight(const lora_quantised_weight *w, const lora_pool_desc *pool) {
+  if (!w) return LORA_ERR_INVALID_ARG;
+  if (w->d_in != pool->d_in || w->d_out != pool->d_out) return LORA_ERR_INVALID_ARG;
+  return LORA_OK;
+}
+
+// A quantised GEMM's buffers at the end of a workspace: fp32 partials, then
+// (tile forms) the rows' codes and scale bytes.
+struct QuantTail {
+  GemmConfig cfg;
+  size_t partial, codes, scales, total;     // bytes
+};
+
+QuantTail quant_tail(int32_t T, int32_t d_k, int32_t d_n, int32_t dtype) {
+  QuantTail t{};
+  t.cfg = choose_quantised_gemm(T > 0 ? T : 1, d_k, d_n, dtype);
+  t.partial = align_up(gemm_partial_bytes(t.cfg, T, d_n));
+  if (t.cfg.kind != 4) {
+    t.codes = align_up(size_t(T) * size_t(q_row_bytes(d_k)));
+    t.scales = align_up(size_t(T) * size_t(q_scale_bytes(d_k)));
+  }
+  t.total = t.partial + t.codes + t.scales;
+  return t;
+}
+
+// Rows [T][d_k] times the weight's codes [d_n][..] in two or one launches
+// (quantise the rows, GEMM); `tail` the tail's memory.
+hipError_t run_quantised(const QuantTail &t, const void *rows, int32_t T, int32_t d_k, int32_t d_n,
+                         const uint8_t *codes, const uint8_t *scale, int32_t dtype, char *tail,
+                         QGemmArgs &q, hipStream_t s) {
+  q.g.X = rows; q.g.W = codes; q.g.M = T; q.g.N = d_n; q.g.Kd = d_k;
+  q.g.k_split = t.cfg.k_split; q.g.sk_g = t.cfg.sk;
+  q.g.partial = reinterpret_cast<float *>(tail);
+  q.lda = q.ldb = q_row_bytes(d_k);
+  q.lsa = q.lsb = q_scale_bytes(d_k);
+  q.sb = scale;
+  if (t.cfg.kind != 4) {
+    uint8_t *c = reinterpret_cast<uint8_t *>(tail) + t.partial, *sc = c + t.codes;
+    const hipError_t e = launch_quantise_rows(rows, dtype, T, d_k, c, sc, s);
+    if (e != hipSuccess) return e;
+    q.g.X = c;
+    q.sa = sc;
+  }
+  return launch_quantised_gemm(t.cfg, q, dtype, s);
+}
+
+// The checks of the quantised apply, and its workspace: the head is laid out
+// as lora_apply's (lora_grad finds U in it), the tail ends where the workspace
+// does, so that its place needs no max_rank.
+struct QuantApply {
+  QuantTail t;
+  ApplyWs w;
+  QGemmArgs q;
+  char *tail;
+};
+
+int32_t quant_apply_args(const void *X, const lora_quantised_weight *W, void *Y, int32_t T,
+                         int32_t K, const float *gates, const lora_pool_desc *pool,
+                         const void *plan, void *ws, size_t ws_bytes, QuantApply &a) {
+  int32_t st = check_batch(T, K);
+  if (st != LORA_OK) return st;
+  if ((st = check_pool(pool, true)) != LORA_OK) return st;
+  if ((st = check_weight(W, pool)) != LORA_OK) return st;
+  if (!plan) return LORA_ERR_INVALID_ARG;
+  if (T == 0) return LORA_OK;
+  if (!X || !Y || !W->q_t || !W->scale || !gates || !ws || Y == X) return LORA_ERR_INVALID_ARG;
+  a.t = quant_tail(T, pool->d_in, pool->d_out, pool->dtype);
+  if (ws_bytes < a.t.total) return LORA_ERR_CAPACITY;
+  const size_t head = (ws_bytes - a.t.total) / kAlign * kAlign;
+  GemmConfig base;
+  a.q = QGemmArgs{};
+  if ((st = base_args(X, W->q_t, Y, T, K, pool, plan, ws, head, base, a.q.g)) != LORA_OK) return st;
+  a.w = apply_layout(ws, head, T, K, pool->d_in, pool->d_out, pool->dtype);
+  a.tail = static_cast<char *>(ws) + head;
+  return LORA_OK;
+}
+
+// The epilogue counts stream-K units in K tiles of 64: one per 128 codes here.
+GemmArgs quant_epilogue_args(const QGemmArgs &q) {
+  GemmArgs g = q.g;
+  g.Kd = int(q.ldb) / kQBlock * 64;
+  return g;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t lora_quantised_row_bytes(int32_t d) { return d > 0 ? q_row_bytes(d) : 0; }
+int64_t lora_quantised_scale_bytes(int32_t d) { return d > 0 ? q_scale_bytes(d) : 0; }
+
+int32_t lora_quantise_rows(const void *X, int32_t dtype, int32_t T, int32_t d, uint8_t *codes,
+                           uint8_t *scale, void *stream) {
+  if (dtype != LORA_F32 && dtype != LORA_BF16) return LORA_ERR_INVALID_ARG;
+  if (T < 0 || T > kMaxPairs) return LORA_ERR_INVALID_ARG;
+  if (!dims_ok(d)) return LORA_ERR_UNSUPPORTED;
+  if (T == 0) return LORA_OK;
+  if (!X || !codes || !scale || X == codes || X == scale || codes == scale) return LORA_ERR_INVALID_ARG;
+  return dev(launch_quantise_rows(X, dtype, T, d, codes, scale, static_cast<hipStream_t>(stream)));
+}
+
+int32_t lora_quantise_weight(const void *W_t, int32_t dtype, const lora_quantised_weight *w,
+                             void *stream) {
+  if (dtype != LORA_F32 && dtype != LORA_BF16) return LORA_ERR_INVALID_ARG;
+  if (!W_t || !w || !w->q_t || !w->scale || (w->q == nullptr) != (w->scale_t == nullptr))
+    return LORA_ERR_INVALID_ARG;
+  if (!dims_ok(w->d_in) || !dims_ok(w->d_out)) return LORA_ERR_UNSUPPORTED;
+  if (W_t == w->q_t || W_t == w->q || w->q == w->q_t) return LORA_ERR_INVALID_ARG;
+  return dev(launch_quantise_weight(W_t, dtype, w->d_out, w->d_in, w->q_t, w->q, w->scale, w->scale_t,
+                                    static_cast<hipStream_t>(stream)));
+}
+
+size_t lora_apply_quantised_workspace_bytes(int32_t T, int32_t K, int32_t d_in, int32_t d_out,
+                                            int32_t max_rank, int32_t dtype) {
+  const size_t head = lora_apply_workspace_bytes(T, K, d_in, d_out, max_rank, dtype);
+  return head ? align_up(head) + quant_tail(T, d_in, d_out, dtype).total : 0;
+}
+
+int32_t lora_apply_quantised(const void *X, const lora_quantised_weight *W, void *Y, int32_t T,
+                             int32_t K, const float *gates, const uint8_t *keep_mask,
+                             float keep_scale, const lora_pool_desc *pool, const void *plan, void *ws,
+                             size_t ws_bytes, void *stream) {
+  QuantApply a;
+  const int32_t st = quant_apply_args(X, W, Y, T, K, gates, pool, plan, ws, ws_bytes, a);
+  if (st != LORA_OK || T == 0) return st;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const int64_t TK = int64_t(T) * K;
+  const PlanView pv = plan_view(plan, TK, pool->n_adapters);
+  hipError_t e = launch_shrink(apply_shrink_args(X, keep_mask, keep_scale, T, K, gates, pool, pv, a.w),
+                               pool->dtype, TK, pool->n_adapters, pool->d_in, pool->d_out, s);
+  if (e == hipSuccess)
+    e = run_quantised(a.t, X, T, pool->d_in, pool->d_out, W->q_t, W->scale, pool->dtype, a.tail, a.q, s);
+  if (e == hipSuccess) e = launch_epilogue(a.t.cfg, quant_epilogue_args(a.q), pool->dtype, s);
+  return dev(e);
+}
+
+int32_t lora_forward_quantised(const int32_t *ids, const float *gates, int32_t T, int32_t K,
+                               const void *X, const lora_quantised_weight *W, void *Y,
+                               const uint8_t *keep_mask, float keep_scale,
+                               const lora_pool_desc *pool, void *plan, size_t plan_bytes, void *ws,
+                               size_t ws_bytes, void *stream) {
+  QuantApply a;
+  int32_t st = quant_apply_args(X, W, Y, T, K, gates, pool, plan, ws, ws_bytes, a);
+  if (st != LORA_OK) return st;
+  if ((st = lora_plan(ids, gates, T, K, pool, plan, plan_bytes, stream)) != LORA_OK) return st;
+  return lora_apply_quantised(X, W, Y, T, K, gates, keep_mask, keep_scale, pool, plan, ws, ws_bytes,
+                              stream);
+}
+
+size_t lora_grad_x_quantised_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out, int32_t dtype) {
+  if (T < 0 || T > kMaxPairs || !dims_ok(d_in) || !dims_ok(d_out)) return 0;
+  if (dtype != LORA_F32 && dtype != LORA_BF16) return 0;
+  const size_t n = quant_tail(T, d_out, d_in, dtype).total;
+  return n > 0 ? n : kAlign;
+}
+
+int32_t lora_grad_x_quantised(const void *dY, const lora_quantised_weight *W,
+                              const uint8_t *keep_mask, int32_t T, int32_t K,
+                              const lora_pool_desc *pool, const void *plan, const void *grad_ws,
+                              size_t grad_ws_bytes, int32_t max_rank, void *dX, void *ws,
+                              size_t ws_bytes, void *stream) {
+  int32_t st = check_batch(T, K);
+  if (st != LORA_OK) return st;
+  if ((st = check_pool(pool, true)) != LORA_OK) return st;
+  if ((st = check_weight(W, pool)) != LORA_OK) return st;
+  if (!plan || max_rank < 1 || max_rank > LORA_MAX_RANK) return LORA_ERR_INVALID_ARG;
+  if (T == 0) return LORA_OK;
+  if (!dY || !W->q || !W->scale_t || !grad_ws || !dX || !ws || dX == dY) return LORA_ERR_INVALID_ARG;
+  if (grad_ws_bytes < lora_grad_workspace_bytes(T, K, pool->n_adapters, pool->d_in, pool->d_out,
+                                                max_rank, pool->dtype))
+    return LORA_ERR_CAPACITY;
+  const QuantTail t = quant_tail(T, pool->d_out, pool->d_in, pool->dtype);
+  if (ws_bytes < t.total) return LORA_ERR_CAPACITY;
+  const int64_t TK = int64_t(T) * K;
+  const PlanView pv = plan_view(plan, TK, pool->n_adapters);
+  QGemmArgs q{};
+  q.g.Y = dX;
+  // the expand on G and the A pages, as in lora_grad_x
+  q.g.ex.K = K;
+  q.g.ex.slot_desc = pv.slot_desc; q.g.ex.pair_tk = pv.pair_tk; q.g.ex.page_ids = pool->page_ids;
+  q.g.ex.b_pages = pool->a_pages; q.g.ex.d_out = pool->d_in;
+  q.g.ex.U = static_cast<const float *>(grad_ws); q.g.ex.hdr = pv.hdr;
+  q.g.ex.u_cap = TK * max_rank;
+  if (t.cfg.fused) q.g.mask = keep_mask;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = run_quantised(t, dY, T, pool->d_out, pool->d_in, W->q, W->scale_t, pool->dtype,
+                               static_cast<char *>(ws), q, s);
+  if (e == hipSuccess && !t.cfg.fused)
+    e = launch_grad_x_epilogue(t.cfg, quant_epilogue_args(q), pool->dtype, keep_mask, s);
+  return dev(e);
 }
 
 }  // extern "C"

@@ -1,0 +1,466 @@
+// The multi-adapter layer's products over e4m3 operands with one power-of-two
+// scale per 128 of K (and, for the weight, per 128 x 128 block):
+//   Y[t][n] = round( sum_b 2^(ex[t][b] + ew[n/128][b]) sum_{k in b} qx[t][k] qw[n][k] + expand )
+// and the input gradient, the same product of the quantised dY rows with the
+// codes of W^T.
+//
+// The scaled MFMA (v_mfma_scale_f32_32x32x64_f8f6f4, exponent bytes as its
+// scale operands) multiplies at twice the bf16 rate and applies both scales
+// itself, so one fp32 accumulator runs over the whole of K and no wave spends
+// an instruction on scaling.  Inside one instruction the products are aligned
+// to the largest of them before they are added, which cost 1.3e-5 (normal
+// values) to 6e-5 (a few columns 40 times the rest) of the result's norm at K
+// 64 .. 11008 (measured against 64 bits): a hundredth of the bf16 rounding
+// that follows, but too much for an fp32 result.  fp32 layers therefore widen
+// the codes to bf16 (exact) and run the bf16 MFMA (2e-7), each block's sum
+// scaled as it is added to the fp32 total.
+//
+// Forms:
+//   * split-K tiles of 128 columns by up to 128 rows (decode, and fp32 layers
+//     of any size): the token rows are quantised by the workgroup that reads
+//     them, straight into LDS, so a decode step has no quantising launch;
+//   * 256 x 256 tiles with the LoRA expand in their epilogue, and 256 x 128
+//     tiles that write fp32 partials: rows quantised ahead by one launch.
+#include "gemm_tile.h"
+#include "lora_internal.h"
+#include "quantise.h"
+
+namespace lora {
+namespace {
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+
+constexpr int kQDecodeKC = 512;           // K elements staged at a time (4 scale blocks)
+
+__device__ __forceinline__ i32x8_t join32(uint4 a, uint4 b) {
+  const i32x8_t r = {int(a.x), int(a.y), int(a.z), int(a.w), int(b.x), int(b.y), int(b.z), int(b.w)};
+  return r;
+}
+
+// Eight codes widened to bf16 (exact: 4 significant bits).
+__device__ __forceinline__ bf16x8_t widen8(uint32_t lo, uint32_t hi) {
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8(int(lo), false);
+  const f32x2_t b = __builtin_amdgcn_cvt_pk_f32_fp8(int(lo), true);
+  const f32x2_t c = __builtin_amdgcn_cvt_pk_f32_fp8(int(hi), false);
+  const f32x2_t d = __builtin_amdgcn_cvt_pk_f32_fp8(int(hi), true);
+  const uint4 w = make_uint4(f2bf2(a[0], a[1]), f2bf2(b[0], b[1]), f2bf2(c[0], c[1]), f2bf2(d[0], d[1]));
+  bf16x8_t r;
+  __builtin_memcpy(&r, &w, 16);
+  return r;
+}
+
+template <int S>
+__device__ __forceinline__ f32x16_t mfma_q(i32x8_t a, i32x8_t b, f32x16_t c, int sa, int sb) {
+  // cbsz = blgp = 0: both operands e4m3; S: the byte of the scale words
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, S, sa, S, sb);
+}
+
+// ------------------------------------------------------------ split-K tiles
+// Columns bx*128 .. +127 (32 per wave), rows by*32*MB .., K from bz*k_split.
+// Per 512 of K: every lane issues its share of W (64 bytes of each 128-byte
+// block: lanes 0-31 the first half, 32-63 the second, the same permutation of
+// K in both operands) into registers, then the workgroup quantises its token
+// rows into LDS while those loads are in flight.
+// A row's 512 codes are 32 slots of 16 bytes, chunk c in slot c ^ (row & 15):
+// the 16 rows that a quarter wave reads at once cover the 64 banks once.
+template <typename E, int MB>
+__device__ __forceinline__ void q_split_tile(const QGemmArgs &q, int bx, int by, int bz,
+                                             uint8_t *xs, uint32_t *ss) {
+  constexpr int KC = kQDecodeKC, NG = KC / kQBlock, BMr = MB * 32;
+  constexpr bool kExact = sizeof(E) == 4;
+  const GemmArgs &g = q.g;
+  const E *X = static_cast<const E *>(g.X);
+  const uint8_t *W = static_cast<const uint8_t *>(g.W);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, half = lane >> 5;
+  const int n0 = bx * 128 + wave * 32, m0 = by * BMr;
+  const int kp = int(q.ldb);                       // K, padded to whole blocks
+  const int k1 = min(kp, (bz + 1) * g.k_split);
+  const uint8_t *wrow = W + int64_t(min(n0 + (lane & 31), g.N - 1)) * q.ldb + half * 64;
+  const uint8_t *srow = q.sb + int64_t(bx) * q.lsb;
+  f32x16_t acc[MB];
+#pragma unroll
+  for (int b = 0; b < MB; ++b)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) acc[b][v] = 0.f;
+  for (int k0 = bz * g.k_split; k0 < k1; k0 += KC) {
+    const int ng = min(NG, (k1 - k0) / kQBlock);
+    uint4 wf[NG][4];
+#pragma unroll
+    for (int gq = 0; gq < NG; ++gq)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        wf[gq][c] = *reinterpret_cast<const uint4 *>(wrow + k0 + min(gq, ng - 1) * kQBlock + c * 16);
+    const int sw = *reinterpret_cast<const int *>(srow + k0 / kQBlock);
+    if (k0 > bz * g.k_split) __syncthreads();      // every wave is done with the last chunk
+    // 16 lanes per (row, block): 8 elements each; rows past M are zero codes
+#pragma unroll
+    for (int i = 0; i < BMr / 4; ++i) {
+      const int it = i * 16 + (tid >> 4);
+      const int r = it >> 2, blk = it & 3;
+      const int c8 = blk * kQBlock + (tid & 15) * 8;
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (m0 + r < g.M && k0 + c8 < g.Kd) Elem<E>::load8(X + int64_t(m0 + r) * g.Kd + k0 + c8, v);
+      const uint32_t byte = q_scale_byte(max16(abs_max8(v)));
+      *reinterpret_cast<uint2 *>(xs + r * KC + (((c8 >> 4) ^ (r & 15)) << 4) + (c8 & 8)) =
+          q_encode8(v, byte);
+      if ((tid & 15) == 0) reinterpret_cast<uint8_t *>(ss)[r * 4 + blk] = uint8_t(byte);
+    }
+    __syncthreads();
+    auto group = [&](auto gi) __attribute__((always_inline)) {
+      constexpr int G = decltype(gi)::value;
+      if (G >= ng) return;
+#pragma unroll
+      for (int b = 0; b < MB; ++b) {
+        const int r = b * 32 + (lane & 31);
+        uint4 xa[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          xa[c] = *reinterpret_cast<const uint4 *>(
+              xs + r * KC + (((G * 8 + half * 4 + c) ^ (r & 15)) << 4));
+        if constexpr (!kExact) {
+          const int sa = int(ss[r]);
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            acc[b] = mfma_q<G>(join32(xa[2 * s], xa[2 * s + 1]), join32(wf[G][2 * s], wf[G][2 * s + 1]),
+                               acc[b], sa, sw);
+        } else {
+          f32x16_t p;
+#pragma unroll
+          for (int v = 0; v < 16; ++v) p[v] = 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            p = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen8(xa[c].x, xa[c].y),
+                                                        widen8(wf[G][c].x, wf[G][c].y), p, 0, 0, 0);
+            p = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen8(xa[c].z, xa[c].w),
+                                                        widen8(wf[G][c].z, wf[G][c].w), p, 0, 0, 0);
+          }
+          // a block of scale byte 255 has NaN codes, so its sum is NaN already
+          const int ew = ((sw >> (8 * G)) & 0xff) - 254;
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const int row = b * 32 + (v >> 2) * 8 + half * 4 + (v & 3);
+            acc[b][v] += ldexpf(p[v], int((ss[row] >> (8 * G)) & 0xffu) + ew);
+          }
+        }
+      }
+    };
+    group(std::integral_constant<int, 0>{});
+    group(std::integral_constant<int, 1>{});
+    group(std::integral_constant<int, 2>{});
+    group(std::integral_constant<int, 3>{});
+  }
+  float *Pz = g.partial + int64_t(bz) * g.M * g.N;
+  const int col = n0 + (lane & 31);
+  if (col < g.N) {
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int row = m0 + b * 32 + (v >> 2) * 8 + half * 4 + (v & 3);
+        if (row < g.M) __builtin_nontemporal_store(acc[b][v], Pz + int64_t(row) * g.N + col);
+      }
+  }
+}
+
+template <typename E, int MB>
+__global__ __launch_bounds__(256) void q_split_kernel(QGemmArgs q) {
+  __shared__ __attribute__((aligned(16))) uint8_t xs[MB * 32 * kQDecodeKC];
+  __shared__ uint32_t ss[MB * 32];
+  q_split_tile<E, MB>(q, blockIdx.x, blockIdx.y, blockIdx.z, xs, ss);
+}
+
+// ------------------------------------------------------------ pipelined tiles
+// Tiles of BM x BN over K tiles of 128 codes (one scale block, 128 bytes per
+// row: the LDS layout of the bf16 tiles), WM x WN waves.  NS stages: before
+// the second half of K tile kt one barrier frees the stage just read for tile
+// kt + NS and publishes tile kt + 1, whose first fragments are read under the
+// second half's MFMAs.  A fragment is 32 bytes per lane; the A fragments of
+// the next half replace each A block's registers after its last MFMA, the B
+// fragments alternate between two sets.
+template <int BM, int BN, int WM, int WN, int NS, bool kFused, bool kMask = false>
+__device__ __forceinline__ void q_tile_run(const QGemmArgs &q, char *smem, int m0, int n0, int kt0,
+                                           int nk, int slot) {
+  using C = TileCfg<BM, BN, WM, WN>;
+  constexpr int TM = C::TM, TN = C::TN, NM = TM * TN;
+  static_assert(BN % 128 == 0 && (TN * 32 <= 128), "a wave's columns lie in one scale block");
+  const GemmArgs &g = q.g;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave / WN, wn = wave % WN;
+  const int frow = lane & 31, half = lane >> 5, lrow = lane >> 3;
+  const uint8_t *abase = static_cast<const uint8_t *>(g.X) + int64_t(m0) * q.lda + int64_t(kt0) * kQBlock;
+  const uint8_t *bbase = static_cast<const uint8_t *>(g.W) + int64_t(n0) * q.ldb + int64_t(kt0) * kQBlock;
+  uint32_t aoff[C::A_INS], boff[C::B_INS];
+#pragma unroll
+  for (int i = 0; i < C::A_INS; ++i) {
+    const int row = (wave * C::A_INS + i) * 8 + lrow;
+    aoff[i] = uint32_t(min(row, g.M - 1 - m0)) * uint32_t(q.lda) + tswz(row, lane & 7) * 16;
+  }
+#pragma unroll
+  for (int i = 0; i < C::B_INS; ++i) {
+    const int row = (wave * C::B_INS + i) * 8 + lrow;
+    boff[i] = uint32_t(min(row, g.N - 1 - n0)) * uint32_t(q.ldb) + tswz(row, lane & 7) * 16;
+  }
+  auto dma_one = [&](char *base, int kt, int i) __attribute__((always_inline)) {
+    const uint32_t lds = lds_addr(base);
+    if (i < C::A_INS)
+      lds_dma16(abase + kt * kQBlock + aoff[i], lds + (wave * C::A_INS + i) * 1024);
+    else
+      lds_dma16(bbase + kt * kQBlock + boff[i - C::A_INS],
+                lds + BM * C::ROWB + (wave * C::B_INS + i - C::A_INS) * 1024);
+  };
+  // scale words: the row's (this wave's row frow of each A block) and the
+  // weight block's, four K tiles per word
+  const uint8_t *sarow[TM];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+    sarow[i] = q.sa + int64_t(min(m0 + wm * TM * 32 + i * 32 + frow, g.M - 1)) * q.lsa;
+  const uint8_t *sbrow = q.sb + int64_t(min(n0 + wn * TN * 32, g.N - 1) / kQBlock) * q.lsb;
+  const int gmax = int(q.lsb) / 4 - 1;
+  uint32_t sa[TM], sb, na[TM], nb;
+  auto load_scales = [&](int grp) __attribute__((always_inline)) {
+    const int o = min(grp, gmax) * 4;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) na[i] = *reinterpret_cast<const uint32_t *>(sarow[i] + o);
+    nb = *reinterpret_cast<const uint32_t *>(sbrow + o);
+  };
+
+  f32x16_t acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+  EpiPre<TM> pre;
+  if constexpr (kFused) epi_fetch_desc<BM, BN, WM, WN>(g, m0, pre);
+  load_scales(kt0 >> 2);
+
+  i32x8_t fa[TM], fb0[TN], fb1[TN];
+  auto frag = [&](const char *base, int s, int row) __attribute__((always_inline)) {
+    const char *p = base + row * C::ROWB;
+    const int c = tswz(frow, 4 * s + 2 * half);
+    return join32(*reinterpret_cast<const uint4 *>(p + (c << 4)),
+                  *reinterpret_cast<const uint4 *>(p + ((c ^ 1) << 4)));
+  };
+  auto frag_a = [&](const char *base, int s, int i) __attribute__((always_inline)) {
+    return frag(base, s, wm * TM * 32 + i * 32 + frow);
+  };
+  auto frag_b = [&](const char *base, int s, int j) __attribute__((always_inline)) {
+    return frag(base, s, BM + wn * TN * 32 + j * 32 + frow);
+  };
+  // MFMAs of one half of a K tile from (fa, xb); the next half's fragments
+  // come from src (half s_next), the copies of K tile kn go into dst (kCopy)
+  auto kstep = [&](auto copy, i32x8_t (&xb)[TN], i32x8_t (&yb)[TN], const char *src, int s_next,
+                   char *dst, int kn, int shift) __attribute__((always_inline)) {
+    constexpr bool kCopy = decltype(copy)::value;
+    const int wsb = int(sb >> shift);
+    int wsa[TM];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) wsa[i] = int(sa[i] >> shift);
+#pragma unroll
+    for (int m = 0; m < NM; ++m) {
+      const int i = m / TN, j = m % TN;
+      acc[i][j] = mfma_q<0>(fa[i], xb[j], acc[i][j], wsa[i], wsb);
+      if (m < TN) yb[m] = frag_b(src, s_next, m);
+      if (j == TN - 1) fa[i] = frag_a(src, s_next, i);
+      if constexpr (kCopy) {
+#pragma unroll
+        for (int c = m * C::LPW / NM; c < (m + 1) * C::LPW / NM; ++c) dma_one(dst, kn, c);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+#pragma unroll
+  for (int p = 0; p < NS; ++p) {
+    if (p < nk) {
+#pragma unroll
+      for (int c = 0; c < C::LPW; ++c) dma_one(smem + p * C::STAGE, p, c);
+    }
+  }
+  // the first tile (and the scale words, issued before it) has landed
+  wait_vmcnt<0>();
+#pragma unroll
+  for (int i = 0; i < TM; ++i) asm volatile("" : "+v"(na[i]));
+  asm volatile("" : "+v"(nb));
+#pragma unroll
+  for (int i = 0; i < TM; ++i) sa[i] = na[i];
+  sb = nb;
+  lds_bar();
+  if (nk > 0) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) fa[i] = frag_a(smem, 0, i);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) fb0[j] = frag_b(smem, 0, j);
+  }
+  int stage = 0;
+  for (int kt = 0; kt < nk; ++kt) {
+    char *const cur = smem + stage * C::STAGE;
+    stage = stage + 1 == NS ? 0 : stage + 1;
+    char *const nxt = smem + stage * C::STAGE;
+    const int at = (kt0 + kt) & 3;
+    // the next word of scales goes out with its group's last tile
+    if (at == 3) load_scales((kt0 + kt + 1) >> 2);
+    kstep(std::false_type{}, fb0, fb1, cur, 1, cur, 0, 8 * at);
+    // tile kt + 1 has landed: everything but the copies of kt + 2 .. kt + NS - 1
+    wait_vmcnt<(NS - 2) * C::LPW>();
+    if (at == 3) {
+      // a use here: the loads' wait falls where nothing else is in flight
+#pragma unroll
+      for (int i = 0; i < TM; ++i) asm volatile("" : "+v"(na[i]));
+      asm volatile("" : "+v"(nb));
+    }
+    lds_bar();
+    if constexpr (kFused) {
+      if (kt == 0) epi_fetch_pid(g, pre);
+    }
+    // past the end the body stays the same: the copy repeats the last tile
+    // into a stage that no one reads again, the fragments go unused
+    kstep(std::true_type{}, fb1, fb0, nxt, 0, cur, min(kt + NS, nk - 1), 8 * at);
+    if (at == 3) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i) sa[i] = na[i];
+      sb = nb;
+    }
+  }
+  if constexpr (kFused) {
+    if (nk <= 0) epi_fetch_pid(g, pre);
+  }
+  // the last copies have landed and every wave is done with the stages
+  wait_vmcnt<0>();
+  lds_bar();
+
+  if constexpr (!kFused) {
+    float *Pz = g.partial + int64_t(slot) * g.M * g.N;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const int col = n0 + wn * TN * 32 + j * 32 + frow;
+        if (col >= g.N) continue;
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const int row = m0 + wm * TM * 32 + i * 32 + (v >> 2) * 8 + half * 4 + (v & 3);
+          if (row < g.M) __builtin_nontemporal_store(acc[i][j][v], Pz + int64_t(row) * g.N + col);
+        }
+      }
+  } else {
+    fused_epilogue<BM, BN, WM, WN, kMask>(g, acc, smem, smem + C::STAGE, m0, n0, pre);
+  }
+}
+
+// Tiles as the bf16 form orders them (consecutive tiles on one XCD).  Split
+// form: stream-K over g.sk_g workgroups (the pieces as the epilogue counts
+// them), or g.k_split of K per blockIdx.y.
+template <int BM, int BN, int WM, int WN, int NS, bool kFused, bool kMask = false>
+__global__ __launch_bounds__(WM * WN * 64, 1) void q_tile_kernel(QGemmArgs q) {
+  using C = TileCfg<BM, BN, WM, WN>;
+  __shared__ __attribute__((aligned(16))) char smem[NS * C::STAGE];
+  const GemmArgs &g = q.g;
+  const int tiles_m = (g.M + BM - 1) / BM, tiles_n = (g.N + BN - 1) / BN;
+  const int ntiles = tiles_m * tiles_n;
+  const int KT = int(q.ldb) / kQBlock;
+  if constexpr (!kFused) {
+    if (g.sk_g > 0) {
+      const int64_t U = int64_t(ntiles) * KT;
+      int64_t u = int64_t(blockIdx.x) * U / g.sk_g;
+      const int64_t u1 = int64_t(blockIdx.x + 1) * U / g.sk_g;
+      while (u < u1) {
+        const int t = int(u / KT), kb = int(u % KT);
+        const int ke = int(min<int64_t>(KT, kb + (u1 - u)));
+        const int wf = int(((int64_t(t) * KT + 1) * g.sk_g - 1) / U);
+        q_tile_run<BM, BN, WM, WN, NS, false>(q, smem, (t / tiles_n) * BM, (t % tiles_n) * BN, kb,
+                                              ke - kb, int(blockIdx.x) - wf);
+        u += ke - kb;
+      }
+      return;
+    }
+  }
+  const int per = (ntiles + 7) / 8;
+  const int t = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if (t >= ntiles) return;
+  int tm, tn;
+  tile_coords(t, tiles_m, tiles_n, tm, tn);
+  const int k0 = blockIdx.y * (g.k_split / kQBlock);
+  q_tile_run<BM, BN, WM, WN, NS, kFused, kMask>(q, smem, tm * BM, tn * BN, k0,
+                                                min(KT - k0, g.k_split / kQBlock), blockIdx.y);
+}
+
+}  // namespace
+
+GemmConfig choose_quantised_gemm(int T, int d_in, int d_out, int dtype) {
+  GemmConfig c{};
+  const int kb = int(q_row_bytes(d_in)) / kQBlock;
+  if (dtype == LORA_F32 || T <= 128) {
+    // decode: W streamed once, 512 of K per workgroup; with more tiles of
+    // output (fp32 layers of many rows) a workgroup keeps more of K, down to
+    // two workgroups per CU
+    c.kind = 4; c.bn = 128;
+    c.bm = T <= 32 ? 32 : (T <= 64 ? 64 : 128);
+    const int64_t tiles = int64_t((T + c.bm - 1) / c.bm) * ((d_out + 127) / 128);
+    const int chunks = (kb + 3) / 4;
+    const int64_t want = (512 + tiles - 1) / tiles;
+    const int splits = int(want < chunks ? want : chunks);
+    const int per = (chunks + splits - 1) / splits;
+    c.k_split = per * kQDecodeKC;
+    c.splits = (chunks + per - 1) / per;
+    return c;
+  }
+  const int64_t big = int64_t((T + 255) / 256) * ((d_out + 255) / 256);
+  if (big >= 256) {
+    c.kind = 5; c.bm = 256; c.bn = 256;
+    c.splits = 1; c.k_split = kb * kQBlock; c.fused = true;
+    return c;
+  }
+  c.kind = 6; c.bm = 256; c.bn = 128;
+  const int64_t tiles = int64_t((T + 255) / 256) * ((d_out + 127) / 128);
+  const int64_t units = tiles * kb;
+  constexpr int kWgs = 256;
+  if (units >= 4 * kWgs) {
+    const int64_t per = units / kWgs;
+    c.sk = kWgs;
+    c.k_split = kQBlock;
+    c.splits = int((kb + per - 1) / per) + 1;
+    return c;
+  }
+  const int64_t want = (kWgs + tiles - 1) / tiles;
+  const int64_t most = kb / 4 > 1 ? kb / 4 : 1;        // every split keeps >= 512 of K
+  const int splits = int(want < most ? want : most);
+  const int per = (kb + splits - 1) / splits;
+  c.k_split = per * kQBlock;
+  c.splits = (kb + per - 1) / per;
+  return c;
+}
+
+hipError_t launch_quantised_gemm(const GemmConfig &c, const QGemmArgs &q, int dtype, hipStream_t s) {
+  const GemmArgs &g = q.g;
+  if (c.kind == 4) {
+    const dim3 grid((g.N + 127) / 128, (g.M + c.bm - 1) / c.bm, c.splits), block(256);
+#define LORA_QS(E) \
+  do { \
+    if (c.bm == 32) hipLaunchKernelGGL((q_split_kernel<E, 1>), grid, block, 0, s, q); \
+    else if (c.bm == 64) hipLaunchKernelGGL((q_split_kernel<E, 2>), grid, block, 0, s, q); \
+    else hipLaunchKernelGGL((q_split_kernel<E, 4>), grid, block, 0, s, q); \
+  } while (0)
+    if (dtype == LORA_BF16) LORA_QS(uint16_t);
+    else LORA_QS(float);
+#undef LORA_QS
+    return hipGetLastError();
+  }
+  if (dtype != LORA_BF16) return hipErrorInvalidConfiguration;
+  const int tiles = ((g.M + c.bm - 1) / c.bm) * ((g.N + c.bn - 1) / c.bn);
+  if (c.kind == 5) {
+    const dim3 grid(8 * ((tiles + 7) / 8));
+    if (g.mask) hipLaunchKernelGGL((q_tile_kernel<256, 256, 2, 2, 2, true, true>), grid, dim3(256), 0, s, q);
+    else hipLaunchKernelGGL((q_tile_kernel<256, 256, 2, 2, 2, true>), grid, dim3(256), 0, s, q);
+    return hipGetLastError();
+  }
+  if (c.kind == 6 && !g.mask) {
+    const dim3 grid = c.sk > 0 ? dim3(c.sk) : dim3(8 * ((tiles + 7) / 8), c.splits);
+    hipLaunchKernelGGL((q_tile_kernel<256, 128, 2, 2, 3, false>), grid, dim3(256), 0, s, q);
+    return hipGetLastError();
+  }
+  return hipErrorInvalidConfiguration;
+}
+
+}  // namespace lora

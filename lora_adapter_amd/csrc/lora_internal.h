@@ -266,6 +266,17 @@ struct GemmArgs {
   const uint8_t *mask;
 };
 
+// The quantised GEMM: g.X are the rows' codes (tiles) or the rows themselves
+// in the layer's dtype (split-K form, which quantises them), g.W the weight's
+// codes.  Scale rows hold one exponent byte per 128 of K.
+struct QGemmArgs {
+  GemmArgs g;
+  const uint8_t *sa;        // [M][lsa] scale bytes of the rows' codes (tiles)
+  const uint8_t *sb;        // [ceil(N/128)][lsb] scale bytes of the weight's blocks
+  int64_t lda, ldb;         // bytes per row of codes (K padded to whole blocks)
+  int64_t lsa, lsb;         // bytes per row of scales (a multiple of 4)
+};
+
 struct EpilogueArgs {
   const float *partial;     // [splits][M][N]
   int splits, M, N;
@@ -438,6 +449,12 @@ hipError_t launch_grad_x_epilogue(const GemmConfig &c, const GemmArgs &g, int dt
 // dst[c][r] = src[r][c] for a rows x cols matrix of the dtype.
 hipError_t launch_transpose(const void *src, void *dst, int rows, int cols, int dtype,
                             hipStream_t s);
+
+// Products over e4m3 operands (see gemm_quantised.hip): the configuration, and
+// the GEMM (partials, or the fused epilogue for kind 5).  Split forms are
+// finished by launch_epilogue / launch_grad_x_epilogue.
+GemmConfig choose_quantised_gemm(int T, int d_in, int d_out, int dtype);
+hipError_t launch_quantised_gemm(const GemmConfig &c, const QGemmArgs &q, int dtype, hipStream_t s);
 
 // Batched tall-skinny QR (see tsqr.hip).
 bool tsqr_shape_ok(int M, int m, int n);

@@ -1,0 +1,146 @@
+// Quantisation to e4m3 with one power-of-two scale per block: rows (one scale
+// per 128 columns: activations and gradients) and weights (one scale per 128 x
+// 128 block, so that the codes of W and of W^T are the same and the input
+// gradient runs over the very weight that the forward used).
+#include "quantise.h"
+
+namespace lora {
+namespace {
+
+// One wave per 512 columns of a row, 8 elements per lane; 16 lanes share a
+// block.  Columns past d are zero codes.
+template <typename E>
+__global__ __launch_bounds__(256) void quantise_rows_kernel(const E *X, int T, int d, int chunks,
+                                                            uint8_t *codes, uint8_t *scale) {
+  const int64_t w = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (w >= int64_t(T) * chunks) return;
+  const int64_t t = w / chunks;
+  const int col = int(w % chunks) * 512 + lane * 8;
+  const int64_t ld = q_row_bytes(d), ls = q_scale_bytes(d);
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (col < d) Elem<E>::load8(X + t * d + col, v);
+  const uint32_t byte = q_scale_byte(max16(abs_max8(v)));
+  if (col < ld) *reinterpret_cast<uint2 *>(codes + t * ld + col) = q_encode8(v, byte);
+  const int blk = col / kQBlock;
+  if ((lane & 15) == 0 && blk < ls) scale[t * ls + blk] = col < ld ? uint8_t(byte) : uint8_t(0);
+}
+
+// 4 x 4 bytes turned: o[j] = byte j of each of d[0..3].
+__device__ __forceinline__ void turn4(const uint32_t d[4], uint32_t o[4]) {
+  const uint32_t a = __builtin_amdgcn_perm(d[1], d[0], 0x05010400u);
+  const uint32_t b = __builtin_amdgcn_perm(d[3], d[2], 0x05010400u);
+  const uint32_t c = __builtin_amdgcn_perm(d[1], d[0], 0x07030602u);
+  const uint32_t e = __builtin_amdgcn_perm(d[3], d[2], 0x07030602u);
+  o[0] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+  o[1] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+  o[2] = __builtin_amdgcn_perm(e, c, 0x05040100u);
+  o[3] = __builtin_amdgcn_perm(e, c, 0x07060302u);
+}
+
+// One workgroup per 128 x 128 block: 16 lanes per row, 16 rows at a time, the
+// whole block in registers between its largest magnitude and its codes; the
+// codes of W^T go through LDS as dwords of four columns.
+template <typename E>
+__global__ __launch_bounds__(256) void quantise_weight_kernel(const E *W, int d_out, int d_in,
+                                                              uint8_t *q_t, uint8_t *q,
+                                                              uint8_t *scale, uint8_t *scale_t) {
+  constexpr int S = kQBlock / 4 + 1;                 // dwords per staged row (padded)
+  __shared__ uint32_t tile[kQBlock * S];
+  __shared__ uint32_t wmax[4];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int r0 = blockIdx.y * kQBlock, c0 = blockIdx.x * kQBlock;
+  const int rr = tid >> 4, cc = (tid & 15) * 8;
+  const int64_t ld = q_row_bytes(d_in), ldt = q_row_bytes(d_out);
+  const bool c_ok = c0 + cc < d_in;
+  float v[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = r0 + rr + 16 * i;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+    if (c_ok && r < d_out) Elem<E>::load8(W + int64_t(r) * d_in + c0 + cc, v[i]);
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, abs_max8(v[i]));
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = max(m, uint32_t(__shfl_xor(int(m), o, 64)));
+  if (lane == 0) wmax[tid >> 6] = m;
+  __syncthreads();
+  m = max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3]));
+  const uint32_t byte = q_scale_byte(m);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = rr + 16 * i;
+    uint2 w = q_encode8(v[i], byte);
+    // a NaN block's padding stays zero
+    if (!c_ok || r0 + r >= d_out) w = make_uint2(0, 0);
+    if (r0 + r < d_out) *reinterpret_cast<uint2 *>(q_t + int64_t(r0 + r) * ld + c0 + cc) = w;
+    tile[r * S + cc / 4] = w.x;
+    tile[r * S + cc / 4 + 1] = w.y;
+  }
+  if (tid == 0) {
+    const int64_t ls = q_scale_bytes(d_in), lst = q_scale_bytes(d_out);
+    const int nbi = gridDim.x, nbo = gridDim.y;
+    scale[blockIdx.y * ls + blockIdx.x] = uint8_t(byte);
+    if (int(blockIdx.x) == nbi - 1)
+      for (int64_t b = nbi; b < ls; ++b) scale[blockIdx.y * ls + b] = 0;
+    if (scale_t) {
+      scale_t[blockIdx.x * lst + blockIdx.y] = uint8_t(byte);
+      if (int(blockIdx.y) == nbo - 1)
+        for (int64_t b = nbo; b < lst; ++b) scale_t[blockIdx.x * lst + b] = 0;
+    }
+  }
+  if (!q) return;
+  __syncthreads();
+  // lane -> 16 rows rg and 4 columns cg: 8 lanes write 128 bytes of one row of W^T
+  const int rg = tid & 7, cg = tid >> 3;
+  uint32_t o[4][4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t d[4], t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] = tile[(rg * 16 + k * 4 + i) * S + cg];
+    turn4(d, t);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j][k] = t[j];
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int c = c0 + cg * 4 + j;
+    if (c < d_in)
+      *reinterpret_cast<uint4 *>(q + int64_t(c) * ldt + r0 + rg * 16) =
+          make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_quantise_rows(const void *X, int dtype, int T, int d, uint8_t *codes,
+                                uint8_t *scale, hipStream_t s) {
+  // whole scale rows: the padding bytes past the last block are written too
+  const int chunks = int((q_scale_bytes(d) + 3) / 4);
+  const dim3 grid(unsigned((int64_t(T) * chunks + 3) / 4)), block(256);
+  if (dtype == LORA_BF16)
+    hipLaunchKernelGGL(quantise_rows_kernel<uint16_t>, grid, block, 0, s,
+                       static_cast<const uint16_t *>(X), T, d, chunks, codes, scale);
+  else
+    hipLaunchKernelGGL(quantise_rows_kernel<float>, grid, block, 0, s, static_cast<const float *>(X),
+                       T, d, chunks, codes, scale);
+  return hipGetLastError();
+}
+
+hipError_t launch_quantise_weight(const void *W_t, int dtype, int d_out, int d_in, uint8_t *q_t,
+                                  uint8_t *q, uint8_t *scale, uint8_t *scale_t, hipStream_t s) {
+  const dim3 grid(unsigned((d_in + kQBlock - 1) / kQBlock), unsigned((d_out + kQBlock - 1) / kQBlock));
+  if (dtype == LORA_BF16)
+    hipLaunchKernelGGL(quantise_weight_kernel<uint16_t>, grid, dim3(256), 0, s,
+                       static_cast<const uint16_t *>(W_t), d_out, d_in, q_t, q, scale, scale_t);
+  else
+    hipLaunchKernelGGL(quantise_weight_kernel<float>, grid, dim3(256), 0, s,
+                       static_cast<const float *>(W_t), d_out, d_in, q_t, q, scale, scale_t);
+  return hipGetLastError();
+}
+
+}  // namespace lora
