@@ -588,6 +588,55 @@ int32_t lora_grad_x_quantised(const void *dY, const lora_quantised_weight *W,
                               size_t grad_ws_bytes, int32_t max_rank, void *dX, void *ws,
                               size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------- orthogonalised updates
+ * The update of the trained factors from the gradients lora_grad leaves
+ * ([LoRAFusion] 解决什么真问题: only A and B train; the pages name no
+ * optimiser).  The matrix of one factor of an adapter is its r x d rank rows
+ * N (rows = its pages); with X_0 = N / (|N|_F + eps), `steps` times
+ *   X <- c0 X + (c1 G + c2 G^2) X,   G = X.X^T
+ * (Newton-Schulz: every singular value s moves to c0 s + c1 s^3 + c2 s^5, the
+ * singular vectors stay).  The r x r products run in float64, the rest in
+ * float32.  A zero N gives zero; an infinity or a NaN in N makes its whole
+ * result NaN.
+ *   adapters [M] int32 device: adapters to take.  One out of range, of rank 0
+ *     or above max_rank, with an inconsistent page table, or listed before is
+ *     skipped: nothing of it is read or written.  out_rank [M] int32 device,
+ *     or NULL: the rank taken, 0 for a skipped entry.
+ *   max_rank 1..LORA_MAX_RANK sizes the workspace and the launches; steps
+ *     1..LORA_MAX_ORTH_STEPS; coef: host float[3]; 1e-20 <= eps <= 1e20; M at
+ *     most 16384 (UNSUPPORTED).  Only the pool's page table is read.
+ * No page may belong to two of the adapters.  Results are deterministic. */
+#define LORA_MAX_ORTH_STEPS 32
+/* out rows <- the orthogonalised src rows, float32 pages [n_pages][d] (d a
+ * multiple of 64: d_in for A's pages, d_out for B's); other pages are not
+ * touched.  src_pages and out_pages must not overlap.
+ * Errors: INVALID_ARG, UNSUPPORTED, CAPACITY (ws), DEVICE. */
+size_t lora_orthogonalise_workspace_bytes(int32_t M, int32_t max_rank, int32_t d);
+int32_t lora_orthogonalise(const lora_pool_desc *pool, const int32_t *adapters, int32_t M,
+                           int32_t max_rank, const float *src_pages, float *out_pages, int32_t d,
+                           int32_t steps, const float *coef, float eps, int32_t *out_rank, void *ws,
+                           size_t ws_bytes, void *stream);
+/* One optimiser step of both factors of every listed adapter, in place:
+ *   m <- momentum . m + g
+ *   N  = g + momentum . m  (nesterov)  or  m
+ *   w <- w . (1 - lr . decay) - lr . orthogonalised N
+ * with w the float32 master row when master is given (the page then takes w
+ * rounded once to the pool's dtype), else the page itself.  Each buffer has
+ * the pages' layout; none of one factor's may overlap another. */
+typedef struct {
+  void *pages;                /* [n_pages][d] pool dtype, updated                 */
+  float *master;              /* [n_pages][d], updated, or NULL                   */
+  float *momentum;            /* [n_pages][d], updated                            */
+  const float *grad;          /* [n_pages][d], as lora_grad writes it             */
+  float lr, decay;
+} lora_factor_update;         /* host struct, device pointers                      */
+size_t lora_orthogonal_step_workspace_bytes(int32_t M, int32_t max_rank, int32_t d_in, int32_t d_out);
+int32_t lora_orthogonal_step(const lora_pool_desc *pool, const int32_t *adapters, int32_t M,
+                             int32_t max_rank, const lora_factor_update *a_update,
+                             const lora_factor_update *b_update, float momentum, int32_t nesterov,
+                             int32_t steps, const float *coef, float eps, int32_t *out_rank, void *ws,
+                             size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

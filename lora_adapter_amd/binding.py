@@ -40,6 +40,8 @@ EXPORTS = (
     "lora_quantised_row_bytes", "lora_quantised_scale_bytes", "lora_quantise_rows",
     "lora_quantise_weight", "lora_apply_quantised_workspace_bytes", "lora_apply_quantised",
     "lora_forward_quantised", "lora_grad_x_quantised_workspace_bytes", "lora_grad_x_quantised",
+    "lora_orthogonalise_workspace_bytes", "lora_orthogonalise",
+    "lora_orthogonal_step_workspace_bytes", "lora_orthogonal_step",
 )
 
 
@@ -70,6 +72,12 @@ class PageCopy(ctypes.Structure):
 class QuantisedWeightDesc(ctypes.Structure):
     _fields_ = [("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32), ("q_t", ctypes.c_void_p),
                 ("scale", ctypes.c_void_p), ("q", ctypes.c_void_p), ("scale_t", ctypes.c_void_p)]
+
+
+class FactorUpdateDesc(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("momentum", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("lr", ctypes.c_float), ("decay", ctypes.c_float)]
 
 
 class ResidencyConfig(ctypes.Structure):
@@ -150,6 +158,13 @@ _PROTOS = {
     "lora_grad_x_quantised_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32]),
     "lora_grad_x_quantised": (_I32, [_VP, _QW, _VP, _I32, _I32, _PD, _VP, _VP, _SZ, _I32, _VP, _VP,
                                      _SZ, _VP]),
+    "lora_orthogonalise_workspace_bytes": (_SZ, [_I32, _I32, _I32]),
+    "lora_orthogonalise": (_I32, [_PD, _VP, _I32, _I32, _VP, _VP, _I32, _I32, ctypes.POINTER(_F32),
+                                  _F32, _VP, _VP, _SZ, _VP]),
+    "lora_orthogonal_step_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32]),
+    "lora_orthogonal_step": (_I32, [_PD, _VP, _I32, _I32, ctypes.POINTER(FactorUpdateDesc),
+                                    ctypes.POINTER(FactorUpdateDesc), _F32, _I32, _I32,
+                                    ctypes.POINTER(_F32), _F32, _VP, _VP, _SZ, _VP]),
 }
 
 
@@ -594,3 +609,50 @@ def lora_grad_x_quantised(dY, W: QuantisedWeight, keep_mask, T: int, K: int, poo
         _ptr(dY), W.ref, _ptr(keep_mask), T, K, pool.ref, _ptr(plan), _ptr(grad_ws),
         grad_ws.numel() * grad_ws.element_size(), int(max_rank), _ptr(dX), _ptr(ws),
         ws.numel() * ws.element_size(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- orthogonalised updates
+
+NS_COEF = (3.4445, -4.7750, 2.0315)     # quintic coefficients whose slope at 0 is largest
+
+
+class FactorUpdate:
+    """One factor's buffers of lora_orthogonal_step: its pages (the pool's own
+    a_pages or b_pages), float32 gradient, momentum and (or None) master pages."""
+
+    def __init__(self, pages, grad, momentum, master, lr: float, decay: float = 0.0):
+        for t in (grad, momentum, master):
+            if t is not None and (t.shape != pages.shape or t.element_size() != 4 or not t.is_contiguous()):
+                raise ValueError(f"expected contiguous float32 pages {tuple(pages.shape)}, got {tuple(t.shape)}")
+        self.tensors = (pages, grad, momentum, master)
+        self.desc = FactorUpdateDesc(_ptr(pages), _ptr(master), _ptr(momentum), _ptr(grad), float(lr),
+                                     float(decay))
+
+    @property
+    def ref(self):
+        return ctypes.byref(self.desc)
+
+
+def lora_orthogonalise_workspace_bytes(M: int, max_rank: int, d: int) -> int:
+    return int(lib().lora_orthogonalise_workspace_bytes(M, max_rank, d))
+
+
+def lora_orthogonalise(pool: Pool, adapters, M: int, max_rank: int, src_pages, out_pages, d: int,
+                       steps: int, coef, eps: float, ws, out_rank=None, stream=None):
+    _check("lora_orthogonalise", lib().lora_orthogonalise(
+        pool.ref, _ptr(adapters), M, max_rank, _ptr(src_pages), _ptr(out_pages), d, steps,
+        (_F32 * 3)(*coef), float(eps), _ptr(out_rank), _ptr(ws), ws.numel() * ws.element_size(),
+        _stream(stream)))
+
+
+def lora_orthogonal_step_workspace_bytes(M: int, max_rank: int, d_in: int, d_out: int) -> int:
+    return int(lib().lora_orthogonal_step_workspace_bytes(M, max_rank, d_in, d_out))
+
+
+def lora_orthogonal_step(pool: Pool, adapters, M: int, max_rank: int, a: FactorUpdate,
+                         b: FactorUpdate, momentum: float, nesterov: bool, steps: int, coef,
+                         eps: float, ws, out_rank=None, stream=None):
+    _check("lora_orthogonal_step", lib().lora_orthogonal_step(
+        pool.ref, _ptr(adapters), M, max_rank, a.ref, b.ref, float(momentum), int(nesterov), steps,
+        (_F32 * 3)(*coef), float(eps), _ptr(out_rank), _ptr(ws), ws.numel() * ws.element_size(),
+        _stream(stream)))

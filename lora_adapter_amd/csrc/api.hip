@@ -880,3 +880,93 @@ int32_t lora_grad_x_quantised(const void *dY, const lora_quantised_weight *W,
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------------ orthogonalised updates
+
+namespace {
+
+constexpr int32_t kMaxOrthAdapters = 16384;
+
+int32_t orth_args(const lora_pool_desc *pool, const int32_t *adapters, int32_t M, int32_t max_rank,
+                  int32_t steps, const float *coef, float eps, OrthArgs &a) {
+  const int32_t st = check_pool(pool, false);
+  if (st != LORA_OK) return st;
+  if (M < 0 || max_rank < 1 || max_rank > LORA_MAX_RANK || steps < 1 || steps > LORA_MAX_ORTH_STEPS || !coef)
+    return LORA_ERR_INVALID_ARG;
+  if (!(eps >= 1e-20f && eps <= 1e20f)) return LORA_ERR_INVALID_ARG;
+  if (M > kMaxOrthAdapters) return LORA_ERR_UNSUPPORTED;
+  if (M > 0 && !adapters) return LORA_ERR_INVALID_ARG;
+  a = OrthArgs{};
+  a.pool = pool_view(pool);
+  a.adapters = adapters;
+  a.M = M; a.max_rank = max_rank; a.steps = steps;
+  a.ca = coef[0]; a.cb = coef[1]; a.cc = coef[2]; a.eps = eps;
+  return LORA_OK;
+}
+
+int32_t orth_factor(const lora_factor_update *u, int32_t d, OrthFactor &f) {
+  if (!u || !u->pages || !u->momentum || !u->grad) return LORA_ERR_INVALID_ARG;
+  const void *b[4] = {u->pages, u->momentum, u->grad, u->master};
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < i; ++j)
+      if (b[i] && b[i] == b[j]) return LORA_ERR_INVALID_ARG;
+  f.src = u->grad; f.momentum = u->momentum; f.master = u->master; f.pages = u->pages;
+  f.d = d; f.lr = u->lr; f.keep = 1.0f - u->lr * u->decay;
+  return LORA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lora_orthogonalise_workspace_bytes(int32_t M, int32_t max_rank, int32_t d) {
+  if (M < 1 || M > kMaxOrthAdapters || max_rank < 1 || max_rank > LORA_MAX_RANK || !dims_ok(d)) return 0;
+  return align_up(orth_workspace_bytes(M, 1, max_rank, d));
+}
+
+int32_t lora_orthogonalise(const lora_pool_desc *pool, const int32_t *adapters, int32_t M,
+                           int32_t max_rank, const float *src_pages, float *out_pages, int32_t d,
+                           int32_t steps, const float *coef, float eps, int32_t *out_rank, void *ws,
+                           size_t ws_bytes, void *stream) {
+  OrthArgs a;
+  const int32_t st = orth_args(pool, adapters, M, max_rank, steps, coef, eps, a);
+  if (st != LORA_OK) return st;
+  if (!dims_ok(d)) return LORA_ERR_UNSUPPORTED;
+  if (M == 0) return LORA_OK;
+  if (!src_pages || !out_pages || src_pages == out_pages || !ws) return LORA_ERR_INVALID_ARG;
+  if (ws_bytes < lora_orthogonalise_workspace_bytes(M, max_rank, d)) return LORA_ERR_CAPACITY;
+  a.f[0].src = src_pages; a.f[0].out = out_pages; a.f[0].d = d;
+  a.out_rank = out_rank;
+  return dev(launch_orthogonal(a, 1, false, LORA_F32, ws, static_cast<hipStream_t>(stream)));
+}
+
+size_t lora_orthogonal_step_workspace_bytes(int32_t M, int32_t max_rank, int32_t d_in, int32_t d_out) {
+  if (M < 1 || M > kMaxOrthAdapters || max_rank < 1 || max_rank > LORA_MAX_RANK || !dims_ok(d_in) ||
+      !dims_ok(d_out))
+    return 0;
+  return align_up(orth_workspace_bytes(M, 2, max_rank, d_in > d_out ? d_in : d_out));
+}
+
+int32_t lora_orthogonal_step(const lora_pool_desc *pool, const int32_t *adapters, int32_t M,
+                             int32_t max_rank, const lora_factor_update *a_update,
+                             const lora_factor_update *b_update, float momentum, int32_t nesterov,
+                             int32_t steps, const float *coef, float eps, int32_t *out_rank, void *ws,
+                             size_t ws_bytes, void *stream) {
+  OrthArgs a;
+  int32_t st = orth_args(pool, adapters, M, max_rank, steps, coef, eps, a);
+  if (st != LORA_OK) return st;
+  if (!dims_ok(pool->d_in) || !dims_ok(pool->d_out)) return LORA_ERR_UNSUPPORTED;
+  if (M == 0) return LORA_OK;
+  if ((st = orth_factor(a_update, pool->d_in, a.f[0])) != LORA_OK) return st;
+  if ((st = orth_factor(b_update, pool->d_out, a.f[1])) != LORA_OK) return st;
+  if (a_update->pages == b_update->pages || a_update->momentum == b_update->momentum ||
+      (a_update->master && a_update->master == b_update->master) || !ws)
+    return LORA_ERR_INVALID_ARG;
+  if (ws_bytes < lora_orthogonal_step_workspace_bytes(M, max_rank, pool->d_in, pool->d_out))
+    return LORA_ERR_CAPACITY;
+  a.mu = momentum; a.nesterov = nesterov ? 1 : 0;
+  a.out_rank = out_rank;
+  return dev(launch_orthogonal(a, 2, true, pool->dtype, ws, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

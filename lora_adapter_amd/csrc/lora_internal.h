@@ -391,6 +391,40 @@ struct PlanLaunch {
 PlanLaunch plan_setup(const int32_t *ids, const float *gates, int T, int K, const PoolView &pool,
                       int32_t *plan, int nt, size_t lds_cap);
 
+// Orthogonalisation of factors (see orthogonal.hip).
+struct OrthRec {            // what the first launch leaves about each matrix
+  int32_t rank;             // 0: skipped
+  int32_t page_start;
+  float inv;                // 1 / (|N|_F + eps), or 0
+  int32_t adapter;
+};
+
+struct OrthFactor {
+  const float *src;         // [n_pages][d] the rows, or (step) the gradient
+  float *out;               // [n_pages][d] (orthogonalise alone)
+  float *momentum;          // step
+  float *master;            // step, or null
+  void *pages;              // step: the pool's pages
+  int d;
+  float lr, keep;           // page <- page . keep - lr . O
+};
+
+struct OrthArgs {
+  PoolView pool;            // rank, page_start, page_ids and their sizes
+  const int32_t *adapters;  // [M]
+  int M, max_rank;
+  OrthFactor f[2];          // matrices m of f[0], then of f[1]
+  int32_t *out_rank;        // [M] or null
+  int steps, nesterov;
+  float mu, ca, cb, cc, eps;
+  // set by the launcher
+  int R, chunks, chunk_cols;
+  OrthRec *rec;
+  float *q;                 // [matrices][R][R]
+  double *gram;             // [matrices][chunks][R][R]
+  double *big;              // [matrices][4][R][R], ranks over 64
+};
+
 // ----------------------------------------------------------------- launchers
 // Each returns hipSuccess or the launch error.
 hipError_t launch_plan(const int32_t *ids, const float *gates, int T, int K, const PoolView &pool,
@@ -467,6 +501,9 @@ size_t compress_workspace_bytes(int M, int d_in, int d_out, int n);
 hipError_t launch_compress(const PoolView &pool, const int32_t *adapters, int M, int n, int policy,
                            float ratio, float energy, int floor_rank, void *out_a, void *out_b,
                            int32_t *out_rank, float *out_sigma, void *ws, hipStream_t s);
+
+size_t orth_workspace_bytes(int M, int factors, int max_rank, int d);
+hipError_t launch_orthogonal(OrthArgs a, int factors, bool step, int dtype, void *ws, hipStream_t s);
 
 hipError_t launch_merge(const MergeArgs &a, int dtype, hipStream_t s);
 // n layers' merges (same list, each layer's own W and pool): one launch per

@@ -1,0 +1,582 @@
+// Newton-Schulz orthogonalisation of adapter factors, and the optimiser step
+// built on it.
+//
+// A factor is the r x d matrix N of one adapter's rank rows (its pages).  With
+// X_0 = N / (|N|_F + eps) each step is X <- (a I + b G + c G^2) X, G = X X^T,
+// which moves every singular value s to s (a + b s^2 + c s^4) and leaves the
+// singular vectors.  All the polynomials are in the one matrix G_0 and
+// commute, so with P_k = a I + b G_k + c G_k^2
+//   G_{k+1} = P_k G_k P_k,   Q_{k+1} = P_k Q_k,   X_n = Q_n X_0:
+// the steps run on r x r matrices alone, and N is read twice (once for G_0,
+// once for the product with Q_n) instead of twice per step.
+//
+// G_0 squares the condition: a singular value of 1e-3 of the norm has the
+// eigenvalue 1e-6, fp32 would know it to 6 %, and the steps amplify small
+// values (3.44 each at the usual coefficients).  G and the r x r products
+// therefore run in fp64 (v_mfma_f64_16x16x4_f64; products of fp32 inputs are
+// exact there): against the steps in 64 bits the result is off by 1e-6 where
+// an fp32 Gram matrix gives 2e-5 .. 2e-4, no more than the steps themselves
+// run in fp32 (5e-6 at rank 128).  Q N is fp32 (v_mfma_f32_16x16x4_f32).
+//
+// Launches: the Gram partials over column chunks (the optimiser step updates
+// the momentum in the same pass); the steps, one workgroup per matrix of rank
+// <= 64, all of it in LDS; the product with N (and the update of the pages).
+// Ranks over 64 take the momentum and the r x r products in launches of their
+// own, tiles of 32 x 32 over the GPU (14 for five steps).
+#include "lora_internal.h"
+
+namespace lora {
+namespace {
+
+typedef double f64x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kSmall = 64;      // ranks whose steps run in one workgroup
+
+// The adapter of list entry m if it can be taken: in range, rank 1..max_rank,
+// its page table consistent, and not listed before.  Called by every thread of
+// a workgroup of 256; ends with the same answer in all of them.
+__device__ __forceinline__ int orth_rank(const OrthArgs &a, int m, int *flag, int &adapter, int &ps) {
+  adapter = a.adapters[m];
+  ps = 0;
+  if (adapter < 0 || adapter >= a.pool.n_adapters) return 0;
+  const int r = a.pool.rank[adapter];
+  ps = a.pool.page_start[adapter];
+  if (r < 1 || r > a.max_rank || a.pool.page_start[adapter + 1] - ps != r || ps < 0 ||
+      int64_t(ps) + r > a.pool.n_page_ids)
+    return 0;
+  __syncthreads();
+  if (threadIdx.x == 0) *flag = 0;
+  __syncthreads();
+  bool bad = false;
+  for (int j = threadIdx.x; j < m; j += 256) bad |= a.adapters[j] == adapter;
+  for (int j = threadIdx.x; j < r; j += 256) {
+    const int p = a.pool.page_ids[ps + j];
+    bad |= p < 0 || p >= a.pool.n_pages;
+  }
+  if (bad) *flag = 1;
+  __syncthreads();
+  return *flag ? 0 : r;
+}
+
+// Eight columns of a row of N.  kStep: N from the gradient and the momentum
+// (which kUpdate moves on first); else the source row.
+template <bool kStep, bool kUpdate>
+__device__ __forceinline__ void load_n8(const OrthFactor &f, const OrthArgs &a, int64_t at, float v[8]) {
+  Elem<float>::load8(f.src + at, v);
+  if constexpr (kStep) {
+    float m[8];
+    Elem<float>::load8(f.momentum + at, m);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float mn = kUpdate ? a.mu * m[e] + v[e] : m[e];
+      m[e] = mn;
+      v[e] = a.nesterov ? v[e] + a.mu * mn : mn;
+    }
+    if constexpr (kUpdate) {
+      *reinterpret_cast<float4 *>(f.momentum + at) = make_float4(m[0], m[1], m[2], m[3]);
+      *reinterpret_cast<float4 *>(f.momentum + at + 4) = make_float4(m[4], m[5], m[6], m[7]);
+    }
+  }
+}
+
+// ------------------------------------------------------------ Gram partials
+// Row blocks bi .. bi+NB-1 against bj .. bj+NB-1 (16 rows each) over columns
+// [c0, c1).  A wave takes 32 columns at a time: lane l holds row l % 16 and
+// columns 8 (l / 16) .. +7 of every block, one MFMA step per column of the 8
+// (four columns each; the order of the sum over columns is free).  The four
+// waves' sums are added in wave order through LDS.
+template <int NB, bool kDiag, bool kStep, bool kUpdate>
+__device__ __forceinline__ void gram_body(const OrthArgs &a, const OrthFactor &f, int r, int ps, int bi,
+                                          int bj, int c0, int c1, double *out, double *red) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lr = lane & 15, lg = lane >> 4;
+  int64_t ri[NB], rj[kDiag ? 1 : NB];
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const int row = (bi + i) * 16 + lr;
+    ri[i] = row < r ? int64_t(a.pool.page_ids[ps + row]) * f.d : -1;
+    if constexpr (!kDiag) {
+      const int col = (bj + i) * 16 + lr;
+      rj[i] = col < r ? int64_t(a.pool.page_ids[ps + col]) * f.d : -1;
+    }
+  }
+  f64x4_t acc[NB][NB];
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) acc[i][j] = f64x4_t{0, 0, 0, 0};
+  for (int c = c0 + wave * 32; c < c1; c += 128) {
+    const int col = c + lg * 8;
+    float x[NB][8], y[kDiag ? 1 : NB][8];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
+      if (ri[i] >= 0) load_n8<kStep, kUpdate>(f, a, ri[i] + col, x[i]);
+      if constexpr (!kDiag) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[i][e] = 0.f;
+        if (rj[i] >= 0) load_n8<kStep, false>(f, a, rj[i] + col, y[i]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      double dx[NB];
+#pragma unroll
+      for (int i = 0; i < NB; ++i) dx[i] = double(x[i][e]);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const double dy = kDiag ? dx[j] : double(y[kDiag ? 0 : j][e]);
+#pragma unroll
+        for (int i = 0; i < (kDiag ? j + 1 : NB); ++i)
+          acc[i][j] = __builtin_amdgcn_mfma_f64_16x16x4f64(dx[i], dy, acc[i][j], 0, 0, 0);
+      }
+    }
+  }
+  // acc element v of lane l: row 4 v + l / 16, column l % 16 of its block
+  constexpr int S = 16 * NB;
+  for (int w = 0; w < 4; ++w) {
+    if (wave == w) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int i = 0; i < (kDiag ? j + 1 : NB); ++i)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            double *p = red + (i * 16 + 4 * v + lg) * S + j * 16 + lr;
+            *p = w == 0 ? acc[i][j][v] : *p + acc[i][j][v];
+          }
+    }
+    __syncthreads();
+  }
+  const int R = a.R;
+  for (int e = threadIdx.x; e < S * S; e += 256) {
+    const int i = e / S, j = e % S;
+    if (kDiag && i / 16 > j / 16) continue;
+    const int gi = bi * 16 + i, gj = bj * 16 + j;
+    if (gi < R && gj < R) out[int64_t(gi) * R + gj] = red[e];
+  }
+}
+
+// Grid: (column chunks x super-tiles, matrices).  Super-tiles are 64 x 64
+// blocks (si <= sj) of the Gram matrix; ranks <= 64 have the first only.
+template <bool kStep>
+__global__ __launch_bounds__(256) void gram_kernel(OrthArgs a) {
+  __shared__ double red[kSmall * kSmall];
+  __shared__ int flag;
+  const int m = blockIdx.y % a.M, fi = blockIdx.y / a.M;
+  const OrthFactor &f = a.f[fi];
+  int adapter, ps;
+  const int r = orth_rank(a, m, &flag, adapter, ps);
+  const int ck = blockIdx.x % a.chunks;
+  int st = blockIdx.x / a.chunks;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    a.rec[blockIdx.y] = OrthRec{r, ps, 0.f, adapter};
+    if (fi == 0 && a.out_rank) a.out_rank[m] = r;
+  }
+  if (r == 0) return;
+  const int c0 = int(int64_t(ck) * a.chunk_cols), c1 = min(f.d, c0 + a.chunk_cols);
+  double *out = a.gram + (int64_t(blockIdx.y) * a.chunks + ck) * a.R * a.R;
+  if (r <= kSmall) {
+    if (st > 0) return;
+    if (r <= 16) gram_body<1, true, kStep, kStep>(a, f, r, ps, 0, 0, c0, c1, out, red);
+    else if (r <= 32) gram_body<2, true, kStep, kStep>(a, f, r, ps, 0, 0, c0, c1, out, red);
+    else gram_body<4, true, kStep, kStep>(a, f, r, ps, 0, 0, c0, c1, out, red);
+    return;
+  }
+  // pair (si, sj), si <= sj, counted along columns sj
+  int sj = 0;
+  while (st > sj) { st -= sj + 1; ++sj; }
+  if (sj * kSmall >= r) return;
+  // the momentum of these ranks was moved on by its own launch
+  if (st == sj) gram_body<4, true, kStep, false>(a, f, r, ps, st * 4, sj * 4, c0, c1, out, red);
+  else gram_body<4, false, kStep, false>(a, f, r, ps, st * 4, sj * 4, c0, c1, out, red);
+}
+
+// Momentum of the matrices of rank over 64 (their Gram super-tiles read a row
+// several times, so it moves on in a launch of its own).  Grid: (columns,
+// matrices, rows).
+__global__ __launch_bounds__(256) void momentum_kernel(OrthArgs a) {
+  __shared__ int flag;
+  const int m = blockIdx.y % a.M;
+  const OrthFactor &f = a.f[blockIdx.y / a.M];
+  int adapter, ps;
+  const int r = orth_rank(a, m, &flag, adapter, ps);
+  if (r <= kSmall) return;
+  const int col = (blockIdx.x * 256 + threadIdx.x) * 8;
+  if (col >= f.d) return;
+  for (int row = blockIdx.z; row < r; row += gridDim.z) {
+    float v[8];
+    load_n8<true, true>(f, a, int64_t(a.pool.page_ids[ps + row]) * f.d + col, v);
+  }
+}
+
+// ------------------------------------------------------------ the steps, rank <= 64
+// Symmetric matrices of 16 NB rows in LDS, rows of S doubles (S = 16 NB + 4
+// puts the 8 rows x 4 columns that a half wave reads at once on distinct
+// banks).  Both operands of a product are read along rows (they are
+// symmetric), its upper tiles are computed, four waves taking them in turn,
+// and stored with their mirror images.
+template <int NB, int CT, typename Store>
+__device__ __forceinline__ void sym_tiles(const double *A, const double *B, int first, int n_tiles,
+                                          const Store &store) {
+  constexpr int S = 16 * NB + 4;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lr = lane & 15, lg = lane >> 4;
+  int ti[CT], tj[CT];
+  bool on[CT];
+  f64x4_t acc[CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    int t = wave + 4 * c - first;
+    on[c] = t >= 0 && t < n_tiles;
+    t = on[c] ? t : 0;
+    int j = 0;
+    while (t > j) { t -= j + 1; ++j; }
+    ti[c] = t; tj[c] = j;
+    acc[c] = f64x4_t{0, 0, 0, 0};
+  }
+#pragma unroll 4
+  for (int k = 0; k < 4 * NB; ++k) {
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+      acc[c] = __builtin_amdgcn_mfma_f64_16x16x4f64(A[(ti[c] * 16 + lr) * S + 4 * k + lg],
+                                                    B[(tj[c] * 16 + lr) * S + 4 * k + lg], acc[c], 0, 0, 0);
+  }
+#pragma unroll
+  for (int c = 0; c < CT; ++c)
+    if (on[c])
+#pragma unroll
+      for (int v = 0; v < 4; ++v) store(ti[c] * 16 + 4 * v + lg, tj[c] * 16 + lr, acc[c][v]);
+}
+
+template <int NB>
+__device__ __forceinline__ void steps_body(const OrthArgs &a, int mat, int r, double *lds) {
+  constexpr int n = 16 * NB, S = n + 4, NT = NB * (NB + 1) / 2, CT = (NT + 3) / 4;
+  double *G = lds, *P = G + n * S, *Q = P + n * S, *T = Q + n * S;
+  const int tid = threadIdx.x, R = a.R;
+  // the chunks' partials in order; elements below the diagonal tiles mirrored
+  for (int e = tid; e < n * n; e += 256) {
+    const int i = e / n, j = e % n;
+    double s = 0;
+    if (i < r && j < r) {
+      const bool up = i / 16 <= j / 16;
+      const double *p = a.gram + int64_t(mat) * a.chunks * R * R + (up ? int64_t(i) * R + j : int64_t(j) * R + i);
+      for (int c = 0; c < a.chunks; ++c) s += p[int64_t(c) * R * R];
+    }
+    G[i * S + j] = s;
+  }
+  __syncthreads();
+  double tr = 0;
+  for (int i = 0; i < r; ++i) tr += G[i * S + i];
+  // no rows to speak of: zero stays zero; a NaN or an infinity reaches every element
+  const double inv = tr == 0 ? 0.0 : 1.0 / (sqrt(tr) + double(a.eps));
+  if (tid == 0) a.rec[mat].inv = float(inv);
+  __syncthreads();
+  for (int e = tid; e < n * n; e += 256) G[(e / n) * S + e % n] *= inv * inv;
+  __syncthreads();
+  const double ca = a.ca, cb = a.cb, cc = a.cc;
+  auto put = [&](double *M, int i, int j, double v) {
+    M[i * S + j] = v;
+    if (i / 16 != j / 16) M[j * S + i] = v;
+  };
+  for (int k = 0; k < a.steps; ++k) {
+    const bool last = k + 1 == a.steps;
+    double *const F = k == 0 ? Q : P;       // the first factor is Q itself
+    sym_tiles<NB, CT>(G, G, 0, NT, [&](int i, int j, double v) {
+      put(F, i, j, (i == j ? ca : 0.0) + cb * G[i * S + j] + cc * v);
+    });
+    __syncthreads();
+    if (!last) {
+      sym_tiles<NB, CT>(F, G, 0, NT, [&](int i, int j, double v) { put(T, i, j, v); });
+      __syncthreads();
+      sym_tiles<NB, CT>(F, T, 0, NT, [&](int i, int j, double v) { put(G, i, j, v); });
+    }
+    if (k > 0) {
+      // Q <- P Q by way of T (free again after the barrier)
+      __syncthreads();
+      sym_tiles<NB, CT>(P, Q, 0, NT, [&](int i, int j, double v) { put(T, i, j, v); });
+      __syncthreads();
+      double *const t = Q; Q = T; T = t;
+    }
+    __syncthreads();
+  }
+  float *q = a.q + int64_t(mat) * R * R;
+  for (int e = tid; e < n * n; e += 256) {
+    const int i = e / n, j = e % n;
+    if (i < R && j < R) q[int64_t(i) * R + j] = float(Q[i * S + j]);
+  }
+}
+
+template <int NBMAX>
+__global__ __launch_bounds__(256) void steps_kernel(OrthArgs a) {
+  __shared__ double steps_lds[4 * (16 * NBMAX) * (16 * NBMAX + 4)];
+  const int mat = blockIdx.x, r = a.rec[mat].rank;
+  if (r < 1 || r > kSmall) return;
+  if (NBMAX == 1 || r <= 16) steps_body<1>(a, mat, r, steps_lds);
+  else if (NBMAX == 2 || r <= 32) steps_body<(NBMAX >= 2 ? 2 : 1)>(a, mat, r, steps_lds);
+  else steps_body<(NBMAX >= 4 ? 4 : 1)>(a, mat, r, steps_lds);
+}
+
+// ------------------------------------------------------------ ranks over 64
+// Sum of the chunks' partials, normalised, both halves filled.  Grid: (matrices).
+__global__ __launch_bounds__(256) void gram_sum_kernel(OrthArgs a) {
+  const int mat = blockIdx.x, r = a.rec[mat].rank, R = a.R;
+  if (r <= kSmall) return;
+  __shared__ double part[256];
+  const double *p = a.gram + int64_t(mat) * a.chunks * R * R;
+  double t = 0;
+  for (int i = threadIdx.x; i < r; i += 256)
+    for (int c = 0; c < a.chunks; ++c) t += p[int64_t(c) * R * R + int64_t(i) * R + i];
+  part[threadIdx.x] = t;
+  __syncthreads();
+  double tr = 0;
+  for (int i = 0; i < 256; ++i) tr += part[i];
+  const double inv = tr == 0 ? 0.0 : 1.0 / (sqrt(tr) + double(a.eps));
+  if (threadIdx.x == 0) a.rec[mat].inv = float(inv);
+  double *G = a.big + int64_t(mat) * 4 * R * R;
+  for (int64_t e = threadIdx.x; e < int64_t(R) * R; e += 256) {
+    const int i = int(e / R), j = int(e % R);
+    double s = 0;
+    if (i < r && j < r) {
+      const int64_t at = i / 16 <= j / 16 ? int64_t(i) * R + j : int64_t(j) * R + i;
+      for (int c = 0; c < a.chunks; ++c) s += p[int64_t(c) * R * R + at];
+    }
+    G[e] = s * (inv * inv);
+  }
+}
+
+// One product of symmetric R x R matrices of every matrix of rank over 64,
+// upper tiles of 32 x 32 (one 16 x 16 block per wave), stored with their
+// mirror images.  Buffers of a matrix: 0 G, 1 P, 2 and 3 Q and T in turn.
+struct SymOp {
+  int A, B, C;            // C = A . B
+  int poly;               // C = ca I + cb A + cc A . B
+  int copy;               // also into this buffer (-1: none)
+  int to_q;               // also, in fp32, into q
+};
+
+__global__ __launch_bounds__(256) void sym_product_kernel(OrthArgs a, SymOp op0, SymOp op1) {
+  const int mat = blockIdx.y, r = a.rec[mat].rank, R = a.R;
+  if (r <= kSmall) return;
+  const SymOp op = blockIdx.z == 0 ? op0 : op1;
+  int t = blockIdx.x, tj = 0;
+  while (t > tj) { t -= tj + 1; ++tj; }
+  if (tj * 32 >= r) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lr = lane & 15, lg = lane >> 4;
+  const int i0 = t * 32 + (wave >> 1) * 16, j0 = tj * 32 + (wave & 1) * 16;
+  if (i0 >= R || j0 >= R) return;
+  double *base = a.big + int64_t(mat) * 4 * R * R;
+  const double *A = base + int64_t(op.A) * R * R, *B = base + int64_t(op.B) * R * R;
+  const double *pa = A + int64_t(i0 + lr) * R + lg, *pb = B + int64_t(j0 + lr) * R + lg;
+  f64x4_t acc = {0, 0, 0, 0};
+  const int n = (r + 15) / 16 * 16;
+#pragma unroll 8
+  for (int k = 0; k < n; k += 4) acc = __builtin_amdgcn_mfma_f64_16x16x4f64(pa[k], pb[k], acc, 0, 0, 0);
+  double *C = base + int64_t(op.C) * R * R;
+  double *D = op.copy >= 0 ? base + int64_t(op.copy) * R * R : nullptr;
+  float *q = a.q + int64_t(mat) * R * R;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const int i = i0 + 4 * v + lg, j = j0 + lr;
+    double x = acc[v];
+    if (op.poly) x = (i == j ? double(a.ca) : 0.0) + double(a.cb) * A[int64_t(i) * R + j] + double(a.cc) * x;
+    const int64_t at = int64_t(i) * R + j, mir = int64_t(j) * R + i;
+    C[at] = x;
+    if (t != tj) C[mir] = x;
+    if (D) {
+      D[at] = x;
+      if (t != tj) D[mir] = x;
+    }
+    if (op.to_q) {
+      q[at] = float(x);
+      if (t != tj) q[mir] = float(x);
+    }
+  }
+}
+
+// ------------------------------------------------------------ the product with N
+// Rows ib*16 .. of O = Q (N inv): a wave takes 64 columns, lane l the four
+// columns 4 (l % 16) .. +3 of row l / 16 of every four, so a load is 256
+// contiguous bytes per row; column tile e holds columns 4 c + e, and the four
+// tiles' results are four consecutive columns again.
+template <int NB, bool kStep, typename E>
+__device__ __forceinline__ void apply_body(const OrthArgs &a, const OrthFactor &f, int r, int ps, float inv,
+                                           int ib, const float *q, int col0) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lr = lane & 15, lg = lane >> 4;
+  const int col = col0 + wave * 64 + lr * 4;
+  const int R = a.R;
+  if (col0 + wave * 64 >= f.d) return;
+  f32x4_t acc[NB][4];
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[i][e] = f32x4_t{0, 0, 0, 0};
+  const int nk = (r + 3) / 4;
+#pragma unroll 4
+  for (int k = 0; k < nk; ++k) {
+    const int row = 4 * k + lg;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (row < r) {
+      const int64_t at = int64_t(a.pool.page_ids[ps + row]) * f.d + col;
+      x = *reinterpret_cast<const float4 *>(f.src + at);
+      if constexpr (kStep) {
+        const float4 m = *reinterpret_cast<const float4 *>(f.momentum + at);
+        if (a.nesterov)
+          x = make_float4(x.x + a.mu * m.x, x.y + a.mu * m.y, x.z + a.mu * m.z, x.w + a.mu * m.w);
+        else
+          x = m;
+      }
+    }
+    const float b[4] = {x.x * inv, x.y * inv, x.z * inv, x.w * inv};
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int qi = min((ib + i) * 16 + lr, R - 1);
+      const float av = row < r ? q[int64_t(qi) * R + row] : 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        acc[i][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(av, b[e], acc[i][e], 0, 0, 0);
+    }
+  }
+  // acc element v of lane l: row 4 (l / 16) + v, column l % 16 of its tile
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int row = (ib + i) * 16 + lg * 4 + v;
+      if (row >= r) continue;
+      const int64_t at = int64_t(a.pool.page_ids[ps + row]) * f.d + col;
+      float o[4] = {acc[i][0][v], acc[i][1][v], acc[i][2][v], acc[i][3][v]};
+      if constexpr (!kStep) {
+        *reinterpret_cast<float4 *>(f.out + at) = make_float4(o[0], o[1], o[2], o[3]);
+      } else {
+        E *pg = static_cast<E *>(f.pages) + at;
+        float w[4];
+        if (f.master) {
+          const float4 mw = *reinterpret_cast<const float4 *>(f.master + at);
+          w[0] = mw.x; w[1] = mw.y; w[2] = mw.z; w[3] = mw.w;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = Elem<E>::load1(pg + e);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = w[e] * f.keep - f.lr * o[e];
+        if (f.master) *reinterpret_cast<float4 *>(f.master + at) = make_float4(w[0], w[1], w[2], w[3]);
+        if constexpr (sizeof(E) == 2)
+          *reinterpret_cast<uint2 *>(pg) = make_uint2(f2bf2(w[0], w[1]), f2bf2(w[2], w[3]));
+        else
+          *reinterpret_cast<float4 *>(pg) = make_float4(w[0], w[1], w[2], w[3]);
+      }
+    }
+}
+
+// Grid: (columns / 256, matrices, row blocks of 64).
+template <bool kStep, typename E>
+__global__ __launch_bounds__(256) void orth_apply_kernel(OrthArgs a) {
+  const OrthRec rc = a.rec[blockIdx.y];
+  const OrthFactor &f = a.f[blockIdx.y / a.M];
+  const int ib = blockIdx.z * 4;
+  if (rc.rank <= ib * 16) return;
+  const float *q = a.q + int64_t(blockIdx.y) * a.R * a.R;
+  const int col0 = blockIdx.x * 256;
+  if (rc.rank <= 16) apply_body<1, kStep, E>(a, f, rc.rank, rc.page_start, rc.inv, ib, q, col0);
+  else if (rc.rank <= 32) apply_body<2, kStep, E>(a, f, rc.rank, rc.page_start, rc.inv, ib, q, col0);
+  else apply_body<4, kStep, E>(a, f, rc.rank, rc.page_start, rc.inv, ib, q, col0);
+}
+
+int orth_r(int max_rank) { return (max_rank + 15) / 16 * 16; }
+
+// Column chunks of the Gram launch: enough workgroups to fill the GPU twice,
+// at least 256 columns each (two steps of each wave).
+int orth_chunk_cols(int64_t mats, int max_rank, int d) {
+  const int s = (max_rank + kSmall - 1) / kSmall;
+  const int64_t per = mats * (s * (s + 1) / 2);
+  const int64_t want = (512 + per - 1) / per;
+  int64_t cols = (d + want - 1) / want;
+  cols = (cols + 127) / 128 * 128;
+  return int(cols < 256 ? 256 : cols);
+}
+
+int orth_chunks(int64_t mats, int max_rank, int d) {
+  const int c = orth_chunk_cols(mats, max_rank, d);
+  return (d + c - 1) / c;
+}
+
+size_t pad256(size_t x) { return (x + 255) & ~size_t(255); }
+
+}  // namespace
+
+// Workspace: records, Q (fp32), Gram partials, and for ranks over 64 four r x
+// r matrices.
+size_t orth_workspace_bytes(int M, int factors, int max_rank, int d) {
+  const int64_t mats = int64_t(M) * factors;
+  const size_t RR = size_t(orth_r(max_rank)) * orth_r(max_rank);
+  size_t b = pad256(size_t(mats) * sizeof(OrthRec)) + pad256(size_t(mats) * RR * 4) +
+             pad256(size_t(mats) * orth_chunks(mats, max_rank, d) * RR * 8);
+  if (max_rank > kSmall) b += pad256(size_t(mats) * 4 * RR * 8);
+  return b;
+}
+
+hipError_t launch_orthogonal(OrthArgs a, int factors, bool step, int dtype, void *ws, hipStream_t s) {
+  const int64_t mats = int64_t(a.M) * factors;
+  int d = a.f[0].d;
+  if (factors > 1 && a.f[1].d > d) d = a.f[1].d;
+  a.R = orth_r(a.max_rank);
+  a.chunk_cols = orth_chunk_cols(mats, a.max_rank, d);
+  a.chunks = orth_chunks(mats, a.max_rank, d);
+  const size_t RR = size_t(a.R) * a.R;
+  char *p = static_cast<char *>(ws);
+  a.rec = reinterpret_cast<OrthRec *>(p);
+  p += pad256(size_t(mats) * sizeof(OrthRec));
+  a.q = reinterpret_cast<float *>(p);
+  p += pad256(size_t(mats) * RR * 4);
+  a.gram = reinterpret_cast<double *>(p);
+  p += pad256(size_t(mats) * a.chunks * RR * 8);
+  a.big = reinterpret_cast<double *>(p);
+  const bool big = a.max_rank > kSmall;
+  const int st = (a.max_rank + kSmall - 1) / kSmall;
+  if (big && step) {
+    const int rows = a.max_rank < 128 ? a.max_rank : 128;
+    hipLaunchKernelGGL(momentum_kernel, dim3(unsigned((d / 8 + 255) / 256), unsigned(mats), unsigned(rows)),
+                       dim3(256), 0, s, a);
+  }
+  const dim3 gg(unsigned(a.chunks * (st * (st + 1) / 2)), unsigned(mats));
+  if (step) hipLaunchKernelGGL(gram_kernel<true>, gg, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL(gram_kernel<false>, gg, dim3(256), 0, s, a);
+  if (a.max_rank <= 16) hipLaunchKernelGGL(steps_kernel<1>, dim3(unsigned(mats)), dim3(256), 0, s, a);
+  else if (a.max_rank <= 32) hipLaunchKernelGGL(steps_kernel<2>, dim3(unsigned(mats)), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL(steps_kernel<4>, dim3(unsigned(mats)), dim3(256), 0, s, a);
+  if (big) {
+    hipLaunchKernelGGL(gram_sum_kernel, dim3(unsigned(mats)), dim3(256), 0, s, a);
+    const int t32 = (a.R + 31) / 32;
+    const unsigned tiles = unsigned(t32 * (t32 + 1) / 2);
+    int Q = 2, T = 3;
+    for (int k = 0; k < a.steps; ++k) {
+      const bool last = k + 1 == a.steps;
+      // P (the first step's is Q too)
+      const SymOp poly{0, 0, 1, 1, k == 0 ? Q : -1, last && k == 0};
+      hipLaunchKernelGGL(sym_product_kernel, dim3(tiles, unsigned(mats), 1), dim3(256), 0, s, a, poly, poly);
+      // Q <- P Q; G <- P (P G), with P G through the free buffer of the two
+      const SymOp pq{1, Q, T, 0, -1, last};
+      if (k > 0) {
+        hipLaunchKernelGGL(sym_product_kernel, dim3(tiles, unsigned(mats), 1), dim3(256), 0, s, a, pq, pq);
+        const int t = Q; Q = T; T = t;
+      }
+      if (!last) {
+        const SymOp pg{1, 0, T, 0, -1, 0}, ppg{1, T, 0, 0, -1, 0};
+        hipLaunchKernelGGL(sym_product_kernel, dim3(tiles, unsigned(mats), 1), dim3(256), 0, s, a, pg, pg);
+        hipLaunchKernelGGL(sym_product_kernel, dim3(tiles, unsigned(mats), 1), dim3(256), 0, s, a, ppg, ppg);
+      }
+    }
+  }
+  const dim3 ga(unsigned((d + 255) / 256), unsigned(mats), unsigned(st));
+  if (!step) hipLaunchKernelGGL((orth_apply_kernel<false, float>), ga, dim3(256), 0, s, a);
+  else if (dtype == LORA_BF16) hipLaunchKernelGGL((orth_apply_kernel<true, uint16_t>), ga, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((orth_apply_kernel<true, float>), ga, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace lora
