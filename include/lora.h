@@ -524,7 +524,8 @@ int32_t lora_transpose(const void *src, void *dst, int32_t rows, int32_t cols, i
  * what is left of it; codes past the end are zero.
  * Layout: a row of d codes is lora_quantised_row_bytes(d) bytes (d rounded up
  * to 128), a row of scales lora_quantised_scale_bytes(d) bytes (ceil(d / 128)
- * rounded up to 4, zeros past the last block).  Buffers 16-byte aligned. */
+ * rounded up to 4, zeros past the last block).  Buffers 16-byte aligned.
+ * Weights at most 524288 wide (UNSUPPORTED beyond). */
 typedef struct {
   int32_t d_in, d_out;
   uint8_t *q_t;               /* [d_out][row_bytes(d_in)]  codes of W_t           */

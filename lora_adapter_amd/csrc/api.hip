@@ -690,6 +690,7 @@ namespace {
 int32_t check_weight(const lora_quantised_weight *w, const lora_pool_desc *pool) {
   if (!w) return LORA_ERR_INVALID_ARG;
   if (w->d_in != pool->d_in || w->d_out != pool->d_out) return LORA_ERR_INVALID_ARG;
+  if (w->d_in > kQMaxWidth || w->d_out > kQMaxWidth) return LORA_ERR_UNSUPPORTED;
   return LORA_OK;
 }
 
@@ -706,7 +707,7 @@ QuantTail quant_tail(int32_t T, int32_t d_k, int32_t d_n, int32_t dtype) {
   t.partial = align_up(gemm_partial_bytes(t.cfg, T, d_n));
   if (t.cfg.kind != 4) {
     t.codes = align_up(size_t(T) * size_t(q_row_bytes(d_k)));
-    t.scales = align_up(size_t(T) * size_t(q_scale_bytes(d_k)));
+    t.scales = align_up(size_t(q_tile_rows(T)) * size_t(q_row_bytes(d_k) / kQBlock));
   }
   t.total = t.partial + t.codes + t.scales;
   return t;
@@ -721,11 +722,12 @@ hipError_t run_quantised(const QuantTail &t, const void *rows, int32_t T, int32_
   q.g.k_split = t.cfg.k_split; q.g.sk_g = t.cfg.sk;
   q.g.partial = reinterpret_cast<float *>(tail);
   q.lda = q.ldb = q_row_bytes(d_k);
-  q.lsa = q.lsb = q_scale_bytes(d_k);
+  q.lsa = q_tile_rows(T);
+  q.lsb = q_scale_bytes(d_k);
   q.sb = scale;
   if (t.cfg.kind != 4) {
     uint8_t *c = reinterpret_cast<uint8_t *>(tail) + t.partial, *sc = c + t.codes;
-    const hipError_t e = launch_quantise_rows(rows, dtype, T, d_k, c, sc, s);
+    const hipError_t e = launch_quantise_rows(rows, dtype, T, d_k, c, sc, true, s);
     if (e != hipSuccess) return e;
     q.g.X = c;
     q.sa = sc;
@@ -785,7 +787,7 @@ int32_t lora_quantise_rows(const void *X, int32_t dtype, int32_t T, int32_t d, u
   if (!dims_ok(d)) return LORA_ERR_UNSUPPORTED;
   if (T == 0) return LORA_OK;
   if (!X || !codes || !scale || X == codes || X == scale || codes == scale) return LORA_ERR_INVALID_ARG;
-  return dev(launch_quantise_rows(X, dtype, T, d, codes, scale, static_cast<hipStream_t>(stream)));
+  return dev(launch_quantise_rows(X, dtype, T, d, codes, scale, false, static_cast<hipStream_t>(stream)));
 }
 
 int32_t lora_quantise_weight(const void *W_t, int32_t dtype, const lora_quantised_weight *w,
@@ -793,7 +795,8 @@ int32_t lora_quantise_weight(const void *W_t, int32_t dtype, const lora_quantise
   if (dtype != LORA_F32 && dtype != LORA_BF16) return LORA_ERR_INVALID_ARG;
   if (!W_t || !w || !w->q_t || !w->scale || (w->q == nullptr) != (w->scale_t == nullptr))
     return LORA_ERR_INVALID_ARG;
-  if (!dims_ok(w->d_in) || !dims_ok(w->d_out)) return LORA_ERR_UNSUPPORTED;
+  if (!dims_ok(w->d_in) || !dims_ok(w->d_out) || w->d_in > kQMaxWidth || w->d_out > kQMaxWidth)
+    return LORA_ERR_UNSUPPORTED;
   if (W_t == w->q_t || W_t == w->q || w->q == w->q_t) return LORA_ERR_INVALID_ARG;
   return dev(launch_quantise_weight(W_t, dtype, w->d_out, w->d_in, w->q_t, w->q, w->scale, w->scale_t,
                                     static_cast<hipStream_t>(stream)));

@@ -50,10 +50,10 @@ __device__ __forceinline__ bf16x8_t widen8(uint32_t lo, uint32_t hi) {
   return r;
 }
 
-template <int S>
+// cbsz = blgp = 0: both operands e4m3; SA, SB: the byte of each scale word.
+template <int SA, int SB>
 __device__ __forceinline__ f32x16_t mfma_q(i32x8_t a, i32x8_t b, f32x16_t c, int sa, int sb) {
-  // cbsz = blgp = 0: both operands e4m3; S: the byte of the scale words
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, S, sa, S, sb);
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, SA, sa, SB, sb);
 }
 
 // ------------------------------------------------------------ split-K tiles
@@ -122,7 +122,7 @@ __device__ __forceinline__ void q_split_tile(const QGemmArgs &q, int bx, int by,
           const int sa = int(ss[r]);
 #pragma unroll
           for (int s = 0; s < 2; ++s)
-            acc[b] = mfma_q<G>(join32(xa[2 * s], xa[2 * s + 1]), join32(wf[G][2 * s], wf[G][2 * s + 1]),
+            acc[b] = mfma_q<G, G>(join32(xa[2 * s], xa[2 * s + 1]), join32(wf[G][2 * s], wf[G][2 * s + 1]),
                                acc[b], sa, sw);
         } else {
           f32x16_t p;
@@ -178,18 +178,45 @@ __global__ __launch_bounds__(256) void q_split_kernel(QGemmArgs q) {
 // second half's MFMAs.  A fragment is 32 bytes per lane; the A fragments of
 // the next half replace each A block's registers after its last MFMA, the B
 // fragments alternate between two sets.
+// Scales: a stage ends with the 256 rows' bytes of its K tile, copied with the
+// codes (rows r, r + 32, r + 64, r + 96 of a group of 128 share a dword, so a
+// lane reads one for its four A blocks); the weight's bytes of the tile's
+// column blocks lie in an LDS table for the whole of K.  The loop has no
+// branch: with one, the compiler sinks the MFMAs past the copies and the
+// barrier they are to cover.
+template <int BM, int BN, int NS>
+struct QTileLds {
+  static constexpr int STAGE = (BM + BN) * 128 + BM;
+  static constexpr int TABLE = NS * STAGE;
+  static constexpr int TOTAL = TABLE + (BN / 128) * kQTableBytes;
+};
+
+// global_load_lds_dword: each lane copies 4 bytes to LDS at lds + 4 * lane
+// (waits and m0 as in lds_dma16).
+__device__ __forceinline__ void lds_dma4(const void *gptr, uint32_t lds) {
+  const uint32_t lds_s = __builtin_amdgcn_readfirstlane(lds);
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
+               :
+               : "v"(gptr), "s"(lds_s)
+               : "memory", "m0");
+}
+
 template <int BM, int BN, int WM, int WN, int NS, bool kFused, bool kMask = false>
 __device__ __forceinline__ void q_tile_run(const QGemmArgs &q, char *smem, int m0, int n0, int kt0,
                                            int nk, int slot) {
   using C = TileCfg<BM, BN, WM, WN>;
-  constexpr int TM = C::TM, TN = C::TN, NM = TM * TN;
-  static_assert(BN % 128 == 0 && (TN * 32 <= 128), "a wave's columns lie in one scale block");
+  using Q = QTileLds<BM, BN, NS>;
+  constexpr int TM = C::TM, TN = C::TN, NM = TM * TN, LPW = C::LPW + 1;
+  static_assert(BM == 256 && TM == 4, "a lane's scale word holds its wave's four row blocks");
+  static_assert(BN % 128 == 0 && TN * 32 <= 128, "a wave's columns lie in one scale block");
+  static_assert(NS >= 2 && (NS - 2) * LPW < 64, "stages / vmcnt range");
   const GemmArgs &g = q.g;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave / WN, wn = wave % WN;
   const int frow = lane & 31, half = lane >> 5, lrow = lane >> 3;
   const uint8_t *abase = static_cast<const uint8_t *>(g.X) + int64_t(m0) * q.lda + int64_t(kt0) * kQBlock;
   const uint8_t *bbase = static_cast<const uint8_t *>(g.W) + int64_t(n0) * q.ldb + int64_t(kt0) * kQBlock;
+  const uint8_t *sbase = q.sa + int64_t(kt0) * q.lsa + m0 + lane * 4;
   uint32_t aoff[C::A_INS], boff[C::B_INS];
 #pragma unroll
   for (int i = 0; i < C::A_INS; ++i) {
@@ -201,30 +228,28 @@ __device__ __forceinline__ void q_tile_run(const QGemmArgs &q, char *smem, int m
     const int row = (wave * C::B_INS + i) * 8 + lrow;
     boff[i] = uint32_t(min(row, g.N - 1 - n0)) * uint32_t(q.ldb) + tswz(row, lane & 7) * 16;
   }
+  // copy i of K tile kt: the wave's A rows, its B rows, the scale bytes (every
+  // wave copies all 256, so that no wave has a branch of its own)
   auto dma_one = [&](char *base, int kt, int i) __attribute__((always_inline)) {
     const uint32_t lds = lds_addr(base);
     if (i < C::A_INS)
       lds_dma16(abase + kt * kQBlock + aoff[i], lds + (wave * C::A_INS + i) * 1024);
-    else
+    else if (i < C::LPW)
       lds_dma16(bbase + kt * kQBlock + boff[i - C::A_INS],
                 lds + BM * C::ROWB + (wave * C::B_INS + i - C::A_INS) * 1024);
-  };
-  // scale words: the row's (this wave's row frow of each A block) and the
-  // weight block's, four K tiles per word
-  const uint8_t *sarow[TM];
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-    sarow[i] = q.sa + int64_t(min(m0 + wm * TM * 32 + i * 32 + frow, g.M - 1)) * q.lsa;
-  const uint8_t *sbrow = q.sb + int64_t(min(n0 + wn * TN * 32, g.N - 1) / kQBlock) * q.lsb;
-  const int gmax = int(q.lsb) / 4 - 1;
-  uint32_t sa[TM], sb, na[TM], nb;
-  auto load_scales = [&](int grp) __attribute__((always_inline)) {
-    const int o = min(grp, gmax) * 4;
-#pragma unroll
-    for (int i = 0; i < TM; ++i) na[i] = *reinterpret_cast<const uint32_t *>(sarow[i] + o);
-    nb = *reinterpret_cast<const uint32_t *>(sbrow + o);
+    else
+      lds_dma4(sbase + int64_t(kt) * q.lsa, lds + C::STAGE);
   };
 
+  EpiPre<TM> pre;
+  if constexpr (kFused) epi_fetch_desc<BM, BN, WM, WN>(g, m0, pre);
+  // the weight's scale bytes of the tile's column blocks, all of K
+  for (int o = tid * 4; o < int(q.lsb) * (BN / 128); o += C::NT * 4) {
+    const int blk = o / int(q.lsb), at = o % int(q.lsb);
+    const int row = min(n0 / kQBlock + blk, (g.N - 1) / kQBlock);
+    *reinterpret_cast<uint32_t *>(smem + Q::TABLE + blk * kQTableBytes + at) =
+        *reinterpret_cast<const uint32_t *>(q.sb + row * q.lsb + at);
+  }
   f32x16_t acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -232,9 +257,6 @@ __device__ __forceinline__ void q_tile_run(const QGemmArgs &q, char *smem, int m
     for (int j = 0; j < TN; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-  EpiPre<TM> pre;
-  if constexpr (kFused) epi_fetch_desc<BM, BN, WM, WN>(g, m0, pre);
-  load_scales(kt0 >> 2);
 
   i32x8_t fa[TM], fb0[TN], fb1[TN];
   auto frag = [&](const char *base, int s, int row) __attribute__((always_inline)) {
@@ -249,82 +271,61 @@ __device__ __forceinline__ void q_tile_run(const QGemmArgs &q, char *smem, int m
   auto frag_b = [&](const char *base, int s, int j) __attribute__((always_inline)) {
     return frag(base, s, BM + wn * TN * 32 + j * 32 + frow);
   };
+  auto scale_a = [&](const char *base) __attribute__((always_inline)) {
+    return *reinterpret_cast<const int *>(base + C::STAGE + wm * TM * 32 + frow * 4);
+  };
+  const char *table = smem + Q::TABLE + (wn * TN * 32 / kQBlock) * kQTableBytes + kt0;
   // MFMAs of one half of a K tile from (fa, xb); the next half's fragments
   // come from src (half s_next), the copies of K tile kn go into dst (kCopy)
   auto kstep = [&](auto copy, i32x8_t (&xb)[TN], i32x8_t (&yb)[TN], const char *src, int s_next,
-                   char *dst, int kn, int shift) __attribute__((always_inline)) {
+                   char *dst, int kn, int sa, int sb) __attribute__((always_inline)) {
     constexpr bool kCopy = decltype(copy)::value;
-    const int wsb = int(sb >> shift);
-    int wsa[TM];
-#pragma unroll
-    for (int i = 0; i < TM; ++i) wsa[i] = int(sa[i] >> shift);
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
       const int i = m / TN, j = m % TN;
-      acc[i][j] = mfma_q<0>(fa[i], xb[j], acc[i][j], wsa[i], wsb);
+      switch (i) {
+        case 0: acc[i][j] = mfma_q<0, 0>(fa[i], xb[j], acc[i][j], sa, sb); break;
+        case 1: acc[i][j] = mfma_q<1, 0>(fa[i], xb[j], acc[i][j], sa, sb); break;
+        case 2: acc[i][j] = mfma_q<2, 0>(fa[i], xb[j], acc[i][j], sa, sb); break;
+        default: acc[i][j] = mfma_q<3, 0>(fa[i], xb[j], acc[i][j], sa, sb); break;
+      }
       if (m < TN) yb[m] = frag_b(src, s_next, m);
       if (j == TN - 1) fa[i] = frag_a(src, s_next, i);
       if constexpr (kCopy) {
 #pragma unroll
-        for (int c = m * C::LPW / NM; c < (m + 1) * C::LPW / NM; ++c) dma_one(dst, kn, c);
+        for (int c = m * LPW / NM; c < (m + 1) * LPW / NM; ++c) dma_one(dst, kn, c);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
 #pragma unroll
   for (int p = 0; p < NS; ++p) {
-    if (p < nk) {
+    // (past the end: the last tile again, into a stage that no one reads)
 #pragma unroll
-      for (int c = 0; c < C::LPW; ++c) dma_one(smem + p * C::STAGE, p, c);
-    }
+    for (int c = 0; c < LPW; ++c) dma_one(smem + p * Q::STAGE, min(p, nk - 1), c);
   }
-  // the first tile (and the scale words, issued before it) has landed
   wait_vmcnt<0>();
+  // the table is in LDS and every wave's first tiles have landed
+  __syncthreads();
+  if constexpr (kFused) epi_fetch_pid(g, pre);
+  int sa = scale_a(smem), sb = uint8_t(table[0]);
 #pragma unroll
-  for (int i = 0; i < TM; ++i) asm volatile("" : "+v"(na[i]));
-  asm volatile("" : "+v"(nb));
+  for (int i = 0; i < TM; ++i) fa[i] = frag_a(smem, 0, i);
 #pragma unroll
-  for (int i = 0; i < TM; ++i) sa[i] = na[i];
-  sb = nb;
-  lds_bar();
-  if (nk > 0) {
-#pragma unroll
-    for (int i = 0; i < TM; ++i) fa[i] = frag_a(smem, 0, i);
-#pragma unroll
-    for (int j = 0; j < TN; ++j) fb0[j] = frag_b(smem, 0, j);
-  }
+  for (int j = 0; j < TN; ++j) fb0[j] = frag_b(smem, 0, j);
   int stage = 0;
   for (int kt = 0; kt < nk; ++kt) {
-    char *const cur = smem + stage * C::STAGE;
+    char *const cur = smem + stage * Q::STAGE;
     stage = stage + 1 == NS ? 0 : stage + 1;
-    char *const nxt = smem + stage * C::STAGE;
-    const int at = (kt0 + kt) & 3;
-    // the next word of scales goes out with its group's last tile
-    if (at == 3) load_scales((kt0 + kt + 1) >> 2);
-    kstep(std::false_type{}, fb0, fb1, cur, 1, cur, 0, 8 * at);
+    char *const nxt = smem + stage * Q::STAGE;
+    kstep(std::false_type{}, fb0, fb1, cur, 1, cur, 0, sa, sb);
     // tile kt + 1 has landed: everything but the copies of kt + 2 .. kt + NS - 1
-    wait_vmcnt<(NS - 2) * C::LPW>();
-    if (at == 3) {
-      // a use here: the loads' wait falls where nothing else is in flight
-#pragma unroll
-      for (int i = 0; i < TM; ++i) asm volatile("" : "+v"(na[i]));
-      asm volatile("" : "+v"(nb));
-    }
+    wait_vmcnt<(NS - 2) * LPW>();
     lds_bar();
-    if constexpr (kFused) {
-      if (kt == 0) epi_fetch_pid(g, pre);
-    }
-    // past the end the body stays the same: the copy repeats the last tile
-    // into a stage that no one reads again, the fragments go unused
-    kstep(std::true_type{}, fb1, fb0, nxt, 0, cur, min(kt + NS, nk - 1), 8 * at);
-    if (at == 3) {
-#pragma unroll
-      for (int i = 0; i < TM; ++i) sa[i] = na[i];
-      sb = nb;
-    }
-  }
-  if constexpr (kFused) {
-    if (nk <= 0) epi_fetch_pid(g, pre);
+    const int na = scale_a(nxt), nb = uint8_t(table[min(kt + 1, nk - 1)]);
+    kstep(std::true_type{}, fb1, fb0, nxt, 0, cur, min(kt + NS, nk - 1), sa, sb);
+    sa = na;
+    sb = nb;
   }
   // the last copies have landed and every wave is done with the stages
   wait_vmcnt<0>();
@@ -354,8 +355,7 @@ __device__ __forceinline__ void q_tile_run(const QGemmArgs &q, char *smem, int m
 // them), or g.k_split of K per blockIdx.y.
 template <int BM, int BN, int WM, int WN, int NS, bool kFused, bool kMask = false>
 __global__ __launch_bounds__(WM * WN * 64, 1) void q_tile_kernel(QGemmArgs q) {
-  using C = TileCfg<BM, BN, WM, WN>;
-  __shared__ __attribute__((aligned(16))) char smem[NS * C::STAGE];
+  __shared__ __attribute__((aligned(16))) char smem[QTileLds<BM, BN, NS>::TOTAL];
   const GemmArgs &g = q.g;
   const int tiles_m = (g.M + BM - 1) / BM, tiles_n = (g.N + BN - 1) / BN;
   const int ntiles = tiles_m * tiles_n;
@@ -382,6 +382,7 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void q_tile_kernel(QGemmArgs q) {
   int tm, tn;
   tile_coords(t, tiles_m, tiles_n, tm, tn);
   const int k0 = blockIdx.y * (g.k_split / kQBlock);
+  if (k0 >= KT) return;
   q_tile_run<BM, BN, WM, WN, NS, kFused, kMask>(q, smem, tm * BM, tn * BN, k0,
                                                 min(KT - k0, g.k_split / kQBlock), blockIdx.y);
 }
@@ -451,8 +452,8 @@ hipError_t launch_quantised_gemm(const GemmConfig &c, const QGemmArgs &q, int dt
   const int tiles = ((g.M + c.bm - 1) / c.bm) * ((g.N + c.bn - 1) / c.bn);
   if (c.kind == 5) {
     const dim3 grid(8 * ((tiles + 7) / 8));
-    if (g.mask) hipLaunchKernelGGL((q_tile_kernel<256, 256, 2, 2, 2, true, true>), grid, dim3(256), 0, s, q);
-    else hipLaunchKernelGGL((q_tile_kernel<256, 256, 2, 2, 2, true>), grid, dim3(256), 0, s, q);
+    if (g.mask) hipLaunchKernelGGL((q_tile_kernel<256, 256, 2, 4, 2, true, true>), grid, dim3(512), 0, s, q);
+    else hipLaunchKernelGGL((q_tile_kernel<256, 256, 2, 4, 2, true>), grid, dim3(512), 0, s, q);
     return hipGetLastError();
   }
   if (c.kind == 6 && !g.mask) {

@@ -271,10 +271,10 @@ struct GemmArgs {
 // codes.  Scale rows hold one exponent byte per 128 of K.
 struct QGemmArgs {
   GemmArgs g;
-  const uint8_t *sa;        // [M][lsa] scale bytes of the rows' codes (tiles)
+  const uint8_t *sa;        // tiles: the rows' scale bytes (q_tile_scale_at), lsa per K tile
   const uint8_t *sb;        // [ceil(N/128)][lsb] scale bytes of the weight's blocks
   int64_t lda, ldb;         // bytes per row of codes (K padded to whole blocks)
-  int64_t lsa, lsb;         // bytes per row of scales (a multiple of 4)
+  int64_t lsa, lsb;         // bytes per K tile of row scales, per row of weight scales
 };
 
 struct EpilogueArgs {

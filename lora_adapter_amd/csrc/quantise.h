@@ -8,12 +8,22 @@
 namespace lora {
 
 constexpr int kQBlock = 128;              // columns (and, for weights, rows) per scale
+constexpr int kQTableBytes = 4096;        // a weight row's scale bytes in the tile GEMM's LDS table
+constexpr int kQMaxWidth = kQTableBytes * kQBlock;
 
 // Bytes of a row of codes (a multiple of the block) and of a row of scale
 // bytes (a multiple of 4, so that a dword holds four blocks' scales).
 __host__ __device__ inline int64_t q_row_bytes(int64_t d) { return (d + kQBlock - 1) / kQBlock * kQBlock; }
 __host__ __device__ inline int64_t q_scale_bytes(int64_t d) {
   return ((d + kQBlock - 1) / kQBlock + 3) / 4 * 4;
+}
+
+// Scale bytes of quantised rows as the tile GEMM copies them: one run per K
+// tile (block) of the rows padded to whole tiles of 256; in each group of 128
+// rows, rows r, r + 32, r + 64 and r + 96 share a dword.
+__host__ __device__ inline int64_t q_tile_rows(int64_t T) { return (T + 255) / 256 * 256; }
+__host__ __device__ inline int64_t q_tile_scale_at(int64_t T, int64_t t, int64_t blk) {
+  return blk * q_tile_rows(T) + (t & ~int64_t(127)) + (t & 31) * 4 + ((t >> 5) & 3);
 }
 
 namespace {
@@ -66,7 +76,7 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
 }  // namespace
 
 hipError_t launch_quantise_rows(const void *X, int dtype, int T, int d, uint8_t *codes,
-                                uint8_t *scale, hipStream_t s);
+                                uint8_t *scale, bool tiled, hipStream_t s);
 hipError_t launch_quantise_weight(const void *W_t, int dtype, int d_out, int d_in, uint8_t *q_t,
                                   uint8_t *q, uint8_t *scale, uint8_t *scale_t, hipStream_t s);
 

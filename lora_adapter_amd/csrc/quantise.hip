@@ -8,8 +8,9 @@ namespace lora {
 namespace {
 
 // One wave per 512 columns of a row, 8 elements per lane; 16 lanes share a
-// block.  Columns past d are zero codes.
-template <typename E>
+// block.  Columns past d are zero codes.  kTiled: scale bytes laid out for the
+// tile GEMM (q_tile_scale_at), else in rows.
+template <typename E, bool kTiled>
 __global__ __launch_bounds__(256) void quantise_rows_kernel(const E *X, int T, int d, int chunks,
                                                             uint8_t *codes, uint8_t *scale) {
   const int64_t w = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
@@ -23,7 +24,12 @@ __global__ __launch_bounds__(256) void quantise_rows_kernel(const E *X, int T, i
   const uint32_t byte = q_scale_byte(max16(abs_max8(v)));
   if (col < ld) *reinterpret_cast<uint2 *>(codes + t * ld + col) = q_encode8(v, byte);
   const int blk = col / kQBlock;
-  if ((lane & 15) == 0 && blk < ls) scale[t * ls + blk] = col < ld ? uint8_t(byte) : uint8_t(0);
+  if ((lane & 15) != 0) return;
+  if constexpr (kTiled) {
+    if (col < ld) scale[q_tile_scale_at(T, t, blk)] = uint8_t(byte);
+  } else {
+    if (blk < ls) scale[t * ls + blk] = col < ld ? uint8_t(byte) : uint8_t(0);
+  }
 }
 
 // 4 x 4 bytes turned: o[j] = byte j of each of d[0..3].
@@ -118,16 +124,20 @@ __global__ __launch_bounds__(256) void quantise_weight_kernel(const E *W, int d_
 }  // namespace
 
 hipError_t launch_quantise_rows(const void *X, int dtype, int T, int d, uint8_t *codes,
-                                uint8_t *scale, hipStream_t s) {
+                                uint8_t *scale, bool tiled, hipStream_t s) {
   // whole scale rows: the padding bytes past the last block are written too
   const int chunks = int((q_scale_bytes(d) + 3) / 4);
   const dim3 grid(unsigned((int64_t(T) * chunks + 3) / 4)), block(256);
-  if (dtype == LORA_BF16)
-    hipLaunchKernelGGL(quantise_rows_kernel<uint16_t>, grid, block, 0, s,
-                       static_cast<const uint16_t *>(X), T, d, chunks, codes, scale);
+  const uint16_t *xb = static_cast<const uint16_t *>(X);
+  const float *xf = static_cast<const float *>(X);
+  if (dtype == LORA_BF16 && tiled)
+    hipLaunchKernelGGL((quantise_rows_kernel<uint16_t, true>), grid, block, 0, s, xb, T, d, chunks, codes, scale);
+  else if (dtype == LORA_BF16)
+    hipLaunchKernelGGL((quantise_rows_kernel<uint16_t, false>), grid, block, 0, s, xb, T, d, chunks, codes, scale);
+  else if (!tiled)
+    hipLaunchKernelGGL((quantise_rows_kernel<float, false>), grid, block, 0, s, xf, T, d, chunks, codes, scale);
   else
-    hipLaunchKernelGGL(quantise_rows_kernel<float>, grid, block, 0, s, static_cast<const float *>(X),
-                       T, d, chunks, codes, scale);
+    return hipErrorInvalidConfiguration;
   return hipGetLastError();
 }
 
