@@ -329,6 +329,19 @@ int32_t forward_args(const int32_t *ids, const float *gates, int32_t T, int32_t 
   return LORA_OK;
 }
 
+SlotShrinkArgs slot_shrink_args(const int32_t *ids, const float *gates, int32_t T, int32_t K,
+                                const void *X, const uint8_t *keep_mask, float keep_scale,
+                                const lora_pool_desc *pool, const ApplyWs &w) {
+  SlotShrinkArgs ss{};
+  ss.ids = ids; ss.gates = gates; ss.K = K; ss.N = pool->n_adapters;
+  ss.Z = X; ss.mask = keep_mask; ss.extra_scale = keep_mask ? keep_scale : 1.0f;
+  ss.d = pool->d_in; ss.pages = pool->a_pages;
+  ss.rank = pool->rank; ss.page_start = pool->page_start; ss.page_ids = pool->page_ids;
+  ss.scale = pool->scale; ss.n_pages = pool->n_pages; ss.n_page_ids = pool->n_page_ids;
+  ss.out = w.slot_u; ss.stride = LORA_MAX_RANK; ss.n_slots = T * K; ss.sdesc = w.sdesc;
+  return ss;
+}
+
 PlanLaunch forward_plan(const int32_t *ids, const float *gates, int32_t T, int32_t K,
                         const lora_pool_desc *pool, void *plan, const Fwd &f, const ApplyWs &w) {
   PlanLaunch pl = plan_setup(ids, gates, T, K, pool_view(pool), static_cast<int32_t *>(plan), 256,
@@ -354,13 +367,7 @@ int32_t lora_forward_gemm(const int32_t *ids, const float *gates, int32_t T, int
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const ApplyWs w = apply_layout(ws, ws_bytes, T, K, pool->d_in, pool->d_out, pool->dtype);
   if (w.slot_u) {
-    SlotShrinkArgs ss{};
-    ss.ids = ids; ss.gates = gates; ss.K = K; ss.N = pool->n_adapters;
-    ss.Z = X; ss.mask = keep_mask; ss.extra_scale = keep_mask ? keep_scale : 1.0f;
-    ss.d = pool->d_in; ss.pages = pool->a_pages;
-    ss.rank = pool->rank; ss.page_start = pool->page_start; ss.page_ids = pool->page_ids;
-    ss.scale = pool->scale; ss.n_pages = pool->n_pages; ss.n_page_ids = pool->n_page_ids;
-    ss.out = w.slot_u; ss.stride = LORA_MAX_RANK; ss.n_slots = T * K; ss.sdesc = w.sdesc;
+    const SlotShrinkArgs ss = slot_shrink_args(ids, gates, T, K, X, keep_mask, keep_scale, pool, w);
     return dev(launch_decode_slot_plan(f.cfg, f.g, ss,
                                        forward_plan(ids, gates, T, K, pool, plan, f, w), s));
   }
@@ -713,11 +720,10 @@ QuantTail quant_tail(int32_t T, int32_t d_k, int32_t d_n, int32_t dtype) {
   return t;
 }
 
-// Rows [T][d_k] times the weight's codes [d_n][..] in two or one launches
-// (quantise the rows, GEMM); `tail` the tail's memory.
-hipError_t run_quantised(const QuantTail &t, const void *rows, int32_t T, int32_t d_k, int32_t d_n,
-                         const uint8_t *codes, const uint8_t *scale, int32_t dtype, char *tail,
-                         QGemmArgs &q, hipStream_t s) {
+// Fills q for rows [T][d_k] times the weight's codes [d_n][..]; `tail` the
+// tail's memory.  For the tile forms q.g.X is where the rows' codes go.
+void quantised_args(const QuantTail &t, const void *rows, int32_t T, int32_t d_k, int32_t d_n,
+                    const uint8_t *codes, const uint8_t *scale, char *tail, QGemmArgs &q) {
   q.g.X = rows; q.g.W = codes; q.g.M = T; q.g.N = d_n; q.g.Kd = d_k;
   q.g.k_split = t.cfg.k_split; q.g.sk_g = t.cfg.sk;
   q.g.partial = reinterpret_cast<float *>(tail);
@@ -726,11 +732,20 @@ hipError_t run_quantised(const QuantTail &t, const void *rows, int32_t T, int32_
   q.lsb = q_scale_bytes(d_k);
   q.sb = scale;
   if (t.cfg.kind != 4) {
-    uint8_t *c = reinterpret_cast<uint8_t *>(tail) + t.partial, *sc = c + t.codes;
-    const hipError_t e = launch_quantise_rows(rows, dtype, T, d_k, c, sc, true, s);
+    q.g.X = tail + t.partial;
+    q.sa = reinterpret_cast<const uint8_t *>(tail) + t.partial + t.codes;
+  }
+}
+
+uint8_t *codes_of(const QGemmArgs &q) { return static_cast<uint8_t *>(const_cast<void *>(q.g.X)); }
+uint8_t *scales_of(const QGemmArgs &q) { return const_cast<uint8_t *>(q.sa); }
+
+// The product: the rows quantised (tile forms), then the GEMM.
+hipError_t run_quantised(const QuantTail &t, const void *rows, int32_t dtype, const QGemmArgs &q,
+                         hipStream_t s) {
+  if (t.cfg.kind != 4) {
+    const hipError_t e = launch_quantise_rows(rows, dtype, q.g.M, q.g.Kd, codes_of(q), scales_of(q), true, s);
     if (e != hipSuccess) return e;
-    q.g.X = c;
-    q.sa = sc;
   }
   return launch_quantised_gemm(t.cfg, q, dtype, s);
 }
@@ -742,7 +757,7 @@ struct QuantApply {
   QuantTail t;
   ApplyWs w;
   QGemmArgs q;
-  char *tail;
+  size_t head;            // bytes of the head
 };
 
 int32_t quant_apply_args(const void *X, const lora_quantised_weight *W, void *Y, int32_t T,
@@ -757,12 +772,12 @@ int32_t quant_apply_args(const void *X, const lora_quantised_weight *W, void *Y,
   if (!X || !Y || !W->q_t || !W->scale || !gates || !ws || Y == X) return LORA_ERR_INVALID_ARG;
   a.t = quant_tail(T, pool->d_in, pool->d_out, pool->dtype);
   if (ws_bytes < a.t.total) return LORA_ERR_CAPACITY;
-  const size_t head = (ws_bytes - a.t.total) / kAlign * kAlign;
+  const size_t head = a.head = (ws_bytes - a.t.total) / kAlign * kAlign;
   GemmConfig base;
   a.q = QGemmArgs{};
   if ((st = base_args(X, W->q_t, Y, T, K, pool, plan, ws, head, base, a.q.g)) != LORA_OK) return st;
   a.w = apply_layout(ws, head, T, K, pool->d_in, pool->d_out, pool->dtype);
-  a.tail = static_cast<char *>(ws) + head;
+  quantised_args(a.t, X, T, pool->d_in, pool->d_out, W->q_t, W->scale, static_cast<char *>(ws) + head, a.q);
   return LORA_OK;
 }
 
@@ -820,8 +835,7 @@ int32_t lora_apply_quantised(const void *X, const lora_quantised_weight *W, void
   const PlanView pv = plan_view(plan, TK, pool->n_adapters);
   hipError_t e = launch_shrink(apply_shrink_args(X, keep_mask, keep_scale, T, K, gates, pool, pv, a.w),
                                pool->dtype, TK, pool->n_adapters, pool->d_in, pool->d_out, s);
-  if (e == hipSuccess)
-    e = run_quantised(a.t, X, T, pool->d_in, pool->d_out, W->q_t, W->scale, pool->dtype, a.tail, a.q, s);
+  if (e == hipSuccess) e = run_quantised(a.t, X, pool->dtype, a.q, s);
   if (e == hipSuccess) e = launch_epilogue(a.t.cfg, quant_epilogue_args(a.q), pool->dtype, s);
   return dev(e);
 }
@@ -834,9 +848,43 @@ int32_t lora_forward_quantised(const int32_t *ids, const float *gates, int32_t T
   QuantApply a;
   int32_t st = quant_apply_args(X, W, Y, T, K, gates, pool, plan, ws, ws_bytes, a);
   if (st != LORA_OK) return st;
-  if ((st = lora_plan(ids, gates, T, K, pool, plan, plan_bytes, stream)) != LORA_OK) return st;
-  return lora_apply_quantised(X, W, Y, T, K, gates, keep_mask, keep_scale, pool, plan, ws, ws_bytes,
-                              stream);
+  if (plan_bytes < lora_plan_bytes(T, K, pool->n_adapters)) return LORA_ERR_CAPACITY;
+  if (T == 0) return lora_plan(ids, gates, T, K, pool, plan, plan_bytes, stream);
+  if (!ids) return LORA_ERR_INVALID_ARG;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const PoolView pv = pool_view(pool);
+  int32_t *const p = static_cast<int32_t *>(plan);
+  hipError_t e;
+  if (quantised_gemm_plan_fusable(a.t.cfg)) {
+    // the plan beside the GEMM
+    PlanLaunch pl = plan_setup(ids, gates, T, K, pv, p, 256, quantised_plan_lds_cap(a.t.cfg));
+    if (a.t.cfg.kind == 4 && pool->dtype == LORA_BF16) {
+      // decode: the per-slot shrink too, whose U the epilogue moves to the plan's places
+      pl.a.no_sched = 1;
+      const SlotShrinkArgs ss = slot_shrink_args(ids, gates, T, K, X, keep_mask, keep_scale, pool, a.w);
+      e = launch_quantised_gemm_plan(a.t.cfg, a.q, &ss, pl, pool->dtype, s);
+      if (e == hipSuccess)
+        e = launch_epilogue_ucopy(a.t.cfg, a.q.g, pool->dtype, a.w.slot_u, a.w.sdesc, a.w.U, a.w.u_cap, s);
+      return dev(e);
+    }
+    e = a.t.cfg.kind == 4 ? hipSuccess
+                          : launch_quantise_rows(X, pool->dtype, T, pool->d_in, codes_of(a.q), scales_of(a.q),
+                                                 true, s);
+    if (e == hipSuccess) e = launch_quantised_gemm_plan(a.t.cfg, a.q, nullptr, pl, pool->dtype, s);
+    if (e != hipSuccess) return LORA_ERR_DEVICE;
+    if ((st = lora_shrink(X, keep_mask, keep_scale, T, K, gates, pool, plan, ws, a.head, stream)) != LORA_OK)
+      return st;
+  } else {
+    // the plan beside the rows' quantisation, then U for the GEMM's epilogue
+    const PlanLaunch pl = plan_setup(ids, gates, T, K, pv, p, kPlanThreads, kQPlanRowsLds);
+    e = launch_quantise_plan(X, T, pool->d_in, codes_of(a.q), scales_of(a.q), pl, s);
+    if (e != hipSuccess) return LORA_ERR_DEVICE;
+    if ((st = lora_shrink(X, keep_mask, keep_scale, T, K, gates, pool, plan, ws, a.head, stream)) != LORA_OK)
+      return st;
+    e = launch_quantised_gemm(a.t.cfg, a.q, pool->dtype, s);
+    if (e != hipSuccess) return LORA_ERR_DEVICE;
+  }
+  return dev(launch_epilogue(a.t.cfg, quant_epilogue_args(a.q), pool->dtype, s));
 }
 
 size_t lora_grad_x_quantised_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out, int32_t dtype) {
@@ -875,8 +923,8 @@ int32_t lora_grad_x_quantised(const void *dY, const lora_quantised_weight *W,
   q.g.ex.u_cap = TK * max_rank;
   if (t.cfg.fused) q.g.mask = keep_mask;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t e = run_quantised(t, dY, T, pool->d_out, pool->d_in, W->q, W->scale_t, pool->dtype,
-                               static_cast<char *>(ws), q, s);
+  quantised_args(t, dY, T, pool->d_out, pool->d_in, W->q, W->scale_t, static_cast<char *>(ws), q);
+  hipError_t e = run_quantised(t, dY, pool->dtype, q, s);
   if (e == hipSuccess && !t.cfg.fused)
     e = launch_grad_x_epilogue(t.cfg, quant_epilogue_args(q), pool->dtype, keep_mask, s);
   return dev(e);

@@ -23,7 +23,9 @@
 //     tiles that write fp32 partials: rows quantised ahead by one launch.
 #include "gemm_tile.h"
 #include "lora_internal.h"
+#include "plan_build.h"
 #include "quantise.h"
+#include "shrink_units.h"
 
 namespace lora {
 namespace {
@@ -168,6 +170,36 @@ __global__ __launch_bounds__(256) void q_split_kernel(QGemmArgs q) {
   __shared__ __attribute__((aligned(16))) uint8_t xs[MB * 32 * kQDecodeKC];
   __shared__ uint32_t ss[MB * 32];
   q_split_tile<E, MB>(q, blockIdx.x, blockIdx.y, blockIdx.z, xs, ss);
+}
+
+// The same tiles with the plan built by the launch's first workgroup (in the
+// LDS of the token rows) and, for bf16 decode batches, the per-slot shrink
+// after the tiles, four workgroups per slot: a decode forward is then this
+// launch and the epilogue.  No part reads what another writes.
+constexpr size_t kQPlanLds = 32 << 10;    // at least this for the plan
+
+template <int MB>
+struct QSplitLds {
+  static constexpr size_t XS = size_t(MB) * 32 * kQDecodeKC, SS = size_t(MB) * 32 * 4;
+  static constexpr size_t TOTAL = XS + SS > kQPlanLds ? XS + SS : kQPlanLds;
+};
+
+template <typename E, int MB, bool kMask, bool kLds>
+__global__ __launch_bounds__(256) void q_split_plan_kernel(QGemmArgs q, SlotShrinkArgs ss, PlanArgs pa,
+                                                            int gx, int gy, int n_gemm) {
+  using L = QSplitLds<MB>;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[L::TOTAL];
+  const int t = int(blockIdx.x) - 1;
+  if (t < 0) {
+    plan_build<kLds>(pa, reinterpret_cast<int *>(lds));
+    return;
+  }
+  if (t < n_gemm) {
+    q_split_tile<E, MB>(q, t % gx, (t / gx) % gy, t / (gx * gy), lds,
+                        reinterpret_cast<uint32_t *>(lds + L::XS));
+    return;
+  }
+  if constexpr (sizeof(E) == 2) slot_shrink_part<kMask>(ss, (t - n_gemm) / kSlotParts, (t - n_gemm) % kSlotParts);
 }
 
 // ------------------------------------------------------------ pipelined tiles
@@ -350,9 +382,41 @@ __device__ __forceinline__ void q_tile_run(const QGemmArgs &q, char *smem, int m
   }
 }
 
+// Stream-K over g.sk_g workgroups: workgroup w takes the units (tile, K tile)
+// [w U / G, (w + 1) U / G), the pieces as the epilogue counts them.
+template <int BM, int BN, int WM, int WN, int NS>
+__device__ __forceinline__ void q_stream_k(const QGemmArgs &q, char *smem, int w) {
+  const GemmArgs &g = q.g;
+  const int tiles_n = (g.N + BN - 1) / BN;
+  const int ntiles = ((g.M + BM - 1) / BM) * tiles_n;
+  const int KT = int(q.ldb) / kQBlock;
+  const int64_t U = int64_t(ntiles) * KT;
+  int64_t u = int64_t(w) * U / g.sk_g;
+  const int64_t u1 = int64_t(w + 1) * U / g.sk_g;
+  while (u < u1) {
+    const int t = int(u / KT), kb = int(u % KT);
+    const int ke = int(min<int64_t>(KT, kb + (u1 - u)));
+    const int wf = int(((int64_t(t) * KT + 1) * g.sk_g - 1) / U);
+    q_tile_run<BM, BN, WM, WN, NS, false>(q, smem, (t / tiles_n) * BM, (t % tiles_n) * BN, kb, ke - kb,
+                                          w - wf);
+    u += ke - kb;
+  }
+}
+
+// Stream-K over workgroups 1 .. G, with the plan built by workgroup 0 in the
+// LDS the others use for their stages.
+template <int BM, int BN, int WM, int WN, int NS, bool kLds>
+__global__ __launch_bounds__(WM * WN * 64, 1) void q_tile_plan_kernel(QGemmArgs q, PlanArgs pa) {
+  __shared__ __attribute__((aligned(16))) char smem[QTileLds<BM, BN, NS>::TOTAL];
+  if (blockIdx.x == 0) {
+    plan_build<kLds>(pa, reinterpret_cast<int *>(smem));
+    return;
+  }
+  q_stream_k<BM, BN, WM, WN, NS>(q, smem, int(blockIdx.x) - 1);
+}
+
 // Tiles as the bf16 form orders them (consecutive tiles on one XCD).  Split
-// form: stream-K over g.sk_g workgroups (the pieces as the epilogue counts
-// them), or g.k_split of K per blockIdx.y.
+// form: stream-K, or g.k_split of K per blockIdx.y.
 template <int BM, int BN, int WM, int WN, int NS, bool kFused, bool kMask = false>
 __global__ __launch_bounds__(WM * WN * 64, 1) void q_tile_kernel(QGemmArgs q) {
   __shared__ __attribute__((aligned(16))) char smem[QTileLds<BM, BN, NS>::TOTAL];
@@ -362,17 +426,7 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void q_tile_kernel(QGemmArgs q) {
   const int KT = int(q.ldb) / kQBlock;
   if constexpr (!kFused) {
     if (g.sk_g > 0) {
-      const int64_t U = int64_t(ntiles) * KT;
-      int64_t u = int64_t(blockIdx.x) * U / g.sk_g;
-      const int64_t u1 = int64_t(blockIdx.x + 1) * U / g.sk_g;
-      while (u < u1) {
-        const int t = int(u / KT), kb = int(u % KT);
-        const int ke = int(min<int64_t>(KT, kb + (u1 - u)));
-        const int wf = int(((int64_t(t) * KT + 1) * g.sk_g - 1) / U);
-        q_tile_run<BM, BN, WM, WN, NS, false>(q, smem, (t / tiles_n) * BM, (t % tiles_n) * BN, kb,
-                                              ke - kb, int(blockIdx.x) - wf);
-        u += ke - kb;
-      }
+      q_stream_k<BM, BN, WM, WN, NS>(q, smem, int(blockIdx.x));
       return;
     }
   }
@@ -416,7 +470,7 @@ GemmConfig choose_quantised_gemm(int T, int d_in, int d_out, int dtype) {
   c.kind = 6; c.bm = 256; c.bn = 128;
   const int64_t tiles = int64_t((T + 255) / 256) * ((d_out + 127) / 128);
   const int64_t units = tiles * kb;
-  constexpr int kWgs = 256;
+  constexpr int kWgs = 255;              // + 1 plan workgroup in launch_quantised_gemm_plan
   if (units >= 4 * kWgs) {
     const int64_t per = units / kWgs;
     c.sk = kWgs;
@@ -462,6 +516,46 @@ hipError_t launch_quantised_gemm(const GemmConfig &c, const QGemmArgs &q, int dt
     return hipGetLastError();
   }
   return hipErrorInvalidConfiguration;
+}
+
+bool quantised_gemm_plan_fusable(const GemmConfig &c) { return c.kind == 4 || (c.kind == 6 && c.sk > 0); }
+
+size_t quantised_plan_lds_cap(const GemmConfig &c) {
+  if (c.kind != 4) return QTileLds<256, 128, 3>::TOTAL;
+  return c.bm == 32 ? QSplitLds<1>::TOTAL : c.bm == 64 ? QSplitLds<2>::TOTAL : QSplitLds<4>::TOTAL;
+}
+
+hipError_t launch_quantised_gemm_plan(const GemmConfig &c, const QGemmArgs &q, const SlotShrinkArgs *ss,
+                                      const PlanLaunch &pl, int dtype, hipStream_t s) {
+  const GemmArgs &g = q.g;
+  if (!quantised_gemm_plan_fusable(c) || pl.lds_bytes > quantised_plan_lds_cap(c))
+    return hipErrorInvalidConfiguration;
+  if (c.kind == 6) {
+    const dim3 grid(unsigned(1 + c.sk)), block(256);
+    if (pl.lds) hipLaunchKernelGGL((q_tile_plan_kernel<256, 128, 2, 2, 3, true>), grid, block, 0, s, q, pl.a);
+    else hipLaunchKernelGGL((q_tile_plan_kernel<256, 128, 2, 2, 3, false>), grid, block, 0, s, q, pl.a);
+    return hipGetLastError();
+  }
+  const int gx = (g.N + 127) / 128, gy = (g.M + c.bm - 1) / c.bm;
+  const int n_gemm = gx * gy * c.splits;
+  const dim3 grid(unsigned(1 + n_gemm + (ss ? kSlotParts * ss->n_slots : 0))), block(256);
+  const SlotShrinkArgs sa = ss ? *ss : SlotShrinkArgs{};
+#define LORA_QP3(E, MB, M, L) \
+  hipLaunchKernelGGL((q_split_plan_kernel<E, MB, M, L>), grid, block, 0, s, q, sa, pl.a, gx, gy, n_gemm)
+#define LORA_QP2(E, MB, M) do { if (pl.lds) LORA_QP3(E, MB, M, true); else LORA_QP3(E, MB, M, false); } while (0)
+#define LORA_QP(MB) \
+  do { \
+    if (dtype == LORA_F32) LORA_QP2(float, MB, false); \
+    else if (sa.mask) LORA_QP2(uint16_t, MB, true); \
+    else LORA_QP2(uint16_t, MB, false); \
+  } while (0)
+  if (c.bm == 32) LORA_QP(1);
+  else if (c.bm == 64) LORA_QP(2);
+  else LORA_QP(4);
+#undef LORA_QP
+#undef LORA_QP2
+#undef LORA_QP3
+  return hipGetLastError();
 }
 
 }  // namespace lora

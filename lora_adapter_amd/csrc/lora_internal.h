@@ -489,6 +489,12 @@ hipError_t launch_transpose(const void *src, void *dst, int rows, int cols, int 
 // finished by launch_epilogue / launch_grad_x_epilogue.
 GemmConfig choose_quantised_gemm(int T, int d_in, int d_out, int dtype);
 hipError_t launch_quantised_gemm(const GemmConfig &c, const QGemmArgs &q, int dtype, hipStream_t s);
+// The split forms with the plan built by one more workgroup of 256 threads
+// and, with ss (bf16, kind 4), the per-slot shrink in the same launch.
+bool quantised_gemm_plan_fusable(const GemmConfig &c);
+size_t quantised_plan_lds_cap(const GemmConfig &c);
+hipError_t launch_quantised_gemm_plan(const GemmConfig &c, const QGemmArgs &q, const SlotShrinkArgs *ss,
+                                      const PlanLaunch &pl, int dtype, hipStream_t s);
 
 // Batched tall-skinny QR (see tsqr.hip).
 bool tsqr_shape_ok(int M, int m, int n);

@@ -77,6 +77,12 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
 
 hipError_t launch_quantise_rows(const void *X, int dtype, int T, int d, uint8_t *codes,
                                 uint8_t *scale, bool tiled, hipStream_t s);
+// bf16 rows in the tile layout, with the plan built by one more workgroup (of
+// kPlanThreads threads) in up to kQPlanRowsLds of LDS (every workgroup of the
+// launch has that LDS: two of them to a CU).
+constexpr size_t kQPlanRowsLds = 72 << 10;
+hipError_t launch_quantise_plan(const void *X, int T, int d, uint8_t *codes, uint8_t *scale,
+                                const PlanLaunch &pl, hipStream_t s);
 hipError_t launch_quantise_weight(const void *W_t, int dtype, int d_out, int d_in, uint8_t *q_t,
                                   uint8_t *q, uint8_t *scale, uint8_t *scale_t, hipStream_t s);
 

@@ -2,18 +2,18 @@
 // per 128 columns: activations and gradients) and weights (one scale per 128 x
 // 128 block, so that the codes of W and of W^T are the same and the input
 // gradient runs over the very weight that the forward used).
+#include "plan_build.h"
 #include "quantise.h"
 
 namespace lora {
 namespace {
 
-// One wave per 512 columns of a row, 8 elements per lane; 16 lanes share a
+// Wave w takes 512 columns of a row, 8 elements per lane; 16 lanes share a
 // block.  Columns past d are zero codes.  kTiled: scale bytes laid out for the
 // tile GEMM (q_tile_scale_at), else in rows.
 template <typename E, bool kTiled>
-__global__ __launch_bounds__(256) void quantise_rows_kernel(const E *X, int T, int d, int chunks,
-                                                            uint8_t *codes, uint8_t *scale) {
-  const int64_t w = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+__device__ __forceinline__ void quantise_chunk(const E *X, int T, int d, int chunks, uint8_t *codes,
+                                               uint8_t *scale, int64_t w) {
   const int lane = threadIdx.x & 63;
   if (w >= int64_t(T) * chunks) return;
   const int64_t t = w / chunks;
@@ -30,6 +30,27 @@ __global__ __launch_bounds__(256) void quantise_rows_kernel(const E *X, int T, i
   } else {
     if (blk < ls) scale[t * ls + blk] = col < ld ? uint8_t(byte) : uint8_t(0);
   }
+}
+
+template <typename E, bool kTiled>
+__global__ __launch_bounds__(256) void quantise_rows_kernel(const E *X, int T, int d, int chunks,
+                                                            uint8_t *codes, uint8_t *scale) {
+  quantise_chunk<E, kTiled>(X, T, d, chunks, codes, scale, int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6));
+}
+
+// The rows quantised while the launch's first workgroup builds the batch's
+// plan (neither needs the other).
+template <bool kLds>
+__global__ __launch_bounds__(kPlanThreads) void quantise_plan_kernel(const uint16_t *X, int T, int d,
+                                                                     int chunks, uint8_t *codes,
+                                                                     uint8_t *scale, PlanArgs pa) {
+  extern __shared__ int qp_dyn[];
+  if (blockIdx.x == 0) {
+    plan_build<kLds>(pa, qp_dyn);
+    return;
+  }
+  quantise_chunk<uint16_t, true>(X, T, d, chunks, codes, scale,
+                                 int64_t(blockIdx.x - 1) * (kPlanThreads / 64) + (threadIdx.x >> 6));
 }
 
 // 4 x 4 bytes turned: o[j] = byte j of each of d[0..3].
@@ -138,6 +159,20 @@ hipError_t launch_quantise_rows(const void *X, int dtype, int T, int d, uint8_t 
     hipLaunchKernelGGL((quantise_rows_kernel<float, false>), grid, block, 0, s, xf, T, d, chunks, codes, scale);
   else
     return hipErrorInvalidConfiguration;
+  return hipGetLastError();
+}
+
+hipError_t launch_quantise_plan(const void *X, int T, int d, uint8_t *codes, uint8_t *scale,
+                                const PlanLaunch &pl, hipStream_t s) {
+  const int chunks = int((q_scale_bytes(d) + 3) / 4);
+  constexpr int W = kPlanThreads / 64;
+  const dim3 grid(unsigned(1 + (int64_t(T) * chunks + W - 1) / W)), block(kPlanThreads);
+  const uint16_t *x = static_cast<const uint16_t *>(X);
+  if (pl.lds_bytes > kQPlanRowsLds) return hipErrorInvalidConfiguration;
+  if (pl.lds)
+    hipLaunchKernelGGL(quantise_plan_kernel<true>, grid, block, pl.lds_bytes, s, x, T, d, chunks, codes, scale, pl.a);
+  else
+    hipLaunchKernelGGL(quantise_plan_kernel<false>, grid, block, pl.lds_bytes, s, x, T, d, chunks, codes, scale, pl.a);
   return hipGetLastError();
 }
 
