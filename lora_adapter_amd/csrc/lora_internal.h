@@ -422,7 +422,7 @@ struct OrthArgs {
   OrthRec *rec;
   float *q;                 // [matrices][R][R]
   double *gram;             // [matrices][chunks][R][R]
-  double *big;              // [matrices][4][R][R], ranks over 64
+  double *big;              // [matrices][5][R][R], ranks over 64
 };
 
 // ----------------------------------------------------------------- launchers

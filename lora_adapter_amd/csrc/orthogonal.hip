@@ -32,6 +32,7 @@ typedef double f64x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kSmall = 64;      // ranks whose steps run in one workgroup
+constexpr int kBigMats = 5;     // r x r buffers of a matrix of rank over 64: G, P, Q and two spare
 
 // The adapter of list entry m if it can be taken: in range, rank 1..max_rank,
 // its page table consistent, and not listed before.  Called by every thread of
@@ -59,26 +60,48 @@ __device__ __forceinline__ int orth_rank(const OrthArgs &a, int m, int *flag, in
   return *flag ? 0 : r;
 }
 
-// Eight columns of a row of N.  kStep: N from the gradient and the momentum
-// (which kUpdate moves on first); else the source row.
-template <bool kStep, bool kUpdate>
-__device__ __forceinline__ void load_n8(const OrthFactor &f, const OrthArgs &a, int64_t at, float v[8]) {
-  Elem<float>::load8(f.src + at, v);
-  if constexpr (kStep) {
-    float m[8];
-    Elem<float>::load8(f.momentum + at, m);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float mn = kUpdate ? a.mu * m[e] + v[e] : m[e];
-      m[e] = mn;
-      v[e] = a.nesterov ? v[e] + a.mu * mn : mn;
-    }
-    if constexpr (kUpdate) {
-      *reinterpret_cast<float4 *>(f.momentum + at) = make_float4(m[0], m[1], m[2], m[3]);
-      *reinterpret_cast<float4 *>(f.momentum + at + 4) = make_float4(m[4], m[5], m[6], m[7]);
+// Eight columns of a row of the source, and (kStep) of the momentum, held raw
+// until used, so that a step's loads are in flight under the step before.
+template <bool kStep>
+struct RawN {
+  float4 g[2], m[kStep ? 2 : 1];
+  __device__ __forceinline__ void load(const OrthFactor &f, int64_t at, bool on) {
+    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+    g[0] = g[1] = m[0] = z;
+    if constexpr (kStep) m[1] = z;
+    if (!on) return;
+    const float4 *pg = reinterpret_cast<const float4 *>(f.src + at);
+    g[0] = pg[0];
+    g[1] = pg[1];
+    if constexpr (kStep) {
+      const float4 *pm = reinterpret_cast<const float4 *>(f.momentum + at);
+      m[0] = pm[0];
+      m[1] = pm[1];
     }
   }
-}
+  // N from the gradient and the momentum (which kUpdate moves on first and
+  // stores); else the source row
+  template <bool kUpdate>
+  __device__ __forceinline__ void value(const OrthFactor &f, const OrthArgs &a, int64_t at, bool on,
+                                        float v[8]) const {
+    const float gv[8] = {g[0].x, g[0].y, g[0].z, g[0].w, g[1].x, g[1].y, g[1].z, g[1].w};
+    if constexpr (!kStep) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = gv[e];
+    } else {
+      float mv[8] = {m[0].x, m[0].y, m[0].z, m[0].w, m[1].x, m[1].y, m[1].z, m[1].w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (kUpdate) mv[e] = a.mu * mv[e] + gv[e];
+        v[e] = a.nesterov ? gv[e] + a.mu * mv[e] : mv[e];
+      }
+      if (kUpdate && on) {
+        *reinterpret_cast<float4 *>(f.momentum + at) = make_float4(mv[0], mv[1], mv[2], mv[3]);
+        *reinterpret_cast<float4 *>(f.momentum + at + 4) = make_float4(mv[4], mv[5], mv[6], mv[7]);
+      }
+    }
+  }
+};
 
 // ------------------------------------------------------------ Gram partials
 // Row blocks bi .. bi+NB-1 against bj .. bj+NB-1 (16 rows each) over columns
@@ -89,16 +112,17 @@ __device__ __forceinline__ void load_n8(const OrthFactor &f, const OrthArgs &a, 
 template <int NB, bool kDiag, bool kStep, bool kUpdate>
 __device__ __forceinline__ void gram_body(const OrthArgs &a, const OrthFactor &f, int r, int ps, int bi,
                                           int bj, int c0, int c1, double *out, double *red) {
+  constexpr int NJ = kDiag ? 1 : NB;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int lr = lane & 15, lg = lane >> 4;
-  int64_t ri[NB], rj[kDiag ? 1 : NB];
+  int64_t ri[NB], rj[NJ];
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
     const int row = (bi + i) * 16 + lr;
-    ri[i] = row < r ? int64_t(a.pool.page_ids[ps + row]) * f.d : -1;
+    ri[i] = row < r ? int64_t(a.pool.page_ids[ps + row]) * f.d + lg * 8 : -1;
     if constexpr (!kDiag) {
       const int col = (bj + i) * 16 + lr;
-      rj[i] = col < r ? int64_t(a.pool.page_ids[ps + col]) * f.d : -1;
+      rj[i] = col < r ? int64_t(a.pool.page_ids[ps + col]) * f.d + lg * 8 : -1;
     }
   }
   f64x4_t acc[NB][NB];
@@ -106,28 +130,32 @@ __device__ __forceinline__ void gram_body(const OrthArgs &a, const OrthFactor &f
   for (int i = 0; i < NB; ++i)
 #pragma unroll
     for (int j = 0; j < NB; ++j) acc[i][j] = f64x4_t{0, 0, 0, 0};
-  for (int c = c0 + wave * 32; c < c1; c += 128) {
-    const int col = c + lg * 8;
-    float x[NB][8], y[kDiag ? 1 : NB][8];
+  RawN<kStep> x[NB], y[NJ];
+  auto load = [&](int c) __attribute__((always_inline)) {
+    const bool in = c < c1;
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
-      if (ri[i] >= 0) load_n8<kStep, kUpdate>(f, a, ri[i] + col, x[i]);
-      if constexpr (!kDiag) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[i][e] = 0.f;
-        if (rj[i] >= 0) load_n8<kStep, false>(f, a, rj[i] + col, y[i]);
-      }
+      x[i].load(f, ri[i] + c, in && ri[i] >= 0);
+      if constexpr (!kDiag) y[i].load(f, rj[i] + c, in && rj[i] >= 0);
     }
+  };
+  load(c0 + wave * 32);
+  for (int c = c0 + wave * 32; c < c1; c += 128) {
+    float xv[NB][8], yv[NJ][8];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      x[i].template value<kUpdate>(f, a, ri[i] + c, ri[i] >= 0, xv[i]);
+      if constexpr (!kDiag) y[i].template value<false>(f, a, 0, false, yv[i]);
+    }
+    load(c + 128);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       double dx[NB];
 #pragma unroll
-      for (int i = 0; i < NB; ++i) dx[i] = double(x[i][e]);
+      for (int i = 0; i < NB; ++i) dx[i] = double(xv[i][e]);
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
-        const double dy = kDiag ? dx[j] : double(y[kDiag ? 0 : j][e]);
+        const double dy = kDiag ? dx[j] : double(yv[kDiag ? 0 : j][e]);
 #pragma unroll
         for (int i = 0; i < (kDiag ? j + 1 : NB); ++i)
           acc[i][j] = __builtin_amdgcn_mfma_f64_16x16x4f64(dx[i], dy, acc[i][j], 0, 0, 0);
@@ -161,9 +189,12 @@ __device__ __forceinline__ void gram_body(const OrthArgs &a, const OrthFactor &f
 
 // Grid: (column chunks x super-tiles, matrices).  Super-tiles are 64 x 64
 // blocks (si <= sj) of the Gram matrix; ranks <= 64 have the first only.
-template <bool kStep>
-__global__ __launch_bounds__(256) void gram_kernel(OrthArgs a) {
-  __shared__ double red[kSmall * kSmall];
+// NBMAX: 16-row blocks of the largest rank, 8 for ranks over 64 (a launch of
+// small ranks then keeps the registers, and the waves per SIMD, of its own).
+template <bool kStep, int NBMAX>
+__global__ __launch_bounds__(256, NBMAX <= 2 ? 4 : NBMAX == 4 ? 2 : 1) void gram_kernel(OrthArgs a) {
+  constexpr int S = 16 * (NBMAX < 4 ? NBMAX : 4);
+  __shared__ double red[S * S];
   __shared__ int flag;
   const int m = blockIdx.y % a.M, fi = blockIdx.y / a.M;
   const OrthFactor &f = a.f[fi];
@@ -178,20 +209,23 @@ __global__ __launch_bounds__(256) void gram_kernel(OrthArgs a) {
   if (r == 0) return;
   const int c0 = int(int64_t(ck) * a.chunk_cols), c1 = min(f.d, c0 + a.chunk_cols);
   double *out = a.gram + (int64_t(blockIdx.y) * a.chunks + ck) * a.R * a.R;
-  if (r <= kSmall) {
-    if (st > 0) return;
-    if (r <= 16) gram_body<1, true, kStep, kStep>(a, f, r, ps, 0, 0, c0, c1, out, red);
-    else if (r <= 32) gram_body<2, true, kStep, kStep>(a, f, r, ps, 0, 0, c0, c1, out, red);
-    else gram_body<4, true, kStep, kStep>(a, f, r, ps, 0, 0, c0, c1, out, red);
-    return;
+  if (NBMAX == 1 || r <= 16) {
+    if (st == 0) gram_body<1, true, kStep, kStep>(a, f, r, ps, 0, 0, c0, c1, out, red);
+  } else if (NBMAX == 2 || r <= 32) {
+    if constexpr (NBMAX >= 2)
+      if (st == 0) gram_body<2, true, kStep, kStep>(a, f, r, ps, 0, 0, c0, c1, out, red);
+  } else if (NBMAX == 4 || r <= kSmall) {
+    if constexpr (NBMAX >= 4)
+      if (st == 0) gram_body<4, true, kStep, kStep>(a, f, r, ps, 0, 0, c0, c1, out, red);
+  } else if constexpr (NBMAX == 8) {
+    // pair (si, sj), si <= sj, counted along columns sj
+    int sj = 0;
+    while (st > sj) { st -= sj + 1; ++sj; }
+    if (sj * kSmall >= r) return;
+    // the momentum of these ranks was moved on by its own launch
+    if (st == sj) gram_body<4, true, kStep, false>(a, f, r, ps, st * 4, sj * 4, c0, c1, out, red);
+    else gram_body<4, false, kStep, false>(a, f, r, ps, st * 4, sj * 4, c0, c1, out, red);
   }
-  // pair (si, sj), si <= sj, counted along columns sj
-  int sj = 0;
-  while (st > sj) { st -= sj + 1; ++sj; }
-  if (sj * kSmall >= r) return;
-  // the momentum of these ranks was moved on by its own launch
-  if (st == sj) gram_body<4, true, kStep, false>(a, f, r, ps, st * 4, sj * 4, c0, c1, out, red);
-  else gram_body<4, false, kStep, false>(a, f, r, ps, st * 4, sj * 4, c0, c1, out, red);
 }
 
 // Momentum of the matrices of rank over 64 (their Gram super-tiles read a row
@@ -207,21 +241,24 @@ __global__ __launch_bounds__(256) void momentum_kernel(OrthArgs a) {
   const int col = (blockIdx.x * 256 + threadIdx.x) * 8;
   if (col >= f.d) return;
   for (int row = blockIdx.z; row < r; row += gridDim.z) {
+    const int64_t at = int64_t(a.pool.page_ids[ps + row]) * f.d + col;
+    RawN<true> x;
+    x.load(f, at, true);
     float v[8];
-    load_n8<true, true>(f, a, int64_t(a.pool.page_ids[ps + row]) * f.d + col, v);
+    x.value<true>(f, a, at, true, v);
   }
 }
 
 // ------------------------------------------------------------ the steps, rank <= 64
-// Symmetric matrices of 16 NB rows in LDS, rows of S doubles (S = 16 NB + 4
-// puts the 8 rows x 4 columns that a half wave reads at once on distinct
+// Symmetric matrices of 16 NB rows in LDS, rows of S doubles (S = 16 NB + 2
+// puts the 16 rows x 2 columns that a half wave reads at once on distinct
 // banks).  Both operands of a product are read along rows (they are
 // symmetric), its upper tiles are computed, four waves taking them in turn,
 // and stored with their mirror images.
 template <int NB, int CT, typename Store>
 __device__ __forceinline__ void sym_tiles(const double *A, const double *B, int first, int n_tiles,
                                           const Store &store) {
-  constexpr int S = 16 * NB + 4;
+  constexpr int S = 16 * NB + 2;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int lr = lane & 15, lg = lane >> 4;
   int ti[CT], tj[CT];
@@ -253,19 +290,40 @@ __device__ __forceinline__ void sym_tiles(const double *A, const double *B, int 
 
 template <int NB>
 __device__ __forceinline__ void steps_body(const OrthArgs &a, int mat, int r, double *lds) {
-  constexpr int n = 16 * NB, S = n + 4, NT = NB * (NB + 1) / 2, CT = (NT + 3) / 4;
+  constexpr int n = 16 * NB, S = n + 2, NT = NB * (NB + 1) / 2, CT = (NT + 3) / 4;
   double *G = lds, *P = G + n * S, *Q = P + n * S, *T = Q + n * S;
   const int tid = threadIdx.x, R = a.R;
-  // the chunks' partials in order; elements below the diagonal tiles mirrored
-  for (int e = tid; e < n * n; e += 256) {
-    const int i = e / n, j = e % n;
-    double s = 0;
-    if (i < r && j < r) {
+  // the chunks' partials in order, the loads of all of a thread's elements
+  // (and of several chunks when it has few) in flight together; elements below
+  // the diagonal tiles mirrored
+  {
+    constexpr int EP = n * n / 256, CB = EP >= 4 ? 2 : 8;
+    const double *p[EP];
+    double sum[EP];
+#pragma unroll
+    for (int q = 0; q < EP; ++q) {
+      const int i = (tid + q * 256) / n, j = (tid + q * 256) % n;
       const bool up = i / 16 <= j / 16;
-      const double *p = a.gram + int64_t(mat) * a.chunks * R * R + (up ? int64_t(i) * R + j : int64_t(j) * R + i);
-      for (int c = 0; c < a.chunks; ++c) s += p[int64_t(c) * R * R];
+      const int gi = min(up ? i : j, R - 1), gj = min(up ? j : i, R - 1);
+      p[q] = a.gram + int64_t(mat) * a.chunks * R * R + int64_t(gi) * R + gj;
+      sum[q] = 0;
     }
-    G[i * S + j] = s;
+    for (int c = 0; c < a.chunks; c += CB) {
+      double t[CB][EP];
+#pragma unroll
+      for (int u = 0; u < CB; ++u)
+#pragma unroll
+        for (int q = 0; q < EP; ++q) t[u][q] = p[q][int64_t(min(c + u, a.chunks - 1)) * R * R];
+#pragma unroll
+      for (int u = 0; u < CB; ++u)
+#pragma unroll
+        for (int q = 0; q < EP; ++q) sum[q] += c + u < a.chunks ? t[u][q] : 0.0;
+    }
+#pragma unroll
+    for (int q = 0; q < EP; ++q) {
+      const int i = (tid + q * 256) / n, j = (tid + q * 256) % n;
+      G[i * S + j] = i < r && j < r ? sum[q] : 0.0;
+    }
   }
   __syncthreads();
   double tr = 0;
@@ -311,7 +369,7 @@ __device__ __forceinline__ void steps_body(const OrthArgs &a, int mat, int r, do
 
 template <int NBMAX>
 __global__ __launch_bounds__(256) void steps_kernel(OrthArgs a) {
-  __shared__ double steps_lds[4 * (16 * NBMAX) * (16 * NBMAX + 4)];
+  __shared__ double steps_lds[4 * (16 * NBMAX) * (16 * NBMAX + 2)];
   const int mat = blockIdx.x, r = a.rec[mat].rank;
   if (r < 1 || r > kSmall) return;
   if (NBMAX == 1 || r <= 16) steps_body<1>(a, mat, r, steps_lds);
@@ -320,61 +378,108 @@ __global__ __launch_bounds__(256) void steps_kernel(OrthArgs a) {
 }
 
 // ------------------------------------------------------------ ranks over 64
-// Sum of the chunks' partials, normalised, both halves filled.  Grid: (matrices).
+// Sum of the chunks' partials, normalised, both halves filled.  Grid:
+// (elements / 1024, matrices); every workgroup takes the trace itself.
 __global__ __launch_bounds__(256) void gram_sum_kernel(OrthArgs a) {
-  const int mat = blockIdx.x, r = a.rec[mat].rank, R = a.R;
+  const int mat = blockIdx.y, r = a.rec[mat].rank, R = a.R;
   if (r <= kSmall) return;
   __shared__ double part[256];
   const double *p = a.gram + int64_t(mat) * a.chunks * R * R;
   double t = 0;
   for (int i = threadIdx.x; i < r; i += 256)
     for (int c = 0; c < a.chunks; ++c) t += p[int64_t(c) * R * R + int64_t(i) * R + i];
+  double sum[4] = {0, 0, 0, 0};
+  int64_t at[4];
+  const int64_t e0 = int64_t(blockIdx.x) * 1024 + threadIdx.x, n = int64_t(R) * R;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int64_t e = min(e0 + q * 256, n - 1);
+    const int i = int(e / R), j = int(e % R);
+    at[q] = i / 16 <= j / 16 ? e : int64_t(j) * R + i;
+  }
+#pragma unroll 2
+  for (int c = 0; c < a.chunks; ++c)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sum[q] += p[int64_t(c) * n + at[q]];
   part[threadIdx.x] = t;
   __syncthreads();
-  double tr = 0;
-  for (int i = 0; i < 256; ++i) tr += part[i];
+  // a fixed tree: the same trace in every workgroup
+  for (int o = 128; o > 0; o >>= 1) {
+    if (int(threadIdx.x) < o) part[threadIdx.x] += part[threadIdx.x + o];
+    __syncthreads();
+  }
+  const double tr = part[0];
   const double inv = tr == 0 ? 0.0 : 1.0 / (sqrt(tr) + double(a.eps));
-  if (threadIdx.x == 0) a.rec[mat].inv = float(inv);
-  double *G = a.big + int64_t(mat) * 4 * R * R;
-  for (int64_t e = threadIdx.x; e < int64_t(R) * R; e += 256) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.rec[mat].inv = float(inv);
+  double *G = a.big + int64_t(mat) * kBigMats * n;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int64_t e = e0 + q * 256;
+    if (e >= n) break;
     const int i = int(e / R), j = int(e % R);
-    double s = 0;
-    if (i < r && j < r) {
-      const int64_t at = i / 16 <= j / 16 ? int64_t(i) * R + j : int64_t(j) * R + i;
-      for (int c = 0; c < a.chunks; ++c) s += p[int64_t(c) * R * R + at];
-    }
-    G[e] = s * (inv * inv);
+    // past the rank the partials were never written
+    G[e] = i < r && j < r ? sum[q] * (inv * inv) : 0.0;
   }
 }
 
-// One product of symmetric R x R matrices of every matrix of rank over 64,
-// upper tiles of 32 x 32 (one 16 x 16 block per wave), stored with their
-// mirror images.  Buffers of a matrix: 0 G, 1 P, 2 and 3 Q and T in turn.
+// Products of symmetric R x R matrices of every matrix of rank over 64: upper
+// tiles of 32 x 32 (one 16 x 16 block per wave), stored with their mirror
+// images.  Both operands are read along rows, 64 columns at a time through LDS
+// (coalesced; the next 64 in flight under the MFMAs; rows of 66 doubles as in
+// sym_tiles).  Grid: (tiles, matrices, products).
 struct SymOp {
-  int A, B, C;            // C = A . B
+  int A, B, C;            // buffers: C = A . B
   int poly;               // C = ca I + cb A + cc A . B
   int copy;               // also into this buffer (-1: none)
   int to_q;               // also, in fp32, into q
 };
 
 __global__ __launch_bounds__(256) void sym_product_kernel(OrthArgs a, SymOp op0, SymOp op1) {
+  constexpr int KB = 64, S = KB + 2;
+  __shared__ double la[32 * S], lb[32 * S];
   const int mat = blockIdx.y, r = a.rec[mat].rank, R = a.R;
   if (r <= kSmall) return;
   const SymOp op = blockIdx.z == 0 ? op0 : op1;
   int t = blockIdx.x, tj = 0;
   while (t > tj) { t -= tj + 1; ++tj; }
   if (tj * 32 >= r) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int lr = lane & 15, lg = lane >> 4;
+  double *base = a.big + int64_t(mat) * kBigMats * R * R;
+  const double *A = base + int64_t(op.A) * R * R, *B = base + int64_t(op.B) * R * R;
+  // thread: row tid / 8 of both tiles, 8 columns of each 64
+  const int row = tid >> 3, cc = (tid & 7) * 8;
+  const double *ga = A + int64_t(min(t * 32 + row, R - 1)) * R, *gb = B + int64_t(min(tj * 32 + row, R - 1)) * R;
+  const int n = (r + 15) / 16 * 16;
+  double2 va[4], vb[4];
+  auto load = [&](int k0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int c = min(k0 + cc + 2 * e, R - 2);     // past n: not used
+      va[e] = *reinterpret_cast<const double2 *>(ga + c);
+      vb[e] = *reinterpret_cast<const double2 *>(gb + c);
+    }
+  };
+  load(0);
+  f64x4_t acc = {0, 0, 0, 0};
+  const double *pa = la + ((wave >> 1) * 16 + lr) * S + lg, *pb = lb + ((wave & 1) * 16 + lr) * S + lg;
+  for (int k0 = 0; k0 < n; k0 += KB) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      la[row * S + cc + 2 * e] = va[e].x; la[row * S + cc + 2 * e + 1] = va[e].y;
+      lb[row * S + cc + 2 * e] = vb[e].x; lb[row * S + cc + 2 * e + 1] = vb[e].y;
+    }
+    __syncthreads();
+    if (k0 + KB < n) load(k0 + KB);
+    const int kn = min(KB, n - k0);
+    for (int k = 0; k < kn; k += 16)
+#pragma unroll
+      for (int u = 0; u < 16; u += 4)
+        acc = __builtin_amdgcn_mfma_f64_16x16x4f64(pa[k + u], pb[k + u], acc, 0, 0, 0);
+    __syncthreads();
+  }
   const int i0 = t * 32 + (wave >> 1) * 16, j0 = tj * 32 + (wave & 1) * 16;
   if (i0 >= R || j0 >= R) return;
-  double *base = a.big + int64_t(mat) * 4 * R * R;
-  const double *A = base + int64_t(op.A) * R * R, *B = base + int64_t(op.B) * R * R;
-  const double *pa = A + int64_t(i0 + lr) * R + lg, *pb = B + int64_t(j0 + lr) * R + lg;
-  f64x4_t acc = {0, 0, 0, 0};
-  const int n = (r + 15) / 16 * 16;
-#pragma unroll 8
-  for (int k = 0; k < n; k += 4) acc = __builtin_amdgcn_mfma_f64_16x16x4f64(pa[k], pb[k], acc, 0, 0, 0);
   double *C = base + int64_t(op.C) * R * R;
   double *D = op.copy >= 0 ? base + int64_t(op.copy) * R * R : nullptr;
   float *q = a.q + int64_t(mat) * R * R;
@@ -401,100 +506,136 @@ __global__ __launch_bounds__(256) void sym_product_kernel(OrthArgs a, SymOp op0,
 // Rows ib*16 .. of O = Q (N inv): a wave takes 64 columns, lane l the four
 // columns 4 (l % 16) .. +3 of row l / 16 of every four, so a load is 256
 // contiguous bytes per row; column tile e holds columns 4 c + e, and the four
-// tiles' results are four consecutive columns again.
+// tiles' results are four consecutive columns again.  128 rows of N at a time:
+// their page offsets and columns of Q go through LDS, and eight loads of N
+// are in flight ahead of the MFMAs.
+constexpr int kApplyRows = 128, kApplyQ = kApplyRows + 4;
+
 template <int NB, bool kStep, typename E>
 __device__ __forceinline__ void apply_body(const OrthArgs &a, const OrthFactor &f, int r, int ps, float inv,
-                                           int ib, const float *q, int col0) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+                                           int ib, const float *q, int col0, float *lq, int *lp) {
+  constexpr int U = 8;                        // groups of four rows in flight
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int lr = lane & 15, lg = lane >> 4;
-  const int col = col0 + wave * 64 + lr * 4;
+  const int col = min(col0 + wave * 64, f.d - 64) + lr * 4;
+  const bool on = col0 + wave * 64 < f.d;     // every wave stays for the barriers
   const int R = a.R;
-  if (col0 + wave * 64 >= f.d) return;
   f32x4_t acc[NB][4];
 #pragma unroll
   for (int i = 0; i < NB; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[i][e] = f32x4_t{0, 0, 0, 0};
-  const int nk = (r + 3) / 4;
-#pragma unroll 4
-  for (int k = 0; k < nk; ++k) {
-    const int row = 4 * k + lg;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (row < r) {
-      const int64_t at = int64_t(a.pool.page_ids[ps + row]) * f.d + col;
-      x = *reinterpret_cast<const float4 *>(f.src + at);
-      if constexpr (kStep) {
-        const float4 m = *reinterpret_cast<const float4 *>(f.momentum + at);
-        if (a.nesterov)
-          x = make_float4(x.x + a.mu * m.x, x.y + a.mu * m.y, x.z + a.mu * m.z, x.w + a.mu * m.w);
-        else
-          x = m;
+  for (int r0 = 0; r0 < r; r0 += kApplyRows) {
+    const int nr = min(kApplyRows, r - r0), n16 = (nr + 15) / 16 * 16;
+    if (r0 > 0) __syncthreads();
+    if (tid < n16) lp[tid] = a.pool.page_ids[ps + r0 + min(tid, nr - 1)];
+    for (int e = tid; e < NB * 16 * n16; e += 256) {
+      const int i = e / n16, k = e % n16;
+      const int qi = ib * 16 + i;
+      lq[i * kApplyQ + k] = k < nr && qi < R ? q[int64_t(qi) * R + r0 + k] : 0.f;
+    }
+    __syncthreads();
+    for (int k0 = 0; k0 < n16; k0 += 4 * U) {
+      float4 x[U], m[kStep ? U : 1];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        // rows past the rank: the last row again, times a zero of Q (its own
+        // Inf or NaN must not enter twice: cleared below)
+        const int k = min(k0 + 4 * u + lg, n16 - 1);
+        const int64_t at = int64_t(lp[k]) * f.d + col;
+        x[u] = *reinterpret_cast<const float4 *>(f.src + at);
+        if constexpr (kStep) m[u] = *reinterpret_cast<const float4 *>(f.momentum + at);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = k0 + 4 * u + lg;
+        if (k0 + 4 * u >= n16) break;
+        float4 v = x[u];
+        if constexpr (kStep) {
+          const float4 w = m[u];
+          if (a.nesterov)
+            v = make_float4(v.x + a.mu * w.x, v.y + a.mu * w.y, v.z + a.mu * w.z, v.w + a.mu * w.w);
+          else
+            v = w;
+        }
+        if (k >= nr) v = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float b[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const float av = lq[(i * 16 + lr) * kApplyQ + k];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[i][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(av, b[e], acc[i][e], 0, 0, 0);
+        }
       }
     }
-    const float b[4] = {x.x * inv, x.y * inv, x.z * inv, x.w * inv};
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int qi = min((ib + i) * 16 + lr, R - 1);
-      const float av = row < r ? q[int64_t(qi) * R + row] : 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        acc[i][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(av, b[e], acc[i][e], 0, 0, 0);
-    }
   }
+  if (!on) return;
   // acc element v of lane l: row 4 (l / 16) + v, column l % 16 of its tile
 #pragma unroll
-  for (int i = 0; i < NB; ++i)
+  for (int i = 0; i < NB; ++i) {
+    int64_t at[4];
+    float4 mw[4];
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const int row = (ib + i) * 16 + lg * 4 + v;
-      if (row >= r) continue;
-      const int64_t at = int64_t(a.pool.page_ids[ps + row]) * f.d + col;
-      float o[4] = {acc[i][0][v], acc[i][1][v], acc[i][2][v], acc[i][3][v]};
-      if constexpr (!kStep) {
-        *reinterpret_cast<float4 *>(f.out + at) = make_float4(o[0], o[1], o[2], o[3]);
-      } else {
-        E *pg = static_cast<E *>(f.pages) + at;
-        float w[4];
+      const int row = min((ib + i) * 16 + lg * 4 + v, r - 1);
+      at[v] = int64_t(a.pool.page_ids[ps + row]) * f.d + col;
+      if constexpr (kStep) {
         if (f.master) {
-          const float4 mw = *reinterpret_cast<const float4 *>(f.master + at);
-          w[0] = mw.x; w[1] = mw.y; w[2] = mw.z; w[3] = mw.w;
+          mw[v] = *reinterpret_cast<const float4 *>(f.master + at[v]);
         } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = Elem<E>::load1(pg + e);
+          const E *pg = static_cast<const E *>(f.pages) + at[v];
+          mw[v] = make_float4(Elem<E>::load1(pg), Elem<E>::load1(pg + 1), Elem<E>::load1(pg + 2),
+                              Elem<E>::load1(pg + 3));
         }
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      if ((ib + i) * 16 + lg * 4 + v >= r) continue;
+      const float o[4] = {acc[i][0][v], acc[i][1][v], acc[i][2][v], acc[i][3][v]};
+      if constexpr (!kStep) {
+        *reinterpret_cast<float4 *>(f.out + at[v]) = make_float4(o[0], o[1], o[2], o[3]);
+      } else {
+        float w[4] = {mw[v].x, mw[v].y, mw[v].z, mw[v].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[e] = w[e] * f.keep - f.lr * o[e];
-        if (f.master) *reinterpret_cast<float4 *>(f.master + at) = make_float4(w[0], w[1], w[2], w[3]);
+        if (f.master) *reinterpret_cast<float4 *>(f.master + at[v]) = make_float4(w[0], w[1], w[2], w[3]);
+        E *pg = static_cast<E *>(f.pages) + at[v];
         if constexpr (sizeof(E) == 2)
           *reinterpret_cast<uint2 *>(pg) = make_uint2(f2bf2(w[0], w[1]), f2bf2(w[2], w[3]));
         else
           *reinterpret_cast<float4 *>(pg) = make_float4(w[0], w[1], w[2], w[3]);
       }
     }
+  }
 }
 
 // Grid: (columns / 256, matrices, row blocks of 64).
 template <bool kStep, typename E>
 __global__ __launch_bounds__(256) void orth_apply_kernel(OrthArgs a) {
+  __shared__ float lq[kSmall * kApplyQ];
+  __shared__ int lp[kApplyRows];
   const OrthRec rc = a.rec[blockIdx.y];
   const OrthFactor &f = a.f[blockIdx.y / a.M];
   const int ib = blockIdx.z * 4;
-  if (rc.rank <= ib * 16) return;
-  const float *q = a.q + int64_t(blockIdx.y) * a.R * a.R;
   const int col0 = blockIdx.x * 256;
-  if (rc.rank <= 16) apply_body<1, kStep, E>(a, f, rc.rank, rc.page_start, rc.inv, ib, q, col0);
-  else if (rc.rank <= 32) apply_body<2, kStep, E>(a, f, rc.rank, rc.page_start, rc.inv, ib, q, col0);
-  else apply_body<4, kStep, E>(a, f, rc.rank, rc.page_start, rc.inv, ib, q, col0);
+  if (rc.rank <= ib * 16 || col0 >= f.d) return;
+  const float *q = a.q + int64_t(blockIdx.y) * a.R * a.R;
+  const int left = rc.rank - ib * 16;         // output rows from ib * 16
+  if (left <= 16) apply_body<1, kStep, E>(a, f, rc.rank, rc.page_start, rc.inv, ib, q, col0, lq, lp);
+  else if (left <= 32) apply_body<2, kStep, E>(a, f, rc.rank, rc.page_start, rc.inv, ib, q, col0, lq, lp);
+  else apply_body<4, kStep, E>(a, f, rc.rank, rc.page_start, rc.inv, ib, q, col0, lq, lp);
 }
 
 int orth_r(int max_rank) { return (max_rank + 15) / 16 * 16; }
 
-// Column chunks of the Gram launch: enough workgroups to fill the GPU twice,
-// at least 256 columns each (two steps of each wave).
+// Column chunks of the Gram launch: about 1024 workgroups, at least 256 columns
+// each (two steps of each wave).
 int orth_chunk_cols(int64_t mats, int max_rank, int d) {
   const int s = (max_rank + kSmall - 1) / kSmall;
   const int64_t per = mats * (s * (s + 1) / 2);
-  const int64_t want = (512 + per - 1) / per;
+  const int64_t want = (1024 + per - 1) / per;
   int64_t cols = (d + want - 1) / want;
   cols = (cols + 127) / 128 * 128;
   return int(cols < 256 ? 256 : cols);
@@ -509,14 +650,14 @@ size_t pad256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
 
-// Workspace: records, Q (fp32), Gram partials, and for ranks over 64 four r x
-// r matrices.
+// Workspace: records, Q (fp32), Gram partials, and for ranks over 64 the r x r
+// matrices.
 size_t orth_workspace_bytes(int M, int factors, int max_rank, int d) {
   const int64_t mats = int64_t(M) * factors;
   const size_t RR = size_t(orth_r(max_rank)) * orth_r(max_rank);
   size_t b = pad256(size_t(mats) * sizeof(OrthRec)) + pad256(size_t(mats) * RR * 4) +
              pad256(size_t(mats) * orth_chunks(mats, max_rank, d) * RR * 8);
-  if (max_rank > kSmall) b += pad256(size_t(mats) * 4 * RR * 8);
+  if (max_rank > kSmall) b += pad256(size_t(mats) * kBigMats * RR * 8);
   return b;
 }
 
@@ -544,32 +685,39 @@ hipError_t launch_orthogonal(OrthArgs a, int factors, bool step, int dtype, void
                        dim3(256), 0, s, a);
   }
   const dim3 gg(unsigned(a.chunks * (st * (st + 1) / 2)), unsigned(mats));
-  if (step) hipLaunchKernelGGL(gram_kernel<true>, gg, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(gram_kernel<false>, gg, dim3(256), 0, s, a);
+#define LORA_GRAM(NB) \
+  do { \
+    if (step) hipLaunchKernelGGL((gram_kernel<true, NB>), gg, dim3(256), 0, s, a); \
+    else hipLaunchKernelGGL((gram_kernel<false, NB>), gg, dim3(256), 0, s, a); \
+  } while (0)
+  if (a.max_rank <= 16) LORA_GRAM(1);
+  else if (a.max_rank <= 32) LORA_GRAM(2);
+  else if (!big) LORA_GRAM(4);
+  else LORA_GRAM(8);
+#undef LORA_GRAM
   if (a.max_rank <= 16) hipLaunchKernelGGL(steps_kernel<1>, dim3(unsigned(mats)), dim3(256), 0, s, a);
   else if (a.max_rank <= 32) hipLaunchKernelGGL(steps_kernel<2>, dim3(unsigned(mats)), dim3(256), 0, s, a);
   else hipLaunchKernelGGL(steps_kernel<4>, dim3(unsigned(mats)), dim3(256), 0, s, a);
   if (big) {
-    hipLaunchKernelGGL(gram_sum_kernel, dim3(unsigned(mats)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(gram_sum_kernel, dim3(unsigned((RR + 1023) / 1024), unsigned(mats)), dim3(256), 0, s, a);
     const int t32 = (a.R + 31) / 32;
     const unsigned tiles = unsigned(t32 * (t32 + 1) / 2);
-    int Q = 2, T = 3;
+    auto products = [&](const SymOp &x, const SymOp &y, unsigned n) {
+      hipLaunchKernelGGL(sym_product_kernel, dim3(tiles, unsigned(mats), n), dim3(256), 0, s, a, x, y);
+    };
+    int Q = 2, Qn = 3;                         // buffers 0 G, 1 P, 4 P G
     for (int k = 0; k < a.steps; ++k) {
       const bool last = k + 1 == a.steps;
       // P (the first step's is Q too)
       const SymOp poly{0, 0, 1, 1, k == 0 ? Q : -1, last && k == 0};
-      hipLaunchKernelGGL(sym_product_kernel, dim3(tiles, unsigned(mats), 1), dim3(256), 0, s, a, poly, poly);
-      // Q <- P Q; G <- P (P G), with P G through the free buffer of the two
-      const SymOp pq{1, Q, T, 0, -1, last};
-      if (k > 0) {
-        hipLaunchKernelGGL(sym_product_kernel, dim3(tiles, unsigned(mats), 1), dim3(256), 0, s, a, pq, pq);
-        const int t = Q; Q = T; T = t;
-      }
-      if (!last) {
-        const SymOp pg{1, 0, T, 0, -1, 0}, ppg{1, T, 0, 0, -1, 0};
-        hipLaunchKernelGGL(sym_product_kernel, dim3(tiles, unsigned(mats), 1), dim3(256), 0, s, a, pg, pg);
-        hipLaunchKernelGGL(sym_product_kernel, dim3(tiles, unsigned(mats), 1), dim3(256), 0, s, a, ppg, ppg);
-      }
+      products(poly, poly, 1);
+      // P G and the next Q in one launch, then G <- P (P G)
+      const SymOp pg{1, 0, 4, 0, -1, 0}, pq{1, Q, Qn, 0, -1, last}, ppg{1, 4, 0, 0, -1, 0};
+      if (!last && k > 0) products(pg, pq, 2);
+      else if (!last) products(pg, pg, 1);
+      else if (k > 0) products(pq, pq, 1);
+      if (k > 0) { const int t = Q; Q = Qn; Qn = t; }
+      if (!last) products(ppg, ppg, 1);
     }
   }
   const dim3 ga(unsigned((d + 255) / 256), unsigned(mats), unsigned(st));
