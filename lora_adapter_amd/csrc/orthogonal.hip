@@ -250,59 +250,162 @@ __global__ __launch_bounds__(256) void momentum_kernel(OrthArgs a) {
 }
 
 // ------------------------------------------------------------ the steps, rank <= 64
-// Symmetric matrices of 16 NB rows in LDS, rows of S doubles (S = 16 NB + 2
-// puts the 16 rows x 2 columns that a half wave reads at once on distinct
-// banks).  Both operands of a product are read along rows (they are
-// symmetric), its upper tiles are computed, four waves taking them in turn,
-// and stored with their mirror images.
-template <int NB, int CT, typename Store>
-__device__ __forceinline__ void sym_tiles(const double *A, const double *B, int first, int n_tiles,
-                                          const Store &store) {
-  constexpr int S = 16 * NB + 2;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// inv from the trace of the summed Gram matrix: zero rows stay zero, a NaN or
+// an infinity reaches every element.
+__device__ __forceinline__ double norm_inv(double tr, float eps) {
+  return tr == 0 ? 0.0 : 1.0 / (sqrt(tr) + double(eps));
+}
+
+// Ranks <= 16: one 16 x 16 tile.  Element v of lane l of an MFMA result is row
+// 4 v + l / 16, column l % 16; operand k of lane l is row l % 16, column 4 k +
+// l / 16.  For a symmetric matrix these are the same value, so a result is the
+// next product's operand as it stands: the steps are MFMAs of one wave and
+// nothing else (four rank-16 matrices, five steps: 6.2 -> 2 us).
+__device__ __forceinline__ f64x4_t sym16(const f64x4_t &A, const f64x4_t &B) {
+  f64x4_t c = {0, 0, 0, 0};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) c = __builtin_amdgcn_mfma_f64_16x16x4f64(A[k], B[k], c, 0, 0, 0);
+  return c;
+}
+
+// All NW waves sum the chunks' partials (each its share, then in wave order);
+// the first runs the steps.
+template <int NW>
+__device__ __forceinline__ void steps16(const OrthArgs &a, int mat, int r, double *lds) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, R = a.R;
   const int lr = lane & 15, lg = lane >> 4;
-  int ti[CT], tj[CT];
-  bool on[CT];
+  const double *p = a.gram + int64_t(mat) * a.chunks * R * R;
+  f64x4_t G = {0, 0, 0, 0};
+  constexpr int CB = 6;                       // chunks whose loads are in flight together
+  for (int c = wave; c < a.chunks; c += NW * CB) {
+    double t[CB][4];
+#pragma unroll
+    for (int u = 0; u < CB; ++u)
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        t[u][v] = p[int64_t(min(c + u * NW, a.chunks - 1)) * R * R + (4 * v + lg) * R + lr];
+#pragma unroll
+    for (int u = 0; u < CB; ++u)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) G[v] += c + u * NW < a.chunks ? t[u][v] : 0.0;
+  }
+#pragma unroll
+  for (int v = 0; v < 4; ++v) lds[(wave * 4 + v) * 64 + lane] = G[v];
+  __syncthreads();
+  if (wave > 0) return;
+  double tr = 0;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const int i = 4 * v + lg;
+    double s = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) s += lds[(w * 4 + v) * 64 + lane];
+    G[v] = i < r && lr < r ? s : 0.0;
+    tr += i == lr ? G[v] : 0.0;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) tr += __shfl_xor(tr, o, 64);
+  const double inv = norm_inv(tr, a.eps);
+  if (lane == 0) a.rec[mat].inv = float(inv);
+  f64x4_t Q, P;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) G[v] *= inv * inv;
+  for (int k = 0; k < a.steps; ++k) {
+    const f64x4_t H = sym16(G, G);
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      P[v] = (4 * v + lg == lr ? double(a.ca) : 0.0) + double(a.cb) * G[v] + double(a.cc) * H[v];
+    if (k + 1 < a.steps) G = sym16(P, sym16(P, G));
+    Q = k == 0 ? P : sym16(P, Q);
+  }
+  float *q = a.q + int64_t(mat) * R * R;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) q[(4 * v + lg) * R + lr] = float(Q[v]);
+}
+
+// Larger: symmetric matrices of 16 NB rows in LDS, rows of S doubles (S = 16 NB
+// + 2 puts the 16 rows x 2 columns that a half wave reads at once on distinct
+// banks).  Both operands of a product are read along rows (they are
+// symmetric); its upper tiles are taken by the waves in turn and stored with
+// their mirror images.
+template <int NB>
+struct SymMat {
+  static constexpr int n = 16 * NB, S = n + 2, SIZE = n * S, NT = NB * (NB + 1) / 2;
+};
+
+// CT tiles (ti, tj) of C = A . B; store(i, j, value, tile off the diagonal).
+template <int NB, int CT, typename Store>
+__device__ __forceinline__ void sym_tiles(const double *A, const double *B, const int (&ti)[CT],
+                                          const int (&tj)[CT], const Store &store) {
+  constexpr int S = SymMat<NB>::S;
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const double *pa[CT], *pb[CT];
   f64x4_t acc[CT];
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
-    int t = wave + 4 * c - first;
-    on[c] = t >= 0 && t < n_tiles;
-    t = on[c] ? t : 0;
-    int j = 0;
-    while (t > j) { t -= j + 1; ++j; }
-    ti[c] = t; tj[c] = j;
+    pa[c] = A + (ti[c] * 16 + lr) * S + lg;
+    pb[c] = B + (tj[c] * 16 + lr) * S + lg;
     acc[c] = f64x4_t{0, 0, 0, 0};
   }
-#pragma unroll 4
-  for (int k = 0; k < 4 * NB; ++k) {
+  // unrolled whole: in a loop the compiler moves every accumulator between the
+  // two register files each time round, behind a drained pipe
+#pragma unroll
+  for (int k = 0; k < 4 * NB; ++k)
 #pragma unroll
     for (int c = 0; c < CT; ++c)
-      acc[c] = __builtin_amdgcn_mfma_f64_16x16x4f64(A[(ti[c] * 16 + lr) * S + 4 * k + lg],
-                                                    B[(tj[c] * 16 + lr) * S + 4 * k + lg], acc[c], 0, 0, 0);
-  }
+      acc[c] = __builtin_amdgcn_mfma_f64_16x16x4f64(pa[c][4 * k], pb[c][4 * k], acc[c], 0, 0, 0);
 #pragma unroll
   for (int c = 0; c < CT; ++c)
-    if (on[c])
 #pragma unroll
-      for (int v = 0; v < 4; ++v) store(ti[c] * 16 + 4 * v + lg, tj[c] * 16 + lr, acc[c][v]);
+    for (int v = 0; v < 4; ++v)
+      store(ti[c] * 16 + 4 * v + lg, tj[c] * 16 + lr, acc[c][v], ti[c] != tj[c]);
 }
 
-template <int NB>
+// This wave's tiles w, w + NW, .. of a product (at most 2), without idle MFMAs
+// for the waves that have fewer.
+template <int NB, int NW>
+struct MyTiles {
+  int n, ti[2], tj[2];
+  __device__ __forceinline__ MyTiles() {
+    constexpr int NT = SymMat<NB>::NT;
+    static_assert(NT <= 2 * NW, "at most two tiles a wave");
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    n = w >= NT ? 0 : (NT - 1 - w) / NW + 1;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      int t = min(w + c * NW, NT - 1), j = 0;
+      while (t > j) { t -= j + 1; ++j; }
+      ti[c] = t; tj[c] = j;
+    }
+  }
+  template <typename Store>
+  __device__ __forceinline__ void product(const double *A, const double *B, const Store &store) const {
+    if (n == 2) {
+      sym_tiles<NB, 2>(A, B, ti, tj, store);
+    } else if (n == 1) {
+      const int i1[1] = {ti[0]}, j1[1] = {tj[0]};
+      sym_tiles<NB, 1>(A, B, i1, j1, store);
+    }
+  }
+};
+
+template <int NB, int NW>
 __device__ __forceinline__ void steps_body(const OrthArgs &a, int mat, int r, double *lds) {
-  constexpr int n = 16 * NB, S = n + 2, NT = NB * (NB + 1) / 2, CT = (NT + 3) / 4;
-  double *G = lds, *P = G + n * S, *Q = P + n * S, *T = Q + n * S;
+  using M = SymMat<NB>;
+  constexpr int n = M::n, S = M::S, NTH = NW * 64;
+  double *G = lds, *P = G + M::SIZE, *Q = P + M::SIZE, *T = Q + M::SIZE;
   const int tid = threadIdx.x, R = a.R;
+  const MyTiles<NB, NW> mine;
   // the chunks' partials in order, the loads of all of a thread's elements
-  // (and of several chunks when it has few) in flight together; elements below
-  // the diagonal tiles mirrored
+  // (and of several chunks) in flight together; elements below the diagonal
+  // tiles mirrored
   {
-    constexpr int EP = n * n / 256, CB = EP >= 4 ? 2 : 8;
+    constexpr int EP = n * n / NTH, CB = 16 / EP > 0 ? 16 / EP : 1;
     const double *p[EP];
     double sum[EP];
 #pragma unroll
     for (int q = 0; q < EP; ++q) {
-      const int i = (tid + q * 256) / n, j = (tid + q * 256) % n;
+      const int i = (tid + q * NTH) / n, j = (tid + q * NTH) % n;
       const bool up = i / 16 <= j / 16;
       const int gi = min(up ? i : j, R - 1), gj = min(up ? j : i, R - 1);
       p[q] = a.gram + int64_t(mat) * a.chunks * R * R + int64_t(gi) * R + gj;
@@ -321,60 +424,65 @@ __device__ __forceinline__ void steps_body(const OrthArgs &a, int mat, int r, do
     }
 #pragma unroll
     for (int q = 0; q < EP; ++q) {
-      const int i = (tid + q * 256) / n, j = (tid + q * 256) % n;
+      const int i = (tid + q * NTH) / n, j = (tid + q * NTH) % n;
       G[i * S + j] = i < r && j < r ? sum[q] : 0.0;
     }
   }
   __syncthreads();
-  double tr = 0;
-  for (int i = 0; i < r; ++i) tr += G[i * S + i];
-  // no rows to speak of: zero stays zero; a NaN or an infinity reaches every element
-  const double inv = tr == 0 ? 0.0 : 1.0 / (sqrt(tr) + double(a.eps));
+  // the trace, the same in every wave
+  double tr = (tid & 63) < n ? G[(tid & 63) * (S + 1)] : 0.0;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) tr += __shfl_xor(tr, o, 64);
+  const double inv = norm_inv(tr, a.eps);
   if (tid == 0) a.rec[mat].inv = float(inv);
   __syncthreads();
-  for (int e = tid; e < n * n; e += 256) G[(e / n) * S + e % n] *= inv * inv;
+  for (int e = tid; e < n * n; e += NTH) G[(e / n) * S + e % n] *= inv * inv;
   __syncthreads();
   const double ca = a.ca, cb = a.cb, cc = a.cc;
-  auto put = [&](double *M, int i, int j, double v) {
-    M[i * S + j] = v;
-    if (i / 16 != j / 16) M[j * S + i] = v;
+  auto put = [](double *D, int i, int j, double v, bool off) {
+    D[i * S + j] = v;
+    if (off) D[j * S + i] = v;
   };
   for (int k = 0; k < a.steps; ++k) {
     const bool last = k + 1 == a.steps;
     double *const F = k == 0 ? Q : P;       // the first factor is Q itself
-    sym_tiles<NB, CT>(G, G, 0, NT, [&](int i, int j, double v) {
-      put(F, i, j, (i == j ? ca : 0.0) + cb * G[i * S + j] + cc * v);
+    mine.product(G, G, [&](int i, int j, double v, bool off) {
+      put(F, i, j, (i == j ? ca : 0.0) + cb * G[i * S + j] + cc * v, off);
     });
     __syncthreads();
     if (!last) {
-      sym_tiles<NB, CT>(F, G, 0, NT, [&](int i, int j, double v) { put(T, i, j, v); });
+      mine.product(F, G, [&](int i, int j, double v, bool off) { put(T, i, j, v, off); });
       __syncthreads();
-      sym_tiles<NB, CT>(F, T, 0, NT, [&](int i, int j, double v) { put(G, i, j, v); });
+      mine.product(F, T, [&](int i, int j, double v, bool off) { put(G, i, j, v, off); });
+      __syncthreads();
     }
     if (k > 0) {
       // Q <- P Q by way of T (free again after the barrier)
-      __syncthreads();
-      sym_tiles<NB, CT>(P, Q, 0, NT, [&](int i, int j, double v) { put(T, i, j, v); });
+      mine.product(P, Q, [&](int i, int j, double v, bool off) { put(T, i, j, v, off); });
       __syncthreads();
       double *const t = Q; Q = T; T = t;
     }
-    __syncthreads();
   }
   float *q = a.q + int64_t(mat) * R * R;
-  for (int e = tid; e < n * n; e += 256) {
+  for (int e = tid; e < n * n; e += NTH) {
     const int i = e / n, j = e % n;
     if (i < R && j < R) q[int64_t(i) * R + j] = float(Q[i * S + j]);
   }
 }
 
+// NBMAX: 16-row blocks of the largest rank (4: all that fit a workgroup).
 template <int NBMAX>
-__global__ __launch_bounds__(256) void steps_kernel(OrthArgs a) {
-  __shared__ double steps_lds[4 * (16 * NBMAX) * (16 * NBMAX + 2)];
+__global__ __launch_bounds__(512) void steps_kernel(OrthArgs a) {
+  __shared__ double steps_lds[NBMAX == 1 ? 8 * 256 : 4 * SymMat<NBMAX>::SIZE];
   const int mat = blockIdx.x, r = a.rec[mat].rank;
   if (r < 1 || r > kSmall) return;
-  if (NBMAX == 1 || r <= 16) steps_body<1>(a, mat, r, steps_lds);
-  else if (NBMAX == 2 || r <= 32) steps_body<(NBMAX >= 2 ? 2 : 1)>(a, mat, r, steps_lds);
-  else steps_body<(NBMAX >= 4 ? 4 : 1)>(a, mat, r, steps_lds);
+  if (NBMAX == 1 || r <= 16) {
+    steps16<8>(a, mat, r, steps_lds);
+  } else if (NBMAX == 2 || r <= 32) {
+    if constexpr (NBMAX >= 2) steps_body<2, 8>(a, mat, r, steps_lds);
+  } else {
+    if constexpr (NBMAX >= 4) steps_body<4, 8>(a, mat, r, steps_lds);
+  }
 }
 
 // ------------------------------------------------------------ ranks over 64
@@ -409,7 +517,7 @@ __global__ __launch_bounds__(256) void gram_sum_kernel(OrthArgs a) {
     __syncthreads();
   }
   const double tr = part[0];
-  const double inv = tr == 0 ? 0.0 : 1.0 / (sqrt(tr) + double(a.eps));
+  const double inv = norm_inv(tr, a.eps);
   if (blockIdx.x == 0 && threadIdx.x == 0) a.rec[mat].inv = float(inv);
   double *G = a.big + int64_t(mat) * kBigMats * n;
 #pragma unroll
@@ -434,7 +542,7 @@ struct SymOp {
   int to_q;               // also, in fp32, into q
 };
 
-__global__ __launch_bounds__(256) void sym_product_kernel(OrthArgs a, SymOp op0, SymOp op1) {
+__global__ __launch_bounds__(256, 2) void sym_product_kernel(OrthArgs a, SymOp op0, SymOp op1) {
   constexpr int KB = 64, S = KB + 2;
   __shared__ double la[32 * S], lb[32 * S];
   const int mat = blockIdx.y, r = a.rec[mat].rank, R = a.R;
@@ -613,7 +721,7 @@ __device__ __forceinline__ void apply_body(const OrthArgs &a, const OrthFactor &
 
 // Grid: (columns / 256, matrices, row blocks of 64).
 template <bool kStep, typename E>
-__global__ __launch_bounds__(256) void orth_apply_kernel(OrthArgs a) {
+__global__ __launch_bounds__(256, 2) void orth_apply_kernel(OrthArgs a) {
   __shared__ float lq[kSmall * kApplyQ];
   __shared__ int lp[kApplyRows];
   const OrthRec rc = a.rec[blockIdx.y];
@@ -695,9 +803,9 @@ hipError_t launch_orthogonal(OrthArgs a, int factors, bool step, int dtype, void
   else if (!big) LORA_GRAM(4);
   else LORA_GRAM(8);
 #undef LORA_GRAM
-  if (a.max_rank <= 16) hipLaunchKernelGGL(steps_kernel<1>, dim3(unsigned(mats)), dim3(256), 0, s, a);
-  else if (a.max_rank <= 32) hipLaunchKernelGGL(steps_kernel<2>, dim3(unsigned(mats)), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(steps_kernel<4>, dim3(unsigned(mats)), dim3(256), 0, s, a);
+  if (a.max_rank <= 16) hipLaunchKernelGGL(steps_kernel<1>, dim3(unsigned(mats)), dim3(512), 0, s, a);
+  else if (a.max_rank <= 32) hipLaunchKernelGGL(steps_kernel<2>, dim3(unsigned(mats)), dim3(512), 0, s, a);
+  else hipLaunchKernelGGL(steps_kernel<4>, dim3(unsigned(mats)), dim3(512), 0, s, a);
   if (big) {
     hipLaunchKernelGGL(gram_sum_kernel, dim3(unsigned((RR + 1023) / 1024), unsigned(mats)), dim3(256), 0, s, a);
     const int t32 = (a.R + 31) / 32;
