@@ -418,7 +418,7 @@ struct OrthArgs {
   int steps, nesterov;
   float mu, ca, cb, cc, eps;
   // set by the launcher
-  int R, chunks, chunk_cols;
+  int R, chunks, chunk_cols, apply_chunks;
   OrthRec *rec;
   float *q;                 // [matrices][R][R]
   double *gram;             // [matrices][chunks][R][R]

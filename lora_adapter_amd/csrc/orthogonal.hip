@@ -60,69 +60,75 @@ __device__ __forceinline__ int orth_rank(const OrthArgs &a, int m, int *flag, in
   return *flag ? 0 : r;
 }
 
-// Eight columns of a row of the source, and (kStep) of the momentum, held raw
-// until used, so that a step's loads are in flight under the step before.
-template <bool kStep>
+// VC (4 or 8) columns of a row of the source, and (kStep) of the momentum,
+// held raw until used, so that a step's loads are in flight under the step
+// before.
+template <bool kStep, int VC>
 struct RawN {
-  float4 g[2], m[kStep ? 2 : 1];
+  static constexpr int W = VC / 4;
+  float4 g[W], m[kStep ? W : 1];
   __device__ __forceinline__ void load(const OrthFactor &f, int64_t at, bool on) {
     const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-    g[0] = g[1] = m[0] = z;
-    if constexpr (kStep) m[1] = z;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      g[w] = z;
+      if constexpr (kStep) m[w] = z;
+    }
     if (!on) return;
-    const float4 *pg = reinterpret_cast<const float4 *>(f.src + at);
-    g[0] = pg[0];
-    g[1] = pg[1];
-    if constexpr (kStep) {
-      const float4 *pm = reinterpret_cast<const float4 *>(f.momentum + at);
-      m[0] = pm[0];
-      m[1] = pm[1];
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      g[w] = reinterpret_cast<const float4 *>(f.src + at)[w];
+      if constexpr (kStep) m[w] = reinterpret_cast<const float4 *>(f.momentum + at)[w];
     }
   }
   // N from the gradient and the momentum (which kUpdate moves on first and
   // stores); else the source row
   template <bool kUpdate>
   __device__ __forceinline__ void value(const OrthFactor &f, const OrthArgs &a, int64_t at, bool on,
-                                        float v[8]) const {
-    const float gv[8] = {g[0].x, g[0].y, g[0].z, g[0].w, g[1].x, g[1].y, g[1].z, g[1].w};
-    if constexpr (!kStep) {
+                                        float v[VC]) const {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = gv[e];
-    } else {
-      float mv[8] = {m[0].x, m[0].y, m[0].z, m[0].w, m[1].x, m[1].y, m[1].z, m[1].w};
+    for (int w = 0; w < W; ++w) {
+      const float gv[4] = {g[w].x, g[w].y, g[w].z, g[w].w};
+      if constexpr (!kStep) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (kUpdate) mv[e] = a.mu * mv[e] + gv[e];
-        v[e] = a.nesterov ? gv[e] + a.mu * mv[e] : mv[e];
-      }
-      if (kUpdate && on) {
-        *reinterpret_cast<float4 *>(f.momentum + at) = make_float4(mv[0], mv[1], mv[2], mv[3]);
-        *reinterpret_cast<float4 *>(f.momentum + at + 4) = make_float4(mv[4], mv[5], mv[6], mv[7]);
+        for (int e = 0; e < 4; ++e) v[4 * w + e] = gv[e];
+      } else {
+        float mv[4] = {m[w].x, m[w].y, m[w].z, m[w].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (kUpdate) mv[e] = a.mu * mv[e] + gv[e];
+          v[4 * w + e] = a.nesterov ? gv[e] + a.mu * mv[e] : mv[e];
+        }
+        if (kUpdate && on)
+          reinterpret_cast<float4 *>(f.momentum + at)[w] = make_float4(mv[0], mv[1], mv[2], mv[3]);
       }
     }
   }
 };
 
 // ------------------------------------------------------------ Gram partials
-// Row blocks bi .. bi+NB-1 against bj .. bj+NB-1 (16 rows each) over columns
-// [c0, c1).  A wave takes 32 columns at a time: lane l holds row l % 16 and
-// columns 8 (l / 16) .. +7 of every block, one MFMA step per column of the 8
-// (four columns each; the order of the sum over columns is free).  The four
-// waves' sums are added in wave order through LDS.
+// Row blocks bi .. bi+NB-1 against bj .. bj+NB-1 (16 rows each, those past the
+// rank left out) over columns [c0, c1).  A wave takes 32 columns of every 128,
+// 4 VC at a time: lane l holds row l % 16 and VC columns of every block, one
+// MFMA step per column of the VC (four columns each; the order of the sum over
+// columns is free).  Pairs of different blocks take VC = 4: with 8 the second
+// of two waves per SIMD would not fit the registers.  The four waves' sums are
+// added in wave order through LDS.
 template <int NB, bool kDiag, bool kStep, bool kUpdate>
 __device__ __forceinline__ void gram_body(const OrthArgs &a, const OrthFactor &f, int r, int ps, int bi,
                                           int bj, int c0, int c1, double *out, double *red) {
-  constexpr int NJ = kDiag ? 1 : NB;
+  constexpr int NJ = kDiag ? 1 : NB, VC = kDiag ? 8 : 4, H = 8 / VC;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int lr = lane & 15, lg = lane >> 4;
+  const int nbj = min(NB, (r + 15) / 16 - bj);     // column blocks with rows of the matrix
   int64_t ri[NB], rj[NJ];
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
     const int row = (bi + i) * 16 + lr;
-    ri[i] = row < r ? int64_t(a.pool.page_ids[ps + row]) * f.d + lg * 8 : -1;
+    ri[i] = row < r ? int64_t(a.pool.page_ids[ps + row]) * f.d + lg * VC : -1;
     if constexpr (!kDiag) {
       const int col = (bj + i) * 16 + lr;
-      rj[i] = col < r ? int64_t(a.pool.page_ids[ps + col]) * f.d + lg * 8 : -1;
+      rj[i] = col < r ? int64_t(a.pool.page_ids[ps + col]) * f.d + lg * VC : -1;
     }
   }
   f64x4_t acc[NB][NB];
@@ -130,7 +136,7 @@ __device__ __forceinline__ void gram_body(const OrthArgs &a, const OrthFactor &f
   for (int i = 0; i < NB; ++i)
 #pragma unroll
     for (int j = 0; j < NB; ++j) acc[i][j] = f64x4_t{0, 0, 0, 0};
-  RawN<kStep> x[NB], y[NJ];
+  RawN<kStep, VC> x[NB], y[NJ];
   auto load = [&](int c) __attribute__((always_inline)) {
     const bool in = c < c1;
 #pragma unroll
@@ -139,22 +145,26 @@ __device__ __forceinline__ void gram_body(const OrthArgs &a, const OrthFactor &f
       if constexpr (!kDiag) y[i].load(f, rj[i] + c, in && rj[i] >= 0);
     }
   };
-  load(c0 + wave * 32);
-  for (int c = c0 + wave * 32; c < c1; c += 128) {
-    float xv[NB][8], yv[NJ][8];
+  // step s: columns of the wave's s-th group of 4 VC
+  auto col_of = [&](int st) { return c0 + wave * 32 + (st / H) * 128 + (st % H) * (4 * VC); };
+  load(col_of(0));
+  for (int st = 0; col_of(st) < c1; ++st) {
+    const int c = col_of(st);
+    float xv[NB][VC], yv[NJ][VC];
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
       x[i].template value<kUpdate>(f, a, ri[i] + c, ri[i] >= 0, xv[i]);
       if constexpr (!kDiag) y[i].template value<false>(f, a, 0, false, yv[i]);
     }
-    load(c + 128);
+    load(col_of(st + 1));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < VC; ++e) {
       double dx[NB];
 #pragma unroll
       for (int i = 0; i < NB; ++i) dx[i] = double(xv[i][e]);
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
+        if (NB > 1 && j >= nbj) break;
         const double dy = kDiag ? dx[j] : double(yv[kDiag ? 0 : j][e]);
 #pragma unroll
         for (int i = 0; i < (kDiag ? j + 1 : NB); ++i)
@@ -180,10 +190,10 @@ __device__ __forceinline__ void gram_body(const OrthArgs &a, const OrthFactor &f
   }
   const int R = a.R;
   for (int e = threadIdx.x; e < S * S; e += 256) {
+    // below the diagonal tiles: the mirror image, so that whole rows are read
     const int i = e / S, j = e % S;
-    if (kDiag && i / 16 > j / 16) continue;
     const int gi = bi * 16 + i, gj = bj * 16 + j;
-    if (gi < R && gj < R) out[int64_t(gi) * R + gj] = red[e];
+    if (gi < R && gj < R) out[int64_t(gi) * R + gj] = red[kDiag && i / 16 > j / 16 ? j * S + i : e];
   }
 }
 
@@ -192,7 +202,7 @@ __device__ __forceinline__ void gram_body(const OrthArgs &a, const OrthFactor &f
 // NBMAX: 16-row blocks of the largest rank, 8 for ranks over 64 (a launch of
 // small ranks then keeps the registers, and the waves per SIMD, of its own).
 template <bool kStep, int NBMAX>
-__global__ __launch_bounds__(256, NBMAX <= 2 ? 4 : NBMAX == 4 ? 2 : 1) void gram_kernel(OrthArgs a) {
+__global__ __launch_bounds__(256, NBMAX <= 2 ? 4 : 2) void gram_kernel(OrthArgs a) {
   constexpr int S = 16 * (NBMAX < 4 ? NBMAX : 4);
   __shared__ double red[S * S];
   __shared__ int flag;
@@ -242,7 +252,7 @@ __global__ __launch_bounds__(256) void momentum_kernel(OrthArgs a) {
   if (col >= f.d) return;
   for (int row = blockIdx.z; row < r; row += gridDim.z) {
     const int64_t at = int64_t(a.pool.page_ids[ps + row]) * f.d + col;
-    RawN<true> x;
+    RawN<true, 8> x;
     x.load(f, at, true);
     float v[8];
     x.value<true>(f, a, at, true, v);
@@ -397,18 +407,15 @@ __device__ __forceinline__ void steps_body(const OrthArgs &a, int mat, int r, do
   const int tid = threadIdx.x, R = a.R;
   const MyTiles<NB, NW> mine;
   // the chunks' partials in order, the loads of all of a thread's elements
-  // (and of several chunks) in flight together; elements below the diagonal
-  // tiles mirrored
+  // (and of several chunks) in flight together
   {
-    constexpr int EP = n * n / NTH, CB = 16 / EP > 0 ? 16 / EP : 1;
+    constexpr int EP = n * n / NTH, CB = 16 / EP;
     const double *p[EP];
     double sum[EP];
 #pragma unroll
     for (int q = 0; q < EP; ++q) {
       const int i = (tid + q * NTH) / n, j = (tid + q * NTH) % n;
-      const bool up = i / 16 <= j / 16;
-      const int gi = min(up ? i : j, R - 1), gj = min(up ? j : i, R - 1);
-      p[q] = a.gram + int64_t(mat) * a.chunks * R * R + int64_t(gi) * R + gj;
+      p[q] = a.gram + int64_t(mat) * a.chunks * R * R + int64_t(min(i, R - 1)) * R + min(j, R - 1);
       sum[q] = 0;
     }
     for (int c = 0; c < a.chunks; c += CB) {
@@ -486,47 +493,67 @@ __global__ __launch_bounds__(512) void steps_kernel(OrthArgs a) {
 }
 
 // ------------------------------------------------------------ ranks over 64
-// Sum of the chunks' partials, normalised, both halves filled.  Grid:
-// (elements / 1024, matrices); every workgroup takes the trace itself.
+// Sum of the chunks' partials, normalised.  Grid: (16-row strips of the 64 x 64
+// blocks (si <= sj), matrices); blocks off the diagonal are stored with their
+// mirror images.  Every workgroup takes the trace itself.
 __global__ __launch_bounds__(256) void gram_sum_kernel(OrthArgs a) {
   const int mat = blockIdx.y, r = a.rec[mat].rank, R = a.R;
   if (r <= kSmall) return;
-  __shared__ double part[256];
-  const double *p = a.gram + int64_t(mat) * a.chunks * R * R;
-  double t = 0;
-  for (int i = threadIdx.x; i < r; i += 256)
-    for (int c = 0; c < a.chunks; ++c) t += p[int64_t(c) * R * R + int64_t(i) * R + i];
-  double sum[4] = {0, 0, 0, 0};
+  __shared__ double part[256], turn[16][65];
+  int si = blockIdx.x >> 2, sj = 0;
+  while (si > sj) { si -= sj + 1; ++sj; }
+  const int64_t n = int64_t(R) * R;
+  const double *p = a.gram + int64_t(mat) * a.chunks * n;
+  const int tid = threadIdx.x, i0 = si * kSmall + (blockIdx.x & 3) * 16, j = sj * kSmall + (tid & 63);
+  if (i0 >= R) return;
+  double t = 0, sum[4] = {0, 0, 0, 0};
   int64_t at[4];
-  const int64_t e0 = int64_t(blockIdx.x) * 1024 + threadIdx.x, n = int64_t(R) * R;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int64_t e = min(e0 + q * 256, n - 1);
-    const int i = int(e / R), j = int(e % R);
-    at[q] = i / 16 <= j / 16 ? e : int64_t(j) * R + i;
+  for (int q = 0; q < 4; ++q) at[q] = int64_t(min(i0 + (tid >> 6) + 4 * q, R - 1)) * R + min(j, R - 1);
+  // eight chunks' loads in flight, added in order
+  for (int c = 0; c < a.chunks; c += 8) {
+    double v[8][4], d[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const double *pc = p + int64_t(min(c + u, a.chunks - 1)) * n;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[u][q] = pc[at[q]];
+      d[u] = pc[int64_t(min(tid, r - 1)) * (R + 1)];
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const bool in = c + u < a.chunks;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sum[q] += in ? v[u][q] : 0.0;
+      t += in && tid < r ? d[u] : 0.0;
+    }
   }
-#pragma unroll 2
-  for (int c = 0; c < a.chunks; ++c)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) sum[q] += p[int64_t(c) * n + at[q]];
-  part[threadIdx.x] = t;
+  for (int i = tid + 256; i < r; i += 256)
+    for (int c = 0; c < a.chunks; ++c) t += p[int64_t(c) * n + int64_t(i) * (R + 1)];
+  part[tid] = t;
   __syncthreads();
   // a fixed tree: the same trace in every workgroup
   for (int o = 128; o > 0; o >>= 1) {
-    if (int(threadIdx.x) < o) part[threadIdx.x] += part[threadIdx.x + o];
+    if (tid < o) part[tid] += part[tid + o];
     __syncthreads();
   }
-  const double tr = part[0];
-  const double inv = norm_inv(tr, a.eps);
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.rec[mat].inv = float(inv);
+  const double inv = norm_inv(part[0], a.eps);
+  if (blockIdx.x == 0 && tid == 0) a.rec[mat].inv = float(inv);
   double *G = a.big + int64_t(mat) * kBigMats * n;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const int64_t e = e0 + q * 256;
-    if (e >= n) break;
-    const int i = int(e / R), j = int(e % R);
+    const int y = (tid >> 6) + 4 * q, i = i0 + y;
     // past the rank the partials were never written
-    G[e] = i < r && j < r ? sum[q] * (inv * inv) : 0.0;
+    const double v = i < r && j < r ? sum[q] * (inv * inv) : 0.0;
+    if (i < R && j < R) G[int64_t(i) * R + j] = v;
+    turn[y][tid & 63] = v;
+  }
+  if (si == sj) return;
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int x = (tid >> 4) + 16 * q, i = sj * kSmall + x, c = i0 + (tid & 15);
+    if (i < R && c < R) G[int64_t(i) * R + c] = turn[tid & 15][x];
   }
 }
 
@@ -569,6 +596,11 @@ __global__ __launch_bounds__(256, 2) void sym_product_kernel(OrthArgs a, SymOp o
     }
   };
   load(0);
+  const int i0 = t * 32 + (wave >> 1) * 16, j0 = tj * 32 + (wave & 1) * 16;
+  double lin[4];                                     // the linear term's elements
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    lin[v] = op.poly ? A[int64_t(min(i0 + 4 * v + lg, R - 1)) * R + min(j0 + lr, R - 1)] : 0.0;
   f64x4_t acc = {0, 0, 0, 0};
   const double *pa = la + ((wave >> 1) * 16 + lr) * S + lg, *pb = lb + ((wave & 1) * 16 + lr) * S + lg;
   for (int k0 = 0; k0 < n; k0 += KB) {
@@ -586,164 +618,215 @@ __global__ __launch_bounds__(256, 2) void sym_product_kernel(OrthArgs a, SymOp o
         acc = __builtin_amdgcn_mfma_f64_16x16x4f64(pa[k + u], pb[k + u], acc, 0, 0, 0);
     __syncthreads();
   }
-  const int i0 = t * 32 + (wave >> 1) * 16, j0 = tj * 32 + (wave & 1) * 16;
-  if (i0 >= R || j0 >= R) return;
-  double *C = base + int64_t(op.C) * R * R;
-  double *D = op.copy >= 0 ? base + int64_t(op.copy) * R * R : nullptr;
-  float *q = a.q + int64_t(mat) * R * R;
+  // the tile through LDS (rows of 33), so that it and its mirror image are
+  // stored along rows
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     const int i = i0 + 4 * v + lg, j = j0 + lr;
     double x = acc[v];
-    if (op.poly) x = (i == j ? double(a.ca) : 0.0) + double(a.cb) * A[int64_t(i) * R + j] + double(a.cc) * x;
-    const int64_t at = int64_t(i) * R + j, mir = int64_t(j) * R + i;
-    C[at] = x;
-    if (t != tj) C[mir] = x;
-    if (D) {
-      D[at] = x;
-      if (t != tj) D[mir] = x;
-    }
-    if (op.to_q) {
-      q[at] = float(x);
-      if (t != tj) q[mir] = float(x);
-    }
+    if (op.poly) x = (i == j ? double(a.ca) : 0.0) + double(a.cb) * lin[v] + double(a.cc) * x;
+    la[((wave >> 1) * 16 + 4 * v + lg) * 33 + (wave & 1) * 16 + lr] = x;
+  }
+  __syncthreads();
+  double *C = base + int64_t(op.C) * R * R;
+  double *D = op.copy >= 0 ? base + int64_t(op.copy) * R * R : nullptr;
+  float *q = a.q + int64_t(mat) * R * R;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    // u < 4: rows of the tile; u >= 4: rows of its mirror image
+    const int e = (u & 3) * 256 + tid, y = e >> 5, x = e & 31;
+    const bool mir = u >= 4;
+    if (mir && t == tj) break;
+    const int i = (mir ? tj : t) * 32 + y, j = (mir ? t : tj) * 32 + x;
+    if (i >= R || j >= R) continue;
+    const double val = mir ? la[x * 33 + y] : la[y * 33 + x];
+    const int64_t at = int64_t(i) * R + j;
+    C[at] = val;
+    if (D) D[at] = val;
+    if (op.to_q) q[at] = float(val);
   }
 }
 
 // ------------------------------------------------------------ the product with N
-// Rows ib*16 .. of O = Q (N inv): a wave takes 64 columns, lane l the four
-// columns 4 (l % 16) .. +3 of row l / 16 of every four, so a load is 256
-// contiguous bytes per row; column tile e holds columns 4 c + e, and the four
-// tiles' results are four consecutive columns again.  128 rows of N at a time:
-// their page offsets and columns of Q go through LDS, and eight loads of N
-// are in flight ahead of the MFMAs.
+// Rows 16 ib .. of O = Q (N inv) for `chunks` runs of 256 columns: a wave takes
+// 64 columns of a run, lane l the four columns 4 (l % 16) .. +3 of row l / 16
+// of every four, so a load is 256 contiguous bytes per row; column tile e
+// holds columns 4 c + e, and the four tiles' results are four consecutive
+// columns again.  The rows come U groups of four at a time, the next groups
+// (of the same run or the next) in flight under the MFMAs of these.  Q's
+// columns and the rows' pages go through LDS, 128 of them at a time (up to
+// rank 128 once for all the runs).
 constexpr int kApplyRows = 128, kApplyQ = kApplyRows + 4;
 
 template <int NB, bool kStep, typename E>
 __device__ __forceinline__ void apply_body(const OrthArgs &a, const OrthFactor &f, int r, int ps, float inv,
-                                           int ib, const float *q, int col0, float *lq, int *lp) {
-  constexpr int U = 8;                        // groups of four rows in flight
+                                           int ib, const float *q, int col0, int chunks, float *lq, int *lp) {
+  constexpr int U = 4;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int lr = lane & 15, lg = lane >> 4;
-  const int col = min(col0 + wave * 64, f.d - 64) + lr * 4;
-  const bool on = col0 + wave * 64 < f.d;     // every wave stays for the barriers
   const int R = a.R;
+  auto column = [&](int ck) { return min(col0 + ck * 256 + wave * 64, f.d - 64) + lr * 4; };
+  struct Rows {
+    float4 x[U], m[kStep ? U : 1];
+  };
+  // groups k0 .. of the staged rows, columns of run ck; rows past the staged
+  // ones repeat the last (they are cleared before use)
+  auto load = [&](Rows &w, int ck, int k0, int n16) __attribute__((always_inline)) {
+    const int col = column(ck);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t at = int64_t(lp[min(k0 + 4 * u + lg, n16 - 1)]) * f.d + col;
+      w.x[u] = *reinterpret_cast<const float4 *>(f.src + at);
+      if constexpr (kStep) w.m[u] = *reinterpret_cast<const float4 *>(f.momentum + at);
+    }
+  };
   f32x4_t acc[NB][4];
+  auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
-  for (int i = 0; i < NB; ++i)
+    for (int i = 0; i < NB; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[i][e] = f32x4_t{0, 0, 0, 0};
-  for (int r0 = 0; r0 < r; r0 += kApplyRows) {
-    const int nr = min(kApplyRows, r - r0), n16 = (nr + 15) / 16 * 16;
-    if (r0 > 0) __syncthreads();
-    if (tid < n16) lp[tid] = a.pool.page_ids[ps + r0 + min(tid, nr - 1)];
-    for (int e = tid; e < NB * 16 * n16; e += 256) {
-      const int i = e / n16, k = e % n16;
-      const int qi = ib * 16 + i;
-      lq[i * kApplyQ + k] = k < nr && qi < R ? q[int64_t(qi) * R + r0 + k] : 0.f;
-    }
-    __syncthreads();
-    for (int k0 = 0; k0 < n16; k0 += 4 * U) {
-      float4 x[U], m[kStep ? U : 1];
+      for (int e = 0; e < 4; ++e) acc[i][e] = f32x4_t{0, 0, 0, 0};
+  };
+  auto add = [&](const Rows &w, int k0, int nr, int n16) __attribute__((always_inline)) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        // rows past the rank: the last row again, times a zero of Q (its own
-        // Inf or NaN must not enter twice: cleared below)
-        const int k = min(k0 + 4 * u + lg, n16 - 1);
-        const int64_t at = int64_t(lp[k]) * f.d + col;
-        x[u] = *reinterpret_cast<const float4 *>(f.src + at);
-        if constexpr (kStep) m[u] = *reinterpret_cast<const float4 *>(f.momentum + at);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = k0 + 4 * u + lg;
-        if (k0 + 4 * u >= n16) break;
-        float4 v = x[u];
-        if constexpr (kStep) {
-          const float4 w = m[u];
-          if (a.nesterov)
-            v = make_float4(v.x + a.mu * w.x, v.y + a.mu * w.y, v.z + a.mu * w.z, v.w + a.mu * w.w);
-          else
-            v = w;
-        }
-        if (k >= nr) v = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float b[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-          const float av = lq[(i * 16 + lr) * kApplyQ + k];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            acc[i][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(av, b[e], acc[i][e], 0, 0, 0);
-        }
-      }
-    }
-  }
-  if (!on) return;
-  // acc element v of lane l: row 4 (l / 16) + v, column l % 16 of its tile
-#pragma unroll
-  for (int i = 0; i < NB; ++i) {
-    int64_t at[4];
-    float4 mw[4];
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int row = min((ib + i) * 16 + lg * 4 + v, r - 1);
-      at[v] = int64_t(a.pool.page_ids[ps + row]) * f.d + col;
+    for (int u = 0; u < U; ++u) {
+      if (k0 + 4 * u >= n16) break;
+      const int k = k0 + 4 * u + lg;
+      float4 v = w.x[u];
       if constexpr (kStep) {
-        if (f.master) {
-          mw[v] = *reinterpret_cast<const float4 *>(f.master + at[v]);
+        const float4 t = w.m[u];
+        if (a.nesterov)
+          v = make_float4(v.x + a.mu * t.x, v.y + a.mu * t.y, v.z + a.mu * t.z, v.w + a.mu * t.w);
+        else
+          v = t;
+      }
+      if (k >= nr) v = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float b[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const float av = lq[(i * 16 + lr) * kApplyQ + k];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc[i][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(av, b[e], acc[i][e], 0, 0, 0);
+      }
+    }
+  };
+  auto pages = [&](int r0, int nr, int n16) __attribute__((always_inline)) {
+    if (tid < n16) lp[tid] = a.pool.page_ids[ps + r0 + min(tid, nr - 1)];
+  };
+  auto stage_q = [&](int r0, int nr, int n16) __attribute__((always_inline)) {
+    for (int i = wave; i < NB * 16; i += 4) {
+      const int qi = ib * 16 + i;
+      for (int k = lane; k < n16; k += 64)
+        lq[i * kApplyQ + k] = k < nr && qi < R ? q[int64_t(qi) * R + r0 + k] : 0.f;
+    }
+  };
+  // acc element v of lane l: row 4 (l / 16) + v, column l % 16 of its tile
+  auto store = [&](int ck) __attribute__((always_inline)) {
+    if (col0 + ck * 256 + wave * 64 >= f.d) return;
+    const int col = column(ck);
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      // one row block at a time: its weights' registers are free for the next
+      __builtin_amdgcn_sched_barrier(0);
+      int64_t at[4];
+      float4 mw[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int row = min((ib + i) * 16 + lg * 4 + v, r - 1);
+        at[v] = int64_t(r <= kApplyRows ? lp[row] : a.pool.page_ids[ps + row]) * f.d + col;
+        if constexpr (kStep) {
+          if (f.master) {
+            mw[v] = *reinterpret_cast<const float4 *>(f.master + at[v]);
+          } else {
+            const E *pg = static_cast<const E *>(f.pages) + at[v];
+            mw[v] = make_float4(Elem<E>::load1(pg), Elem<E>::load1(pg + 1), Elem<E>::load1(pg + 2),
+                                Elem<E>::load1(pg + 3));
+          }
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        if ((ib + i) * 16 + lg * 4 + v >= r) continue;
+        const float o[4] = {acc[i][0][v], acc[i][1][v], acc[i][2][v], acc[i][3][v]};
+        if constexpr (!kStep) {
+          *reinterpret_cast<float4 *>(f.out + at[v]) = make_float4(o[0], o[1], o[2], o[3]);
         } else {
-          const E *pg = static_cast<const E *>(f.pages) + at[v];
-          mw[v] = make_float4(Elem<E>::load1(pg), Elem<E>::load1(pg + 1), Elem<E>::load1(pg + 2),
-                              Elem<E>::load1(pg + 3));
+          float w[4] = {mw[v].x, mw[v].y, mw[v].z, mw[v].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = w[e] * f.keep - f.lr * o[e];
+          if (f.master) *reinterpret_cast<float4 *>(f.master + at[v]) = make_float4(w[0], w[1], w[2], w[3]);
+          E *pg = static_cast<E *>(f.pages) + at[v];
+          if constexpr (sizeof(E) == 2)
+            *reinterpret_cast<uint2 *>(pg) = make_uint2(f2bf2(w[0], w[1]), f2bf2(w[2], w[3]));
+          else
+            *reinterpret_cast<float4 *>(pg) = make_float4(w[0], w[1], w[2], w[3]);
         }
       }
     }
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      if ((ib + i) * 16 + lg * 4 + v >= r) continue;
-      const float o[4] = {acc[i][0][v], acc[i][1][v], acc[i][2][v], acc[i][3][v]};
-      if constexpr (!kStep) {
-        *reinterpret_cast<float4 *>(f.out + at[v]) = make_float4(o[0], o[1], o[2], o[3]);
-      } else {
-        float w[4] = {mw[v].x, mw[v].y, mw[v].z, mw[v].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = w[e] * f.keep - f.lr * o[e];
-        if (f.master) *reinterpret_cast<float4 *>(f.master + at[v]) = make_float4(w[0], w[1], w[2], w[3]);
-        E *pg = static_cast<E *>(f.pages) + at[v];
-        if constexpr (sizeof(E) == 2)
-          *reinterpret_cast<uint2 *>(pg) = make_uint2(f2bf2(w[0], w[1]), f2bf2(w[2], w[3]));
-        else
-          *reinterpret_cast<float4 *>(pg) = make_float4(w[0], w[1], w[2], w[3]);
+  };
+  Rows w0;
+  if (r <= kApplyRows) {
+    const int n16 = (r + 15) / 16 * 16;
+    pages(0, r, n16);
+    __syncthreads();
+    stage_q(0, r, n16);
+    __syncthreads();
+    for (int ck = 0; ck < chunks; ++ck) {
+      clear();
+      for (int k0 = 0; k0 < n16; k0 += 4 * U) {
+        load(w0, ck, k0, n16);
+        add(w0, k0, r, n16);
+      }
+      store(ck);
+    }
+    return;
+  }
+  for (int ck = 0; ck < chunks; ++ck) {
+    clear();
+    for (int r0 = 0; r0 < r; r0 += kApplyRows) {
+      const int nr = min(kApplyRows, r - r0), n16 = (nr + 15) / 16 * 16;
+      __syncthreads();                         // the last rows and Q are done with
+      pages(r0, nr, n16);
+      __syncthreads();
+      stage_q(r0, nr, n16);
+      __syncthreads();
+      for (int k0 = 0; k0 < n16; k0 += 4 * U) {
+        load(w0, ck, k0, n16);
+        add(w0, k0, nr, n16);
       }
     }
+    store(ck);
   }
 }
 
-// Grid: (columns / 256, matrices, row blocks of 64).
+// Grid: (runs of a.apply_chunks x 256 columns, matrices, row blocks of 64).
 template <bool kStep, typename E>
-__global__ __launch_bounds__(256, 2) void orth_apply_kernel(OrthArgs a) {
+__global__ __launch_bounds__(256, 4) void orth_apply_kernel(OrthArgs a) {
   __shared__ float lq[kSmall * kApplyQ];
   __shared__ int lp[kApplyRows];
   const OrthRec rc = a.rec[blockIdx.y];
   const OrthFactor &f = a.f[blockIdx.y / a.M];
   const int ib = blockIdx.z * 4;
-  const int col0 = blockIdx.x * 256;
+  const int col0 = blockIdx.x * a.apply_chunks * 256;
   if (rc.rank <= ib * 16 || col0 >= f.d) return;
+  const int chunks = min(a.apply_chunks, (f.d - col0 + 255) / 256);
   const float *q = a.q + int64_t(blockIdx.y) * a.R * a.R;
   const int left = rc.rank - ib * 16;         // output rows from ib * 16
-  if (left <= 16) apply_body<1, kStep, E>(a, f, rc.rank, rc.page_start, rc.inv, ib, q, col0, lq, lp);
-  else if (left <= 32) apply_body<2, kStep, E>(a, f, rc.rank, rc.page_start, rc.inv, ib, q, col0, lq, lp);
-  else apply_body<4, kStep, E>(a, f, rc.rank, rc.page_start, rc.inv, ib, q, col0, lq, lp);
+  if (left <= 16) apply_body<1, kStep, E>(a, f, rc.rank, rc.page_start, rc.inv, ib, q, col0, chunks, lq, lp);
+  else if (left <= 32) apply_body<2, kStep, E>(a, f, rc.rank, rc.page_start, rc.inv, ib, q, col0, chunks, lq, lp);
+  else apply_body<4, kStep, E>(a, f, rc.rank, rc.page_start, rc.inv, ib, q, col0, chunks, lq, lp);
 }
 
 int orth_r(int max_rank) { return (max_rank + 15) / 16 * 16; }
 
 // Column chunks of the Gram launch: about 1024 workgroups, at least 256 columns
-// each (two steps of each wave).
+// each (two steps of each wave); 3072 where ranks go over 64, whose pairs of
+// blocks take unlike times.
 int orth_chunk_cols(int64_t mats, int max_rank, int d) {
   const int s = (max_rank + kSmall - 1) / kSmall;
   const int64_t per = mats * (s * (s + 1) / 2);
-  const int64_t want = (1024 + per - 1) / per;
+  const int64_t want = ((max_rank > kSmall ? 3072 : 1024) + per - 1) / per;
   int64_t cols = (d + want - 1) / want;
   cols = (cols + 127) / 128 * 128;
   return int(cols < 256 ? 256 : cols);
@@ -807,7 +890,7 @@ hipError_t launch_orthogonal(OrthArgs a, int factors, bool step, int dtype, void
   else if (a.max_rank <= 32) hipLaunchKernelGGL(steps_kernel<2>, dim3(unsigned(mats)), dim3(512), 0, s, a);
   else hipLaunchKernelGGL(steps_kernel<4>, dim3(unsigned(mats)), dim3(512), 0, s, a);
   if (big) {
-    hipLaunchKernelGGL(gram_sum_kernel, dim3(unsigned((RR + 1023) / 1024), unsigned(mats)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(gram_sum_kernel, dim3(unsigned(4 * (st * (st + 1) / 2)), unsigned(mats)), dim3(256), 0, s, a);
     const int t32 = (a.R + 31) / 32;
     const unsigned tiles = unsigned(t32 * (t32 + 1) / 2);
     auto products = [&](const SymOp &x, const SymOp &y, unsigned n) {
@@ -828,7 +911,11 @@ hipError_t launch_orthogonal(OrthArgs a, int factors, bool step, int dtype, void
       if (!last) products(ppg, ppg, 1);
     }
   }
-  const dim3 ga(unsigned((d + 255) / 256), unsigned(mats), unsigned(st));
+  // about 8192 workgroups: enough to even out unlike ranks, few enough that Q
+  // is staged for several runs of columns where matrices are many
+  const int64_t runs = (d + 255) / 256, all = runs * mats * st;
+  a.apply_chunks = int(all / 8192 < 1 ? 1 : all / 8192 > runs ? runs : all / 8192);
+  const dim3 ga(unsigned((runs + a.apply_chunks - 1) / a.apply_chunks), unsigned(mats), unsigned(st));
   if (!step) hipLaunchKernelGGL((orth_apply_kernel<false, float>), ga, dim3(256), 0, s, a);
   else if (dtype == LORA_BF16) hipLaunchKernelGGL((orth_apply_kernel<true, uint16_t>), ga, dim3(256), 0, s, a);
   else hipLaunchKernelGGL((orth_apply_kernel<true, float>), ga, dim3(256), 0, s, a);
