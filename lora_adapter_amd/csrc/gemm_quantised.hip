@@ -239,7 +239,7 @@ __device__ __forceinline__ void q_tile_run(const QGemmArgs &q, char *smem, int m
   using C = TileCfg<BM, BN, WM, WN>;
   using Q = QTileLds<BM, BN, NS>;
   constexpr int TM = C::TM, TN = C::TN, NM = TM * TN, LPW = C::LPW + 1;
-  static_assert(BM == 256 && TM == 4, "a lane's scale word holds its wave's four row blocks");
+  static_assert(BM == 256 && (TM == 4 || TM == 2), "a lane's scale word holds its wave's row blocks");
   static_assert(BN % 128 == 0 && TN * 32 <= 128, "a wave's columns lie in one scale block");
   static_assert(NS >= 2 && (NS - 2) * LPW < 64, "stages / vmcnt range");
   const GemmArgs &g = q.g;
@@ -303,8 +303,10 @@ __device__ __forceinline__ void q_tile_run(const QGemmArgs &q, char *smem, int m
   auto frag_b = [&](const char *base, int s, int j) __attribute__((always_inline)) {
     return frag(base, s, BM + wn * TN * 32 + j * 32 + frow);
   };
+  // (waves of two row blocks: the word's upper half for the odd ones)
   auto scale_a = [&](const char *base) __attribute__((always_inline)) {
-    return *reinterpret_cast<const int *>(base + C::STAGE + wm * TM * 32 + frow * 4);
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(base + C::STAGE + wm * TM / 4 * 128 + frow * 4);
+    return int(TM == 4 ? w : w >> (16 * (wm & 1)));
   };
   const char *table = smem + Q::TABLE + (wn * TN * 32 / kQBlock) * kQTableBytes + kt0;
   // MFMAs of one half of a K tile from (fa, xb); the next half's fragments
@@ -431,12 +433,31 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void q_tile_kernel(QGemmArgs q) {
     }
   }
   const int per = (ntiles + 7) / 8;
-  const int t = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  int b = int(blockIdx.x), half = -1;
+  if constexpr (kFused && BN == 256) {
+    // a grid larger than 8 * per asks for the last, partial round of tiles as
+    // two 256 x 128 halves each (as in the bf16 tile kernel)
+    const int nb = 8 * per, n_first = nb - nb % 256;
+    if (int(gridDim.x) > nb && b >= n_first) {
+      half = (b - n_first) & 1;
+      b = n_first + (b - n_first) / 2;
+    }
+  }
+  const int t = (b & 7) * per + (b >> 3);
   if (t >= ntiles) return;
   int tm, tn;
   tile_coords(t, tiles_m, tiles_n, tm, tn);
   const int k0 = blockIdx.y * (g.k_split / kQBlock);
   if (k0 >= KT) return;
+  if constexpr (kFused && BN == 256) {
+    if (half >= 0) {
+      const int n0 = tn * BN + half * (BN / 2);
+      if (n0 >= g.N) return;           // a half wholly past the last column
+      q_tile_run<BM, BN / 2, 4, 2, NS, kFused, kMask>(q, smem, tm * BM, n0, k0,
+                                                      min(KT - k0, g.k_split / kQBlock), blockIdx.y);
+      return;
+    }
+  }
   q_tile_run<BM, BN, WM, WN, NS, kFused, kMask>(q, smem, tm * BM, tn * BN, k0,
                                                 min(KT - k0, g.k_split / kQBlock), blockIdx.y);
 }
@@ -505,7 +526,10 @@ hipError_t launch_quantised_gemm(const GemmConfig &c, const QGemmArgs &q, int dt
   if (dtype != LORA_BF16) return hipErrorInvalidConfiguration;
   const int tiles = ((g.M + c.bm - 1) / c.bm) * ((g.N + c.bn - 1) / c.bn);
   if (c.kind == 5) {
-    const dim3 grid(8 * ((tiles + 7) / 8));
+    unsigned gx = 8 * ((tiles + 7) / 8);
+    const unsigned nf = gx - gx % 256, rem = gx - nf;
+    if (nf > 0 && rem > 0 && rem <= 128) gx = nf + 2 * rem;
+    const dim3 grid(gx);
     if (g.mask) hipLaunchKernelGGL((q_tile_kernel<256, 256, 2, 4, 2, true, true>), grid, dim3(512), 0, s, q);
     else hipLaunchKernelGGL((q_tile_kernel<256, 256, 2, 4, 2, true>), grid, dim3(512), 0, s, q);
     return hipGetLastError();
