@@ -66,10 +66,13 @@ __device__ __forceinline__ uint32_t abs_max8(const float v[8]) {
   return m;
 }
 
-// Largest of 16 consecutive lanes, in every one of them.
+// Largest of 16 consecutive lanes (a DPP row), in every one of them: row
+// rotations by 8, 4, 2 and 1, no trip through LDS.
 __device__ __forceinline__ uint32_t max16(uint32_t v) {
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v = max(v, uint32_t(__shfl_xor(int(v), o, 64)));
+  v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x128, 0xf, 0xf, false)));
+  v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x124, 0xf, 0xf, false)));
+  v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x122, 0xf, 0xf, false)));
+  v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x121, 0xf, 0xf, false)));
   return v;
 }
 

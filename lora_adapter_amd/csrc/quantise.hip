@@ -8,38 +8,51 @@
 namespace lora {
 namespace {
 
-// Wave w takes 512 columns of a row, 8 elements per lane; 16 lanes share a
-// block.  Columns past d are zero codes.  kTiled: scale bytes laid out for the
-// tile GEMM (q_tile_scale_at), else in rows.
-template <typename E, bool kTiled>
-__device__ __forceinline__ void quantise_chunk(const E *X, int T, int d, int chunks, uint8_t *codes,
-                                               uint8_t *scale, int64_t w) {
+// Chunks w, w + stride, .. (NC of them; chunk = 512 columns of a row, 8
+// elements per lane), their loads in flight together; 16 lanes share a block.
+// Columns past d are zero codes.  kTiled: scale bytes laid out for the tile
+// GEMM (q_tile_scale_at), else in rows.
+template <typename E, bool kTiled, int NC>
+__device__ __forceinline__ void quantise_chunks(const E *X, int T, int d, int chunks, uint8_t *codes,
+                                                uint8_t *scale, int64_t w, int64_t stride) {
   const int lane = threadIdx.x & 63;
-  if (w >= int64_t(T) * chunks) return;
-  const int64_t t = w / chunks;
-  const int col = int(w % chunks) * 512 + lane * 8;
+  const int64_t total = int64_t(T) * chunks;
   const int64_t ld = q_row_bytes(d), ls = q_scale_bytes(d);
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (col < d) Elem<E>::load8(X + t * d + col, v);
-  const uint32_t byte = q_scale_byte(max16(abs_max8(v)));
-  if (col < ld) *reinterpret_cast<uint2 *>(codes + t * ld + col) = q_encode8(v, byte);
-  const int blk = col / kQBlock;
-  if ((lane & 15) != 0) return;
-  if constexpr (kTiled) {
-    if (col < ld) scale[q_tile_scale_at(T, t, blk)] = uint8_t(byte);
-  } else {
-    if (blk < ls) scale[t * ls + blk] = col < ld ? uint8_t(byte) : uint8_t(0);
+  float v[NC][8];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int64_t wc = w + c * stride, t = wc / chunks;
+    const int col = int(wc % chunks) * 512 + lane * 8;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[c][e] = 0.f;
+    if (wc < total && col < d) Elem<E>::load8(X + t * d + col, v[c]);
+  }
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int64_t wc = w + c * stride, t = wc / chunks;
+    if (wc >= total) return;
+    const int col = int(wc % chunks) * 512 + lane * 8;
+    const uint32_t byte = q_scale_byte(max16(abs_max8(v[c])));
+    if (col < ld) *reinterpret_cast<uint2 *>(codes + t * ld + col) = q_encode8(v[c], byte);
+    const int blk = col / kQBlock;
+    if ((lane & 15) != 0) continue;
+    if constexpr (kTiled) {
+      if (col < ld) scale[q_tile_scale_at(T, t, blk)] = uint8_t(byte);
+    } else {
+      if (blk < ls) scale[t * ls + blk] = col < ld ? uint8_t(byte) : uint8_t(0);
+    }
   }
 }
 
 template <typename E, bool kTiled>
 __global__ __launch_bounds__(256) void quantise_rows_kernel(const E *X, int T, int d, int chunks,
                                                             uint8_t *codes, uint8_t *scale) {
-  quantise_chunk<E, kTiled>(X, T, d, chunks, codes, scale, int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6));
+  quantise_chunks<E, kTiled, 1>(X, T, d, chunks, codes, scale, int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6), 0);
 }
 
 // The rows quantised while the launch's first workgroup builds the batch's
-// plan (neither needs the other).
+// plan (neither needs the other).  The others keep two to a CU (the plan's LDS)
+// and walk the chunks, four loads of each wave in flight.
 template <bool kLds>
 __global__ __launch_bounds__(kPlanThreads) void quantise_plan_kernel(const uint16_t *X, int T, int d,
                                                                      int chunks, uint8_t *codes,
@@ -49,8 +62,10 @@ __global__ __launch_bounds__(kPlanThreads) void quantise_plan_kernel(const uint1
     plan_build<kLds>(pa, qp_dyn);
     return;
   }
-  quantise_chunk<uint16_t, true>(X, T, d, chunks, codes, scale,
-                                 int64_t(blockIdx.x - 1) * (kPlanThreads / 64) + (threadIdx.x >> 6));
+  constexpr int W = kPlanThreads / 64, NC = 4;
+  const int64_t waves = int64_t(gridDim.x - 1) * W, total = int64_t(T) * chunks;
+  for (int64_t w = int64_t(blockIdx.x - 1) * W + (threadIdx.x >> 6); w < total; w += NC * waves)
+    quantise_chunks<uint16_t, true, NC>(X, T, d, chunks, codes, scale, w, waves);
 }
 
 // 4 x 4 bytes turned: o[j] = byte j of each of d[0..3].
@@ -166,7 +181,8 @@ hipError_t launch_quantise_plan(const void *X, int T, int d, uint8_t *codes, uin
                                 const PlanLaunch &pl, hipStream_t s) {
   const int chunks = int((q_scale_bytes(d) + 3) / 4);
   constexpr int W = kPlanThreads / 64;
-  const dim3 grid(unsigned(1 + (int64_t(T) * chunks + W - 1) / W)), block(kPlanThreads);
+  const int64_t wgs = (int64_t(T) * chunks + W - 1) / W;
+  const dim3 grid(unsigned(1 + (wgs < 510 ? wgs : 510))), block(kPlanThreads);
   const uint16_t *x = static_cast<const uint16_t *>(X);
   if (pl.lds_bytes > kQPlanRowsLds) return hipErrorInvalidConfiguration;
   if (pl.lds)
