@@ -473,8 +473,12 @@ GemmConfig choose_quantised_gemm(int T, int d_in, int d_out, int dtype) {
     // two workgroups per CU
     c.kind = 4; c.bn = 128;
     c.bm = T <= 32 ? 32 : (T <= 64 ? 64 : 128);
-    const int64_t tiles = int64_t((T + c.bm - 1) / c.bm) * ((d_out + 127) / 128);
     const int chunks = (kb + 3) / 4;
+    // fp32 layers: fewer rows per workgroup while that leaves CUs without one
+    // (333 x 576 -> 1344 has 66 of 128 rows and 242 of 32)
+    if (dtype == LORA_F32)
+      while (c.bm > 32 && int64_t((T + c.bm - 1) / c.bm) * ((d_out + 127) / 128) * chunks < 256) c.bm /= 2;
+    const int64_t tiles = int64_t((T + c.bm - 1) / c.bm) * ((d_out + 127) / 128);
     const int64_t want = (512 + tiles - 1) / tiles;
     const int splits = int(want < chunks ? want : chunks);
     const int per = (chunks + splits - 1) / splits;
