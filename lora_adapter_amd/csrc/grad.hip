@@ -184,7 +184,10 @@ __global__ __launch_bounds__(kGradThreads) void seg_outer_partial_kernel(SegOute
 // (256 columns, chunk of 256 pairs, 16 rank rows); per step of 32 pairs the
 // gathered token rows (keep mask applied: exact zeros) are staged in LDS, the
 // next step's rows in flight meanwhile.  The fp32 coefficients are split
-// exactly into bf16 high and low parts (two MFMAs), which keeps ~16 bits.
+// exactly into three bf16 parts (three MFMAs), which keeps all their 24 bits:
+// with two the pages were off by 2.5e-6 of their norm at 8192 pairs, more than
+// the fp32 sums themselves (3e-7), and the third costs no time (the kernel is
+// bound by the rows it streams).
 // Workgroup barrier for LDS only: the next step's token-row loads and the
 // partial stores stay in flight across it (__syncthreads() would wait for
 // every outstanding load and store).
@@ -239,14 +242,15 @@ void seg_outer_mfma_kernel(SegOuterArgs a) {
   constexpr int ZP = kOuterCols + 8;
   __shared__ int s_row[kGradPairChunk];
   __shared__ int s_ad[kGradPairChunk];
-  __shared__ int s_rk[kGradPairChunk];
-  // the coefficients split once into bf16 high and low parts, rank row
+  __shared__ uint16_t s_rk[kGradPairChunk];   // 16 bits: three workgroups' LDS fit a CU
+  // the coefficients split once into three bf16 parts, rank row
   // major, so that a lane's A operand (8 consecutive pairs of one rank row)
   // is one 16-byte read; the row pitch puts the 16 rank rows of a read on
   // distinct banks
   constexpr int AP = kGradPairChunk + 8;
   __shared__ __attribute__((aligned(16))) uint16_t s_ah[RB][AP];
   __shared__ __attribute__((aligned(16))) uint16_t s_al[RB][AP];
+  __shared__ __attribute__((aligned(16))) uint16_t s_ar[RB][AP];
   __shared__ __attribute__((aligned(16))) uint16_t s_z[kOuterK][ZP];
   __shared__ uint64_t s_start[4];          // segment starts of the chunk, one bit per pair
   __shared__ int s_cnt[4];
@@ -402,12 +406,15 @@ void seg_outer_mfma_kernel(SegOuterArgs a) {
 #pragma unroll
     for (int jj = 0; jj < RB; ++jj)
       if (valid && jj < nr) cf[jj] = c[jj];
-    s_rk[tid] = rk;
+    s_rk[tid] = uint16_t(min(max(rk, 0), 0xffff));
 #pragma unroll
     for (int jj = 0; jj < RB; ++jj) {
       const uint16_t h = f2bf(cf[jj]);
       s_ah[jj][tid] = h;
-      s_al[jj][tid] = f2bf(cf[jj] - bf2f(h));
+      const float rest = cf[jj] - bf2f(h);
+      const uint16_t l = f2bf(rest);
+      s_al[jj][tid] = l;
+      s_ar[jj][tid] = f2bf(rest - bf2f(l));
     }
   }
   int s = seg_of_wg(a.plan.seg_off, S, pbeg, s_cnt);
@@ -415,7 +422,7 @@ void seg_outer_mfma_kernel(SegOuterArgs a) {
     g_rows(nr0);
     g_put();
   }
-  lds_bar();                                             // s_rk, s_ah, s_al, s_gb
+  lds_bar();                                             // s_rk, s_ah, s_al, s_ar, s_gb
 
   for (int l_beg = 0; l_beg < n; ++s) {
     const int l_end = l_beg == 0 ? l_end0 : next_start(s_start, l_beg, n);
@@ -461,9 +468,10 @@ void seg_outer_mfma_kernel(SegOuterArgs a) {
         // (a step wholly past the chunk's end reads the last step's)
         const int kk = (lane >> 4) * 8;
         const int ka = min(k0, kGradPairChunk - kOuterK) + kk;
-        bf16x8_t ahi, alo;
+        bf16x8_t ahi, alo, arest;
         __builtin_memcpy(&ahi, &s_ah[lane & 15][ka], 16);
         __builtin_memcpy(&alo, &s_al[lane & 15][ka], 16);
+        __builtin_memcpy(&arest, &s_ar[lane & 15][ka], 16);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           // B operand: column wave*64 + 16b + lane % 16, the same 8 pairs,
@@ -481,6 +489,7 @@ void seg_outer_mfma_kernel(SegOuterArgs a) {
           __builtin_memcpy(reinterpret_cast<char *>(&bfrag) + 8, &hi, 8);
           acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ahi, bfrag, acc[b], 0, 0, 0);
           acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(alo, bfrag, acc[b], 0, 0, 0);
+          acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(arest, bfrag, acc[b], 0, 0, 0);
         }
         if constexpr (kG) {
           if (wave < 2) {
