@@ -623,7 +623,8 @@ int32_t lora_orthogonalise(const lora_pool_desc *pool, const int32_t *adapters, 
  *   w <- w . (1 - lr . decay) - lr . orthogonalised N
  * with w the float32 master row when master is given (the page then takes w
  * rounded once to the pool's dtype), else the page itself.  Each buffer has
- * the pages' layout; none of one factor's may overlap another. */
+ * the pages' layout; none of one factor's may overlap another, but that
+ * float32 pages may be given as their own master (as if NULL). */
 typedef struct {
   void *pages;                /* [n_pages][d] pool dtype, updated                 */
   float *master;              /* [n_pages][d], updated, or NULL                   */

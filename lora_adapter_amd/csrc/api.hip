@@ -955,13 +955,15 @@ int32_t orth_args(const lora_pool_desc *pool, const int32_t *adapters, int32_t M
   return LORA_OK;
 }
 
-int32_t orth_factor(const lora_factor_update *u, int32_t d, OrthFactor &f) {
+int32_t orth_factor(const lora_factor_update *u, int32_t d, int32_t dtype, OrthFactor &f) {
   if (!u || !u->pages || !u->momentum || !u->grad) return LORA_ERR_INVALID_ARG;
-  const void *b[4] = {u->pages, u->momentum, u->grad, u->master};
+  // float32 pages may be named as their own master
+  float *const master = dtype == LORA_F32 && u->master == u->pages ? nullptr : u->master;
+  const void *b[4] = {u->pages, u->momentum, u->grad, master};
   for (int i = 0; i < 4; ++i)
     for (int j = 0; j < i; ++j)
       if (b[i] && b[i] == b[j]) return LORA_ERR_INVALID_ARG;
-  f.src = u->grad; f.momentum = u->momentum; f.master = u->master; f.pages = u->pages;
+  f.src = u->grad; f.momentum = u->momentum; f.master = master; f.pages = u->pages;
   f.d = d; f.lr = u->lr; f.keep = 1.0f - u->lr * u->decay;
   return LORA_OK;
 }
@@ -1008,10 +1010,10 @@ int32_t lora_orthogonal_step(const lora_pool_desc *pool, const int32_t *adapters
   if (st != LORA_OK) return st;
   if (!dims_ok(pool->d_in) || !dims_ok(pool->d_out)) return LORA_ERR_UNSUPPORTED;
   if (M == 0) return LORA_OK;
-  if ((st = orth_factor(a_update, pool->d_in, a.f[0])) != LORA_OK) return st;
-  if ((st = orth_factor(b_update, pool->d_out, a.f[1])) != LORA_OK) return st;
-  if (a_update->pages == b_update->pages || a_update->momentum == b_update->momentum ||
-      (a_update->master && a_update->master == b_update->master) || !ws)
+  if ((st = orth_factor(a_update, pool->d_in, pool->dtype, a.f[0])) != LORA_OK) return st;
+  if ((st = orth_factor(b_update, pool->d_out, pool->dtype, a.f[1])) != LORA_OK) return st;
+  if (a.f[0].pages == a.f[1].pages || a.f[0].momentum == a.f[1].momentum ||
+      (a.f[0].master && a.f[0].master == a.f[1].master) || !ws)
     return LORA_ERR_INVALID_ARG;
   if (ws_bytes < lora_orthogonal_step_workspace_bytes(M, max_rank, pool->d_in, pool->d_out))
     return LORA_ERR_CAPACITY;

@@ -221,6 +221,18 @@ def test_step(ranks, d_in, d_out, nesterov, dtype, with_master):
             assert np.array_equal(w1[~done], w0[~done])
 
 
+def test_fp32_pages_as_their_own_master():
+    got = []
+    for own in (False, True):
+        fl = Fleet([9, 70], 128, 192, "f32", seed=6)
+        dev = lambda a: torch.from_numpy(a).cuda()
+        grad, mom = [dev(fl.values(d)) for d in fl.d], [dev(fl.values(d)) for d in fl.d]
+        keep = step_once(fl, [0, 1], 70, mom, grad, fl.pages if own else [None, None], (0.1, 0.2), 0.3, True)
+        torch.cuda.synchronize()
+        got.append([*fl.pages, *mom])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 def test_step_repeats_on_a_stream_and_in_a_graph():
     def state():
         fl = Fleet([16, 9, 70], 192, 320, "bf16", seed=5)

@@ -73,6 +73,8 @@ def test_refusals_before_any_hip_call(B):
     assert call(a=r(F(16, 32, 48, None, 0.1, 0))) == INV
     assert call(a=r(F(16, 32, 48, 48, 0.1, 0))) == INV                      # gradient is the momentum
     assert call(b=r(F(16, 96, 112, 128, 0.1, 0))) == INV                    # the other factor's pages
+    assert call(a=r(F(16, 16, 48, 64, 0.1, 0))) == INV                      # bf16 pages as their own master
+    assert call(pool=r(_pool(B, dtype=B.LORA_F32)), a=r(F(16, 16, 48, 64, 0.1, 0)), n=64) == CAP   # fp32: allowed
     assert call(pool=r(_pool(B, d_in=100))) == UNS
     assert call(n=64) == CAP and call(ws=None) == INV
     assert call(M=0, a=None, b=None, ws=None) == 0
