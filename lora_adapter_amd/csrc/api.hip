@@ -708,9 +708,11 @@ struct QuantTail {
   size_t partial, codes, scales, total;     // bytes
 };
 
-QuantTail quant_tail(int32_t T, int32_t d_k, int32_t d_n, int32_t dtype) {
+bool few_adapters(int32_t K, const lora_pool_desc *pool) { return K == 1 && pool->n_adapters <= 16; }
+
+QuantTail quant_tail(int32_t T, bool few, int32_t d_k, int32_t d_n, int32_t dtype) {
   QuantTail t{};
-  t.cfg = choose_quantised_gemm(T > 0 ? T : 1, d_k, d_n, dtype);
+  t.cfg = choose_quantised_gemm(T > 0 ? T : 1, few, d_k, d_n, dtype);
   t.partial = align_up(gemm_partial_bytes(t.cfg, T, d_n));
   if (t.cfg.kind != 4) {
     t.codes = align_up(size_t(T) * size_t(q_row_bytes(d_k)));
@@ -718,6 +720,13 @@ QuantTail quant_tail(int32_t T, int32_t d_k, int32_t d_n, int32_t dtype) {
   }
   t.total = t.partial + t.codes + t.scales;
   return t;
+}
+
+// The larger tail of the two forms: the size queries do not know the pool.
+size_t quant_tail_bytes(int32_t T, int32_t d_k, int32_t d_n, int32_t dtype) {
+  const size_t a = quant_tail(T, true, d_k, d_n, dtype).total;
+  const size_t b = quant_tail(T, false, d_k, d_n, dtype).total;
+  return a > b ? a : b;
 }
 
 // Fills q for rows [T][d_k] times the weight's codes [d_n][..]; `tail` the
@@ -770,7 +779,7 @@ int32_t quant_apply_args(const void *X, const lora_quantised_weight *W, void *Y,
   if (!plan) return LORA_ERR_INVALID_ARG;
   if (T == 0) return LORA_OK;
   if (!X || !Y || !W->q_t || !W->scale || !gates || !ws || Y == X) return LORA_ERR_INVALID_ARG;
-  a.t = quant_tail(T, pool->d_in, pool->d_out, pool->dtype);
+  a.t = quant_tail(T, few_adapters(K, pool), pool->d_in, pool->d_out, pool->dtype);
   if (ws_bytes < a.t.total) return LORA_ERR_CAPACITY;
   const size_t head = a.head = (ws_bytes - a.t.total) / kAlign * kAlign;
   GemmConfig base;
@@ -820,7 +829,7 @@ int32_t lora_quantise_weight(const void *W_t, int32_t dtype, const lora_quantise
 size_t lora_apply_quantised_workspace_bytes(int32_t T, int32_t K, int32_t d_in, int32_t d_out,
                                             int32_t max_rank, int32_t dtype) {
   const size_t head = lora_apply_workspace_bytes(T, K, d_in, d_out, max_rank, dtype);
-  return head ? align_up(head) + quant_tail(T, d_in, d_out, dtype).total : 0;
+  return head ? align_up(head) + quant_tail_bytes(T, d_in, d_out, dtype) : 0;
 }
 
 int32_t lora_apply_quantised(const void *X, const lora_quantised_weight *W, void *Y, int32_t T,
@@ -890,7 +899,7 @@ int32_t lora_forward_quantised(const int32_t *ids, const float *gates, int32_t T
 size_t lora_grad_x_quantised_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out, int32_t dtype) {
   if (T < 0 || T > kMaxPairs || !dims_ok(d_in) || !dims_ok(d_out)) return 0;
   if (dtype != LORA_F32 && dtype != LORA_BF16) return 0;
-  const size_t n = quant_tail(T, d_out, d_in, dtype).total;
+  const size_t n = quant_tail_bytes(T, d_out, d_in, dtype);
   return n > 0 ? n : kAlign;
 }
 
@@ -909,7 +918,7 @@ int32_t lora_grad_x_quantised(const void *dY, const lora_quantised_weight *W,
   if (grad_ws_bytes < lora_grad_workspace_bytes(T, K, pool->n_adapters, pool->d_in, pool->d_out,
                                                 max_rank, pool->dtype))
     return LORA_ERR_CAPACITY;
-  const QuantTail t = quant_tail(T, pool->d_out, pool->d_in, pool->dtype);
+  const QuantTail t = quant_tail(T, few_adapters(K, pool), pool->d_out, pool->d_in, pool->dtype);
   if (ws_bytes < t.total) return LORA_ERR_CAPACITY;
   const int64_t TK = int64_t(T) * K;
   const PlanView pv = plan_view(plan, TK, pool->n_adapters);

@@ -233,6 +233,141 @@ __device__ __forceinline__ void lds_dma4(const void *gptr, uint32_t lds) {
                : "memory", "m0");
 }
 
+// The expand of the 32-row blocks that the fused epilogue leaves (ranks over
+// 16, or several slots per token): MFMA passes of 16 rank rows, one slot and
+// one adapter at a time, into accumulators of their own, then added to the
+// staged base product (times the keep mask with kMask), rounded and stored.
+// One rolled loop over the blocks, apart from the fused epilogue: inside its
+// unrolled blocks the same code slowed the common ones (8192 x 4096 -> 11008,
+// rank 16: 357 -> 449 us).
+template <int BM, int BN, int WM, int WN, bool kMask>
+__device__ __forceinline__ void q_expand_wide(const GemmArgs &g,
+                                              f32x16_t (&acc)[TileCfg<BM, BN, WM, WN>::TM]
+                                                             [TileCfg<BM, BN, WM, WN>::TN],
+                                              char *lds0, char *lds1, int m0, int n0, unsigned blocks) {
+  using C = TileCfg<BM, BN, WM, WN>;
+  constexpr int TM = C::TM, TN = C::TN, WC = TN * 32, SC = WC + 4, LPR = WC / 8, RPS = 64 / LPR;
+  static_assert((C::NW / 2) * 40 * SC * 4 <= C::STAGE && RPS <= 8, "staging must fit in LDS");
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / WN, wn = wave % WN, frow = lane & 31, half = lane >> 5;
+  const uint16_t *Bp = static_cast<const uint16_t *>(g.ex.b_pages);
+  char *const mem = wave < C::NW / 2 ? lds0 : lds1;
+  float *stage = reinterpret_cast<float *>(mem) + (wave % (C::NW / 2)) * 32 * SC;
+  float *lstage = reinterpret_cast<float *>(mem) + (C::NW / 2) * 32 * SC + (wave % (C::NW / 2)) * 8 * SC;
+  uint16_t *Y = static_cast<uint16_t *>(g.Y);
+  const int cbase = n0 + wn * WC, vr = lane / LPR, vc = (lane % LPR) * 8;
+  const bool c8 = cbase + vc + 8 <= g.N;
+  int key_ps = -1, key_j = -1;               // adapter slice held in bfr
+  bf16x8_t bfr[TN] = {};
+  auto put = [&](const f32x16_t (&a)[TN]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) stage[((v >> 2) * 8 + half * 4 + (v & 3)) * SC + j * 32 + frow] = a[j][v];
+  };
+#pragma unroll 1
+  for (int i = 0; i < TM; ++i) {
+    if (!((blocks >> i) & 1u)) continue;
+    // (acc is addressed by constants only)
+#pragma unroll
+    for (int b = 0; b < TM; ++b)
+      if (b == i) put(acc[b]);
+    f32x16_t l[TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) l[j] = f32x16_t{};
+    const int rbase = m0 + wm * TM * 32 + i * 32;
+#pragma unroll 1
+    for (int k = 0; k < g.ex.K; ++k) {
+      int4 sd = g.ex.slot_desc[int64_t(min(rbase + frow, g.M - 1)) * g.ex.K + k];
+      if (rbase + frow >= g.M) sd.x = -1;
+      unsigned long long pending = __ballot(sd.x >= 0) & 0xffffffffull;
+      while (pending) {
+        const int leader = __ffsll(pending) - 1;
+        const int kps = __builtin_amdgcn_readfirstlane(__shfl(sd.w, leader, 64));
+        const int kr = __builtin_amdgcn_readfirstlane(__shfl(sd.y, leader, 64));
+        const bool mine = sd.x >= 0 && sd.w == kps && sd.y == kr;
+        pending &= ~__ballot(mine);
+#pragma unroll 1
+        for (int jb = 0; jb < kr; jb += 16) {
+          const int rc = min(16, kr - jb);
+          // A operand: U of row frow (zero unless the row is on this
+          // adapter), rank rows jb + 8*half .. +7, as bf16 hi + lo
+          float u[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int ja = half * 8 + e;
+            u[e] = mine ? g.ex.U[sd.z + jb + min(ja, rc - 1)] : 0.f;
+            if (ja >= rc) u[e] = 0.f;
+          }
+          if (kps != key_ps || jb != key_j) {
+            // B operand: lane (column frow of block j, rank rows jb + 8*half .. +7)
+            const int pidl = g.ex.page_ids[kps + jb + min(lane, rc - 1)];
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+              const int cj = min(cbase + j * 32 + frow, g.N - 1);
+              uint32_t w4[4];
+#pragma unroll
+              for (int e = 0; e < 8; e += 2) {
+                const int ja = half * 8 + e;
+                uint32_t lo = Bp[int64_t(__shfl(pidl, ja, 64)) * g.ex.d_out + cj];
+                uint32_t hi = Bp[int64_t(__shfl(pidl, ja + 1, 64)) * g.ex.d_out + cj];
+                if (ja >= rc) lo = 0;
+                if (ja + 1 >= rc) hi = 0;
+                w4[e >> 1] = lo | (hi << 16);
+              }
+              const uint4 packed = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+              __builtin_memcpy(&bfr[j], &packed, 16);
+            }
+            key_ps = kps;
+            key_j = jb;
+          }
+          uint32_t hw[4], lw[4];
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const uint32_t h2 = f2bf2(u[e], u[e + 1]);
+            hw[e >> 1] = h2;
+            lw[e >> 1] = f2bf2(u[e] - bf_lo(h2), u[e + 1] - bf_hi(h2));
+          }
+          bf16x8_t ahi, alo;
+          const uint4 ph = make_uint4(hw[0], hw[1], hw[2], hw[3]), pl = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+          __builtin_memcpy(&ahi, &ph, 16);
+          __builtin_memcpy(&alo, &pl, 16);
+#pragma unroll
+          for (int j = 0; j < TN; ++j) {
+            l[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ahi, bfr[j], l[j], 0, 0, 0);
+            l[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(alo, bfr[j], l[j], 0, 0, 0);
+          }
+        }
+      }
+    }
+    // quarter qr: MFMA registers v = 4qr .. 4qr+3 hold rows 8qr .. 8qr+7
+#pragma unroll
+    for (int qr = 0; qr < 4; ++qr) {
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int v = 4 * qr; v < 4 * qr + 4; ++v)
+          lstage[(half * 4 + (v & 3)) * SC + j * 32 + frow] = l[j][v];
+#pragma unroll
+      for (int q = 0; q < 8 / RPS; ++q) {
+        const int lr = q * RPS + vr, rr = qr * 8 + lr, row = rbase + rr;
+        if (row >= g.M || !c8) continue;
+        float b8[8], l8[8], v8[8];
+        Elem<float>::load8(stage + rr * SC + vc, b8);
+        Elem<float>::load8(lstage + lr * SC + vc, l8);
+        uint2 mw = make_uint2(0x01010101u, 0x01010101u);
+        if constexpr (kMask) mw = *reinterpret_cast<const uint2 *>(g.mask + int64_t(row) * g.N + cbase + vc);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint32_t word = c < 4 ? mw.x : mw.y;
+          v8[c] = kMask ? b8[c] + float((word >> (8 * (c & 3))) & 0xffu) * l8[c] : b8[c] + l8[c];
+        }
+        store8_nt(Y + int64_t(row) * g.N + cbase + vc, v8);
+      }
+    }
+  }
+}
+
 template <int BM, int BN, int WM, int WN, int NS, bool kFused, bool kMask = false>
 __device__ __forceinline__ void q_tile_run(const QGemmArgs &q, char *smem, int m0, int n0, int kt0,
                                            int nk, int slot) {
@@ -286,9 +421,7 @@ __device__ __forceinline__ void q_tile_run(const QGemmArgs &q, char *smem, int m
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+    for (int j = 0; j < TN; ++j) acc[i][j] = f32x16_t{};
 
   i32x8_t fa[TM], fb0[TN], fb1[TN];
   auto frag = [&](const char *base, int s, int row) __attribute__((always_inline)) {
@@ -380,7 +513,9 @@ __device__ __forceinline__ void q_tile_run(const QGemmArgs &q, char *smem, int m
         }
       }
   } else {
-    fused_epilogue<BM, BN, WM, WN, kMask>(g, acc, smem, smem + C::STAGE, m0, n0, pre);
+    const unsigned wide =
+        fused_epilogue<BM, BN, WM, WN, kMask, true>(g, acc, smem, smem + C::STAGE, m0, n0, pre);
+    if (wide) q_expand_wide<BM, BN, WM, WN, kMask>(g, acc, smem, smem + C::STAGE, m0, n0, wide);
   }
 }
 
@@ -464,7 +599,7 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void q_tile_kernel(QGemmArgs q) {
 
 }  // namespace
 
-GemmConfig choose_quantised_gemm(int T, int d_in, int d_out, int dtype) {
+GemmConfig choose_quantised_gemm(int T, bool few, int d_in, int d_out, int dtype) {
   GemmConfig c{};
   const int kb = int(q_row_bytes(d_in)) / kQBlock;
   if (dtype == LORA_F32 || T <= 128) {
@@ -486,8 +621,15 @@ GemmConfig choose_quantised_gemm(int T, int d_in, int d_out, int dtype) {
     c.splits = (chunks + per - 1) / per;
     return c;
   }
+  // 256 x 256 tiles with the epilogue inside where they fill the GPU, and from
+  // 24 tiles on for 1024 tokens or more of few adapters (the epilogue takes a
+  // pass per adapter in each 32 rows): a partly filled GPU costs less than fp32
+  // partials written, read and finished in a second launch (1024 x 4096 ->
+  // 11008: 54 us against 70 + 45; 2048 x 4096 -> 4096: 51 against 45 + 34; 1710
+  // x 640 -> 1088, 35 tiles: 19 against 12 + 12), but not with many adapters
+  // side by side (1024 x 4096 -> 4096 over 96 in any order: 133 us)
   const int64_t big = int64_t((T + 255) / 256) * ((d_out + 255) / 256);
-  if (big >= 256) {
+  if (big >= 256 || (few && T >= 1024 && big >= 24)) {
     c.kind = 5; c.bm = 256; c.bn = 256;
     c.splits = 1; c.k_split = kb * kQBlock; c.fused = true;
     return c;

@@ -339,8 +339,10 @@ __device__ __forceinline__ void epi_fetch_pid(const GemmArgs &g, EpiPre<TM> &p) 
 // An MFMA block stages its base product first, accumulates the LoRA term in
 // the same registers, and moves it through a second, 8-row staging region a
 // quarter at a time; the row path keeps the term in registers of its own.
-template <int BM, int BN, int WM, int WN, bool kMask>
-__device__ __forceinline__ void fused_epilogue(const GemmArgs &g,
+// kLeaveRows: blocks for the row path are left to the caller, which gets them
+// as bits (bit i: 32-row block i of the wave); otherwise 0 is returned.
+template <int BM, int BN, int WM, int WN, bool kMask, bool kLeaveRows = false>
+__device__ __forceinline__ unsigned fused_epilogue(const GemmArgs &g,
                                                f32x16_t (&acc)[TileCfg<BM, BN, WM, WN>::TM]
                                                               [TileCfg<BM, BN, WM, WN>::TN],
                                                char *lds0, char *lds1, int m0, int n0,
@@ -428,6 +430,7 @@ __device__ __forceinline__ void fused_epilogue(const GemmArgs &g,
   bf16x8_t bfr[TN] = {};
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
+    if (kLeaveRows && ((rowwise >> i) & 1u)) continue;
     bool lterm = false;                      // kMask: acc[i] holds the LoRA term
     if (mfma_ok && !((rowwise >> i) & 1u)) {
       // one MFMA pass per adapter present in the block (lanes 0-31 = rows)
@@ -438,13 +441,14 @@ __device__ __forceinline__ void fused_epilogue(const GemmArgs &g,
         if (lterm) {
           // the staging region is this wave's own (see below)
 #pragma unroll
-          for (int j = 0; j < TN; ++j)
+          for (int j = 0; j < TN; ++j) {
 #pragma unroll
             for (int v = 0; v < 16; ++v) {
               const int r = (v >> 2) * 8 + half * 4 + (v & 3);
               stage[r * SC + j * 32 + frow] = acc[i][j][v];
-              acc[i][j][v] = 0.f;
             }
+            acc[i][j] = f32x16_t{};
+          }
         }
       }
       while (pending) {
@@ -545,7 +549,7 @@ __device__ __forceinline__ void fused_epilogue(const GemmArgs &g,
           }
         }
       }
-    } else if (!((rowwise >> i) & 1u)) {
+    } else if (kLeaveRows || !((rowwise >> i) & 1u)) {
 #pragma unroll
       for (int rr0 = 0; rr0 < 32; rr0 += RPS) {
         const int rr = rr0 + vr;
@@ -579,6 +583,7 @@ __device__ __forceinline__ void fused_epilogue(const GemmArgs &g,
       }
     }
   }
+  return kLeaveRows ? rowwise : 0u;
 }
 
 // Fragment read slot i of a K step (A blocks 0 .. TM-1 are fragments

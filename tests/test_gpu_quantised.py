@@ -220,10 +220,12 @@ def test_forward_and_backward(T, K, d_in, d_out, dtype, extra):
 
 
 @pytest.mark.parametrize("T,d_in,d_out,runs,K,hi", [(4096, 192, 4096, True, 1, 16), (3900, 320, 4160, False, 1, 16),
-                                                    (4096, 128, 4096, False, 2, 40)])
+                                                    (4096, 128, 4096, False, 2, 40),
+                                                    (1030, 256, 1536, True, 1, 70)])
 def test_fused_tiles(T, d_in, d_out, runs, K, hi):
     """Enough 256 x 256 tiles for the epilogue in the GEMM, forward; the
-    backward of the mirrored layer fills them too."""
+    backward of the mirrored layer fills them too.  Ranks below, at and over
+    the 16 rows of a pass, one slot per token and two."""
     w = workload(T, K, d_in, d_out, N=9, hi=hi, mask=True, runs=runs)
     L = Layer(w)
     L.forward()
