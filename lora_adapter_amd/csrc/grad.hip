@@ -55,17 +55,18 @@ __device__ __forceinline__ int seg_of(const int32_t *seg_off, int S, int p) {
   return lo;
 }
 
-// One workgroup per (column slice of 1024, chunk of 256 pairs, block of 16
+// One workgroup per (column slice of 1024, chunk of 256 pairs, block of RB
 // rank rows, share of the chunk's segments).  The chunk's token rows and
 // coefficients are staged in LDS by one load per thread; each lane then streams
 // its 4 columns of the pairs' token rows, kGradAhead rows in flight, and
-// accumulates 16 x 4 sums.  The nsplit workgroups of a chunk take its segments
+// accumulates RB x 4 sums.  The nsplit workgroups of a chunk take its segments
 // in turn (each segment's sum is one workgroup's, whatever the split): a small
 // batch's few chunks alone would leave the GPU idle (333 tokens, top 2 of 24
-// fp32 adapters, 576 and 1344 columns: 77 us in 3 and 6 workgroups).
-template <typename E, bool kMask>
+// fp32 adapters, 576 and 1344 columns: 77 us in 3 and 6 workgroups).  RB is 16,
+// or 4 where even so the workgroups are few: a sum is the same, its chain of
+// pairs shorter by the rank rows left to others.
+template <typename E, bool kMask, int RB>
 __global__ __launch_bounds__(kGradThreads) void seg_outer_partial_kernel(SegOuterArgs a, int nsplit) {
-  constexpr int RB = kGradRankChunk;
   __shared__ int s_row[kGradPairChunk];
   __shared__ __attribute__((aligned(16))) float s_cf[kGradPairChunk][RB];
   const int P = a.plan.hdr[LORA_PH_PAIRS];
@@ -639,19 +640,29 @@ hipError_t launch_seg_outer(const SegOuterArgs &a, int dtype, int64_t TK, int64_
   if (ns > most) ns = most;
   if (ns < 1) ns = 1;
   const int nsplit = int(ns);
-  const dim3 g1(cols, chunks, rchunks * unsigned(nsplit)), block(kGradThreads);
+  const bool narrow = int64_t(cols) * chunks * rchunks * nsplit < 512;
+  const unsigned rblocks = narrow ? unsigned((a.max_rank + 3) / 4) : rchunks;
+  const dim3 g1(cols, chunks, rblocks * unsigned(nsplit)), block(kGradThreads);
   if (grad_mfma_form(dtype, TK, a.d)) {
     // prefill-size batches: the MFMA form (long segments make it dense)
     const dim3 gm(unsigned(a.d / kOuterCols), chunks, rchunks);
     if (a.mask) hipLaunchKernelGGL((seg_outer_mfma_kernel<true, false>), gm, block, 0, st, a);
     else if (a.gpart) hipLaunchKernelGGL((seg_outer_mfma_kernel<false, true>), gm, block, 0, st, a);
     else hipLaunchKernelGGL((seg_outer_mfma_kernel<false, false>), gm, block, 0, st, a);
-  } else if (dtype == LORA_BF16) {
-    if (a.mask) hipLaunchKernelGGL((seg_outer_partial_kernel<uint16_t, true>), g1, block, 0, st, a, nsplit);
-    else hipLaunchKernelGGL((seg_outer_partial_kernel<uint16_t, false>), g1, block, 0, st, a, nsplit);
   } else {
-    if (a.mask) hipLaunchKernelGGL((seg_outer_partial_kernel<float, true>), g1, block, 0, st, a, nsplit);
-    else hipLaunchKernelGGL((seg_outer_partial_kernel<float, false>), g1, block, 0, st, a, nsplit);
+#define LORA_SOP(E, M) \
+  do { \
+    if (narrow) hipLaunchKernelGGL((seg_outer_partial_kernel<E, M, 4>), g1, block, 0, st, a, nsplit); \
+    else hipLaunchKernelGGL((seg_outer_partial_kernel<E, M, kGradRankChunk>), g1, block, 0, st, a, nsplit); \
+  } while (0)
+    if (dtype == LORA_BF16) {
+      if (a.mask) LORA_SOP(uint16_t, true);
+      else LORA_SOP(uint16_t, false);
+    } else {
+      if (a.mask) LORA_SOP(float, true);
+      else LORA_SOP(float, false);
+    }
+#undef LORA_SOP
   }
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
