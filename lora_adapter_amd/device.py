@@ -122,6 +122,59 @@ class DeviceLayer:
         B.lora_grad_x(self.dY, Wn, self.keep_mask, self.T, self.K, self.pool, self.plan, gws,
                       self.max_rank, dX, xws, stream)
 
+    # -- the 8-bit base ----------------------------------------------------
+    def quantise_weight(self, both: bool = True, stream=None) -> B.QuantisedWeight:
+        """e4m3 codes of W_t (`both`: and of W, for the input gradient)."""
+        W8 = B.QuantisedWeight.empty(self.w.d_out, self.w.d_in, self.device, both)
+        B.lora_quantise_weight(self.W_t, self.dtype, W8, stream)
+        return W8
+
+    def quantised_workspace(self):
+        """The apply workspace of the quantised forward (run_grad takes it as
+        its own when it is put in place of `ws`)."""
+        w = self.w
+        n = B.lora_apply_quantised_workspace_bytes(w.T, w.K, w.d_in, w.d_out, self.max_rank, self.dtype)
+        return torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def run_forward_quantised(self, W8, ws, stream=None, Y=None):
+        B.lora_forward_quantised(self.ids, self.gates, self.T, self.K, self.X, W8,
+                                 self.Y if Y is None else Y, self.keep_mask, self.keep_scale,
+                                 self.pool, self.plan, ws, stream)
+
+    def run_apply_quantised(self, W8, ws, stream=None, Y=None):
+        B.lora_apply_quantised(self.X, W8, self.Y if Y is None else Y, self.T, self.K, self.gates,
+                               self.keep_mask, self.keep_scale, self.pool, self.plan, ws, stream)
+
+    def grad_x_quantised_buffers(self):
+        w = self.w
+        dX = torch.empty((w.T, w.d_in), dtype=self.Y.dtype, device=self.device)
+        n = B.lora_grad_x_quantised_workspace_bytes(w.T, w.d_in, w.d_out, self.dtype)
+        return dX, torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def run_grad_x_quantised(self, W8, gws, dX, xws, stream=None):
+        B.lora_grad_x_quantised(self.dY, W8, self.keep_mask, self.T, self.K, self.pool, self.plan,
+                                gws, self.max_rank, dX, xws, stream)
+
+    # -- the update of the factors -----------------------------------------
+    def orthogonal_buffers(self, master: bool = True):
+        """Momentum (zero) and, for bf16 pages, float32 master pages of A and
+        of B, and the step's workspace for all adapters."""
+        w = self.w
+        pages = (self.a_pages, self.b_pages)
+        mom = [torch.zeros(p.shape, dtype=torch.float32, device=self.device) for p in pages]
+        own = [p.float() if master and p.dtype != torch.float32 else None for p in pages]
+        n = B.lora_orthogonal_step_workspace_bytes(w.n_adapters, self.max_rank, w.d_in, w.d_out)
+        return mom, own, torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def run_orthogonal_step(self, adapters, grads, mom, master, ws, lr: float, decay: float = 0.0,
+                            momentum: float = 0.95, nesterov: bool = True, steps: int = 5,
+                            coef=B.NS_COEF, eps: float = 1e-7, out_rank=None, stream=None):
+        """One update of A and B of `adapters` (int32 device) from (dA, dB)."""
+        a, b = (B.FactorUpdate(p, g, m, w, lr, decay)
+                for p, g, m, w in zip((self.a_pages, self.b_pages), grads, mom, master))
+        B.lora_orthogonal_step(self.pool, adapters, int(adapters.numel()), self.max_rank, a, b,
+                               momentum, nesterov, steps, coef, eps, ws, out_rank, stream)
+
     # -- reading results ---------------------------------------------------
     def read_plan(self) -> dict:
         P = self.plan.cpu().numpy()

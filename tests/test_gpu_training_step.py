@@ -102,6 +102,42 @@ def test_captured_loop_beside_an_eager_one():
             assert torch.equal(a, b), i
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_layer_methods(dtype):
+    """DeviceLayer's calls give what the binding's give."""
+    w = workload(70, 2, 320, 192, dtype, N=4, hi=20, mask=True, seed=5)
+    L, R = D.DeviceLayer(w), Layer(w)
+    R.forward()
+    W8, L.ws = L.quantise_weight(), L.quantised_workspace()
+    L.run_forward_quantised(W8, L.ws)
+    assert torch.equal(L.Y, R.Y)
+    Y = torch.empty_like(L.Y)
+    L.run_apply_quantised(L.quantise_weight(both=False), L.quantised_workspace(), Y=Y)
+    assert torch.equal(Y, R.Y)
+    dA, dB, dX = R.backward()
+    ga, gb, gws = L.grad_buffers()
+    L.run_grad(ga, gb, gws)
+    gx, xws = L.grad_x_quantised_buffers()
+    L.run_grad_x_quantised(W8, gws, gx, xws)
+    for a, b in ((ga, dA), (gb, dB), (gx, dX)):
+        assert torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0))
+    ads = torch.arange(4, dtype=torch.int32, device="cuda")
+    grads = [ga.nan_to_num(0.0), gb.nan_to_num(0.0)]
+    for master in (True, False):
+        mom, own, ws = L.orthogonal_buffers(master)
+        assert all((o is not None) == (master and dtype == "bf16") for o in own)
+        want = [p.clone() for p in (L.a_pages, L.b_pages)]
+        wm, wo = [m.clone() for m in mom], [None if o is None else o.clone() for o in own]
+        rank = torch.zeros(4, dtype=torch.int32, device="cuda")
+        L.run_orthogonal_step(ads, grads, mom, own, ws, lr=0.05, decay=0.1, out_rank=rank)
+        f = [B.FactorUpdate(p, g, m, o, 0.05, 0.1) for p, g, m, o in zip(want, grads, wm, wo)]
+        B.lora_orthogonal_step(L.pool, ads, 4, L.max_rank, f[0], f[1], 0.95, True, 5, B.NS_COEF, 1e-7, ws)
+        torch.cuda.synchronize()
+        assert rank.cpu().numpy().tolist() == w.rank.tolist()
+        for a, b in ((L.a_pages, want[0]), (L.b_pages, want[1]), (mom[0], wm[0]), (mom[1], wm[1])):
+            assert torch.equal(a, b)
+
+
 def test_factor_gradients_against_differences():
     """Y is linear in A and in B: <dY, Y(A + D) - Y(A)> = <dA, D>, up to the
     fp32 sums of the two Y: at most d_in + 8 additions in a row for the base
