@@ -553,7 +553,7 @@ int32_t lora_quantise_weight(const void *W_t, int32_t dtype, const lora_quantise
  *   Y[t][n] = round( sum_i X^[t][i].W^[n][i] + sum_{p of t} sum_j U[u_off[p]+j].B_a[j][n] )
  * and U as in lora_apply, from X itself: the LoRA branch is not quantised.
  * Arguments as for lora_apply, W in place of W_t; the pool's dtype is that of
- * X and Y.  bf16 layers sum on the scaled 8-bit MFMA, whose alignment inside
+ * X and Y, and Y overlaps no input.  bf16 layers sum on the scaled 8-bit MFMA, whose alignment inside
  * one instruction costs up to about 6e-5 of the result's norm; fp32 layers
  * sum the same codes with fp32 accuracy on the bf16 MFMA.
  *   ws >= lora_apply_quantised_workspace_bytes(...); U stays in it where
@@ -606,7 +606,7 @@ int32_t lora_grad_x_quantised(const void *dY, const lora_quantised_weight *W,
  *   max_rank 1..LORA_MAX_RANK sizes the workspace and the launches; steps
  *     1..LORA_MAX_ORTH_STEPS; coef: host float[3]; 1e-20 <= eps <= 1e20; M at
  *     most 16384 (UNSUPPORTED).  Only the pool's page table is read.
- * No page may belong to two of the adapters.  Results are deterministic. */
+ * No page may stand twice in the adapters' page tables.  Results are deterministic. */
 #define LORA_MAX_ORTH_STEPS 32
 /* out rows <- the orthogonalised src rows, float32 pages [n_pages][d] (d a
  * multiple of 64: d_in for A's pages, d_out for B's); other pages are not
@@ -623,8 +623,10 @@ int32_t lora_orthogonalise(const lora_pool_desc *pool, const int32_t *adapters, 
  *   w <- w . (1 - lr . decay) - lr . orthogonalised N
  * with w the float32 master row when master is given (the page then takes w
  * rounded once to the pool's dtype), else the page itself.  Each buffer has
- * the pages' layout; none of one factor's may overlap another, but that
- * float32 pages may be given as their own master (as if NULL). */
+ * the pages' layout; no two of the eight may overlap, but that float32 pages
+ * may be given as their own master (as if NULL) and both gradients may be one
+ * buffer.  Errors: INVALID_ARG (null, the same buffer twice, bad sizes),
+ * UNSUPPORTED (widths not multiples of 64, M), CAPACITY (ws), DEVICE. */
 typedef struct {
   void *pages;                /* [n_pages][d] pool dtype, updated                 */
   float *master;              /* [n_pages][d], updated, or NULL                   */

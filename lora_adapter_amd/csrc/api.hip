@@ -821,7 +821,10 @@ int32_t lora_quantise_weight(const void *W_t, int32_t dtype, const lora_quantise
     return LORA_ERR_INVALID_ARG;
   if (!dims_ok(w->d_in) || !dims_ok(w->d_out) || w->d_in > kQMaxWidth || w->d_out > kQMaxWidth)
     return LORA_ERR_UNSUPPORTED;
-  if (W_t == w->q_t || W_t == w->q || w->q == w->q_t) return LORA_ERR_INVALID_ARG;
+  const void *b[5] = {W_t, w->q_t, w->scale, w->q, w->scale_t};
+  for (int i = 0; i < 5; ++i)
+    for (int j = 0; j < i; ++j)
+      if (b[i] && b[i] == b[j]) return LORA_ERR_INVALID_ARG;
   return dev(launch_quantise_weight(W_t, dtype, w->d_out, w->d_in, w->q_t, w->q, w->scale, w->scale_t,
                                     static_cast<hipStream_t>(stream)));
 }
@@ -1021,9 +1024,15 @@ int32_t lora_orthogonal_step(const lora_pool_desc *pool, const int32_t *adapters
   if (M == 0) return LORA_OK;
   if ((st = orth_factor(a_update, pool->d_in, pool->dtype, a.f[0])) != LORA_OK) return st;
   if ((st = orth_factor(b_update, pool->d_out, pool->dtype, a.f[1])) != LORA_OK) return st;
-  if (a.f[0].pages == a.f[1].pages || a.f[0].momentum == a.f[1].momentum ||
-      (a.f[0].master && a.f[0].master == a.f[1].master) || !ws)
-    return LORA_ERR_INVALID_ARG;
+  // what one factor writes is not the other's (their gradients may be the same)
+  const void *b[2][4];
+  for (int i = 0; i < 2; ++i) {
+    b[i][0] = a.f[i].pages; b[i][1] = a.f[i].momentum; b[i][2] = a.f[i].master; b[i][3] = a.f[i].src;
+  }
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < 4; ++j)
+      if ((i < 3 || j < 3) && b[0][i] && b[0][i] == b[1][j]) return LORA_ERR_INVALID_ARG;
+  if (!ws) return LORA_ERR_INVALID_ARG;
   if (ws_bytes < lora_orthogonal_step_workspace_bytes(M, max_rank, pool->d_in, pool->d_out))
     return LORA_ERR_CAPACITY;
   a.mu = momentum; a.nesterov = nesterov ? 1 : 0;

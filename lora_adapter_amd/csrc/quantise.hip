@@ -47,7 +47,8 @@ __device__ __forceinline__ void quantise_chunks(const E *X, int T, int d, int ch
 template <typename E, bool kTiled>
 __global__ __launch_bounds__(256) void quantise_rows_kernel(const E *X, int T, int d, int chunks,
                                                             uint8_t *codes, uint8_t *scale) {
-  quantise_chunks<E, kTiled, 1>(X, T, d, chunks, codes, scale, int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6), 0);
+  const int64_t wg = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
+  quantise_chunks<E, kTiled, 1>(X, T, d, chunks, codes, scale, wg * 4 + (threadIdx.x >> 6), 0);
 }
 
 // The rows quantised while the launch's first workgroup builds the batch's
@@ -163,7 +164,9 @@ hipError_t launch_quantise_rows(const void *X, int dtype, int T, int d, uint8_t 
                                 uint8_t *scale, bool tiled, hipStream_t s) {
   // whole scale rows: the padding bytes past the last block are written too
   const int chunks = int((q_scale_bytes(d) + 3) / 4);
-  const dim3 grid(unsigned((int64_t(T) * chunks + 3) / 4)), block(256);
+  // (a grid dimension holds less than 2^32 threads)
+  const int64_t wgs = (int64_t(T) * chunks + 3) / 4, gx = wgs < (1 << 20) ? wgs : 1 << 20;
+  const dim3 grid(unsigned(gx), unsigned((wgs + gx - 1) / gx)), block(256);
   const uint16_t *xb = static_cast<const uint16_t *>(X);
   const float *xf = static_cast<const float *>(X);
   if (dtype == LORA_BF16 && tiled)

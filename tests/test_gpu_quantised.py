@@ -343,3 +343,32 @@ def test_canaries_around_every_output():
     assert (wbuf[:pad] == 0x3c).all() and (wbuf[-pad:] == 0x3c).all()
     y, ty, _, _ = expected(w)
     check(L.Y, y, ty, "Y")
+
+
+def test_rows_of_more_than_32_bits():
+    """2^20 rows of 65 chunks: more threads than one grid dimension holds, and
+    byte offsets past 32 bits."""
+    T, d = 1 << 20, 32832
+    if torch.cuda.mem_get_info()[0] < 130 << 30:
+        pytest.skip("needs 130 GB of device memory")
+    X = torch.zeros(T, d, dtype=torch.bfloat16, device="cuda")
+    c = torch.full((T, B.lora_quantised_row_bytes(d)), 0x5a, dtype=torch.uint8, device="cuda")
+    s = torch.full((T, B.lora_quantised_scale_bytes(d)), 0x5a, dtype=torch.uint8, device="cuda")
+    rows = [0, 65535, 65536, T // 2 + 3, T - 2, T - 1]
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    for r in rows:
+        X[r] = torch.randn(d, generator=gen, device="cuda").bfloat16()
+    B.lora_quantise_rows(X, B.LORA_BF16, T, d, c, s)
+    torch.cuda.synchronize()
+    v, sb = Q.quantise_rows(X[rows].double().cpu().numpy())
+    assert np.array_equal(c[rows].view(torch.float8_e4m3fn).float().cpu().numpy(), v)
+    assert np.array_equal(s[rows].cpu().numpy()[:, :sb.shape[1]], sb)
+    rest = torch.ones(T, dtype=torch.bool, device="cuda")
+    rest[rows] = False
+    nb = (d + 127) // 128
+    for i in range(0, T, 1 << 16):
+        k = rest[i:i + (1 << 16)]
+        assert not bool(c[i:i + (1 << 16)][k].any())
+        assert bool((s[i:i + (1 << 16), :nb][k] == 1).all()) and not bool(s[i:i + (1 << 16), nb:].any())
+    del X, c
+    torch.cuda.empty_cache()

@@ -82,3 +82,21 @@ def test_refusals_before_any_hip_call(B):
     assert B.lora_orthogonalise_workspace_bytes(4, 2000, 128) == 0
     assert B.lora_orthogonal_step_workspace_bytes(4, 16, 100, 128) == 0
     assert B.lora_orthogonal_step_workspace_bytes(4, 16, 128, 192) > 0
+
+
+def test_a_buffer_of_both_factors_is_refused(B):
+    r, st = ctypes.byref, B.lib().lora_orthogonal_step
+    names = ("pages", "master", "momentum", "grad")
+    fa, fb = dict(zip(names, (16, 32, 48, 64))), dict(zip(names, (80, 96, 112, 128)))
+    co = (ctypes.c_float * 3)(*COEF)
+
+    def call(a, b):
+        F = lambda u: r(B.FactorUpdateDesc(*(u[n] for n in names), 0.1, 0.0))
+        return st(r(_pool(B)), 8, 2, 4, F(a), F(b), 0.9, 1, 5, co, 1e-7, None, 48, 64, None)
+
+    for x in names:
+        for y in names:
+            # ws of 64 bytes: what is not refused for its buffers is too small
+            want = B.LORA_ERR_CAPACITY if x == y == "grad" else B.LORA_ERR_INVALID_ARG
+            assert call(fa, {**fb, y: fa[x]}) == want, (x, y)
+    assert call({**fa, "master": None}, {**fb, "master": None}) == B.LORA_ERR_CAPACITY

@@ -109,6 +109,17 @@ def test_refusals_before_any_hip_call(B):
     assert n > B.lora_apply_workspace_bytes(300, 1, 512, 640, 16, B.LORA_BF16)
 
 
+def test_a_buffer_twice_is_refused(B):
+    f, r = B.lib().lora_quantise_weight, ctypes.byref
+    one = dict(q_t=16, scale=32, q=48, scale_t=64)
+    for a in one:
+        assert f(one[a], B.LORA_BF16, r(_weight(B, **one)), None) == B.LORA_ERR_INVALID_ARG
+        for b in one:
+            if a != b:
+                w = _weight(B, **{**one, a: one[b]})
+                assert f(8, B.LORA_BF16, r(w), None) == B.LORA_ERR_INVALID_ARG, (a, b)
+
+
 def test_weight_buffers_are_checked(B):
     e = lambda *s: torch.empty(s, dtype=torch.uint8)
     w = B.QuantisedWeight.empty(192, 128, "cpu")
