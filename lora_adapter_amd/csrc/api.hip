@@ -553,13 +553,14 @@ int32_t lora_grad(const void *X, const uint8_t *keep_mask, float keep_scale, con
   ob.coef = aw.U; ob.coef_cap = aw.u_cap; ob.plan = pv;
   ob.rank = pool->rank; ob.page_start = pool->page_start; ob.page_ids = pool->page_ids;
   ob.part = partB; ob.max_rank = max_rank; ob.out_pages = dB_pages; ob.err_word = err_word;
-  e = launch_seg_outer(ob, pool->dtype, TK, pool->n_adapters, s);
-  if (e != hipSuccess) return LORA_ERR_DEVICE;
-
   SegOuterArgs oa = ob;
   oa.Z = X; oa.mask = keep_mask; oa.d = pool->d_in; oa.coef = G; oa.coef_cap = sa.out_cap;
   oa.part = partA;
   oa.out_pages = dA_pages;
+  if (!grad_mfma_form(pool->dtype, TK, pool->d_in))
+    return dev(launch_seg_outer_both(ob, oa, pool->dtype, TK, pool->n_adapters, s));
+  e = launch_seg_outer(ob, pool->dtype, TK, pool->n_adapters, s);
+  if (e != hipSuccess) return LORA_ERR_DEVICE;
   e = launch_seg_outer(oa, pool->dtype, TK, pool->n_adapters, s);
   return dev(e);
 }

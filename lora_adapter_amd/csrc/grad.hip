@@ -65,17 +65,24 @@ __device__ __forceinline__ int seg_of(const int32_t *seg_off, int S, int p) {
 // fp32 adapters, 576 and 1344 columns: 77 us in 3 and 6 workgroups).  RB is 16,
 // or 4 where even so the workgroups are few: a sum is the same, its chain of
 // pairs shorter by the rank rows left to others.
+template <int RB>
+struct OuterLds {
+  int row[kGradPairChunk];
+  __attribute__((aligned(16))) float cf[kGradPairChunk][RB];
+};
+
 template <typename E, bool kMask, int RB>
-__global__ __launch_bounds__(kGradThreads) void seg_outer_partial_kernel(SegOuterArgs a, int nsplit) {
-  __shared__ int s_row[kGradPairChunk];
-  __shared__ __attribute__((aligned(16))) float s_cf[kGradPairChunk][RB];
+__device__ __forceinline__ void seg_outer_partial_wg(const SegOuterArgs &a, int nsplit, int bx,
+                                                     OuterLds<RB> &lds) {
+  int (&s_row)[kGradPairChunk] = lds.row;
+  float (&s_cf)[kGradPairChunk][RB] = lds.cf;
   const int P = a.plan.hdr[LORA_PH_PAIRS];
   const int S = a.plan.hdr[LORA_PH_SEGS];
   const int q = blockIdx.y;
   const int pbeg = q * kGradPairChunk;
   if (pbeg >= P) return;
   if (int64_t(a.plan.hdr[LORA_PH_RPAIRS]) > a.coef_cap) {
-    if (q == 0 && blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0)
+    if (q == 0 && bx == 0 && blockIdx.z == 0 && threadIdx.x == 0)
       atomicOr(a.err_word, LORA_DEVERR_CAPACITY);
     return;
   }
@@ -105,7 +112,7 @@ __global__ __launch_bounds__(kGradThreads) void seg_outer_partial_kernel(SegOute
   }
   __syncthreads();
 
-  const int col_raw = (blockIdx.x * kGradThreads + tid) * kGradCPL;
+  const int col_raw = (bx * kGradThreads + tid) * kGradCPL;
   const bool col_ok = col_raw < a.d;
   const int col = col_ok ? col_raw : a.d - kGradCPL;     // loads stay in bounds
   const E *Z = static_cast<const E *>(a.Z);
@@ -116,7 +123,7 @@ __global__ __launch_bounds__(kGradThreads) void seg_outer_partial_kernel(SegOute
     const int ad = a.plan.seg_adapter[s];
     const int r = a.rank[ad];
     if (r > a.max_rank) {
-      if (tid == 0 && blockIdx.x == 0 && j0 == 0) atomicOr(a.err_word, LORA_DEVERR_CAPACITY);
+      if (tid == 0 && bx == 0 && j0 == 0) atomicOr(a.err_word, LORA_DEVERR_CAPACITY);
     } else if (j0 < r) {
       const int nr = min(RB, r - j0);
       float acc[RB][kGradCPL];
@@ -177,6 +184,23 @@ __global__ __launch_bounds__(kGradThreads) void seg_outer_partial_kernel(SegOute
       }
     }
   }
+}
+
+template <typename E, bool kMask, int RB>
+__global__ __launch_bounds__(kGradThreads) void seg_outer_partial_kernel(SegOuterArgs a, int nsplit) {
+  __shared__ OuterLds<RB> lds;
+  seg_outer_partial_wg<E, kMask, RB>(a, nsplit, blockIdx.x, lds);
+}
+
+// The partials of both factors in one launch: column slices 0 .. bcols - 1 are
+// b's (dB, never masked), the rest a's.  A small batch's two launches of a few
+// workgroups are latency twice (333 tokens as above: 9 + 9 -> 10 us).
+template <typename E, bool kMask, int RB>
+__global__ __launch_bounds__(kGradThreads) void seg_outer_both_kernel(SegOuterArgs b, SegOuterArgs a,
+                                                                      int bcols, int nsplit) {
+  __shared__ OuterLds<RB> lds;
+  if (int(blockIdx.x) < bcols) seg_outer_partial_wg<E, false, RB>(b, nsplit, blockIdx.x, lds);
+  else seg_outer_partial_wg<E, kMask, RB>(a, nsplit, int(blockIdx.x) - bcols, lds);
 }
 
 // The same partials with bf16 MFMA (prefill-size batches): out[j][n] =
@@ -573,6 +597,13 @@ __global__ __launch_bounds__(kGradThreads) void seg_outer_reduce_kernel(SegOuter
   seg_outer_reduce_wg(a, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.y);
 }
 
+// Both factors' sums, column slices as in seg_outer_both_kernel.
+__global__ __launch_bounds__(kGradThreads) void seg_reduce_both_kernel(SegOuterArgs b, SegOuterArgs a,
+                                                                       int bcols) {
+  if (int(blockIdx.x) < bcols) seg_outer_reduce_wg(b, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.y);
+  else seg_outer_reduce_wg(a, int(blockIdx.x) - bcols, blockIdx.y, blockIdx.z, gridDim.y);
+}
+
 // G[u_off[p] + j] = (gate . scale . extra) . sum over tiles of gpart, one
 // thread per (pair, rank row), tiles added in order; workgroup b.
 __device__ __forceinline__ void g_reduce_wg(const GReduceArgs &a, int64_t b) {
@@ -628,21 +659,65 @@ int64_t grad_pieces(int64_t TK, int64_t N) {
   return segs + (TK + kGradPairChunk - 1) / kGradPairChunk + 1;
 }
 
+namespace {
+
+// Segment shares and rank blocks of the vector-ALU form on `cols` column
+// slices: shares towards 1024 workgroups, at most 32 (and the adapters) a chunk.
+struct OuterShape {
+  unsigned chunks, rblocks;
+  int nsplit;
+  bool narrow;
+};
+
+OuterShape outer_shape(int64_t cols, int64_t TK, int64_t N, int max_rank) {
+  OuterShape o{};
+  o.chunks = unsigned((TK + kGradPairChunk - 1) / kGradPairChunk);
+  const int64_t rchunks = (max_rank + kGradRankChunk - 1) / kGradRankChunk;
+  int64_t ns = 1024 / (cols * o.chunks * rchunks);
+  const int64_t most = N < 32 ? N : 32;
+  if (ns > most) ns = most;
+  o.nsplit = int(ns > 1 ? ns : 1);
+  o.narrow = cols * o.chunks * rchunks * o.nsplit < 512;
+  o.rblocks = unsigned(o.narrow ? (max_rank + 3) / 4 : rchunks);
+  return o;
+}
+
+}  // namespace
+
+hipError_t launch_seg_outer_both(const SegOuterArgs &b, const SegOuterArgs &a, int dtype, int64_t TK,
+                                 int64_t N, hipStream_t st) {
+  if (TK == 0) return hipSuccess;
+  const int bcols = (b.d + kGradCols - 1) / kGradCols, cols = bcols + (a.d + kGradCols - 1) / kGradCols;
+  const OuterShape o = outer_shape(cols, TK, N, a.max_rank);
+  const dim3 g1(unsigned(cols), o.chunks, o.rblocks * unsigned(o.nsplit)), block(kGradThreads);
+#define LORA_SOB(E, M) \
+  do { \
+    if (o.narrow) hipLaunchKernelGGL((seg_outer_both_kernel<E, M, 4>), g1, block, 0, st, b, a, bcols, o.nsplit); \
+    else hipLaunchKernelGGL((seg_outer_both_kernel<E, M, kGradRankChunk>), g1, block, 0, st, b, a, bcols, o.nsplit); \
+  } while (0)
+  if (dtype == LORA_BF16) {
+    if (a.mask) LORA_SOB(uint16_t, true);
+    else LORA_SOB(uint16_t, false);
+  } else {
+    if (a.mask) LORA_SOB(float, true);
+    else LORA_SOB(float, false);
+  }
+#undef LORA_SOB
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  const int64_t segs = TK < N ? TK : N;
+  const dim3 g2(unsigned(cols), unsigned(segs < 65535 ? segs : 65535), unsigned(a.max_rank));
+  hipLaunchKernelGGL(seg_reduce_both_kernel, g2, block, 0, st, b, a, bcols);
+  return hipGetLastError();
+}
+
 hipError_t launch_seg_outer(const SegOuterArgs &a, int dtype, int64_t TK, int64_t N, hipStream_t st,
                             const GReduceArgs *g) {
   if (TK == 0) return hipSuccess;
   const unsigned cols = unsigned((a.d + kGradCols - 1) / kGradCols);
   const unsigned chunks = unsigned((TK + kGradPairChunk - 1) / kGradPairChunk);
   const unsigned rchunks = unsigned((a.max_rank + kGradRankChunk - 1) / kGradRankChunk);
-  // segment shares: towards 1024 workgroups, at most 32 (and the adapters) a chunk
-  int64_t ns = 1024 / (int64_t(cols) * chunks * rchunks);
-  const int64_t most = N < 32 ? N : 32;
-  if (ns > most) ns = most;
-  if (ns < 1) ns = 1;
-  const int nsplit = int(ns);
-  const bool narrow = int64_t(cols) * chunks * rchunks * nsplit < 512;
-  const unsigned rblocks = narrow ? unsigned((a.max_rank + 3) / 4) : rchunks;
-  const dim3 g1(cols, chunks, rblocks * unsigned(nsplit)), block(kGradThreads);
+  const dim3 block(kGradThreads);
   if (grad_mfma_form(dtype, TK, a.d)) {
     // prefill-size batches: the MFMA form (long segments make it dense)
     const dim3 gm(unsigned(a.d / kOuterCols), chunks, rchunks);
@@ -650,18 +725,17 @@ hipError_t launch_seg_outer(const SegOuterArgs &a, int dtype, int64_t TK, int64_
     else if (a.gpart) hipLaunchKernelGGL((seg_outer_mfma_kernel<false, true>), gm, block, 0, st, a);
     else hipLaunchKernelGGL((seg_outer_mfma_kernel<false, false>), gm, block, 0, st, a);
   } else {
-#define LORA_SOP(E, M) \
+    // (the other factor's width takes the MFMA form, so dtype is bf16)
+    if (dtype != LORA_BF16) return hipErrorInvalidConfiguration;
+    const OuterShape o = outer_shape(cols, TK, N, a.max_rank);
+    const dim3 g1(cols, chunks, o.rblocks * unsigned(o.nsplit));
+#define LORA_SOP(M) \
   do { \
-    if (narrow) hipLaunchKernelGGL((seg_outer_partial_kernel<E, M, 4>), g1, block, 0, st, a, nsplit); \
-    else hipLaunchKernelGGL((seg_outer_partial_kernel<E, M, kGradRankChunk>), g1, block, 0, st, a, nsplit); \
+    if (o.narrow) hipLaunchKernelGGL((seg_outer_partial_kernel<uint16_t, M, 4>), g1, block, 0, st, a, o.nsplit); \
+    else hipLaunchKernelGGL((seg_outer_partial_kernel<uint16_t, M, kGradRankChunk>), g1, block, 0, st, a, o.nsplit); \
   } while (0)
-    if (dtype == LORA_BF16) {
-      if (a.mask) LORA_SOP(uint16_t, true);
-      else LORA_SOP(uint16_t, false);
-    } else {
-      if (a.mask) LORA_SOP(float, true);
-      else LORA_SOP(float, false);
-    }
+    if (a.mask) LORA_SOP(true);
+    else LORA_SOP(false);
 #undef LORA_SOP
   }
   hipError_t err = hipGetLastError();

@@ -524,5 +524,9 @@ int grad_gpart_tiles(int d_out);
 // reduction launch also forms G from gpart.
 hipError_t launch_seg_outer(const SegOuterArgs &a, int dtype, int64_t TK, int64_t n_adapters,
                             hipStream_t s, const GReduceArgs *g = nullptr);
+// Both factors (b: dB, a: dA) where neither takes the MFMA form: one launch of
+// partials, one of their sums.
+hipError_t launch_seg_outer_both(const SegOuterArgs &b, const SegOuterArgs &a, int dtype, int64_t TK,
+                                 int64_t n_adapters, hipStream_t s);
 
 }  // namespace lora
