@@ -709,9 +709,11 @@ struct QuantTail {
   size_t partial, codes, scales, total;     // bytes
 };
 
-bool few_adapters(int32_t K, const lora_pool_desc *pool) { return K == 1 && pool->n_adapters <= 16; }
+int few_adapters(int32_t K, const lora_pool_desc *pool) {
+  return K == 1 && pool->n_adapters <= 16 ? pool->n_adapters : 0;
+}
 
-QuantTail quant_tail(int32_t T, bool few, int32_t d_k, int32_t d_n, int32_t dtype) {
+QuantTail quant_tail(int32_t T, int few, int32_t d_k, int32_t d_n, int32_t dtype) {
   QuantTail t{};
   t.cfg = choose_quantised_gemm(T > 0 ? T : 1, few, d_k, d_n, dtype);
   t.partial = align_up(gemm_partial_bytes(t.cfg, T, d_n));
@@ -725,8 +727,8 @@ QuantTail quant_tail(int32_t T, bool few, int32_t d_k, int32_t d_n, int32_t dtyp
 
 // The larger tail of the two forms: the size queries do not know the pool.
 size_t quant_tail_bytes(int32_t T, int32_t d_k, int32_t d_n, int32_t dtype) {
-  const size_t a = quant_tail(T, true, d_k, d_n, dtype).total;
-  const size_t b = quant_tail(T, false, d_k, d_n, dtype).total;
+  const size_t a = quant_tail(T, 1, d_k, d_n, dtype).total;
+  const size_t b = quant_tail(T, 0, d_k, d_n, dtype).total;
   return a > b ? a : b;
 }
 

@@ -16,8 +16,8 @@
 // scaled as it is added to the fp32 total.
 //
 // Forms:
-//   * split-K tiles of 128 columns by up to 128 rows (decode, and fp32 layers
-//     of any size): the token rows are quantised by the workgroup that reads
+//   * split-K tiles of 128 columns by up to 128 rows (decode; fp32 layers of
+//     any size by 32): the token rows are quantised by the workgroup that reads
 //     them, straight into LDS, so a decode step has no quantising launch;
 //   * 256 x 256 tiles with the LoRA expand in their epilogue, and 256 x 128
 //     tiles that write fp32 partials: rows quantised ahead by one launch.
@@ -599,20 +599,19 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void q_tile_kernel(QGemmArgs q) {
 
 }  // namespace
 
-GemmConfig choose_quantised_gemm(int T, bool few, int d_in, int d_out, int dtype) {
+GemmConfig choose_quantised_gemm(int T, int few, int d_in, int d_out, int dtype) {
   GemmConfig c{};
   const int kb = int(q_row_bytes(d_in)) / kQBlock;
   if (dtype == LORA_F32 || T <= 128) {
     // decode: W streamed once, 512 of K per workgroup; with more tiles of
     // output (fp32 layers of many rows) a workgroup keeps more of K, down to
     // two workgroups per CU
+    // (fp32: 32 rows always.  Their widened operands make a workgroup of 128
+    // rows four times as long, and two of those are all that a CU holds: 669 x
+    // 2496 -> 1472 63 -> 36 us, 3000 x 4096 -> 4096 733 -> 631 a forward)
     c.kind = 4; c.bn = 128;
-    c.bm = T <= 32 ? 32 : (T <= 64 ? 64 : 128);
+    c.bm = T <= 32 || dtype == LORA_F32 ? 32 : (T <= 64 ? 64 : 128);
     const int chunks = (kb + 3) / 4;
-    // fp32 layers: fewer rows per workgroup while that leaves CUs without one
-    // (333 x 576 -> 1344 has 66 of 128 rows and 242 of 32)
-    if (dtype == LORA_F32)
-      while (c.bm > 32 && int64_t((T + c.bm - 1) / c.bm) * ((d_out + 127) / 128) * chunks < 256) c.bm /= 2;
     const int64_t tiles = int64_t((T + c.bm - 1) / c.bm) * ((d_out + 127) / 128);
     const int64_t want = (512 + tiles - 1) / tiles;
     const int splits = int(want < chunks ? want : chunks);
@@ -621,15 +620,21 @@ GemmConfig choose_quantised_gemm(int T, bool few, int d_in, int d_out, int dtype
     c.splits = (chunks + per - 1) / per;
     return c;
   }
-  // 256 x 256 tiles with the epilogue inside where they fill the GPU, and from
-  // 24 tiles on for 1024 tokens or more of few adapters (the epilogue takes a
-  // pass per adapter in each 32 rows): a partly filled GPU costs less than fp32
-  // partials written, read and finished in a second launch (1024 x 4096 ->
-  // 11008: 54 us against 70 + 45; 2048 x 4096 -> 4096: 51 against 45 + 34; 1710
-  // x 640 -> 1088, 35 tiles: 19 against 12 + 12), but not with many adapters
-  // side by side (1024 x 4096 -> 4096 over 96 in any order: 133 us)
+  // 256 x 256 tiles with the epilogue inside where they fill the GPU, or where
+  // that is quicker for a prefill of few adapters.  With fewer tiles than CUs a
+  // fused tile costs its CU 1.1 us per block of K whatever their number; the
+  // split form spreads K over the GPU (6 ns a tile and block) but writes fp32
+  // partials, reads them and finishes in a second launch (0.23 us a tile and 3
+  // us).  Each adapter costs the fused epilogue a pass over the 32 rows that it
+  // shares with others: nothing in runs of tokens, 3 us each in any order,
+  // taken as 0.5.  Fused against split, whole calls, four adapters in runs: 80
+  // tiles and 7 blocks of K (2048 x 832 -> 2496) 41 against 56 us, 128 and 32
+  // (4096 x 4096 -> 2048) 81 against 105, 153 and 83 (the input gradient of
+  // 4234 x 2304 -> 10560) 90 less; but 24 and 36 (2048 x 4544 -> 640) 78
+  // against 60, 32 and 64 (2048 x 8192 -> 1024) 122 against 81.
   const int64_t big = int64_t((T + 255) / 256) * ((d_out + 255) / 256);
-  if (big >= 256 || (few && T >= 1024 && big >= 24)) {
+  if (big >= 256 ||
+      (few > 0 && T >= 1024 && big * (6 * kb + 230) + 3000 >= 1100 * int64_t(kb) + 500 * few)) {
     c.kind = 5; c.bm = 256; c.bn = 256;
     c.splits = 1; c.k_split = kb * kQBlock; c.fused = true;
     return c;
@@ -658,15 +663,10 @@ hipError_t launch_quantised_gemm(const GemmConfig &c, const QGemmArgs &q, int dt
   const GemmArgs &g = q.g;
   if (c.kind == 4) {
     const dim3 grid((g.N + 127) / 128, (g.M + c.bm - 1) / c.bm, c.splits), block(256);
-#define LORA_QS(E) \
-  do { \
-    if (c.bm == 32) hipLaunchKernelGGL((q_split_kernel<E, 1>), grid, block, 0, s, q); \
-    else if (c.bm == 64) hipLaunchKernelGGL((q_split_kernel<E, 2>), grid, block, 0, s, q); \
-    else hipLaunchKernelGGL((q_split_kernel<E, 4>), grid, block, 0, s, q); \
-  } while (0)
-    if (dtype == LORA_BF16) LORA_QS(uint16_t);
-    else LORA_QS(float);
-#undef LORA_QS
+    if (dtype == LORA_F32) hipLaunchKernelGGL((q_split_kernel<float, 1>), grid, block, 0, s, q);
+    else if (c.bm == 32) hipLaunchKernelGGL((q_split_kernel<uint16_t, 1>), grid, block, 0, s, q);
+    else if (c.bm == 64) hipLaunchKernelGGL((q_split_kernel<uint16_t, 2>), grid, block, 0, s, q);
+    else hipLaunchKernelGGL((q_split_kernel<uint16_t, 4>), grid, block, 0, s, q);
     return hipGetLastError();
   }
   if (dtype != LORA_BF16) return hipErrorInvalidConfiguration;
@@ -715,11 +715,11 @@ hipError_t launch_quantised_gemm_plan(const GemmConfig &c, const QGemmArgs &q, c
 #define LORA_QP2(E, MB, M) do { if (pl.lds) LORA_QP3(E, MB, M, true); else LORA_QP3(E, MB, M, false); } while (0)
 #define LORA_QP(MB) \
   do { \
-    if (dtype == LORA_F32) LORA_QP2(float, MB, false); \
-    else if (sa.mask) LORA_QP2(uint16_t, MB, true); \
+    if (sa.mask) LORA_QP2(uint16_t, MB, true); \
     else LORA_QP2(uint16_t, MB, false); \
   } while (0)
-  if (c.bm == 32) LORA_QP(1);
+  if (dtype == LORA_F32) LORA_QP2(float, 1, false);
+  else if (c.bm == 32) LORA_QP(1);
   else if (c.bm == 64) LORA_QP(2);
   else LORA_QP(4);
 #undef LORA_QP

@@ -31,20 +31,35 @@ constexpr int kGradCols = kGradThreads * kGradCPL;    // columns per workgroup
 constexpr int kGradAhead = 8;                         // token rows per batch (two in flight)
 static_assert(kGradPairChunk == kGradThreads, "one staged pair per thread");
 
-// 4 consecutive elements held raw until used.
-template <typename E> struct Z4;
-template <> struct Z4<uint16_t> {
+// C (2 or 4) consecutive elements, or mask bytes, held raw until used.
+template <typename E, int C> struct ZC;
+template <> struct ZC<uint16_t, 4> {
   uint2 w;
   __device__ __forceinline__ void load(const uint16_t *p) { w = *reinterpret_cast<const uint2 *>(p); }
   __device__ __forceinline__ void get(float v[4]) const {
     v[0] = bf_lo(w.x); v[1] = bf_hi(w.x); v[2] = bf_lo(w.y); v[3] = bf_hi(w.y);
   }
 };
-template <> struct Z4<float> {
+template <> struct ZC<uint16_t, 2> {
+  uint32_t w;
+  __device__ __forceinline__ void load(const uint16_t *p) { w = *reinterpret_cast<const uint32_t *>(p); }
+  __device__ __forceinline__ void get(float v[2]) const { v[0] = bf_lo(w); v[1] = bf_hi(w); }
+};
+template <> struct ZC<float, 4> {
   float4 w;
   __device__ __forceinline__ void load(const float *p) { w = *reinterpret_cast<const float4 *>(p); }
   __device__ __forceinline__ void get(float v[4]) const { v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w; }
 };
+template <> struct ZC<float, 2> {
+  float2 w;
+  __device__ __forceinline__ void load(const float *p) { w = *reinterpret_cast<const float2 *>(p); }
+  __device__ __forceinline__ void get(float v[2]) const { v[0] = w.x; v[1] = w.y; }
+};
+template <int C>
+__device__ __forceinline__ uint32_t mask_bytes(const uint8_t *p) {
+  if constexpr (C == 4) return *reinterpret_cast<const uint32_t *>(p);
+  else return *reinterpret_cast<const uint16_t *>(p);
+}
 
 __device__ __forceinline__ int seg_of(const int32_t *seg_off, int S, int p) {
   int lo = 0, hi = S;
@@ -55,23 +70,27 @@ __device__ __forceinline__ int seg_of(const int32_t *seg_off, int S, int p) {
   return lo;
 }
 
-// One workgroup per (column slice of 1024, chunk of 256 pairs, block of RB
+// One workgroup per (slice of 1024 columns, chunk of 256 pairs, block of RB
 // rank rows, share of the chunk's segments).  The chunk's token rows and
 // coefficients are staged in LDS by one load per thread; each lane then streams
-// its 4 columns of the pairs' token rows, kGradAhead rows in flight, and
-// accumulates RB x 4 sums.  The nsplit workgroups of a chunk take its segments
+// its 4 (or 2) columns of the pairs' token rows, kGradAhead rows in flight, and
+// accumulates RB x 4 (or 2) sums.  The nsplit workgroups of a chunk take its segments
 // in turn (each segment's sum is one workgroup's, whatever the split): a small
 // batch's few chunks alone would leave the GPU idle (333 tokens, top 2 of 24
 // fp32 adapters, 576 and 1344 columns: 77 us in 3 and 6 workgroups).  RB is 16,
-// or 4 where even so the workgroups are few: a sum is the same, its chain of
-// pairs shorter by the rank rows left to others.
+// or 4 where even so the workgroups are under 512, and the slices 512 columns
+// where those of 4 rank rows are under 1024: a sum is the same, its chain of
+// pairs (bound by the instructions of a row) shorter by the rank rows and
+// columns left to others (2319 tokens, 832 and 2496 columns, bf16, rank 8: 36
+// -> 28 us for the 512 columns; 60 fp32 adapters, 669 tokens, 1920 workgroups:
+// 37 -> 41, so not there).
 template <int RB>
 struct OuterLds {
   int row[kGradPairChunk];
   __attribute__((aligned(16))) float cf[kGradPairChunk][RB];
 };
 
-template <typename E, bool kMask, int RB>
+template <typename E, bool kMask, int RB, int CPL>
 __device__ __forceinline__ void seg_outer_partial_wg(const SegOuterArgs &a, int nsplit, int bx,
                                                      OuterLds<RB> &lds) {
   int (&s_row)[kGradPairChunk] = lds.row;
@@ -112,9 +131,9 @@ __device__ __forceinline__ void seg_outer_partial_wg(const SegOuterArgs &a, int 
   }
   __syncthreads();
 
-  const int col_raw = (bx * kGradThreads + tid) * kGradCPL;
+  const int col_raw = (bx * kGradThreads + tid) * CPL;
   const bool col_ok = col_raw < a.d;
-  const int col = col_ok ? col_raw : a.d - kGradCPL;     // loads stay in bounds
+  const int col = col_ok ? col_raw : a.d - CPL;     // loads stay in bounds
   const E *Z = static_cast<const E *>(a.Z);
   for (int s = seg_of(a.plan.seg_off, S, pbeg) + int(blockIdx.z) % nsplit; s < S; s += nsplit) {
     const int p = max(pbeg, a.plan.seg_off[s]);
@@ -126,33 +145,33 @@ __device__ __forceinline__ void seg_outer_partial_wg(const SegOuterArgs &a, int 
       if (tid == 0 && bx == 0 && j0 == 0) atomicOr(a.err_word, LORA_DEVERR_CAPACITY);
     } else if (j0 < r) {
       const int nr = min(RB, r - j0);
-      float acc[RB][kGradCPL];
+      float acc[RB][CPL];
 #pragma unroll
       for (int jj = 0; jj < RB; ++jj)
 #pragma unroll
-        for (int c = 0; c < kGradCPL; ++c) acc[jj][c] = 0.f;
+        for (int c = 0; c < CPL; ++c) acc[jj][c] = 0.f;
       const int l_end = send - pbeg;
       // two batches of kGradAhead token rows, the next one in flight while
       // the current one is added (rows clamped to the segment's last pair; a
       // row past the end, or a masked element, is multiplied by an exact 0)
-      Z4<E> za[kGradAhead], zb[kGradAhead];
+      ZC<E, CPL> za[kGradAhead], zb[kGradAhead];
       uint32_t ma[kGradAhead], mb[kGradAhead];
-      auto load_batch = [&](Z4<E> (&z)[kGradAhead], uint32_t (&m)[kGradAhead], int l0) {
+      auto load_batch = [&](ZC<E, CPL> (&z)[kGradAhead], uint32_t (&m)[kGradAhead], int l0) {
 #pragma unroll
         for (int u = 0; u < kGradAhead; ++u) {
           const int64_t row = s_row[min(l0 + u, l_end - 1)];
           z[u].load(Z + row * a.d + col);
-          if (kMask) m[u] = *reinterpret_cast<const uint32_t *>(a.mask + row * a.d + col);
+          if (kMask) m[u] = mask_bytes<CPL>(a.mask + row * a.d + col);
         }
       };
-      auto add_batch = [&](const Z4<E> (&z)[kGradAhead], const uint32_t (&m)[kGradAhead], int l0) {
+      auto add_batch = [&](const ZC<E, CPL> (&z)[kGradAhead], const uint32_t (&m)[kGradAhead], int l0) {
 #pragma unroll
         for (int u = 0; u < kGradAhead; ++u) {
-          float zv[kGradCPL];
+          float zv[CPL];
           z[u].get(zv);
           const float in = l0 + u < l_end ? 1.f : 0.f;
 #pragma unroll
-          for (int c = 0; c < kGradCPL; ++c) {
+          for (int c = 0; c < CPL; ++c) {
             float f = in;
             if (kMask) f *= float((m[u] >> (8 * c)) & 0xffu);   // keep mask is 0/1
             zv[c] *= f;
@@ -162,7 +181,7 @@ __device__ __forceinline__ void seg_outer_partial_wg(const SegOuterArgs &a, int 
           for (int jj = 0; jj < RB; ++jj) {
             const float cj = cf[jj];   // zero past nr
 #pragma unroll
-            for (int c = 0; c < kGradCPL; ++c) acc[jj][c] = fmaf(cj, zv[c], acc[jj][c]);
+            for (int c = 0; c < CPL; ++c) acc[jj][c] = fmaf(cj, zv[c], acc[jj][c]);
           }
         }
       };
@@ -178,29 +197,31 @@ __device__ __forceinline__ void seg_outer_partial_wg(const SegOuterArgs &a, int 
         float *dst = a.part + (int64_t(s + q) * a.max_rank + j0) * a.d + col;
 #pragma unroll
         for (int jj = 0; jj < RB; ++jj)
-          if (jj < nr)
-            *reinterpret_cast<float4 *>(dst + int64_t(jj) * a.d) =
-                make_float4(acc[jj][0], acc[jj][1], acc[jj][2], acc[jj][3]);
+          if (jj < nr) {
+            float *o = dst + int64_t(jj) * a.d;
+            if constexpr (CPL == 4) *reinterpret_cast<float4 *>(o) = make_float4(acc[jj][0], acc[jj][1], acc[jj][2], acc[jj][3]);
+            else *reinterpret_cast<float2 *>(o) = make_float2(acc[jj][0], acc[jj][1]);
+          }
       }
     }
   }
 }
 
-template <typename E, bool kMask, int RB>
+template <typename E, bool kMask, int RB, int CPL>
 __global__ __launch_bounds__(kGradThreads) void seg_outer_partial_kernel(SegOuterArgs a, int nsplit) {
   __shared__ OuterLds<RB> lds;
-  seg_outer_partial_wg<E, kMask, RB>(a, nsplit, blockIdx.x, lds);
+  seg_outer_partial_wg<E, kMask, RB, CPL>(a, nsplit, blockIdx.x, lds);
 }
 
 // The partials of both factors in one launch: column slices 0 .. bcols - 1 are
 // b's (dB, never masked), the rest a's.  A small batch's two launches of a few
 // workgroups are latency twice (333 tokens as above: 9 + 9 -> 10 us).
-template <typename E, bool kMask, int RB>
+template <typename E, bool kMask, int RB, int CPL>
 __global__ __launch_bounds__(kGradThreads) void seg_outer_both_kernel(SegOuterArgs b, SegOuterArgs a,
                                                                       int bcols, int nsplit) {
   __shared__ OuterLds<RB> lds;
-  if (int(blockIdx.x) < bcols) seg_outer_partial_wg<E, false, RB>(b, nsplit, blockIdx.x, lds);
-  else seg_outer_partial_wg<E, kMask, RB>(a, nsplit, int(blockIdx.x) - bcols, lds);
+  if (int(blockIdx.x) < bcols) seg_outer_partial_wg<E, false, RB, CPL>(b, nsplit, blockIdx.x, lds);
+  else seg_outer_partial_wg<E, kMask, RB, CPL>(a, nsplit, int(blockIdx.x) - bcols, lds);
 }
 
 // The same partials with bf16 MFMA (prefill-size batches): out[j][n] =
@@ -666,7 +687,8 @@ namespace {
 struct OuterShape {
   unsigned chunks, rblocks;
   int nsplit;
-  bool narrow;
+  int rb, cpl;
+  int slices(int d) const { return (d + cpl * kGradThreads - 1) / (cpl * kGradThreads); }
 };
 
 OuterShape outer_shape(int64_t cols, int64_t TK, int64_t N, int max_rank) {
@@ -677,8 +699,9 @@ OuterShape outer_shape(int64_t cols, int64_t TK, int64_t N, int max_rank) {
   const int64_t most = N < 32 ? N : 32;
   if (ns > most) ns = most;
   o.nsplit = int(ns > 1 ? ns : 1);
-  o.narrow = cols * o.chunks * rchunks * o.nsplit < 512;
-  o.rblocks = unsigned(o.narrow ? (max_rank + 3) / 4 : rchunks);
+  o.rb = cols * o.chunks * rchunks * o.nsplit < 512 ? 4 : kGradRankChunk;
+  o.rblocks = unsigned((max_rank + o.rb - 1) / o.rb);
+  o.cpl = o.rb == 4 && cols * o.chunks * o.rblocks * o.nsplit < 1024 ? 2 : kGradCPL;
   return o;
 }
 
@@ -689,11 +712,15 @@ hipError_t launch_seg_outer_both(const SegOuterArgs &b, const SegOuterArgs &a, i
   if (TK == 0) return hipSuccess;
   const int bcols = (b.d + kGradCols - 1) / kGradCols, cols = bcols + (a.d + kGradCols - 1) / kGradCols;
   const OuterShape o = outer_shape(cols, TK, N, a.max_rank);
-  const dim3 g1(unsigned(cols), o.chunks, o.rblocks * unsigned(o.nsplit)), block(kGradThreads);
+  const int bc1 = o.slices(b.d);
+  const dim3 g1(unsigned(bc1 + o.slices(a.d)), o.chunks, o.rblocks * unsigned(o.nsplit)), block(kGradThreads);
+#define LORA_SOB3(E, M, RB, C) \
+  hipLaunchKernelGGL((seg_outer_both_kernel<E, M, RB, C>), g1, block, 0, st, b, a, bc1, o.nsplit)
 #define LORA_SOB(E, M) \
   do { \
-    if (o.narrow) hipLaunchKernelGGL((seg_outer_both_kernel<E, M, 4>), g1, block, 0, st, b, a, bcols, o.nsplit); \
-    else hipLaunchKernelGGL((seg_outer_both_kernel<E, M, kGradRankChunk>), g1, block, 0, st, b, a, bcols, o.nsplit); \
+    if (o.cpl == 2) LORA_SOB3(E, M, 4, 2); \
+    else if (o.rb == 4) LORA_SOB3(E, M, 4, kGradCPL); \
+    else LORA_SOB3(E, M, kGradRankChunk, kGradCPL); \
   } while (0)
   if (dtype == LORA_BF16) {
     if (a.mask) LORA_SOB(uint16_t, true);
@@ -703,6 +730,7 @@ hipError_t launch_seg_outer_both(const SegOuterArgs &b, const SegOuterArgs &a, i
     else LORA_SOB(float, false);
   }
 #undef LORA_SOB
+#undef LORA_SOB3
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   const int64_t segs = TK < N ? TK : N;
@@ -728,15 +756,19 @@ hipError_t launch_seg_outer(const SegOuterArgs &a, int dtype, int64_t TK, int64_
     // (the other factor's width takes the MFMA form, so dtype is bf16)
     if (dtype != LORA_BF16) return hipErrorInvalidConfiguration;
     const OuterShape o = outer_shape(cols, TK, N, a.max_rank);
-    const dim3 g1(cols, chunks, o.rblocks * unsigned(o.nsplit));
+    const dim3 g1(unsigned(o.slices(a.d)), chunks, o.rblocks * unsigned(o.nsplit));
+#define LORA_SOP3(M, RB, C) \
+  hipLaunchKernelGGL((seg_outer_partial_kernel<uint16_t, M, RB, C>), g1, block, 0, st, a, o.nsplit)
 #define LORA_SOP(M) \
   do { \
-    if (o.narrow) hipLaunchKernelGGL((seg_outer_partial_kernel<uint16_t, M, 4>), g1, block, 0, st, a, o.nsplit); \
-    else hipLaunchKernelGGL((seg_outer_partial_kernel<uint16_t, M, kGradRankChunk>), g1, block, 0, st, a, o.nsplit); \
+    if (o.cpl == 2) LORA_SOP3(M, 4, 2); \
+    else if (o.rb == 4) LORA_SOP3(M, 4, kGradCPL); \
+    else LORA_SOP3(M, kGradRankChunk, kGradCPL); \
   } while (0)
     if (a.mask) LORA_SOP(true);
     else LORA_SOP(false);
 #undef LORA_SOP
+#undef LORA_SOP3
   }
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;

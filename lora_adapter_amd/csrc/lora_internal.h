@@ -487,8 +487,9 @@ hipError_t launch_transpose(const void *src, void *dst, int rows, int cols, int 
 // Products over e4m3 operands (see gemm_quantised.hip): the configuration, and
 // the GEMM (partials, or the fused epilogue for kind 5).  Split forms are
 // finished by launch_epilogue / launch_grad_x_epilogue.
-// few: one slot per token and a pool of few adapters.
-GemmConfig choose_quantised_gemm(int T, bool few, int d_in, int d_out, int dtype);
+// few: the pool's adapters where they are at most 16 and a token has one slot,
+// else 0.
+GemmConfig choose_quantised_gemm(int T, int few, int d_in, int d_out, int dtype);
 hipError_t launch_quantised_gemm(const GemmConfig &c, const QGemmArgs &q, int dtype, hipStream_t s);
 // The split forms with the plan built by one more workgroup of 256 threads
 // and, with ss (bf16, kind 4), the per-slot shrink in the same launch.
