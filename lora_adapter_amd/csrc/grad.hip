@@ -84,6 +84,11 @@ __device__ __forceinline__ int seg_of(const int32_t *seg_off, int S, int p) {
 // columns left to others (2319 tokens, 832 and 2496 columns, bf16, rank 8: 36
 // -> 28 us for the 512 columns; 60 fp32 adapters, 669 tokens, 1920 workgroups:
 // 37 -> 41, so not there).
+// (the sums over chunks skip those segments)
+__device__ __forceinline__ bool one_chunk(int beg, int end) {
+  return beg / kGradPairChunk == (end - 1) / kGradPairChunk;
+}
+
 template <int RB>
 struct OuterLds {
   int row[kGradPairChunk];
@@ -145,6 +150,12 @@ __device__ __forceinline__ void seg_outer_partial_wg(const SegOuterArgs &a, int 
       if (tid == 0 && bx == 0 && j0 == 0) atomicOr(a.err_word, LORA_DEVERR_CAPACITY);
     } else if (j0 < r) {
       const int nr = min(RB, r - j0);
+      // a segment within one chunk goes to its pages at once
+      const bool whole = one_chunk(a.plan.seg_off[s], a.plan.seg_off[s + 1]);
+      const int ps = a.page_start[ad] + j0;
+      int pid[RB];
+#pragma unroll
+      for (int jj = 0; jj < RB; ++jj) pid[jj] = a.page_ids[ps + min(jj, nr - 1)];
       float acc[RB][CPL];
 #pragma unroll
       for (int jj = 0; jj < RB; ++jj)
@@ -198,9 +209,13 @@ __device__ __forceinline__ void seg_outer_partial_wg(const SegOuterArgs &a, int 
 #pragma unroll
         for (int jj = 0; jj < RB; ++jj)
           if (jj < nr) {
-            float *o = dst + int64_t(jj) * a.d;
-            if constexpr (CPL == 4) *reinterpret_cast<float4 *>(o) = make_float4(acc[jj][0], acc[jj][1], acc[jj][2], acc[jj][3]);
-            else *reinterpret_cast<float2 *>(o) = make_float2(acc[jj][0], acc[jj][1]);
+            // (+ 0: a -0 of a whole segment's sum as the sum over chunks gives it)
+            float *o = whole ? a.out_pages + int64_t(pid[jj]) * a.d + col : dst + int64_t(jj) * a.d;
+            if constexpr (CPL == 4)
+              *reinterpret_cast<float4 *>(o) =
+                  make_float4(acc[jj][0] + 0.f, acc[jj][1] + 0.f, acc[jj][2] + 0.f, acc[jj][3] + 0.f);
+            else
+              *reinterpret_cast<float2 *>(o) = make_float2(acc[jj][0] + 0.f, acc[jj][1] + 0.f);
           }
       }
     }
@@ -584,6 +599,8 @@ void seg_outer_mfma_kernel(SegOuterArgs a) {
 // Adds each segment's partials in chunk order (up to 8 loads in flight) and
 // writes the fp32 gradient page of every rank row: one workgroup per (1024
 // columns, segment, rank row); workgroup (bx, by, bz) of a (., gy, .) grid.
+// kDone: segments within one chunk are in their pages already.
+template <bool kDone>
 __device__ __forceinline__ void seg_outer_reduce_wg(const SegOuterArgs &a, int bx, int by, int bz, int gy) {
   const int S = a.plan.hdr[LORA_PH_SEGS];
   const int col = (bx * kGradThreads + threadIdx.x) * kGradCPL;
@@ -594,6 +611,7 @@ __device__ __forceinline__ void seg_outer_reduce_wg(const SegOuterArgs &a, int b
     const int ad = a.plan.seg_adapter[s];
     const int r = a.rank[ad];
     if (r > a.max_rank || j >= r) continue;
+    if (kDone && one_chunk(a.plan.seg_off[s], a.plan.seg_off[s + 1])) continue;
     const int q0 = a.plan.seg_off[s] / kGradPairChunk;
     const int q1 = (a.plan.seg_off[s + 1] - 1) / kGradPairChunk;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -614,15 +632,16 @@ __device__ __forceinline__ void seg_outer_reduce_wg(const SegOuterArgs &a, int b
   }
 }
 
+template <bool kDone>
 __global__ __launch_bounds__(kGradThreads) void seg_outer_reduce_kernel(SegOuterArgs a) {
-  seg_outer_reduce_wg(a, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.y);
+  seg_outer_reduce_wg<kDone>(a, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.y);
 }
 
 // Both factors' sums, column slices as in seg_outer_both_kernel.
 __global__ __launch_bounds__(kGradThreads) void seg_reduce_both_kernel(SegOuterArgs b, SegOuterArgs a,
                                                                        int bcols) {
-  if (int(blockIdx.x) < bcols) seg_outer_reduce_wg(b, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.y);
-  else seg_outer_reduce_wg(a, int(blockIdx.x) - bcols, blockIdx.y, blockIdx.z, gridDim.y);
+  if (int(blockIdx.x) < bcols) seg_outer_reduce_wg<true>(b, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.y);
+  else seg_outer_reduce_wg<true>(a, int(blockIdx.x) - bcols, blockIdx.y, blockIdx.z, gridDim.y);
 }
 
 // G[u_off[p] + j] = (gate . scale . extra) . sum over tiles of gpart, one
@@ -661,7 +680,7 @@ __global__ __launch_bounds__(256) void seg_g_reduce_kernel(SegOuterArgs a, GRedu
                                                            int gy, int64_t n_seg) {
   const int64_t b = blockIdx.x;
   if (b < n_seg) {
-    seg_outer_reduce_wg(a, int(b % cols), int((b / cols) % gy), int(b / (int64_t(cols) * gy)), gy);
+    seg_outer_reduce_wg<false>(a, int(b % cols), int((b / cols) % gy), int(b / (int64_t(cols) * gy)), gy);
   } else {
     g_reduce_wg(g, b - n_seg);
   }
@@ -782,7 +801,8 @@ hipError_t launch_seg_outer(const SegOuterArgs &a, int dtype, int64_t TK, int64_
     return hipGetLastError();
   }
   const dim3 g2(cols, gy, unsigned(a.max_rank));
-  hipLaunchKernelGGL(seg_outer_reduce_kernel, g2, block, 0, st, a);
+  if (grad_mfma_form(dtype, TK, a.d)) hipLaunchKernelGGL(seg_outer_reduce_kernel<false>, g2, block, 0, st, a);
+  else hipLaunchKernelGGL(seg_outer_reduce_kernel<true>, g2, block, 0, st, a);
   return hipGetLastError();
 }
 
