@@ -14,7 +14,9 @@
 // Prefill-size bf16 batches run the outer products on MFMA with the pairs as
 // K (seg_outer_mfma_kernel), and the dB pass also forms the per-tile partials
 // of G from the same staged dY rows; other batches use the vector ALU
-// (seg_outer_partial_kernel) and the shrink kernel on (dY, B pages) for G.
+// (seg_outer_both_kernel; seg_outer_partial_kernel where the other factor's
+// width takes the MFMA form) and the shrink kernel on (dY, B pages) for G, and
+// write the segments that lie in one chunk to their pages at once.
 // Both forms are organised for bandwidth (rows in flight, 16-byte loads).
 #include "lora_internal.h"
 

@@ -820,13 +820,13 @@ __global__ __launch_bounds__(256, 4) void orth_apply_kernel(OrthArgs a) {
 
 int orth_r(int max_rank) { return (max_rank + 15) / 16 * 16; }
 
-// Column chunks of the Gram launch: about 1024 workgroups, at least 256 columns
-// each (two steps of each wave); 3072 where ranks go over 64, whose pairs of
-// blocks take unlike times.
+// Column chunks of the Gram launch: about four workgroups per CU, at least 256
+// columns each (two steps of each wave); twelve where ranks go over 64, whose
+// pairs of blocks take unlike times.
 int orth_chunk_cols(int64_t mats, int max_rank, int d) {
   const int s = (max_rank + kSmall - 1) / kSmall;
   const int64_t per = mats * (s * (s + 1) / 2);
-  const int64_t want = ((max_rank > kSmall ? 3072 : 1024) + per - 1) / per;
+  const int64_t want = ((max_rank > kSmall ? 12 : 4) * 256 + per - 1) / per;
   int64_t cols = (d + want - 1) / want;
   cols = (cols + 127) / 128 * 128;
   return int(cols < 256 ? 256 : cols);
