@@ -467,7 +467,9 @@ __device__ __forceinline__ void tile_run(const GemmArgs &g, char *smem, int m0, 
         }
       }
   } else {
-    fused_epilogue<BM, BN, WM, WN, kMask>(g, acc, st0, st1, m0, n0, pre);
+    unsigned nf;
+    fused_epilogue<BM, BN, WM, WN, kMask>(g, acc, st0, st1, m0, n0, pre, nf);
+    if (nf) expand_nonfinite<TM, TN * 32, kMask>(g, m0 + wm * TM * 32, n0 + wn * TN * 32, nf);
   }
 }
 

@@ -237,14 +237,15 @@ __device__ __forceinline__ void lds_dma4(const void *gptr, uint32_t lds) {
 // 16, or several slots per token): MFMA passes of 16 rank rows, one slot and
 // one adapter at a time, into accumulators of their own, then added to the
 // staged base product (times the keep mask with kMask), rounded and stored.
+// Returns the blocks left to expand_nonfinite.
 // One rolled loop over the blocks, apart from the fused epilogue: inside its
 // unrolled blocks the same code slowed the common ones (8192 x 4096 -> 11008,
 // rank 16: 357 -> 449 us).
 template <int BM, int BN, int WM, int WN, bool kMask>
-__device__ __forceinline__ void q_expand_wide(const GemmArgs &g,
-                                              f32x16_t (&acc)[TileCfg<BM, BN, WM, WN>::TM]
-                                                             [TileCfg<BM, BN, WM, WN>::TN],
-                                              char *lds0, char *lds1, int m0, int n0, unsigned blocks) {
+__device__ __forceinline__ unsigned q_expand_wide(const GemmArgs &g,
+                                                  f32x16_t (&acc)[TileCfg<BM, BN, WM, WN>::TM]
+                                                                 [TileCfg<BM, BN, WM, WN>::TN],
+                                                  char *lds0, char *lds1, int m0, int n0, unsigned blocks) {
   using C = TileCfg<BM, BN, WM, WN>;
   constexpr int TM = C::TM, TN = C::TN, WC = TN * 32, SC = WC + 4, LPR = WC / 8, RPS = 64 / LPR;
   static_assert((C::NW / 2) * 40 * SC * 4 <= C::STAGE && RPS <= 8, "staging must fit in LDS");
@@ -258,6 +259,8 @@ __device__ __forceinline__ void q_expand_wide(const GemmArgs &g,
   const int cbase = n0 + wn * WC, vr = lane / LPR, vc = (lane % LPR) * 8;
   const bool c8 = cbase + vc + 8 <= g.N;
   int key_ps = -1, key_j = -1;               // adapter slice held in bfr
+  bool b_dropped = false;                    // .. less its non-finite values
+  unsigned nonfinite = 0;
   bf16x8_t bfr[TN] = {};
   auto put = [&](const f32x16_t (&a)[TN]) __attribute__((always_inline)) {
 #pragma unroll
@@ -318,9 +321,11 @@ __device__ __forceinline__ void q_expand_wide(const GemmArgs &g,
               const uint4 packed = make_uint4(w4[0], w4[1], w4[2], w4[3]);
               __builtin_memcpy(&bfr[j], &packed, 16);
             }
+            b_dropped = drop_nonfinite<TN>(bfr);
             key_ps = kps;
             key_j = jb;
           }
+          if (b_dropped) nonfinite |= 1u << i;
           uint32_t hw[4], lw[4];
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
@@ -366,6 +371,7 @@ __device__ __forceinline__ void q_expand_wide(const GemmArgs &g,
       }
     }
   }
+  return nonfinite;
 }
 
 template <int BM, int BN, int WM, int WN, int NS, bool kFused, bool kMask = false>
@@ -513,9 +519,11 @@ __device__ __forceinline__ void q_tile_run(const QGemmArgs &q, char *smem, int m
         }
       }
   } else {
+    unsigned nf;
     const unsigned wide =
-        fused_epilogue<BM, BN, WM, WN, kMask, true>(g, acc, smem, smem + C::STAGE, m0, n0, pre);
-    if (wide) q_expand_wide<BM, BN, WM, WN, kMask>(g, acc, smem, smem + C::STAGE, m0, n0, wide);
+        fused_epilogue<BM, BN, WM, WN, kMask, true>(g, acc, smem, smem + C::STAGE, m0, n0, pre, nf);
+    if (wide) nf |= q_expand_wide<BM, BN, WM, WN, kMask>(g, acc, smem, smem + C::STAGE, m0, n0, wide);
+    if (nf) expand_nonfinite<TM, TN * 32, kMask>(g, m0 + wm * TM * 32, n0 + wn * TN * 32, nf);
   }
 }
 

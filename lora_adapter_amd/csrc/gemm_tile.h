@@ -314,6 +314,84 @@ __device__ __forceinline__ void epi_fetch_pid(const GemmArgs &g, EpiPre<TM> &p) 
   }
 }
 
+// An MFMA pass of the expand takes one adapter's B rows for all 32 rows of a
+// block, with U = 0 in the rows of other adapters: an infinity or a NaN of B
+// would reach those as 0 . inf.  The passes therefore run on B fragments whose
+// non-finite values are zero (drop_nonfinite, when a fragment has any), and
+// expand_nonfinite adds what was left out to the rows it belongs to.  The test
+// is one dot product with zeros per pair of values, NaN if either is not
+// finite (16 adapters in any order, 8192 x 4096 -> 4096, bf16: 314.3 -> 317.3 us
+// of the call; 325 with integer compares; nothing measurable in runs).
+template <int TN>
+__device__ __forceinline__ bool drop_nonfinite(bf16x8_t (&b)[TN]) {
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  const bf16x2_t zero = {};
+  uint32_t w[TN][4];
+  float t[TN];
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    __builtin_memcpy(w[j], &b[j], 16);
+    t[j] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      bf16x2_t v;
+      __builtin_memcpy(&v, &w[j][e], 4);
+      t[j] = __builtin_amdgcn_fdot2_f32_bf16(v, zero, t[j], false);
+    }
+    if (j > 0) t[0] += t[j];
+  }
+  if (__builtin_expect(__ballot(t[0] != t[0]) == 0, 1)) return false;
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      // the exponents' carry: bits 15 and 31 of a half that is not finite
+      const uint32_t x = (((w[j][e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u) >> 15;
+      w[j][e] &= ~((x << 16) - x);
+    }
+    __builtin_memcpy(&b[j], w[j], 16);
+  }
+  return true;
+}
+
+// Y += the products of U with the non-finite B values alone, for the 32-row
+// blocks `blocks` (bit i: rows row0 + 32 i ..) and the wave's WC columns, which
+// this wave has stored: each sum is an infinity or a NaN, so that the rounding
+// of Y before it is no loss.
+template <int TM, int WC, bool kMask>
+__device__ __forceinline__ void expand_nonfinite(const GemmArgs &g, int row0, int cbase, unsigned blocks) {
+  const int lane = threadIdx.x & 63;
+  const uint16_t *Bp = static_cast<const uint16_t *>(g.ex.b_pages);
+  __threadfence();                             // the lanes' stores of Y before the loads here
+#pragma unroll 1
+  for (int rr = 0; rr < TM * 32; ++rr) {
+    const int row = row0 + rr;
+    if (row >= g.M) break;
+    if (!((blocks >> (rr >> 5)) & 1u)) continue;
+#pragma unroll 1
+    for (int c = cbase + lane; c < min(cbase + WC, g.N); c += 64) {
+      float sum = 0.f;
+      bool any = false;
+#pragma unroll 1
+      for (int k = 0; k < g.ex.K; ++k) {
+        const int4 sd = g.ex.slot_desc[int64_t(row) * g.ex.K + k];
+        if (sd.x < 0) continue;
+#pragma unroll 1
+        for (int j = 0; j < sd.y; ++j) {
+          const uint16_t b = Bp[int64_t(g.ex.page_ids[sd.w + j]) * g.ex.d_out + c];
+          if ((b & 0x7f80u) != 0x7f80u) continue;
+          sum = fmaf(g.ex.U[sd.z + j], bf2f(b), sum);
+          any = true;
+        }
+      }
+      if (!any) continue;
+      uint16_t *y = static_cast<uint16_t *>(g.Y) + int64_t(row) * g.N + c;
+      if constexpr (kMask) sum *= float(g.mask[int64_t(row) * g.N + c]);
+      *y = f2bf(bf2f(*y) + sum);
+    }
+  }
+}
+
 // Fused epilogue of a tile: add the expand to the fp32 accumulators, round
 // once, store Y.
 //   * One slot per token (K = 1) and ranks <= 16 -- prefill: the expand of a
@@ -340,13 +418,15 @@ __device__ __forceinline__ void epi_fetch_pid(const GemmArgs &g, EpiPre<TM> &p) 
 // the same registers, and moves it through a second, 8-row staging region a
 // quarter at a time; the row path keeps the term in registers of its own.
 // kLeaveRows: blocks for the row path are left to the caller, which gets them
-// as bits (bit i: 32-row block i of the wave); otherwise 0 is returned.
+// as bits (bit i: 32-row block i of the wave).  nonfinite: the blocks, so, that
+// the caller has to take to expand_nonfinite.
 template <int BM, int BN, int WM, int WN, bool kMask, bool kLeaveRows = false>
 __device__ __forceinline__ unsigned fused_epilogue(const GemmArgs &g,
                                                f32x16_t (&acc)[TileCfg<BM, BN, WM, WN>::TM]
                                                               [TileCfg<BM, BN, WM, WN>::TN],
                                                char *lds0, char *lds1, int m0, int n0,
-                                               const EpiPre<TileCfg<BM, BN, WM, WN>::TM> &pre) {
+                                               const EpiPre<TileCfg<BM, BN, WM, WN>::TM> &pre,
+                                               unsigned &nonfinite) {
   using C = TileCfg<BM, BN, WM, WN>;
   constexpr int TM = C::TM, TN = C::TN;
   constexpr int WC = TN * 32;                // columns of this wave's sub-tile
@@ -427,7 +507,9 @@ __device__ __forceinline__ unsigned fused_epilogue(const GemmArgs &g,
   cache.ps = -1;
   cache.r = -1;
   int bkey_ps = -1, bkey_r = -1;             // adapter slice held in bfr
+  bool b_dropped = false;                    // .. less its non-finite values
   bf16x8_t bfr[TN] = {};
+  nonfinite = 0;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     if (kLeaveRows && ((rowwise >> i) & 1u)) continue;
@@ -450,6 +532,14 @@ __device__ __forceinline__ unsigned fused_epilogue(const GemmArgs &g,
             acc[i][j] = f32x16_t{};
           }
         }
+      }
+      // A operand: U of row frow, rank rows 8*half .. +7, as bf16 hi + lo
+      uint32_t hw[4], lw[4];
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const uint32_t h2 = f2bf2(uv[i][e], uv[i][e + 1]);
+        hw[e >> 1] = h2;
+        lw[e >> 1] = f2bf2(uv[i][e] - bf_lo(h2), uv[i][e + 1] - bf_hi(h2));
       }
       while (pending) {
         const int leader = __ffsll(pending) - 1;
@@ -478,22 +568,15 @@ __device__ __forceinline__ unsigned fused_epilogue(const GemmArgs &g,
             const uint4 packed = make_uint4(w4[0], w4[1], w4[2], w4[3]);
             __builtin_memcpy(&bfr[j], &packed, 16);
           }
+          b_dropped = drop_nonfinite<TN>(bfr);
           bkey_ps = kps;
           bkey_r = kr;
         }
-        // A operand: U of row frow (zero unless the row is on this adapter),
-        // rank rows 8*half .. +7, as bf16 hi + lo
-        uint32_t hw[4], lw[4];
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const float ua = mine ? uv[i][e] : 0.f, ub = mine ? uv[i][e + 1] : 0.f;
-          const uint32_t h2 = f2bf2(ua, ub);
-          hw[e >> 1] = h2;
-          lw[e >> 1] = f2bf2(ua - bf_lo(h2), ub - bf_hi(h2));
-        }
+        if (b_dropped) nonfinite |= 1u << i;
+        // zero unless the row is on this adapter
         bf16x8_t ahi, alo;
-        const uint4 ph = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-        const uint4 pl = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+        const uint4 ph = mine ? make_uint4(hw[0], hw[1], hw[2], hw[3]) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 pl = mine ? make_uint4(lw[0], lw[1], lw[2], lw[3]) : make_uint4(0u, 0u, 0u, 0u);
         __builtin_memcpy(&ahi, &ph, 16);
         __builtin_memcpy(&alo, &pl, 16);
 #pragma unroll
