@@ -526,15 +526,31 @@ void seg_outer_mfma_kernel(SegOuterArgs a) {
         stage(zv, mv, k0, l_beg, l_end);
         lds_bar();
         // A operand: rank row j = lane % 16, pairs k0 + 8 * (lane / 16) .. + 7
-        // (pairs of other segments meet zeroed rows; past the chunk's end
-        // the coefficients are zero)
-        // (a step wholly past the chunk's end reads the last step's)
+        // (past the chunk's end the coefficients are zero; a step wholly past
+        // it reads the last step's)
         const int kk = (lane >> 4) * 8;
         const int ka = min(k0, kGradPairChunk - kOuterK) + kk;
         bf16x8_t ahi, alo, arest;
         __builtin_memcpy(&ahi, &s_ah[lane & 15][ka], 16);
         __builtin_memcpy(&alo, &s_al[lane & 15][ka], 16);
         __builtin_memcpy(&arest, &s_ar[lane & 15][ka], 16);
+        if (k0 < l_beg || k0 + kOuterK > l_end) {
+          // pairs of other segments: zero like their rows (an infinity or a
+          // NaN of another adapter's coefficients times those is NaN)
+          auto keep = [&](bf16x8_t &v) {
+            uint32_t w[4];
+            __builtin_memcpy(w, &v, 16);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int l = k0 + kk + e;
+              if (l < l_beg || l >= l_end) w[e >> 1] &= (e & 1) ? 0x0000ffffu : 0xffff0000u;
+            }
+            __builtin_memcpy(&v, w, 16);
+          };
+          keep(ahi);
+          keep(alo);
+          keep(arest);
+        }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           // B operand: column wave*64 + 16b + lane % 16, the same 8 pairs,

@@ -114,3 +114,15 @@ def test_rows_of_other_adapters(kind, T, K, d_in, d_out, extra):
     assert not torch.isfinite(P.rows(dX, P.b[3], every(d_in))[keep]).any()     # through G
     assert not torch.isfinite(P.rows(Y, P.a[0], every(d_out))).any()           # through U
     assert not torch.isfinite(P.rows(dX, P.a[3], P.a_cols)[keep[:, P.a_cols]]).any()
+
+
+@pytest.mark.parametrize("kind,T,K,d_in,d_out,extra", CASES)
+def test_gradients_of_other_adapters(kind, T, K, d_in, d_out, extra):
+    P = Poisoned(kind, T, K, d_in, d_out, extra)
+    _, dA, dB, _ = P.clean
+    for clean, got, page in ((dA, P.b[1], P.b_page), (dB, P.a[2], P.a_page)):
+        rest = torch.ones(got.shape[0], dtype=torch.bool, device="cuda")
+        rest[page] = False
+        assert same(got[rest], clean[rest])
+        assert not torch.isfinite(got[page]).any()
+    assert same(P.b[2], dB) and same(P.a[1], dA)
