@@ -126,3 +126,32 @@ def test_gradients_of_other_adapters(kind, T, K, d_in, d_out, extra):
         assert same(got[rest], clean[rest])
         assert not torch.isfinite(got[page]).any()
     assert same(P.b[2], dB) and same(P.a[1], dA)
+
+
+@pytest.mark.parametrize("kind,T,K,d_in,d_out,extra", CASES)
+def test_a_non_finite_token_stays_its_own(kind, T, K, d_in, d_out, extra):
+    """A NaN in a row of X, then an infinity in a row of dY: the row's own
+    outputs, and the pages of the adapters that the row uses."""
+    w = workload(T, K, d_in, d_out, **extra)
+    t = int(np.flatnonzero(((w.ids >= 0) & (w.gates != 0)).all(axis=1))[T // 3])
+    L = kind(w)
+    clean = run(L)
+    pages = np.concatenate([w.page_ids[w.page_start[a]:w.page_start[a + 1]] for a in set(w.ids[t].tolist())])
+    row = torch.arange(T, device="cuda") != t
+    page = torch.ones(w.n_pages, dtype=torch.bool, device="cuda")
+    page[torch.from_numpy(pages).long().cuda()] = False
+
+    def others(got):
+        for i, rest in ((0, row), (1, page), (2, page), (3, row)):
+            assert same(got[i][rest], clean[i][rest]), i
+
+    keep = L.X.clone()
+    L.X[t, d_in - 1] = float("nan")
+    got = run(L)
+    others(got)
+    assert torch.isnan(got[0][t]).all() and same(got[3], clean[3])     # dX does not read X
+    L.X.copy_(keep)
+    L.dY[t, 1] = float("inf")
+    got = run(L)
+    others(got)
+    assert same(got[0], clean[0]) and not torch.isfinite(got[3][t]).any()
