@@ -33,7 +33,9 @@ __device__ __forceinline__ void quantise_chunks(const E *X, int T, int d, int ch
     if (wc >= total) return;
     const int col = int(wc % chunks) * 512 + lane * 8;
     const uint32_t byte = q_scale_byte(max16(abs_max8(v[c])));
-    if (col < ld) *reinterpret_cast<uint2 *>(codes + t * ld + col) = q_encode8(v[c], byte);
+    // (past d: zero in a block of scale byte 255 too)
+    if (col < ld)
+      *reinterpret_cast<uint2 *>(codes + t * ld + col) = col < d ? q_encode8(v[c], byte) : make_uint2(0, 0);
     const int blk = col / kQBlock;
     if ((lane & 15) != 0) continue;
     if constexpr (kTiled) {
