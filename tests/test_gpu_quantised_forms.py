@@ -1,4 +1,6 @@
-"""Rows of the 8-bit layer whose last block is short."""
+"""The 8-bit layer's product split over its workgroups at any K tile (the
+stream form: more than 128 tokens, fewer tiles than fill the GPU, long K), and
+rows whose last block is short.  Tolerances as in test_gpu_quantised."""
 import numpy as np
 import pytest
 
@@ -6,6 +8,7 @@ torch = pytest.importorskip("torch")
 
 from lora_adapter_amd import binding as B
 from oracle import quantised as Q
+from tests.test_gpu_quantised import Layer, check, expected, workload
 
 pytestmark = pytest.mark.gpu
 
@@ -15,6 +18,43 @@ def _gpu():
     if not torch.cuda.is_available():
         pytest.skip("no GPU")
     B.lib()
+
+
+# forward: ceil(T / 256) x ceil(d_out / 128) tiles of ceil(d_in / 128) blocks of
+# K, at least 1020 in all (255 workgroups, four blocks each); dX the other way
+# round.  Widths are odd multiples of 64, so that tiles begin inside a
+# workgroup's run and the last block of K is short.
+STREAM = [  # T, K, d_in, d_out, extra
+    (300, 1, 4288, 1984, {}),                       # 2 x 16 tiles of 34
+    (300, 1, 1984, 4288, {"mask": True}),
+    (300, 2, 4288, 1984, {"mask": True, "hi": 40}),
+    (300, 2, 1984, 4288, {"hi": 40}),
+    (129, 1, 2112, 8000, {"mask": True}),           # 1 x 63 tiles of 17
+    (700, 1, 8000, 704, {"runs": True, "hi": 80}),  # 3 x 6 tiles of 63
+    (700, 1, 704, 8000, {"runs": True, "mask": True}),
+]
+
+
+@pytest.mark.parametrize("T,K,d_in,d_out,extra", STREAM)
+def test_stream_form(T, K, d_in, d_out, extra):
+    tiles = lambda d_k, d_n: -(-T // 256) * -(-d_n // 128) * -(-d_k // 128)
+    assert max(tiles(d_in, d_out), tiles(d_out, d_in)) >= 1020
+    w = workload(T, K, d_in, d_out, **extra)
+    L = Layer(w)
+    L.forward()
+    _, _, dX = L.backward()
+    torch.cuda.synchronize()
+    y, ty, x, tx = expected(w)
+    check(L.Y, y, ty, "Y")
+    check(dX, x, tx, "dX")
+    # the plan apart from the product, and the same again
+    Y, U = L.Y.clone(), L.U()
+    L.Y.fill_(float("nan"))
+    L.ws.fill_(0x11)
+    L.run_plan()
+    B.lora_apply_quantised(L.X, L.W8, L.Y, L.T, L.K, L.gates, L.keep_mask, L.keep_scale, L.pool, L.plan, L.ws)
+    torch.cuda.synchronize()
+    assert torch.equal(L.Y, Y) and np.array_equal(L.U(), U)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
