@@ -781,7 +781,8 @@ int32_t quant_apply_args(const void *X, const lora_quantised_weight *W, void *Y,
   if ((st = check_weight(W, pool)) != LORA_OK) return st;
   if (!plan) return LORA_ERR_INVALID_ARG;
   if (T == 0) return LORA_OK;
-  if (!X || !Y || !W->q_t || !W->scale || !gates || !ws || Y == X) return LORA_ERR_INVALID_ARG;
+  if (!X || !Y || !W->q_t || !W->scale || !gates || !ws) return LORA_ERR_INVALID_ARG;
+  if (Y == X || Y == W->q_t || Y == W->scale) return LORA_ERR_INVALID_ARG;
   a.t = quant_tail(T, few_adapters(K, pool), pool->d_in, pool->d_out, pool->dtype);
   if (ws_bytes < a.t.total) return LORA_ERR_CAPACITY;
   const size_t head = a.head = (ws_bytes - a.t.total) / kAlign * kAlign;
@@ -920,7 +921,8 @@ int32_t lora_grad_x_quantised(const void *dY, const lora_quantised_weight *W,
   if ((st = check_weight(W, pool)) != LORA_OK) return st;
   if (!plan || max_rank < 1 || max_rank > LORA_MAX_RANK) return LORA_ERR_INVALID_ARG;
   if (T == 0) return LORA_OK;
-  if (!dY || !W->q || !W->scale_t || !grad_ws || !dX || !ws || dX == dY) return LORA_ERR_INVALID_ARG;
+  if (!dY || !W->q || !W->scale_t || !grad_ws || !dX || !ws) return LORA_ERR_INVALID_ARG;
+  if (dX == dY || dX == W->q || dX == W->scale_t) return LORA_ERR_INVALID_ARG;
   if (grad_ws_bytes < lora_grad_workspace_bytes(T, K, pool->n_adapters, pool->d_in, pool->d_out,
                                                 max_rank, pool->dtype))
     return LORA_ERR_CAPACITY;
