@@ -395,8 +395,8 @@ PlanLaunch plan_setup(const int32_t *ids, const float *gates, int T, int K, cons
 struct OrthRec {            // what the first launch leaves about each matrix
   int32_t rank;             // 0: skipped
   int32_t page_start;
-  float inv;                // 1 / (|N|_F + eps), or 0
-  int32_t adapter;
+  float inv;                // 1 / ((|N|_F + eps) pre), or 0
+  float pre;                // 1; 2^-64 where the norm is past 2^64, to keep inv a normal number
 };
 
 struct OrthFactor {

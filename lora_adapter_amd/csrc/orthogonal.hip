@@ -213,7 +213,7 @@ __global__ __launch_bounds__(256, NBMAX <= 2 ? 4 : 2) void gram_kernel(OrthArgs 
   const int ck = blockIdx.x % a.chunks;
   int st = blockIdx.x / a.chunks;
   if (blockIdx.x == 0 && threadIdx.x == 0) {
-    a.rec[blockIdx.y] = OrthRec{r, ps, 0.f, adapter};
+    a.rec[blockIdx.y] = OrthRec{r, ps, 0.f, 1.f};
     if (fi == 0 && a.out_rank) a.out_rank[m] = r;
   }
   if (r == 0) return;
@@ -266,6 +266,14 @@ __device__ __forceinline__ double norm_inv(double tr, float eps) {
   return tr == 0 ? 0.0 : 1.0 / (sqrt(tr) + double(eps));
 }
 
+// The factor of N in two parts: past 2^126 its reciprocal would be a subnormal
+// float of few bits (16 x 8256 numbers up to 3e38 have a norm of 2^135: 4e-5).
+__device__ __forceinline__ void store_inv(OrthRec &rec, double inv) {
+  const bool far = inv > 0 && inv < 0x1p-64;
+  rec.pre = far ? 0x1p-64f : 1.f;
+  rec.inv = float(far ? inv * 0x1p64 : inv);
+}
+
 // Ranks <= 16: one 16 x 16 tile.  Element v of lane l of an MFMA result is row
 // 4 v + l / 16, column l % 16; operand k of lane l is row l % 16, column 4 k +
 // l / 16.  For a symmetric matrix these are the same value, so a result is the
@@ -316,7 +324,7 @@ __device__ __forceinline__ void steps16(const OrthArgs &a, int mat, int r, doubl
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) tr += __shfl_xor(tr, o, 64);
   const double inv = norm_inv(tr, a.eps);
-  if (lane == 0) a.rec[mat].inv = float(inv);
+  if (lane == 0) store_inv(a.rec[mat], inv);
   f64x4_t Q, P;
 #pragma unroll
   for (int v = 0; v < 4; ++v) G[v] *= inv * inv;
@@ -441,7 +449,7 @@ __device__ __forceinline__ void steps_body(const OrthArgs &a, int mat, int r, do
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) tr += __shfl_xor(tr, o, 64);
   const double inv = norm_inv(tr, a.eps);
-  if (tid == 0) a.rec[mat].inv = float(inv);
+  if (tid == 0) store_inv(a.rec[mat], inv);
   __syncthreads();
   for (int e = tid; e < n * n; e += NTH) G[(e / n) * S + e % n] *= inv * inv;
   __syncthreads();
@@ -538,7 +546,7 @@ __global__ __launch_bounds__(256) void gram_sum_kernel(OrthArgs a) {
     __syncthreads();
   }
   const double inv = norm_inv(part[0], a.eps);
-  if (blockIdx.x == 0 && tid == 0) a.rec[mat].inv = float(inv);
+  if (blockIdx.x == 0 && tid == 0) store_inv(a.rec[mat], inv);
   double *G = a.big + int64_t(mat) * kBigMats * n;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -659,9 +667,11 @@ __global__ __launch_bounds__(256, 2) void sym_product_kernel(OrthArgs a, SymOp o
 constexpr int kApplyRows = 128, kApplyQ = kApplyRows + 4;
 
 template <int NB, bool kStep, typename E>
-__device__ __forceinline__ void apply_body(const OrthArgs &a, const OrthFactor &f, int r, int ps, float inv,
+__device__ __forceinline__ void apply_body(const OrthArgs &a, const OrthFactor &f, const OrthRec &rc,
                                            int ib, const float *q, int col0, int chunks, float *lq, int *lp) {
   constexpr int U = 4;
+  const int r = rc.rank, ps = rc.page_start;
+  const float pre = rc.pre, inv = rc.inv;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int lr = lane & 15, lg = lane >> 4;
   const int R = a.R;
@@ -701,7 +711,7 @@ __device__ __forceinline__ void apply_body(const OrthArgs &a, const OrthFactor &
           v = t;
       }
       if (k >= nr) v = make_float4(0.f, 0.f, 0.f, 0.f);
-      const float b[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+      const float b[4] = {v.x * pre * inv, v.y * pre * inv, v.z * pre * inv, v.w * pre * inv};
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
         const float av = lq[(i * 16 + lr) * kApplyQ + k];
@@ -813,9 +823,9 @@ __global__ __launch_bounds__(256, 4) void orth_apply_kernel(OrthArgs a) {
   const int chunks = min(a.apply_chunks, (f.d - col0 + 255) / 256);
   const float *q = a.q + int64_t(blockIdx.y) * a.R * a.R;
   const int left = rc.rank - ib * 16;         // output rows from ib * 16
-  if (left <= 16) apply_body<1, kStep, E>(a, f, rc.rank, rc.page_start, rc.inv, ib, q, col0, chunks, lq, lp);
-  else if (left <= 32) apply_body<2, kStep, E>(a, f, rc.rank, rc.page_start, rc.inv, ib, q, col0, chunks, lq, lp);
-  else apply_body<4, kStep, E>(a, f, rc.rank, rc.page_start, rc.inv, ib, q, col0, chunks, lq, lp);
+  if (left <= 16) apply_body<1, kStep, E>(a, f, rc, ib, q, col0, chunks, lq, lp);
+  else if (left <= 32) apply_body<2, kStep, E>(a, f, rc, ib, q, col0, chunks, lq, lp);
+  else apply_body<4, kStep, E>(a, f, rc, ib, q, col0, chunks, lq, lp);
 }
 
 int orth_r(int max_rank) { return (max_rank + 15) / 16 * 16; }

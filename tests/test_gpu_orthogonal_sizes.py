@@ -13,7 +13,7 @@ torch = pytest.importorskip("torch")
 
 from lora_adapter_amd import binding as B
 from oracle import orthogonal as NS
-from tests.test_gpu_orthogonal import COEF, EPS, Fleet, run_ortho
+from tests.test_gpu_orthogonal import COEF, EPS, Fleet, run_ortho, step_once
 
 pytestmark = pytest.mark.gpu
 
@@ -76,3 +76,25 @@ def test_subnormal_rows():
     v = (fl.values(1088).astype(np.float64) * 2.0 ** -130).astype(np.float32)
     out, _ = run_ortho(fl, torch.from_numpy(v).cuda(), list(range(len(ranks))), 70, eps=1e-20)
     compare(fl, v, out, range(len(ranks)), eps=1e-20)
+
+
+@pytest.mark.parametrize("nesterov", [None, False, True])
+def test_norms_past_2_to_the_126(nesterov):
+    """.. whose reciprocal is no normal float32: rows of numbers up to 1e38,
+    orthogonalised, and as the gradient of a step."""
+    ranks = [1, 3, 16, 33, 70]
+    fl = Fleet(ranks, 4160, 4160, seed=17)
+    v = fl.rng.uniform(-1e38, 1e38, (fl.n_pages, 4160)).astype(np.float32)
+    ads = list(range(len(ranks)))
+    if nesterov is None:
+        out, _ = run_ortho(fl, torch.from_numpy(v).cuda(), ads, 70)
+        compare(fl, v, out, ads)
+        return
+    # a step of lr 1 on pages of zero with no decay leaves -O; momentum 0 makes N the gradient
+    zero = lambda: torch.zeros(fl.n_pages, 4160, device="cuda")
+    fl.pages = [zero(), zero()]
+    grad = torch.from_numpy(v).cuda()
+    keep = step_once(fl, ads, 70, [zero(), zero()], [grad, grad], [None, None], (1.0, 1.0), 0.0, nesterov, 0.0)
+    torch.cuda.synchronize()
+    for p in fl.pages:
+        compare(fl, v, -p.double().cpu().numpy(), ads)
