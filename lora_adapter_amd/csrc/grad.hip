@@ -166,7 +166,7 @@ __device__ __forceinline__ void seg_outer_partial_wg(const SegOuterArgs &a, int 
       const int l_end = send - pbeg;
       // two batches of kGradAhead token rows, the next one in flight while
       // the current one is added (rows clamped to the segment's last pair; a
-      // row past the end, or a masked element, is multiplied by an exact 0)
+      // row past the end, or a masked element, counts as an exact 0)
       ZC<E, CPL> za[kGradAhead], zb[kGradAhead];
       uint32_t ma[kGradAhead], mb[kGradAhead];
       auto load_batch = [&](ZC<E, CPL> (&z)[kGradAhead], uint32_t (&m)[kGradAhead], int l0) {
@@ -182,12 +182,11 @@ __device__ __forceinline__ void seg_outer_partial_wg(const SegOuterArgs &a, int 
         for (int u = 0; u < kGradAhead; ++u) {
           float zv[CPL];
           z[u].get(zv);
-          const float in = l0 + u < l_end ? 1.f : 0.f;
+          const bool in = l0 + u < l_end;
 #pragma unroll
           for (int c = 0; c < CPL; ++c) {
-            float f = in;
-            if (kMask) f *= float((m[u] >> (8 * c)) & 0xffu);   // keep mask is 0/1
-            zv[c] *= f;
+            const bool keep = !kMask || ((m[u] >> (8 * c)) & 0xffu) != 0;
+            zv[c] = in && keep ? zv[c] : 0.f;
           }
           const float *cf = s_cf[min(l0 + u, l_end - 1)];
 #pragma unroll

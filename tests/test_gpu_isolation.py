@@ -155,3 +155,19 @@ def test_a_non_finite_token_stays_its_own(kind, T, K, d_in, d_out, extra):
     got = run(L)
     others(got)
     assert same(got[0], clean[0]) and not torch.isfinite(got[3][t]).any()
+
+
+@pytest.mark.parametrize("kind,T,K,d_in,d_out,extra", [c for c in CASES if c[5].get("mask")])
+def test_dropped_elements_do_not_enter_the_branch(kind, T, K, d_in, d_out, extra):
+    """Infinities and NaNs of X where the keep mask is 0: U and the gradients
+    of the factors are those of any other value there."""
+    w = workload(T, K, d_in, d_out, **extra)
+    L = kind(w)
+    clean = run(L)
+    U = L.U()
+    off = torch.from_numpy(w.keep_mask == 0).cuda()
+    bad = torch.where(torch.arange(d_in, device="cuda") % 3 == 0, float("inf"), float("nan")).to(L.X.dtype)
+    L.X.copy_(torch.where(off, bad, L.X))
+    got = run(L)
+    assert np.array_equal(L.U(), U)
+    assert all(same(got[i], clean[i]) for i in (1, 2, 3))
