@@ -558,7 +558,9 @@ int32_t lora_quantise_weight(const void *W_t, int32_t dtype, const lora_quantise
  * sum the same codes with fp32 accuracy on the bf16 MFMA.
  *   ws >= lora_apply_quantised_workspace_bytes(...); U stays in it where
  *   lora_apply_u_offset says, so that lora_grad takes (ws, ws_bytes) as its
- *   apply workspace.
+ *   apply workspace.  (Where U does not fit, LORA_DEVERR_CAPACITY, it is not
+ *   stored, and dB of a lora_grad over this workspace means nothing: the codes
+ *   lie behind U.)
  * Rows without an active slot equal the base product alone.
  * Errors: those of lora_apply, INVALID_ARG when W's widths are not the pool's. */
 size_t lora_apply_quantised_workspace_bytes(int32_t T, int32_t K, int32_t d_in, int32_t d_out,

@@ -702,18 +702,21 @@ int32_t check_weight(const lora_quantised_weight *w, const lora_pool_desc *pool)
   return LORA_OK;
 }
 
-// A quantised GEMM's buffers at the end of a workspace: fp32 partials, then
-// (tile forms) the rows' codes and scale bytes.
+// A quantised GEMM's buffers: fp32 partials and (tile forms) the rows' codes and
+// scale bytes.  They lie at the end of a workspace, but that each of the two
+// takes room at its start where the first `slab` bytes are free and hold it.
 struct QuantTail {
   GemmConfig cfg;
-  size_t partial, codes, scales, total;     // bytes
+  size_t partial, codes, scales;            // bytes
+  bool partial_in, codes_in;                // at the start
+  size_t total;                             // bytes at the end
 };
 
 int few_adapters(int32_t K, const lora_pool_desc *pool) {
   return K == 1 && pool->n_adapters <= 16 ? pool->n_adapters : 0;
 }
 
-QuantTail quant_tail(int32_t T, int few, int32_t d_k, int32_t d_n, int32_t dtype) {
+QuantTail quant_tail(int32_t T, int few, int32_t d_k, int32_t d_n, int32_t dtype, size_t slab) {
   QuantTail t{};
   t.cfg = choose_quantised_gemm(T > 0 ? T : 1, few, d_k, d_n, dtype);
   t.partial = align_up(gemm_partial_bytes(t.cfg, T, d_n));
@@ -721,31 +724,36 @@ QuantTail quant_tail(int32_t T, int few, int32_t d_k, int32_t d_n, int32_t dtype
     t.codes = align_up(size_t(T) * size_t(q_row_bytes(d_k)));
     t.scales = align_up(size_t(q_tile_rows(T)) * size_t(q_row_bytes(d_k) / kQBlock));
   }
-  t.total = t.partial + t.codes + t.scales;
+  const size_t rows = t.codes + t.scales;
+  t.partial_in = t.partial <= slab;
+  t.codes_in = (t.partial_in ? t.partial : 0) + rows <= slab;
+  t.total = (t.partial_in ? 0 : t.partial) + (t.codes_in ? 0 : rows);
   return t;
 }
 
 // The larger tail of the two forms: the size queries do not know the pool.
-size_t quant_tail_bytes(int32_t T, int32_t d_k, int32_t d_n, int32_t dtype) {
-  const size_t a = quant_tail(T, 1, d_k, d_n, dtype).total;
-  const size_t b = quant_tail(T, 0, d_k, d_n, dtype).total;
+size_t quant_tail_bytes(int32_t T, int32_t d_k, int32_t d_n, int32_t dtype, size_t slab) {
+  const size_t a = quant_tail(T, 1, d_k, d_n, dtype, slab).total;
+  const size_t b = quant_tail(T, 0, d_k, d_n, dtype, slab).total;
   return a > b ? a : b;
 }
 
-// Fills q for rows [T][d_k] times the weight's codes [d_n][..]; `tail` the
-// tail's memory.  For the tile forms q.g.X is where the rows' codes go.
+// Fills q for rows [T][d_k] times the weight's codes [d_n][..]; `ws` the
+// workspace, `tail` the tail's place in it.  For the tile forms q.g.X is where
+// the rows' codes go.
 void quantised_args(const QuantTail &t, const void *rows, int32_t T, int32_t d_k, int32_t d_n,
-                    const uint8_t *codes, const uint8_t *scale, char *tail, QGemmArgs &q) {
+                    const uint8_t *codes, const uint8_t *scale, char *ws, size_t tail, QGemmArgs &q) {
   q.g.X = rows; q.g.W = codes; q.g.M = T; q.g.N = d_n; q.g.Kd = d_k;
   q.g.k_split = t.cfg.k_split; q.g.sk_g = t.cfg.sk;
-  q.g.partial = reinterpret_cast<float *>(tail);
+  q.g.partial = reinterpret_cast<float *>(t.partial_in ? ws : ws + tail);
   q.lda = q.ldb = q_row_bytes(d_k);
   q.lsa = q_tile_rows(T);
   q.lsb = q_scale_bytes(d_k);
   q.sb = scale;
   if (t.cfg.kind != 4) {
-    q.g.X = tail + t.partial;
-    q.sa = reinterpret_cast<const uint8_t *>(tail) + t.partial + t.codes;
+    const char *at = ws + (t.codes_in ? (t.partial_in ? t.partial : 0) : tail + (t.partial_in ? 0 : t.partial));
+    q.g.X = at;
+    q.sa = reinterpret_cast<const uint8_t *>(at) + t.codes;
   }
 }
 
@@ -763,8 +771,9 @@ hipError_t run_quantised(const QuantTail &t, const void *rows, int32_t dtype, co
 }
 
 // The checks of the quantised apply, and its workspace: the head is laid out
-// as lora_apply's (lora_grad finds U in it), the tail ends where the workspace
-// does, so that its place needs no max_rank.
+// as lora_apply's (lora_grad finds U in it; the partials of lora_apply's product
+// are the room at its start), the tail ends where the workspace does, so that
+// its place needs no max_rank.
 struct QuantApply {
   QuantTail t;
   ApplyWs w;
@@ -783,14 +792,15 @@ int32_t quant_apply_args(const void *X, const lora_quantised_weight *W, void *Y,
   if (T == 0) return LORA_OK;
   if (!X || !Y || !W->q_t || !W->scale || !gates || !ws) return LORA_ERR_INVALID_ARG;
   if (Y == X || Y == W->q_t || Y == W->scale) return LORA_ERR_INVALID_ARG;
-  a.t = quant_tail(T, few_adapters(K, pool), pool->d_in, pool->d_out, pool->dtype);
+  const size_t slab = apply_layout(nullptr, 0, T, K, pool->d_in, pool->d_out, pool->dtype).partial_bytes;
+  a.t = quant_tail(T, few_adapters(K, pool), pool->d_in, pool->d_out, pool->dtype, slab);
   if (ws_bytes < a.t.total) return LORA_ERR_CAPACITY;
   const size_t head = a.head = (ws_bytes - a.t.total) / kAlign * kAlign;
   GemmConfig base;
   a.q = QGemmArgs{};
   if ((st = base_args(X, W->q_t, Y, T, K, pool, plan, ws, head, base, a.q.g)) != LORA_OK) return st;
   a.w = apply_layout(ws, head, T, K, pool->d_in, pool->d_out, pool->dtype);
-  quantised_args(a.t, X, T, pool->d_in, pool->d_out, W->q_t, W->scale, static_cast<char *>(ws) + head, a.q);
+  quantised_args(a.t, X, T, pool->d_in, pool->d_out, W->q_t, W->scale, static_cast<char *>(ws), head, a.q);
   return LORA_OK;
 }
 
@@ -836,7 +846,9 @@ int32_t lora_quantise_weight(const void *W_t, int32_t dtype, const lora_quantise
 size_t lora_apply_quantised_workspace_bytes(int32_t T, int32_t K, int32_t d_in, int32_t d_out,
                                             int32_t max_rank, int32_t dtype) {
   const size_t head = lora_apply_workspace_bytes(T, K, d_in, d_out, max_rank, dtype);
-  return head ? align_up(head) + quant_tail_bytes(T, d_in, d_out, dtype) : 0;
+  if (!head) return 0;
+  const size_t slab = apply_layout(nullptr, 0, T, K, d_in, d_out, dtype).partial_bytes;
+  return align_up(head) + quant_tail_bytes(T, d_in, d_out, dtype, slab);
 }
 
 int32_t lora_apply_quantised(const void *X, const lora_quantised_weight *W, void *Y, int32_t T,
@@ -906,7 +918,7 @@ int32_t lora_forward_quantised(const int32_t *ids, const float *gates, int32_t T
 size_t lora_grad_x_quantised_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out, int32_t dtype) {
   if (T < 0 || T > kMaxPairs || !dims_ok(d_in) || !dims_ok(d_out)) return 0;
   if (dtype != LORA_F32 && dtype != LORA_BF16) return 0;
-  const size_t n = quant_tail_bytes(T, d_out, d_in, dtype);
+  const size_t n = quant_tail_bytes(T, d_out, d_in, dtype, 0);
   return n > 0 ? n : kAlign;
 }
 
@@ -926,7 +938,7 @@ int32_t lora_grad_x_quantised(const void *dY, const lora_quantised_weight *W,
   if (grad_ws_bytes < lora_grad_workspace_bytes(T, K, pool->n_adapters, pool->d_in, pool->d_out,
                                                 max_rank, pool->dtype))
     return LORA_ERR_CAPACITY;
-  const QuantTail t = quant_tail(T, few_adapters(K, pool), pool->d_out, pool->d_in, pool->dtype);
+  const QuantTail t = quant_tail(T, few_adapters(K, pool), pool->d_out, pool->d_in, pool->dtype, 0);
   if (ws_bytes < t.total) return LORA_ERR_CAPACITY;
   const int64_t TK = int64_t(T) * K;
   const PlanView pv = plan_view(plan, TK, pool->n_adapters);
@@ -940,7 +952,7 @@ int32_t lora_grad_x_quantised(const void *dY, const lora_quantised_weight *W,
   q.g.ex.u_cap = TK * max_rank;
   if (t.cfg.fused) q.g.mask = keep_mask;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  quantised_args(t, dY, T, pool->d_out, pool->d_in, W->q, W->scale_t, static_cast<char *>(ws), q);
+  quantised_args(t, dY, T, pool->d_out, pool->d_in, W->q, W->scale_t, static_cast<char *>(ws), 0, q);
   hipError_t e = run_quantised(t, dY, pool->dtype, q, s);
   if (e == hipSuccess && !t.cfg.fused)
     e = launch_grad_x_epilogue(t.cfg, quant_epilogue_args(q), pool->dtype, keep_mask, s);

@@ -72,3 +72,35 @@ def test_codes_past_the_end_are_zero(d, dtype):
     v, sb = Q.quantise_rows(x.double().cpu().numpy())
     assert np.array_equal(c.view(torch.float8_e4m3fn).float().cpu().numpy(), v, equal_nan=True)
     assert np.array_equal(s.cpu().numpy()[:, :sb.shape[1]], sb) and not c[:, d:].any()
+
+
+FORMS = [
+    (40, 1, 576, 704, {}),
+    (130, 2, 1344, 320, {"dtype": "f32", "mask": True}),
+    (300, 2, 640, 1344, {"mask": True}),
+    (300, 1, 4288, 1984, {}),
+    (1030, 1, 256, 1536, {"runs": True, "hi": 70}),
+    (4096, 1, 192, 4096, {"mask": True}),
+]
+
+
+@pytest.mark.parametrize("T,K,d_in,d_out,extra", FORMS)
+def test_workspace_of_the_asked_size_and_of_more(T, K, d_in, d_out, extra):
+    """Canaries around a workspace of the size the query gives, a longer one,
+    and gradients over both."""
+    w = workload(T, K, d_in, d_out, **extra)
+    got = []
+    for more in (0, 100 * 256 + 64):
+        L = Layer(w)
+        n, pad = L.ws.numel() + more, 4096
+        buf = torch.full((n + 2 * pad,), 0x3c, dtype=torch.uint8, device="cuda")
+        L.ws = buf[pad:pad + n]
+        L.forward()
+        dA, dB, dX = L.backward()
+        torch.cuda.synchronize()
+        assert (buf[:pad] == 0x3c).all() and (buf[pad + n:] == 0x3c).all()
+        got.append((L.Y, dA.nan_to_num(7.0), dB.nan_to_num(7.0), dX, torch.from_numpy(L.U())))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    y, ty, x, tx = expected(w)
+    check(got[0][0], y, ty, "Y")
+    check(got[0][3], x, tx, "dX")
