@@ -104,3 +104,55 @@ def test_workspace_of_the_asked_size_and_of_more(T, K, d_in, d_out, extra):
     y, ty, x, tx = expected(w)
     check(got[0][0], y, ty, "Y")
     check(got[0][3], x, tx, "dX")
+
+
+@pytest.mark.parametrize("T,K,d_in,d_out,extra", FORMS + [(2500, 1, 512, 768, {"mask": True, "hi": 40})])
+def test_captured_and_beside_another_stream(T, K, d_in, d_out, extra):
+    """Forward, gradients and dX of every form captured and replayed, and two
+    layers at once on two streams, against eager calls."""
+    w = workload(T, K, d_in, d_out, **extra)
+
+    class Whole(Layer):
+        def __init__(self, w):
+            super().__init__(w)
+            self.dA, self.dB, self.gws = self.grad_buffers()
+            self.dX, self.xws = self.grad_x_quantised_buffers()
+            self.out = (self.Y, self.dA, self.dB, self.dX)
+
+        def step(self):
+            self.forward()
+            self.run_grad(self.dA, self.dB, self.gws)
+            self.run_grad_x_quantised(self.W8, self.gws, self.dX, self.xws)
+
+        def clear(self):
+            for t in self.out:
+                t.fill_(7.0)
+
+    def equal(a, b):
+        return all(torch.equal(x, y) for x, y in zip(a.out, b))
+
+    L, M = Whole(w), Whole(w)
+    L.clear()
+    L.step()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in L.out]
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for x in (L, M):
+        x.clear()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(s1):
+            L.step()
+        with torch.cuda.stream(s2):
+            M.step()
+    torch.cuda.synchronize()
+    assert equal(L, want) and equal(M, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        L.step()
+    for i in range(3):
+        L.clear()
+        M.step()                                     # eager work between the replays
+        g.replay()
+        torch.cuda.synchronize()
+        assert equal(L, want), i
