@@ -616,11 +616,20 @@ def lora_grad_x_quantised(dY, W: QuantisedWeight, keep_mask, T: int, K: int, poo
 NS_COEF = (3.4445, -4.7750, 2.0315)     # quintic coefficients whose slope at 0 is largest
 
 
+def _check_pages(pool: Pool, t, d: int, size: int):
+    """Pages that a call takes as [n_pages][d] elements of `size` bytes."""
+    n = int(pool.desc.n_pages)
+    if tuple(t.shape) != (n, d) or t.element_size() != size or not t.is_contiguous():
+        raise ValueError(f"expected contiguous pages [{n}][{d}] of {size}-byte elements, got {tuple(t.shape)}")
+
+
 class FactorUpdate:
     """One factor's buffers of lora_orthogonal_step: its pages (the pool's own
     a_pages or b_pages), float32 gradient, momentum and (or None) master pages."""
 
     def __init__(self, pages, grad, momentum, master, lr: float, decay: float = 0.0):
+        if not pages.is_contiguous():
+            raise ValueError("expected contiguous pages")
         for t in (grad, momentum, master):
             if t is not None and (t.shape != pages.shape or t.element_size() != 4 or not t.is_contiguous()):
                 raise ValueError(f"expected contiguous float32 pages {tuple(pages.shape)}, got {tuple(t.shape)}")
@@ -639,6 +648,8 @@ def lora_orthogonalise_workspace_bytes(M: int, max_rank: int, d: int) -> int:
 
 def lora_orthogonalise(pool: Pool, adapters, M: int, max_rank: int, src_pages, out_pages, d: int,
                        steps: int, coef, eps: float, ws, out_rank=None, stream=None):
+    for t in (src_pages, out_pages):
+        _check_pages(pool, t, d, 4)
     _check("lora_orthogonalise", lib().lora_orthogonalise(
         pool.ref, _ptr(adapters), M, max_rank, _ptr(src_pages), _ptr(out_pages), d, steps,
         (_F32 * 3)(*coef), float(eps), _ptr(out_rank), _ptr(ws), ws.numel() * ws.element_size(),
@@ -652,6 +663,8 @@ def lora_orthogonal_step_workspace_bytes(M: int, max_rank: int, d_in: int, d_out
 def lora_orthogonal_step(pool: Pool, adapters, M: int, max_rank: int, a: FactorUpdate,
                          b: FactorUpdate, momentum: float, nesterov: bool, steps: int, coef,
                          eps: float, ws, out_rank=None, stream=None):
+    for f, d in ((a, pool.d_in), (b, pool.d_out)):
+        _check_pages(pool, f.tensors[0], d, 2 if pool.dtype == LORA_BF16 else 4)
     _check("lora_orthogonal_step", lib().lora_orthogonal_step(
         pool.ref, _ptr(adapters), M, max_rank, a.ref, b.ref, float(momentum), int(nesterov), steps,
         (_F32 * 3)(*coef), float(eps), _ptr(out_rank), _ptr(ws), ws.numel() * ws.element_size(),
