@@ -640,6 +640,13 @@ GemmConfig choose_quantised_gemm(int T, int few, int d_in, int d_out, int dtype)
   // (4096 x 4096 -> 2048) 81 against 105, 153 and 83 (the input gradient of
   // 4234 x 2304 -> 10560) 90 less; but 24 and 36 (2048 x 4544 -> 640) 78
   // against 60, 32 and 64 (2048 x 8192 -> 1024) 122 against 81.
+  // (few counts the pool's adapters: the batch's own are known on the device
+  // alone.)  From 256 tiles on the adapters are not asked for: in runs of four
+  // 8192 x 11008 -> 4096 takes 400 us fused and 824 split, with 64 adapters of
+  // ranks 2 .. 16 in any order 8192 x 4096 -> 4096 takes 353 and 388.  Blocks
+  // that need q_expand_wide turn that round (two slots of rank 16: 488 and 426;
+  // ranks 2 .. 64 of 16 adapters in any order: 536 and 461), but ranks are
+  // known on the device alone too.
   const int64_t big = int64_t((T + 255) / 256) * ((d_out + 255) / 256);
   if (big >= 256 ||
       (few > 0 && T >= 1024 && big * (6 * kb + 230) + 3000 >= 1100 * int64_t(kb) + 500 * few)) {

@@ -14,9 +14,10 @@
 // eigenvalue 1e-6, fp32 would know it to 6 %, and the steps amplify small
 // values (3.44 each at the usual coefficients).  G and the r x r products
 // therefore run in fp64 (v_mfma_f64_16x16x4_f64; products of fp32 inputs are
-// exact there): against the steps in 64 bits the result is off by 1e-6 where
-// an fp32 Gram matrix gives 2e-5 .. 2e-4, no more than the steps themselves
-// run in fp32 (5e-6 at rank 128).  Q N is fp32 (v_mfma_f32_16x16x4_f32).
+// exact there): against the steps in 64 bits the result is off by 1.3e-7 (four
+// of rank 16) and 2.6e-7 (64 of ranks 8 .. 128) of its norm, where an fp32 Gram
+// matrix gives 2e-5 .. 2e-4 and the steps themselves run in fp32 1.2e-6 and
+// 4.6e-6.  Q N is fp32 (v_mfma_f32_16x16x4_f32).
 //
 // Launches: the Gram partials over column chunks (the optimiser step updates
 // the momentum in the same pass); the steps, one workgroup per matrix of rank
@@ -278,7 +279,8 @@ __device__ __forceinline__ void store_inv(OrthRec &rec, double inv) {
 // 4 v + l / 16, column l % 16; operand k of lane l is row l % 16, column 4 k +
 // l / 16.  For a symmetric matrix these are the same value, so a result is the
 // next product's operand as it stands: the steps are MFMAs of one wave and
-// nothing else (four rank-16 matrices, five steps: 6.2 -> 2 us).
+// nothing else (a step: 1.2 -> 0.5 us; the launch of four rank-16 matrices,
+// five steps with the sum of the partials before them: 5.8 .. 6.4 us).
 __device__ __forceinline__ f64x4_t sym16(const f64x4_t &A, const f64x4_t &B) {
   f64x4_t c = {0, 0, 0, 0};
 #pragma unroll
