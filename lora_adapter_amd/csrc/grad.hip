@@ -248,8 +248,9 @@ __global__ __launch_bounds__(kGradThreads) void seg_outer_both_kernel(SegOuterAr
 // next step's rows in flight meanwhile.  The fp32 coefficients are split
 // exactly into three bf16 parts (three MFMAs), which keeps all their 24 bits:
 // with two the pages were off by 2.5e-6 of their norm at 8192 pairs, more than
-// the fp32 sums themselves (3e-7), and the third costs no time (the kernel is
-// bound by the rows it streams).
+// the fp32 sums themselves (3e-7); the third costs 1 to 3 % of lora_grad (8192
+// tokens of 8 adapters, 4096 -> 11008: 97.5 -> 99.2 us; the kernel is bound by
+// the rows it streams).
 // Workgroup barrier for LDS only: the next step's token-row loads and the
 // partial stores stay in flight across it (__syncthreads() would wait for
 // every outstanding load and store).
@@ -316,6 +317,7 @@ void seg_outer_mfma_kernel(SegOuterArgs a) {
   __shared__ __attribute__((aligned(16))) uint16_t s_z[kOuterK][ZP];
   __shared__ uint64_t s_start[4];          // segment starts of the chunk, one bit per pair
   __shared__ int s_cnt[4];
+  __shared__ int s_nf[4];                  // a wave's pairs have a non-finite coefficient
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int q = blockIdx.y;
   const int pbeg = q * kGradPairChunk;
@@ -468,6 +470,11 @@ void seg_outer_mfma_kernel(SegOuterArgs a) {
 #pragma unroll
     for (int jj = 0; jj < RB; ++jj)
       if (valid && jj < nr) cf[jj] = c[jj];
+    float z = 0.f;                             // NaN if one is not finite
+#pragma unroll
+    for (int jj = 0; jj < RB; ++jj) z = fmaf(cf[jj], 0.f, z);
+    const uint64_t nf = __ballot(z != z);
+    if (lane == 0) s_nf[wave] = nf != 0;
     s_rk[tid] = uint16_t(min(max(rk, 0), 0xffff));
 #pragma unroll
     for (int jj = 0; jj < RB; ++jj) {
@@ -484,7 +491,8 @@ void seg_outer_mfma_kernel(SegOuterArgs a) {
     g_rows(nr0);
     g_put();
   }
-  lds_bar();                                             // s_rk, s_ah, s_al, s_ar, s_gb
+  lds_bar();                                             // s_rk, s_ah, s_al, s_ar, s_nf, s_gb
+  const bool nonfinite = __builtin_amdgcn_readfirstlane(s_nf[0] | s_nf[1] | s_nf[2] | s_nf[3]) != 0;
 
   for (int l_beg = 0; l_beg < n; ++s) {
     const int l_end = l_beg == 0 ? l_end0 : next_start(s_start, l_beg, n);
@@ -533,9 +541,11 @@ void seg_outer_mfma_kernel(SegOuterArgs a) {
         __builtin_memcpy(&ahi, &s_ah[lane & 15][ka], 16);
         __builtin_memcpy(&alo, &s_al[lane & 15][ka], 16);
         __builtin_memcpy(&arest, &s_ar[lane & 15][ka], 16);
-        if (k0 < l_beg || k0 + kOuterK > l_end) {
+        if (nonfinite && (k0 < l_beg || k0 + kOuterK > l_end)) {
           // pairs of other segments: zero like their rows (an infinity or a
-          // NaN of another adapter's coefficients times those is NaN)
+          // NaN of another adapter's coefficients times those is NaN).  Only in
+          // chunks that have one: in every edge step it cost 5 % of lora_grad at
+          // 4000 tokens of 64 adapters
           auto keep = [&](bf16x8_t &v) {
             uint32_t w[4];
             __builtin_memcpy(w, &v, 16);
