@@ -237,7 +237,9 @@ __device__ __forceinline__ void lds_dma4(const void *gptr, uint32_t lds) {
 // 16, or several slots per token): MFMA passes of 16 rank rows, one slot and
 // one adapter at a time, into accumulators of their own, then added to the
 // staged base product (times the keep mask with kMask), rounded and stored.
-// Returns the blocks left to expand_nonfinite.
+// Returns the blocks left to expand_nonfinite (whose test of every B fragment
+// takes 3 to 4 % of a call whose adapters are in any order: 8192 x 4096 -> 4096,
+// 16 adapters of ranks 2 .. 64 510 -> 532 us; in runs of rank 64 271 -> 272).
 // One rolled loop over the blocks, apart from the fused epilogue: inside its
 // unrolled blocks the same code slowed the common ones (8192 x 4096 -> 11008,
 // rank 16: 357 -> 449 us).

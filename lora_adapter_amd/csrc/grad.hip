@@ -182,11 +182,13 @@ __device__ __forceinline__ void seg_outer_partial_wg(const SegOuterArgs &a, int 
         for (int u = 0; u < kGradAhead; ++u) {
           float zv[CPL];
           z[u].get(zv);
-          const bool in = l0 + u < l_end;
+          // all bits or none of a value, as its mask byte (0 or 1) and the
+          // segment's end say: no infinity or NaN passes, and two operations
+          const uint32_t in = l0 + u < l_end ? ~0u : 0u;
 #pragma unroll
           for (int c = 0; c < CPL; ++c) {
-            const bool keep = !kMask || ((m[u] >> (8 * c)) & 0xffu) != 0;
-            zv[c] = in && keep ? zv[c] : 0.f;
+            const uint32_t keep = kMask ? uint32_t(__builtin_amdgcn_sbfe(int(m[u] & in), 8 * c, 1)) : in;
+            zv[c] = __uint_as_float(__float_as_uint(zv[c]) & keep);
           }
           const float *cf = s_cf[min(l0 + u, l_end - 1)];
 #pragma unroll
