@@ -472,21 +472,20 @@ void seg_outer_mfma_kernel(SegOuterArgs a) {
 #pragma unroll
     for (int jj = 0; jj < RB; ++jj)
       if (valid && jj < nr) cf[jj] = c[jj];
-    float z = 0.f;                             // NaN if one is not finite
-#pragma unroll
-    for (int jj = 0; jj < RB; ++jj) z = fmaf(cf[jj], 0.f, z);
-    const uint64_t nf = __ballot(z != z);
-    if (lane == 0) s_nf[wave] = nf != 0;
+    float z = 0.f;                             // NaN if a first part is not finite
     s_rk[tid] = uint16_t(min(max(rk, 0), 0xffff));
 #pragma unroll
     for (int jj = 0; jj < RB; ++jj) {
       const uint16_t h = f2bf(cf[jj]);
       s_ah[jj][tid] = h;
+      z = fmaf(bf2f(h), 0.f, z);
       const float rest = cf[jj] - bf2f(h);
       const uint16_t l = f2bf(rest);
       s_al[jj][tid] = l;
       s_ar[jj][tid] = f2bf(rest - bf2f(l));
     }
+    const uint64_t nf = __ballot(z != z);
+    if (lane == 0) s_nf[wave] = nf != 0;
   }
   int s = seg_of_wg(a.plan.seg_off, S, pbeg, s_cnt);
   if (g0) {
