@@ -643,6 +643,130 @@ int32_t lora_orthogonal_step(const lora_pool_desc *pool, const int32_t *adapters
                              int32_t steps, const float *coef, float eps, int32_t *out_rank, void *ws,
                              size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------- gated feed-forward
+ * Two adapted projections of the same rows, an activation and their product
+ * ([S-LoRA] 批处理, [LoRAFusion] 解决什么真问题: adapters sit on the frozen
+ * projections; the pages do not give the block's own formula):
+ *   g = X.W_gate + adapters,  u = X.W_up + adapters,  H = round( act(g) . u )
+ * with each projection as in lora_apply, but that g and u stay float32 up to
+ * the one rounding of H.  The two pools share routing and page table: rank,
+ * page_start and page_ids are the same arrays, and dtype, widths and counts
+ * are equal (INVALID_ARG otherwise), so that one plan serves both; factors and
+ * scales are each one's own.  The keep mask is that of the block's input, for
+ * both.  d_out is the width of H.
+ *   activation   LORA_ACT_SILU  x sigmoid(x);  LORA_ACT_GELU  x Phi(x);
+ *                LORA_ACT_GELU_TANH  x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2
+ *   H            [T][d_out] dtype.
+ *   pre_gate, pre_up  [T][d_out] dtype, both or neither: g and u rounded once,
+ *                what lora_gated_grad reads.
+ *   ws_gate, ws_up    a workspace of lora_apply_workspace_bytes each; each
+ *                projection's U stays in its own, where lora_grad finds it.
+ * Other arguments as for lora_apply.  No output may be another buffer of the
+ * call.  lora_gated_forward = lora_plan then lora_gated_apply, as one call
+ * with fewer launches (plan, U, H, pre_gate and pre_up are the same bit for bit).
+ * Errors: those of lora_apply and lora_forward. */
+#define LORA_ACT_SILU 0
+#define LORA_ACT_GELU 1
+#define LORA_ACT_GELU_TANH 2
+int32_t lora_gated_apply(const void *X, const void *W_gate_t, const void *W_up_t, int32_t activation,
+                         void *H, void *pre_gate, void *pre_up, int32_t T, int32_t K,
+                         const float *gates, const uint8_t *keep_mask, float keep_scale,
+                         const lora_pool_desc *gate, const lora_pool_desc *up, const void *plan,
+                         void *ws_gate, size_t ws_gate_bytes, void *ws_up, size_t ws_up_bytes,
+                         void *stream);
+int32_t lora_gated_forward(const int32_t *ids, const float *gates, int32_t T, int32_t K,
+                           const void *X, const void *W_gate_t, const void *W_up_t,
+                           int32_t activation, void *H, void *pre_gate, void *pre_up,
+                           const uint8_t *keep_mask, float keep_scale, const lora_pool_desc *gate,
+                           const lora_pool_desc *up, void *plan, size_t plan_bytes, void *ws_gate,
+                           size_t ws_gate_bytes, void *ws_up, size_t ws_up_bytes, void *stream);
+/* The block's backward (the derivative of the forward above):
+ *   d_gate = round( dH . u . act'(g) ),  d_up = round( dH . act(g) )
+ *   dX = round( d_gate.W_gate^T + d_up.W_up^T + m . (G_gate.A_gate + G_up.A_up) ),
+ *   G[u_off[p]+j] = g_p . s_a . kappa . (d_t . B_a[j])  of each projection
+ * with g and u as the forward stored them.  The factors' gradients are
+ * lora_grad's, once for each projection, with d_gate or d_up as its dY and
+ * ws_gate or ws_up as its apply workspace.
+ *   dH [T][d_out] dtype; pre_gate, pre_up as stored; W_gate, W_up [d_in][d_out]:
+ *   the weights in their mathematical orientation (lora_transpose), unused
+ *   and possibly NULL without dX; keep_mask, keep_scale, gates, plan as for the
+ *   forward; max_rank bounds every used adapter's rank (LORA_DEVERR_CAPACITY if
+ *   not); d_gate, d_up [T][d_out] dtype, may be pre_gate, pre_up (in place); dX
+ *   [T][d_in] dtype, or NULL.  ws >= lora_gated_grad_workspace_bytes(...).
+ * Errors: INVALID_ARG, UNSUPPORTED, CAPACITY, DEVICE. */
+size_t lora_gated_grad_workspace_bytes(int32_t T, int32_t K, int32_t d_in, int32_t d_out,
+                                       int32_t max_rank, int32_t dtype);
+int32_t lora_gated_grad(const void *dH, const void *pre_gate, const void *pre_up, int32_t activation,
+                        const void *W_gate, const void *W_up, const uint8_t *keep_mask,
+                        float keep_scale, int32_t T, int32_t K, const float *gates,
+                        const lora_pool_desc *gate, const lora_pool_desc *up, const void *plan,
+                        int32_t max_rank, void *d_gate, void *d_up, void *dX, void *ws,
+                        size_t ws_bytes, void *stream);
+
+/* -------------------------------------------------------- cross entropy
+ * Softmax cross entropy of the tokens' targets over a vocabulary of V, from
+ * the hidden states and the frozen output weight, with the gradient of the
+ * hidden states: where a fine-tuning step's backward begins ([LoRAFusion]
+ * 解决什么真问题; the pages name no loss).  The logits [T][V] are never held:
+ *   l[v] = logit_scale . sum_i X[t][i].W_t[v][i]
+ *   loss[t] = w[t] . (log sum_v e^{l[v]} - l[y[t]])
+ *   dX[t] = round( w[t] . logit_scale . (sum_v softmax(l)[v].W_t[v] - W_t[y[t]]) )
+ *   X [T][d], W_t [V][d] dtype, 16-byte aligned; any V >= 1, d a multiple of 64;
+ *   targets [T] int32: below 0 ignored.  V or more: the token's loss is NaN,
+ *   and it is ignored otherwise.  weights [T] float32 or NULL (1 each): a mean
+ *   over a job's tokens is 1 / their number; a weight of 0 ignores the token.
+ *   Ignored tokens cost nothing, have a loss of 0 and a gradient of 0, whatever
+ *   their X holds.  logit_scale is finite and not 0.
+ *   loss [T] float32; dX [T][d] dtype, or NULL for the loss alone.
+ *   ws >= lora_cross_entropy_workspace_bytes(..., dX != NULL): tokens are taken
+ *   in blocks whose exponentials (dtype) take at most 512 MiB.
+ * A logit of +infinity or NaN makes its token's loss and gradient NaN, and no
+ * other token's.  At most 2^20 tokens and V of 2^24 (UNSUPPORTED).  Results are
+ * deterministic.
+ * Errors: INVALID_ARG (null, alignment, an output that is an input, sizes),
+ * UNSUPPORTED, CAPACITY, DEVICE. */
+size_t lora_cross_entropy_workspace_bytes(int32_t T, int32_t V, int32_t d, int32_t dtype,
+                                          int32_t with_grad);
+int32_t lora_cross_entropy(const void *X, const void *W_t, int32_t dtype, int32_t T, int32_t V,
+                           int32_t d, const int32_t *targets, const float *weights,
+                           float logit_scale, float *loss, void *dX, void *ws, size_t ws_bytes,
+                           void *stream);
+
+/* ------------------------------------------------------- gradient clipping
+ * Norms of adapters' gradients over all their layers, and clipping: between
+ * lora_grad of every layer and the optimiser's step.  Each adapter is a
+ * training job of its own, so each has a norm of its own:
+ *   norm[m] = sqrt( sum over layers of |dA|^2 + |dB|^2, pages of adapters[m] )
+ *   norm[M] = sqrt( sum_m norm[m]^2 )
+ *   out = grad . min(1, max_norm / n),  n = together ? norm[M] : norm[m]
+ * A norm that is not finite clips nothing: the gradients go through as they
+ * are, and norm tells.
+ *   layers    host array [n_layers]: a pool (its page table alone is read, and
+ *             its widths) and float32 pages as lora_grad writes them, 16-byte
+ *             aligned.  dA_out may be dA_pages (in place; rows whose factor is 1
+ *             are then not written) or other pages of the same layout; dB_out so.
+ *             Pages of adapters that are not listed are neither read nor written.
+ *   adapters  [M] int32 device; in a layer, one that is out of range there, of
+ *             rank 0 or above max_rank, with an inconsistent page table, or
+ *             listed before is skipped (its norm gets nothing from that layer).
+ *   max_norm > 0, INFINITY for the norms alone;  norm [M + 1] float32 device.
+ * Squares and sums are float64, in a fixed order.  At most 16384 adapters and
+ * 1024 layers (UNSUPPORTED).  No two outputs, and no output and another
+ * gradient, may overlap.  ws >= lora_clip_grad_workspace_bytes(...).
+ * Errors: INVALID_ARG (null, alignment, overlap, sizes), UNSUPPORTED, CAPACITY,
+ * DEVICE. */
+typedef struct {
+  lora_pool_desc pool;
+  const float *dA_pages;      /* [n_pages][d_in]                               */
+  const float *dB_pages;      /* [n_pages][d_out]                              */
+  float *dA_out;              /* [n_pages][d_in]                               */
+  float *dB_out;              /* [n_pages][d_out]                              */
+} lora_grad_desc;             /* host struct, device pointers                  */
+size_t lora_clip_grad_workspace_bytes(int32_t n_layers, int32_t M, int32_t max_rank);
+int32_t lora_clip_grad(const lora_grad_desc *layers, int32_t n_layers, const int32_t *adapters,
+                       int32_t M, int32_t max_rank, float max_norm, int32_t together, float *norm,
+                       void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -42,6 +42,9 @@ EXPORTS = (
     "lora_forward_quantised", "lora_grad_x_quantised_workspace_bytes", "lora_grad_x_quantised",
     "lora_orthogonalise_workspace_bytes", "lora_orthogonalise",
     "lora_orthogonal_step_workspace_bytes", "lora_orthogonal_step",
+    "lora_gated_apply", "lora_gated_forward", "lora_gated_grad_workspace_bytes", "lora_gated_grad",
+    "lora_cross_entropy_workspace_bytes", "lora_cross_entropy", "lora_clip_grad_workspace_bytes",
+    "lora_clip_grad",
 )
 
 
@@ -78,6 +81,11 @@ class FactorUpdateDesc(ctypes.Structure):
     _fields_ = [("pages", ctypes.c_void_p), ("master", ctypes.c_void_p),
                 ("momentum", ctypes.c_void_p), ("grad", ctypes.c_void_p),
                 ("lr", ctypes.c_float), ("decay", ctypes.c_float)]
+
+
+class GradDesc(ctypes.Structure):
+    _fields_ = [("pool", PoolDesc), ("dA_pages", ctypes.c_void_p), ("dB_pages", ctypes.c_void_p),
+                ("dA_out", ctypes.c_void_p), ("dB_out", ctypes.c_void_p)]
 
 
 class ResidencyConfig(ctypes.Structure):
@@ -165,6 +173,17 @@ _PROTOS = {
     "lora_orthogonal_step": (_I32, [_PD, _VP, _I32, _I32, ctypes.POINTER(FactorUpdateDesc),
                                     ctypes.POINTER(FactorUpdateDesc), _F32, _I32, _I32,
                                     ctypes.POINTER(_F32), _F32, _VP, _VP, _SZ, _VP]),
+    "lora_gated_apply": (_I32, [_VP, _VP, _VP, _I32, _VP, _VP, _VP, _I32, _I32, _VP, _VP, _F32, _PD, _PD,
+                                _VP, _VP, _SZ, _VP, _SZ, _VP]),
+    "lora_gated_forward": (_I32, [_VP, _VP, _I32, _I32, _VP, _VP, _VP, _I32, _VP, _VP, _VP, _VP, _F32,
+                                  _PD, _PD, _VP, _SZ, _VP, _SZ, _VP, _SZ, _VP]),
+    "lora_gated_grad_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32]),
+    "lora_gated_grad": (_I32, [_VP, _VP, _VP, _I32, _VP, _VP, _VP, _F32, _I32, _I32, _VP, _PD, _PD, _VP,
+                               _I32, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "lora_cross_entropy_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32, _I32]),
+    "lora_cross_entropy": (_I32, [_VP, _VP, _I32, _I32, _I32, _I32, _VP, _VP, _F32, _VP, _VP, _VP, _SZ, _VP]),
+    "lora_clip_grad_workspace_bytes": (_SZ, [_I32, _I32, _I32]),
+    "lora_clip_grad": (_I32, [ctypes.POINTER(GradDesc), _I32, _VP, _I32, _I32, _F32, _I32, _VP, _VP, _SZ, _VP]),
 }
 
 
@@ -669,3 +688,107 @@ def lora_orthogonal_step(pool: Pool, adapters, M: int, max_rank: int, a: FactorU
         pool.ref, _ptr(adapters), M, max_rank, a.ref, b.ref, float(momentum), int(nesterov), steps,
         (_F32 * 3)(*coef), float(eps), _ptr(out_rank), _ptr(ws), ws.numel() * ws.element_size(),
         _stream(stream)))
+
+
+# ---------------------------------------------------------------- gated feed-forward
+
+LORA_ACT_SILU, LORA_ACT_GELU, LORA_ACT_GELU_TANH = range(3)
+
+
+def _size(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _check_rows(pool: Pool, T: int, **tensors):
+    """Contiguous rows [T][width] of the pool's dtype: name=(tensor or None, width)."""
+    size = 2 if pool.dtype == LORA_BF16 else 4
+    for name, (t, width) in tensors.items():
+        if t is not None and (tuple(t.shape) != (T, width) or t.element_size() != size or not t.is_contiguous()):
+            raise ValueError(f"{name}: expected contiguous [{T}][{width}] of {size}-byte elements, got {tuple(t.shape)}")
+
+
+def lora_gated_apply(X, W_gate_t, W_up_t, activation: int, H, pre_gate, pre_up, T: int, K: int, gates,
+                     keep_mask, keep_scale: float, gate: Pool, up: Pool, plan, ws_gate, ws_up, stream=None):
+    F = gate.d_out
+    _check_rows(gate, T, X=(X, gate.d_in), H=(H, F), pre_gate=(pre_gate, F), pre_up=(pre_up, F))
+    _check_rows(gate, F, W_gate_t=(W_gate_t, gate.d_in), W_up_t=(W_up_t, gate.d_in))
+    _check("lora_gated_apply", lib().lora_gated_apply(
+        _ptr(X), _ptr(W_gate_t), _ptr(W_up_t), activation, _ptr(H), _ptr(pre_gate), _ptr(pre_up), T, K,
+        _ptr(gates), _ptr(keep_mask), float(keep_scale), gate.ref, up.ref, _ptr(plan), _ptr(ws_gate),
+        _size(ws_gate), _ptr(ws_up), _size(ws_up), _stream(stream)))
+
+
+def lora_gated_forward(ids, gates, T: int, K: int, X, W_gate_t, W_up_t, activation: int, H, pre_gate, pre_up,
+                       keep_mask, keep_scale: float, gate: Pool, up: Pool, plan, ws_gate, ws_up, stream=None):
+    F = gate.d_out
+    _check_rows(gate, T, X=(X, gate.d_in), H=(H, F), pre_gate=(pre_gate, F), pre_up=(pre_up, F))
+    _check_rows(gate, F, W_gate_t=(W_gate_t, gate.d_in), W_up_t=(W_up_t, gate.d_in))
+    _check("lora_gated_forward", lib().lora_gated_forward(
+        _ptr(ids), _ptr(gates), T, K, _ptr(X), _ptr(W_gate_t), _ptr(W_up_t), activation, _ptr(H),
+        _ptr(pre_gate), _ptr(pre_up), _ptr(keep_mask), float(keep_scale), gate.ref, up.ref, _ptr(plan),
+        _size(plan), _ptr(ws_gate), _size(ws_gate), _ptr(ws_up), _size(ws_up), _stream(stream)))
+
+
+def lora_gated_grad_workspace_bytes(T: int, K: int, d_in: int, d_out: int, max_rank: int, dtype: int) -> int:
+    return int(lib().lora_gated_grad_workspace_bytes(T, K, d_in, d_out, max_rank, dtype))
+
+
+def lora_gated_grad(dH, pre_gate, pre_up, activation: int, W_gate, W_up, keep_mask, keep_scale: float, T: int,
+                    K: int, gates, gate: Pool, up: Pool, plan, max_rank: int, d_gate, d_up, dX, ws, stream=None):
+    F = gate.d_out
+    _check_rows(gate, T, dH=(dH, F), pre_gate=(pre_gate, F), pre_up=(pre_up, F), d_gate=(d_gate, F),
+                d_up=(d_up, F), dX=(dX, gate.d_in))
+    _check_rows(gate, gate.d_in, W_gate=(W_gate, F), W_up=(W_up, F))
+    _check("lora_gated_grad", lib().lora_gated_grad(
+        _ptr(dH), _ptr(pre_gate), _ptr(pre_up), activation, _ptr(W_gate), _ptr(W_up), _ptr(keep_mask),
+        float(keep_scale), T, K, _ptr(gates), gate.ref, up.ref, _ptr(plan), max_rank, _ptr(d_gate),
+        _ptr(d_up), _ptr(dX), _ptr(ws), _size(ws), _stream(stream)))
+
+
+# ---------------------------------------------------------------- cross entropy
+
+def lora_cross_entropy_workspace_bytes(T: int, V: int, d: int, dtype: int, with_grad: bool = True) -> int:
+    return int(lib().lora_cross_entropy_workspace_bytes(T, V, d, dtype, int(with_grad)))
+
+
+def lora_cross_entropy(X, W_t, dtype: int, T: int, V: int, d: int, targets, weights, logit_scale: float, loss,
+                       dX, ws, stream=None):
+    """weights and dX may be None (1 for each token; the loss alone)."""
+    size = 2 if dtype == LORA_BF16 else 4
+    for name, t, shape, n in (("X", X, (T, d), size), ("W_t", W_t, (V, d), size), ("targets", targets, (T,), 4),
+                              ("weights", weights, (T,), 4), ("loss", loss, (T,), 4), ("dX", dX, (T, d), size)):
+        if t is not None and (tuple(t.shape) != shape or t.element_size() != n or not t.is_contiguous()):
+            raise ValueError(f"{name}: expected contiguous {list(shape)} of {n}-byte elements, got {tuple(t.shape)}")
+    _check("lora_cross_entropy", lib().lora_cross_entropy(
+        _ptr(X), _ptr(W_t), dtype, T, V, d, _ptr(targets), _ptr(weights), float(logit_scale), _ptr(loss),
+        _ptr(dX), _ptr(ws), _size(ws), _stream(stream)))
+
+
+# ---------------------------------------------------------------- gradient clipping
+
+class GradLayers:
+    """The gradient pages of many layers for lora_clip_grad: entries (pool, dA,
+    dB) to clip in place, or (pool, dA, dB, dA_out, dB_out)."""
+
+    def __init__(self, layers):
+        self.layers = [tuple(e) if len(e) == 5 else (e[0], e[1], e[2], e[1], e[2]) for e in layers]
+        self.n = len(self.layers)
+        self.desc = (GradDesc * max(self.n, 1))()
+        for d, (pool, a, b, oa, ob) in zip(self.desc, self.layers):
+            for t, width in ((a, pool.d_in), (b, pool.d_out), (oa, pool.d_in), (ob, pool.d_out)):
+                _check_pages(pool, t, width, 4)
+            d.pool = pool.desc
+            d.dA_pages, d.dB_pages, d.dA_out, d.dB_out = _ptr(a), _ptr(b), _ptr(oa), _ptr(ob)
+
+
+def lora_clip_grad_workspace_bytes(layers: GradLayers, M: int, max_rank: int) -> int:
+    return int(lib().lora_clip_grad_workspace_bytes(layers.n, M, max_rank))
+
+
+def lora_clip_grad(layers: GradLayers, adapters, M: int, max_rank: int, max_norm: float, together: bool, norm,
+                   ws, stream=None):
+    if norm.numel() != M + 1 or norm.element_size() != 4 or not norm.is_contiguous():
+        raise ValueError(f"norm: expected {M + 1} contiguous float32, got {tuple(norm.shape)}")
+    _check("lora_clip_grad", lib().lora_clip_grad(
+        layers.desc, layers.n, _ptr(adapters), M, max_rank, float(max_norm), int(together), _ptr(norm), _ptr(ws),
+        _size(ws), _stream(stream)))

@@ -2,6 +2,8 @@
 // HIP call), workspace layout, and kernel dispatch on the caller's stream.
 #include <string.h>
 
+#include <algorithm>
+
 #include "lora_internal.h"
 #include "quantise.h"
 
@@ -1055,6 +1057,352 @@ int32_t lora_orthogonal_step(const lora_pool_desc *pool, const int32_t *adapters
   a.mu = momentum; a.nesterov = nesterov ? 1 : 0;
   a.out_rank = out_rank;
   return dev(launch_orthogonal(a, 2, true, pool->dtype, ws, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------ gated block
+
+namespace {
+
+// The second pool's tables are the first's: one plan serves both.
+int32_t check_pair(const lora_pool_desc *a, const lora_pool_desc *b) {
+  int32_t st = check_pool(a, true);
+  if (st == LORA_OK) st = check_pool(b, true);
+  if (st != LORA_OK) return st;
+  const bool same = a->dtype == b->dtype && a->d_in == b->d_in && a->d_out == b->d_out &&
+                    a->n_adapters == b->n_adapters && a->n_pages == b->n_pages &&
+                    a->n_page_ids == b->n_page_ids && a->rank == b->rank &&
+                    a->page_start == b->page_start && a->page_ids == b->page_ids;
+  return same ? LORA_OK : LORA_ERR_INVALID_ARG;
+}
+
+bool activation_ok(int32_t act) {
+  return act == LORA_ACT_SILU || act == LORA_ACT_GELU || act == LORA_ACT_GELU_TANH;
+}
+
+// out[0 .. n_out) name no buffer twice, and none of in[0 .. n_in).
+bool outputs_apart(const void *const *out, int n_out, const void *const *in, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    if (!out[i]) continue;
+    for (int j = 0; j < i; ++j)
+      if (out[i] == out[j]) return false;
+    for (int j = 0; j < n_in; ++j)
+      if (out[i] == in[j]) return false;
+  }
+  return true;
+}
+
+struct GatedCall {
+  ApplyWs w[2];
+  GemmArgs g[2];
+  GemmConfig cfg;
+  GatedArgs a;
+  bool fused;
+};
+
+// The checks of the gated forward (T > 0 from the workspaces on), and its
+// arguments.
+int32_t gated_args(const void *X, const void *W_gate_t, const void *W_up_t, int32_t activation,
+                   void *H, void *pre_gate, void *pre_up, int32_t T, int32_t K, const float *gates,
+                   const lora_pool_desc *gate, const lora_pool_desc *up, const void *plan,
+                   void *ws_gate, size_t ws_gate_bytes, void *ws_up, size_t ws_up_bytes, GatedCall &c) {
+  int32_t st = check_batch(T, K);
+  if (st != LORA_OK) return st;
+  if ((st = check_pair(gate, up)) != LORA_OK) return st;
+  if (!plan || !activation_ok(activation) || !pre_gate != !pre_up) return LORA_ERR_INVALID_ARG;
+  if (T == 0) return LORA_OK;
+  if (!X || !W_gate_t || !W_up_t || !H || !gates || !ws_gate || !ws_up) return LORA_ERR_INVALID_ARG;
+  const void *out[] = {H, pre_gate, pre_up, ws_gate, ws_up}, *in[] = {X, W_gate_t, W_up_t, plan};
+  if (!outputs_apart(out, 5, in, 4)) return LORA_ERR_INVALID_ARG;
+  if ((st = base_args(X, W_gate_t, H, T, K, gate, plan, ws_gate, ws_gate_bytes, c.cfg, c.g[0])) != LORA_OK ||
+      (st = base_args(X, W_up_t, H, T, K, up, plan, ws_up, ws_up_bytes, c.cfg, c.g[1])) != LORA_OK)
+    return st;
+  c.w[0] = apply_layout(ws_gate, ws_gate_bytes, T, K, gate->d_in, gate->d_out, gate->dtype);
+  c.w[1] = apply_layout(ws_up, ws_up_bytes, T, K, up->d_in, up->d_out, up->dtype);
+  c.fused = gated_fused(T, gate->d_out, gate->dtype);
+  GatedArgs &a = c.a;
+  a = GatedArgs{};
+  a.X = X; a.W[0] = W_gate_t; a.W[1] = W_up_t;
+  a.M = T; a.N = gate->d_out; a.Kd = gate->d_in;
+  a.ex = c.g[0].ex;
+  // U of both or of neither
+  if (c.w[1].u_cap < a.ex.u_cap) a.ex.u_cap = c.w[1].u_cap;
+  a.U_up = c.w[1].U; a.b_up = up->b_pages;
+  a.act = activation;
+  a.H = H; a.pre_gate = pre_gate; a.pre_up = pre_up;
+  a.part[0] = c.g[0].partial; a.part[1] = c.g[1].partial;
+  a.splits = c.cfg.splits; a.sk_g = c.cfg.sk; a.sk_kt = gate->d_in / 64;
+  a.bm = c.cfg.bm; a.bn = c.cfg.bn;
+  return LORA_OK;
+}
+
+hipError_t gated_shrinks(const GatedCall &c, const void *X, const uint8_t *keep_mask, float keep_scale,
+                         int32_t T, int32_t K, const float *gates, const lora_pool_desc *const (&pool)[2],
+                         const PlanView &pv, hipStream_t s) {
+  for (int p = 0; p < 2; ++p) {
+    const ShrinkArgs a = apply_shrink_args(X, keep_mask, keep_scale, T, K, gates, pool[p], pv, c.w[p]);
+    const hipError_t e = launch_shrink(a, pool[p]->dtype, int64_t(T) * K, pool[p]->n_adapters, pool[p]->d_in,
+                                       pool[p]->d_out, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t lora_gated_apply(const void *X, const void *W_gate_t, const void *W_up_t, int32_t activation,
+                         void *H, void *pre_gate, void *pre_up, int32_t T, int32_t K,
+                         const float *gates, const uint8_t *keep_mask, float keep_scale,
+                         const lora_pool_desc *gate, const lora_pool_desc *up, const void *plan,
+                         void *ws_gate, size_t ws_gate_bytes, void *ws_up, size_t ws_up_bytes,
+                         void *stream) {
+  GatedCall c;
+  const int32_t st = gated_args(X, W_gate_t, W_up_t, activation, H, pre_gate, pre_up, T, K, gates, gate, up,
+                                plan, ws_gate, ws_gate_bytes, ws_up, ws_up_bytes, c);
+  if (st != LORA_OK || T == 0) return st;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const lora_pool_desc *const pool[2] = {gate, up};
+  const PlanView pv = plan_view(plan, int64_t(T) * K, gate->n_adapters);
+  hipError_t e = gated_shrinks(c, X, keep_mask, keep_scale, T, K, gates, pool, pv, s);
+  if (e != hipSuccess) return LORA_ERR_DEVICE;
+  if (c.fused) return dev(launch_gated_tiles(c.a, s));
+  for (int p = 0; p < 2 && e == hipSuccess; ++p) e = launch_base_gemm(c.cfg, c.g[p], s);
+  if (e == hipSuccess) e = launch_gated_epilogue(c.a, gate->dtype, s);
+  return dev(e);
+}
+
+int32_t lora_gated_forward(const int32_t *ids, const float *gates, int32_t T, int32_t K,
+                           const void *X, const void *W_gate_t, const void *W_up_t,
+                           int32_t activation, void *H, void *pre_gate, void *pre_up,
+                           const uint8_t *keep_mask, float keep_scale, const lora_pool_desc *gate,
+                           const lora_pool_desc *up, void *plan, size_t plan_bytes, void *ws_gate,
+                           size_t ws_gate_bytes, void *ws_up, size_t ws_up_bytes, void *stream) {
+  GatedCall c;
+  int32_t st = gated_args(X, W_gate_t, W_up_t, activation, H, pre_gate, pre_up, T, K, gates, gate, up, plan,
+                          ws_gate, ws_gate_bytes, ws_up, ws_up_bytes, c);
+  if (st != LORA_OK) return st;
+  if ((st = lora_plan(ids, gates, T, K, gate, plan, plan_bytes, stream)) != LORA_OK || T == 0) return st;
+  return lora_gated_apply(X, W_gate_t, W_up_t, activation, H, pre_gate, pre_up, T, K, gates, keep_mask,
+                          keep_scale, gate, up, plan, ws_gate, ws_gate_bytes, ws_up, ws_up_bytes, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Workspace of the gated backward: [G of the gate][G of the up projection]
+// [partials of both products].
+struct GatedGradWs {
+  GemmConfig cfg;
+  bool fused;
+  size_t g, part, total;
+};
+
+GatedGradWs gated_grad_ws(int32_t T, int32_t K, int32_t d_in, int32_t d_out, int32_t max_rank, int32_t dtype) {
+  GatedGradWs w{};
+  w.cfg = grad_x_config(T, d_in, d_out, dtype);
+  w.fused = gated_grad_x_fused(T, d_in, dtype);
+  w.g = align_up(size_t(T) * size_t(K) * size_t(max_rank) * sizeof(float) + 4);
+  w.part = w.fused ? 0 : align_up(gemm_partial_bytes(w.cfg, T, d_in));
+  w.total = 2 * (w.g + w.part);
+  return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lora_gated_grad_workspace_bytes(int32_t T, int32_t K, int32_t d_in, int32_t d_out,
+                                       int32_t max_rank, int32_t dtype) {
+  if (check_batch(T, K) != LORA_OK || !dims_ok(d_in) || !dims_ok(d_out)) return 0;
+  if (max_rank < 1 || max_rank > LORA_MAX_RANK || (dtype != LORA_F32 && dtype != LORA_BF16)) return 0;
+  return gated_grad_ws(T, K, d_in, d_out, max_rank, dtype).total;
+}
+
+int32_t lora_gated_grad(const void *dH, const void *pre_gate, const void *pre_up, int32_t activation,
+                        const void *W_gate, const void *W_up, const uint8_t *keep_mask,
+                        float keep_scale, int32_t T, int32_t K, const float *gates,
+                        const lora_pool_desc *gate, const lora_pool_desc *up, const void *plan,
+                        int32_t max_rank, void *d_gate, void *d_up, void *dX, void *ws,
+                        size_t ws_bytes, void *stream) {
+  int32_t st = check_batch(T, K);
+  if (st != LORA_OK) return st;
+  if ((st = check_pair(gate, up)) != LORA_OK) return st;
+  if (!plan || !activation_ok(activation) || max_rank < 1 || max_rank > LORA_MAX_RANK)
+    return LORA_ERR_INVALID_ARG;
+  if (T == 0) return LORA_OK;
+  if (!dH || !pre_gate || !pre_up || !d_gate || !d_up) return LORA_ERR_INVALID_ARG;
+  const void *out[] = {d_gate, d_up, dX, ws}, *in[] = {dH, W_gate, W_up, plan, keep_mask};
+  if (!outputs_apart(out, 4, in, 5) || d_gate == pre_up || d_up == pre_gate) return LORA_ERR_INVALID_ARG;
+  if (dX && (!W_gate || !W_up || !gates || !ws || dX == pre_gate || dX == pre_up)) return LORA_ERR_INVALID_ARG;
+  const int32_t F = gate->d_out, d = gate->d_in, dtype = gate->dtype;
+  const GatedGradWs w = gated_grad_ws(T, K, d, F, max_rank, dtype);
+  if (dX && ws_bytes < w.total) return LORA_ERR_CAPACITY;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = launch_gated_act_grad(dH, pre_gate, pre_up, activation, d_gate, d_up, int64_t(T) * F, dtype, s);
+  if (e != hipSuccess || !dX) return dev(e);
+
+  const int64_t TK = int64_t(T) * K;
+  const PlanView pv = plan_view(plan, TK, gate->n_adapters);
+  char *base = static_cast<char *>(ws);
+  const lora_pool_desc *const pool[2] = {gate, up};
+  const void *const dY[2] = {d_gate, d_up}, *const W[2] = {W_gate, W_up};
+  GatedGradXArgs a{};
+  for (int p = 0; p < 2; ++p) {
+    ShrinkArgs sa{};
+    sa.Z = dY[p]; sa.extra_scale = keep_mask ? keep_scale : 1.0f;
+    sa.T = T; sa.K = K; sa.d = F;
+    sa.pages = pool[p]->b_pages;
+    sa.rank = gate->rank; sa.page_start = gate->page_start; sa.page_ids = gate->page_ids;
+    sa.scale = pool[p]->scale; sa.gates = gates; sa.plan = pv;
+    sa.err_word = const_cast<int32_t *>(pv.hdr) + LORA_PH_ERR;
+    sa.out = reinterpret_cast<float *>(base + p * w.g); sa.out_cap = TK * max_rank;
+    if ((e = launch_shrink(sa, dtype, TK, gate->n_adapters, d, F, s)) != hipSuccess) return LORA_ERR_DEVICE;
+    a.dY[p] = dY[p]; a.W[p] = W[p];
+    a.part[p] = reinterpret_cast<float *>(base + 2 * w.g + p * w.part);
+  }
+  a.M = T; a.N = d; a.Kd = F;
+  a.ex.K = K;
+  a.ex.slot_desc = pv.slot_desc; a.ex.pair_tk = pv.pair_tk; a.ex.page_ids = gate->page_ids;
+  a.ex.b_pages = gate->a_pages; a.ex.d_out = d;
+  a.ex.U = reinterpret_cast<float *>(base); a.ex.hdr = pv.hdr; a.ex.u_cap = TK * max_rank;
+  a.U_up = reinterpret_cast<float *>(base + w.g); a.b_up = up->a_pages;
+  a.mask = keep_mask; a.dX = dX;
+  a.splits = w.cfg.splits; a.sk_g = w.cfg.sk; a.sk_kt = F / 64; a.bm = w.cfg.bm; a.bn = w.cfg.bn;
+  if (w.fused) return dev(launch_gated_grad_x_tiles(a, s));
+  for (int p = 0; p < 2 && e == hipSuccess; ++p) {
+    GemmArgs g{};
+    g.X = dY[p]; g.W = W[p]; g.M = T; g.N = d; g.Kd = F;
+    g.k_split = w.cfg.k_split; g.sk_g = w.cfg.sk;
+    g.partial = const_cast<float *>(a.part[p]);
+    e = launch_base_gemm(w.cfg, g, s);
+  }
+  if (e == hipSuccess) e = launch_gated_grad_x_epilogue(a, dtype, s);
+  return dev(e);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------ cross entropy
+
+namespace {
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+int32_t check_entropy(int32_t T, int32_t V, int32_t d, int32_t dtype) {
+  if (T < 0 || V < 1 || (dtype != LORA_F32 && dtype != LORA_BF16)) return LORA_ERR_INVALID_ARG;
+  if (T > kMaxPairs || V > (1 << 24) || !dims_ok(d)) return LORA_ERR_UNSUPPORTED;
+  return LORA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lora_cross_entropy_workspace_bytes(int32_t T, int32_t V, int32_t d, int32_t dtype,
+                                          int32_t with_grad) {
+  if (check_entropy(T, V, d, dtype) != LORA_OK) return 0;
+  return align_up(cross_entropy_workspace_bytes(T > 0 ? T : 1, V, d, dtype, with_grad != 0));
+}
+
+int32_t lora_cross_entropy(const void *X, const void *W_t, int32_t dtype, int32_t T, int32_t V,
+                           int32_t d, const int32_t *targets, const float *weights,
+                           float logit_scale, float *loss, void *dX, void *ws, size_t ws_bytes,
+                           void *stream) {
+  const int32_t st = check_entropy(T, V, d, dtype);
+  if (st != LORA_OK) return st;
+  if (!(logit_scale - logit_scale == 0.f) || logit_scale == 0.f) return LORA_ERR_INVALID_ARG;
+  if (T == 0) return LORA_OK;
+  if (!X || !W_t || !targets || !loss || !ws) return LORA_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(W_t) || !aligned16(dX) || !aligned16(ws)) return LORA_ERR_INVALID_ARG;
+  const void *out[] = {loss, dX, ws}, *in[] = {X, W_t, targets, weights};
+  if (!outputs_apart(out, 3, in, 4)) return LORA_ERR_INVALID_ARG;
+  if (ws_bytes < lora_cross_entropy_workspace_bytes(T, V, d, dtype, dX != nullptr)) return LORA_ERR_CAPACITY;
+  CrossEntropyArgs a{};
+  a.X = X; a.W = W_t; a.T = T; a.V = V; a.d = d;
+  a.targets = targets; a.weights = weights; a.logit_scale = logit_scale;
+  a.loss = loss; a.dX = dX;
+  return dev(launch_cross_entropy(a, dtype, ws, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------ gradient clipping
+
+namespace {
+
+constexpr int32_t kMaxClipLayers = 1024;
+
+struct Span {
+  uintptr_t at, end;
+  int32_t id;          // 2 x layer + factor
+};
+
+// The outputs are apart from each other, and from every gradient but the one
+// they replace in place.
+bool spans_apart(Span *out, int n_out, const Span *in, int n_in) {
+  std::sort(out, out + n_out, [](const Span &a, const Span &b) { return a.at < b.at; });
+  for (int i = 1; i < n_out; ++i)
+    if (out[i].at < out[i - 1].end) return false;
+  for (int i = 0; i < n_in; ++i) {
+    // the first output that ends behind the gradient's start, and those after it
+    const Span *o = std::upper_bound(out, out + n_out, in[i].at, [](uintptr_t at, const Span &b) { return at < b.end; });
+    for (; o < out + n_out && o->at < in[i].end; ++o)
+      if (o->id != in[i].id || o->at != in[i].at) return false;
+  }
+  return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lora_clip_grad_workspace_bytes(int32_t n_layers, int32_t M, int32_t max_rank) {
+  if (n_layers < 0 || n_layers > kMaxClipLayers || M < 0 || M > kMaxOrthAdapters || max_rank < 1 ||
+      max_rank > LORA_MAX_RANK)
+    return 0;
+  return align_up(clip_workspace_bytes(n_layers, M, max_rank) + 8);
+}
+
+int32_t lora_clip_grad(const lora_grad_desc *layers, int32_t n_layers, const int32_t *adapters,
+                       int32_t M, int32_t max_rank, float max_norm, int32_t together, float *norm,
+                       void *ws, size_t ws_bytes, void *stream) {
+  if (n_layers < 0 || M < 0 || (n_layers > 0 && !layers) || (M > 0 && !adapters) || !norm || !ws)
+    return LORA_ERR_INVALID_ARG;
+  if (max_rank < 1 || max_rank > LORA_MAX_RANK || !(max_norm > 0.f)) return LORA_ERR_INVALID_ARG;
+  if (n_layers > kMaxClipLayers || M > kMaxOrthAdapters) return LORA_ERR_UNSUPPORTED;
+  ClipLayer l[kMaxClipLayers];
+  Span outs[2 * kMaxClipLayers], ins[2 * kMaxClipLayers];
+  int n = 0;
+  for (int32_t i = 0; i < n_layers; ++i) {
+    const lora_grad_desc &g = layers[i];
+    const int32_t st = check_pool(&g.pool, false);
+    if (st != LORA_OK) return st;
+    if (!dims_ok(g.pool.d_in) || !dims_ok(g.pool.d_out)) return LORA_ERR_UNSUPPORTED;
+    const bool none = g.pool.n_pages == 0;
+    const float *in[2] = {g.dA_pages, g.dB_pages};
+    float *out[2] = {g.dA_out, g.dB_out};
+    l[i] = ClipLayer{{in[0], in[1]}, {out[0], out[1]}, g.pool.rank, g.pool.page_start, g.pool.page_ids,
+                     g.pool.n_pages, g.pool.n_page_ids, {g.pool.d_in, g.pool.d_out}, g.pool.n_adapters};
+    for (int f = 0; f < 2; ++f) {
+      if ((!in[f] || !out[f]) && !none) return LORA_ERR_INVALID_ARG;
+      if (!aligned16(in[f]) || !aligned16(out[f])) return LORA_ERR_INVALID_ARG;
+      const size_t bytes = size_t(g.pool.n_pages) * size_t(l[i].d[f]) * sizeof(float);
+      const uintptr_t a = reinterpret_cast<uintptr_t>(in[f]), b = reinterpret_cast<uintptr_t>(out[f]);
+      if (bytes == 0) continue;
+      ins[n] = Span{a, a + bytes, 2 * i + f};
+      outs[n++] = Span{b, b + bytes, 2 * i + f};
+    }
+  }
+  if (!spans_apart(outs, n, ins, n)) return LORA_ERR_INVALID_ARG;
+  if (ws_bytes < lora_clip_grad_workspace_bytes(n_layers, M, max_rank)) return LORA_ERR_CAPACITY;
+  ClipArgs a{};
+  a.adapters = adapters; a.M = M; a.max_rank = max_rank; a.together = together ? 1 : 0;
+  a.max_norm = max_norm; a.norm = norm;
+  return dev(launch_clip(l, n_layers, a, ws, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,570 @@
+// Softmax cross entropy of a large vocabulary, with the gradient of the hidden
+// states, without the logits.
+//
+//   l_v = scale . X_t.W_v,   loss_t = w_t (log sum_v e^{l_v} - l_y)
+//   dX_t = w_t scale (sum_v p_v W_v - W_y),   p = softmax(l)
+//
+// In base 2, L = l log2 e, with a whole number ref near the target's L_y:
+//   e_v = 2^{L_v - ref},  S = sum over v != y of e_v,  q = S / e_y
+//   loss = w ln(1 + q),   dX = w scale / (S + e_y) . (sum over v != y of e_v W_v - S W_y)
+// The target's term stands apart: where p_y is near 1, both results come from
+// S alone and keep their relative precision.  A row's largest L is at least
+// L_y, so that nothing that counts underflows against ref; a 64-column piece
+// of a row whose largest L - ref is over 64 takes a further shift of its own
+// (a whole number, so that putting the pieces on one shift later is exact).
+//
+// So the products run once each: the first launch of a block of tokens leaves
+// e in bf16 (float32 layers: float32), relative error 2^-9 of each term and no
+// common reference to wait for, and the sums of each piece; a small one makes
+// S, the loss and the two coefficients of each row; the second product is
+// e.W, split along the vocabulary.  Memory is bounded by taking the tokens in
+// blocks (kBlockBytes of e).  Tokens without a target are left out before the
+// first product, by a list of the others.
+#include "tile_loop.h"
+
+namespace lora {
+namespace {
+
+constexpr int kSub = 64;                               // columns of one piece of a row
+constexpr size_t kBlockBytes = size_t(512) << 20;      // e of one block of tokens
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kMaxExp = 64.f;                        // a piece's exponents over this are shifted
+
+struct CeWs {
+  int32_t *count;      // [1] tokens with a target
+  int32_t *rows;       // [T] those tokens, ascending
+  double *ly;          // [T] their target's logit in base 2
+  float2 *coef;        // [T] (w scale / Z, -w scale S / Z)
+  float2 *part;        // [block][pieces] (sum, shift)
+  void *e;             // [block][lde]
+  float *acc;          // [splits][block][d]
+  int block, pieces, splits;
+  int64_t lde;
+  size_t bytes;
+};
+
+struct CeArgs {
+  CrossEntropyArgs a;
+  CeWs w;
+  int row0;            // first row (of the list) of this block
+};
+
+__device__ __forceinline__ int block_rows(const CeArgs &c) { return min(c.w.block, c.w.count[0] - c.row0); }
+
+// ref of a row, from its target's logit
+__device__ __forceinline__ float ref_of(double ly) {
+  const float r = float(rint(ly));
+  return r - r == 0.f ? r : 0.f;
+}
+
+// ------------------------------------------------------------ rows
+// One workgroup: the list of tokens that have a target and a weight.
+__global__ __launch_bounds__(1024) void ce_rows_kernel(CeArgs c) {
+  __shared__ int sums[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int per = (c.a.T + 1023) / 1024, t0 = min(tid * per, c.a.T), t1 = min(t0 + per, c.a.T);
+  int n = 0;
+  for (int t = t0; t < t1; ++t) {
+    const int y = c.a.targets[t];
+    const bool zero = c.a.weights && c.a.weights[t] == 0.f;
+    if (y >= 0 && y < c.a.V && !zero) ++n;
+    else c.a.loss[t] = y >= c.a.V ? __builtin_nanf("") : 0.f;
+  }
+  int incl = n;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int v = __shfl_up(incl, o, 64);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 63) sums[wave] = incl;
+  __syncthreads();
+  int at = incl - n;
+  for (int w = 0; w < wave; ++w) at += sums[w];
+  for (int t = t0; t < t1; ++t) {
+    const int y = c.a.targets[t];
+    const bool zero = c.a.weights && c.a.weights[t] == 0.f;
+    if (y >= 0 && y < c.a.V && !zero) c.w.rows[at++] = t;
+  }
+  if (tid == 1023) c.w.count[0] = at;
+}
+
+// One wave per row: the target's logit of list entry r (float64 sums: both
+// results hang on it), and the zero gradient of a token r that is not listed.
+template <typename E>
+__global__ __launch_bounds__(256) void ce_target_kernel(CeArgs c) {
+  const int r = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (r >= c.a.T) return;
+  const int d = c.a.d;
+  if (c.a.dX) {
+    const int y = c.a.targets[r];
+    if (y < 0 || y >= c.a.V || (c.a.weights && c.a.weights[r] == 0.f)) {
+      const float z[8] = {};
+      for (int i = lane * 8; i < d; i += 512) Cols<E, 8>::store(static_cast<E *>(c.a.dX) + int64_t(r) * d + i, z);
+    }
+  }
+  if (r >= c.w.count[0]) return;
+  const int t = c.w.rows[r];
+  const E *x = static_cast<const E *>(c.a.X) + int64_t(t) * d;
+  const E *w = static_cast<const E *>(c.a.W) + int64_t(c.a.targets[t]) * d;
+  double sum = 0.0;
+  for (int i = lane * 8; i < d; i += 512) {
+    float xv[8], wv[8];
+    Elem<E>::load8(x + i, xv);
+    Elem<E>::load8(w + i, wv);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum = fma(double(xv[k]), double(wv[k]), sum);
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+  if (lane == 0) c.w.ly[r] = sum * double(c.a.logit_scale) * 1.4426950408889634074;
+}
+
+// ------------------------------------------------------------ first product
+// 8 logits of one row (list entry r, columns col .. col + 7 of a 64-column
+// piece that 8 neighbouring lanes share) to e: the piece's sum and shift, and
+// with a gradient e itself.  Columns past V and the target's count as nothing.
+// Every lane of the wave calls this.
+template <typename E>
+__device__ __forceinline__ void ce_store8(const CeArgs &c, float (&v)[8], int lr, bool row_ok, int col, float ref,
+                                          int y) {
+  const float s2 = c.a.logit_scale * kLog2e;
+  float top = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    v[k] = col + k < c.a.V ? fmaf(v[k], s2, -ref) : -INFINITY;
+    top = fmaxf(top, v[k]);
+  }
+  float shift = 0.f;
+  if (__ballot(row_ok && top > kMaxExp)) {
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+    // an infinity keeps its place: the row's sum then is no number
+    shift = top > kMaxExp && top < INFINITY ? ceilf(top) : 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] -= shift;
+  }
+  float sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    v[k] = __builtin_amdgcn_exp2f(v[k]);
+    if (col + k == y) v[k] = 0.f;
+    sum += v[k];
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor(sum, o, 64);
+  if (!row_ok) return;
+  if (c.a.dX && col < c.w.lde) Cols<E, 8>::store(static_cast<E *>(c.w.e) + int64_t(lr) * c.w.lde + col, v);
+  if ((threadIdx.x & 7) == 0 && col / kSub < c.w.pieces)
+    c.w.part[int64_t(lr) * c.w.pieces + col / kSub] = make_float2(sum, shift);
+}
+
+// Rows of the list (64-bit addresses: the list's tokens lie anywhere in X) by
+// rows of W, both along d.
+template <int BM, int BN, int WM, int WN>
+struct LogitsSrc {
+  using C = TileCfg<BM, BN, WM, WN>;
+  const uint16_t *a[C::A_INS], *b[C::B_INS];
+  int wave;
+  __device__ __forceinline__ void copy(uint32_t lds, int kt, int i) const {
+    if (i < C::A_INS) lds_dma16(a[i] + kt * 64, lds + (wave * C::A_INS + i) * 1024);
+    else lds_dma16(b[i - C::A_INS] + kt * 64, lds + BM * C::ROWB + (wave * C::B_INS + i - C::A_INS) * 1024);
+  }
+  __device__ __forceinline__ bf16x8_t frag(const char *base, int s, int q) const {
+    const int frow = threadIdx.x & 31, wm = wave / WN, wn = wave % WN;
+    return frag_rows<C, WN>(base, s, q < C::TM ? (wm * C::TM + q) * 32 + frow
+                                               : BM + (wn * C::TN + q - C::TM) * 32 + frow);
+  }
+};
+
+template <int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM * WN * 64, 1) void ce_logits_kernel(CeArgs c) {
+  using C = TileCfg<BM, BN, WM, WN>;
+  constexpr int WC = C::TN * 32, SC = WC + 4;
+  static_assert(WC == kSub, "one piece per wave");
+  static_assert(C::NW * 32 * SC * 4 <= 2 * C::STAGE, "staging must fit in LDS");
+  __shared__ __attribute__((aligned(16))) char smem[2 * C::STAGE];
+  const int M = block_rows(c);
+  int tm, tn;
+  if (M <= 0 || !tile_of_workgroup(blockIdx.x, (M + BM - 1) / BM, (c.a.V + BN - 1) / BN, tm, tn)) return;
+  const int m0 = tm * BM, n0 = tn * BN, d = c.a.d;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave / WN, wn = wave % WN, lrow = lane >> 3;
+
+  LogitsSrc<BM, BN, WM, WN> src;
+  src.wave = wave;
+#pragma unroll
+  for (int i = 0; i < C::A_INS; ++i) {
+    const int row = (wave * C::A_INS + i) * 8 + lrow;
+    const int t = c.w.rows[c.row0 + min(m0 + row, M - 1)];
+    src.a[i] = static_cast<const uint16_t *>(c.a.X) + int64_t(t) * d + tswz(row, lane & 7) * 8;
+  }
+#pragma unroll
+  for (int i = 0; i < C::B_INS; ++i) {
+    const int row = (wave * C::B_INS + i) * 8 + lrow;
+    src.b[i] = static_cast<const uint16_t *>(c.a.W) + int64_t(min(n0 + row, c.a.V - 1)) * d + tswz(row, lane & 7) * 8;
+  }
+  f32x16_t acc[C::TM][C::TN];
+  tile_loop<BM, BN, WM, WN>(src, smem, d / 64, acc);
+
+  // through the wave's own LDS, to lanes that hold 8 columns of a row
+  float *stage = reinterpret_cast<float *>(smem) + wave * 32 * SC;
+  const int frow = lane & 31, half = lane >> 5, vr = lane >> 3, col = n0 + wn * WC + (lane & 7) * 8;
+#pragma unroll
+  for (int i = 0; i < C::TM; ++i) {
+#pragma unroll
+    for (int j = 0; j < C::TN; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v)
+        stage[((v >> 2) * 8 + half * 4 + (v & 3)) * SC + j * 32 + frow] = acc[i][j][v];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int lr = m0 + (wm * C::TM + i) * 32 + q * 8 + vr;
+      const bool ok = lr < M;
+      const int r = c.row0 + (ok ? lr : M - 1);
+      const float4 lo = *reinterpret_cast<const float4 *>(stage + (q * 8 + vr) * SC + (lane & 7) * 8);
+      const float4 hi = *reinterpret_cast<const float4 *>(stage + (q * 8 + vr) * SC + (lane & 7) * 8 + 4);
+      float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      ce_store8<uint16_t>(c, x, lr, ok, col, ref_of(c.w.ly[r]), c.a.targets[c.w.rows[r]]);
+    }
+  }
+}
+
+// ------------------------------------------------------------ float32 tiles
+// 64 x 64 of A.B on v_mfma_f32_32x32x2_f32, a 32 x 32 block for each of four
+// waves, K in chunks of 32 through LDS.  a(r, k) and b(k, c) give 4 values:
+// along k for A, along k (kBAlongK) or along c for B; k is a multiple of 4.
+constexpr int kF32K = 32;
+struct F32Tile {
+  float as[64][kF32K + 1], bs[64][kF32K + 1];
+};
+
+template <bool kBAlongK, typename FA, typename FB>
+__device__ __forceinline__ f32x16_t tile_f32(F32Tile &t, int k_begin, int k_end, const FA &fa, const FB &fb) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  f32x16_t acc = {};
+  for (int k0 = k_begin; k0 < k_end; k0 += kF32K) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = (tid + i * 256) * 4;
+      const int row = at / kF32K, k = at % kF32K;
+      const float4 v = fa(row, k0 + k);
+      t.as[row][k] = v.x; t.as[row][k + 1] = v.y; t.as[row][k + 2] = v.z; t.as[row][k + 3] = v.w;
+      if constexpr (kBAlongK) {
+        const float4 w = fb(row, k0 + k);
+        t.bs[row][k] = w.x; t.bs[row][k + 1] = w.y; t.bs[row][k + 2] = w.z; t.bs[row][k + 3] = w.w;
+      } else {
+        const int kk = at / 64, cc = at % 64;
+        const float4 w = fb(cc, k0 + kk);
+        t.bs[cc][kk] = w.x; t.bs[cc + 1][kk] = w.y; t.bs[cc + 2][kk] = w.z; t.bs[cc + 3][kk] = w.w;
+      }
+    }
+    __syncthreads();
+    const int ra = (wave >> 1) * 32 + (lane & 31), rb = (wave & 1) * 32 + (lane & 31);
+#pragma unroll
+    for (int k = 0; k < kF32K; k += 2)
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(t.as[ra][k + (lane >> 5)], t.bs[rb][k + (lane >> 5)], acc, 0, 0, 0);
+  }
+  return acc;
+}
+
+__global__ __launch_bounds__(256) void ce_logits_f32_kernel(CeArgs c) {
+  __shared__ F32Tile t;
+  __shared__ __attribute__((aligned(16))) float stage[64][64 + 4];
+  const int M = block_rows(c), d = c.a.d;
+  const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
+  if (m0 >= M) return;
+  const float *X = static_cast<const float *>(c.a.X), *W = static_cast<const float *>(c.a.W);
+  const f32x16_t acc = tile_f32<true>(
+      t, 0, d,
+      [&](int r, int k) {
+        return *reinterpret_cast<const float4 *>(X + int64_t(c.w.rows[c.row0 + min(m0 + r, M - 1)]) * d + k);
+      },
+      [&](int r, int k) { return *reinterpret_cast<const float4 *>(W + int64_t(min(n0 + r, c.a.V - 1)) * d + k); });
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int v = 0; v < 16; ++v)
+    stage[(wave >> 1) * 32 + (v >> 2) * 8 + (lane >> 5) * 4 + (v & 3)][(wave & 1) * 32 + (lane & 31)] = acc[v];
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int rr = q * 32 + (threadIdx.x >> 3), lr = m0 + rr;
+    const bool ok = lr < M;
+    const int r = c.row0 + (ok ? lr : M - 1);
+    float x[8];
+    Elem<float>::load8(&stage[rr][(lane & 7) * 8], x);
+    ce_store8<float>(c, x, lr, ok, n0 + (lane & 7) * 8, ref_of(c.w.ly[r]), c.a.targets[c.w.rows[r]]);
+  }
+}
+
+// ------------------------------------------------------------ rows' sums
+// One workgroup per row: its pieces on one shift, the loss and the
+// coefficients of its gradient.
+template <typename E>
+__global__ __launch_bounds__(256) void ce_row_kernel(CeArgs c) {
+  __shared__ float red[2][4];
+  const int lr = blockIdx.x;
+  if (lr >= block_rows(c)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const float2 *part = c.w.part + int64_t(lr) * c.w.pieces;
+  float R = 0.f;
+  for (int i = tid; i < c.w.pieces; i += 256) R = fmaxf(R, part[i].y);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) R = fmaxf(R, __shfl_xor(R, o, 64));
+  if (lane == 0) red[0][wave] = R;
+  __syncthreads();
+  R = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+  float S = 0.f;
+  for (int i = tid; i < c.w.pieces; i += 256) {
+    const float2 p = part[i];
+    S += R > 0.f ? p.x * exp2f(p.y - R) : p.x;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) S += __shfl_xor(S, o, 64);
+  if (lane == 0) red[1][wave] = S;
+  __syncthreads();
+  S = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+  if (R > 0.f && c.a.dX) {
+    E *e = static_cast<E *>(c.w.e) + int64_t(lr) * c.w.lde;
+    for (int64_t i = tid * 8; i < c.w.lde; i += 256 * 8) {
+      const float f = exp2f(part[i / kSub].y - R);
+      if (f == 1.f) continue;
+      float v[8];
+      Elem<E>::load8(e + i, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] *= f;
+      Cols<E, 8>::store(e + i, v);
+    }
+  }
+  if (tid != 0) return;
+  const int r = c.row0 + lr, t = c.w.rows[r];
+  const float w = c.a.weights ? c.a.weights[t] : 1.f;
+  const double ly = c.w.ly[r], up = double(ref_of(ly)) + double(R) - ly;   // ref + R - L_y
+  const double ey = exp2(-up);                    // the target's e on the row's shift
+  double loss, z = double(S) + ey;
+  if (!(S < INFINITY) || !(ly < double(INFINITY))) loss = z = __builtin_nan("");
+  else if (up > 900.0) loss = log(double(S)) + up * 0.69314718055994530942;
+  else loss = log1p(double(S) * exp2(up));
+  c.a.loss[t] = float(double(w) * loss);
+  const double k = double(w) * double(c.a.logit_scale) / z;
+  c.w.coef[r] = make_float2(float(k), float(-k * double(S)));
+}
+
+// ------------------------------------------------------------ second product
+// e [rows][lde] along the vocabulary by W [V][d] across it.  A K tile of W is
+// 64 rows of BN columns in LDS, 16-byte piece p of row k in slot
+// p ^ ((k & 3) << 2): the transposing reads of a fragment take 4 rows by 64
+// bytes at once, which then cover the 64 banks once.  Rows past V meet zeros
+// of e.
+template <int BM, int BN, int WM, int WN>
+struct ExpSrc {
+  using C = TileCfg<BM, BN, WM, WN>;
+  static_assert(BN == 256, "a row of the B tile is 512 bytes");
+  const uint16_t *a[C::A_INS];
+  const uint16_t *W;
+  int wave, k0, V, d, bcol[C::B_INS];
+  __device__ __forceinline__ void copy(uint32_t lds, int kt, int i) const {
+    if (i < C::A_INS) {
+      lds_dma16(a[i] + kt * 64, lds + (wave * C::A_INS + i) * 1024);
+    } else {
+      const int ib = wave * C::B_INS + i - C::A_INS, k = k0 + kt * 64 + 2 * ib + ((threadIdx.x & 63) >> 5);
+      lds_dma16(W + int64_t(min(k, V - 1)) * d + bcol[i - C::A_INS], lds + BM * C::ROWB + ib * 1024);
+    }
+  }
+  __device__ __forceinline__ bf16x8_t frag(const char *base, int s, int q) const {
+    const int lane = threadIdx.x & 63, wm = wave / WN, wn = wave % WN;
+    if (q < C::TM) return frag_rows<C, WN>(base, s, (wm * C::TM + q) * 32 + (lane & 31));
+    // lane (column n, k of 8 half .. + 7): two transposing reads.  In each
+    // group of 16 lanes, lane L gives the address of row L / 4 of a 4-row
+    // block, columns 4 (L % 4) .. + 3, and receives column L of the 4 rows.
+    const int L = lane & 15, cb = (wn * C::TN + q - C::TM) * 32 + (lane & 16) + 4 * (L & 3);
+    const int kk = 16 * s + 8 * (lane >> 5) + (L >> 2);
+    const char *p = base + BM * C::ROWB + kk * 512 + (((cb >> 3) ^ ((L >> 2) << 2)) << 4) + (cb & 7) * 2;
+    typedef __attribute__((address_space(3))) v4i16_t lds_v4;
+    const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4 *)(p));
+    const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4 *)(p + 4 * 512));
+    bf16x8_t f;
+    __builtin_memcpy(&f, &lo, 8);
+    __builtin_memcpy(reinterpret_cast<char *>(&f) + 8, &hi, 8);
+    return f;
+  }
+};
+
+// K tiles of split z of n
+__device__ __forceinline__ void split_range(int kt, int splits, int z, int &k0, int &nk) {
+  const int b = int(int64_t(kt) * z / splits);
+  k0 = b * 64;
+  nk = int(int64_t(kt) * (z + 1) / splits) - b;
+}
+
+template <int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM * WN * 64, 1) void ce_grad_kernel(CeArgs c) {
+  using C = TileCfg<BM, BN, WM, WN>;
+  __shared__ __attribute__((aligned(16))) char smem[2 * C::STAGE];
+  const int M = block_rows(c), d = c.a.d;
+  int tm, tn;
+  if (M <= 0 || !tile_of_workgroup(blockIdx.x, (M + BM - 1) / BM, (d + BN - 1) / BN, tm, tn)) return;
+  const int m0 = tm * BM, n0 = tn * BN;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / WN, wn = wave % WN;
+  int k0, nk;
+  split_range(int(c.w.lde / 64), c.w.splits, blockIdx.y, k0, nk);
+  ExpSrc<BM, BN, WM, WN> src;
+  src.wave = wave; src.k0 = k0; src.V = c.a.V; src.d = d;
+  src.W = static_cast<const uint16_t *>(c.a.W);
+#pragma unroll
+  for (int i = 0; i < C::A_INS; ++i) {
+    const int row = (wave * C::A_INS + i) * 8 + (lane >> 3);
+    src.a[i] = static_cast<const uint16_t *>(c.w.e) + int64_t(min(m0 + row, M - 1)) * c.w.lde + k0 +
+               tswz(row, lane & 7) * 8;
+  }
+#pragma unroll
+  for (int i = 0; i < C::B_INS; ++i) {
+    const int k = 2 * (wave * C::B_INS + i) + (lane >> 5);
+    src.bcol[i] = min(n0 + ((lane & 31) ^ ((k & 3) << 2)) * 8, d - 8);
+  }
+  f32x16_t acc[C::TM][C::TN];
+  tile_loop<BM, BN, WM, WN>(src, smem, nk, acc);
+  float *out = c.w.acc + int64_t(blockIdx.y) * c.w.block * d;
+#pragma unroll
+  for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::TN; ++j) {
+      const int col = n0 + (wn * C::TN + j) * 32 + (lane & 31);
+      if (col >= d) continue;
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int lr = m0 + (wm * C::TM + i) * 32 + (v >> 2) * 8 + (lane >> 5) * 4 + (v & 3);
+        if (lr < M) __builtin_nontemporal_store(acc[i][j][v], out + int64_t(lr) * d + col);
+      }
+    }
+}
+
+__global__ __launch_bounds__(256) void ce_grad_f32_kernel(CeArgs c) {
+  __shared__ F32Tile t;
+  const int M = block_rows(c), d = c.a.d;
+  const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
+  if (m0 >= M) return;
+  const float *e = static_cast<const float *>(c.w.e), *W = static_cast<const float *>(c.a.W);
+  int k0, nk;
+  split_range(int(c.w.lde / 64), c.w.splits, blockIdx.z, k0, nk);
+  const f32x16_t acc = tile_f32<false>(
+      t, k0, k0 + nk * 64,
+      [&](int r, int k) { return *reinterpret_cast<const float4 *>(e + int64_t(min(m0 + r, M - 1)) * c.w.lde + k); },
+      [&](int n, int k) { return *reinterpret_cast<const float4 *>(W + int64_t(min(k, c.a.V - 1)) * d + n0 + n); });
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float *out = c.w.acc + int64_t(blockIdx.z) * c.w.block * d;
+#pragma unroll
+  for (int v = 0; v < 16; ++v) {
+    const int lr = m0 + (wave >> 1) * 32 + (v >> 2) * 8 + (lane >> 5) * 4 + (v & 3);
+    if (lr < M) out[int64_t(lr) * d + n0 + (wave & 1) * 32 + (lane & 31)] = acc[v];
+  }
+}
+
+// dX of one row: the splits' sums in order, the target's term, one rounding.
+template <typename E>
+__global__ __launch_bounds__(256) void ce_finish_kernel(CeArgs c) {
+  const int lr = blockIdx.x;
+  if (lr >= block_rows(c)) return;
+  const int d = c.a.d, r = c.row0 + lr, t = c.w.rows[r];
+  const float2 k = c.w.coef[r];
+  const E *wy = static_cast<const E *>(c.a.W) + int64_t(c.a.targets[t]) * d;
+  for (int i = threadIdx.x * 8; i < d; i += 256 * 8) {
+    float v[8], w[8];
+    Elem<E>::load8(wy + i, w);
+    Elem<float>::load8(c.w.acc + int64_t(lr) * d + i, v);
+    for (int z = 1; z < c.w.splits; ++z) {
+      float o[8];
+      Elem<float>::load8(c.w.acc + (int64_t(z) * c.w.block + lr) * d + i, o);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] += o[q];
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = fmaf(k.x, v[q], k.y * w[q]);
+    Cols<E, 8>::store(static_cast<E *>(c.a.dX) + int64_t(t) * d + i, v);
+  }
+}
+
+size_t up(size_t x) { return (x + 255) & ~size_t(255); }
+
+CeWs ce_layout(char *ws, int T, int V, int d, int dtype, bool grad) {
+  CeWs w{};
+  const size_t e = dtype == LORA_BF16 ? 2 : 4;
+  const int tile = dtype == LORA_BF16 ? 256 : 64;
+  w.lde = (int64_t(V) + 63) / 64 * 64;
+  w.pieces = int(w.lde / kSub);
+  // rows of a block: as many as kBlockBytes hold, the blocks alike
+  int64_t most = int64_t(kBlockBytes / (size_t(w.lde) * e)) / tile * tile;
+  if (most < tile) most = tile;
+  const int64_t blocks = (T + most - 1) / most;
+  int64_t rows = blocks > 0 ? (T + blocks - 1) / blocks : 1;
+  rows = (rows + tile - 1) / tile * tile;
+  w.block = int(rows < T ? rows : T);
+  size_t at = 0;
+  auto take = [&](size_t n) { char *p = ws ? ws + at : nullptr; at += up(n); return p; };
+  w.count = reinterpret_cast<int32_t *>(take(4));
+  w.rows = reinterpret_cast<int32_t *>(take(size_t(T) * 4));
+  w.ly = reinterpret_cast<double *>(take(size_t(T) * 8));
+  w.coef = reinterpret_cast<float2 *>(take(size_t(T) * 8));
+  w.part = reinterpret_cast<float2 *>(take(size_t(w.block) * size_t(w.pieces) * 8));
+  if (grad) {
+    const int bn = dtype == LORA_BF16 ? 256 : 64;
+    const int64_t tiles = ((w.block + tile - 1) / tile) * int64_t((d + bn - 1) / bn), kt = w.lde / 64;
+    const int64_t fill = dtype == LORA_BF16 ? 256 : 512;
+    int64_t s = fill / (tiles > 0 ? tiles : 1);
+    if (s > kt / 8) s = kt / 8;
+    w.splits = s < 1 ? 1 : int(s);
+    w.e = take(size_t(w.block) * size_t(w.lde) * e);
+    w.acc = reinterpret_cast<float *>(take(size_t(w.splits) * size_t(w.block) * size_t(d) * 4));
+  }
+  w.bytes = at;
+  return w;
+}
+
+template <typename E>
+hipError_t run(CeArgs c, hipStream_t s) {
+  constexpr bool bf = sizeof(E) == 2;
+  const int T = c.a.T, V = c.a.V, d = c.a.d;
+  hipLaunchKernelGGL(ce_rows_kernel, dim3(1), dim3(1024), 0, s, c);
+  hipLaunchKernelGGL(ce_target_kernel<E>, dim3(unsigned((T + 3) / 4)), dim3(256), 0, s, c);
+  for (int r0 = 0; r0 < T; r0 += c.w.block) {
+    c.row0 = r0;
+    const int rows = T - r0 < c.w.block ? T - r0 : c.w.block;
+    if (bf) {
+      const int tiles = ((rows + 255) / 256) * ((V + 255) / 256);
+      hipLaunchKernelGGL((ce_logits_kernel<256, 256, 2, 4>), dim3(8 * unsigned((tiles + 7) / 8)), dim3(512), 0, s, c);
+    } else {
+      hipLaunchKernelGGL(ce_logits_f32_kernel, dim3(unsigned((V + 63) / 64), unsigned((rows + 63) / 64)), dim3(256), 0,
+                         s, c);
+    }
+    hipLaunchKernelGGL(ce_row_kernel<E>, dim3(unsigned(rows)), dim3(256), 0, s, c);
+    if (c.a.dX) {
+      if (bf) {
+        const int tiles = ((rows + 255) / 256) * ((d + 255) / 256);
+        hipLaunchKernelGGL((ce_grad_kernel<256, 256, 2, 4>), dim3(8 * unsigned((tiles + 7) / 8), unsigned(c.w.splits)),
+                           dim3(512), 0, s, c);
+      } else {
+        hipLaunchKernelGGL(ce_grad_f32_kernel, dim3(unsigned(d / 64), unsigned((rows + 63) / 64), unsigned(c.w.splits)),
+                           dim3(256), 0, s, c);
+      }
+      hipLaunchKernelGGL(ce_finish_kernel<E>, dim3(unsigned(rows)), dim3(256), 0, s, c);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t cross_entropy_workspace_bytes(int T, int V, int d, int dtype, bool grad) {
+  return ce_layout(nullptr, T, V, d, dtype, grad).bytes;
+}
+
+hipError_t launch_cross_entropy(const CrossEntropyArgs &a, int dtype, void *ws, hipStream_t s) {
+  CeArgs c{};
+  c.a = a;
+  c.w = ce_layout(static_cast<char *>(ws), a.T, a.V, a.d, dtype, a.dX != nullptr);
+  return dtype == LORA_BF16 ? run<uint16_t>(c, s) : run<float>(c, s);
+}
+
+}  // namespace lora

@@ -425,6 +425,72 @@ struct OrthArgs {
   double *big;              // [matrices][5][R][R], ranks over 64
 };
 
+// Gradient norms and clipping (see clip.hip).
+struct ClipLayer {
+  const float *grad[2];     // dA, dB pages
+  float *out[2];            // where the clipped pages go (may be grad)
+  const int32_t *rank, *page_start, *page_ids;
+  int64_t n_pages, n_page_ids;
+  int d[2];
+  int n_adapters;
+};
+constexpr int kClipLayers = 32;   // layers of one launch: they travel as kernel arguments
+
+struct ClipArgs {
+  const int32_t *adapters;  // [M]
+  int M, max_rank, together;
+  float max_norm;
+  float *norm;              // [M + 1]
+  // set by the launcher
+  int factors, first;       // 2 n_layers, and 2 x the launch's first layer
+  double *square;           // [M]
+  double *part;             // [M][factors][rows]
+  ClipLayer layer[kClipLayers];
+};
+
+// Softmax cross entropy (see cross_entropy.hip).
+struct CrossEntropyArgs {
+  const void *X;            // [T][d]
+  const void *W;            // [V][d]
+  int T, V, d;
+  const int32_t *targets;   // [T]
+  const float *weights;     // [T] or null
+  float logit_scale;
+  float *loss;              // [T]
+  void *dX;                 // [T][d] or null
+};
+
+// The gated block (see gated.hip).  The two projections' slots, pair order,
+// page ids and header are the same; U and the pages are each one's own.
+struct GatedArgs {
+  const void *X;            // [M][Kd]
+  const void *W[2];         // gate, up: [N][Kd]
+  int M, N, Kd;
+  ExpandArgs ex;            // .U and .b_pages: the gate's
+  const float *U_up;
+  const void *b_up;
+  int act;
+  void *H, *pre_gate, *pre_up;   // [M][N]; pre_* null unless training
+  // split forms: the partials of both products
+  const float *part[2];
+  int splits, sk_g, sk_kt, bm, bn;
+};
+
+// The gradient of X of the gated block: dX = dg.Wg^T + du.Wu^T + mask . (both
+// adapter terms).  The expand's U are the coefficients G, its pages A.
+struct GatedGradXArgs {
+  const void *dY[2];        // [M][Kd]: dg, du
+  const void *W[2];         // [N][Kd]
+  int M, N, Kd;
+  ExpandArgs ex;
+  const float *U_up;
+  const void *b_up;
+  const uint8_t *mask;      // [M][N] or null
+  void *dX;                 // [M][N]
+  const float *part[2];
+  int splits, sk_g, sk_kt, bm, bn;
+};
+
 // ----------------------------------------------------------------- launchers
 // Each returns hipSuccess or the launch error.
 hipError_t launch_plan(const int32_t *ids, const float *gates, int T, int K, const PoolView &pool,
@@ -512,6 +578,25 @@ hipError_t launch_compress(const PoolView &pool, const int32_t *adapters, int M,
 
 size_t orth_workspace_bytes(int M, int factors, int max_rank, int d);
 hipError_t launch_orthogonal(OrthArgs a, int factors, bool step, int dtype, void *ws, hipStream_t s);
+
+size_t clip_workspace_bytes(int n_layers, int M, int max_rank);
+hipError_t launch_clip(const ClipLayer *layers, int n_layers, ClipArgs a, void *ws, hipStream_t s);
+
+size_t cross_entropy_workspace_bytes(int T, int V, int d, int dtype, bool grad);
+hipError_t launch_cross_entropy(const CrossEntropyArgs &a, int dtype, void *ws, hipStream_t s);
+
+// The gated block takes tiles with both projections inside (no partials) when
+// they fill the GPU.
+bool gated_fused(int T, int d_out, int dtype);
+hipError_t launch_gated_tiles(const GatedArgs &a, hipStream_t s);
+// The split forms' second launch: both sums, both expands, activation, product.
+hipError_t launch_gated_epilogue(const GatedArgs &a, int dtype, hipStream_t s);
+// d_gate and d_up [n] from dH and the stored results of both projections.
+hipError_t launch_gated_act_grad(const void *dH, const void *pre_gate, const void *pre_up, int act,
+                                 void *d_gate, void *d_up, int64_t n, int dtype, hipStream_t s);
+bool gated_grad_x_fused(int T, int d_in, int dtype);
+hipError_t launch_gated_grad_x_tiles(const GatedGradXArgs &a, hipStream_t s);
+hipError_t launch_gated_grad_x_epilogue(const GatedGradXArgs &a, int dtype, hipStream_t s);
 
 hipError_t launch_merge(const MergeArgs &a, int dtype, hipStream_t s);
 // n layers' merges (same list, each layer's own W and pool): one launch per
