@@ -721,7 +721,7 @@ int32_t lora_gated_grad(const void *dH, const void *pre_gate, const void *pre_up
  *   ws >= lora_cross_entropy_workspace_bytes(..., dX != NULL): tokens are taken
  *   in blocks whose exponentials (dtype) take at most 512 MiB.
  * A logit of +infinity or NaN makes its token's loss and gradient NaN, and no
- * other token's.  At most 2^20 tokens and V of 2^24 (UNSUPPORTED).  Results are
+ * other token's.  At most 2^20 tokens and V of 2^22 (UNSUPPORTED).  Results are
  * deterministic.
  * Errors: INVALID_ARG (null, alignment, an output that is an input, sizes),
  * UNSUPPORTED, CAPACITY, DEVICE. */

@@ -1294,7 +1294,7 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 
 int32_t check_entropy(int32_t T, int32_t V, int32_t d, int32_t dtype) {
   if (T < 0 || V < 1 || (dtype != LORA_F32 && dtype != LORA_BF16)) return LORA_ERR_INVALID_ARG;
-  if (T > kMaxPairs || V > (1 << 24) || !dims_ok(d)) return LORA_ERR_UNSUPPORTED;
+  if (T > kMaxPairs || V > (1 << 22) || !dims_ok(d)) return LORA_ERR_UNSUPPORTED;
   return LORA_OK;
 }
 

@@ -158,67 +158,74 @@ __device__ __forceinline__ void ce_store8(const CeArgs &c, float (&v)[8], int lr
     c.w.part[int64_t(lr) * c.w.pieces + col / kSub] = make_float2(sum, shift);
 }
 
-// Rows of the list (64-bit addresses: the list's tokens lie anywhere in X) by
-// rows of W, both along d.
-template <int BM, int BN, int WM, int WN>
+// Rows of the list (anywhere in X: kWide takes 64-bit lane addresses where X
+// passes 2^32 bytes) by rows of W, both along d.
+template <typename C, bool kWide>
 struct LogitsSrc {
-  using C = TileCfg<BM, BN, WM, WN>;
-  const uint16_t *a[C::A_INS], *b[C::B_INS];
-  int wave;
+  const uint16_t *X, *W;
+  uint32_t ao[C::A_INS], bo[C::B_INS];
+  const uint16_t *aw[kWide ? C::A_INS : 1];
+  int wave, wm, wn;
   __device__ __forceinline__ void copy(uint32_t lds, int kt, int i) const {
-    if (i < C::A_INS) lds_dma16(a[i] + kt * 64, lds + (wave * C::A_INS + i) * 1024);
-    else lds_dma16(b[i - C::A_INS] + kt * 64, lds + BM * C::ROWB + (wave * C::B_INS + i - C::A_INS) * 1024);
+    if (i < C::A_INS) {
+      const uint32_t at = lds + (wave * C::A_INS + i) * 1024;
+      if constexpr (kWide) lds_dma16(aw[i] + kt * 64, at);
+      else lds_dma16_s(X + kt * 64, ao[i], at);
+    } else {
+      lds_dma16_s(W + kt * 64, bo[i - C::A_INS], lds + C::BM * C::ROWB + (wave * C::B_INS + i - C::A_INS) * 1024);
+    }
   }
   __device__ __forceinline__ bf16x8_t frag(const char *base, int s, int q) const {
-    const int frow = threadIdx.x & 31, wm = wave / WN, wn = wave % WN;
-    return frag_rows<C, WN>(base, s, q < C::TM ? (wm * C::TM + q) * 32 + frow
-                                               : BM + (wn * C::TN + q - C::TM) * 32 + frow);
+    return frag_rows(base, s, q < C::TM ? (wm * C::TM + q) * 16 : C::BM + (wn * C::TN + q - C::TM) * 16);
   }
 };
 
-template <int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM * WN * 64, 1) void ce_logits_kernel(CeArgs c) {
-  using C = TileCfg<BM, BN, WM, WN>;
-  constexpr int WC = C::TN * 32, SC = WC + 4;
+template <typename C, bool kWide>
+__global__ __launch_bounds__(C::NT, 1) void ce_logits_kernel(CeArgs c) {
+  constexpr int WC = C::TN * 16, SC = WC + 4;
   static_assert(WC == kSub, "one piece per wave");
   static_assert(C::NW * 32 * SC * 4 <= 2 * C::STAGE, "staging must fit in LDS");
   __shared__ __attribute__((aligned(16))) char smem[2 * C::STAGE];
   const int M = block_rows(c);
   int tm, tn;
-  if (M <= 0 || !tile_of_workgroup(blockIdx.x, (M + BM - 1) / BM, (c.a.V + BN - 1) / BN, tm, tn)) return;
-  const int m0 = tm * BM, n0 = tn * BN, d = c.a.d;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wm = wave / WN, wn = wave % WN, lrow = lane >> 3;
+  if (M <= 0 || !tile_of_workgroup(blockIdx.x, (M + C::BM - 1) / C::BM, (c.a.V + C::BN - 1) / C::BN, tm, tn)) return;
+  const int m0 = tm * C::BM, n0 = tn * C::BN, d = c.a.d;
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int wm = wave / C::WN, wn = wave % C::WN, lrow = lane >> 3;
 
-  LogitsSrc<BM, BN, WM, WN> src;
-  src.wave = wave;
+  LogitsSrc<C, kWide> src;
+  src.wave = wave; src.wm = wm; src.wn = wn;
+  src.X = static_cast<const uint16_t *>(c.a.X);
+  src.W = static_cast<const uint16_t *>(c.a.W) + int64_t(n0) * d;
 #pragma unroll
   for (int i = 0; i < C::A_INS; ++i) {
     const int row = (wave * C::A_INS + i) * 8 + lrow;
-    const int t = c.w.rows[c.row0 + min(m0 + row, M - 1)];
-    src.a[i] = static_cast<const uint16_t *>(c.a.X) + int64_t(t) * d + tswz(row, lane & 7) * 8;
+    const int64_t at = int64_t(c.w.rows[c.row0 + min(m0 + row, M - 1)]) * d + tswz(row, lane & 7) * 8;
+    if constexpr (kWide) src.aw[i] = src.X + at;
+    else src.ao[i] = uint32_t(at) * 2;
   }
 #pragma unroll
   for (int i = 0; i < C::B_INS; ++i) {
     const int row = (wave * C::B_INS + i) * 8 + lrow;
-    src.b[i] = static_cast<const uint16_t *>(c.a.W) + int64_t(min(n0 + row, c.a.V - 1)) * d + tswz(row, lane & 7) * 8;
+    src.bo[i] = (uint32_t(min(row, c.a.V - 1 - n0)) * uint32_t(d) + tswz(row, lane & 7) * 8) * 2;
   }
-  f32x16_t acc[C::TM][C::TN];
-  tile_loop<BM, BN, WM, WN>(src, smem, d / 64, acc);
+  f32x4_t acc[C::TM][C::TN];
+  tile_loop<C>(src, smem, d / 64, acc);
 
   // through the wave's own LDS, to lanes that hold 8 columns of a row
   float *stage = reinterpret_cast<float *>(smem) + wave * 32 * SC;
-  const int frow = lane & 31, half = lane >> 5, vr = lane >> 3, col = n0 + wn * WC + (lane & 7) * 8;
+  const int vr = lane >> 3, col = n0 + wn * WC + (lane & 7) * 8;
 #pragma unroll
-  for (int i = 0; i < C::TM; ++i) {
+  for (int i = 0; i < C::TM; i += 2) {
 #pragma unroll
-    for (int j = 0; j < C::TN; ++j)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int v = 0; v < 16; ++v)
-        stage[((v >> 2) * 8 + half * 4 + (v & 3)) * SC + j * 32 + frow] = acc[i][j][v];
+      for (int j = 0; j < C::TN; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) stage[acc_row(h, v) * SC + acc_col(j)] = acc[i + h][j][v];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int lr = m0 + (wm * C::TM + i) * 32 + q * 8 + vr;
+      const int lr = m0 + (wm * C::TM + i) * 16 + q * 8 + vr;
       const bool ok = lr < M;
       const int r = c.row0 + (ok ? lr : M - 1);
       const float4 lo = *reinterpret_cast<const float4 *>(stage + (q * 8 + vr) * SC + (lane & 7) * 8);
@@ -353,33 +360,37 @@ __global__ __launch_bounds__(256) void ce_row_kernel(CeArgs c) {
 // ------------------------------------------------------------ second product
 // e [rows][lde] along the vocabulary by W [V][d] across it.  A K tile of W is
 // 64 rows of BN columns in LDS, 16-byte piece p of row k in slot
-// p ^ ((k & 3) << 2): the transposing reads of a fragment take 4 rows by 64
-// bytes at once, which then cover the 64 banks once.  Rows past V meet zeros
-// of e.
-template <int BM, int BN, int WM, int WN>
+// p ^ (2 (k % 4) + 8 (k / 8 % 2)): the transposing reads of a fragment take
+// rows k .. k + 3 and k + 8 .. k + 11 by 32 bytes at once, which then cover the
+// 64 banks once.  Rows past V meet zeros of e.
+__device__ __forceinline__ int exp_swz(int k) { return ((k & 3) << 1) | (((k >> 3) & 1) << 3); }
+
+template <typename C>
 struct ExpSrc {
-  using C = TileCfg<BM, BN, WM, WN>;
-  static_assert(BN == 256, "a row of the B tile is 512 bytes");
-  const uint16_t *a[C::A_INS];
-  const uint16_t *W;
-  int wave, k0, V, d, bcol[C::B_INS];
+  static_assert(C::BN == 256, "a row of the B tile is 512 bytes");
+  const uint16_t *e, *W;              // from the split's first K tile
+  uint32_t ao[C::A_INS], brow[C::B_INS], bcol[C::B_INS];
+  uint32_t pitch;                     // bytes of a row of W
+  int wave, wm, wn, last;             // last: V - 1, from the first K tile
   __device__ __forceinline__ void copy(uint32_t lds, int kt, int i) const {
     if (i < C::A_INS) {
-      lds_dma16(a[i] + kt * 64, lds + (wave * C::A_INS + i) * 1024);
+      lds_dma16_s(e + kt * 64, ao[i], lds + (wave * C::A_INS + i) * 1024);
     } else {
-      const int ib = wave * C::B_INS + i - C::A_INS, k = k0 + kt * 64 + 2 * ib + ((threadIdx.x & 63) >> 5);
-      lds_dma16(W + int64_t(min(k, V - 1)) * d + bcol[i - C::A_INS], lds + BM * C::ROWB + ib * 1024);
+      const uint32_t top = uint32_t(min(last - kt * 64, 63)) * pitch;   // the last row's offset in this K tile
+      const uint32_t off = min(brow[i - C::A_INS], top) + bcol[i - C::A_INS];
+      lds_dma16_s(reinterpret_cast<const char *>(W) + int64_t(kt) * 64 * pitch, off,
+                  lds + C::BM * C::ROWB + (wave * C::B_INS + i - C::A_INS) * 1024);
     }
   }
   __device__ __forceinline__ bf16x8_t frag(const char *base, int s, int q) const {
-    const int lane = threadIdx.x & 63, wm = wave / WN, wn = wave % WN;
-    if (q < C::TM) return frag_rows<C, WN>(base, s, (wm * C::TM + q) * 32 + (lane & 31));
-    // lane (column n, k of 8 half .. + 7): two transposing reads.  In each
-    // group of 16 lanes, lane L gives the address of row L / 4 of a 4-row
-    // block, columns 4 (L % 4) .. + 3, and receives column L of the 4 rows.
-    const int L = lane & 15, cb = (wn * C::TN + q - C::TM) * 32 + (lane & 16) + 4 * (L & 3);
-    const int kk = 16 * s + 8 * (lane >> 5) + (L >> 2);
-    const char *p = base + BM * C::ROWB + kk * 512 + (((cb >> 3) ^ ((L >> 2) << 2)) << 4) + (cb & 7) * 2;
+    if (q < C::TM) return frag_rows(base, s, (wm * C::TM + q) * 16);
+    // lane (column lane % 16, k of 8 (lane / 16) .. + 7): two transposing
+    // reads.  In each group of 16 lanes, lane L gives the address of row L / 4
+    // of a 4-row block, columns 4 (L % 4) .. + 3, and receives column L of the
+    // 4 rows.
+    const int lane = threadIdx.x & 63, L = lane & 15, cb = (wn * C::TN + q - C::TM) * 16 + 4 * (L & 3);
+    const int kk = 32 * s + 8 * (lane >> 4) + (L >> 2);
+    const char *p = base + C::BM * C::ROWB + kk * 512 + (((cb >> 3) ^ exp_swz(kk)) << 4) + (cb & 7) * 2;
     typedef __attribute__((address_space(3))) v4i16_t lds_v4;
     const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4 *)(p));
     const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4 *)(p + 4 * 512));
@@ -397,43 +408,45 @@ __device__ __forceinline__ void split_range(int kt, int splits, int z, int &k0, 
   nk = int(int64_t(kt) * (z + 1) / splits) - b;
 }
 
-template <int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM * WN * 64, 1) void ce_grad_kernel(CeArgs c) {
-  using C = TileCfg<BM, BN, WM, WN>;
+template <typename C>
+__global__ __launch_bounds__(C::NT, 1) void ce_grad_kernel(CeArgs c) {
   __shared__ __attribute__((aligned(16))) char smem[2 * C::STAGE];
   const int M = block_rows(c), d = c.a.d;
   int tm, tn;
-  if (M <= 0 || !tile_of_workgroup(blockIdx.x, (M + BM - 1) / BM, (d + BN - 1) / BN, tm, tn)) return;
-  const int m0 = tm * BM, n0 = tn * BN;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / WN, wn = wave % WN;
+  if (M <= 0 || !tile_of_workgroup(blockIdx.x, (M + C::BM - 1) / C::BM, (d + C::BN - 1) / C::BN, tm, tn)) return;
+  const int m0 = tm * C::BM, n0 = tn * C::BN;
+  const int lane = threadIdx.x & 63, wave = wave_id();
   int k0, nk;
   split_range(int(c.w.lde / 64), c.w.splits, blockIdx.y, k0, nk);
-  ExpSrc<BM, BN, WM, WN> src;
-  src.wave = wave; src.k0 = k0; src.V = c.a.V; src.d = d;
-  src.W = static_cast<const uint16_t *>(c.a.W);
+  ExpSrc<C> src;
+  src.wave = wave; src.wm = wave / C::WN; src.wn = wave % C::WN;
+  src.last = c.a.V - 1 - k0;
+  src.pitch = uint32_t(d) * 2;
+  src.e = static_cast<const uint16_t *>(c.w.e) + int64_t(m0) * c.w.lde + k0;
+  src.W = static_cast<const uint16_t *>(c.a.W) + int64_t(k0) * d;
 #pragma unroll
   for (int i = 0; i < C::A_INS; ++i) {
     const int row = (wave * C::A_INS + i) * 8 + (lane >> 3);
-    src.a[i] = static_cast<const uint16_t *>(c.w.e) + int64_t(min(m0 + row, M - 1)) * c.w.lde + k0 +
-               tswz(row, lane & 7) * 8;
+    src.ao[i] = (uint32_t(min(row, M - 1 - m0)) * uint32_t(c.w.lde) + tswz(row, lane & 7) * 8) * 2;
   }
 #pragma unroll
   for (int i = 0; i < C::B_INS; ++i) {
     const int k = 2 * (wave * C::B_INS + i) + (lane >> 5);
-    src.bcol[i] = min(n0 + ((lane & 31) ^ ((k & 3) << 2)) * 8, d - 8);
+    src.brow[i] = uint32_t(k) * src.pitch;
+    src.bcol[i] = uint32_t(min(n0 + ((lane & 31) ^ exp_swz(k)) * 8, d - 8)) * 2;
   }
-  f32x16_t acc[C::TM][C::TN];
-  tile_loop<BM, BN, WM, WN>(src, smem, nk, acc);
+  f32x4_t acc[C::TM][C::TN];
+  tile_loop<C>(src, smem, nk, acc);
   float *out = c.w.acc + int64_t(blockIdx.y) * c.w.block * d;
 #pragma unroll
   for (int i = 0; i < C::TM; ++i)
 #pragma unroll
     for (int j = 0; j < C::TN; ++j) {
-      const int col = n0 + (wn * C::TN + j) * 32 + (lane & 31);
+      const int col = n0 + src.wn * C::TN * 16 + acc_col(j);
       if (col >= d) continue;
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int lr = m0 + (wm * C::TM + i) * 32 + (v >> 2) * 8 + (lane >> 5) * 4 + (v & 3);
+      for (int v = 0; v < 4; ++v) {
+        const int lr = m0 + src.wm * C::TM * 16 + acc_row(i, v);
         if (lr < M) __builtin_nontemporal_store(acc[i][j][v], out + int64_t(lr) * d + col);
       }
     }
@@ -520,6 +533,8 @@ CeWs ce_layout(char *ws, int T, int V, int d, int dtype, bool grad) {
   return w;
 }
 
+using Big = LoopCfg<256, 256, 2, 4>;
+
 template <typename E>
 hipError_t run(CeArgs c, hipStream_t s) {
   constexpr bool bf = sizeof(E) == 2;
@@ -531,7 +546,11 @@ hipError_t run(CeArgs c, hipStream_t s) {
     const int rows = T - r0 < c.w.block ? T - r0 : c.w.block;
     if (bf) {
       const int tiles = ((rows + 255) / 256) * ((V + 255) / 256);
-      hipLaunchKernelGGL((ce_logits_kernel<256, 256, 2, 4>), dim3(8 * unsigned((tiles + 7) / 8)), dim3(512), 0, s, c);
+      const dim3 grid(8 * unsigned((tiles + 7) / 8));
+      if (int64_t(T) * d < (int64_t(1) << 31))
+        hipLaunchKernelGGL((ce_logits_kernel<Big, false>), grid, dim3(Big::NT), 0, s, c);
+      else
+        hipLaunchKernelGGL((ce_logits_kernel<Big, true>), grid, dim3(Big::NT), 0, s, c);
     } else {
       hipLaunchKernelGGL(ce_logits_f32_kernel, dim3(unsigned((V + 63) / 64), unsigned((rows + 63) / 64)), dim3(256), 0,
                          s, c);
@@ -540,8 +559,8 @@ hipError_t run(CeArgs c, hipStream_t s) {
     if (c.a.dX) {
       if (bf) {
         const int tiles = ((rows + 255) / 256) * ((d + 255) / 256);
-        hipLaunchKernelGGL((ce_grad_kernel<256, 256, 2, 4>), dim3(8 * unsigned((tiles + 7) / 8), unsigned(c.w.splits)),
-                           dim3(512), 0, s, c);
+        hipLaunchKernelGGL((ce_grad_kernel<Big>), dim3(8 * unsigned((tiles + 7) / 8), unsigned(c.w.splits)),
+                           dim3(Big::NT), 0, s, c);
       } else {
         hipLaunchKernelGGL(ce_grad_f32_kernel, dim3(unsigned(d / 64), unsigned((rows + 63) / 64), unsigned(c.w.splits)),
                            dim3(256), 0, s, c);

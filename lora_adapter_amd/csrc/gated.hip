@@ -48,29 +48,99 @@ __device__ __forceinline__ float activate(float x, float &slope) {
 }
 
 // ------------------------------------------------------------ adapters' terms
-// Both projections' adapter terms of a 32-row block as MFMA passes: for every
-// slot, adapter and 16 rank rows, U (fp32, as bf16 hi + lo, error < 2^-16 of
-// U; rows of other adapters zero) times the pages' rows.  kBlocks 32-column
-// blocks: block j takes projection kPair ? j : both.  kPair (the forward):
-// acc[0] is the gate's, acc[1] the up projection's, both of column col[0].
-// Otherwise (dX) both projections' terms go into both blocks, columns col[0]
-// and col[1].  Returns whether a page value that is not finite was left out
-// (see drop_nonfinite); terms_nonfinite adds those.
+// Both projections' adapter terms of a 16-row block and the wave's 64
+// accumulator columns as MFMA passes: for every slot, adapter and 16 rank rows,
+// U times the pages' rows.  U (fp32; rows of other adapters zero) is bf16 hi
+// in the first 16 of K and lo in the second (error < 2^-16 of U), against the
+// page rows twice.  kPair (the forward): columns 0 .. 31 are the gate's c0 ..,
+// 32 .. 63 the up projection's, the same c0 ...  Otherwise (dX) both
+// projections' terms go into all of c0 .. c0 + 63.
+// The page rows come in 16-byte loads through the wave's LDS, read transposed
+// from there; the last adapter's fragments are kept, so that a run of blocks
+// loads them once.
 struct Terms {
   ExpandArgs ex;
   const float *U_up;
   const void *b_up;
 };
 
+constexpr int kTermLds = 4096;             // bytes of LDS per wave
+
 template <bool kPair>
-__device__ __forceinline__ bool add_terms(const Terms &e, int row, bool row_ok, const int (&col)[2],
-                                          f32x16_t (&acc)[2]) {
-  const int lane = threadIdx.x & 63, half = lane >> 5;
+struct TermCache {
+  static constexpr int NF = kPair ? 4 : 8;
+  int key = -1;                            // first page id's place, or -1
+  bool dropped = false;                    // its values that are not finite were left out
+  bf16x8_t b[NF];                          // kPair: gate 0, 1, up 0, 1; else gate 0 .. 3, up 0 .. 3
+};
+
+// 8 bf16 values with those that are not finite zero; whether there were any.
+__device__ __forceinline__ bool drop8(uint4 &w) {
+  uint32_t v[4] = {w.x, w.y, w.z, w.w}, any = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    // the exponents' carry: bits 15 and 31 of a half that is not finite
+    const uint32_t x = (((v[e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u) >> 15;
+    any |= x;
+    v[e] &= ~((x << 16) - x);
+  }
+  w = make_uint4(v[0], v[1], v[2], v[3]);
+  return any != 0;
+}
+
+template <bool kPair>
+__device__ __forceinline__ void load_terms(const Terms &e, char *lds, int at, int nr, int c0, int N,
+                                           TermCache<kPair> &t) {
+  constexpr int CPL = kPair ? 4 : 8;       // lanes along a page's columns
+  constexpr int NL = kPair ? 1 : 2;        // loads of a projection
+  constexpr int PITCH = CPL * 16, SIZE = 16 * PITCH;
+  const int lane = threadIdx.x & 63, col = min(c0 + (lane % CPL) * 8, N - 8);
+  uint4 v[2][NL];
+#pragma unroll
+  for (int h = 0; h < NL; ++h) {
+    const int j = lane / CPL + h * (64 / CPL);
+    const int64_t row = int64_t(e.ex.page_ids[at + min(j, nr - 1)]) * e.ex.d_out + col;
+    v[0][h] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(e.ex.b_pages) + row);
+    v[1][h] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(e.b_up) + row);
+  }
+  bool bad = false;
+#pragma unroll
+  for (int h = 0; h < NL; ++h) {
+    const int j = lane / CPL + h * (64 / CPL);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      if (j >= nr) v[p][h] = make_uint4(0u, 0u, 0u, 0u);
+      bad |= drop8(v[p][h]);
+      *reinterpret_cast<uint4 *>(lds + p * SIZE + j * PITCH + (lane % CPL) * 16) = v[p][h];
+    }
+  }
+  t.dropped = __ballot(bad) != 0;
+  t.key = at;
+  // B operand: lane (column lane % 16, rank rows 8 (lane / 16 % 2) .. + 7)
+  constexpr int NB = kPair ? 2 : 4;        // blocks of a projection
+  typedef __attribute__((address_space(3))) v4i16_t lds_v4;
+  const int L = lane & 15, k = 8 * ((lane >> 4) & 1) + (L >> 2);
+#pragma unroll
+  for (int f = 0; f < 2 * NB; ++f) {
+    const char *p = lds + (f / NB) * SIZE + k * PITCH + (f % NB) * 32 + (L & 3) * 8;
+    const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4 *)(p));
+    const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4 *)(p + 4 * PITCH));
+    __builtin_memcpy(&t.b[f], &lo, 8);
+    __builtin_memcpy(reinterpret_cast<char *>(&t.b[f]) + 8, &hi, 8);
+  }
+}
+
+// Returns whether a page value that is not finite was left out of the block:
+// it would reach other adapters' rows as 0 . inf.  terms_nonfinite adds those.
+template <bool kPair>
+__device__ __forceinline__ bool add_terms(const Terms &e, char *lds, int row0, int M, int c0, int N,
+                                          f32x4_t (&acc)[4], TermCache<kPair> &t) {
+  const int lane = threadIdx.x & 63, row = row0 + (lane & 15);
   bool dropped = false;
   for (int k = 0; k < e.ex.K; ++k) {
     int4 sd = make_int4(-1, 0, 0, 0);
-    if (row_ok) sd = e.ex.slot_desc[int64_t(row) * e.ex.K + k];
-    unsigned long long pending = __ballot(sd.x >= 0) & 0xffffffffull;
+    if (row < M) sd = e.ex.slot_desc[int64_t(row) * e.ex.K + k];
+    unsigned long long pending = __ballot(sd.x >= 0) & 0xffffull;
     while (pending) {
       const int leader = __ffsll(pending) - 1;
       const int kps = __builtin_amdgcn_readfirstlane(__shfl(sd.w, leader, 64));
@@ -78,51 +148,32 @@ __device__ __forceinline__ bool add_terms(const Terms &e, int row, bool row_ok, 
       const bool mine = sd.x >= 0 && sd.w == kps && sd.y == kr;
       pending &= ~__ballot(mine);
       for (int jb = 0; jb < kr; jb += 16) {
-        const int nr = min(16, kr - jb);
-        const int pid = e.ex.page_ids[kps + jb + min(lane & 15, nr - 1)];
-        // lane (row lane % 32, or column): rank rows jb + 8 half .. + 7
+        const int nr = min(16, kr - jb), j0 = 8 * ((lane >> 4) & 1);
+        // A operand: lane (row lane % 16, rank rows j0 .. j0 + 7), hi or lo
+        bf16x8_t u[2];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          const float *U = p ? e.U_up : e.ex.U;
-          const uint16_t *B = static_cast<const uint16_t *>(p ? e.b_up : e.ex.b_pages);
-          constexpr int NB = kPair ? 1 : 2;
-          float uv[8];
-          bf16x8_t bf[NB];
+          const float *U = (p ? e.U_up : e.ex.U) + int64_t(sd.z) + jb;
+          uint32_t w[4];
+          float v[8];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const int j = half * 8 + q;
-            uv[q] = mine && j < nr ? U[int64_t(sd.z) + jb + j] : 0.f;
-          }
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            uint32_t w[4];
-#pragma unroll
-            for (int q = 0; q < 8; q += 2) {
-              const int ja = half * 8 + q;
-              const int pa = __shfl(pid, ja, 64), pb = __shfl(pid, ja + 1, 64);
-              uint32_t lo = B[int64_t(pa) * e.ex.d_out + col[b]], hi = B[int64_t(pb) * e.ex.d_out + col[b]];
-              if (ja >= nr) lo = 0;
-              if (ja + 1 >= nr) hi = 0;
-              w[q >> 1] = lo | (hi << 16);
-            }
-            __builtin_memcpy(&bf[b], w, 16);
-          }
-          dropped |= drop_nonfinite<NB>(bf);
-          uint32_t hw[4], lw[4];
+          for (int q = 0; q < 8; ++q) v[q] = mine && j0 + q < nr ? U[j0 + q] : 0.f;
 #pragma unroll
           for (int q = 0; q < 8; q += 2) {
-            const uint32_t h = f2bf2(uv[q], uv[q + 1]);
-            hw[q >> 1] = h;
-            lw[q >> 1] = f2bf2(uv[q] - bf_lo(h), uv[q + 1] - bf_hi(h));
+            const uint32_t h = f2bf2(v[q], v[q + 1]);
+            w[q >> 1] = lane < 32 ? h : f2bf2(v[q] - bf_lo(h), v[q + 1] - bf_hi(h));
           }
-          bf16x8_t hi, lo;
-          __builtin_memcpy(&hi, hw, 16);
-          __builtin_memcpy(&lo, lw, 16);
+          __builtin_memcpy(&u[p], w, 16);
+        }
+        if (t.key != kps + jb) load_terms<kPair>(e, lds, kps + jb, nr, c0, N, t);
+        dropped |= t.dropped;
 #pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            f32x16_t &a = acc[kPair ? p : b];
-            a = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hi, bf[b], a, 0, 0, 0);
-            a = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lo, bf[b], a, 0, 0, 0);
+        for (int b = 0; b < 4; ++b) {
+          if constexpr (kPair) {
+            acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u[b >> 1], t.b[b], acc[b], 0, 0, 0);
+          } else {
+            acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u[0], t.b[b], acc[b], 0, 0, 0);
+            acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u[1], t.b[4 + b], acc[b], 0, 0, 0);
           }
         }
       }
@@ -152,94 +203,94 @@ __device__ __forceinline__ float terms_nonfinite(const Terms &e, int row, int co
 
 // ------------------------------------------------------------ forward, tiles
 // A rows of X by 32 rows of the gate's and 32 of the up projection's weight in
-// turn (a wave's copies are all of one weight).
-template <int BM, int BN, int WM, int WN>
+// turn.
+template <typename C>
 struct GatedSrc {
-  using C = TileCfg<BM, BN, WM, WN>;
-  static_assert(C::B_INS * 8 == 32 && C::TN == 2, "a wave copies 32 rows of one weight");
-  const uint16_t *a, *b;
+  static_assert(C::TN == 4, "32 columns of each projection per wave");
+  const uint16_t *a, *b[2];
   uint32_t ao[C::A_INS], bo[C::B_INS];
-  int wave;
+  int wave, wm, wn;
   __device__ __forceinline__ void copy(uint32_t lds, int kt, int i) const {
-    if (i < C::A_INS) lds_dma16(a + kt * 64 + ao[i], lds + (wave * C::A_INS + i) * 1024);
-    else lds_dma16(b + kt * 64 + bo[i - C::A_INS], lds + BM * C::ROWB + (wave * C::B_INS + i - C::A_INS) * 1024);
+    if (i < C::A_INS) {
+      lds_dma16_s(a + kt * 64, ao[i], lds + (wave * C::A_INS + i) * 1024);
+    } else {
+      const int ib = wave * C::B_INS + i - C::A_INS;     // 8 rows of the B tile, all of one weight
+      lds_dma16_s(((ib >> 2) & 1 ? b[1] : b[0]) + kt * 64, bo[i - C::A_INS], lds + C::BM * C::ROWB + ib * 1024);
+    }
   }
   __device__ __forceinline__ bf16x8_t frag(const char *base, int s, int q) const {
-    const int frow = threadIdx.x & 31, wm = wave / WN, wn = wave % WN;
-    return frag_rows<C, WN>(base, s, q < C::TM ? (wm * C::TM + q) * 32 + frow
-                                               : BM + (wn * C::TN + q - C::TM) * 32 + frow);
+    return frag_rows(base, s, q < C::TM ? (wm * C::TM + q) * 16 : C::BM + (wn * C::TN + q - C::TM) * 16);
   }
 };
 
-template <int BM, int BN, int WM, int WN, int kAct>
-__global__ __launch_bounds__(WM * WN * 64, 1) void gated_tile_kernel(GatedArgs g) {
-  using C = TileCfg<BM, BN, WM, WN>;
+template <typename C, int kAct>
+__global__ __launch_bounds__(C::NT, 1) void gated_tile_kernel(GatedArgs g) {
   constexpr int SC = 64 + 4;                            // floats of a staged row: 32 of g, 32 of u
-  constexpr int NO = BN / 2;                            // output columns of the tile
+  constexpr int NO = C::BN / 2;                         // output columns of the tile
+  constexpr int WLDS = 16 * SC * 4 + kTermLds;          // bytes of a wave's epilogue
   __shared__ __attribute__((aligned(16))) char smem[2 * C::STAGE];
-  static_assert(C::NW * 32 * SC * 4 <= 2 * C::STAGE, "staging must fit in LDS");
+  static_assert(C::NW * WLDS <= 2 * C::STAGE, "staging must fit in LDS");
   int tm, tn;
-  if (!tile_of_workgroup(blockIdx.x, (g.M + BM - 1) / BM, (g.N + NO - 1) / NO, tm, tn)) return;
-  const int m0 = tm * BM, n0 = tn * NO;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / WN, wn = wave % WN;
+  if (!tile_of_workgroup(blockIdx.x, (g.M + C::BM - 1) / C::BM, (g.N + NO - 1) / NO, tm, tn)) return;
+  const int m0 = tm * C::BM, n0 = tn * NO;
+  const int lane = threadIdx.x & 63, wave = wave_id(), wm = wave / C::WN, wn = wave % C::WN;
 
-  GatedSrc<BM, BN, WM, WN> src;
-  src.wave = wave;
+  GatedSrc<C> src;
+  src.wave = wave; src.wm = wm; src.wn = wn;
   src.a = static_cast<const uint16_t *>(g.X) + int64_t(m0) * g.Kd;
-  src.b = static_cast<const uint16_t *>(g.W[wave & 1]) + int64_t(n0) * g.Kd;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) src.b[p] = static_cast<const uint16_t *>(g.W[p]) + int64_t(n0) * g.Kd;
 #pragma unroll
   for (int i = 0; i < C::A_INS; ++i) {
     const int row = (wave * C::A_INS + i) * 8 + (lane >> 3);
-    src.ao[i] = uint32_t(min(row, g.M - 1 - m0)) * uint32_t(g.Kd) + tswz(row, lane & 7) * 8;
+    src.ao[i] = (uint32_t(min(row, g.M - 1 - m0)) * uint32_t(g.Kd) + tswz(row, lane & 7) * 8) * 2;
   }
 #pragma unroll
   for (int i = 0; i < C::B_INS; ++i) {
-    const int row = i * 8 + (lane >> 3);                // of the wave's 32
-    src.bo[i] = uint32_t(min((wave >> 1) * 32 + row, g.N - 1 - n0)) * uint32_t(g.Kd) + tswz(row, lane & 7) * 8;
+    const int row = (wave * C::B_INS + i) * 8 + (lane >> 3);
+    const int of = (row >> 6) * 32 + (row & 31);        // of its weight
+    src.bo[i] = (uint32_t(min(of, g.N - 1 - n0)) * uint32_t(g.Kd) + tswz(row, lane & 7) * 8) * 2;
   }
-  f32x16_t acc[C::TM][C::TN];
-  tile_loop<BM, BN, WM, WN>(src, smem, g.Kd / 64, acc);
+  f32x4_t acc[C::TM][C::TN];
+  tile_loop<C>(src, smem, g.Kd / 64, acc);
 
   const Terms e{g.ex, g.U_up, g.b_up};
   const bool lora_on = expand_enabled(g.ex);
-  const int frow = lane & 31, half = lane >> 5;
   const int c0 = n0 + wn * 32;                          // the wave's output columns
-  const int col[2] = {min(c0 + frow, g.N - 1), 0};
-  float *stage = reinterpret_cast<float *>(smem) + wave * 32 * SC;
+  if (c0 >= g.N) return;
+  float *stage = reinterpret_cast<float *>(smem + wave * WLDS);
+  char *tlds = smem + wave * WLDS + 16 * SC * 4;
+  TermCache<true> cache;
 #pragma unroll
   for (int i = 0; i < C::TM; ++i) {
-    const int r0 = m0 + (wm * C::TM + i) * 32;
+    const int r0 = m0 + (wm * C::TM + i) * 16;
     bool dropped = false;
-    if (lora_on) dropped = add_terms<true>(e, r0 + frow, r0 + frow < g.M, col, acc[i]);
+    if (lora_on) dropped = add_terms<true>(e, tlds, r0, g.M, c0, g.N, acc[i], cache);
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int v = 0; v < 16; ++v)
-        stage[((v >> 2) * 8 + half * 4 + (v & 3)) * SC + j * 32 + frow] = acc[i][j][v];
+      for (int v = 0; v < 4; ++v) stage[acc_row(0, v) * SC + acc_col(j)] = acc[i][j][v];
     if (dropped) {
 #pragma unroll 1
-      for (int rr = 0; rr < 32 && r0 + rr < g.M; ++rr)
-        if (c0 + frow < g.N) stage[rr * SC + lane] += terms_nonfinite(e, r0 + rr, c0 + frow, half);
+      for (int rr = 0; rr < 16 && r0 + rr < g.M; ++rr)
+        stage[rr * SC + lane] += terms_nonfinite(e, r0 + rr, c0 + (lane & 31), lane >> 5);
     }
-    // a lane takes 8 columns of one of 16 rows
+    // a lane takes 8 columns of one of the rows
+    const int rr = lane >> 2, row = r0 + rr, cc = (lane & 3) * 8;
+    if (row >= g.M) continue;
+    float gv[8], uv[8], h[8];
+    Elem<float>::load8(stage + rr * SC + cc, gv);
+    Elem<float>::load8(stage + rr * SC + 32 + cc, uv);
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int rr = q * 16 + (lane >> 2), row = r0 + rr, cc = (lane & 3) * 8;
-      if (row >= g.M || c0 + cc >= g.N) continue;
-      float gv[8], uv[8], h[8];
-      Elem<float>::load8(stage + rr * SC + cc, gv);
-      Elem<float>::load8(stage + rr * SC + 32 + cc, uv);
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        float slope;
-        h[x] = activate<kAct, true>(gv[x], slope) * uv[x];
-      }
-      const int64_t at = int64_t(row) * g.N + c0 + cc;
-      store8_nt(static_cast<uint16_t *>(g.H) + at, h);
-      if (g.pre_gate) {
-        store8_nt(static_cast<uint16_t *>(g.pre_gate) + at, gv);
-        store8_nt(static_cast<uint16_t *>(g.pre_up) + at, uv);
-      }
+    for (int x = 0; x < 8; ++x) {
+      float slope;
+      h[x] = activate<kAct, true>(gv[x], slope) * uv[x];
+    }
+    const int64_t at = int64_t(row) * g.N + c0 + cc;
+    store8_nt(static_cast<uint16_t *>(g.H) + at, h);
+    if (g.pre_gate) {
+      store8_nt(static_cast<uint16_t *>(g.pre_gate) + at, gv);
+      store8_nt(static_cast<uint16_t *>(g.pre_up) + at, uv);
     }
   }
 }
@@ -333,37 +384,39 @@ __global__ __launch_bounds__(256) void gated_act_grad_kernel(const E *dH, const 
 }
 
 // K tiles of dg.Wg^T, then those of du.Wu^T.
-template <int BM, int BN, int WM, int WN>
+template <typename C>
 struct GatedGradSrc {
-  using C = TileCfg<BM, BN, WM, WN>;
   const uint16_t *a[2], *b[2];
   uint32_t ao[C::A_INS], bo[C::B_INS];
-  int wave, kt1;
+  int wave, wm, wn, kt1;
   __device__ __forceinline__ void copy(uint32_t lds, int kt, int i) const {
-    const int p = kt >= kt1, k = (kt - (p ? kt1 : 0)) * 64;
-    if (i < C::A_INS) lds_dma16((p ? a[1] : a[0]) + k + ao[i], lds + (wave * C::A_INS + i) * 1024);
-    else lds_dma16((p ? b[1] : b[0]) + k + bo[i - C::A_INS], lds + BM * C::ROWB + (wave * C::B_INS + i - C::A_INS) * 1024);
+    const bool p = kt >= kt1;
+    const int k = (p ? kt - kt1 : kt) * 64;
+    if (i < C::A_INS) {
+      lds_dma16_s((p ? a[1] : a[0]) + k, ao[i], lds + (wave * C::A_INS + i) * 1024);
+    } else {
+      lds_dma16_s((p ? b[1] : b[0]) + k, bo[i - C::A_INS],
+                  lds + C::BM * C::ROWB + (wave * C::B_INS + i - C::A_INS) * 1024);
+    }
   }
   __device__ __forceinline__ bf16x8_t frag(const char *base, int s, int q) const {
-    const int frow = threadIdx.x & 31, wm = wave / WN, wn = wave % WN;
-    return frag_rows<C, WN>(base, s, q < C::TM ? (wm * C::TM + q) * 32 + frow
-                                               : BM + (wn * C::TN + q - C::TM) * 32 + frow);
+    return frag_rows(base, s, q < C::TM ? (wm * C::TM + q) * 16 : C::BM + (wn * C::TN + q - C::TM) * 16);
   }
 };
 
-template <int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM * WN * 64, 1) void gated_grad_x_tile_kernel(GatedGradXArgs g) {
-  using C = TileCfg<BM, BN, WM, WN>;
-  constexpr int SC = 64 + 4, RS = 32 + 8;               // a wave stages 32 rows, and 8 of the adapters' term
-  static_assert(C::TN == 2, "64 columns per wave");
+template <typename C>
+__global__ __launch_bounds__(C::NT, 1) void gated_grad_x_tile_kernel(GatedGradXArgs g) {
+  constexpr int SC = 64 + 4;                            // a wave stages 16 rows, and those of the adapters' term
+  constexpr int WLDS = 2 * 16 * SC * 4 + kTermLds;
+  static_assert(C::TN == 4, "64 columns per wave");
   __shared__ __attribute__((aligned(16))) char smem[2 * C::STAGE];
-  static_assert(C::NW * RS * SC * 4 <= 2 * C::STAGE, "staging must fit in LDS");
+  static_assert(C::NW * WLDS <= 2 * C::STAGE, "staging must fit in LDS");
   int tm, tn;
-  if (!tile_of_workgroup(blockIdx.x, (g.M + BM - 1) / BM, (g.N + BN - 1) / BN, tm, tn)) return;
-  const int m0 = tm * BM, n0 = tn * BN;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / WN, wn = wave % WN;
-  GatedGradSrc<BM, BN, WM, WN> src;
-  src.wave = wave;
+  if (!tile_of_workgroup(blockIdx.x, (g.M + C::BM - 1) / C::BM, (g.N + C::BN - 1) / C::BN, tm, tn)) return;
+  const int m0 = tm * C::BM, n0 = tn * C::BN;
+  const int lane = threadIdx.x & 63, wave = wave_id(), wm = wave / C::WN, wn = wave % C::WN;
+  GatedGradSrc<C> src;
+  src.wave = wave; src.wm = wm; src.wn = wn;
   src.kt1 = g.Kd / 64;
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
@@ -373,62 +426,57 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void gated_grad_x_tile_kernel(Gate
 #pragma unroll
   for (int i = 0; i < C::A_INS; ++i) {
     const int row = (wave * C::A_INS + i) * 8 + (lane >> 3);
-    src.ao[i] = uint32_t(min(row, g.M - 1 - m0)) * uint32_t(g.Kd) + tswz(row, lane & 7) * 8;
+    src.ao[i] = (uint32_t(min(row, g.M - 1 - m0)) * uint32_t(g.Kd) + tswz(row, lane & 7) * 8) * 2;
   }
 #pragma unroll
   for (int i = 0; i < C::B_INS; ++i) {
     const int row = (wave * C::B_INS + i) * 8 + (lane >> 3);
-    src.bo[i] = uint32_t(min(row, g.N - 1 - n0)) * uint32_t(g.Kd) + tswz(row, lane & 7) * 8;
+    src.bo[i] = (uint32_t(min(row, g.N - 1 - n0)) * uint32_t(g.Kd) + tswz(row, lane & 7) * 8) * 2;
   }
-  f32x16_t acc[C::TM][C::TN];
-  tile_loop<BM, BN, WM, WN>(src, smem, 2 * src.kt1, acc);
+  f32x4_t acc[C::TM][C::TN];
+  tile_loop<C>(src, smem, 2 * src.kt1, acc);
 
   const Terms e{g.ex, g.U_up, g.b_up};
   const bool lora_on = expand_enabled(g.ex);
-  const int frow = lane & 31, half = lane >> 5, vr = lane >> 3, vc = (lane & 7) * 8;
-  const int c0 = n0 + wn * 64;
-  const int col[2] = {min(c0 + frow, g.N - 1), min(c0 + 32 + frow, g.N - 1)};
-  float *stage = reinterpret_cast<float *>(smem) + wave * RS * SC, *lstage = stage + 32 * SC;
+  const int vr = lane >> 3, vc = (lane & 7) * 8, c0 = n0 + wn * 64;
+  if (c0 >= g.N) return;
+  float *stage = reinterpret_cast<float *>(smem + wave * WLDS), *lstage = stage + 16 * SC;
+  char *tlds = smem + wave * WLDS + 2 * 16 * SC * 4;
+  TermCache<false> cache;
 #pragma unroll
   for (int i = 0; i < C::TM; ++i) {
-    const int r0 = m0 + (wm * C::TM + i) * 32;
+    const int r0 = m0 + (wm * C::TM + i) * 16;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 4; ++j) {
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        stage[((v >> 2) * 8 + half * 4 + (v & 3)) * SC + j * 32 + frow] = acc[i][j][v];
-        acc[i][j][v] = 0.f;
-      }
+      for (int v = 0; v < 4; ++v) stage[acc_row(0, v) * SC + acc_col(j)] = acc[i][j][v];
+      acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
     bool dropped = false;
-    if (lora_on) dropped = add_terms<false>(e, r0 + frow, r0 + frow < g.M, col, acc[i]);
-    // the adapters' term a quarter of the rows at a time: MFMA registers
-    // 4 q .. 4 q + 3 hold rows 8 q .. 8 q + 7
+    if (lora_on) dropped = add_terms<false>(e, tlds, r0, g.M, c0, g.N, acc[i], cache);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int row = r0 + q * 8 + vr;
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int v = 4 * q; v < 4 * q + 4; ++v) lstage[(half * 4 + (v & 3)) * SC + j * 32 + frow] = acc[i][j][v];
-      if (dropped) {
+      for (int v = 0; v < 4; ++v) lstage[acc_row(0, v) * SC + acc_col(j)] = acc[i][j][v];
+    if (dropped) {
 #pragma unroll 1
-        for (int rr = 0; rr < 8 && r0 + q * 8 + rr < g.M; ++rr)
-          if (c0 + lane < g.N)
-            lstage[rr * SC + lane] += terms_nonfinite(e, r0 + q * 8 + rr, c0 + lane, 0) +
-                                      terms_nonfinite(e, r0 + q * 8 + rr, c0 + lane, 1);
-      }
-      if (row < g.M && c0 + vc < g.N) {
-        float b[8], l[8];
-        Elem<float>::load8(stage + (q * 8 + vr) * SC + vc, b);
-        Elem<float>::load8(lstage + vr * SC + vc, l);
-        const int64_t at = int64_t(row) * g.N + c0 + vc;
-        uint2 mw = make_uint2(0x01010101u, 0x01010101u);
-        if (g.mask) mw = *reinterpret_cast<const uint2 *>(g.mask + at);
+      for (int rr = 0; rr < 16 && r0 + rr < g.M; ++rr)
+        lstage[rr * SC + lane] += terms_nonfinite(e, r0 + rr, c0 + lane, 0) + terms_nonfinite(e, r0 + rr, c0 + lane, 1);
+    }
 #pragma unroll
-        for (int x = 0; x < 8; ++x)
-          b[x] += float(((x < 4 ? mw.x : mw.y) >> (8 * (x & 3))) & 0xffu) * l[x];
-        store8_nt(static_cast<uint16_t *>(g.dX) + at, b);
-      }
+    for (int q = 0; q < 2; ++q) {
+      const int rr = q * 8 + vr, row = r0 + rr;
+      if (row >= g.M) continue;
+      float b[8], l[8];
+      Elem<float>::load8(stage + rr * SC + vc, b);
+      Elem<float>::load8(lstage + rr * SC + vc, l);
+      const int64_t at = int64_t(row) * g.N + c0 + vc;
+      uint2 mw = make_uint2(0x01010101u, 0x01010101u);
+      if (g.mask) mw = *reinterpret_cast<const uint2 *>(g.mask + at);
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        b[x] += float(((x < 4 ? mw.x : mw.y) >> (8 * (x & 3))) & 0xffu) * l[x];
+      store8_nt(static_cast<uint16_t *>(g.dX) + at, b);
     }
   }
 }
@@ -461,6 +509,8 @@ __global__ __launch_bounds__(NW * 64) void gated_grad_x_epilogue_kernel(GatedGra
   }
   if (ok) Cols<E, 8>::store(static_cast<E *>(g.dX) + int64_t(row) * g.N + col, v);
 }
+
+using Big = LoopCfg<256, 256, 2, 4>;
 
 template <typename E, int kAct>
 void launch_epilogue_rows(const GatedArgs &g, hipStream_t s) {
@@ -497,11 +547,11 @@ hipError_t launch_gated_tiles(const GatedArgs &g, hipStream_t s) {
   const int tiles = ((g.M + 255) / 256) * ((g.N + 127) / 128);
   const dim3 grid(8 * unsigned((tiles + 7) / 8)), block(512);
   if (g.act == LORA_ACT_SILU)
-    hipLaunchKernelGGL((gated_tile_kernel<256, 256, 2, 4, LORA_ACT_SILU>), grid, block, 0, s, g);
+    hipLaunchKernelGGL((gated_tile_kernel<Big, LORA_ACT_SILU>), grid, block, 0, s, g);
   else if (g.act == LORA_ACT_GELU)
-    hipLaunchKernelGGL((gated_tile_kernel<256, 256, 2, 4, LORA_ACT_GELU>), grid, block, 0, s, g);
+    hipLaunchKernelGGL((gated_tile_kernel<Big, LORA_ACT_GELU>), grid, block, 0, s, g);
   else
-    hipLaunchKernelGGL((gated_tile_kernel<256, 256, 2, 4, LORA_ACT_GELU_TANH>), grid, block, 0, s, g);
+    hipLaunchKernelGGL((gated_tile_kernel<Big, LORA_ACT_GELU_TANH>), grid, block, 0, s, g);
   return hipGetLastError();
 }
 
@@ -526,7 +576,7 @@ bool gated_grad_x_fused(int T, int d_in, int dtype) {
 
 hipError_t launch_gated_grad_x_tiles(const GatedGradXArgs &g, hipStream_t s) {
   const int tiles = ((g.M + 255) / 256) * ((g.N + 255) / 256);
-  hipLaunchKernelGGL((gated_grad_x_tile_kernel<256, 256, 2, 4>), dim3(8 * unsigned((tiles + 7) / 8)), dim3(512), 0, s, g);
+  hipLaunchKernelGGL((gated_grad_x_tile_kernel<Big>), dim3(8 * unsigned((tiles + 7) / 8)), dim3(512), 0, s, g);
   return hipGetLastError();
 }
 

@@ -1,7 +1,14 @@
-// The K loop of a bf16 output tile over two LDS stages, for products whose
-// operands are not plain rows of two matrices: the gated block (two weights
-// side by side, or two products added along K) and the cross entropy (weights
-// read along their other axis).  Internal to liblora (gfx950 only).
+// The K loop of a bf16 output tile over two LDS stages, for the products of
+// the gated block (two weights side by side, or two products added along K)
+// and of the cross entropy (weights read along their other axis).
+// Internal to liblora (gfx950 only).
+//
+// v_mfma_f32_16x16x32_bf16 with scalar-based copies: on 8192 x 8192 x 4096 a
+// 256 x 256 tile of eight waves runs at 1480 TFLOP/s in a steady state, where
+// 32x32x16 MFMAs and copies with 64-bit lane addresses reach 1270.  The card's
+// power limit sets the clock there (1.7 of 2.4 GHz): the 16x16x32 form moves
+// its accumulators a quarter as often per product, and a copy with a scalar
+// base and a constant 32-bit lane offset has no address arithmetic.
 #pragma once
 
 #include "gemm_tile.h"
@@ -9,95 +16,114 @@
 namespace lora {
 namespace {
 
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef short v4i16_t __attribute__((ext_vector_type(4)));
 
-// Where a tile's operands come from.  `copy(lds, kt, i)` issues copy i of the
-// wave's TileCfg::LPW copies of K tile kt (64 of K) into the stage at LDS
-// address lds; `frag(base, s, q)` reads fragment q (A blocks 0 .. TM-1, then B
-// blocks) of 16-wide K step s from the stage at base.
-//
-// Rows of 64 of K, 128 bytes each, in tswz order: the A operand everywhere and
-// the B operand of products with both sides along K.
-template <typename C, int WN>
-__device__ __forceinline__ bf16x8_t frag_rows(const char *base, int s, int row) {
-  const int lane = threadIdx.x & 63;
-  return *reinterpret_cast<const bf16x8_t *>(base + row * C::ROWB + (tswz(lane & 31, 2 * s + (lane >> 5)) << 4));
+// A tile of BM x BN over WM x WN waves, in blocks of 16 x 16.
+template <int BM_, int BN_, int WM_, int WN_>
+struct LoopCfg {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int NW = WM * WN, NT = NW * 64;
+  static constexpr int ROWB = 128;                     // bytes per row of 64 of K
+  static constexpr int STAGE = (BM + BN) * ROWB;       // bytes per LDS stage
+  static constexpr int TM = BM / (WM * 16), TN = BN / (WN * 16);
+  static constexpr int A_INS = BM / 8 / NW, B_INS = BN / 8 / NW, LPW = A_INS + B_INS;
+  static_assert(A_INS * 8 * NW == BM && B_INS * 8 * NW == BN, "tile rows / waves");
+};
+
+// One 16-byte copy per lane from base + off to LDS at lds + 16 lane; base and
+// lds are the wave's.  (The s_nop: an LDS DMA needs a wait state after the
+// scalar write of m0.)
+__device__ __forceinline__ void lds_dma16_s(const void *base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(off), "s"(base), "s"(lds)
+               : "memory", "m0");
 }
 
-// The loop: acc += A.B over nk K tiles.  The fragments of K step s + 1 are
-// read from LDS while the MFMAs of step s run (two register sets); before the
-// last step of a K tile one barrier frees the stage just read (the copies of
-// the tile after next go into it, spread over that step's MFMAs) and publishes
-// the next tile.  Each step's instructions are pinned in this order.  On
-// return no copy is in flight and every wave is done with the stages.
-template <int BM, int BN, int WM, int WN, typename P>
-__device__ __forceinline__ void tile_loop(const P &p, char *smem, int nk,
-                                          f32x16_t (&acc)[TileCfg<BM, BN, WM, WN>::TM]
-                                                         [TileCfg<BM, BN, WM, WN>::TN]) {
-  using C = TileCfg<BM, BN, WM, WN>;
-  constexpr int TM = C::TM, TN = C::TN;
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6); }
+
+// Fragment of 16 rows from `row0` (a multiple of 16) of a stage whose rows are
+// 64 of K in tswz order: lane (row lane % 16, k of 8 (lane / 16) .. + 7) of
+// 32-wide K step s.
+__device__ __forceinline__ bf16x8_t frag_rows(const char *base, int s, int row0) {
+  const int lane = threadIdx.x & 63;
+  return *reinterpret_cast<const bf16x8_t *>(base + row0 * 128 + (lane & 15) * 128 +
+                                             (tswz(lane & 15, 4 * s + (lane >> 4)) << 4));
+}
+
+// acc += A.B over nk K tiles of 64.  Src: `copy(lds, kt, i)` issues copy i of
+// the wave's LPW copies of K tile kt into the stage at LDS address lds;
+// `frag(base, s, q)` reads fragment q (A blocks 0 .. TM-1, then B blocks) of K
+// step s from the stage at base.
+// The fragments of a step are read from LDS while the MFMAs of the step before
+// run (two register sets).  Between the two steps of a K tile one barrier frees
+// the stage just read (the copies of the tile after next go into it, spread
+// over the second step's MFMAs) and publishes the next tile.  The instructions
+// of a step are pinned in this order; every other row of blocks runs backwards,
+// so that one operand of an MFMA is always the last one's.  On return no copy
+// is in flight and every wave is done with the stages.
+template <typename C, typename Src>
+__device__ __forceinline__ void tile_loop(const Src &p, char *smem, int nk, f32x4_t (&acc)[C::TM][C::TN]) {
+  constexpr int TM = C::TM, TN = C::TN, NM = TM * TN, NQ = TM + TN, LPW = C::LPW;
   char *const st0 = smem;
   char *const st1 = smem + C::STAGE;
+  const uint32_t l0 = __builtin_amdgcn_readfirstlane(lds_addr(smem)), l1 = l0 + C::STAGE;
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+    for (int j = 0; j < TN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   if (nk <= 0) return;
 
   bf16x8_t fa0[TM], fb0[TN], fa1[TM], fb1[TN];
-  auto kstep = [&](auto mode, bf16x8_t (&xa)[TM], bf16x8_t (&xb)[TN], bf16x8_t (&ya)[TM],
-                   bf16x8_t (&yb)[TN], const char *src, int s_next, char *dst,
-                   int kn) __attribute__((always_inline)) {
-    constexpr int MD = decltype(mode)::value;   // bit 0: read the next fragments, bit 1: copy tile kn
-    constexpr int NM = TM * TN, NQ = TM + TN;
-    static_assert(NQ <= NM, "one fragment read after each of the first MFMAs");
+  // copies: mode 1 issues those of tile kn into the stage at `dst`
+  auto step = [&](auto mode, bf16x8_t (&xa)[TM], bf16x8_t (&xb)[TN], bf16x8_t (&ya)[TM], bf16x8_t (&yb)[TN],
+                  const char *src, int s, uint32_t dst, int kn) __attribute__((always_inline)) {
+    constexpr bool kCopy = decltype(mode)::value != 0;
+    // a fragment read after every kPer-th MFMA
+    constexpr int kPer = NM >= 2 * NQ ? 2 : 1;
+    static_assert(NM >= NQ, "a fragment read after an MFMA each");
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
-      acc[m / TN][m % TN] =
-          __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[m / TN], xb[m % TN], acc[m / TN][m % TN], 0, 0, 0);
-      if constexpr ((MD & 1) != 0) {
-        const int q = frag_order<TM, TN>(m);
-        if (m < NQ) {
-          if (q < TM) ya[q] = p.frag(src, s_next, q);
-          else yb[q - TM] = p.frag(src, s_next, q);
-        }
+      const int i = m / TN, j = (i & 1) ? TN - 1 - m % TN : m % TN;
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa[i], xb[j], acc[i][j], 0, 0, 0);
+      if (m % kPer == 0 && m / kPer < NQ) {
+        const int q = frag_order<TM, TN>(m / kPer);
+        if (q < TM) ya[q] = p.frag(src, s, q);
+        else yb[q - TM] = p.frag(src, s, q);
       }
-      if constexpr ((MD & 2) != 0) {
+      if constexpr (kCopy) {
 #pragma unroll
-        for (int c = m * C::LPW / NM; c < (m + 1) * C::LPW / NM; ++c) p.copy(lds_addr(dst), kn, c);
+        for (int c = m * LPW / NM; c < (m + 1) * LPW / NM; ++c) p.copy(dst, kn, c);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
 #pragma unroll
-  for (int c = 0; c < C::LPW; ++c) p.copy(lds_addr(st0), 0, c);
-  if (nk > 1) {
+  for (int c = 0; c < LPW; ++c) p.copy(l0, 0, c);
 #pragma unroll
-    for (int c = 0; c < C::LPW; ++c) p.copy(lds_addr(st1), 1, c);
-    wait_vmcnt<C::LPW>();
-  } else {
-    wait_vmcnt<0>();
-  }
+  for (int c = 0; c < LPW; ++c) p.copy(l1, min(1, nk - 1), c);
+  wait_vmcnt<LPW>();
   lds_bar();
 #pragma unroll
-  for (int q = 0; q < TM + TN; ++q) {
+  for (int q = 0; q < NQ; ++q) {
     if (q < TM) fa0[q] = p.frag(st0, 0, q);
     else fb0[q - TM] = p.frag(st0, 0, q);
   }
   // past the end the body stays the same: the copy repeats the last tile into
-  // a stage no one reads again, and the reads of nxt go unused
-  for (int kt = 0; kt < nk; ++kt) {
-    char *const cur = (kt & 1) ? st1 : st0;
-    char *const nxt = (kt & 1) ? st0 : st1;
-    kstep(std::integral_constant<int, 1>{}, fa0, fb0, fa1, fb1, cur, 1, cur, 0);
-    kstep(std::integral_constant<int, 1>{}, fa1, fb1, fa0, fb0, cur, 2, cur, 0);
-    kstep(std::integral_constant<int, 1>{}, fa0, fb0, fa1, fb1, cur, 3, cur, 0);
+  // a stage that no one reads again, and the reads of the next stage go unused
+  auto tile = [&](int kt, const char *cur, const char *nxt, uint32_t dst) __attribute__((always_inline)) {
+    step(std::integral_constant<int, 0>{}, fa0, fb0, fa1, fb1, cur, 1, dst, 0);
     wait_vmcnt<0>();   // tile kt + 1, the only copies in flight, has landed
     lds_bar();         // for every wave, and every wave has read cur
-    kstep(std::integral_constant<int, 3>{}, fa1, fb1, fa0, fb0, nxt, 0, cur, min(kt + 2, nk - 1));
+    step(std::integral_constant<int, 1>{}, fa1, fb1, fa0, fb0, nxt, 0, dst, min(kt + 2, nk - 1));
+  };
+  int kt = 0;
+  for (; kt + 1 < nk; kt += 2) {
+    tile(kt, st0, st1, l0);
+    tile(kt + 1, st1, st0, l1);
   }
+  if (kt < nk) tile(kt, st0, st1, l0);
   wait_vmcnt<0>();
   lds_bar();
 }
@@ -112,6 +138,11 @@ __device__ __forceinline__ bool tile_of_workgroup(int b, int tiles_m, int tiles_
   tile_coords(t, tiles_m, tiles_n, tm, tn);
   return true;
 }
+
+// Row of the wave's part of the tile that lane's register v of block i holds,
+// and its column in block j.
+__device__ __forceinline__ int acc_row(int i, int v) { return i * 16 + (int(threadIdx.x & 63) >> 4) * 4 + v; }
+__device__ __forceinline__ int acc_col(int j) { return j * 16 + int(threadIdx.x & 15); }
 
 }  // namespace
 }  // namespace lora
