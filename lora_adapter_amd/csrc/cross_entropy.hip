@@ -209,8 +209,24 @@ __global__ __launch_bounds__(C::NT, 1) void ce_logits_kernel(CeArgs c) {
     const int row = (wave * C::B_INS + i) * 8 + lrow;
     src.bo[i] = (uint32_t(min(row, c.a.V - 1 - n0)) * uint32_t(d) + tswz(row, lane & 7) * 8) * 2;
   }
+  // ref and target of the tile's rows, fetched under the K loop: as loads of
+  // the epilogue they were a third of it
+  __shared__ float s_ref[C::BM];
+  __shared__ int s_y[C::BM];
+  float ref = 0.f;
+  int y = -1;
+  if (int(threadIdx.x) < C::BM) {
+    const int r = c.row0 + min(m0 + int(threadIdx.x), M - 1);
+    ref = ref_of(c.w.ly[r]);
+    y = c.a.targets[c.w.rows[r]];
+  }
   f32x4_t acc[C::TM][C::TN];
   tile_loop<C>(src, smem, d / 64, acc);
+  if (int(threadIdx.x) < C::BM) {
+    s_ref[threadIdx.x] = ref;
+    s_y[threadIdx.x] = y;
+  }
+  lds_bar();
 
   // through the wave's own LDS, to lanes that hold 8 columns of a row
   float *stage = reinterpret_cast<float *>(smem) + wave * 32 * SC;
@@ -225,13 +241,11 @@ __global__ __launch_bounds__(C::NT, 1) void ce_logits_kernel(CeArgs c) {
         for (int v = 0; v < 4; ++v) stage[acc_row(h, v) * SC + acc_col(j)] = acc[i + h][j][v];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int lr = m0 + (wm * C::TM + i) * 16 + q * 8 + vr;
-      const bool ok = lr < M;
-      const int r = c.row0 + (ok ? lr : M - 1);
+      const int tr = (wm * C::TM + i) * 16 + q * 8 + vr, lr = m0 + tr;
       const float4 lo = *reinterpret_cast<const float4 *>(stage + (q * 8 + vr) * SC + (lane & 7) * 8);
       const float4 hi = *reinterpret_cast<const float4 *>(stage + (q * 8 + vr) * SC + (lane & 7) * 8 + 4);
       float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-      ce_store8<uint16_t>(c, x, lr, ok, col, ref_of(c.w.ly[r]), c.a.targets[c.w.rows[r]]);
+      ce_store8<uint16_t>(c, x, lr, lr < M, col, s_ref[tr], s_y[tr]);
     }
   }
 }

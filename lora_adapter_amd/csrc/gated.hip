@@ -182,6 +182,101 @@ __device__ __forceinline__ bool add_terms(const Terms &e, char *lds, int row0, i
   return dropped;
 }
 
+// The common case (one slot for each token, ranks of at most 16): the tile's
+// slot descriptors are fetched under the K loop, and U of all its rows goes to
+// LDS at once, as the bf16 fragments of add_terms; block by block each of
+// those is a round trip with the matrix cores idle (8192 x 4096 -> 11008, three
+// outputs: 1403 -> 1240 us).
+template <typename C>
+struct TileTerms {
+  int4 sd[C::BM];                          // .x < 0: no adapter
+  uint16_t u[2][2][C::BM][16];             // [projection][hi, lo][row][rank row]
+  int wide;                                // a rank over 16
+};
+
+// Slot descriptor of tile row threadIdx.x, or none.
+template <typename C>
+__device__ __forceinline__ int4 tile_desc(const ExpandArgs &ex, int m0, int M) {
+  const int row = m0 + int(threadIdx.x);
+  if (int(threadIdx.x) >= C::BM || row >= M || ex.K != 1 || ex.U == nullptr) return make_int4(-1, 0, 0, 0);
+  return ex.slot_desc[row];
+}
+
+// After the K loop: fills t; false where the tile takes add_terms instead.
+// t lies in the stages, which the loop has left.
+template <typename C>
+__device__ __forceinline__ bool tile_terms(const Terms &e, TileTerms<C> &t, int4 sd) {
+  const int tid = threadIdx.x;
+  if (tid == 0) t.wide = 0;
+  lds_bar();
+  if (tid < C::BM) {
+    t.sd[tid] = sd;
+    if (sd.x >= 0 && sd.y > 16) t.wide = 1;
+  }
+  lds_bar();
+  if (__builtin_amdgcn_readfirstlane(t.wide)) return false;
+  // a thread takes 8 rank rows of one token
+  for (int at = tid; at < 2 * C::BM; at += C::NT) {
+    const int r = at >> 1, j0 = (at & 1) * 8;
+    const int4 d = t.sd[r];
+    float v[2][8];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const float *U = (p ? e.U_up : e.ex.U) + int64_t(d.z) + j0;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[p][q] = d.x >= 0 && j0 + q < d.y ? U[q] : 0.f;
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      uint32_t h[4], l[4];
+#pragma unroll
+      for (int q = 0; q < 8; q += 2) {
+        h[q >> 1] = f2bf2(v[p][q], v[p][q + 1]);
+        l[q >> 1] = f2bf2(v[p][q] - bf_lo(h[q >> 1]), v[p][q + 1] - bf_hi(h[q >> 1]));
+      }
+      *reinterpret_cast<uint4 *>(&t.u[p][0][r][j0]) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4 *>(&t.u[p][1][r][j0]) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+  }
+  lds_bar();
+  return true;
+}
+
+// add_terms from them; tr: the block's first row in the tile.
+template <bool kPair, typename C>
+__device__ __forceinline__ bool add_tile_terms(const Terms &e, const TileTerms<C> &tt, char *lds, int tr, int c0,
+                                               int N, f32x4_t (&acc)[4], TermCache<kPair> &t) {
+  const int lane = threadIdx.x & 63;
+  const int4 sd = tt.sd[tr + (lane & 15)];
+  bf16x8_t u[2];
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+    u[p] = *reinterpret_cast<const bf16x8_t *>(&tt.u[p][lane >> 5][tr + (lane & 15)][8 * ((lane >> 4) & 1)]);
+  bool dropped = false;
+  unsigned long long pending = __ballot(sd.x >= 0) & 0xffffull;
+  while (pending) {
+    const int leader = __ffsll(pending) - 1;
+    const int kps = __builtin_amdgcn_readfirstlane(__shfl(sd.w, leader, 64));
+    const int kr = __builtin_amdgcn_readfirstlane(__shfl(sd.y, leader, 64));
+    const bool mine = sd.x >= 0 && sd.w == kps && sd.y == kr;
+    pending &= ~__ballot(mine);
+    bf16x8_t um[2] = {u[0], u[1]};
+    if (!mine) um[0] = um[1] = bf16x8_t{};
+    if (t.key != kps) load_terms<kPair>(e, lds, kps, kr, c0, N, t);
+    dropped |= t.dropped;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      if constexpr (kPair) {
+        acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(um[b >> 1], t.b[b], acc[b], 0, 0, 0);
+      } else {
+        acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(um[0], t.b[b], acc[b], 0, 0, 0);
+        acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(um[1], t.b[4 + b], acc[b], 0, 0, 0);
+      }
+    }
+  }
+  return dropped;
+}
+
 // What add_terms left out: the products of U with the page values that are not
 // finite, of token `row` at column col, for projection p.  Rare.
 __device__ __forceinline__ float terms_nonfinite(const Terms &e, int row, int col, int p) {
@@ -228,8 +323,9 @@ __global__ __launch_bounds__(C::NT, 1) void gated_tile_kernel(GatedArgs g) {
   constexpr int SC = 64 + 4;                            // floats of a staged row: 32 of g, 32 of u
   constexpr int NO = C::BN / 2;                         // output columns of the tile
   constexpr int WLDS = 16 * SC * 4 + kTermLds;          // bytes of a wave's epilogue
+  constexpr int TT = C::NW * WLDS;                      // the tile's terms lie behind those
   __shared__ __attribute__((aligned(16))) char smem[2 * C::STAGE];
-  static_assert(C::NW * WLDS <= 2 * C::STAGE, "staging must fit in LDS");
+  static_assert(TT % 16 == 0 && TT + sizeof(TileTerms<C>) <= 2 * C::STAGE, "staging must fit in LDS");
   int tm, tn;
   if (!tile_of_workgroup(blockIdx.x, (g.M + C::BM - 1) / C::BM, (g.N + NO - 1) / NO, tm, tn)) return;
   const int m0 = tm * C::BM, n0 = tn * NO;
@@ -251,11 +347,14 @@ __global__ __launch_bounds__(C::NT, 1) void gated_tile_kernel(GatedArgs g) {
     const int of = (row >> 6) * 32 + (row & 31);        // of its weight
     src.bo[i] = (uint32_t(min(of, g.N - 1 - n0)) * uint32_t(g.Kd) + tswz(row, lane & 7) * 8) * 2;
   }
+  const int4 sd = tile_desc<C>(g.ex, m0, g.M);
   f32x4_t acc[C::TM][C::TN];
   tile_loop<C>(src, smem, g.Kd / 64, acc);
 
   const Terms e{g.ex, g.U_up, g.b_up};
   const bool lora_on = expand_enabled(g.ex);
+  TileTerms<C> &tt = *reinterpret_cast<TileTerms<C> *>(smem + TT);
+  const bool common = lora_on && g.ex.K == 1 && tile_terms<C>(e, tt, sd);
   const int c0 = n0 + wn * 32;                          // the wave's output columns
   if (c0 >= g.N) return;
   float *stage = reinterpret_cast<float *>(smem + wave * WLDS);
@@ -265,7 +364,8 @@ __global__ __launch_bounds__(C::NT, 1) void gated_tile_kernel(GatedArgs g) {
   for (int i = 0; i < C::TM; ++i) {
     const int r0 = m0 + (wm * C::TM + i) * 16;
     bool dropped = false;
-    if (lora_on) dropped = add_terms<true>(e, tlds, r0, g.M, c0, g.N, acc[i], cache);
+    if (common) dropped = add_tile_terms<true, C>(e, tt, tlds, (wm * C::TM + i) * 16, c0, g.N, acc[i], cache);
+    else if (lora_on) dropped = add_terms<true>(e, tlds, r0, g.M, c0, g.N, acc[i], cache);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -408,9 +508,11 @@ template <typename C>
 __global__ __launch_bounds__(C::NT, 1) void gated_grad_x_tile_kernel(GatedGradXArgs g) {
   constexpr int SC = 64 + 4;                            // a wave stages 16 rows, and those of the adapters' term
   constexpr int WLDS = 2 * 16 * SC * 4 + kTermLds;
+  constexpr int TT = C::NW * WLDS;
+  constexpr int LDS = TT + int(sizeof(TileTerms<C>)) > 2 * C::STAGE ? TT + int(sizeof(TileTerms<C>)) : 2 * C::STAGE;
   static_assert(C::TN == 4, "64 columns per wave");
-  __shared__ __attribute__((aligned(16))) char smem[2 * C::STAGE];
-  static_assert(C::NW * WLDS <= 2 * C::STAGE, "staging must fit in LDS");
+  static_assert(TT % 16 == 0 && LDS <= 160 * 1024, "staging must fit in LDS");
+  __shared__ __attribute__((aligned(16))) char smem[LDS];
   int tm, tn;
   if (!tile_of_workgroup(blockIdx.x, (g.M + C::BM - 1) / C::BM, (g.N + C::BN - 1) / C::BN, tm, tn)) return;
   const int m0 = tm * C::BM, n0 = tn * C::BN;
@@ -433,11 +535,14 @@ __global__ __launch_bounds__(C::NT, 1) void gated_grad_x_tile_kernel(GatedGradXA
     const int row = (wave * C::B_INS + i) * 8 + (lane >> 3);
     src.bo[i] = (uint32_t(min(row, g.N - 1 - n0)) * uint32_t(g.Kd) + tswz(row, lane & 7) * 8) * 2;
   }
+  const int4 sd = tile_desc<C>(g.ex, m0, g.M);
   f32x4_t acc[C::TM][C::TN];
   tile_loop<C>(src, smem, 2 * src.kt1, acc);
 
   const Terms e{g.ex, g.U_up, g.b_up};
   const bool lora_on = expand_enabled(g.ex);
+  TileTerms<C> &tt = *reinterpret_cast<TileTerms<C> *>(smem + TT);
+  const bool common = lora_on && g.ex.K == 1 && tile_terms<C>(e, tt, sd);
   const int vr = lane >> 3, vc = (lane & 7) * 8, c0 = n0 + wn * 64;
   if (c0 >= g.N) return;
   float *stage = reinterpret_cast<float *>(smem + wave * WLDS), *lstage = stage + 16 * SC;
@@ -453,7 +558,8 @@ __global__ __launch_bounds__(C::NT, 1) void gated_grad_x_tile_kernel(GatedGradXA
       acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
     bool dropped = false;
-    if (lora_on) dropped = add_terms<false>(e, tlds, r0, g.M, c0, g.N, acc[i], cache);
+    if (common) dropped = add_tile_terms<false, C>(e, tt, tlds, (wm * C::TM + i) * 16, c0, g.N, acc[i], cache);
+    else if (lora_on) dropped = add_terms<false>(e, tlds, r0, g.M, c0, g.N, acc[i], cache);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
