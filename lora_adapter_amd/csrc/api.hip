@@ -1138,15 +1138,11 @@ int32_t gated_args(const void *X, const void *W_gate_t, const void *W_up_t, int3
 }
 
 hipError_t gated_shrinks(const GatedCall &c, const void *X, const uint8_t *keep_mask, float keep_scale,
-                         int32_t T, int32_t K, const float *gates, const lora_pool_desc *const (&pool)[2],
-                         const PlanView &pv, hipStream_t s) {
-  for (int p = 0; p < 2; ++p) {
-    const ShrinkArgs a = apply_shrink_args(X, keep_mask, keep_scale, T, K, gates, pool[p], pv, c.w[p]);
-    const hipError_t e = launch_shrink(a, pool[p]->dtype, int64_t(T) * K, pool[p]->n_adapters, pool[p]->d_in,
-                                       pool[p]->d_out, s);
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+                         int32_t T, int32_t K, const float *gates, const lora_pool_desc *gate,
+                         const lora_pool_desc *up, const PlanView &pv, hipStream_t s) {
+  return launch_shrink_pair(apply_shrink_args(X, keep_mask, keep_scale, T, K, gates, gate, pv, c.w[0]),
+                            apply_shrink_args(X, keep_mask, keep_scale, T, K, gates, up, pv, c.w[1]), gate->dtype,
+                            int64_t(T) * K, gate->n_adapters, gate->d_in, gate->d_out, s);
 }
 
 }  // namespace
@@ -1164,12 +1160,13 @@ int32_t lora_gated_apply(const void *X, const void *W_gate_t, const void *W_up_t
                                 plan, ws_gate, ws_gate_bytes, ws_up, ws_up_bytes, c);
   if (st != LORA_OK || T == 0) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const lora_pool_desc *const pool[2] = {gate, up};
   const PlanView pv = plan_view(plan, int64_t(T) * K, gate->n_adapters);
-  hipError_t e = gated_shrinks(c, X, keep_mask, keep_scale, T, K, gates, pool, pv, s);
+  hipError_t e = gated_shrinks(c, X, keep_mask, keep_scale, T, K, gates, gate, up, pv, s);
   if (e != hipSuccess) return LORA_ERR_DEVICE;
   if (c.fused) return dev(launch_gated_tiles(c.a, s));
-  for (int p = 0; p < 2 && e == hipSuccess; ++p) e = launch_base_gemm(c.cfg, c.g[p], s);
+  if (c.cfg.kind == 4) e = launch_gated_decode(c.cfg, c.g, s);
+  else
+    for (int p = 0; p < 2 && e == hipSuccess; ++p) e = launch_base_gemm(c.cfg, c.g[p], s);
   if (e == hipSuccess) e = launch_gated_epilogue(c.a, gate->dtype, s);
   return dev(e);
 }
@@ -1184,6 +1181,24 @@ int32_t lora_gated_forward(const int32_t *ids, const float *gates, int32_t T, in
   int32_t st = gated_args(X, W_gate_t, W_up_t, activation, H, pre_gate, pre_up, T, K, gates, gate, up, plan,
                           ws_gate, ws_gate_bytes, ws_up, ws_up_bytes, c);
   if (st != LORA_OK) return st;
+  if (plan_bytes < lora_plan_bytes(T, K, gate->n_adapters)) return LORA_ERR_CAPACITY;
+  if (T > 0 && !ids) return LORA_ERR_INVALID_ARG;
+  if (T > 0 && c.cfg.kind == 4) {
+    // decode: plan, per-slot shrinks and both products' partials in one
+    // launch, and an epilogue that also stores U in the plan's layout
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    Fwd f{c.cfg, c.g[0], true};
+    const SlotShrinkArgs ss[2] = {slot_shrink_args(ids, gates, T, K, X, keep_mask, keep_scale, gate, c.w[0]),
+                                  slot_shrink_args(ids, gates, T, K, X, keep_mask, keep_scale, up, c.w[1])};
+    const hipError_t e = launch_gated_decode_plan(c.cfg, c.g, ss, forward_plan(ids, gates, T, K, gate, plan, f, c.w[0]), s);
+    if (e != hipSuccess) return LORA_ERR_DEVICE;
+    c.a.sdesc = c.w[0].sdesc;
+    c.a.slot_stride = LORA_MAX_RANK;
+    for (int p = 0; p < 2; ++p) c.a.u_out[p] = c.w[p].U;
+    c.a.ex.U = c.w[0].slot_u;
+    c.a.U_up = c.w[1].slot_u;
+    return dev(launch_gated_epilogue(c.a, gate->dtype, s));
+  }
   if ((st = lora_plan(ids, gates, T, K, gate, plan, plan_bytes, stream)) != LORA_OK || T == 0) return st;
   return lora_gated_apply(X, W_gate_t, W_up_t, activation, H, pre_gate, pre_up, T, K, gates, keep_mask,
                           keep_scale, gate, up, plan, ws_gate, ws_gate_bytes, ws_up, ws_up_bytes, stream);
@@ -1251,8 +1266,9 @@ int32_t lora_gated_grad(const void *dH, const void *pre_gate, const void *pre_up
   const lora_pool_desc *const pool[2] = {gate, up};
   const void *const dY[2] = {d_gate, d_up}, *const W[2] = {W_gate, W_up};
   GatedGradXArgs a{};
+  ShrinkArgs shrink[2] = {};
   for (int p = 0; p < 2; ++p) {
-    ShrinkArgs sa{};
+    ShrinkArgs &sa = shrink[p];
     sa.Z = dY[p]; sa.extra_scale = keep_mask ? keep_scale : 1.0f;
     sa.T = T; sa.K = K; sa.d = F;
     sa.pages = pool[p]->b_pages;
@@ -1260,10 +1276,11 @@ int32_t lora_gated_grad(const void *dH, const void *pre_gate, const void *pre_up
     sa.scale = pool[p]->scale; sa.gates = gates; sa.plan = pv;
     sa.err_word = const_cast<int32_t *>(pv.hdr) + LORA_PH_ERR;
     sa.out = reinterpret_cast<float *>(base + p * w.g); sa.out_cap = TK * max_rank;
-    if ((e = launch_shrink(sa, dtype, TK, gate->n_adapters, d, F, s)) != hipSuccess) return LORA_ERR_DEVICE;
     a.dY[p] = dY[p]; a.W[p] = W[p];
     a.part[p] = reinterpret_cast<float *>(base + 2 * w.g + p * w.part);
   }
+  e = launch_shrink_pair(shrink[0], shrink[1], dtype, TK, gate->n_adapters, d, F, s);
+  if (e != hipSuccess) return LORA_ERR_DEVICE;
   a.M = T; a.N = d; a.Kd = F;
   a.ex.K = K;
   a.ex.slot_desc = pv.slot_desc; a.ex.pair_tk = pv.pair_tk; a.ex.page_ids = gate->page_ids;

@@ -12,6 +12,9 @@
 // activation, product and the one rounding happen on the way out.  Smaller
 // batches take the split products of the single projections and an epilogue
 // that finishes both.
+#include "decode_tile.h"
+#include "plan_build.h"
+#include "shrink_units.h"
 #include "tile_loop.h"
 
 namespace lora {
@@ -426,6 +429,126 @@ __device__ __forceinline__ void add_pieces(const float *part, int np, int M, int
   }
 }
 
+// Decode: workgroup 0 builds the plan, then come the decode GEMM tiles of the
+// gate's weight and of the up projection's, then the per-slot shrinks (four
+// parts a slot) of both.  No part reads what another writes.
+template <int MB, bool kMask, bool kLds>
+__global__ __launch_bounds__(256) void gated_decode_plan_kernel(GemmArgs g0, GemmArgs g1, SlotShrinkArgs s0,
+                                                                 SlotShrinkArgs s1, PlanArgs pa, int gx, int gy,
+                                                                 int n_gemm) {
+  __shared__ __attribute__((aligned(16))) uint16_t xs[MB * 32 * kDecodeKC];
+  int b = int(blockIdx.x);
+  if (b == 0) {
+    plan_build<kLds>(pa, reinterpret_cast<int *>(xs));
+    return;
+  }
+  b -= 1;
+  if (b < 2 * n_gemm) {
+    const int t = b < n_gemm ? b : b - n_gemm;
+    decode_tile<MB>(b < n_gemm ? g0 : g1, t % gx, (t / gx) % gy, t / (gx * gy), xs);
+    return;
+  }
+  b -= 2 * n_gemm;
+  const int parts = kSlotParts * s0.n_slots, q = b < parts ? b : b - parts;
+  slot_shrink_part<kMask>(b < parts ? s0 : s1, q / kSlotParts, q % kSlotParts);
+}
+
+template <int MB>
+__global__ __launch_bounds__(256) void gated_decode_kernel(GemmArgs g0, GemmArgs g1) {
+  __shared__ __attribute__((aligned(16))) uint16_t xs[MB * 32 * kDecodeKC];
+  const int z = blockIdx.z >> 1;
+  decode_tile<MB>(blockIdx.z & 1 ? g1 : g0, blockIdx.x, blockIdx.y, z, xs);
+}
+
+// Decode epilogue: a workgroup per row and 512 columns, its waves the two
+// projections by halves of the pieces and of each slot's rank rows, joined
+// through LDS.  A row's rank rows come one batch after another, so that the
+// launch lasts as long as its longest chain: one wave for all four took 39 us
+// at 48 tokens of two adapters of ranks 8 .. 64 (4096 -> 11008).
+template <int kAct>
+__global__ __launch_bounds__(256) void gated_decode_epilogue_kernel(GatedArgs g) {
+  __shared__ __attribute__((aligned(16))) float part[4][512];
+  const int lane = threadIdx.x & 63, wave = wave_id(), p = wave & 1, h = wave >> 1;
+  const int row = blockIdx.y;
+  const int col_raw = (blockIdx.x * 64 + lane) * 8, col = min(col_raw, g.N - 8);   // loads stay in bounds
+  const bool lora_on = expand_enabled(g.ex);
+  const int4 *desc = g.sdesc ? g.sdesc : g.ex.slot_desc;
+  int4 sd = make_int4(-1, 0, 0, 0);
+  if (lora_on && lane < g.ex.K) sd = desc[int64_t(row) * g.ex.K + lane];
+  float v[8] = {};
+  {
+    // pieces h, h + 2, ..: up to 8 loads in flight
+    const int np = (g.splits - h + 1) / 2;
+    const float *src = g.part[p] + (int64_t(h) * g.M + row) * g.N + col;
+    for (int z0 = 0; z0 < np; z0 += 8) {
+      Raw8<float> pr[8];
+#pragma unroll
+      for (int z = 0; z < 8; ++z) pr[z].load(src + 2 * int64_t(min(z0 + z, np - 1)) * g.M * g.N);
+#pragma unroll
+      for (int z = 0; z < 8; ++z) {
+        if (z0 + z < np) {
+          float o[8];
+          pr[z].to8(o);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) v[c] += o[c];
+        }
+      }
+    }
+  }
+  if (lora_on) {
+    ExpandArgs e = g.ex;
+    if (p) {
+      e.U = g.U_up;
+      e.b_pages = g.b_up;
+    }
+    int4 mine = sd;
+    const int first = (sd.y + 1) / 2;
+    if (h == 0) {
+      mine.y = first;
+    } else {
+      mine.y = sd.y - first;
+      mine.z += first;
+      mine.w += first;
+      if (mine.y == 0) mine.x = -1;
+    }
+    expand_row8<uint16_t>(v, mine, col, e);
+  }
+  Cols<float, 8>::store(&part[wave][lane * 8], v);
+  __syncthreads();
+  const int c = int(threadIdx.x) * 2, at_col = int(blockIdx.x) * 512 + c;
+  if (at_col < g.N) {
+    float gv[2], uv[2], o[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float slope;
+      gv[x] = part[0][c + x] + part[2][c + x];
+      uv[x] = part[1][c + x] + part[3][c + x];
+      o[x] = activate<kAct, true>(gv[x], slope) * uv[x];
+    }
+    const int64_t at = int64_t(row) * g.N + at_col;
+    Cols<uint16_t, 2>::store(static_cast<uint16_t *>(g.H) + at, o);
+    if (g.pre_gate) {
+      Cols<uint16_t, 2>::store(static_cast<uint16_t *>(g.pre_gate) + at, gv);
+      Cols<uint16_t, 2>::store(static_cast<uint16_t *>(g.pre_up) + at, uv);
+    }
+  }
+  if (g.sdesc == nullptr || blockIdx.x != 0) return;
+  // the row's per-slot U to the places the plan gave its active slots
+  int32_t *hdr = const_cast<int32_t *>(g.ex.hdr);
+  if (!lora_on) {
+    if (row == 0 && threadIdx.x == 0) atomicOr(hdr + LORA_PH_ERR, LORA_DEVERR_CAPACITY);
+    return;
+  }
+  if (h) return;
+  for (int k = 0; k < g.ex.K; ++k) {
+    const int64_t i = int64_t(row) * g.ex.K + k;
+    const int4 d = g.ex.slot_desc[i];
+    if (d.x < 0) continue;
+    const float *src = (p ? g.U_up : g.ex.U) + i * g.slot_stride;
+    for (int j = lane; j < d.y; j += 64) g.u_out[p][d.z + j] = src[j];
+  }
+}
+
 // One wave per row and 512 columns.
 template <typename E, int NW, int kAct>
 __global__ __launch_bounds__(NW * 64) void gated_epilogue_kernel(GatedArgs g) {
@@ -617,16 +740,7 @@ __global__ __launch_bounds__(NW * 64) void gated_grad_x_epilogue_kernel(GatedGra
 }
 
 using Big = LoopCfg<256, 256, 2, 4>;
-
-template <typename E, int kAct>
-void launch_epilogue_rows(const GatedArgs &g, hipStream_t s) {
-  const unsigned n_x = unsigned((g.N + 511) / 512);
-  // one wave a workgroup where four leave CUs idle
-  if (int64_t(n_x) * ((g.M + 3) / 4) < 256)
-    hipLaunchKernelGGL((gated_epilogue_kernel<E, 1, kAct>), dim3(n_x, unsigned(g.M)), dim3(64), 0, s, g);
-  else
-    hipLaunchKernelGGL((gated_epilogue_kernel<E, 4, kAct>), dim3(n_x, unsigned((g.M + 3) / 4)), dim3(256), 0, s, g);
-}
+using Mid = LoopCfg<128, 128, 2, 2>;
 
 template <typename E>
 void launch_act_grad(const void *dH, const void *pg, const void *pu, int act, void *dg, void *du, int64_t n,
@@ -645,27 +759,75 @@ void launch_act_grad(const void *dH, const void *pg, const void *pu, int act, vo
 
 }  // namespace
 
-bool gated_fused(int T, int d_out, int dtype) {
-  return dtype == LORA_BF16 && T > 128 && int64_t((T + 255) / 256) * ((d_out + 127) / 128) >= 256;
+bool gated_fused(int T, int d_out, int dtype) { return dtype == LORA_BF16 && T > 128; }
+
+namespace {
+
+template <typename C>
+void launch_tiles(const GatedArgs &g, hipStream_t s) {
+  const int tiles = ((g.M + C::BM - 1) / C::BM) * ((g.N + C::BN / 2 - 1) / (C::BN / 2));
+  const dim3 grid(8 * unsigned((tiles + 7) / 8)), block(C::NT);
+  if (g.act == LORA_ACT_SILU) hipLaunchKernelGGL((gated_tile_kernel<C, LORA_ACT_SILU>), grid, block, 0, s, g);
+  else if (g.act == LORA_ACT_GELU) hipLaunchKernelGGL((gated_tile_kernel<C, LORA_ACT_GELU>), grid, block, 0, s, g);
+  else hipLaunchKernelGGL((gated_tile_kernel<C, LORA_ACT_GELU_TANH>), grid, block, 0, s, g);
 }
 
+}  // namespace
+
 hipError_t launch_gated_tiles(const GatedArgs &g, hipStream_t s) {
-  const int tiles = ((g.M + 255) / 256) * ((g.N + 127) / 128);
-  const dim3 grid(8 * unsigned((tiles + 7) / 8)), block(512);
-  if (g.act == LORA_ACT_SILU)
-    hipLaunchKernelGGL((gated_tile_kernel<Big, LORA_ACT_SILU>), grid, block, 0, s, g);
-  else if (g.act == LORA_ACT_GELU)
-    hipLaunchKernelGGL((gated_tile_kernel<Big, LORA_ACT_GELU>), grid, block, 0, s, g);
-  else
-    hipLaunchKernelGGL((gated_tile_kernel<Big, LORA_ACT_GELU_TANH>), grid, block, 0, s, g);
+  const int64_t big = int64_t((g.M + 255) / 256) * ((g.N + 127) / 128);
+  if (big >= 256) launch_tiles<Big>(g, s);
+  else launch_tiles<Mid>(g, s);
   return hipGetLastError();
 }
 
+hipError_t launch_gated_decode_plan(const GemmConfig &c, const GemmArgs (&g)[2], const SlotShrinkArgs (&ss)[2],
+                                    const PlanLaunch &pl, hipStream_t s) {
+  if (c.kind != 4 || pl.lds_bytes > plan_lds_cap(c)) return hipErrorInvalidConfiguration;
+  const int gx = (g[0].N + 127) / 128, gy = (g[0].M + c.bm - 1) / c.bm, n_gemm = gx * gy * c.splits;
+  const dim3 grid(unsigned(1 + 2 * n_gemm + 2 * kSlotParts * ss[0].n_slots)), block(256);
+  const bool m = ss[0].mask != nullptr;
+#define LORA_GD3(MB, M, L) \
+  hipLaunchKernelGGL((gated_decode_plan_kernel<MB, M, L>), grid, block, 0, s, g[0], g[1], ss[0], ss[1], pl.a, gx, gy, n_gemm)
+#define LORA_GD2(MB, M) do { if (pl.lds) LORA_GD3(MB, M, true); else LORA_GD3(MB, M, false); } while (0)
+#define LORA_GD(MB) do { if (m) LORA_GD2(MB, true); else LORA_GD2(MB, false); } while (0)
+  if (c.bm == 32) LORA_GD(1);
+  else if (c.bm == 64) LORA_GD(2);
+  else LORA_GD(4);
+#undef LORA_GD
+#undef LORA_GD2
+#undef LORA_GD3
+  return hipGetLastError();
+}
+
+hipError_t launch_gated_decode(const GemmConfig &c, const GemmArgs (&g)[2], hipStream_t s) {
+  if (c.kind != 4) return hipErrorInvalidConfiguration;
+  const dim3 grid((g[0].N + 127) / 128, (g[0].M + c.bm - 1) / c.bm, 2 * c.splits), block(256);
+  if (c.bm == 32) hipLaunchKernelGGL(gated_decode_kernel<1>, grid, block, 0, s, g[0], g[1]);
+  else if (c.bm == 64) hipLaunchKernelGGL(gated_decode_kernel<2>, grid, block, 0, s, g[0], g[1]);
+  else hipLaunchKernelGGL(gated_decode_kernel<4>, grid, block, 0, s, g[0], g[1]);
+  return hipGetLastError();
+}
+
+namespace {
+
+template <int kAct>
+void launch_epilogue(const GatedArgs &g, int dtype, hipStream_t s) {
+  const unsigned n_x = unsigned((g.N + 511) / 512);
+  if (dtype == LORA_BF16)
+    hipLaunchKernelGGL(gated_decode_epilogue_kernel<kAct>, dim3(n_x, unsigned(g.M)), dim3(256), 0, s, g);
+  else if (int64_t(n_x) * ((g.M + 3) / 4) < 256)      // one wave a workgroup where four leave CUs idle
+    hipLaunchKernelGGL((gated_epilogue_kernel<float, 1, kAct>), dim3(n_x, unsigned(g.M)), dim3(64), 0, s, g);
+  else
+    hipLaunchKernelGGL((gated_epilogue_kernel<float, 4, kAct>), dim3(n_x, unsigned((g.M + 3) / 4)), dim3(256), 0, s, g);
+}
+
+}  // namespace
+
 hipError_t launch_gated_epilogue(const GatedArgs &g, int dtype, hipStream_t s) {
-  const bool bf = dtype == LORA_BF16;
-  if (g.act == LORA_ACT_SILU) bf ? launch_epilogue_rows<uint16_t, LORA_ACT_SILU>(g, s) : launch_epilogue_rows<float, LORA_ACT_SILU>(g, s);
-  else if (g.act == LORA_ACT_GELU) bf ? launch_epilogue_rows<uint16_t, LORA_ACT_GELU>(g, s) : launch_epilogue_rows<float, LORA_ACT_GELU>(g, s);
-  else bf ? launch_epilogue_rows<uint16_t, LORA_ACT_GELU_TANH>(g, s) : launch_epilogue_rows<float, LORA_ACT_GELU_TANH>(g, s);
+  if (g.act == LORA_ACT_SILU) launch_epilogue<LORA_ACT_SILU>(g, dtype, s);
+  else if (g.act == LORA_ACT_GELU) launch_epilogue<LORA_ACT_GELU>(g, dtype, s);
+  else launch_epilogue<LORA_ACT_GELU_TANH>(g, dtype, s);
   return hipGetLastError();
 }
 

@@ -471,6 +471,12 @@ struct GatedArgs {
   const void *b_up;
   int act;
   void *H, *pre_gate, *pre_up;   // [M][N]; pre_* null unless training
+  // not null (decode forward): ex.U and U_up hold U per slot, with the slot
+  // descriptors that the per-slot shrink wrote; the epilogue also stores U
+  // in the plan's layout (see EpilogueArgs)
+  const int4 *sdesc;
+  float *u_out[2];
+  int slot_stride;
   // split forms: the partials of both products
   const float *part[2];
   int splits, sk_g, sk_kt, bm, bn;
@@ -499,6 +505,10 @@ hipError_t launch_plan(const int32_t *ids, const float *gates, int T, int K, con
 // shrink takes the big segments (shrink_tile_enabled, as in the plan).
 hipError_t launch_shrink(const ShrinkArgs &a, int dtype, int64_t TK, int64_t n_adapters,
                          int d_in, int d_out, hipStream_t s);
+
+// Two of them that share plan, mask and width, in one launch.
+hipError_t launch_shrink_pair(const ShrinkArgs &a, const ShrinkArgs &b, int dtype, int64_t TK,
+                              int64_t n_adapters, int d_in, int d_out, hipStream_t s);
 
 // Base GEMM configuration chosen from the shape (host-side, deterministic).
 struct GemmConfig {
@@ -588,6 +598,11 @@ hipError_t launch_cross_entropy(const CrossEntropyArgs &a, int dtype, void *ws, 
 // The gated block takes tiles with both projections inside (no partials) when
 // they fill the GPU.
 bool gated_fused(int T, int d_out, int dtype);
+// Decode: both products' partials, the per-slot shrinks and the plan.
+hipError_t launch_gated_decode_plan(const GemmConfig &c, const GemmArgs (&g)[2], const SlotShrinkArgs (&ss)[2],
+                                    const PlanLaunch &pl, hipStream_t s);
+// Decode with a plan: both products' partials.
+hipError_t launch_gated_decode(const GemmConfig &c, const GemmArgs (&g)[2], hipStream_t s);
 hipError_t launch_gated_tiles(const GatedArgs &a, hipStream_t s);
 // The split forms' second launch: both sums, both expands, activation, product.
 hipError_t launch_gated_epilogue(const GatedArgs &a, int dtype, hipStream_t s);

@@ -53,6 +53,13 @@ __global__ __launch_bounds__(64) void shrink_units_kernel(ShrinkArgs s) {
   shrink_units_wave<E, kMask, kCh, kResident>(s, blockIdx.x);
 }
 
+// Two shrinks of one plan that differ in pages, scale and output (and, backward,
+// in Z), side by side: blockIdx.y takes one.
+template <typename E, bool kMask, int kCh, bool kResident>
+__global__ __launch_bounds__(64) void shrink_units_pair_kernel(ShrinkArgs a, ShrinkArgs b) {
+  shrink_units_wave<E, kMask, kCh, kResident>(blockIdx.y ? b : a, blockIdx.x);
+}
+
 // Finds the big segment and the 32-pair tile of workgroup b, the tiles of the
 // big list numbered in list order (a wave-wide scan over 64 entries at a
 // time).  Returns false past the last tile.
@@ -214,6 +221,11 @@ __global__ __launch_bounds__(256) void shrink_tile_kernel(ShrinkArgs s) {
   shrink_tile_wg<kMask>(s, blockIdx.x);
 }
 
+template <bool kMask>
+__global__ __launch_bounds__(256) void shrink_tile_pair_kernel(ShrinkArgs a, ShrinkArgs b) {
+  shrink_tile_wg<kMask>(blockIdx.y ? b : a, blockIdx.x);
+}
+
 // Both shrinks in one launch (bf16 batches with big segments): workgroups
 // 0 .. n_tile-1 run the tile kernel's tiles, the others the units
 // schedule, one schedule wave per wave.  The two write disjoint pairs.
@@ -225,6 +237,13 @@ __global__ __launch_bounds__(256) void shrink_both_kernel(ShrinkArgs s, int n_ti
     return;
   }
   shrink_units_wave<uint16_t, kMask, kCh, true>(s, (b - n_tile) * 4 + int(threadIdx.x >> 6));
+}
+
+template <bool kMask, int kCh>
+__global__ __launch_bounds__(256) void shrink_both_pair_kernel(ShrinkArgs a, ShrinkArgs b, int n_tile) {
+  const int i = int(blockIdx.x);
+  if (i < n_tile) shrink_tile_wg<kMask>(blockIdx.y ? b : a, i);
+  else shrink_units_wave<uint16_t, kMask, kCh, true>(blockIdx.y ? b : a, (i - n_tile) * 4 + int(threadIdx.x >> 6));
 }
 
 // Workgroups of the tile shrink: the whole 32-pair tiles of the big
@@ -290,6 +309,41 @@ hipError_t launch_shrink_big(const ShrinkArgs &a, int dtype, int64_t TK, int64_t
   const dim3 g2{unsigned(shrink_tile_wgs(TK, n_adapters)), 1, 1}, b2{256, 1, 1};
   if (s.mask) hipLaunchKernelGGL((shrink_tile_kernel<true>), g2, b2, 0, st, s);
   else hipLaunchKernelGGL((shrink_tile_kernel<false>), g2, b2, 0, st, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_shrink_pair(const ShrinkArgs &a0, const ShrinkArgs &b0, int dtype, int64_t TK,
+                              int64_t n_adapters, int d_in, int d_out, hipStream_t st) {
+  const int64_t segs = TK < n_adapters ? TK : n_adapters;
+  if (segs <= 0) return hipSuccess;
+  ShrinkArgs a = a0, b = b0;
+  // one capacity: the first reports for both
+  a.out_cap = b.out_cap = a0.out_cap < b0.out_cap ? a0.out_cap : b0.out_cap;
+  a.big_segments = b.big_segments = shrink_tile_enabled(dtype, TK, d_in, d_out) ? 1 : 0;
+  const int d = a.d, n_tile = shrink_tile_wgs(TK, n_adapters);
+  const bool m = a.mask != nullptr;
+#define LORA_PAIR(K, G, B, ...) hipLaunchKernelGGL((K), dim3(unsigned(G), 2), dim3(B), 0, st, a, b, ##__VA_ARGS__)
+#define LORA_PAIR_M(T, F, G, B, ...) do { if (m) LORA_PAIR(T, G, B, ##__VA_ARGS__); else LORA_PAIR(F, G, B, ##__VA_ARGS__); } while (0)
+  if (a.big_segments && d <= 12 * 512) {
+    const int g = n_tile + kShrinkWaves / 4;
+    if (d <= 8 * 512) LORA_PAIR_M((shrink_both_pair_kernel<true, 8>), (shrink_both_pair_kernel<false, 8>), g, 256, n_tile);
+    else LORA_PAIR_M((shrink_both_pair_kernel<true, 12>), (shrink_both_pair_kernel<false, 12>), g, 256, n_tile);
+    return hipGetLastError();
+  }
+#define LORA_UNITS(E, CH, RES) \
+  LORA_PAIR_M((shrink_units_pair_kernel<E, true, CH, RES>), (shrink_units_pair_kernel<E, false, CH, RES>), kShrinkWaves, 64)
+  if (dtype == LORA_BF16) {
+    if (d <= 8 * 512) LORA_UNITS(uint16_t, 8, true);
+    else if (d <= 12 * 512) LORA_UNITS(uint16_t, 12, true);
+    else LORA_UNITS(uint16_t, 8, false);
+  } else {
+    if (d <= 4 * 512) LORA_UNITS(float, 4, true);
+    else LORA_UNITS(float, 4, false);
+  }
+  if (a.big_segments) LORA_PAIR_M((shrink_tile_pair_kernel<true>), (shrink_tile_pair_kernel<false>), n_tile, 256);
+#undef LORA_UNITS
+#undef LORA_PAIR_M
+#undef LORA_PAIR
   return hipGetLastError();
 }
 
