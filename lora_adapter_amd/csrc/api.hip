@@ -1098,8 +1098,17 @@ struct GatedCall {
   GemmArgs g[2];
   GemmConfig cfg;
   GatedArgs a;
-  bool fused;
+  TermsArgs t;
 };
+
+TermsArgs terms_args(const PlanView &pv, const lora_pool_desc *pool, int32_t K) {
+  TermsArgs t{};
+  t.hdr = pv.hdr; t.pair_tk = pv.pair_tk; t.pair_adapter = pv.pair_adapter; t.u_off = pv.u_off;
+  t.slot_pos = pv.slot_pos;
+  t.rank = pool->rank; t.page_start = pool->page_start; t.page_ids = pool->page_ids;
+  t.K = K;
+  return t;
+}
 
 // The checks of the gated forward (T > 0 from the workspaces on), and its
 // arguments.
@@ -1120,7 +1129,7 @@ int32_t gated_args(const void *X, const void *W_gate_t, const void *W_up_t, int3
     return st;
   c.w[0] = apply_layout(ws_gate, ws_gate_bytes, T, K, gate->d_in, gate->d_out, gate->dtype);
   c.w[1] = apply_layout(ws_up, ws_up_bytes, T, K, up->d_in, up->d_out, up->dtype);
-  c.fused = gated_fused(T, gate->d_out, gate->dtype);
+  const PlanView pv = plan_view(plan, int64_t(T) * K, gate->n_adapters);
   GatedArgs &a = c.a;
   a = GatedArgs{};
   a.X = X; a.W[0] = W_gate_t; a.W[1] = W_up_t;
@@ -1132,8 +1141,17 @@ int32_t gated_args(const void *X, const void *W_gate_t, const void *W_up_t, int3
   a.act = activation;
   a.H = H; a.pre_gate = pre_gate; a.pre_up = pre_up;
   a.part[0] = c.g[0].partial; a.part[1] = c.g[1].partial;
-  a.splits = c.cfg.splits; a.sk_g = c.cfg.sk; a.sk_kt = gate->d_in / 64;
-  a.bm = c.cfg.bm; a.bn = c.cfg.bn;
+  a.splits = c.cfg.splits;
+  a.slot_pos = pv.slot_pos;
+  // where lora_apply would keep partial products there is room for the
+  // adapters' terms
+  if (c.cfg.kind != 4 && !c.cfg.fused)
+    for (int p = 0; p < 2; ++p) a.term[p] = c.g[p].partial;
+  c.t = terms_args(pv, gate, K);
+  c.t.U[0] = a.ex.U; c.t.U[1] = a.U_up; c.t.u_cap = a.ex.u_cap;
+  c.t.pages[0] = gate->b_pages; c.t.pages[1] = up->b_pages;
+  c.t.out[0] = a.term[0]; c.t.out[1] = a.term[1];
+  c.t.N = gate->d_out;
   return LORA_OK;
 }
 
@@ -1163,11 +1181,9 @@ int32_t lora_gated_apply(const void *X, const void *W_gate_t, const void *W_up_t
   const PlanView pv = plan_view(plan, int64_t(T) * K, gate->n_adapters);
   hipError_t e = gated_shrinks(c, X, keep_mask, keep_scale, T, K, gates, gate, up, pv, s);
   if (e != hipSuccess) return LORA_ERR_DEVICE;
-  if (c.fused) return dev(launch_gated_tiles(c.a, s));
-  if (c.cfg.kind == 4) e = launch_gated_decode(c.cfg, c.g, s);
-  else
-    for (int p = 0; p < 2 && e == hipSuccess; ++p) e = launch_base_gemm(c.cfg, c.g[p], s);
-  if (e == hipSuccess) e = launch_gated_epilogue(c.a, gate->dtype, s);
+  if (c.cfg.kind != 4) return dev(launch_gated(c.a, c.t, gate->dtype, s));
+  e = launch_gated_decode(c.cfg, c.g, s);
+  if (e == hipSuccess) e = launch_gated_decode_epilogue(c.a, s);
   return dev(e);
 }
 
@@ -1197,7 +1213,7 @@ int32_t lora_gated_forward(const int32_t *ids, const float *gates, int32_t T, in
     for (int p = 0; p < 2; ++p) c.a.u_out[p] = c.w[p].U;
     c.a.ex.U = c.w[0].slot_u;
     c.a.U_up = c.w[1].slot_u;
-    return dev(launch_gated_epilogue(c.a, gate->dtype, s));
+    return dev(launch_gated_decode_epilogue(c.a, s));
   }
   if ((st = lora_plan(ids, gates, T, K, gate, plan, plan_bytes, stream)) != LORA_OK || T == 0) return st;
   return lora_gated_apply(X, W_gate_t, W_up_t, activation, H, pre_gate, pre_up, T, K, gates, keep_mask,
@@ -1208,21 +1224,20 @@ int32_t lora_gated_forward(const int32_t *ids, const float *gates, int32_t T, in
 
 namespace {
 
-// Workspace of the gated backward: [G of the gate][G of the up projection]
-// [partials of both products].
+// Workspace of the gated backward: [G of the gate][G of the up projection], and
+// where the product is split [the splits' sums][the adapters' terms].
 struct GatedGradWs {
-  GemmConfig cfg;
-  bool fused;
-  size_t g, part, total;
+  int splits;
+  size_t g, sums, total;
 };
 
 GatedGradWs gated_grad_ws(int32_t T, int32_t K, int32_t d_in, int32_t d_out, int32_t max_rank, int32_t dtype) {
   GatedGradWs w{};
-  w.cfg = grad_x_config(T, d_in, d_out, dtype);
-  w.fused = gated_grad_x_fused(T, d_in, dtype);
+  w.splits = gated_grad_x_splits(T > 0 ? T : 1, d_in, d_out, dtype);
   w.g = align_up(size_t(T) * size_t(K) * size_t(max_rank) * sizeof(float) + 4);
-  w.part = w.fused ? 0 : align_up(gemm_partial_bytes(w.cfg, T, d_in));
-  w.total = 2 * (w.g + w.part);
+  const size_t one = size_t(T) * size_t(d_in) * sizeof(float);
+  w.sums = align_up(size_t(w.splits) * one);
+  w.total = 2 * w.g + w.sums + (w.splits ? align_up(one) : 0);
   return w;
 }
 
@@ -1277,7 +1292,6 @@ int32_t lora_gated_grad(const void *dH, const void *pre_gate, const void *pre_up
     sa.err_word = const_cast<int32_t *>(pv.hdr) + LORA_PH_ERR;
     sa.out = reinterpret_cast<float *>(base + p * w.g); sa.out_cap = TK * max_rank;
     a.dY[p] = dY[p]; a.W[p] = W[p];
-    a.part[p] = reinterpret_cast<float *>(base + 2 * w.g + p * w.part);
   }
   e = launch_shrink_pair(shrink[0], shrink[1], dtype, TK, gate->n_adapters, d, F, s);
   if (e != hipSuccess) return LORA_ERR_DEVICE;
@@ -1288,17 +1302,18 @@ int32_t lora_gated_grad(const void *dH, const void *pre_gate, const void *pre_up
   a.ex.U = reinterpret_cast<float *>(base); a.ex.hdr = pv.hdr; a.ex.u_cap = TK * max_rank;
   a.U_up = reinterpret_cast<float *>(base + w.g); a.b_up = up->a_pages;
   a.mask = keep_mask; a.dX = dX;
-  a.splits = w.cfg.splits; a.sk_g = w.cfg.sk; a.sk_kt = F / 64; a.bm = w.cfg.bm; a.bn = w.cfg.bn;
-  if (w.fused) return dev(launch_gated_grad_x_tiles(a, s));
-  for (int p = 0; p < 2 && e == hipSuccess; ++p) {
-    GemmArgs g{};
-    g.X = dY[p]; g.W = W[p]; g.M = T; g.N = d; g.Kd = F;
-    g.k_split = w.cfg.k_split; g.sk_g = w.cfg.sk;
-    g.partial = const_cast<float *>(a.part[p]);
-    e = launch_base_gemm(w.cfg, g, s);
+  a.slot_pos = pv.slot_pos;
+  a.splits = w.splits;
+  TermsArgs t = terms_args(pv, gate, K);
+  if (w.splits) {
+    a.sums = reinterpret_cast<float *>(base + 2 * w.g);
+    a.term = reinterpret_cast<float *>(base + 2 * w.g + w.sums);
+    t.U[0] = a.ex.U; t.U[1] = a.U_up; t.u_cap = a.ex.u_cap;
+    t.pages[0] = gate->a_pages; t.pages[1] = up->a_pages;
+    t.out[0] = a.term;
+    t.N = d;
   }
-  if (e == hipSuccess) e = launch_gated_grad_x_epilogue(a, dtype, s);
-  return dev(e);
+  return dev(launch_gated_grad_x(a, t, dtype, s));
 }
 
 }  // extern "C"

@@ -20,6 +20,7 @@
 // e.W, split along the vocabulary.  Memory is bounded by taking the tokens in
 // blocks (kBlockBytes of e).  Tokens without a target are left out before the
 // first product, by a list of the others.
+#include "tile_f32.h"
 #include "tile_loop.h"
 
 namespace lora {
@@ -158,19 +159,16 @@ __device__ __forceinline__ void ce_store8(const CeArgs &c, float (&v)[8], int lr
     c.w.part[int64_t(lr) * c.w.pieces + col / kSub] = make_float2(sum, shift);
 }
 
-// Rows of the list (anywhere in X: kWide takes 64-bit lane addresses where X
-// passes 2^32 bytes) by rows of W, both along d.
+// Rows of the list, anywhere in X, by rows of W, both along d.
 template <typename C, bool kWide>
 struct LogitsSrc {
   const uint16_t *X, *W;
-  uint32_t ao[C::A_INS], bo[C::B_INS];
-  const uint16_t *aw[kWide ? C::A_INS : 1];
+  RowOffsets<C::A_INS, kWide> ao;
+  uint32_t bo[C::B_INS];
   int wave, wm, wn;
   __device__ __forceinline__ void copy(uint32_t lds, int kt, int i) const {
     if (i < C::A_INS) {
-      const uint32_t at = lds + (wave * C::A_INS + i) * 1024;
-      if constexpr (kWide) lds_dma16(aw[i] + kt * 64, at);
-      else lds_dma16_s(X + kt * 64, ao[i], at);
+      ao.copy(X + kt * 64, i, lds + (wave * C::A_INS + i) * 1024);
     } else {
       lds_dma16_s(W + kt * 64, bo[i - C::A_INS], lds + C::BM * C::ROWB + (wave * C::B_INS + i - C::A_INS) * 1024);
     }
@@ -200,9 +198,7 @@ __global__ __launch_bounds__(C::NT, 1) void ce_logits_kernel(CeArgs c) {
 #pragma unroll
   for (int i = 0; i < C::A_INS; ++i) {
     const int row = (wave * C::A_INS + i) * 8 + lrow;
-    const int64_t at = int64_t(c.w.rows[c.row0 + min(m0 + row, M - 1)]) * d + tswz(row, lane & 7) * 8;
-    if constexpr (kWide) src.aw[i] = src.X + at;
-    else src.ao[i] = uint32_t(at) * 2;
+    src.ao.set(i, int64_t(c.w.rows[c.row0 + min(m0 + row, M - 1)]) * d + tswz(row, lane & 7) * 8);
   }
 #pragma unroll
   for (int i = 0; i < C::B_INS; ++i) {
@@ -250,45 +246,7 @@ __global__ __launch_bounds__(C::NT, 1) void ce_logits_kernel(CeArgs c) {
   }
 }
 
-// ------------------------------------------------------------ float32 tiles
-// 64 x 64 of A.B on v_mfma_f32_32x32x2_f32, a 32 x 32 block for each of four
-// waves, K in chunks of 32 through LDS.  a(r, k) and b(k, c) give 4 values:
-// along k for A, along k (kBAlongK) or along c for B; k is a multiple of 4.
-constexpr int kF32K = 32;
-struct F32Tile {
-  float as[64][kF32K + 1], bs[64][kF32K + 1];
-};
-
-template <bool kBAlongK, typename FA, typename FB>
-__device__ __forceinline__ f32x16_t tile_f32(F32Tile &t, int k_begin, int k_end, const FA &fa, const FB &fb) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  f32x16_t acc = {};
-  for (int k0 = k_begin; k0 < k_end; k0 += kF32K) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int at = (tid + i * 256) * 4;
-      const int row = at / kF32K, k = at % kF32K;
-      const float4 v = fa(row, k0 + k);
-      t.as[row][k] = v.x; t.as[row][k + 1] = v.y; t.as[row][k + 2] = v.z; t.as[row][k + 3] = v.w;
-      if constexpr (kBAlongK) {
-        const float4 w = fb(row, k0 + k);
-        t.bs[row][k] = w.x; t.bs[row][k + 1] = w.y; t.bs[row][k + 2] = w.z; t.bs[row][k + 3] = w.w;
-      } else {
-        const int kk = at / 64, cc = at % 64;
-        const float4 w = fb(cc, k0 + kk);
-        t.bs[cc][kk] = w.x; t.bs[cc + 1][kk] = w.y; t.bs[cc + 2][kk] = w.z; t.bs[cc + 3][kk] = w.w;
-      }
-    }
-    __syncthreads();
-    const int ra = (wave >> 1) * 32 + (lane & 31), rb = (wave & 1) * 32 + (lane & 31);
-#pragma unroll
-    for (int k = 0; k < kF32K; k += 2)
-      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(t.as[ra][k + (lane >> 5)], t.bs[rb][k + (lane >> 5)], acc, 0, 0, 0);
-  }
-  return acc;
-}
-
+// ------------------------------------------------------------ float32
 __global__ __launch_bounds__(256) void ce_logits_f32_kernel(CeArgs c) {
   __shared__ F32Tile t;
   __shared__ __attribute__((aligned(16))) float stage[64][64 + 4];
@@ -296,16 +254,15 @@ __global__ __launch_bounds__(256) void ce_logits_f32_kernel(CeArgs c) {
   const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
   if (m0 >= M) return;
   const float *X = static_cast<const float *>(c.a.X), *W = static_cast<const float *>(c.a.W);
-  const f32x16_t acc = tile_f32<true>(
+  const f32x16_t acc = tile_f32<false>(
       t, 0, d,
       [&](int r, int k) {
         return *reinterpret_cast<const float4 *>(X + int64_t(c.w.rows[c.row0 + min(m0 + r, M - 1)]) * d + k);
       },
       [&](int r, int k) { return *reinterpret_cast<const float4 *>(W + int64_t(min(n0 + r, c.a.V - 1)) * d + k); });
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int v = 0; v < 16; ++v)
-    stage[(wave >> 1) * 32 + (v >> 2) * 8 + (lane >> 5) * 4 + (v & 3)][(wave & 1) * 32 + (lane & 31)] = acc[v];
+  for (int v = 0; v < 16; ++v) stage[f32_row(v)][f32_col()] = acc[v];
   __syncthreads();
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
@@ -417,9 +374,10 @@ struct ExpSrc {
 
 // K tiles of split z of n
 __device__ __forceinline__ void split_range(int kt, int splits, int z, int &k0, int &nk) {
-  const int b = int(int64_t(kt) * z / splits);
+  // scalar: the division is not, and the copies' bases have to be
+  const int b = __builtin_amdgcn_readfirstlane(int(int64_t(kt) * z / splits));
   k0 = b * 64;
-  nk = int(int64_t(kt) * (z + 1) / splits) - b;
+  nk = __builtin_amdgcn_readfirstlane(int(int64_t(kt) * (z + 1) / splits)) - b;
 }
 
 template <typename C>
@@ -474,16 +432,15 @@ __global__ __launch_bounds__(256) void ce_grad_f32_kernel(CeArgs c) {
   const float *e = static_cast<const float *>(c.w.e), *W = static_cast<const float *>(c.a.W);
   int k0, nk;
   split_range(int(c.w.lde / 64), c.w.splits, blockIdx.z, k0, nk);
-  const f32x16_t acc = tile_f32<false>(
+  const f32x16_t acc = tile_f32<true>(
       t, k0, k0 + nk * 64,
       [&](int r, int k) { return *reinterpret_cast<const float4 *>(e + int64_t(min(m0 + r, M - 1)) * c.w.lde + k); },
       [&](int n, int k) { return *reinterpret_cast<const float4 *>(W + int64_t(min(k, c.a.V - 1)) * d + n0 + n); });
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float *out = c.w.acc + int64_t(blockIdx.z) * c.w.block * d;
 #pragma unroll
   for (int v = 0; v < 16; ++v) {
-    const int lr = m0 + (wave >> 1) * 32 + (v >> 2) * 8 + (lane >> 5) * 4 + (v & 3);
-    if (lr < M) out[int64_t(lr) * d + n0 + (wave & 1) * 32 + (lane & 31)] = acc[v];
+    const int lr = m0 + f32_row(v);
+    if (lr < M) out[int64_t(lr) * d + n0 + f32_col()] = acc[v];
   }
 }
 

@@ -15,6 +15,7 @@
 #include "decode_tile.h"
 #include "plan_build.h"
 #include "shrink_units.h"
+#include "tile_f32.h"
 #include "tile_loop.h"
 
 namespace lora {
@@ -51,16 +52,18 @@ __device__ __forceinline__ float activate(float x, float &slope) {
 }
 
 // ------------------------------------------------------------ adapters' terms
-// Both projections' adapter terms of a 16-row block and the wave's 64
-// accumulator columns as MFMA passes: for every slot, adapter and 16 rank rows,
-// U times the pages' rows.  U (fp32; rows of other adapters zero) is bf16 hi
-// in the first 16 of K and lo in the second (error < 2^-16 of U), against the
-// page rows twice.  kPair (the forward): columns 0 .. 31 are the gate's c0 ..,
+// Both projections' adapter terms of a tile as MFMA passes, a slot of the rows
+// at a time: the tile's adapters are listed once, and each wave walks the list,
+// 16 rank rows a pass, over those of its 16-row blocks that hold the adapter.
+// A pass multiplies U (fp32; rows of other adapters zero), as bf16 hi in the
+// first 16 of K and lo in the second (error < 2^-16 of U), by the page rows
+// twice.  kPair (the forward): accumulator columns 0 .. 31 are the gate's c0 ..,
 // 32 .. 63 the up projection's, the same c0 ...  Otherwise (dX) both
 // projections' terms go into all of c0 .. c0 + 63.
-// The page rows come in 16-byte loads through the wave's LDS, read transposed
-// from there; the last adapter's fragments are kept, so that a run of blocks
-// loads them once.
+// Page rows come in 16-byte loads, a pass ahead, through the wave's LDS, and are
+// read transposed from there.  With one slot for each token the tile takes its
+// rows in the plan's order, so that an adapter's tokens lie together and its
+// pages are read by few tiles.
 struct Terms {
   ExpandArgs ex;
   const float *U_up;
@@ -69,13 +72,68 @@ struct Terms {
 
 constexpr int kTermLds = 4096;             // bytes of LDS per wave
 
-template <bool kPair>
-struct TermCache {
-  static constexpr int NF = kPair ? 4 : 8;
-  int key = -1;                            // first page id's place, or -1
-  bool dropped = false;                    // its values that are not finite were left out
-  bf16x8_t b[NF];                          // kPair: gate 0, 1, up 0, 1; else gate 0 .. 3, up 0 .. 3
+template <typename C>
+struct TileSegs {
+  int ps[C::BM], z[C::BM], lead[C::BM];    // page start (-1: none), U offset and list entry of each row
+  int l_ps[C::BM], l_r[C::BM], l_blocks[C::BM];
+  int cnt[C::BM / 64], n;
 };
+
+// Slot descriptor k of tile row threadIdx.x, or none.
+__device__ __forceinline__ int4 row_desc(const ExpandArgs &ex, const int *rows, int nrows, int k) {
+  int4 sd = make_int4(-1, 0, 0, 0);
+  if (int(threadIdx.x) < nrows && ex.U) sd = ex.slot_desc[int64_t(rows[threadIdx.x]) * ex.K + k];
+  return sd;
+}
+
+// Lists the adapters of a slot of the tile's rows (sd: row_desc).  Every thread
+// of the workgroup calls it.
+template <typename C>
+__device__ __forceinline__ void list_segs(TileSegs<C> &t, int4 sd) {
+  const int r = threadIdx.x, lane = r & 63;
+  lds_bar();                               // the last list is done with
+  if (r < C::BM) {
+    t.ps[r] = sd.x >= 0 ? sd.w : -1;
+    t.z[r] = sd.z;
+    t.l_blocks[r] = 0;
+  }
+  lds_bar();
+  int first = r;
+  bool leads = false;
+  if (r < C::BM && sd.x >= 0) {
+    for (int i = 0; i < r; i += 4) {
+      const int4 v = *reinterpret_cast<const int4 *>(&t.ps[i]);
+      if (v.x == sd.w || v.y == sd.w || v.z == sd.w || v.w == sd.w) {
+        first = i + (v.x == sd.w ? 0 : v.y == sd.w ? 1 : v.z == sd.w ? 2 : 3);
+        break;
+      }
+    }
+    first = min(first, r);
+    leads = first == r;
+  }
+  const unsigned long long m = __ballot(leads);
+  if (r < C::BM && lane == 0) t.cnt[r >> 6] = __popcll(m);
+  lds_bar();
+  int at = __popcll(m & ((1ull << lane) - 1));
+  for (int w = 0; w < (r >> 6) && w < C::BM / 64; ++w) at += t.cnt[w];
+  if (leads) {
+    t.lead[r] = at;
+    t.l_ps[at] = sd.w;
+    t.l_r[at] = sd.y;
+  }
+  if (r == 0) {
+    int n = 0;
+    for (int w = 0; w < C::BM / 64; ++w) n += t.cnt[w];
+    t.n = n;
+  }
+  lds_bar();
+  if (r < C::BM) {
+    const int l = sd.x >= 0 ? t.lead[first] : -1;
+    if (!leads) t.lead[r] = l;             // of rows that lead no list entry: no one else reads those
+    if (l >= 0) atomicOr(&t.l_blocks[l], 1 << (r >> 4));
+  }
+  lds_bar();
+}
 
 // 8 bf16 values with those that are not finite zero; whether there were any.
 __device__ __forceinline__ bool drop8(uint4 &w) {
@@ -90,6 +148,167 @@ __device__ __forceinline__ bool drop8(uint4 &w) {
   w = make_uint4(v[0], v[1], v[2], v[3]);
   return any != 0;
 }
+
+// 8 floats from 4-byte aligned memory, of which the first `have` are there.
+__device__ __forceinline__ void load8_tail(const float *p, int have, float (&v)[8]) {
+  if (__ballot(have < 8) == 0) {
+    __builtin_memcpy(v, p, 32);
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) v[q] = q < have ? p[q] : 0.f;
+}
+
+// acc += the listed terms for blocks blk0 .. blk0 + NB - 1 of the tile.  Returns the blocks (bit i: block blk0 + i)
+// that a page value which is not finite was left out of: it would reach other
+// adapters' rows as 0 . inf.  terms_nonfinite adds those.
+template <bool kPair, typename C, int NB>
+__device__ __forceinline__ unsigned add_segs(const Terms &e, const TileSegs<C> &t, char *lds, int blk0, int c0, int N,
+                                             f32x4_t (&acc)[NB][4]) {
+  constexpr int CPL = kPair ? 4 : 8;       // lanes along a page's columns
+  constexpr int NL = kPair ? 1 : 2;        // loads of a projection
+  constexpr int NF = kPair ? 2 : 4;        // fragments of a projection
+  constexpr int PITCH = CPL * 16, SIZE = 16 * PITCH;
+  const int lane = threadIdx.x & 63, col = min(c0 + (lane % CPL) * 8, N - 8);
+  const int n = __builtin_amdgcn_readfirstlane(t.n), mine_mask = ((1 << NB) - 1) << blk0;
+  const int total = e.ex.hdr[LORA_PH_RPAIRS];
+
+  auto entry = [&](int li) __attribute__((always_inline)) {
+    while (li < n && !(__builtin_amdgcn_readfirstlane(t.l_blocks[li]) & mine_mask)) ++li;
+    return li;
+  };
+  // the pass after (li, jb)
+  auto after = [&](int &li, int &jb) __attribute__((always_inline)) {
+    jb += 16;
+    if (jb >= __builtin_amdgcn_readfirstlane(t.l_r[li])) {
+      jb = 0;
+      li = entry(li + 1);
+    }
+  };
+  auto ids = [&](int li, int jb, int (&id)[NL]) __attribute__((always_inline)) {
+    const int nr = min(16, t.l_r[li] - jb), at = t.l_ps[li] + jb;
+#pragma unroll
+    for (int h = 0; h < NL; ++h) id[h] = e.ex.page_ids[at + min(lane / CPL + h * (64 / CPL), nr - 1)];
+  };
+  auto rows = [&](const int (&id)[NL], uint4 (&v)[2][NL]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int h = 0; h < NL; ++h) {
+      const int64_t at = int64_t(id[h]) * e.ex.d_out + col;
+      v[0][h] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(e.ex.b_pages) + at);
+      v[1][h] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(e.b_up) + at);
+    }
+  };
+
+  unsigned dropped = 0;
+  int li = entry(0), jb = 0;
+  if (li >= n) return 0;
+  int id[NL];
+  uint4 v[2][NL], w[2][NL];
+  ids(li, jb, id);
+  rows(id, v);
+  int lj = li, jj = jb;                    // the next pass
+  after(lj, jj);
+  if (lj < n) ids(lj, jj, id);
+  while (true) {
+    const bool more = lj < n;
+    if (more) rows(id, w);
+    int lk = lj, jk = jj;
+    if (more) after(lk, jk);
+    if (more && lk < n) ids(lk, jk, id);
+
+    const int nr = min(16, __builtin_amdgcn_readfirstlane(t.l_r[li]) - jb), j0 = 8 * ((lane >> 4) & 1);
+    const int blocks = __builtin_amdgcn_readfirstlane(t.l_blocks[li]) >> blk0;
+    // page rows: to LDS, and back as the B operand (column lane % 16, rank rows j0 .. + 7)
+    bool bad = false;
+#pragma unroll
+    for (int h = 0; h < NL; ++h) {
+      const int j = lane / CPL + h * (64 / CPL);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        if (j >= nr) v[p][h] = make_uint4(0u, 0u, 0u, 0u);
+        bad |= drop8(v[p][h]);
+        *reinterpret_cast<uint4 *>(lds + p * SIZE + j * PITCH + (lane % CPL) * 16) = v[p][h];
+      }
+    }
+    const bool any_bad = __ballot(bad) != 0;
+    bf16x8_t b[2 * NF];
+    typedef __attribute__((address_space(3))) v4i16_t lds_v4;
+    const int L = lane & 15, kk = j0 + (L >> 2);
+#pragma unroll
+    for (int f = 0; f < 2 * NF; ++f) {
+      const char *p = lds + (f / NF) * SIZE + kk * PITCH + (f % NF) * 32 + (L & 3) * 8;
+      const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4 *)(p));
+      const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4 *)(p + 4 * PITCH));
+      __builtin_memcpy(&b[f], &lo, 8);
+      __builtin_memcpy(reinterpret_cast<char *>(&b[f]) + 8, &hi, 8);
+    }
+    // U of two blocks in flight (registers)
+    constexpr int UB = 2;
+#pragma unroll
+    for (int i0 = 0; i0 < NB; i0 += UB) {
+      if (!((blocks >> i0) & ((1 << UB) - 1))) continue;
+      float x[UB][2][8];
+#pragma unroll
+      for (int i = 0; i < UB; ++i) {
+        // lane (row lane % 16, rank rows j0 .. j0 + 7); U's end may cut the 8 off
+        const int r = (blk0 + i0 + i) * 16 + L, at = t.z[r] + jb + j0;
+        const bool mine = ((blocks >> (i0 + i)) & 1) && t.lead[r] == li;
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          load8_tail((p ? e.U_up : e.ex.U) + (mine ? at : 0), min(8, mine ? total - at : total), x[i][p]);
+      }
+#pragma unroll
+      for (int i = 0; i < UB; ++i) {
+        if (!((blocks >> (i0 + i)) & 1)) continue;
+        if (any_bad) dropped |= 1u << (i0 + i);
+        const bool mine = t.lead[(blk0 + i0 + i) * 16 + L] == li;
+        bf16x8_t u[2];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          uint32_t q4[4];
+#pragma unroll
+          for (int q = 0; q < 8; q += 2) {
+            const float x0 = mine && j0 + q < nr ? x[i][p][q] : 0.f, x1 = mine && j0 + q + 1 < nr ? x[i][p][q + 1] : 0.f;
+            const uint32_t h = f2bf2(x0, x1);
+            q4[q >> 1] = lane < 32 ? h : f2bf2(x0 - bf_lo(h), x1 - bf_hi(h));
+          }
+          __builtin_memcpy(&u[p], q4, 16);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          f32x4_t &o = acc[i0 + i][c];
+          if constexpr (kPair) {
+            o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u[c >> 1], b[c], o, 0, 0, 0);
+          } else {
+            o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u[0], b[c], o, 0, 0, 0);
+            o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u[1], b[4 + c], o, 0, 0, 0);
+          }
+        }
+      }
+    }
+    if (!more) return dropped;
+    li = lj; jb = jj;
+    lj = lk; jj = jk;
+#pragma unroll
+    for (int h = 0; h < NL; ++h) {
+      v[0][h] = w[0][h];
+      v[1][h] = w[1][h];
+    }
+  }
+}
+
+// The common case of a prefill (one slot for each token, ranks of at most 16):
+// U of all the tile's rows goes to LDS at once, as the fragments of add_segs, and
+// the blocks take theirs one by one, the last adapter's page rows kept in
+// registers.  8192 tokens of four adapters in runs, 4096 -> 11008, three outputs:
+// 1272 us, 1343 by add_segs.
+template <bool kPair>
+struct TermCache {
+  static constexpr int NF = kPair ? 4 : 8;
+  int key = -1;                            // first page id's place, or -1
+  bool dropped = false;                    // its values that are not finite were left out
+  bf16x8_t b[NF];                          // kPair: gate 0, 1, up 0, 1; else gate 0 .. 3, up 0 .. 3
+};
 
 template <bool kPair>
 __device__ __forceinline__ void load_terms(const Terms &e, char *lds, int at, int nr, int c0, int N,
@@ -133,63 +352,6 @@ __device__ __forceinline__ void load_terms(const Terms &e, char *lds, int at, in
   }
 }
 
-// Returns whether a page value that is not finite was left out of the block:
-// it would reach other adapters' rows as 0 . inf.  terms_nonfinite adds those.
-template <bool kPair>
-__device__ __forceinline__ bool add_terms(const Terms &e, char *lds, int row0, int M, int c0, int N,
-                                          f32x4_t (&acc)[4], TermCache<kPair> &t) {
-  const int lane = threadIdx.x & 63, row = row0 + (lane & 15);
-  bool dropped = false;
-  for (int k = 0; k < e.ex.K; ++k) {
-    int4 sd = make_int4(-1, 0, 0, 0);
-    if (row < M) sd = e.ex.slot_desc[int64_t(row) * e.ex.K + k];
-    unsigned long long pending = __ballot(sd.x >= 0) & 0xffffull;
-    while (pending) {
-      const int leader = __ffsll(pending) - 1;
-      const int kps = __builtin_amdgcn_readfirstlane(__shfl(sd.w, leader, 64));
-      const int kr = __builtin_amdgcn_readfirstlane(__shfl(sd.y, leader, 64));
-      const bool mine = sd.x >= 0 && sd.w == kps && sd.y == kr;
-      pending &= ~__ballot(mine);
-      for (int jb = 0; jb < kr; jb += 16) {
-        const int nr = min(16, kr - jb), j0 = 8 * ((lane >> 4) & 1);
-        // A operand: lane (row lane % 16, rank rows j0 .. j0 + 7), hi or lo
-        bf16x8_t u[2];
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const float *U = (p ? e.U_up : e.ex.U) + int64_t(sd.z) + jb;
-          uint32_t w[4];
-          float v[8];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) v[q] = mine && j0 + q < nr ? U[j0 + q] : 0.f;
-#pragma unroll
-          for (int q = 0; q < 8; q += 2) {
-            const uint32_t h = f2bf2(v[q], v[q + 1]);
-            w[q >> 1] = lane < 32 ? h : f2bf2(v[q] - bf_lo(h), v[q + 1] - bf_hi(h));
-          }
-          __builtin_memcpy(&u[p], w, 16);
-        }
-        if (t.key != kps + jb) load_terms<kPair>(e, lds, kps + jb, nr, c0, N, t);
-        dropped |= t.dropped;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          if constexpr (kPair) {
-            acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u[b >> 1], t.b[b], acc[b], 0, 0, 0);
-          } else {
-            acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u[0], t.b[b], acc[b], 0, 0, 0);
-            acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u[1], t.b[4 + b], acc[b], 0, 0, 0);
-          }
-        }
-      }
-    }
-  }
-  return dropped;
-}
-
-// The common case (one slot for each token, ranks of at most 16): the tile's
-// slot descriptors are fetched under the K loop, and U of all its rows goes to
-// LDS at once, as the bf16 fragments of add_terms; block by block each of
-// those is a round trip with the matrix cores idle (8192 x 4096 -> 11008, three
-// outputs: 1403 -> 1240 us).
 template <typename C>
 struct TileTerms {
   int4 sd[C::BM];                          // .x < 0: no adapter
@@ -197,16 +359,8 @@ struct TileTerms {
   int wide;                                // a rank over 16
 };
 
-// Slot descriptor of tile row threadIdx.x, or none.
-template <typename C>
-__device__ __forceinline__ int4 tile_desc(const ExpandArgs &ex, int m0, int M) {
-  const int row = m0 + int(threadIdx.x);
-  if (int(threadIdx.x) >= C::BM || row >= M || ex.K != 1 || ex.U == nullptr) return make_int4(-1, 0, 0, 0);
-  return ex.slot_desc[row];
-}
-
-// After the K loop: fills t; false where the tile takes add_terms instead.
-// t lies in the stages, which the loop has left.
+// Fills t (sd: row_desc, of slot 0); false where a rank is over 16.  Every thread
+// of the workgroup calls it.
 template <typename C>
 __device__ __forceinline__ bool tile_terms(const Terms &e, TileTerms<C> &t, int4 sd) {
   const int tid = threadIdx.x;
@@ -245,7 +399,8 @@ __device__ __forceinline__ bool tile_terms(const Terms &e, TileTerms<C> &t, int4
   return true;
 }
 
-// add_terms from them; tr: the block's first row in the tile.
+// The terms of the block from tile row tr; returns whether values that are not
+// finite were left out.
 template <bool kPair, typename C>
 __device__ __forceinline__ bool add_tile_terms(const Terms &e, const TileTerms<C> &tt, char *lds, int tr, int c0,
                                                int N, f32x4_t (&acc)[4], TermCache<kPair> &t) {
@@ -280,7 +435,48 @@ __device__ __forceinline__ bool add_tile_terms(const Terms &e, const TileTerms<C
   return dropped;
 }
 
-// What add_terms left out: the products of U with the page values that are not
+template <typename C>
+struct TileLists {
+  static constexpr int SIZE = int(sizeof(TileTerms<C>) > sizeof(TileSegs<C>) ? sizeof(TileTerms<C>) : sizeof(TileSegs<C>));
+};
+
+// The tokens of tile rows m0 ..: with one slot for each token those of the
+// plan's pairs in its order, then the tokens without an active slot; else, or
+// where `in_order` asks for it, in token order.  Returns their number.  Every thread of the workgroup calls it.
+template <typename C>
+__device__ __forceinline__ int tile_rows(const ExpandArgs &ex, const int32_t *slot_pos, int *rows, int *cnt, int m0,
+                                         int M, bool in_order) {
+  const int n = min(C::BM, M - m0), tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (ex.K != 1 || in_order) {
+    if (tid < n) rows[tid] = m0 + tid;
+    lds_bar();
+    return n;
+  }
+  // (the pair's place exists in the plan, past its pairs too)
+  const int P = ex.hdr[LORA_PH_PAIRS], t = ex.pair_tk[m0 + min(tid, n - 1)];
+  if (tid < n && m0 + tid < P) rows[tid] = t;
+  if (m0 + n > P) {
+    int at = P - m0;                       // tile row of the next token without a pair
+    for (int t0 = 0; t0 < M && at < n; t0 += C::NT) {
+      const bool idle = t0 + tid < M && slot_pos[t0 + tid] < 0;
+      const unsigned long long m = __ballot(idle);
+      lds_bar();
+      if (lane == 0) cnt[wave] = __popcll(m);
+      lds_bar();
+      int mine = at + __popcll(m & ((1ull << lane) - 1)), all = 0;
+      for (int w = 0; w < C::NW; ++w) {
+        if (w < wave) mine += cnt[w];
+        all += cnt[w];
+      }
+      if (idle && mine >= 0 && mine < n) rows[mine] = t0 + tid;
+      at += all;
+    }
+  }
+  lds_bar();
+  return n;
+}
+
+// What add_segs left out: the products of U with the page values that are not
 // finite, of token `row` at column col, for projection p.  Rare.
 __device__ __forceinline__ float terms_nonfinite(const Terms &e, int row, int col, int p) {
   const float *U = p ? e.U_up : e.ex.U;
@@ -299,18 +495,247 @@ __device__ __forceinline__ float terms_nonfinite(const Terms &e, int row, int co
   return sum;
 }
 
+// Whether the plan has a pair for one of token t's first n slots.
+__device__ __forceinline__ bool any_slot(const int32_t *slot_pos, int t, int K, int n) {
+  bool any = false;
+  for (int k = 0; k < n; ++k) any |= slot_pos[int64_t(t) * K + k] >= 0;
+  return any;
+}
+__device__ __forceinline__ bool any_slot(const int32_t *slot_pos, int t, int K) { return any_slot(slot_pos, t, K, K); }
+
+// ------------------------------------------------------------ adapters' terms to memory
+// Batches of some hundred tokens have few tiles and many adapters for each of
+// them: walking those in the tiles is a chain of round trips (700 tokens of 96
+// adapters of ranks 8 .. 64, 2240 -> 5824: 235 us for the tiles).  Their terms are
+// formed ahead by a launch of their own, out[t][n] = sum_j U[u + j] . page_j[n] for
+// slot k of the tokens, in float32: a wave takes 16 pairs of the plan's order and
+// 128 columns, so that pages are read once for the pairs of an adapter among
+// them, and there are thousands of waves.  It walks their adapters, 16 rank rows
+// a pass, with the page ids two passes ahead and page rows and U one.  kSum: both
+// projections' terms into out[0] (dX), otherwise blockIdx.y's into its own.
+// Launched slot by slot; a token's first active slot writes, its others add.
+// The products are MFMAs with the rows of other adapters zero, so that all runs
+// of a window share accumulators: with a branch for each row and rank row, or
+// every product on the vector units, the same launch took 270 us and 73.
+// bf16 pages: U as hi | lo against the rows twice, as in add_segs; float32 pages:
+// v_mfma_f32_16x16x4_f32.
+template <typename E> struct TermTile;
+template <> struct TermTile<uint16_t> {
+  static constexpr int COLS = 128, NBLK = 8, NV = 4;
+  uint4 v[NV];
+  // rank rows lane / 16 + 4 h (page id in lane of that number), columns 8 (lane % 16) ..
+  __device__ __forceinline__ void load(const uint16_t *pages, int id, int c0, int N) {
+    const int lane = threadIdx.x, col = min(c0 + (lane & 15) * 8, N - 8);
+#pragma unroll
+    for (int h = 0; h < NV; ++h)
+      v[h] = *reinterpret_cast<const uint4 *>(pages + int64_t(__shfl(id, (lane >> 4) + 4 * h, 64)) * N + col);
+  }
+  // acc += U.rows; whether values that are not finite were left out
+  __device__ __forceinline__ bool add(char *lds, int nr, const float (&u)[8], f32x4_t (&acc)[NBLK]) {
+    const int lane = threadIdx.x, L = lane & 15;
+    bool bad = false;
+#pragma unroll
+    for (int h = 0; h < NV; ++h) {
+      const int j = (lane >> 4) + 4 * h;
+      if (j >= nr) v[h] = make_uint4(0u, 0u, 0u, 0u);
+      bad |= drop8(v[h]);
+      *reinterpret_cast<uint4 *>(lds + j * 256 + (L ^ ((j & 3) << 1)) * 16) = v[h];
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < 8; q += 2) {
+      const uint32_t h = f2bf2(u[q], u[q + 1]);
+      w[q >> 1] = lane < 32 ? h : f2bf2(u[q] - bf_lo(h), u[q + 1] - bf_hi(h));
+    }
+    bf16x8_t a;
+    __builtin_memcpy(&a, w, 16);
+    typedef __attribute__((address_space(3))) v4i16_t lds_v4;
+    const int k = 8 * ((lane >> 4) & 1) + (L >> 2);
+#pragma unroll
+    for (int b = 0; b < NBLK; ++b) {
+      // 16-byte piece 2 b + L % 4 / 2 of row k, in slot ^ 2 (k % 4)
+      const char *p = lds + k * 256 + ((2 * b + ((L & 3) >> 1)) ^ ((k & 3) << 1)) * 16 + (L & 1) * 8;
+      const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4 *)(p));
+      const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4 *)(p + 4 * 256));
+      bf16x8_t f;
+      __builtin_memcpy(&f, &lo, 8);
+      __builtin_memcpy(reinterpret_cast<char *>(&f) + 8, &hi, 8);
+      acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, f, acc[b], 0, 0, 0);
+    }
+    return __ballot(bad) != 0;
+  }
+  static __device__ __forceinline__ bool finite(uint16_t v) { return (v & 0x7f80u) != 0x7f80u; }
+};
+template <> struct TermTile<float> {
+  static constexpr int COLS = 64, NBLK = 4, NV = 16;
+  float v[NV];
+  // v[4 b + s]: rank row 4 s + lane / 16, column 16 b + lane % 16
+  __device__ __forceinline__ void load(const float *pages, int id, int c0, int N) {
+    const int lane = threadIdx.x;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const float *row = pages + int64_t(__shfl(id, 4 * s + (lane >> 4), 64)) * N + (lane & 15);
+#pragma unroll
+      for (int b = 0; b < NBLK; ++b) v[4 * b + s] = row[min(c0 + 16 * b, N - 16)];
+    }
+  }
+  __device__ __forceinline__ bool add(char *, int nr, const float (&u)[8], f32x4_t (&acc)[NBLK]) {
+    const int lane = threadIdx.x;
+    bool bad = false;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      // u: ranks 8 (lane / 16 % 2) .. of row lane % 16; wanted: rank 4 s + lane / 16
+      float a = 0.f;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float x = __shfl(u[(4 * s + g) & 7], (lane & 15) + 16 * ((4 * s + g) >> 3), 64);
+        if ((lane >> 4) == g) a = x;
+      }
+#pragma unroll
+      for (int b = 0; b < NBLK; ++b) {
+        float x = v[4 * b + s];
+        if (4 * s + (lane >> 4) >= nr) x = 0.f;
+        if (!(x - x == 0.f)) {
+          bad = true;
+          x = 0.f;
+        }
+        acc[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, x, acc[b], 0, 0, 0);
+      }
+    }
+    return __ballot(bad) != 0;
+  }
+  static __device__ __forceinline__ bool finite(float v) { return v - v == 0.f; }
+};
+
+template <typename E, bool kSum>
+__global__ __launch_bounds__(64) void terms_kernel(TermsArgs a) {
+  using Tile = TermTile<E>;
+  __shared__ __attribute__((aligned(16))) char lds[sizeof(E) == 2 ? 4096 : 16];
+  const int P = a.hdr[LORA_PH_PAIRS], total = a.hdr[LORA_PH_RPAIRS], lane = threadIdx.x;
+  const int n_x = (a.N + Tile::COLS - 1) / Tile::COLS, p0 = int(blockIdx.x / unsigned(n_x)) * 16, m = min(16, P - p0);
+  if (m <= 0 || int64_t(total) > a.u_cap) return;
+  // lane l (mod 16): pair p0 + l
+  const int pl = p0 + min(lane & 15, m - 1);
+  const int tk = a.pair_tk[pl], ad = a.pair_adapter[pl], uo = a.u_off[pl];
+  const int rk = a.rank[ad], pst = a.page_start[ad];
+  const int c0 = int(blockIdx.x % unsigned(n_x)) * Tile::COLS;
+  const unsigned want = unsigned(__ballot(lane < m && tk % a.K == a.k)) & 0xffffu;
+  if (!want) return;
+  auto lane_of = [&](int v, int l) __attribute__((always_inline)) { return __builtin_amdgcn_readlane(v, l); };
+  // a pass: projection p, the run of pairs [i, j) of one adapter, rank rows jb ..
+  struct Pass {
+    int p, i, j, jb;
+  };
+  auto run_at = [&](Pass &x, int i) __attribute__((always_inline)) {
+    // the next run from pair i that has a wanted pair
+    while (i < m) {
+      const int who = lane_of(ad, i);
+      const unsigned same = unsigned(__ballot(lane < m && ad == who)) & 0xffffu;
+      const int j = i + __popc(same >> i);         // pairs of an adapter lie together
+      if (want & same) {
+        x.i = i; x.j = j; x.jb = 0;
+        return;
+      }
+      i = j;
+    }
+    x.i = x.j = m;
+  };
+  auto after = [&](Pass &x) __attribute__((always_inline)) {
+    x.jb += 16;
+    if (x.jb < lane_of(rk, x.i)) return;
+    x.jb = 0;
+    if (kSum && x.p == 0) {
+      x.p = 1;
+      return;
+    }
+    if (kSum) x.p = 0;
+    run_at(x, x.j);
+  };
+  auto ids = [&](const Pass &x) __attribute__((always_inline)) {
+    const int nr = min(16, lane_of(rk, x.i) - x.jb);
+    return a.page_ids[lane_of(pst, x.i) + x.jb + min(lane & 15, nr - 1)];
+  };
+  auto fetch = [&](const Pass &x, int id, Tile &v, float (&u)[8]) __attribute__((always_inline)) {
+    v.load(static_cast<const E *>(x.p ? a.pages[1] : a.pages[0]), id, c0, a.N);
+    // U of row lane % 16, ranks 8 (lane / 16 % 2) .. + 7 of the pass
+    const int r = lane & 15, j0 = 8 * ((lane >> 4) & 1), nr = min(16, lane_of(rk, x.i) - x.jb);
+    const bool mine = r >= x.i && r < x.j;
+    const int at = uo + x.jb + j0;
+    load8_tail((x.p ? a.U[1] : a.U[0]) + (mine ? at : 0), min(8, mine ? total - at : total), u);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (!mine || j0 + q >= nr) u[q] = 0.f;
+  };
+
+  Pass c, n1;
+  c.p = kSum ? 0 : int(blockIdx.y);
+  run_at(c, 0);
+  n1 = c;
+  Tile v, w;
+  float u[8], un[8];
+  int id = ids(c);
+  fetch(c, id, v, u);
+  after(n1);
+  if (n1.i < m) id = ids(n1);
+  f32x4_t acc[Tile::NBLK];
+#pragma unroll
+  for (int b = 0; b < Tile::NBLK; ++b) acc[b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  bool dropped = false;
+  while (true) {
+    Pass n2 = n1;
+    const bool more = n1.i < m;
+    if (more) {
+      fetch(n1, id, w, un);
+      after(n2);
+      if (n2.i < m) id = ids(n2);
+    }
+    dropped |= v.add(lds, min(16, lane_of(rk, c.i) - c.jb), u, acc);
+    if (!more) break;
+    c = n1;
+    n1 = n2;
+    v = w;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) u[q] = un[q];
+  }
+  float *out = a.out[kSum ? 0 : blockIdx.y];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const int r = acc_row(0, x);
+    const int t = __shfl(tk, r, 64) / a.K, rr = __shfl(rk, r, 64), ps = __shfl(pst, r, 64), at = __shfl(uo, r, 64);
+    if (!((want >> r) & 1)) continue;
+    const bool add = any_slot(a.slot_pos, t, a.K, a.k);
+#pragma unroll
+    for (int b = 0; b < Tile::NBLK; ++b) {
+      const int col = c0 + acc_col(b);
+      if (col >= a.N) continue;
+      float *o = out + int64_t(t) * a.N + col;
+      float y = acc[b][x];
+      if (dropped) {
+        // the values left out: infinities and NaN
+        for (int p = kSum ? 0 : int(blockIdx.y); p < (kSum ? 2 : int(blockIdx.y) + 1); ++p)
+          for (int j = 0; j < rr; ++j) {
+            const E z = static_cast<const E *>(a.pages[p])[int64_t(a.page_ids[ps + j]) * a.N + col];
+            if (!Tile::finite(z)) y = fmaf(a.U[p][int64_t(at) + j], Elem<E>::to_f(z), y);
+          }
+      }
+      *o = add ? *o + y : y;
+    }
+  }
+}
+
 // ------------------------------------------------------------ forward, tiles
 // A rows of X by 32 rows of the gate's and 32 of the up projection's weight in
 // turn.
-template <typename C>
+template <typename C, bool kWide>
 struct GatedSrc {
   static_assert(C::TN == 4, "32 columns of each projection per wave");
   const uint16_t *a, *b[2];
-  uint32_t ao[C::A_INS], bo[C::B_INS];
+  RowOffsets<C::A_INS, kWide> ao;
+  uint32_t bo[C::B_INS];
   int wave, wm, wn;
   __device__ __forceinline__ void copy(uint32_t lds, int kt, int i) const {
     if (i < C::A_INS) {
-      lds_dma16_s(a + kt * 64, ao[i], lds + (wave * C::A_INS + i) * 1024);
+      ao.copy(a + kt * 64, i, lds + (wave * C::A_INS + i) * 1024);
     } else {
       const int ib = wave * C::B_INS + i - C::A_INS;     // 8 rows of the B tile, all of one weight
       lds_dma16_s(((ib >> 2) & 1 ? b[1] : b[0]) + kt * 64, bo[i - C::A_INS], lds + C::BM * C::ROWB + ib * 1024);
@@ -321,28 +746,31 @@ struct GatedSrc {
   }
 };
 
-template <typename C, int kAct>
+// kTerms: the adapters' terms come from terms_kernel's buffers.
+template <typename C, bool kWide, bool kTerms, int kAct>
 __global__ __launch_bounds__(C::NT, 1) void gated_tile_kernel(GatedArgs g) {
   constexpr int SC = 64 + 4;                            // floats of a staged row: 32 of g, 32 of u
   constexpr int NO = C::BN / 2;                         // output columns of the tile
   constexpr int WLDS = 16 * SC * 4 + kTermLds;          // bytes of a wave's epilogue
-  constexpr int TT = C::NW * WLDS;                      // the tile's terms lie behind those
-  __shared__ __attribute__((aligned(16))) char smem[2 * C::STAGE];
-  static_assert(TT % 16 == 0 && TT + sizeof(TileTerms<C>) <= 2 * C::STAGE, "staging must fit in LDS");
+  constexpr int TS = C::NW * WLDS;                      // the list of adapters lies behind those
+  __shared__ __attribute__((aligned(16))) char smem[C::LDS];
+  __shared__ int rows[C::BM], cnt[C::NW];
+  static_assert(TS % 16 == 0 && TS + (kTerms ? 0 : TileLists<C>::SIZE) <= C::LDS, "staging must fit in LDS");
   int tm, tn;
   if (!tile_of_workgroup(blockIdx.x, (g.M + C::BM - 1) / C::BM, (g.N + NO - 1) / NO, tm, tn)) return;
   const int m0 = tm * C::BM, n0 = tn * NO;
   const int lane = threadIdx.x & 63, wave = wave_id(), wm = wave / C::WN, wn = wave % C::WN;
+  const int nrows = tile_rows<C>(g.ex, g.slot_pos, rows, cnt, m0, g.M, kTerms);
 
-  GatedSrc<C> src;
+  GatedSrc<C, kWide> src;
   src.wave = wave; src.wm = wm; src.wn = wn;
-  src.a = static_cast<const uint16_t *>(g.X) + int64_t(m0) * g.Kd;
+  src.a = static_cast<const uint16_t *>(g.X);
 #pragma unroll
   for (int p = 0; p < 2; ++p) src.b[p] = static_cast<const uint16_t *>(g.W[p]) + int64_t(n0) * g.Kd;
 #pragma unroll
   for (int i = 0; i < C::A_INS; ++i) {
     const int row = (wave * C::A_INS + i) * 8 + (lane >> 3);
-    src.ao[i] = (uint32_t(min(row, g.M - 1 - m0)) * uint32_t(g.Kd) + tswz(row, lane & 7) * 8) * 2;
+    src.ao.set(i, int64_t(rows[min(row, nrows - 1)]) * g.Kd + tswz(row, lane & 7) * 8);
   }
 #pragma unroll
   for (int i = 0; i < C::B_INS; ++i) {
@@ -350,46 +778,79 @@ __global__ __launch_bounds__(C::NT, 1) void gated_tile_kernel(GatedArgs g) {
     const int of = (row >> 6) * 32 + (row & 31);        // of its weight
     src.bo[i] = (uint32_t(min(of, g.N - 1 - n0)) * uint32_t(g.Kd) + tswz(row, lane & 7) * 8) * 2;
   }
-  const int4 sd = tile_desc<C>(g.ex, m0, g.M);
+  // fetched under the K loop
+  const int4 sd0 = kTerms ? make_int4(-1, 0, 0, 0) : row_desc(g.ex, rows, nrows, 0);
   f32x4_t acc[C::TM][C::TN];
   tile_loop<C>(src, smem, g.Kd / 64, acc);
 
   const Terms e{g.ex, g.U_up, g.b_up};
-  const bool lora_on = expand_enabled(g.ex);
-  TileTerms<C> &tt = *reinterpret_cast<TileTerms<C> *>(smem + TT);
-  const bool common = lora_on && g.ex.K == 1 && tile_terms<C>(e, tt, sd);
+  TileSegs<C> &segs = *reinterpret_cast<TileSegs<C> *>(smem + TS);
   const int c0 = n0 + wn * 32;                          // the wave's output columns
-  if (c0 >= g.N) return;
+  const bool inside = c0 < g.N;
   float *stage = reinterpret_cast<float *>(smem + wave * WLDS);
   char *tlds = smem + wave * WLDS + 16 * SC * 4;
+  unsigned dropped = 0;
+  const bool lora_on = expand_enabled(g.ex);
+  TileTerms<C> &tt = *reinterpret_cast<TileTerms<C> *>(smem + TS);
+  bool common = false;
+  if constexpr (!kTerms) common = lora_on && g.ex.K == 1 && tile_terms<C>(e, tt, sd0);
+  if (lora_on && !kTerms && !common) {
+    for (int k = 0; k < g.ex.K; ++k) {
+      list_segs<C>(segs, k ? row_desc(g.ex, rows, nrows, k) : sd0);
+      if (inside) dropped |= add_segs<true, C, C::TM>(e, segs, tlds, wm * C::TM, c0, g.N, acc);
+    }
+  }
+  if (!inside) return;
   TermCache<true> cache;
+  // kTerms: the adapters' terms of a row, a block ahead
+  Raw8<float> tg, tu;
+  bool has = false;
+  auto fetch = [&](int i) __attribute__((always_inline)) {
+    const int rr = (wm * C::TM + i) * 16 + (lane >> 2), cc = (lane & 3) * 8;
+    has = lora_on && rr < nrows && any_slot(g.slot_pos, rows[rr], g.ex.K);
+    if (!has) return;
+    const int64_t at = int64_t(rows[rr]) * g.N + c0 + cc;
+    tg.load(g.term[0] + at);
+    tu.load(g.term[1] + at);
+  };
+  if constexpr (kTerms) fetch(0);
 #pragma unroll
   for (int i = 0; i < C::TM; ++i) {
-    const int r0 = m0 + (wm * C::TM + i) * 16;
-    bool dropped = false;
-    if (common) dropped = add_tile_terms<true, C>(e, tt, tlds, (wm * C::TM + i) * 16, c0, g.N, acc[i], cache);
-    else if (lora_on) dropped = add_terms<true>(e, tlds, r0, g.M, c0, g.N, acc[i], cache);
+    const int r0 = (wm * C::TM + i) * 16;
+    if (common && add_tile_terms<true, C>(e, tt, tlds, r0, c0, g.N, acc[i], cache)) dropped |= 1u << i;
+    float dg[8] = {}, du[8] = {};
+    if constexpr (kTerms) {
+      if (has) {
+        tg.to8(dg);
+        tu.to8(du);
+      }
+      if (i + 1 < C::TM) fetch(i + 1);
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int v = 0; v < 4; ++v) stage[acc_row(0, v) * SC + acc_col(j)] = acc[i][j][v];
-    if (dropped) {
+    if ((dropped >> i) & 1) {
 #pragma unroll 1
-      for (int rr = 0; rr < 16 && r0 + rr < g.M; ++rr)
-        stage[rr * SC + lane] += terms_nonfinite(e, r0 + rr, c0 + (lane & 31), lane >> 5);
+      for (int rr = 0; rr < 16 && r0 + rr < nrows; ++rr)
+        stage[rr * SC + lane] += terms_nonfinite(e, rows[r0 + rr], c0 + (lane & 31), lane >> 5);
     }
     // a lane takes 8 columns of one of the rows
-    const int rr = lane >> 2, row = r0 + rr, cc = (lane & 3) * 8;
-    if (row >= g.M) continue;
+    const int rr = lane >> 2, cc = (lane & 3) * 8;
+    if (r0 + rr >= nrows) continue;
     float gv[8], uv[8], h[8];
     Elem<float>::load8(stage + rr * SC + cc, gv);
     Elem<float>::load8(stage + rr * SC + 32 + cc, uv);
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
       float slope;
+      if constexpr (kTerms) {
+        gv[x] += dg[x];
+        uv[x] += du[x];
+      }
       h[x] = activate<kAct, true>(gv[x], slope) * uv[x];
     }
-    const int64_t at = int64_t(row) * g.N + c0 + cc;
+    const int64_t at = int64_t(rows[r0 + rr]) * g.N + c0 + cc;
     store8_nt(static_cast<uint16_t *>(g.H) + at, h);
     if (g.pre_gate) {
       store8_nt(static_cast<uint16_t *>(g.pre_gate) + at, gv);
@@ -398,37 +859,7 @@ __global__ __launch_bounds__(C::NT, 1) void gated_tile_kernel(GatedArgs g) {
   }
 }
 
-// ------------------------------------------------------------ split forms
-// Pieces of an output element: the K splits, or the stream-K workgroups that
-// covered its tile.
-__device__ __forceinline__ int pieces_of(int splits, int sk_g, int sk_kt, int bm, int bn, int M, int N, int row,
-                                         int col) {
-  if (sk_g <= 0) return splits;
-  const int tiles_n = (N + bn - 1) / bn;
-  const int t = (row / bm) * tiles_n + col / bn;
-  const int64_t U = int64_t((M + bm - 1) / bm) * tiles_n * sk_kt;
-  const int64_t x0 = int64_t(t) * sk_kt, x1 = x0 + sk_kt - 1;
-  return int(((x1 + 1) * sk_g - 1) / U - ((x0 + 1) * sk_g - 1) / U) + 1;
-}
-
-// v += pieces of 8 columns of both products, 8 loads in flight.
-__device__ __forceinline__ void add_pieces(const float *part, int np, int M, int N, int row, int col, float (&v)[8]) {
-  for (int z0 = 0; z0 < np; z0 += 8) {
-    Raw8<float> pr[8];
-#pragma unroll
-    for (int z = 0; z < 8; ++z) pr[z].load(part + (int64_t(min(z0 + z, np - 1)) * M + row) * N + col);
-#pragma unroll
-    for (int z = 0; z < 8; ++z) {
-      if (z0 + z < np) {
-        float o[8];
-        pr[z].to8(o);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] += o[c];
-      }
-    }
-  }
-}
-
+// ------------------------------------------------------------ decode
 // Decode: workgroup 0 builds the plan, then come the decode GEMM tiles of the
 // gate's weight and of the up projection's, then the per-slot shrinks (four
 // parts a slot) of both.  No part reads what another writes.
@@ -549,39 +980,50 @@ __global__ __launch_bounds__(256) void gated_decode_epilogue_kernel(GatedArgs g)
   }
 }
 
-// One wave per row and 512 columns.
-template <typename E, int NW, int kAct>
-__global__ __launch_bounds__(NW * 64) void gated_epilogue_kernel(GatedArgs g) {
-  const int lane = threadIdx.x & 63, row = blockIdx.y * NW + (threadIdx.x >> 6);
+// ------------------------------------------------------------ float32
+// 64 tokens by 32 output columns: the B side of a tile_f32 is 32 rows of each
+// weight, g and u meet in LDS.
+template <int kAct>
+__global__ __launch_bounds__(256) void gated_f32_kernel(GatedArgs g) {
+  __shared__ F32Tile t;
+  __shared__ __attribute__((aligned(16))) float stage[64][64 + 4];
+  const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 32;
+  const float *X = static_cast<const float *>(g.X);
+  const float *Wg = static_cast<const float *>(g.W[0]), *Wu = static_cast<const float *>(g.W[1]);
+  const f32x16_t acc = tile_f32<false>(
+      t, 0, g.Kd,
+      [&](int r, int k) { return *reinterpret_cast<const float4 *>(X + int64_t(min(m0 + r, g.M - 1)) * g.Kd + k); },
+      [&](int r, int k) {
+        return *reinterpret_cast<const float4 *>((r < 32 ? Wg : Wu) + int64_t(n0 + (r & 31)) * g.Kd + k);
+      });
+#pragma unroll
+  for (int v = 0; v < 16; ++v) stage[f32_row(v)][f32_col()] = acc[v];
+  __syncthreads();
+  const int rr = threadIdx.x >> 2, cc = (threadIdx.x & 3) * 8, row = m0 + rr;
   if (row >= g.M) return;
-  const int col_raw = (blockIdx.x * 64 + lane) * 8;
-  const bool ok = col_raw < g.N;
-  const int col = ok ? col_raw : g.N - 8;               // loads stay in bounds
-  const bool lora_on = expand_enabled(g.ex);
-  int4 sd = make_int4(-1, 0, 0, 0);
-  if (lora_on) sd = expand_row_desc<E>(row, g.ex);
-  const int np = pieces_of(g.splits, g.sk_g, g.sk_kt, g.bm, g.bn, g.M, g.N, row, col);
-  float gv[8] = {}, uv[8] = {}, h[8];
-  add_pieces(g.part[0], np, g.M, g.N, row, col, gv);
-  add_pieces(g.part[1], np, g.M, g.N, row, col, uv);
-  if (lora_on) {
-    ExpandArgs eu = g.ex;
-    eu.U = g.U_up;
-    eu.b_pages = g.b_up;
-    expand_row8<E>(gv, sd, col, g.ex);
-    expand_row8<E>(uv, sd, col, eu);
+  const int64_t at = int64_t(row) * g.N + n0 + cc;
+  float gv[8], uv[8], h[8];
+  Elem<float>::load8(&stage[rr][cc], gv);
+  Elem<float>::load8(&stage[rr][32 + cc], uv);
+  if (expand_enabled(g.ex) && any_slot(g.slot_pos, row, g.ex.K)) {
+    float dg[8], du[8];
+    Elem<float>::load8(g.term[0] + at, dg);
+    Elem<float>::load8(g.term[1] + at, du);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      gv[x] += dg[x];
+      uv[x] += du[x];
+    }
   }
 #pragma unroll
   for (int x = 0; x < 8; ++x) {
     float slope;
-    h[x] = activate<kAct, sizeof(E) == 2>(gv[x], slope) * uv[x];
+    h[x] = activate<kAct, false>(gv[x], slope) * uv[x];
   }
-  if (!ok) return;
-  const int64_t at = int64_t(row) * g.N + col;
-  Cols<E, 8>::store(static_cast<E *>(g.H) + at, h);
+  Cols<float, 8>::store(static_cast<float *>(g.H) + at, h);
   if (g.pre_gate) {
-    Cols<E, 8>::store(static_cast<E *>(g.pre_gate) + at, gv);
-    Cols<E, 8>::store(static_cast<E *>(g.pre_up) + at, uv);
+    Cols<float, 8>::store(static_cast<float *>(g.pre_gate) + at, gv);
+    Cols<float, 8>::store(static_cast<float *>(g.pre_up) + at, uv);
   }
 }
 
@@ -607,16 +1049,17 @@ __global__ __launch_bounds__(256) void gated_act_grad_kernel(const E *dH, const 
 }
 
 // K tiles of dg.Wg^T, then those of du.Wu^T.
-template <typename C>
+template <typename C, bool kWide>
 struct GatedGradSrc {
   const uint16_t *a[2], *b[2];
-  uint32_t ao[C::A_INS], bo[C::B_INS];
+  RowOffsets<C::A_INS, kWide> ao;
+  uint32_t bo[C::B_INS];
   int wave, wm, wn, kt1;
   __device__ __forceinline__ void copy(uint32_t lds, int kt, int i) const {
     const bool p = kt >= kt1;
     const int k = (p ? kt - kt1 : kt) * 64;
     if (i < C::A_INS) {
-      lds_dma16_s((p ? a[1] : a[0]) + k, ao[i], lds + (wave * C::A_INS + i) * 1024);
+      ao.copy((p ? a[1] : a[0]) + k, i, lds + (wave * C::A_INS + i) * 1024);
     } else {
       lds_dma16_s((p ? b[1] : b[0]) + k, bo[i - C::A_INS],
                   lds + C::BM * C::ROWB + (wave * C::B_INS + i - C::A_INS) * 1024);
@@ -627,120 +1070,192 @@ struct GatedGradSrc {
   }
 };
 
-template <typename C>
+// Split z of kSplit takes a part of the K tiles and leaves float32 sums for
+// gated_grad_x_sum_kernel; without kSplit dX itself, adapters' terms and all.
+template <typename C, bool kSplit, bool kWide>
 __global__ __launch_bounds__(C::NT, 1) void gated_grad_x_tile_kernel(GatedGradXArgs g) {
   constexpr int SC = 64 + 4;                            // a wave stages 16 rows, and those of the adapters' term
   constexpr int WLDS = 2 * 16 * SC * 4 + kTermLds;
-  constexpr int TT = C::NW * WLDS;
-  constexpr int LDS = TT + int(sizeof(TileTerms<C>)) > 2 * C::STAGE ? TT + int(sizeof(TileTerms<C>)) : 2 * C::STAGE;
-  static_assert(C::TN == 4, "64 columns per wave");
-  static_assert(TT % 16 == 0 && LDS <= 160 * 1024, "staging must fit in LDS");
+  constexpr int TS = C::NW * WLDS;
+  constexpr int NB = 2;                                 // blocks whose adapters' term is in registers
+  static_assert(C::TN == 4 && C::TM % NB == 0, "64 columns per wave");
+  constexpr int LDS = !kSplit && TS + TileLists<C>::SIZE > C::LDS ? TS + TileLists<C>::SIZE : C::LDS;
+  static_assert(TS % 16 == 0 && LDS <= 156 * 1024, "staging must fit in LDS");
   __shared__ __attribute__((aligned(16))) char smem[LDS];
+  __shared__ int rows[C::BM], cnt[C::NW];
   int tm, tn;
   if (!tile_of_workgroup(blockIdx.x, (g.M + C::BM - 1) / C::BM, (g.N + C::BN - 1) / C::BN, tm, tn)) return;
   const int m0 = tm * C::BM, n0 = tn * C::BN;
   const int lane = threadIdx.x & 63, wave = wave_id(), wm = wave / C::WN, wn = wave % C::WN;
-  GatedGradSrc<C> src;
+  const int nrows = tile_rows<C>(g.ex, g.slot_pos, rows, cnt, m0, g.M, kSplit);
+  GatedGradSrc<C, kWide> src;
   src.wave = wave; src.wm = wm; src.wn = wn;
-  src.kt1 = g.Kd / 64;
+  const int kt = g.Kd / 64, z = kSplit ? int(blockIdx.y) : 0;
+  // (scalar: the division is not, and the copies' bases have to be)
+  const int kb = kSplit ? __builtin_amdgcn_readfirstlane(int(int64_t(2 * kt) * z / g.splits)) : 0;
+  const int ke = kSplit ? __builtin_amdgcn_readfirstlane(int(int64_t(2 * kt) * (z + 1) / g.splits)) : 2 * kt;
+  const int nk = ke - kb;
+  src.kt1 = max(kt - kb, 0);                            // K tiles of the gate's product
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
-    src.a[p] = static_cast<const uint16_t *>(g.dY[p]) + int64_t(m0) * g.Kd;
-    src.b[p] = static_cast<const uint16_t *>(g.W[p]) + int64_t(n0) * g.Kd;
+    const int k0 = p == 0 ? min(kb, kt - 1) : max(kb - kt, 0);
+    src.a[p] = static_cast<const uint16_t *>(g.dY[p]) + k0 * 64;
+    src.b[p] = static_cast<const uint16_t *>(g.W[p]) + int64_t(n0) * g.Kd + k0 * 64;
   }
 #pragma unroll
   for (int i = 0; i < C::A_INS; ++i) {
     const int row = (wave * C::A_INS + i) * 8 + (lane >> 3);
-    src.ao[i] = (uint32_t(min(row, g.M - 1 - m0)) * uint32_t(g.Kd) + tswz(row, lane & 7) * 8) * 2;
+    src.ao.set(i, int64_t(rows[min(row, nrows - 1)]) * g.Kd + tswz(row, lane & 7) * 8);
   }
 #pragma unroll
   for (int i = 0; i < C::B_INS; ++i) {
     const int row = (wave * C::B_INS + i) * 8 + (lane >> 3);
     src.bo[i] = (uint32_t(min(row, g.N - 1 - n0)) * uint32_t(g.Kd) + tswz(row, lane & 7) * 8) * 2;
   }
-  const int4 sd = tile_desc<C>(g.ex, m0, g.M);
+  const int4 sd0 = kSplit ? make_int4(-1, 0, 0, 0) : row_desc(g.ex, rows, nrows, 0);
   f32x4_t acc[C::TM][C::TN];
-  tile_loop<C>(src, smem, 2 * src.kt1, acc);
+  tile_loop<C>(src, smem, nk, acc);
+  if constexpr (kSplit) {
+    float *out = g.sums + int64_t(z) * g.M * g.N;
+#pragma unroll
+    for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::TN; ++j) {
+        const int col = n0 + wn * C::TN * 16 + acc_col(j);
+        if (col >= g.N) continue;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int row = m0 + wm * C::TM * 16 + acc_row(i, v);
+          if (row < g.M) out[int64_t(row) * g.N + col] = acc[i][j][v];
+        }
+      }
+    return;
+  }
 
   const Terms e{g.ex, g.U_up, g.b_up};
+  TileSegs<C> &segs = *reinterpret_cast<TileSegs<C> *>(smem + TS);
   const bool lora_on = expand_enabled(g.ex);
-  TileTerms<C> &tt = *reinterpret_cast<TileTerms<C> *>(smem + TT);
-  const bool common = lora_on && g.ex.K == 1 && tile_terms<C>(e, tt, sd);
   const int vr = lane >> 3, vc = (lane & 7) * 8, c0 = n0 + wn * 64;
-  if (c0 >= g.N) return;
+  const bool inside = c0 < g.N;
   float *stage = reinterpret_cast<float *>(smem + wave * WLDS), *lstage = stage + 16 * SC;
   char *tlds = smem + wave * WLDS + 2 * 16 * SC * 4;
+  TileTerms<C> &tt = *reinterpret_cast<TileTerms<C> *>(smem + TS);
+  const bool common = lora_on && g.ex.K == 1 && tile_terms<C>(e, tt, sd0);
   TermCache<false> cache;
 #pragma unroll
-  for (int i = 0; i < C::TM; ++i) {
-    const int r0 = m0 + (wm * C::TM + i) * 16;
+  for (int half = 0; half < C::TM / NB; ++half) {
+    f32x4_t term[NB][4];
+    unsigned dropped = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int i = 0; i < NB; ++i)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) stage[acc_row(0, v) * SC + acc_col(j)] = acc[i][j][v];
-      acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < 4; ++j) term[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    if (lora_on && !common) {
+      for (int k = 0; k < g.ex.K; ++k) {
+        if (half == 0 || g.ex.K > 1) list_segs<C>(segs, k ? row_desc(g.ex, rows, nrows, k) : sd0);
+        if (inside)
+          dropped |= add_segs<false, C, NB>(e, segs, tlds, wm * C::TM + half * NB, c0, g.N, term);
+      }
     }
-    bool dropped = false;
-    if (common) dropped = add_tile_terms<false, C>(e, tt, tlds, (wm * C::TM + i) * 16, c0, g.N, acc[i], cache);
-    else if (lora_on) dropped = add_terms<false>(e, tlds, r0, g.M, c0, g.N, acc[i], cache);
+    if (!inside) continue;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int i = 0; i < NB; ++i) {
+      const int r0 = (wm * C::TM + half * NB + i) * 16;
+      if (common && add_tile_terms<false, C>(e, tt, tlds, r0, c0, g.N, term[i], cache)) dropped |= 1u << i;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) lstage[acc_row(0, v) * SC + acc_col(j)] = acc[i][j][v];
-    if (dropped) {
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          stage[acc_row(0, v) * SC + acc_col(j)] = acc[half * NB + i][j][v];
+          lstage[acc_row(0, v) * SC + acc_col(j)] = term[i][j][v];
+        }
+      if ((dropped >> i) & 1) {
 #pragma unroll 1
-      for (int rr = 0; rr < 16 && r0 + rr < g.M; ++rr)
-        lstage[rr * SC + lane] += terms_nonfinite(e, r0 + rr, c0 + lane, 0) + terms_nonfinite(e, r0 + rr, c0 + lane, 1);
-    }
+        for (int rr = 0; rr < 16 && r0 + rr < nrows; ++rr)
+          lstage[rr * SC + lane] += terms_nonfinite(e, rows[r0 + rr], c0 + lane, 0) +
+                                    terms_nonfinite(e, rows[r0 + rr], c0 + lane, 1);
+      }
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int rr = q * 8 + vr, row = r0 + rr;
-      if (row >= g.M) continue;
-      float b[8], l[8];
-      Elem<float>::load8(stage + rr * SC + vc, b);
-      Elem<float>::load8(lstage + rr * SC + vc, l);
-      const int64_t at = int64_t(row) * g.N + c0 + vc;
-      uint2 mw = make_uint2(0x01010101u, 0x01010101u);
-      if (g.mask) mw = *reinterpret_cast<const uint2 *>(g.mask + at);
+      for (int q = 0; q < 2; ++q) {
+        const int rr = q * 8 + vr;
+        if (r0 + rr >= nrows) continue;
+        float b[8], l[8];
+        Elem<float>::load8(stage + rr * SC + vc, b);
+        Elem<float>::load8(lstage + rr * SC + vc, l);
+        const int64_t at = int64_t(rows[r0 + rr]) * g.N + c0 + vc;
+        uint2 mw = make_uint2(0x01010101u, 0x01010101u);
+        if (g.mask) mw = *reinterpret_cast<const uint2 *>(g.mask + at);
 #pragma unroll
-      for (int x = 0; x < 8; ++x)
-        b[x] += float(((x < 4 ? mw.x : mw.y) >> (8 * (x & 3))) & 0xffu) * l[x];
-      store8_nt(static_cast<uint16_t *>(g.dX) + at, b);
+        for (int x = 0; x < 8; ++x)
+          b[x] += float(((x < 4 ? mw.x : mw.y) >> (8 * (x & 3))) & 0xffu) * l[x];
+        store8_nt(static_cast<uint16_t *>(g.dX) + at, b);
+      }
     }
   }
 }
 
-template <typename E, int NW>
-__global__ __launch_bounds__(NW * 64) void gated_grad_x_epilogue_kernel(GatedGradXArgs g) {
-  const int lane = threadIdx.x & 63, row = blockIdx.y * NW + (threadIdx.x >> 6);
-  if (row >= g.M) return;
-  const int col_raw = (blockIdx.x * 64 + lane) * 8;
-  const bool ok = col_raw < g.N;
-  const int col = ok ? col_raw : g.N - 8;
-  const bool lora_on = expand_enabled(g.ex);
-  int4 sd = make_int4(-1, 0, 0, 0);
-  if (lora_on) sd = expand_row_desc<E>(row, g.ex);
-  const int np = pieces_of(g.splits, g.sk_g, g.sk_kt, g.bm, g.bn, g.M, g.N, row, col);
-  float v[8] = {}, l[8] = {};
-  add_pieces(g.part[0], np, g.M, g.N, row, col, v);
-  add_pieces(g.part[1], np, g.M, g.N, row, col, v);
-  if (lora_on) {
-    ExpandArgs eu = g.ex;
-    eu.U = g.U_up;
-    eu.b_pages = g.b_up;
-    expand_row8<E>(l, sd, col, g.ex);
-    expand_row8<E>(l, sd, col, eu);
-    uint2 mw = make_uint2(0x01010101u, 0x01010101u);
-    if (g.mask) mw = *reinterpret_cast<const uint2 *>(g.mask + int64_t(row) * g.N + col);
+// float32: the K range of split blockIdx.z, over both products.
+__global__ __launch_bounds__(256) void gated_grad_x_f32_kernel(GatedGradXArgs g) {
+  __shared__ F32Tile t;
+  const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64, z = blockIdx.z, kt = 2 * (g.Kd / 64);
+  const int kb = int(int64_t(kt) * z / g.splits) * 64, ke = int(int64_t(kt) * (z + 1) / g.splits) * 64;
+  auto at = [&](const void *const (&m)[2], int row, int k) __attribute__((always_inline)) {
+    const bool p = k >= g.Kd;
+    return *reinterpret_cast<const float4 *>(static_cast<const float *>(p ? m[1] : m[0]) + int64_t(row) * g.Kd +
+                                             (p ? k - g.Kd : k));
+  };
+  const f32x16_t acc = tile_f32<false>(
+      t, kb, ke, [&](int r, int k) { return at(g.dY, min(m0 + r, g.M - 1), k); },
+      [&](int r, int k) { return at(g.W, n0 + r, k); });
+  float *out = g.sums + int64_t(z) * g.M * g.N;
 #pragma unroll
-    for (int x = 0; x < 8; ++x)
-      v[x] += float(((x < 4 ? mw.x : mw.y) >> (8 * (x & 3))) & 0xffu) * l[x];
+  for (int v = 0; v < 16; ++v) {
+    const int row = m0 + f32_row(v);
+    if (row < g.M) out[int64_t(row) * g.N + n0 + f32_col()] = acc[v];
   }
-  if (ok) Cols<E, 8>::store(static_cast<E *>(g.dX) + int64_t(row) * g.N + col, v);
+}
+
+// dX from the splits' sums, in order, and the masked adapters' term; 8 elements
+// a thread.
+template <typename E>
+__global__ __launch_bounds__(256) void gated_grad_x_sum_kernel(GatedGradXArgs g) {
+  const int64_t n = int64_t(g.M) * g.N, i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 8;
+  if (i >= n) return;
+  const int row = int(i / g.N);
+  const bool has = expand_enabled(g.ex) && any_slot(g.slot_pos, row, g.ex.K);
+  Raw8<float> term;
+  uint2 mw = make_uint2(0x01010101u, 0x01010101u);
+  if (has) {
+    term.load(g.term + i);
+    if (g.mask) mw = *reinterpret_cast<const uint2 *>(g.mask + i);
+  }
+  float v[8];
+  Elem<float>::load8(g.sums + i, v);
+  for (int z0 = 1; z0 < g.splits; z0 += 4) {
+    Raw8<float> pr[4];
+#pragma unroll
+    for (int z = 0; z < 4; ++z) pr[z].load(g.sums + int64_t(min(z0 + z, g.splits - 1)) * n + i);
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+      if (z0 + z < g.splits) {
+        float o[8];
+        pr[z].to8(o);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] += o[c];
+      }
+    }
+  }
+  if (has) {
+    float l[8];
+    term.to8(l);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) v[x] += float(((x < 4 ? mw.x : mw.y) >> (8 * (x & 3))) & 0xffu) * l[x];
+  }
+  Cols<E, 8>::store(static_cast<E *>(g.dX) + i, v);
 }
 
 using Big = LoopCfg<256, 256, 2, 4>;
-using Mid = LoopCfg<128, 128, 2, 2>;
+using Mid = LoopCfg<128, 256, 2, 4, 3>;
 
 template <typename E>
 void launch_act_grad(const void *dH, const void *pg, const void *pu, int act, void *dg, void *du, int64_t n,
@@ -759,25 +1274,65 @@ void launch_act_grad(const void *dH, const void *pg, const void *pu, int act, vo
 
 }  // namespace
 
-bool gated_fused(int T, int d_out, int dtype) { return dtype == LORA_BF16 && T > 128; }
-
 namespace {
 
-template <typename C>
+template <typename C, bool kWide, bool kTerms>
 void launch_tiles(const GatedArgs &g, hipStream_t s) {
   const int tiles = ((g.M + C::BM - 1) / C::BM) * ((g.N + C::BN / 2 - 1) / (C::BN / 2));
   const dim3 grid(8 * unsigned((tiles + 7) / 8)), block(C::NT);
-  if (g.act == LORA_ACT_SILU) hipLaunchKernelGGL((gated_tile_kernel<C, LORA_ACT_SILU>), grid, block, 0, s, g);
-  else if (g.act == LORA_ACT_GELU) hipLaunchKernelGGL((gated_tile_kernel<C, LORA_ACT_GELU>), grid, block, 0, s, g);
-  else hipLaunchKernelGGL((gated_tile_kernel<C, LORA_ACT_GELU_TANH>), grid, block, 0, s, g);
+  if (g.act == LORA_ACT_SILU)
+    hipLaunchKernelGGL((gated_tile_kernel<C, kWide, kTerms, LORA_ACT_SILU>), grid, block, 0, s, g);
+  else if (g.act == LORA_ACT_GELU)
+    hipLaunchKernelGGL((gated_tile_kernel<C, kWide, kTerms, LORA_ACT_GELU>), grid, block, 0, s, g);
+  else
+    hipLaunchKernelGGL((gated_tile_kernel<C, kWide, kTerms, LORA_ACT_GELU_TANH>), grid, block, 0, s, g);
+}
+
+// Rows anywhere in [M][Kd]: 32-bit byte offsets reach them all, or not.
+bool wide_rows(int64_t M, int64_t Kd) { return M * Kd >= (int64_t(1) << 31); }
+
+// Both projections' terms, slot by slot; sum: into out[0].
+hipError_t launch_terms(TermsArgs a, bool sum, int dtype, int M, hipStream_t s) {
+  const int64_t windows = (int64_t(M) * a.K + 15) / 16, cols = dtype == LORA_BF16 ? 128 : 64;
+  const dim3 grid(unsigned(windows * ((a.N + cols - 1) / cols)), sum ? 1 : 2), block(64);
+  for (a.k = 0; a.k < a.K; ++a.k) {
+    if (dtype == LORA_BF16) {
+      if (sum) hipLaunchKernelGGL((terms_kernel<uint16_t, true>), grid, block, 0, s, a);
+      else hipLaunchKernelGGL((terms_kernel<uint16_t, false>), grid, block, 0, s, a);
+    } else {
+      if (sum) hipLaunchKernelGGL((terms_kernel<float, true>), grid, block, 0, s, a);
+      else hipLaunchKernelGGL((terms_kernel<float, false>), grid, block, 0, s, a);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
 
-hipError_t launch_gated_tiles(const GatedArgs &g, hipStream_t s) {
-  const int64_t big = int64_t((g.M + 255) / 256) * ((g.N + 127) / 128);
-  if (big >= 256) launch_tiles<Big>(g, s);
-  else launch_tiles<Mid>(g, s);
+hipError_t launch_gated(const GatedArgs &g, const TermsArgs &t, int dtype, hipStream_t s) {
+  if (dtype == LORA_F32) {
+    const hipError_t e = launch_terms(t, false, dtype, g.M, s);
+    if (e != hipSuccess) return e;
+    const dim3 grid(unsigned(g.N / 32), unsigned((g.M + 63) / 64)), block(256);
+    if (g.act == LORA_ACT_SILU) hipLaunchKernelGGL(gated_f32_kernel<LORA_ACT_SILU>, grid, block, 0, s, g);
+    else if (g.act == LORA_ACT_GELU) hipLaunchKernelGGL(gated_f32_kernel<LORA_ACT_GELU>, grid, block, 0, s, g);
+    else hipLaunchKernelGGL(gated_f32_kernel<LORA_ACT_GELU_TANH>, grid, block, 0, s, g);
+    return hipGetLastError();
+  }
+  if (g.term[0]) {
+    const hipError_t e = launch_terms(t, false, dtype, g.M, s);
+    if (e != hipSuccess) return e;
+    // rounds of tiles over the CUs; one of 128 rows takes 0.6 of one of 256
+    const int64_t n = (g.N + 127) / 128, big = ((g.M + 255) / 256) * n, mid = ((g.M + 127) / 128) * n;
+    if (6 * ((mid + 255) / 256) < 10 * ((big + 255) / 256)) launch_tiles<Mid, false, true>(g, s);
+    else launch_tiles<Big, false, true>(g, s);
+  } else if (wide_rows(g.M, g.Kd)) {
+    launch_tiles<Big, true, false>(g, s);
+  } else {
+    launch_tiles<Big, false, false>(g, s);
+  }
   return hipGetLastError();
 }
 
@@ -809,25 +1364,11 @@ hipError_t launch_gated_decode(const GemmConfig &c, const GemmArgs (&g)[2], hipS
   return hipGetLastError();
 }
 
-namespace {
-
-template <int kAct>
-void launch_epilogue(const GatedArgs &g, int dtype, hipStream_t s) {
-  const unsigned n_x = unsigned((g.N + 511) / 512);
-  if (dtype == LORA_BF16)
-    hipLaunchKernelGGL(gated_decode_epilogue_kernel<kAct>, dim3(n_x, unsigned(g.M)), dim3(256), 0, s, g);
-  else if (int64_t(n_x) * ((g.M + 3) / 4) < 256)      // one wave a workgroup where four leave CUs idle
-    hipLaunchKernelGGL((gated_epilogue_kernel<float, 1, kAct>), dim3(n_x, unsigned(g.M)), dim3(64), 0, s, g);
-  else
-    hipLaunchKernelGGL((gated_epilogue_kernel<float, 4, kAct>), dim3(n_x, unsigned((g.M + 3) / 4)), dim3(256), 0, s, g);
-}
-
-}  // namespace
-
-hipError_t launch_gated_epilogue(const GatedArgs &g, int dtype, hipStream_t s) {
-  if (g.act == LORA_ACT_SILU) launch_epilogue<LORA_ACT_SILU>(g, dtype, s);
-  else if (g.act == LORA_ACT_GELU) launch_epilogue<LORA_ACT_GELU>(g, dtype, s);
-  else launch_epilogue<LORA_ACT_GELU_TANH>(g, dtype, s);
+hipError_t launch_gated_decode_epilogue(const GatedArgs &g, hipStream_t s) {
+  const dim3 grid(unsigned((g.N + 511) / 512), unsigned(g.M)), block(256);
+  if (g.act == LORA_ACT_SILU) hipLaunchKernelGGL(gated_decode_epilogue_kernel<LORA_ACT_SILU>, grid, block, 0, s, g);
+  else if (g.act == LORA_ACT_GELU) hipLaunchKernelGGL(gated_decode_epilogue_kernel<LORA_ACT_GELU>, grid, block, 0, s, g);
+  else hipLaunchKernelGGL(gated_decode_epilogue_kernel<LORA_ACT_GELU_TANH>, grid, block, 0, s, g);
   return hipGetLastError();
 }
 
@@ -838,21 +1379,44 @@ hipError_t launch_gated_act_grad(const void *dH, const void *pre_gate, const voi
   return hipGetLastError();
 }
 
-bool gated_grad_x_fused(int T, int d_in, int dtype) {
-  return dtype == LORA_BF16 && T > 128 && int64_t((T + 255) / 256) * ((d_in + 255) / 256) >= 192;
+int gated_grad_x_splits(int T, int d_in, int d_out, int dtype) {
+  const int64_t kt = 2 * int64_t(d_out / 64);
+  int64_t tiles, want;
+  if (dtype == LORA_BF16) {
+    if (int64_t((T + 255) / 256) * ((d_in + 255) / 256) >= 192 || wide_rows(T, d_out)) return 0;
+    tiles = int64_t((T + 127) / 128) * ((d_in + 255) / 256);       // one on a CU
+    want = 256;
+  } else {
+    tiles = int64_t((T + 63) / 64) * (d_in / 64);                  // several on a CU
+    want = 512;
+  }
+  // at least 8 K tiles of 64 each
+  int64_t s = want / (tiles > 0 ? tiles : 1);
+  if (s > kt / 8) s = kt / 8;
+  return s < 1 ? 1 : int(s);
 }
 
-hipError_t launch_gated_grad_x_tiles(const GatedGradXArgs &g, hipStream_t s) {
-  const int tiles = ((g.M + 255) / 256) * ((g.N + 255) / 256);
-  hipLaunchKernelGGL((gated_grad_x_tile_kernel<Big>), dim3(8 * unsigned((tiles + 7) / 8)), dim3(512), 0, s, g);
-  return hipGetLastError();
-}
-
-hipError_t launch_gated_grad_x_epilogue(const GatedGradXArgs &g, int dtype, hipStream_t s) {
-  const unsigned n_x = unsigned((g.N + 511) / 512);
-  const dim3 grid(n_x, unsigned((g.M + 3) / 4));
-  if (dtype == LORA_BF16) hipLaunchKernelGGL((gated_grad_x_epilogue_kernel<uint16_t, 4>), grid, dim3(256), 0, s, g);
-  else hipLaunchKernelGGL((gated_grad_x_epilogue_kernel<float, 4>), grid, dim3(256), 0, s, g);
+hipError_t launch_gated_grad_x(const GatedGradXArgs &g, const TermsArgs &t, int dtype, hipStream_t s) {
+  if (g.splits == 0) {
+    const int tiles = ((g.M + 255) / 256) * ((g.N + 255) / 256);
+    const dim3 grid(8 * unsigned((tiles + 7) / 8)), block(Big::NT);
+    if (wide_rows(g.M, g.Kd)) hipLaunchKernelGGL((gated_grad_x_tile_kernel<Big, false, true>), grid, block, 0, s, g);
+    else hipLaunchKernelGGL((gated_grad_x_tile_kernel<Big, false, false>), grid, block, 0, s, g);
+    return hipGetLastError();
+  }
+  hipError_t e = launch_terms(t, true, dtype, g.M, s);
+  if (e != hipSuccess) return e;
+  const unsigned sums = unsigned((int64_t(g.M) * g.N / 8 + 255) / 256);
+  if (dtype == LORA_F32) {
+    hipLaunchKernelGGL(gated_grad_x_f32_kernel, dim3(unsigned(g.N / 64), unsigned((g.M + 63) / 64), unsigned(g.splits)),
+                       dim3(256), 0, s, g);
+    hipLaunchKernelGGL(gated_grad_x_sum_kernel<float>, dim3(sums), dim3(256), 0, s, g);
+    return hipGetLastError();
+  }
+  const int tiles = ((g.M + 127) / 128) * ((g.N + 255) / 256);
+  hipLaunchKernelGGL((gated_grad_x_tile_kernel<Mid, true, false>), dim3(8 * unsigned((tiles + 7) / 8), unsigned(g.splits)),
+                     dim3(Mid::NT), 0, s, g);
+  hipLaunchKernelGGL(gated_grad_x_sum_kernel<uint16_t>, dim3(sums), dim3(256), 0, s, g);
   return hipGetLastError();
 }
 

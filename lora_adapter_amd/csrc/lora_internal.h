@@ -469,17 +469,32 @@ struct GatedArgs {
   ExpandArgs ex;            // .U and .b_pages: the gate's
   const float *U_up;
   const void *b_up;
+  const int32_t *slot_pos;  // the plan's
   int act;
   void *H, *pre_gate, *pre_up;   // [M][N]; pre_* null unless training
-  // not null (decode forward): ex.U and U_up hold U per slot, with the slot
+  // decode: the partials of both products
+  const float *part[2];
+  int splits;
+  // decode forward: not null, and ex.U and U_up hold U per slot, with the slot
   // descriptors that the per-slot shrink wrote; the epilogue also stores U
   // in the plan's layout (see EpilogueArgs)
   const int4 *sdesc;
   float *u_out[2];
   int slot_stride;
-  // split forms: the partials of both products
-  const float *part[2];
-  int splits, sk_g, sk_kt, bm, bn;
+  // otherwise: where the adapters' terms go ahead of the tiles [M][N], or null
+  // (the tiles form them)
+  float *term[2];
+};
+
+// The adapters' terms of both projections (see terms_kernel).
+struct TermsArgs {
+  const int32_t *hdr, *pair_tk, *pair_adapter, *u_off, *slot_pos;   // the plan's
+  const int32_t *rank, *page_start, *page_ids;
+  const float *U[2];
+  int64_t u_cap;
+  const void *pages[2];     // [n_pages][N]
+  float *out[2];            // [M][N]
+  int N, K, k;              // k: the slot, set by the launcher
 };
 
 // The gradient of X of the gated block: dX = dg.Wg^T + du.Wu^T + mask . (both
@@ -491,10 +506,12 @@ struct GatedGradXArgs {
   ExpandArgs ex;
   const float *U_up;
   const void *b_up;
+  const int32_t *slot_pos;  // the plan's
   const uint8_t *mask;      // [M][N] or null
   void *dX;                 // [M][N]
-  const float *part[2];
-  int splits, sk_g, sk_kt, bm, bn;
+  int splits;               // 0: whole tiles
+  float *sums;              // splits > 0: [splits][M][N]
+  float *term;              // splits > 0: [M][N], the adapters' terms
 };
 
 // ----------------------------------------------------------------- launchers
@@ -595,23 +612,22 @@ hipError_t launch_clip(const ClipLayer *layers, int n_layers, ClipArgs a, void *
 size_t cross_entropy_workspace_bytes(int T, int V, int d, int dtype, bool grad);
 hipError_t launch_cross_entropy(const CrossEntropyArgs &a, int dtype, void *ws, hipStream_t s);
 
-// The gated block takes tiles with both projections inside (no partials) when
-// they fill the GPU.
-bool gated_fused(int T, int d_out, int dtype);
-// Decode: both products' partials, the per-slot shrinks and the plan.
+// More than decode: tiles of both projections, behind a launch of the adapters'
+// terms where a.term is given (float32 needs it).
+hipError_t launch_gated(const GatedArgs &a, const TermsArgs &t, int dtype, hipStream_t s);
+// Decode: both products' partials, the per-slot shrinks and the plan; or, with
+// a plan, both products' partials.  Then both sums, both expands, activation and
+// product.
 hipError_t launch_gated_decode_plan(const GemmConfig &c, const GemmArgs (&g)[2], const SlotShrinkArgs (&ss)[2],
                                     const PlanLaunch &pl, hipStream_t s);
-// Decode with a plan: both products' partials.
 hipError_t launch_gated_decode(const GemmConfig &c, const GemmArgs (&g)[2], hipStream_t s);
-hipError_t launch_gated_tiles(const GatedArgs &a, hipStream_t s);
-// The split forms' second launch: both sums, both expands, activation, product.
-hipError_t launch_gated_epilogue(const GatedArgs &a, int dtype, hipStream_t s);
+hipError_t launch_gated_decode_epilogue(const GatedArgs &a, hipStream_t s);
 // d_gate and d_up [n] from dH and the stored results of both projections.
 hipError_t launch_gated_act_grad(const void *dH, const void *pre_gate, const void *pre_up, int act,
                                  void *d_gate, void *d_up, int64_t n, int dtype, hipStream_t s);
-bool gated_grad_x_fused(int T, int d_in, int dtype);
-hipError_t launch_gated_grad_x_tiles(const GatedGradXArgs &a, hipStream_t s);
-hipError_t launch_gated_grad_x_epilogue(const GatedGradXArgs &a, int dtype, hipStream_t s);
+// K splits of the dX product, 0 for whole tiles.
+int gated_grad_x_splits(int T, int d_in, int d_out, int dtype);
+hipError_t launch_gated_grad_x(const GatedGradXArgs &a, const TermsArgs &t, int dtype, hipStream_t s);
 
 hipError_t launch_merge(const MergeArgs &a, int dtype, hipStream_t s);
 // n layers' merges (same list, each layer's own W and pool): one launch per

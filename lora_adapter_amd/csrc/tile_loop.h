@@ -19,27 +19,49 @@ namespace {
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef short v4i16_t __attribute__((ext_vector_type(4)));
 
-// A tile of BM x BN over WM x WN waves, in blocks of 16 x 16.
-template <int BM_, int BN_, int WM_, int WN_>
+// A tile of BM x BN over WM x WN waves, in blocks of 16 x 16, with NS LDS stages.
+template <int BM_, int BN_, int WM_, int WN_, int NS_ = 2>
 struct LoopCfg {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;
   static constexpr int NW = WM * WN, NT = NW * 64;
   static constexpr int ROWB = 128;                     // bytes per row of 64 of K
   static constexpr int STAGE = (BM + BN) * ROWB;       // bytes per LDS stage
   static constexpr int TM = BM / (WM * 16), TN = BN / (WN * 16);
   static constexpr int A_INS = BM / 8 / NW, B_INS = BN / 8 / NW, LPW = A_INS + B_INS;
+  static constexpr int LDS = NS * STAGE;
   static_assert(A_INS * 8 * NW == BM && B_INS * 8 * NW == BN, "tile rows / waves");
+  static_assert(NS >= 2 && (NS - 1) * LPW < 64, "stages, and the copies that may be in flight");
 };
 
 // One 16-byte copy per lane from base + off to LDS at lds + 16 lane; base and
-// lds are the wave's.  (The s_nop: an LDS DMA needs a wait state after the
-// scalar write of m0.)
-__device__ __forceinline__ void lds_dma16_s(const void *base, uint32_t off, uint32_t lds) {
+// lds are the wave's.  (The s_nop: an LDS DMA needs a wait state after the scalar
+// write of m0.  The readfirstlanes: a uniform value may have come out of vector
+// arithmetic, where the compiler leaves it; of a scalar one they are nothing.)
+__device__ __forceinline__ void lds_dma16_s(const void *ptr, uint32_t off, uint32_t lds) {
+  const uint64_t p = reinterpret_cast<uint64_t>(ptr);
+  const uint64_t base = uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(p)))) |
+                        uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(p >> 32)))) << 32;
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                :
                : "v"(off), "s"(base), "s"(lds)
                : "memory", "m0");
 }
+
+// Where a lane's pieces of n copies' rows lie, from a base that moves along K:
+// 32-bit byte offsets, or (kWide) 64 bits where the rows pass 2^32 bytes.
+template <int n, bool kWide>
+struct RowOffsets {
+  uint32_t o[kWide ? 1 : n];
+  int64_t w[kWide ? n : 1];
+  __device__ __forceinline__ void set(int i, int64_t elements) {
+    if constexpr (kWide) w[i] = elements;
+    else o[i] = uint32_t(elements) * 2;
+  }
+  __device__ __forceinline__ void copy(const uint16_t *base, int i, uint32_t lds) const {
+    if constexpr (kWide) lds_dma16(base + w[i], lds);
+    else lds_dma16_s(base, o[i], lds);
+  }
+};
 
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6); }
 
@@ -57,18 +79,17 @@ __device__ __forceinline__ bf16x8_t frag_rows(const char *base, int s, int row0)
 // `frag(base, s, q)` reads fragment q (A blocks 0 .. TM-1, then B blocks) of K
 // step s from the stage at base.
 // The fragments of a step are read from LDS while the MFMAs of the step before
-// run (two register sets).  Between the two steps of a K tile one barrier frees
-// the stage just read (the copies of the tile after next go into it, spread
-// over the second step's MFMAs) and publishes the next tile.  The instructions
-// of a step are pinned in this order; every other row of blocks runs backwards,
-// so that one operand of an MFMA is always the last one's.  On return no copy
-// is in flight and every wave is done with the stages.
+// run (two register sets).  K tile kt lies in stage kt % NS.  Between the two
+// steps of a K tile one barrier frees the stage just read (the copies of tile
+// kt + NS go into it, spread over the second step's MFMAs) and publishes the
+// next tile.  The instructions of a step are pinned in this order; every other
+// row of blocks runs backwards, so that one operand of an MFMA is always the
+// last one's.  On return no copy is in flight and every wave is done with the
+// stages.
 template <typename C, typename Src>
 __device__ __forceinline__ void tile_loop(const Src &p, char *smem, int nk, f32x4_t (&acc)[C::TM][C::TN]) {
-  constexpr int TM = C::TM, TN = C::TN, NM = TM * TN, NQ = TM + TN, LPW = C::LPW;
-  char *const st0 = smem;
-  char *const st1 = smem + C::STAGE;
-  const uint32_t l0 = __builtin_amdgcn_readfirstlane(lds_addr(smem)), l1 = l0 + C::STAGE;
+  constexpr int TM = C::TM, TN = C::TN, NM = TM * TN, NQ = TM + TN, LPW = C::LPW, NS = C::NS;
+  const uint32_t l0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -100,30 +121,33 @@ __device__ __forceinline__ void tile_loop(const Src &p, char *smem, int nk, f32x
     }
   };
 #pragma unroll
-  for (int c = 0; c < LPW; ++c) p.copy(l0, 0, c);
+  for (int t = 0; t < NS; ++t)
 #pragma unroll
-  for (int c = 0; c < LPW; ++c) p.copy(l1, min(1, nk - 1), c);
-  wait_vmcnt<LPW>();
+    for (int c = 0; c < LPW; ++c) p.copy(l0 + t * C::STAGE, min(t, nk - 1), c);
+  wait_vmcnt<(NS - 1) * LPW>();
   lds_bar();
 #pragma unroll
   for (int q = 0; q < NQ; ++q) {
-    if (q < TM) fa0[q] = p.frag(st0, 0, q);
-    else fb0[q - TM] = p.frag(st0, 0, q);
+    if (q < TM) fa0[q] = p.frag(smem, 0, q);
+    else fb0[q - TM] = p.frag(smem, 0, q);
   }
-  // past the end the body stays the same: the copy repeats the last tile into
-  // a stage that no one reads again, and the reads of the next stage go unused
-  auto tile = [&](int kt, const char *cur, const char *nxt, uint32_t dst) __attribute__((always_inline)) {
-    step(std::integral_constant<int, 0>{}, fa0, fb0, fa1, fb1, cur, 1, dst, 0);
-    wait_vmcnt<0>();   // tile kt + 1, the only copies in flight, has landed
-    lds_bar();         // for every wave, and every wave has read cur
-    step(std::integral_constant<int, 1>{}, fa1, fb1, fa0, fb0, nxt, 0, dst, min(kt + 2, nk - 1));
+  // past the end the body stays the same: the copies repeat the last tile into
+  // stages that no one reads again, and the reads of the next stage go unused
+  auto tile = [&](int kt, int cur, int nxt) __attribute__((always_inline)) {
+    step(std::integral_constant<int, 0>{}, fa0, fb0, fa1, fb1, smem + cur * C::STAGE, 1, 0, 0);
+    wait_vmcnt<(NS - 2) * LPW>();   // tile kt + 1 has landed
+    lds_bar();                      // for every wave, and every wave has read tile kt
+    step(std::integral_constant<int, 1>{}, fa1, fb1, fa0, fb0, smem + nxt * C::STAGE, 0, l0 + cur * C::STAGE,
+         min(kt + NS, nk - 1));
   };
   int kt = 0;
-  for (; kt + 1 < nk; kt += 2) {
-    tile(kt, st0, st1, l0);
-    tile(kt + 1, st1, st0, l1);
+  for (; kt + NS <= nk; kt += NS) {
+#pragma unroll
+    for (int u = 0; u < NS; ++u) tile(kt + u, u, (u + 1) % NS);
   }
-  if (kt < nk) tile(kt, st0, st1, l0);
+#pragma unroll
+  for (int u = 0; u < NS - 1; ++u)
+    if (kt + u < nk) tile(kt + u, u, u + 1);
   wait_vmcnt<0>();
   lds_bar();
 }
