@@ -242,8 +242,8 @@ __device__ __forceinline__ unsigned add_segs(const Terms &e, const TileSegs<C> &
       __builtin_memcpy(&b[f], &lo, 8);
       __builtin_memcpy(reinterpret_cast<char *>(&b[f]) + 8, &hi, 8);
     }
-    // U of two blocks in flight (registers)
-    constexpr int UB = 2;
+    // U of two blocks in flight (one where both projections' fragments take the registers)
+    constexpr int UB = kPair ? 2 : 1;
 #pragma unroll
     for (int i0 = 0; i0 < NB; i0 += UB) {
       if (!((blocks >> i0) & ((1 << UB) - 1))) continue;
