@@ -443,6 +443,7 @@ struct ClipArgs {
   float *norm;              // [M + 1]
   // set by the launcher
   int factors, first;       // 2 n_layers, and 2 x the launch's first layer
+  int64_t parts;            // factors x rows: partials of an entry
   double *square;           // [M]
   double *part;             // [M][factors][rows]
   ClipLayer layer[kClipLayers];
