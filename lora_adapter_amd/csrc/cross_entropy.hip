@@ -34,7 +34,7 @@ constexpr float kMaxExp = 64.f;                        // a piece's exponents ov
 struct CeWs {
   int32_t *count;      // [1] tokens with a target
   int32_t *rows;       // [T] those tokens, ascending
-  double *ly;          // [T] their target's logit in base 2
+  double *ly;          // [T] the tokens' target's logit in base 2
   float2 *coef;        // [T] (w scale / Z, -w scale S / Z)
   float2 *part;        // [block][pieces] (sum, shift)
   void *e;             // [block][lde]
@@ -59,52 +59,47 @@ __device__ __forceinline__ float ref_of(double ly) {
 }
 
 // ------------------------------------------------------------ rows
-// One workgroup: the list of tokens that have a target and a weight.
-__global__ __launch_bounds__(1024) void ce_rows_kernel(CeArgs c) {
-  __shared__ int sums[16];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int per = (c.a.T + 1023) / 1024, t0 = min(tid * per, c.a.T), t1 = min(t0 + per, c.a.T);
-  int n = 0;
-  for (int t = t0; t < t1; ++t) {
-    const int y = c.a.targets[t];
-    const bool zero = c.a.weights && c.a.weights[t] == 0.f;
-    if (y >= 0 && y < c.a.V && !zero) ++n;
-    else c.a.loss[t] = y >= c.a.V ? __builtin_nanf("") : 0.f;
-  }
-  int incl = n;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int v = __shfl_up(incl, o, 64);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 63) sums[wave] = incl;
-  __syncthreads();
-  int at = incl - n;
-  for (int w = 0; w < wave; ++w) at += sums[w];
-  for (int t = t0; t < t1; ++t) {
-    const int y = c.a.targets[t];
-    const bool zero = c.a.weights && c.a.weights[t] == 0.f;
-    if (y >= 0 && y < c.a.V && !zero) c.w.rows[at++] = t;
-  }
-  if (tid == 1023) c.w.count[0] = at;
+__device__ __forceinline__ bool ce_listed(const CeArgs &c, int t) {
+  const int y = c.a.targets[t];
+  return y >= 0 && y < c.a.V && !(c.a.weights && c.a.weights[t] == 0.f);
 }
 
-// One wave per row: the target's logit of list entry r (float64 sums: both
-// results hang on it), and the zero gradient of a token r that is not listed.
+// Workgroup 0: the list of tokens that have a target and a weight.  Beside it,
+// one wave per token: the target's logit of a listed one (float64 sums: both
+// results hang on it), the zero loss and gradient of another.  (As launches one
+// after the other 48 us at 8192 tokens, as one 29.)
 template <typename E>
-__global__ __launch_bounds__(256) void ce_target_kernel(CeArgs c) {
-  const int r = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (r >= c.a.T) return;
-  const int d = c.a.d;
-  if (c.a.dX) {
-    const int y = c.a.targets[r];
-    if (y < 0 || y >= c.a.V || (c.a.weights && c.a.weights[r] == 0.f)) {
-      const float z[8] = {};
-      for (int i = lane * 8; i < d; i += 512) Cols<E, 8>::store(static_cast<E *>(c.a.dX) + int64_t(r) * d + i, z);
+__global__ __launch_bounds__(1024) void ce_rows_kernel(CeArgs c) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, T = c.a.T;
+  if (blockIdx.x == 0) {
+    __shared__ int sums[16];
+    const int per = (T + 1023) / 1024, t0 = min(tid * per, T), t1 = min(t0 + per, T);
+    int n = 0;
+    for (int t = t0; t < t1; ++t) n += ce_listed(c, t) ? 1 : 0;
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(incl, o, 64);
+      if (lane >= o) incl += v;
     }
+    if (lane == 63) sums[wave] = incl;
+    __syncthreads();
+    int at = incl - n;
+    for (int w = 0; w < wave; ++w) at += sums[w];
+    for (int t = t0; t < t1; ++t)
+      if (ce_listed(c, t)) c.w.rows[at++] = t;
+    if (tid == 1023) c.w.count[0] = at;
+    return;
   }
-  if (r >= c.w.count[0]) return;
-  const int t = c.w.rows[r];
+  const int t = (int(blockIdx.x) - 1) * 16 + wave, d = c.a.d;
+  if (t >= T) return;
+  if (!ce_listed(c, t)) {
+    if (lane == 0) c.a.loss[t] = c.a.targets[t] >= c.a.V ? __builtin_nanf("") : 0.f;
+    const float z[8] = {};
+    for (int i = lane * 8; c.a.dX && i < d; i += 512)
+      Cols<E, 8>::store(static_cast<E *>(c.a.dX) + int64_t(t) * d + i, z);
+    return;
+  }
   const E *x = static_cast<const E *>(c.a.X) + int64_t(t) * d;
   const E *w = static_cast<const E *>(c.a.W) + int64_t(c.a.targets[t]) * d;
   double sum = 0.0;
@@ -117,7 +112,7 @@ __global__ __launch_bounds__(256) void ce_target_kernel(CeArgs c) {
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
-  if (lane == 0) c.w.ly[r] = sum * double(c.a.logit_scale) * 1.4426950408889634074;
+  if (lane == 0) c.w.ly[t] = sum * double(c.a.logit_scale) * 1.4426950408889634074;
 }
 
 // ------------------------------------------------------------ first product
@@ -212,9 +207,9 @@ __global__ __launch_bounds__(C::NT, 1) void ce_logits_kernel(CeArgs c) {
   float ref = 0.f;
   int y = -1;
   if (int(threadIdx.x) < C::BM) {
-    const int r = c.row0 + min(m0 + int(threadIdx.x), M - 1);
-    ref = ref_of(c.w.ly[r]);
-    y = c.a.targets[c.w.rows[r]];
+    const int t = c.w.rows[c.row0 + min(m0 + int(threadIdx.x), M - 1)];
+    ref = ref_of(c.w.ly[t]);
+    y = c.a.targets[t];
   }
   f32x4_t acc[C::TM][C::TN];
   tile_loop<C>(src, smem, d / 64, acc);
@@ -248,14 +243,14 @@ __global__ __launch_bounds__(C::NT, 1) void ce_logits_kernel(CeArgs c) {
 
 // ------------------------------------------------------------ float32
 __global__ __launch_bounds__(256) void ce_logits_f32_kernel(CeArgs c) {
-  __shared__ F32Tile t;
+  __shared__ F32Tile lds;
   __shared__ __attribute__((aligned(16))) float stage[64][64 + 4];
   const int M = block_rows(c), d = c.a.d;
   const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
   if (m0 >= M) return;
   const float *X = static_cast<const float *>(c.a.X), *W = static_cast<const float *>(c.a.W);
   const f32x16_t acc = tile_f32<false>(
-      t, 0, d,
+      lds, 0, d,
       [&](int r, int k) {
         return *reinterpret_cast<const float4 *>(X + int64_t(c.w.rows[c.row0 + min(m0 + r, M - 1)]) * d + k);
       },
@@ -268,10 +263,10 @@ __global__ __launch_bounds__(256) void ce_logits_f32_kernel(CeArgs c) {
   for (int q = 0; q < 2; ++q) {
     const int rr = q * 32 + (threadIdx.x >> 3), lr = m0 + rr;
     const bool ok = lr < M;
-    const int r = c.row0 + (ok ? lr : M - 1);
+    const int t = c.w.rows[c.row0 + (ok ? lr : M - 1)];
     float x[8];
     Elem<float>::load8(&stage[rr][(lane & 7) * 8], x);
-    ce_store8<float>(c, x, lr, ok, n0 + (lane & 7) * 8, ref_of(c.w.ly[r]), c.a.targets[c.w.rows[r]]);
+    ce_store8<float>(c, x, lr, ok, n0 + (lane & 7) * 8, ref_of(c.w.ly[t]), c.a.targets[t]);
   }
 }
 
@@ -317,7 +312,7 @@ __global__ __launch_bounds__(256) void ce_row_kernel(CeArgs c) {
   if (tid != 0) return;
   const int r = c.row0 + lr, t = c.w.rows[r];
   const float w = c.a.weights ? c.a.weights[t] : 1.f;
-  const double ly = c.w.ly[r], up = double(ref_of(ly)) + double(R) - ly;   // ref + R - L_y
+  const double ly = c.w.ly[t], up = double(ref_of(ly)) + double(R) - ly;   // ref + R - L_y
   const double ey = exp2(-up);                    // the target's e on the row's shift
   double loss, z = double(S) + ey;
   if (!(S < INFINITY) || !(ly < double(INFINITY))) loss = z = __builtin_nan("");
@@ -425,7 +420,7 @@ __global__ __launch_bounds__(C::NT, 1) void ce_grad_kernel(CeArgs c) {
 }
 
 __global__ __launch_bounds__(256) void ce_grad_f32_kernel(CeArgs c) {
-  __shared__ F32Tile t;
+  __shared__ F32Tile lds;
   const int M = block_rows(c), d = c.a.d;
   const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
   if (m0 >= M) return;
@@ -433,7 +428,7 @@ __global__ __launch_bounds__(256) void ce_grad_f32_kernel(CeArgs c) {
   int k0, nk;
   split_range(int(c.w.lde / 64), c.w.splits, blockIdx.z, k0, nk);
   const f32x16_t acc = tile_f32<true>(
-      t, k0, k0 + nk * 64,
+      lds, k0, k0 + nk * 64,
       [&](int r, int k) { return *reinterpret_cast<const float4 *>(e + int64_t(min(m0 + r, M - 1)) * c.w.lde + k); },
       [&](int n, int k) { return *reinterpret_cast<const float4 *>(W + int64_t(min(k, c.a.V - 1)) * d + n0 + n); });
   float *out = c.w.acc + int64_t(blockIdx.z) * c.w.block * d;
@@ -510,8 +505,7 @@ template <typename E>
 hipError_t run(CeArgs c, hipStream_t s) {
   constexpr bool bf = sizeof(E) == 2;
   const int T = c.a.T, V = c.a.V, d = c.a.d;
-  hipLaunchKernelGGL(ce_rows_kernel, dim3(1), dim3(1024), 0, s, c);
-  hipLaunchKernelGGL(ce_target_kernel<E>, dim3(unsigned((T + 3) / 4)), dim3(256), 0, s, c);
+  hipLaunchKernelGGL(ce_rows_kernel<E>, dim3(unsigned(1 + (T + 15) / 16)), dim3(1024), 0, s, c);
   for (int r0 = 0; r0 < T; r0 += c.w.block) {
     c.row0 = r0;
     const int rows = T - r0 < c.w.block ? T - r0 : c.w.block;

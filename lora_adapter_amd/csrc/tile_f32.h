@@ -14,53 +14,62 @@ struct F32Tile {
 
 // A 32 x 32 block of the tile for each of four waves: rows 32 (wave / 2), columns
 // 32 (wave % 2), as the MFMA's registers hold them.  K in chunks of 32 through
-// LDS, the next chunk's loads in flight while one feeds the MFMAs, one barrier a
-// chunk.  a(r, k) and b(r, k) give 4 values along k; with kBAcross b(c, k) gives
-// row k's columns c .. c + 3.  k_end - k_begin is a multiple of 32.
+// LDS, one barrier a chunk, the loads two chunks ahead: with few workgroups on a
+// CU one chunk's 0.4 us of MFMAs does not cover a load.  a(r, k) and b(r, k) give
+// 4 values along k; with kBAcross b(c, k) gives row k's columns c .. c + 3.
+// k_end - k_begin is a multiple of 32.
 template <bool kBAcross, typename FA, typename FB>
 __device__ __forceinline__ f32x16_t tile_f32(F32Tile &t, int k_begin, int k_end, const FA &fa, const FB &fb) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   f32x16_t acc = {};
-  float4 va[2], vb[2];
-  auto load = [&](int k0) __attribute__((always_inline)) {
+  if (k_begin >= k_end) return acc;
+  const int last = k_end - kF32K;
+  float4 va[2][2], vb[2][2];
+  // of a chunk past the end: the last one, which no one reads
+  auto load = [&](int b, int k) __attribute__((always_inline)) {
+    const int k0 = min(k, last);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int at = (tid + i * 256) * 4;
-      va[i] = fa(at / kF32K, k0 + at % kF32K);
-      if constexpr (kBAcross) vb[i] = fb(at % 64, k0 + at / 64);
-      else vb[i] = fb(at / kF32K, k0 + at % kF32K);
+      va[b][i] = fa(at / kF32K, k0 + at % kF32K);
+      if constexpr (kBAcross) vb[b][i] = fb(at % 64, k0 + at / 64);
+      else vb[b][i] = fb(at / kF32K, k0 + at % kF32K);
     }
   };
-  auto put = [&](int s) __attribute__((always_inline)) {
+  auto put = [&](int b, int s) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int at = (tid + i * 256) * 4;
       float *p = &t.a[s][at / kF32K][at % kF32K];
-      p[0] = va[i].x; p[1] = va[i].y; p[2] = va[i].z; p[3] = va[i].w;
+      p[0] = va[b][i].x; p[1] = va[b][i].y; p[2] = va[b][i].z; p[3] = va[b][i].w;
       if constexpr (kBAcross) {
         const int c = at % 64, k = at / 64;
-        t.b[s][c][k] = vb[i].x; t.b[s][c + 1][k] = vb[i].y; t.b[s][c + 2][k] = vb[i].z; t.b[s][c + 3][k] = vb[i].w;
+        t.b[s][c][k] = vb[b][i].x; t.b[s][c + 1][k] = vb[b][i].y;
+        t.b[s][c + 2][k] = vb[b][i].z; t.b[s][c + 3][k] = vb[b][i].w;
       } else {
         float *q = &t.b[s][at / kF32K][at % kF32K];
-        q[0] = vb[i].x; q[1] = vb[i].y; q[2] = vb[i].z; q[3] = vb[i].w;
+        q[0] = vb[b][i].x; q[1] = vb[b][i].y; q[2] = vb[b][i].z; q[3] = vb[b][i].w;
       }
     }
   };
   const int ra = (wave >> 1) * 32 + (lane & 31), rb = (wave & 1) * 32 + (lane & 31), kh = lane >> 5;
-  if (k_begin < k_end) {
-    load(k_begin);
-    put(0);
-  }
+  load(0, k_begin);
+  load(1, k_begin + kF32K);
+  put(0, 0);
+  load(0, k_begin + 2 * kF32K);
   __syncthreads();
-  int s = 0;
-  for (int k0 = k_begin; k0 < k_end; k0 += kF32K, s ^= 1) {
-    const bool more = k0 + kF32K < k_end;
-    if (more) load(k0 + kF32K);
+  for (int k0 = k_begin; k0 < k_end; k0 += 2 * kF32K) {
 #pragma unroll
-    for (int k = 0; k < kF32K; k += 2)
-      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(t.a[s][ra][k + kh], t.b[s][rb][k + kh], acc, 0, 0, 0);
-    if (more) put(s ^ 1);
-    __syncthreads();
+    for (int s = 0; s < 2; ++s) {
+      const int kc = k0 + s * kF32K;
+      if (kc >= k_end) break;
+#pragma unroll
+      for (int k = 0; k < kF32K; k += 2)
+        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(t.a[s][ra][k + kh], t.b[s][rb][k + kh], acc, 0, 0, 0);
+      put(s ^ 1, s ^ 1);
+      load(s ^ 1, kc + 3 * kF32K);
+      __syncthreads();
+    }
   }
   return acc;
 }
