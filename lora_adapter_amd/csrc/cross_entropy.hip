@@ -40,6 +40,7 @@ struct CeWs {
   void *e;             // [block][lde]
   float *acc;          // [splits][block][d]
   int block, pieces, splits;
+  int shape;           // of the second product's tiles (bf16)
   int64_t lde;
   size_t bytes;
 };
@@ -177,8 +178,8 @@ template <typename C, bool kWide>
 __global__ __launch_bounds__(C::NT, 1) void ce_logits_kernel(CeArgs c) {
   constexpr int WC = C::TN * 16, SC = WC + 4;
   static_assert(WC == kSub, "one piece per wave");
-  static_assert(C::NW * 32 * SC * 4 <= 2 * C::STAGE, "staging must fit in LDS");
-  __shared__ __attribute__((aligned(16))) char smem[2 * C::STAGE];
+  static_assert(C::NW * 32 * SC * 4 <= C::LDS && C::TM % 2 == 0, "staging must fit in LDS");
+  __shared__ __attribute__((aligned(16))) char smem[C::LDS];
   const int M = block_rows(c);
   int tm, tn;
   if (M <= 0 || !tile_of_workgroup(blockIdx.x, (M + C::BM - 1) / C::BM, (c.a.V + C::BN - 1) / C::BN, tm, tn)) return;
@@ -377,14 +378,15 @@ __device__ __forceinline__ void split_range(int kt, int splits, int z, int &k0, 
 
 template <typename C>
 __global__ __launch_bounds__(C::NT, 1) void ce_grad_kernel(CeArgs c) {
-  __shared__ __attribute__((aligned(16))) char smem[2 * C::STAGE];
+  __shared__ __attribute__((aligned(16))) char smem[C::LDS];
   const int M = block_rows(c), d = c.a.d;
-  int tm, tn;
-  if (M <= 0 || !tile_of_workgroup(blockIdx.x, (M + C::BM - 1) / C::BM, (d + C::BN - 1) / C::BN, tm, tn)) return;
+  int tm, tn, z;
+  if (M <= 0 || !tile_of_workgroup(blockIdx.x, (M + C::BM - 1) / C::BM, (d + C::BN - 1) / C::BN, c.w.splits, tm, tn, z))
+    return;
   const int m0 = tm * C::BM, n0 = tn * C::BN;
   const int lane = threadIdx.x & 63, wave = wave_id();
   int k0, nk;
-  split_range(int(c.w.lde / 64), c.w.splits, blockIdx.y, k0, nk);
+  split_range(int(c.w.lde / 64), c.w.splits, z, k0, nk);
   ExpSrc<C> src;
   src.wave = wave; src.wm = wave / C::WN; src.wn = wave % C::WN;
   src.last = c.a.V - 1 - k0;
@@ -404,7 +406,7 @@ __global__ __launch_bounds__(C::NT, 1) void ce_grad_kernel(CeArgs c) {
   }
   f32x4_t acc[C::TM][C::TN];
   tile_loop<C>(src, smem, nk, acc);
-  float *out = c.w.acc + int64_t(blockIdx.y) * c.w.block * d;
+  float *out = c.w.acc + int64_t(z) * c.w.block * d;
 #pragma unroll
   for (int i = 0; i < C::TM; ++i)
 #pragma unroll
@@ -439,28 +441,36 @@ __global__ __launch_bounds__(256) void ce_grad_f32_kernel(CeArgs c) {
   }
 }
 
-// dX of one row: the splits' sums in order, the target's term, one rounding.
+// dX of one row's 2048 columns from blockIdx.y: the splits' sums in order, the
+// target's term, one rounding.
 template <typename E>
 __global__ __launch_bounds__(256) void ce_finish_kernel(CeArgs c) {
-  const int lr = blockIdx.x;
-  if (lr >= block_rows(c)) return;
-  const int d = c.a.d, r = c.row0 + lr, t = c.w.rows[r];
+  const int lr = blockIdx.x, d = c.a.d, i = (int(blockIdx.y) * 256 + int(threadIdx.x)) * 8;
+  if (lr >= block_rows(c) || i >= d) return;
+  const int r = c.row0 + lr, t = c.w.rows[r];
   const float2 k = c.w.coef[r];
-  const E *wy = static_cast<const E *>(c.a.W) + int64_t(c.a.targets[t]) * d;
-  for (int i = threadIdx.x * 8; i < d; i += 256 * 8) {
-    float v[8], w[8];
-    Elem<E>::load8(wy + i, w);
-    Elem<float>::load8(c.w.acc + int64_t(lr) * d + i, v);
-    for (int z = 1; z < c.w.splits; ++z) {
-      float o[8];
-      Elem<float>::load8(c.w.acc + (int64_t(z) * c.w.block + lr) * d + i, o);
+  const int64_t pitch = int64_t(c.w.block) * d;
+  const float *src = c.w.acc + int64_t(lr) * d + i;
+  float v[8], w[8];
+  Elem<float>::load8(src, v);
+  Elem<E>::load8(static_cast<const E *>(c.a.W) + int64_t(c.a.targets[t]) * d + i, w);
+  for (int z0 = 1; z0 < c.w.splits; z0 += 4) {
+    Raw8<float> pr[4];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] += o[q];
+    for (int z = 0; z < 4; ++z) pr[z].load(src + min(z0 + z, c.w.splits - 1) * pitch);
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+      if (z0 + z < c.w.splits) {
+        float o[8];
+        pr[z].to8(o);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] += o[q];
+      }
     }
-#pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] = fmaf(k.x, v[q], k.y * w[q]);
-    Cols<E, 8>::store(static_cast<E *>(c.a.dX) + int64_t(t) * d + i, v);
   }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) v[q] = fmaf(k.x, v[q], k.y * w[q]);
+  Cols<E, 8>::store(static_cast<E *>(c.a.dX) + int64_t(t) * d + i, v);
 }
 
 size_t up(size_t x) { return (x + 255) & ~size_t(255); }
@@ -486,12 +496,30 @@ CeWs ce_layout(char *ws, int T, int V, int d, int dtype, bool grad) {
   w.coef = reinterpret_cast<float2 *>(take(size_t(T) * 8));
   w.part = reinterpret_cast<float2 *>(take(size_t(w.block) * size_t(w.pieces) * 8));
   if (grad) {
-    const int bn = dtype == LORA_BF16 ? 256 : 64;
-    const int64_t tiles = ((w.block + tile - 1) / tile) * int64_t((d + bn - 1) / bn), kt = w.lde / 64;
-    const int64_t fill = dtype == LORA_BF16 ? 256 : 512;
-    int64_t s = fill / (tiles > 0 ? tiles : 1);
-    if (s > kt / 8) s = kt / 8;
-    w.splits = s < 1 ? 1 : int(s);
+    const int64_t kt = w.lde / 64;
+    auto split = [&](int64_t tiles, int64_t fill) {
+      int64_t n = fill / (tiles > 0 ? tiles : 1);
+      if (n > kt / 8) n = kt / 8;
+      return int(n < 1 ? 1 : n);
+    };
+    if (dtype == LORA_BF16) {
+      // the K tiles of a workgroup's share, and what its sums cost at 4 TB/s
+      // written and read once more
+      double least = 0.0;
+      for (int i = kBig; i <= kMid; ++i) {
+        const int64_t tiles = tile_count(i, w.block, d);
+        const int n = split(tiles, 256);
+        const double rounds = double((tiles * n + 255) / 256) * double((kt + n - 1) / n);
+        const double us = 0.17 * kTileShapes[i].cost * rounds + 2.0 * n * double(w.block) * d * 4.0 / 4e6;
+        if (i == kBig || us < least) {
+          least = us;
+          w.shape = i;
+          w.splits = n;
+        }
+      }
+    } else {
+      w.splits = split(int64_t((w.block + 63) / 64) * (d / 64), 512);
+    }
     w.e = take(size_t(w.block) * size_t(w.lde) * e);
     w.acc = reinterpret_cast<float *>(take(size_t(w.splits) * size_t(w.block) * size_t(d) * 4));
   }
@@ -499,7 +527,21 @@ CeWs ce_layout(char *ws, int T, int V, int d, int dtype, bool grad) {
   return w;
 }
 
-using Big = LoopCfg<256, 256, 2, 4>;
+template <typename C>
+void launch_logits(const CeArgs &c, int rows, hipStream_t s) {
+  const int tiles = ((rows + C::BM - 1) / C::BM) * ((c.a.V + C::BN - 1) / C::BN);
+  const dim3 grid(8 * unsigned((tiles + 7) / 8));
+  if (int64_t(c.a.T) * c.a.d < (int64_t(1) << 31))
+    hipLaunchKernelGGL((ce_logits_kernel<C, false>), grid, dim3(C::NT), 0, s, c);
+  else
+    hipLaunchKernelGGL((ce_logits_kernel<C, true>), grid, dim3(C::NT), 0, s, c);
+}
+
+template <typename C>
+void launch_grad(const CeArgs &c, int rows, hipStream_t s) {
+  const int tiles = ((rows + C::BM - 1) / C::BM) * ((c.a.d + C::BN - 1) / C::BN);
+  hipLaunchKernelGGL((ce_grad_kernel<C>), dim3(8 * unsigned((tiles * c.w.splits + 7) / 8)), dim3(C::NT), 0, s, c);
+}
 
 template <typename E>
 hipError_t run(CeArgs c, hipStream_t s) {
@@ -510,12 +552,12 @@ hipError_t run(CeArgs c, hipStream_t s) {
     c.row0 = r0;
     const int rows = T - r0 < c.w.block ? T - r0 : c.w.block;
     if (bf) {
-      const int tiles = ((rows + 255) / 256) * ((V + 255) / 256);
-      const dim3 grid(8 * unsigned((tiles + 7) / 8));
-      if (int64_t(T) * d < (int64_t(1) << 31))
-        hipLaunchKernelGGL((ce_logits_kernel<Big, false>), grid, dim3(Big::NT), 0, s, c);
-      else
-        hipLaunchKernelGGL((ce_logits_kernel<Big, true>), grid, dim3(Big::NT), 0, s, c);
+      switch (pick_shape(rows, V)) {
+        case kBig: launch_logits<Big>(c, rows, s); break;
+        case kTall: launch_logits<Tall>(c, rows, s); break;
+        case kMid: launch_logits<Mid>(c, rows, s); break;
+        default: launch_logits<Small>(c, rows, s);
+      }
     } else {
       hipLaunchKernelGGL(ce_logits_f32_kernel, dim3(unsigned((V + 63) / 64), unsigned((rows + 63) / 64)), dim3(256), 0,
                          s, c);
@@ -523,14 +565,16 @@ hipError_t run(CeArgs c, hipStream_t s) {
     hipLaunchKernelGGL(ce_row_kernel<E>, dim3(unsigned(rows)), dim3(256), 0, s, c);
     if (c.a.dX) {
       if (bf) {
-        const int tiles = ((rows + 255) / 256) * ((d + 255) / 256);
-        hipLaunchKernelGGL((ce_grad_kernel<Big>), dim3(8 * unsigned((tiles + 7) / 8), unsigned(c.w.splits)),
-                           dim3(Big::NT), 0, s, c);
+        switch (c.w.shape) {
+          case kBig: launch_grad<Big>(c, rows, s); break;
+          case kTall: launch_grad<Tall>(c, rows, s); break;
+          default: launch_grad<Mid>(c, rows, s);
+        }
       } else {
         hipLaunchKernelGGL(ce_grad_f32_kernel, dim3(unsigned(d / 64), unsigned((rows + 63) / 64), unsigned(c.w.splits)),
                            dim3(256), 0, s, c);
       }
-      hipLaunchKernelGGL(ce_finish_kernel<E>, dim3(unsigned(rows)), dim3(256), 0, s, c);
+      hipLaunchKernelGGL(ce_finish_kernel<E>, dim3(unsigned(rows), unsigned((d + 2047) / 2048)), dim3(256), 0, s, c);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -1083,14 +1083,16 @@ __global__ __launch_bounds__(C::NT, 1) void gated_grad_x_tile_kernel(GatedGradXA
   static_assert(TS % 16 == 0 && LDS <= 156 * 1024, "staging must fit in LDS");
   __shared__ __attribute__((aligned(16))) char smem[LDS];
   __shared__ int rows[C::BM], cnt[C::NW];
-  int tm, tn;
-  if (!tile_of_workgroup(blockIdx.x, (g.M + C::BM - 1) / C::BM, (g.N + C::BN - 1) / C::BN, tm, tn)) return;
+  int tm, tn, z;
+  if (!tile_of_workgroup(blockIdx.x, (g.M + C::BM - 1) / C::BM, (g.N + C::BN - 1) / C::BN, kSplit ? g.splits : 1, tm, tn,
+                         z))
+    return;
   const int m0 = tm * C::BM, n0 = tn * C::BN;
   const int lane = threadIdx.x & 63, wave = wave_id(), wm = wave / C::WN, wn = wave % C::WN;
   const int nrows = tile_rows<C>(g.ex, g.slot_pos, rows, cnt, m0, g.M, kSplit);
   GatedGradSrc<C, kWide> src;
   src.wave = wave; src.wm = wm; src.wn = wn;
-  const int kt = g.Kd / 64, z = kSplit ? int(blockIdx.y) : 0;
+  const int kt = g.Kd / 64;
   // (scalar: the division is not, and the copies' bases have to be)
   const int kb = kSplit ? __builtin_amdgcn_readfirstlane(int(int64_t(2 * kt) * z / g.splits)) : 0;
   const int ke = kSplit ? __builtin_amdgcn_readfirstlane(int(int64_t(2 * kt) * (z + 1) / g.splits)) : 2 * kt;
@@ -1254,9 +1256,6 @@ __global__ __launch_bounds__(256) void gated_grad_x_sum_kernel(GatedGradXArgs g)
   Cols<E, 8>::store(static_cast<E *>(g.dX) + i, v);
 }
 
-using Big = LoopCfg<256, 256, 2, 4>;
-using Mid = LoopCfg<128, 256, 2, 4, 3>;
-
 template <typename E>
 void launch_act_grad(const void *dH, const void *pg, const void *pu, int act, void *dg, void *du, int64_t n,
                      hipStream_t s) {
@@ -1324,10 +1323,12 @@ hipError_t launch_gated(const GatedArgs &g, const TermsArgs &t, int dtype, hipSt
   if (g.term[0]) {
     const hipError_t e = launch_terms(t, false, dtype, g.M, s);
     if (e != hipSuccess) return e;
-    // rounds of tiles over the CUs; one of 128 rows takes 0.6 of one of 256
-    const int64_t n = (g.N + 127) / 128, big = ((g.M + 255) / 256) * n, mid = ((g.M + 127) / 128) * n;
-    if (6 * ((mid + 255) / 256) < 10 * ((big + 255) / 256)) launch_tiles<Mid, false, true>(g, s);
-    else launch_tiles<Big, false, true>(g, s);
+    switch (pick_shape(g.M, 2 * int64_t(g.N))) {
+      case kBig: launch_tiles<Big, false, true>(g, s); break;
+      case kTall: launch_tiles<Tall, false, true>(g, s); break;
+      case kMid: launch_tiles<Mid, false, true>(g, s); break;
+      default: launch_tiles<Small, false, true>(g, s);
+    }
   } else if (wide_rows(g.M, g.Kd)) {
     launch_tiles<Big, true, false>(g, s);
   } else {
@@ -1414,7 +1415,7 @@ hipError_t launch_gated_grad_x(const GatedGradXArgs &g, const TermsArgs &t, int 
     return hipGetLastError();
   }
   const int tiles = ((g.M + 127) / 128) * ((g.N + 255) / 256);
-  hipLaunchKernelGGL((gated_grad_x_tile_kernel<Mid, true, false>), dim3(8 * unsigned((tiles + 7) / 8), unsigned(g.splits)),
+  hipLaunchKernelGGL((gated_grad_x_tile_kernel<Mid, true, false>), dim3(8 * unsigned((tiles * g.splits + 7) / 8)),
                      dim3(Mid::NT), 0, s, g);
   hipLaunchKernelGGL(gated_grad_x_sum_kernel<uint16_t>, dim3(sums), dim3(256), 0, s, g);
   return hipGetLastError();

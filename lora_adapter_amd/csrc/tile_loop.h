@@ -33,6 +33,39 @@ struct LoopCfg {
   static_assert(NS >= 2 && (NS - 1) * LPW < 64, "stages, and the copies that may be in flight");
 };
 
+// The shapes, one workgroup on a CU each, and the time of a K tile on a full card
+// in units of about 0.17 us (measured with 64 K tiles: 107, 95, 62 and 40 us).
+// The larger ones do more with what they read; which one is fastest depends on
+// how well a problem's tiles divide into rounds of 256 CUs.
+using Big = LoopCfg<256, 256, 2, 4>;
+using Tall = LoopCfg<192, 256, 2, 4>;
+using Mid = LoopCfg<128, 256, 2, 4, 3>;
+using Small = LoopCfg<128, 128, 2, 2, 4>;
+struct TileShape {
+  int bm, bn, cost;
+};
+constexpr TileShape kTileShapes[4] = {{256, 256, 10}, {192, 256, 9}, {128, 256, 6}, {128, 128, 4}};
+enum { kBig, kTall, kMid, kSmall };
+
+// Tiles of an M x N output.
+inline int64_t tile_count(int shape, int64_t M, int64_t N) {
+  const TileShape &t = kTileShapes[shape];
+  return ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
+}
+// The shape whose rounds over the CUs cost least; `more`: further workgroups in the launch.
+inline int pick_shape(int64_t M, int64_t N, int64_t more = 0) {
+  int best = 0;
+  int64_t least = 0;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t c = kTileShapes[i].cost * ((tile_count(i, M, N) + more + 255) / 256);
+    if (i == 0 || c < least) {
+      best = i;
+      least = c;
+    }
+  }
+  return best;
+}
+
 // One 16-byte copy per lane from base + off to LDS at lds + 16 lane; base and
 // lds are the wave's.  (The s_nop: an LDS DMA needs a wait state after the scalar
 // write of m0.  The readfirstlanes: a uniform value may have come out of vector
@@ -160,6 +193,17 @@ __device__ __forceinline__ bool tile_of_workgroup(int b, int tiles_m, int tiles_
   const int t = (b & 7) * per + (b >> 3);
   if ((b >> 3) >= per || t >= tiles_m * tiles_n) return false;
   tile_coords(t, tiles_m, tiles_n, tm, tn);
+  return true;
+}
+
+// The same for `splits` parts of K of each tile: the tiles of one part lie
+// together, on XCDs that hold its rows of both operands.
+__device__ __forceinline__ bool tile_of_workgroup(int b, int tiles_m, int tiles_n, int splits, int &tm, int &tn, int &z) {
+  const int n = tiles_m * tiles_n, per = (n * splits + 7) / 8;
+  const int t = (b & 7) * per + (b >> 3);
+  if ((b >> 3) >= per || t >= n * splits) return false;
+  z = __builtin_amdgcn_readfirstlane(t / n);
+  tile_coords(t - z * n, tiles_m, tiles_n, tm, tn);
   return true;
 }
 
