@@ -1097,16 +1097,17 @@ struct GatedCall {
   ApplyWs w[2];
   GemmArgs g[2];
   GemmConfig cfg;
+  bool whole;
   GatedArgs a;
   TermsArgs t;
 };
 
-TermsArgs terms_args(const PlanView &pv, const lora_pool_desc *pool, int32_t K) {
+TermsArgs terms_args(const PlanView &pv, const lora_pool_desc *pool, int32_t T, int32_t K) {
   TermsArgs t{};
   t.hdr = pv.hdr; t.pair_tk = pv.pair_tk; t.pair_adapter = pv.pair_adapter; t.u_off = pv.u_off;
   t.slot_pos = pv.slot_pos;
   t.rank = pool->rank; t.page_start = pool->page_start; t.page_ids = pool->page_ids;
-  t.K = K;
+  t.M = T; t.K = K;
   return t;
 }
 
@@ -1143,15 +1144,17 @@ int32_t gated_args(const void *X, const void *W_gate_t, const void *W_up_t, int3
   a.part[0] = c.g[0].partial; a.part[1] = c.g[1].partial;
   a.splits = c.cfg.splits;
   a.slot_pos = pv.slot_pos;
-  // where lora_apply would keep partial products there is room for the
-  // adapters' terms
-  if (c.cfg.kind != 4 && !c.cfg.fused)
-    for (int p = 0; p < 2; ++p) a.term[p] = c.g[p].partial;
-  c.t = terms_args(pv, gate, K);
-  c.t.U[0] = a.ex.U; c.t.U[1] = a.U_up; c.t.u_cap = a.ex.u_cap;
-  c.t.pages[0] = gate->b_pages; c.t.pages[1] = up->b_pages;
-  c.t.out[0] = a.term[0]; c.t.out[1] = a.term[1];
-  c.t.N = gate->d_out;
+  c.whole = c.cfg.kind != 4 && gated_whole(T, a.Kd, gate->dtype, c.cfg.fused);
+  if (c.cfg.kind == 4 || c.whole) return LORA_OK;
+  a.splits = gated_base_splits(T, a.N, a.Kd, gate->dtype, c.cfg.splits);
+  TermsArgs &t = c.t;
+  t = terms_args(pv, gate, T, K);
+  for (int p = 0; p < 2; ++p) t.sums[p] = a.sums[p] = c.g[p].partial;
+  t.U[0] = a.ex.U; t.U[1] = a.U_up; t.u_cap = a.ex.u_cap;
+  t.pages[0] = gate->b_pages; t.pages[1] = up->b_pages;
+  t.N = a.N; t.splits = a.splits;
+  t.act = activation;
+  t.H = H; t.pre_gate = pre_gate; t.pre_up = pre_up;
   return LORA_OK;
 }
 
@@ -1179,9 +1182,12 @@ int32_t lora_gated_apply(const void *X, const void *W_gate_t, const void *W_up_t
   if (st != LORA_OK || T == 0) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const PlanView pv = plan_view(plan, int64_t(T) * K, gate->n_adapters);
-  hipError_t e = gated_shrinks(c, X, keep_mask, keep_scale, T, K, gates, gate, up, pv, s);
+  const bool base = c.cfg.kind != 4 && !c.whole;
+  hipError_t e = base ? launch_gated_base(c.a, gate->dtype, nullptr, s) : hipSuccess;
+  if (e == hipSuccess) e = gated_shrinks(c, X, keep_mask, keep_scale, T, K, gates, gate, up, pv, s);
   if (e != hipSuccess) return LORA_ERR_DEVICE;
-  if (c.cfg.kind != 4) return dev(launch_gated(c.a, c.t, gate->dtype, s));
+  if (base) return dev(launch_terms(c.t, false, gate->dtype, s));
+  if (c.whole) return dev(launch_gated(c.a, s));
   e = launch_gated_decode(c.cfg, c.g, s);
   if (e == hipSuccess) e = launch_gated_decode_epilogue(c.a, s);
   return dev(e);
@@ -1215,6 +1221,18 @@ int32_t lora_gated_forward(const int32_t *ids, const float *gates, int32_t T, in
     c.a.U_up = c.w[1].slot_u;
     return dev(launch_gated_decode_epilogue(c.a, s));
   }
+  if (T > 0 && !c.whole) {
+    // the plan beside the base products
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const PlanLaunch pl = gated_base_plan(c.a, gate->dtype, ids, gates, T, K, pool_view(gate), static_cast<int32_t *>(plan));
+    if (pl.lds) {
+      const PlanView pv = plan_view(plan, int64_t(T) * K, gate->n_adapters);
+      hipError_t e = launch_gated_base(c.a, gate->dtype, &pl.a, s);
+      if (e == hipSuccess) e = gated_shrinks(c, X, keep_mask, keep_scale, T, K, gates, gate, up, pv, s);
+      if (e == hipSuccess) e = launch_terms(c.t, false, gate->dtype, s);
+      return dev(e);
+    }
+  }
   if ((st = lora_plan(ids, gates, T, K, gate, plan, plan_bytes, stream)) != LORA_OK || T == 0) return st;
   return lora_gated_apply(X, W_gate_t, W_up_t, activation, H, pre_gate, pre_up, T, K, gates, keep_mask,
                           keep_scale, gate, up, plan, ws_gate, ws_gate_bytes, ws_up, ws_up_bytes, stream);
@@ -1225,7 +1243,7 @@ int32_t lora_gated_forward(const int32_t *ids, const float *gates, int32_t T, in
 namespace {
 
 // Workspace of the gated backward: [G of the gate][G of the up projection], and
-// where the product is split [the splits' sums][the adapters' terms].
+// where the product is split [the splits' sums].
 struct GatedGradWs {
   int splits;
   size_t g, sums, total;
@@ -1237,7 +1255,7 @@ GatedGradWs gated_grad_ws(int32_t T, int32_t K, int32_t d_in, int32_t d_out, int
   w.g = align_up(size_t(T) * size_t(K) * size_t(max_rank) * sizeof(float) + 4);
   const size_t one = size_t(T) * size_t(d_in) * sizeof(float);
   w.sums = align_up(size_t(w.splits) * one);
-  w.total = 2 * w.g + w.sums + (w.splits ? align_up(one) : 0);
+  w.total = 2 * w.g + w.sums;
   return w;
 }
 
@@ -1304,14 +1322,13 @@ int32_t lora_gated_grad(const void *dH, const void *pre_gate, const void *pre_up
   a.mask = keep_mask; a.dX = dX;
   a.slot_pos = pv.slot_pos;
   a.splits = w.splits;
-  TermsArgs t = terms_args(pv, gate, K);
+  TermsArgs t = terms_args(pv, gate, T, K);
   if (w.splits) {
-    a.sums = reinterpret_cast<float *>(base + 2 * w.g);
-    a.term = reinterpret_cast<float *>(base + 2 * w.g + w.sums);
+    t.sums[0] = a.sums = reinterpret_cast<float *>(base + 2 * w.g);
     t.U[0] = a.ex.U; t.U[1] = a.U_up; t.u_cap = a.ex.u_cap;
     t.pages[0] = gate->a_pages; t.pages[1] = up->a_pages;
-    t.out[0] = a.term;
-    t.N = d;
+    t.N = d; t.splits = w.splits;
+    t.mask = keep_mask; t.dX = dX;
   }
   return dev(launch_gated_grad_x(a, t, dtype, s));
 }

@@ -506,49 +506,66 @@ __device__ __forceinline__ bool any_slot(const int32_t *slot_pos, int t, int K) 
 // ------------------------------------------------------------ adapters' terms to memory
 // Batches of some hundred tokens have few tiles and many adapters for each of
 // them: walking those in the tiles is a chain of round trips (700 tokens of 96
-// adapters of ranks 8 .. 64, 2240 -> 5824: 235 us for the tiles).  Their terms are
-// formed ahead by a launch of their own, out[t][n] = sum_j U[u + j] . page_j[n] for
-// slot k of the tokens, in float32: a wave takes 16 pairs of the plan's order and
-// 128 columns, so that pages are read once for the pairs of an adapter among
+// adapters of ranks 8 .. 64, 2240 -> 5824: 235 us for the tiles).  There the base
+// products go to memory in float32 (which needs no plan: one workgroup of that
+// launch builds it), and a launch of one-wave workgroups forms the terms
+// sum_j U[u + j] . page_j[n] for slot k of the tokens and finishes what it can.
+// A wave takes 16 pairs of the plan's order and 128 columns (64 of each
+// projection), so that pages are read once for the pairs of an adapter among
 // them, and there are thousands of waves.  It walks their adapters, 16 rank rows
-// a pass, with the page ids two passes ahead and page rows and U one.  kSum: both
-// projections' terms into out[0] (dX), otherwise blockIdx.y's into its own.
-// Launched slot by slot; a token's first active slot writes, its others add.
+// a pass, with the page ids two passes ahead and page rows and U one.
+// Launched slot by slot: a token's first active slot adds the base product's
+// splits, its last one finishes (activation, product and rounding; for kSum,
+// dX, both projections' terms under the mask and the rounding), the ones between
+// leave the sum in split 0.  The first launch also finishes, 16 tokens a wave,
+// those without an active slot.
 // The products are MFMAs with the rows of other adapters zero, so that all runs
 // of a window share accumulators: with a branch for each row and rank row, or
-// every product on the vector units, the same launch took 270 us and 73.
+// every product on the vector units, the same launch took 270 us and 73, now
+// NEWTERMS.
 // bf16 pages: U as hi | lo against the rows twice, as in add_segs; float32 pages:
 // v_mfma_f32_16x16x4_f32.
-template <typename E> struct TermTile;
-template <> struct TermTile<uint16_t> {
+template <typename E, bool kPair> struct TermTile;
+template <bool kPair> struct TermTile<uint16_t, kPair> {
   static constexpr int COLS = 128, NBLK = 8, NV = 4;
   uint4 v[NV];
-  // rank rows lane / 16 + 4 h (page id in lane of that number), columns 8 (lane % 16) ..
-  __device__ __forceinline__ void load(const uint16_t *pages, int id, int c0, int N) {
-    const int lane = threadIdx.x, col = min(c0 + (lane & 15) * 8, N - 8);
+  // kPair: rank rows lane / 8 + 8 (h % 2) of projection h / 2, columns 8 (lane % 8) ..;
+  // else of projection p rows lane / 16 + 4 h, columns 8 (lane % 16) ..  (page id in
+  // the lane of the row's number)
+  static __device__ __forceinline__ int row(int h) {
+    const int lane = threadIdx.x;
+    return kPair ? (lane >> 3) + 8 * (h & 1) : (lane >> 4) + 4 * h;
+  }
+  __device__ __forceinline__ void load(const void *const (&pages)[2], int p, int id, int c0, int N) {
+    const int lane = threadIdx.x, col = min(c0 + (kPair ? lane & 7 : lane & 15) * 8, N - 8);
 #pragma unroll
-    for (int h = 0; h < NV; ++h)
-      v[h] = *reinterpret_cast<const uint4 *>(pages + int64_t(__shfl(id, (lane >> 4) + 4 * h, 64)) * N + col);
+    for (int h = 0; h < NV; ++h) {
+      const uint16_t *from = static_cast<const uint16_t *>((kPair ? h >> 1 : p) ? pages[1] : pages[0]);
+      v[h] = *reinterpret_cast<const uint4 *>(from + int64_t(__shfl(id, row(h), 64)) * N + col);
+    }
   }
   // acc += U.rows; whether values that are not finite were left out
-  __device__ __forceinline__ bool add(char *lds, int nr, const float (&u)[8], f32x4_t (&acc)[NBLK]) {
+  __device__ __forceinline__ bool add(char *lds, int nr, const float (&u)[kPair ? 2 : 1][8], f32x4_t (&acc)[NBLK]) {
     const int lane = threadIdx.x, L = lane & 15;
     bool bad = false;
 #pragma unroll
     for (int h = 0; h < NV; ++h) {
-      const int j = (lane >> 4) + 4 * h;
+      const int j = row(h), piece = kPair ? (lane & 7) + 8 * (h >> 1) : L;
       if (j >= nr) v[h] = make_uint4(0u, 0u, 0u, 0u);
       bad |= drop8(v[h]);
-      *reinterpret_cast<uint4 *>(lds + j * 256 + (L ^ ((j & 3) << 1)) * 16) = v[h];
+      *reinterpret_cast<uint4 *>(lds + j * 256 + (piece ^ ((j & 3) << 1)) * 16) = v[h];
     }
-    uint32_t w[4];
+    bf16x8_t a[kPair ? 2 : 1];
 #pragma unroll
-    for (int q = 0; q < 8; q += 2) {
-      const uint32_t h = f2bf2(u[q], u[q + 1]);
-      w[q >> 1] = lane < 32 ? h : f2bf2(u[q] - bf_lo(h), u[q + 1] - bf_hi(h));
+    for (int p = 0; p < (kPair ? 2 : 1); ++p) {
+      uint32_t w[4];
+#pragma unroll
+      for (int q = 0; q < 8; q += 2) {
+        const uint32_t h = f2bf2(u[p][q], u[p][q + 1]);
+        w[q >> 1] = lane < 32 ? h : f2bf2(u[p][q] - bf_lo(h), u[p][q + 1] - bf_hi(h));
+      }
+      __builtin_memcpy(&a[p], w, 16);
     }
-    bf16x8_t a;
-    __builtin_memcpy(&a, w, 16);
     typedef __attribute__((address_space(3))) v4i16_t lds_v4;
     const int k = 8 * ((lane >> 4) & 1) + (L >> 2);
 #pragma unroll
@@ -560,36 +577,44 @@ template <> struct TermTile<uint16_t> {
       bf16x8_t f;
       __builtin_memcpy(&f, &lo, 8);
       __builtin_memcpy(reinterpret_cast<char *>(&f) + 8, &hi, 8);
-      acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, f, acc[b], 0, 0, 0);
+      acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[kPair ? b / 4 : 0], f, acc[b], 0, 0, 0);
     }
     return __ballot(bad) != 0;
   }
   static __device__ __forceinline__ bool finite(uint16_t v) { return (v & 0x7f80u) != 0x7f80u; }
 };
-template <> struct TermTile<float> {
+template <bool kPair> struct TermTile<float, kPair> {
   static constexpr int COLS = 64, NBLK = 4, NV = 16;
   float v[NV];
-  // v[4 b + s]: rank row 4 s + lane / 16, column 16 b + lane % 16
-  __device__ __forceinline__ void load(const float *pages, int id, int c0, int N) {
+  // v[4 b + s]: rank row 4 s + lane / 16, column 16 b + lane % 16 (kPair: 16 (b % 2)
+  // + lane % 16 of projection b / 2)
+  __device__ __forceinline__ void load(const void *const (&pages)[2], int p, int id, int c0, int N) {
     const int lane = threadIdx.x;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const float *row = pages + int64_t(__shfl(id, 4 * s + (lane >> 4), 64)) * N + (lane & 15);
+      const int64_t at = int64_t(__shfl(id, 4 * s + (lane >> 4), 64)) * N + (lane & 15);
 #pragma unroll
-      for (int b = 0; b < NBLK; ++b) v[4 * b + s] = row[min(c0 + 16 * b, N - 16)];
+      for (int b = 0; b < NBLK; ++b) {
+        const float *from = static_cast<const float *>((kPair ? b >> 1 : p) ? pages[1] : pages[0]);
+        v[4 * b + s] = from[at + min(c0 + 16 * (kPair ? b & 1 : b), N - 16)];
+      }
     }
   }
-  __device__ __forceinline__ bool add(char *, int nr, const float (&u)[8], f32x4_t (&acc)[NBLK]) {
+  __device__ __forceinline__ bool add(char *, int nr, const float (&u)[kPair ? 2 : 1][8], f32x4_t (&acc)[NBLK]) {
     const int lane = threadIdx.x;
     bool bad = false;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       // u: ranks 8 (lane / 16 % 2) .. of row lane % 16; wanted: rank 4 s + lane / 16
-      float a = 0.f;
+      float a[kPair ? 2 : 1];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const float x = __shfl(u[(4 * s + g) & 7], (lane & 15) + 16 * ((4 * s + g) >> 3), 64);
-        if ((lane >> 4) == g) a = x;
+      for (int p = 0; p < (kPair ? 2 : 1); ++p) {
+        a[p] = 0.f;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const float x = __shfl(u[p][(4 * s + g) & 7], (lane & 15) + 16 * ((4 * s + g) >> 3), 64);
+          if ((lane >> 4) == g) a[p] = x;
+        }
       }
 #pragma unroll
       for (int b = 0; b < NBLK; ++b) {
@@ -599,7 +624,7 @@ template <> struct TermTile<float> {
           bad = true;
           x = 0.f;
         }
-        acc[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, x, acc[b], 0, 0, 0);
+        acc[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[kPair ? b / 2 : 0], x, acc[b], 0, 0, 0);
       }
     }
     return __ballot(bad) != 0;
@@ -607,22 +632,103 @@ template <> struct TermTile<float> {
   static __device__ __forceinline__ bool finite(float v) { return v - v == 0.f; }
 };
 
+// v += the base product's sums at i, of all splits (`first`) or what an earlier
+// slot left in split 0.
+__device__ __forceinline__ void add_sums(const TermsArgs &a, int p, int64_t i, bool first, float (&v)[8]) {
+  const int64_t n = int64_t(a.M) * a.N;
+  const int splits = first ? a.splits : 1;
+  for (int z0 = 0; z0 < splits; z0 += 4) {
+    Raw8<float> pr[4];
+#pragma unroll
+    for (int z = 0; z < 4; ++z) pr[z].load(a.sums[p] + int64_t(min(z0 + z, splits - 1)) * n + i);
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+      if (z0 + z < splits) {
+        float o[8];
+        pr[z].to8(o);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] += o[c];
+      }
+    }
+  }
+}
+
+// 8 columns of a token, whose terms of this slot are in term[0] (kSum) or term[0]
+// and term[1].
+template <typename E, bool kSum>
+__device__ __forceinline__ void finish8(const TermsArgs &a, int64_t i, bool first, bool last, float (&term)[2][8]) {
+  if constexpr (kSum) {
+    float v[8] = {};
+    add_sums(a, 0, i, first, v);
+    uint2 mw = make_uint2(0x01010101u, 0x01010101u);
+    if (a.mask) mw = *reinterpret_cast<const uint2 *>(a.mask + i);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) v[x] += float(((x < 4 ? mw.x : mw.y) >> (8 * (x & 3))) & 0xffu) * term[0][x];
+    if (last) Cols<E, 8>::store(static_cast<E *>(a.dX) + i, v);
+    else Cols<float, 8>::store(a.sums[0] + i, v);
+  } else {
+    add_sums(a, 0, i, first, term[0]);
+    add_sums(a, 1, i, first, term[1]);
+    if (!last) {
+      Cols<float, 8>::store(a.sums[0] + i, term[0]);
+      Cols<float, 8>::store(a.sums[1] + i, term[1]);
+      return;
+    }
+    constexpr bool kFast = sizeof(E) == 2;
+    float h[8], slope;
+    if (a.act == LORA_ACT_SILU) {
+#pragma unroll
+      for (int x = 0; x < 8; ++x) h[x] = activate<LORA_ACT_SILU, kFast>(term[0][x], slope) * term[1][x];
+    } else if (a.act == LORA_ACT_GELU) {
+#pragma unroll
+      for (int x = 0; x < 8; ++x) h[x] = activate<LORA_ACT_GELU, kFast>(term[0][x], slope) * term[1][x];
+    } else {
+#pragma unroll
+      for (int x = 0; x < 8; ++x) h[x] = activate<LORA_ACT_GELU_TANH, kFast>(term[0][x], slope) * term[1][x];
+    }
+    Cols<E, 8>::store(static_cast<E *>(a.H) + i, h);
+    if (a.pre_gate) {
+      Cols<E, 8>::store(static_cast<E *>(a.pre_gate) + i, term[0]);
+      Cols<E, 8>::store(static_cast<E *>(a.pre_up) + i, term[1]);
+    }
+  }
+}
+
 template <typename E, bool kSum>
 __global__ __launch_bounds__(64) void terms_kernel(TermsArgs a) {
-  using Tile = TermTile<E>;
-  __shared__ __attribute__((aligned(16))) char lds[sizeof(E) == 2 ? 4096 : 16];
+  constexpr bool kPair = !kSum;
+  constexpr int NP = kPair ? 2 : 1;
+  using Tile = TermTile<E, kPair>;
+  constexpr int COLS = Tile::COLS / NP;                 // output columns of the wave
+  constexpr int SC = Tile::COLS + 4;                    // floats of a staged row: COLS of each projection
+  __shared__ __attribute__((aligned(16))) char lds[16 * SC * 4];
+  static_assert(sizeof(lds) >= 4096, "a pass's page rows");
   const int P = a.hdr[LORA_PH_PAIRS], total = a.hdr[LORA_PH_RPAIRS], lane = threadIdx.x;
-  const int n_x = (a.N + Tile::COLS - 1) / Tile::COLS, p0 = int(blockIdx.x / unsigned(n_x)) * 16, m = min(16, P - p0);
-  if (m <= 0 || int64_t(total) > a.u_cap) return;
+  const int n_x = (a.N + COLS - 1) / COLS, window = int(blockIdx.x / unsigned(n_x));
+  const int c0 = int(blockIdx.x % unsigned(n_x)) * COLS;
+  const bool lora_on = int64_t(total) <= a.u_cap;
+  if (window >= a.windows) {
+    // tokens without an active slot
+    const int t = (window - a.windows) * 16 + (lane >> 2);
+    if (t >= a.M || (lora_on && any_slot(a.slot_pos, t, a.K))) return;
+#pragma unroll
+    for (int h = 0; h < COLS / 32; ++h) {
+      const int col = c0 + h * 32 + (lane & 3) * 8;
+      float zero[2][8] = {};
+      if (col < a.N) finish8<E, kSum>(a, int64_t(t) * a.N + col, true, true, zero);
+    }
+    return;
+  }
+  const int p0 = window * 16, m = min(16, P - p0);
+  if (m <= 0 || !lora_on) return;
   // lane l (mod 16): pair p0 + l
   const int pl = p0 + min(lane & 15, m - 1);
   const int tk = a.pair_tk[pl], ad = a.pair_adapter[pl], uo = a.u_off[pl];
   const int rk = a.rank[ad], pst = a.page_start[ad];
-  const int c0 = int(blockIdx.x % unsigned(n_x)) * Tile::COLS;
   const unsigned want = unsigned(__ballot(lane < m && tk % a.K == a.k)) & 0xffffu;
   if (!want) return;
   auto lane_of = [&](int v, int l) __attribute__((always_inline)) { return __builtin_amdgcn_readlane(v, l); };
-  // a pass: projection p, the run of pairs [i, j) of one adapter, rank rows jb ..
+  // a pass: projection p (kPair: both), the run of pairs [i, j) of one adapter, rank rows jb ..
   struct Pass {
     int p, i, j, jb;
   };
@@ -655,24 +761,27 @@ __global__ __launch_bounds__(64) void terms_kernel(TermsArgs a) {
     const int nr = min(16, lane_of(rk, x.i) - x.jb);
     return a.page_ids[lane_of(pst, x.i) + x.jb + min(lane & 15, nr - 1)];
   };
-  auto fetch = [&](const Pass &x, int id, Tile &v, float (&u)[8]) __attribute__((always_inline)) {
-    v.load(static_cast<const E *>(x.p ? a.pages[1] : a.pages[0]), id, c0, a.N);
+  auto fetch = [&](const Pass &x, int id, Tile &v, float (&u)[NP][8]) __attribute__((always_inline)) {
+    v.load(a.pages, x.p, id, c0, a.N);
     // U of row lane % 16, ranks 8 (lane / 16 % 2) .. + 7 of the pass
     const int r = lane & 15, j0 = 8 * ((lane >> 4) & 1), nr = min(16, lane_of(rk, x.i) - x.jb);
     const bool mine = r >= x.i && r < x.j;
     const int at = uo + x.jb + j0;
-    load8_tail((x.p ? a.U[1] : a.U[0]) + (mine ? at : 0), min(8, mine ? total - at : total), u);
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (!mine || j0 + q >= nr) u[q] = 0.f;
+    for (int p = 0; p < NP; ++p) {
+      load8_tail(((kPair ? p : x.p) ? a.U[1] : a.U[0]) + (mine ? at : 0), min(8, mine ? total - at : total), u[p]);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (!mine || j0 + q >= nr) u[p][q] = 0.f;
+    }
   };
 
   Pass c, n1;
-  c.p = kSum ? 0 : int(blockIdx.y);
+  c.p = 0;
   run_at(c, 0);
   n1 = c;
   Tile v, w;
-  float u[8], un[8];
+  float u[NP][8], un[NP][8];
   int id = ids(c);
   fetch(c, id, v, u);
   after(n1);
@@ -695,31 +804,44 @@ __global__ __launch_bounds__(64) void terms_kernel(TermsArgs a) {
     n1 = n2;
     v = w;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) u[q] = un[q];
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) u[p][q] = un[p][q];
   }
-  float *out = a.out[kSum ? 0 : blockIdx.y];
+  // through LDS, to lanes that hold 8 columns of a row
+  float *stage = reinterpret_cast<float *>(lds);
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
     const int r = acc_row(0, x);
-    const int t = __shfl(tk, r, 64) / a.K, rr = __shfl(rk, r, 64), ps = __shfl(pst, r, 64), at = __shfl(uo, r, 64);
-    if (!((want >> r) & 1)) continue;
-    const bool add = any_slot(a.slot_pos, t, a.K, a.k);
+    const int rr = __shfl(rk, r, 64), ps = __shfl(pst, r, 64), at = __shfl(uo, r, 64);
 #pragma unroll
     for (int b = 0; b < Tile::NBLK; ++b) {
-      const int col = c0 + acc_col(b);
-      if (col >= a.N) continue;
-      float *o = out + int64_t(t) * a.N + col;
       float y = acc[b][x];
-      if (dropped) {
+      const int col = c0 + (acc_col(b) % COLS), p = acc_col(b) / COLS;
+      if (dropped && r < m && col < a.N) {
         // the values left out: infinities and NaN
-        for (int p = kSum ? 0 : int(blockIdx.y); p < (kSum ? 2 : int(blockIdx.y) + 1); ++p)
+        for (int q = p; q < (kSum ? 2 : p + 1); ++q)
           for (int j = 0; j < rr; ++j) {
-            const E z = static_cast<const E *>(a.pages[p])[int64_t(a.page_ids[ps + j]) * a.N + col];
-            if (!Tile::finite(z)) y = fmaf(a.U[p][int64_t(at) + j], Elem<E>::to_f(z), y);
+            const E z = static_cast<const E *>(a.pages[q])[int64_t(a.page_ids[ps + j]) * a.N + col];
+            if (!Tile::finite(z)) y = fmaf(a.U[q][int64_t(at) + j], Elem<E>::to_f(z), y);
           }
       }
-      *o = add ? *o + y : y;
+      stage[r * SC + acc_col(b)] = y;
     }
+  }
+  const int r = lane >> 2, t = __shfl(tk, r, 64) / a.K;
+  if (!((want >> r) & 1)) return;
+  const bool first = !any_slot(a.slot_pos, t, a.K, a.k);
+  bool last = true;
+  for (int k = a.k + 1; k < a.K; ++k) last &= a.slot_pos[int64_t(t) * a.K + k] < 0;
+#pragma unroll
+  for (int h = 0; h < COLS / 32; ++h) {
+    const int cc = h * 32 + (lane & 3) * 8, col = c0 + cc;
+    if (col >= a.N) continue;
+    float term[2][8];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) Elem<float>::load8(stage + r * SC + p * COLS + cc, term[p]);
+    finish8<E, kSum>(a, int64_t(t) * a.N + col, first, last, term);
   }
 }
 
@@ -733,6 +855,28 @@ struct GatedSrc {
   RowOffsets<C::A_INS, kWide> ao;
   uint32_t bo[C::B_INS];
   int wave, wm, wn;
+  // row_of(r): the token of tile row r
+  template <typename F>
+  __device__ __forceinline__ void set(const GatedArgs &g, int n0, const F &row_of) {
+    const int lane = threadIdx.x & 63;
+    wave = wave_id();
+    wm = wave / C::WN;
+    wn = wave % C::WN;
+    a = static_cast<const uint16_t *>(g.X);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) b[p] = static_cast<const uint16_t *>(g.W[p]) + int64_t(n0) * g.Kd;
+#pragma unroll
+    for (int i = 0; i < C::A_INS; ++i) {
+      const int row = (wave * C::A_INS + i) * 8 + (lane >> 3);
+      ao.set(i, int64_t(row_of(row)) * g.Kd + tswz(row, lane & 7) * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < C::B_INS; ++i) {
+      const int row = (wave * C::B_INS + i) * 8 + (lane >> 3);
+      const int of = (row >> 6) * 32 + (row & 31);        // of its weight
+      bo[i] = (uint32_t(min(of, g.N - 1 - n0)) * uint32_t(g.Kd) + tswz(row, lane & 7) * 8) * 2;
+    }
+  }
   __device__ __forceinline__ void copy(uint32_t lds, int kt, int i) const {
     if (i < C::A_INS) {
       ao.copy(a + kt * 64, i, lds + (wave * C::A_INS + i) * 1024);
@@ -746,8 +890,7 @@ struct GatedSrc {
   }
 };
 
-// kTerms: the adapters' terms come from terms_kernel's buffers.
-template <typename C, bool kWide, bool kTerms, int kAct>
+template <typename C, bool kWide, int kAct>
 __global__ __launch_bounds__(C::NT, 1) void gated_tile_kernel(GatedArgs g) {
   constexpr int SC = 64 + 4;                            // floats of a staged row: 32 of g, 32 of u
   constexpr int NO = C::BN / 2;                         // output columns of the tile
@@ -755,31 +898,17 @@ __global__ __launch_bounds__(C::NT, 1) void gated_tile_kernel(GatedArgs g) {
   constexpr int TS = C::NW * WLDS;                      // the list of adapters lies behind those
   __shared__ __attribute__((aligned(16))) char smem[C::LDS];
   __shared__ int rows[C::BM], cnt[C::NW];
-  static_assert(TS % 16 == 0 && TS + (kTerms ? 0 : TileLists<C>::SIZE) <= C::LDS, "staging must fit in LDS");
+  static_assert(TS % 16 == 0 && TS + TileLists<C>::SIZE <= C::LDS, "staging must fit in LDS");
   int tm, tn;
   if (!tile_of_workgroup(blockIdx.x, (g.M + C::BM - 1) / C::BM, (g.N + NO - 1) / NO, tm, tn)) return;
   const int m0 = tm * C::BM, n0 = tn * NO;
   const int lane = threadIdx.x & 63, wave = wave_id(), wm = wave / C::WN, wn = wave % C::WN;
-  const int nrows = tile_rows<C>(g.ex, g.slot_pos, rows, cnt, m0, g.M, kTerms);
+  const int nrows = tile_rows<C>(g.ex, g.slot_pos, rows, cnt, m0, g.M, false);
 
   GatedSrc<C, kWide> src;
-  src.wave = wave; src.wm = wm; src.wn = wn;
-  src.a = static_cast<const uint16_t *>(g.X);
-#pragma unroll
-  for (int p = 0; p < 2; ++p) src.b[p] = static_cast<const uint16_t *>(g.W[p]) + int64_t(n0) * g.Kd;
-#pragma unroll
-  for (int i = 0; i < C::A_INS; ++i) {
-    const int row = (wave * C::A_INS + i) * 8 + (lane >> 3);
-    src.ao.set(i, int64_t(rows[min(row, nrows - 1)]) * g.Kd + tswz(row, lane & 7) * 8);
-  }
-#pragma unroll
-  for (int i = 0; i < C::B_INS; ++i) {
-    const int row = (wave * C::B_INS + i) * 8 + (lane >> 3);
-    const int of = (row >> 6) * 32 + (row & 31);        // of its weight
-    src.bo[i] = (uint32_t(min(of, g.N - 1 - n0)) * uint32_t(g.Kd) + tswz(row, lane & 7) * 8) * 2;
-  }
+  src.set(g, n0, [&](int row) { return rows[min(row, nrows - 1)]; });
   // fetched under the K loop
-  const int4 sd0 = kTerms ? make_int4(-1, 0, 0, 0) : row_desc(g.ex, rows, nrows, 0);
+  const int4 sd0 = row_desc(g.ex, rows, nrows, 0);
   f32x4_t acc[C::TM][C::TN];
   tile_loop<C>(src, smem, g.Kd / 64, acc);
 
@@ -792,9 +921,8 @@ __global__ __launch_bounds__(C::NT, 1) void gated_tile_kernel(GatedArgs g) {
   unsigned dropped = 0;
   const bool lora_on = expand_enabled(g.ex);
   TileTerms<C> &tt = *reinterpret_cast<TileTerms<C> *>(smem + TS);
-  bool common = false;
-  if constexpr (!kTerms) common = lora_on && g.ex.K == 1 && tile_terms<C>(e, tt, sd0);
-  if (lora_on && !kTerms && !common) {
+  const bool common = lora_on && g.ex.K == 1 && tile_terms<C>(e, tt, sd0);
+  if (lora_on && !common) {
     for (int k = 0; k < g.ex.K; ++k) {
       list_segs<C>(segs, k ? row_desc(g.ex, rows, nrows, k) : sd0);
       if (inside) dropped |= add_segs<true, C, C::TM>(e, segs, tlds, wm * C::TM, c0, g.N, acc);
@@ -802,30 +930,10 @@ __global__ __launch_bounds__(C::NT, 1) void gated_tile_kernel(GatedArgs g) {
   }
   if (!inside) return;
   TermCache<true> cache;
-  // kTerms: the adapters' terms of a row, a block ahead
-  Raw8<float> tg, tu;
-  bool has = false;
-  auto fetch = [&](int i) __attribute__((always_inline)) {
-    const int rr = (wm * C::TM + i) * 16 + (lane >> 2), cc = (lane & 3) * 8;
-    has = lora_on && rr < nrows && any_slot(g.slot_pos, rows[rr], g.ex.K);
-    if (!has) return;
-    const int64_t at = int64_t(rows[rr]) * g.N + c0 + cc;
-    tg.load(g.term[0] + at);
-    tu.load(g.term[1] + at);
-  };
-  if constexpr (kTerms) fetch(0);
 #pragma unroll
   for (int i = 0; i < C::TM; ++i) {
     const int r0 = (wm * C::TM + i) * 16;
     if (common && add_tile_terms<true, C>(e, tt, tlds, r0, c0, g.N, acc[i], cache)) dropped |= 1u << i;
-    float dg[8] = {}, du[8] = {};
-    if constexpr (kTerms) {
-      if (has) {
-        tg.to8(dg);
-        tu.to8(du);
-      }
-      if (i + 1 < C::TM) fetch(i + 1);
-    }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -844,10 +952,6 @@ __global__ __launch_bounds__(C::NT, 1) void gated_tile_kernel(GatedArgs g) {
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
       float slope;
-      if constexpr (kTerms) {
-        gv[x] += dg[x];
-        uv[x] += du[x];
-      }
       h[x] = activate<kAct, true>(gv[x], slope) * uv[x];
     }
     const int64_t at = int64_t(rows[r0 + rr]) * g.N + c0 + cc;
@@ -857,6 +961,40 @@ __global__ __launch_bounds__(C::NT, 1) void gated_tile_kernel(GatedArgs g) {
       store8_nt(static_cast<uint16_t *>(g.pre_up) + at, uv);
     }
   }
+}
+
+// The base products alone, in float32 (no plan needed: where pa has one to build,
+// the first workgroup does, so that its 12 .. 20 us lie under the product's).
+template <typename C>
+__global__ __launch_bounds__(C::NT, 1) void gated_base_tile_kernel(GatedArgs g, PlanArgs pa) {
+  __shared__ __attribute__((aligned(16))) char smem[C::LDS];
+  int b = blockIdx.x, tm, tn;
+  if (pa.plan) {
+    if (b == 0) {
+      plan_build<true>(pa, reinterpret_cast<int *>(smem));
+      return;
+    }
+    --b;
+  }
+  constexpr int NO = C::BN / 2;
+  if (!tile_of_workgroup(b, (g.M + C::BM - 1) / C::BM, (g.N + NO - 1) / NO, tm, tn)) return;
+  const int m0 = tm * C::BM, n0 = tn * NO;
+  GatedSrc<C, false> src;
+  src.set(g, n0, [&](int row) { return min(m0 + row, g.M - 1); });
+  f32x4_t acc[C::TM][C::TN];
+  tile_loop<C>(src, smem, g.Kd / 64, acc);
+#pragma unroll
+  for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int col = n0 + src.wn * 32 + acc_col(j & 1);
+      if (col >= g.N) continue;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int row = m0 + src.wm * C::TM * 16 + acc_row(i, v);
+        if (row < g.M) g.sums[j >> 1][int64_t(row) * g.N + col] = acc[i][j][v];
+      }
+    }
 }
 
 // ------------------------------------------------------------ decode
@@ -981,49 +1119,33 @@ __global__ __launch_bounds__(256) void gated_decode_epilogue_kernel(GatedArgs g)
 }
 
 // ------------------------------------------------------------ float32
-// 64 tokens by 32 output columns: the B side of a tile_f32 is 32 rows of each
-// weight, g and u meet in LDS.
-template <int kAct>
-__global__ __launch_bounds__(256) void gated_f32_kernel(GatedArgs g) {
-  __shared__ F32Tile t;
-  __shared__ __attribute__((aligned(16))) float stage[64][64 + 4];
-  const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 32;
+// The base products of 64 tokens by 32 output columns, of a split of K: the B side
+// of a tile_f32 is 32 rows of each weight.  The plan as in gated_base_tile_kernel.
+__global__ __launch_bounds__(256) void gated_base_f32_kernel(GatedArgs g, PlanArgs pa) {
+  __shared__ F32Tile lds;
+  int b = blockIdx.x;
+  if (pa.plan) {
+    if (b == 0) {
+      plan_build<true>(pa, reinterpret_cast<int *>(&lds));
+      return;
+    }
+    --b;
+  }
+  const int gx = g.N / 32, gy = (g.M + 63) / 64;
+  const int n0 = b % gx * 32, m0 = b / gx % gy * 64, z = b / gx / gy, kt = g.Kd / 64;
   const float *X = static_cast<const float *>(g.X);
   const float *Wg = static_cast<const float *>(g.W[0]), *Wu = static_cast<const float *>(g.W[1]);
   const f32x16_t acc = tile_f32<false>(
-      t, 0, g.Kd,
+      lds, int(int64_t(kt) * z / g.splits) * 64, int(int64_t(kt) * (z + 1) / g.splits) * 64,
       [&](int r, int k) { return *reinterpret_cast<const float4 *>(X + int64_t(min(m0 + r, g.M - 1)) * g.Kd + k); },
       [&](int r, int k) {
         return *reinterpret_cast<const float4 *>((r < 32 ? Wg : Wu) + int64_t(n0 + (r & 31)) * g.Kd + k);
       });
+  float *out = (f32_col() < 32 ? g.sums[0] : g.sums[1]) + int64_t(z) * g.M * g.N + n0 + (f32_col() & 31);
 #pragma unroll
-  for (int v = 0; v < 16; ++v) stage[f32_row(v)][f32_col()] = acc[v];
-  __syncthreads();
-  const int rr = threadIdx.x >> 2, cc = (threadIdx.x & 3) * 8, row = m0 + rr;
-  if (row >= g.M) return;
-  const int64_t at = int64_t(row) * g.N + n0 + cc;
-  float gv[8], uv[8], h[8];
-  Elem<float>::load8(&stage[rr][cc], gv);
-  Elem<float>::load8(&stage[rr][32 + cc], uv);
-  if (expand_enabled(g.ex) && any_slot(g.slot_pos, row, g.ex.K)) {
-    float dg[8], du[8];
-    Elem<float>::load8(g.term[0] + at, dg);
-    Elem<float>::load8(g.term[1] + at, du);
-#pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      gv[x] += dg[x];
-      uv[x] += du[x];
-    }
-  }
-#pragma unroll
-  for (int x = 0; x < 8; ++x) {
-    float slope;
-    h[x] = activate<kAct, false>(gv[x], slope) * uv[x];
-  }
-  Cols<float, 8>::store(static_cast<float *>(g.H) + at, h);
-  if (g.pre_gate) {
-    Cols<float, 8>::store(static_cast<float *>(g.pre_gate) + at, gv);
-    Cols<float, 8>::store(static_cast<float *>(g.pre_up) + at, uv);
+  for (int v = 0; v < 16; ++v) {
+    const int row = m0 + f32_row(v);
+    if (row < g.M) out[int64_t(row) * g.N] = acc[v];
   }
 }
 
@@ -1071,7 +1193,7 @@ struct GatedGradSrc {
 };
 
 // Split z of kSplit takes a part of the K tiles and leaves float32 sums for
-// gated_grad_x_sum_kernel; without kSplit dX itself, adapters' terms and all.
+// terms_kernel; without kSplit dX itself, adapters' terms and all.
 template <typename C, bool kSplit, bool kWide>
 __global__ __launch_bounds__(C::NT, 1) void gated_grad_x_tile_kernel(GatedGradXArgs g) {
   constexpr int SC = 64 + 4;                            // a wave stages 16 rows, and those of the adapters' term
@@ -1217,45 +1339,6 @@ __global__ __launch_bounds__(256) void gated_grad_x_f32_kernel(GatedGradXArgs g)
   }
 }
 
-// dX from the splits' sums, in order, and the masked adapters' term; 8 elements
-// a thread.
-template <typename E>
-__global__ __launch_bounds__(256) void gated_grad_x_sum_kernel(GatedGradXArgs g) {
-  const int64_t n = int64_t(g.M) * g.N, i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 8;
-  if (i >= n) return;
-  const int row = int(i / g.N);
-  const bool has = expand_enabled(g.ex) && any_slot(g.slot_pos, row, g.ex.K);
-  Raw8<float> term;
-  uint2 mw = make_uint2(0x01010101u, 0x01010101u);
-  if (has) {
-    term.load(g.term + i);
-    if (g.mask) mw = *reinterpret_cast<const uint2 *>(g.mask + i);
-  }
-  float v[8];
-  Elem<float>::load8(g.sums + i, v);
-  for (int z0 = 1; z0 < g.splits; z0 += 4) {
-    Raw8<float> pr[4];
-#pragma unroll
-    for (int z = 0; z < 4; ++z) pr[z].load(g.sums + int64_t(min(z0 + z, g.splits - 1)) * n + i);
-#pragma unroll
-    for (int z = 0; z < 4; ++z) {
-      if (z0 + z < g.splits) {
-        float o[8];
-        pr[z].to8(o);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] += o[c];
-      }
-    }
-  }
-  if (has) {
-    float l[8];
-    term.to8(l);
-#pragma unroll
-    for (int x = 0; x < 8; ++x) v[x] += float(((x < 4 ? mw.x : mw.y) >> (8 * (x & 3))) & 0xffu) * l[x];
-  }
-  Cols<E, 8>::store(static_cast<E *>(g.dX) + i, v);
-}
-
 template <typename E>
 void launch_act_grad(const void *dH, const void *pg, const void *pu, int act, void *dg, void *du, int64_t n,
                      hipStream_t s) {
@@ -1275,26 +1358,35 @@ void launch_act_grad(const void *dH, const void *pg, const void *pu, int act, vo
 
 namespace {
 
-template <typename C, bool kWide, bool kTerms>
+template <bool kWide>
 void launch_tiles(const GatedArgs &g, hipStream_t s) {
-  const int tiles = ((g.M + C::BM - 1) / C::BM) * ((g.N + C::BN / 2 - 1) / (C::BN / 2));
-  const dim3 grid(8 * unsigned((tiles + 7) / 8)), block(C::NT);
+  const int tiles = int(tile_count(kBig, g.M, 2 * int64_t(g.N)));
+  const dim3 grid(8 * unsigned((tiles + 7) / 8)), block(Big::NT);
   if (g.act == LORA_ACT_SILU)
-    hipLaunchKernelGGL((gated_tile_kernel<C, kWide, kTerms, LORA_ACT_SILU>), grid, block, 0, s, g);
+    hipLaunchKernelGGL((gated_tile_kernel<Big, kWide, LORA_ACT_SILU>), grid, block, 0, s, g);
   else if (g.act == LORA_ACT_GELU)
-    hipLaunchKernelGGL((gated_tile_kernel<C, kWide, kTerms, LORA_ACT_GELU>), grid, block, 0, s, g);
+    hipLaunchKernelGGL((gated_tile_kernel<Big, kWide, LORA_ACT_GELU>), grid, block, 0, s, g);
   else
-    hipLaunchKernelGGL((gated_tile_kernel<C, kWide, kTerms, LORA_ACT_GELU_TANH>), grid, block, 0, s, g);
+    hipLaunchKernelGGL((gated_tile_kernel<Big, kWide, LORA_ACT_GELU_TANH>), grid, block, 0, s, g);
+}
+
+template <typename C>
+void launch_base(const GatedArgs &g, const PlanArgs &pa, int64_t tiles, hipStream_t s) {
+  hipLaunchKernelGGL((gated_base_tile_kernel<C>), dim3(8 * unsigned((tiles + 7) / 8) + (pa.plan ? 1 : 0)), dim3(C::NT),
+                     0, s, g, pa);
 }
 
 // Rows anywhere in [M][Kd]: 32-bit byte offsets reach them all, or not.
 bool wide_rows(int64_t M, int64_t Kd) { return M * Kd >= (int64_t(1) << 31); }
 
-// Both projections' terms, slot by slot; sum: into out[0].
-hipError_t launch_terms(TermsArgs a, bool sum, int dtype, int M, hipStream_t s) {
-  const int64_t windows = (int64_t(M) * a.K + 15) / 16, cols = dtype == LORA_BF16 ? 128 : 64;
-  const dim3 grid(unsigned(windows * ((a.N + cols - 1) / cols)), sum ? 1 : 2), block(64);
+}  // namespace
+
+hipError_t launch_terms(TermsArgs a, bool sum, int dtype, hipStream_t s) {
+  const int64_t cols = (dtype == LORA_BF16 ? 128 : 64) / (sum ? 1 : 2), n_x = (a.N + cols - 1) / cols;
+  a.windows = int((int64_t(a.M) * a.K + 15) / 16);
   for (a.k = 0; a.k < a.K; ++a.k) {
+    const int64_t idle = a.k == 0 ? (a.M + 15) / 16 : 0;
+    const dim3 grid(unsigned((a.windows + idle) * n_x)), block(64);
     if (dtype == LORA_BF16) {
       if (sum) hipLaunchKernelGGL((terms_kernel<uint16_t, true>), grid, block, 0, s, a);
       else hipLaunchKernelGGL((terms_kernel<uint16_t, false>), grid, block, 0, s, a);
@@ -1308,31 +1400,48 @@ hipError_t launch_terms(TermsArgs a, bool sum, int dtype, int M, hipStream_t s) 
   return hipSuccess;
 }
 
-}  // namespace
+bool gated_whole(int64_t M, int64_t Kd, int dtype, bool fused) { return dtype == LORA_BF16 && (fused || wide_rows(M, Kd)); }
 
-hipError_t launch_gated(const GatedArgs &g, const TermsArgs &t, int dtype, hipStream_t s) {
+hipError_t launch_gated(const GatedArgs &g, hipStream_t s) {
+  if (wide_rows(g.M, g.Kd)) launch_tiles<true>(g, s);
+  else launch_tiles<false>(g, s);
+  return hipGetLastError();
+}
+
+// With at most `most` splits: 512 float32 workgroups, at least 4 K tiles of 64 each.
+int gated_base_splits(int M, int N, int Kd, int dtype, int most) {
+  if (dtype == LORA_BF16) return 1;
+  const int64_t tiles = int64_t((M + 63) / 64) * (N / 32);
+  int64_t n = 768 / tiles;
+  if (n > Kd / 256) n = Kd / 256;
+  if (n > most) n = most;
+  return n < 1 ? 1 : int(n);
+}
+
+PlanLaunch gated_base_plan(const GatedArgs &g, int dtype, const int32_t *ids, const float *gates, int T, int K,
+                           const PoolView &pool, int32_t *plan) {
+  static const int nt[] = {Big::NT, Tall::NT, Mid::NT, Small::NT};
+  static const size_t lds[] = {Big::LDS, Tall::LDS, Mid::LDS, Small::LDS};
+  const int i = pick_shape(g.M, 2 * int64_t(g.N), 1);
+  if (dtype == LORA_F32) return plan_setup(ids, gates, T, K, pool, plan, 256, sizeof(F32Tile));
+  return plan_setup(ids, gates, T, K, pool, plan, nt[i], lds[i]);
+}
+
+hipError_t launch_gated_base(const GatedArgs &g, int dtype, const PlanArgs *plan, hipStream_t s) {
+  PlanArgs pa{};
+  if (plan) pa = *plan;
   if (dtype == LORA_F32) {
-    const hipError_t e = launch_terms(t, false, dtype, g.M, s);
-    if (e != hipSuccess) return e;
-    const dim3 grid(unsigned(g.N / 32), unsigned((g.M + 63) / 64)), block(256);
-    if (g.act == LORA_ACT_SILU) hipLaunchKernelGGL(gated_f32_kernel<LORA_ACT_SILU>, grid, block, 0, s, g);
-    else if (g.act == LORA_ACT_GELU) hipLaunchKernelGGL(gated_f32_kernel<LORA_ACT_GELU>, grid, block, 0, s, g);
-    else hipLaunchKernelGGL(gated_f32_kernel<LORA_ACT_GELU_TANH>, grid, block, 0, s, g);
+    const int64_t wgs = int64_t(g.N / 32) * ((g.M + 63) / 64) * g.splits + (plan ? 1 : 0);
+    hipLaunchKernelGGL(gated_base_f32_kernel, dim3(unsigned(wgs)), dim3(256), 0, s, g, pa);
     return hipGetLastError();
   }
-  if (g.term[0]) {
-    const hipError_t e = launch_terms(t, false, dtype, g.M, s);
-    if (e != hipSuccess) return e;
-    switch (pick_shape(g.M, 2 * int64_t(g.N))) {
-      case kBig: launch_tiles<Big, false, true>(g, s); break;
-      case kTall: launch_tiles<Tall, false, true>(g, s); break;
-      case kMid: launch_tiles<Mid, false, true>(g, s); break;
-      default: launch_tiles<Small, false, true>(g, s);
-    }
-  } else if (wide_rows(g.M, g.Kd)) {
-    launch_tiles<Big, true, false>(g, s);
-  } else {
-    launch_tiles<Big, false, false>(g, s);
+  const int i = pick_shape(g.M, 2 * int64_t(g.N), 1);
+  const int64_t tiles = tile_count(i, g.M, 2 * int64_t(g.N));
+  switch (i) {
+    case kBig: launch_base<Big>(g, pa, tiles, s); break;
+    case kTall: launch_base<Tall>(g, pa, tiles, s); break;
+    case kMid: launch_base<Mid>(g, pa, tiles, s); break;
+    default: launch_base<Small>(g, pa, tiles, s);
   }
   return hipGetLastError();
 }
@@ -1405,20 +1514,16 @@ hipError_t launch_gated_grad_x(const GatedGradXArgs &g, const TermsArgs &t, int 
     else hipLaunchKernelGGL((gated_grad_x_tile_kernel<Big, false, false>), grid, block, 0, s, g);
     return hipGetLastError();
   }
-  hipError_t e = launch_terms(t, true, dtype, g.M, s);
-  if (e != hipSuccess) return e;
-  const unsigned sums = unsigned((int64_t(g.M) * g.N / 8 + 255) / 256);
   if (dtype == LORA_F32) {
     hipLaunchKernelGGL(gated_grad_x_f32_kernel, dim3(unsigned(g.N / 64), unsigned((g.M + 63) / 64), unsigned(g.splits)),
                        dim3(256), 0, s, g);
-    hipLaunchKernelGGL(gated_grad_x_sum_kernel<float>, dim3(sums), dim3(256), 0, s, g);
-    return hipGetLastError();
+  } else {
+    const int tiles = ((g.M + 127) / 128) * ((g.N + 255) / 256);
+    hipLaunchKernelGGL((gated_grad_x_tile_kernel<Mid, true, false>), dim3(8 * unsigned((tiles * g.splits + 7) / 8)),
+                       dim3(Mid::NT), 0, s, g);
   }
-  const int tiles = ((g.M + 127) / 128) * ((g.N + 255) / 256);
-  hipLaunchKernelGGL((gated_grad_x_tile_kernel<Mid, true, false>), dim3(8 * unsigned((tiles * g.splits + 7) / 8)),
-                     dim3(Mid::NT), 0, s, g);
-  hipLaunchKernelGGL(gated_grad_x_sum_kernel<uint16_t>, dim3(sums), dim3(256), 0, s, g);
-  return hipGetLastError();
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? launch_terms(t, true, dtype, s) : e;
 }
 
 }  // namespace lora

@@ -482,20 +482,27 @@ struct GatedArgs {
   const int4 *sdesc;
   float *u_out[2];
   int slot_stride;
-  // otherwise: where the adapters' terms go ahead of the tiles [M][N], or null
-  // (the tiles form them)
-  float *term[2];
+  // otherwise: where the base products go for terms_kernel [splits][M][N], or null
+  // (whole tiles)
+  float *sums[2];
 };
 
-// The adapters' terms of both projections (see terms_kernel).
+// The adapters' terms of both projections, and what they finish (see
+// terms_kernel): H of the gate's sums[0] and the up projection's sums[1], or dX of
+// sums[0].
 struct TermsArgs {
   const int32_t *hdr, *pair_tk, *pair_adapter, *u_off, *slot_pos;   // the plan's
   const int32_t *rank, *page_start, *page_ids;
   const float *U[2];
   int64_t u_cap;
   const void *pages[2];     // [n_pages][N]
-  float *out[2];            // [M][N]
-  int N, K, k;              // k: the slot, set by the launcher
+  float *sums[2];           // [splits][M][N]
+  int M, N, K, splits;
+  int act;
+  void *H, *pre_gate, *pre_up;
+  const uint8_t *mask;      // [M][N] or null
+  void *dX;
+  int k, windows;           // the slot, windows of 16 pairs: set by the launcher
 };
 
 // The gradient of X of the gated block: dX = dg.Wg^T + du.Wu^T + mask . (both
@@ -512,7 +519,6 @@ struct GatedGradXArgs {
   void *dX;                 // [M][N]
   int splits;               // 0: whole tiles
   float *sums;              // splits > 0: [splits][M][N]
-  float *term;              // splits > 0: [M][N], the adapters' terms
 };
 
 // ----------------------------------------------------------------- launchers
@@ -615,7 +621,15 @@ hipError_t launch_cross_entropy(const CrossEntropyArgs &a, int dtype, void *ws, 
 
 // More than decode: tiles of both projections, behind a launch of the adapters'
 // terms where a.term is given (float32 needs it).
-hipError_t launch_gated(const GatedArgs &a, const TermsArgs &t, int dtype, hipStream_t s);
+bool gated_whole(int64_t M, int64_t Kd, int dtype, bool fused);   // tiles that finish themselves
+hipError_t launch_gated(const GatedArgs &g, hipStream_t s);
+// Otherwise the base products, with the plan beside them if it fits (lds) ...
+int gated_base_splits(int M, int N, int Kd, int dtype, int most);
+PlanLaunch gated_base_plan(const GatedArgs &g, int dtype, const int32_t *ids, const float *gates, int T, int K,
+                           const PoolView &pool, int32_t *plan);
+hipError_t launch_gated_base(const GatedArgs &g, int dtype, const PlanArgs *plan, hipStream_t s);
+// ... and the rest; sum: dX
+hipError_t launch_terms(TermsArgs a, bool sum, int dtype, hipStream_t s);
 // Decode: both products' partials, the per-slot shrinks and the plan; or, with
 // a plan, both products' partials.  Then both sums, both expands, activation and
 // product.
