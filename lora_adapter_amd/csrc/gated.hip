@@ -529,6 +529,7 @@ template <typename E, bool kPair> struct TermTile;
 template <bool kPair> struct TermTile<uint16_t, kPair> {
   static constexpr int COLS = 128, NBLK = 8, NV = 4;
   uint4 v[NV];
+  float u[kPair ? 2 : 1][8];
   // kPair: rank rows lane / 8 + 8 (h % 2) of projection h / 2, columns 8 (lane % 8) ..;
   // else of projection p rows lane / 16 + 4 h, columns 8 (lane % 16) ..  (page id in
   // the lane of the row's number)
@@ -544,18 +545,19 @@ template <bool kPair> struct TermTile<uint16_t, kPair> {
       v[h] = *reinterpret_cast<const uint4 *>(from + int64_t(__shfl(id, row(h), 64)) * N + col);
     }
   }
-  // acc += U.rows; whether values that are not finite were left out
-  __device__ __forceinline__ bool add(char *lds, int nr, const float (&u)[kPair ? 2 : 1][8], f32x4_t (&acc)[NBLK]) {
-    const int lane = threadIdx.x, L = lane & 15;
+  // the loaded pass to LDS and to the A operand; whether values that are not
+  // finite were left out
+  bf16x8_t a[kPair ? 2 : 1];
+  __device__ __forceinline__ bool put(char *lds, int nr) {
+    const int lane = threadIdx.x;
     bool bad = false;
 #pragma unroll
     for (int h = 0; h < NV; ++h) {
-      const int j = row(h), piece = kPair ? (lane & 7) + 8 * (h >> 1) : L;
+      const int j = row(h), piece = kPair ? (lane & 7) + 8 * (h >> 1) : lane & 15;
       if (j >= nr) v[h] = make_uint4(0u, 0u, 0u, 0u);
       bad |= drop8(v[h]);
       *reinterpret_cast<uint4 *>(lds + j * 256 + (piece ^ ((j & 3) << 1)) * 16) = v[h];
     }
-    bf16x8_t a[kPair ? 2 : 1];
 #pragma unroll
     for (int p = 0; p < (kPair ? 2 : 1); ++p) {
       uint32_t w[4];
@@ -566,6 +568,11 @@ template <bool kPair> struct TermTile<uint16_t, kPair> {
       }
       __builtin_memcpy(&a[p], w, 16);
     }
+    return __ballot(bad) != 0;
+  }
+  // acc += U.rows of the pass that was put
+  __device__ __forceinline__ void mul(const char *lds, f32x4_t (&acc)[NBLK]) const {
+    const int lane = threadIdx.x, L = lane & 15;
     typedef __attribute__((address_space(3))) v4i16_t lds_v4;
     const int k = 8 * ((lane >> 4) & 1) + (L >> 2);
 #pragma unroll
@@ -579,13 +586,13 @@ template <bool kPair> struct TermTile<uint16_t, kPair> {
       __builtin_memcpy(reinterpret_cast<char *>(&f) + 8, &hi, 8);
       acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[kPair ? b / 4 : 0], f, acc[b], 0, 0, 0);
     }
-    return __ballot(bad) != 0;
   }
   static __device__ __forceinline__ bool finite(uint16_t v) { return (v & 0x7f80u) != 0x7f80u; }
 };
 template <bool kPair> struct TermTile<float, kPair> {
   static constexpr int COLS = 64, NBLK = 4, NV = 16;
-  float v[NV];
+  float v[NV], x[NV];
+  float u[kPair ? 2 : 1][8], a[kPair ? 2 : 1][4];
   // v[4 b + s]: rank row 4 s + lane / 16, column 16 b + lane % 16 (kPair: 16 (b % 2)
   // + lane % 16 of projection b / 2)
   __device__ __forceinline__ void load(const void *const (&pages)[2], int p, int id, int c0, int N) {
@@ -600,34 +607,38 @@ template <bool kPair> struct TermTile<float, kPair> {
       }
     }
   }
-  __device__ __forceinline__ bool add(char *, int nr, const float (&u)[kPair ? 2 : 1][8], f32x4_t (&acc)[NBLK]) {
+  __device__ __forceinline__ bool put(char *, int nr) {
     const int lane = threadIdx.x;
     bool bad = false;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       // u: ranks 8 (lane / 16 % 2) .. of row lane % 16; wanted: rank 4 s + lane / 16
-      float a[kPair ? 2 : 1];
 #pragma unroll
       for (int p = 0; p < (kPair ? 2 : 1); ++p) {
-        a[p] = 0.f;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const float x = __shfl(u[p][(4 * s + g) & 7], (lane & 15) + 16 * ((4 * s + g) >> 3), 64);
-          if ((lane >> 4) == g) a[p] = x;
+          const float t = __shfl(u[p][(4 * s + g) & 7], (lane & 15) + 16 * ((4 * s + g) >> 3), 64);
+          if ((lane >> 4) == g) a[p][s] = t;
         }
       }
 #pragma unroll
       for (int b = 0; b < NBLK; ++b) {
-        float x = v[4 * b + s];
-        if (4 * s + (lane >> 4) >= nr) x = 0.f;
-        if (!(x - x == 0.f)) {
+        float &o = x[4 * b + s];
+        o = 4 * s + (lane >> 4) < nr ? v[4 * b + s] : 0.f;
+        if (!(o - o == 0.f)) {
           bad = true;
-          x = 0.f;
+          o = 0.f;
         }
-        acc[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[kPair ? b / 2 : 0], x, acc[b], 0, 0, 0);
       }
     }
     return __ballot(bad) != 0;
+  }
+  __device__ __forceinline__ void mul(const char *, f32x4_t (&acc)[NBLK]) const {
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int b = 0; b < NBLK; ++b)
+        acc[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[kPair ? b / 2 : 0][s], x[4 * b + s], acc[b], 0, 0, 0);
   }
   static __device__ __forceinline__ bool finite(float v) { return v - v == 0.f; }
 };
@@ -761,7 +772,7 @@ __global__ __launch_bounds__(64) void terms_kernel(TermsArgs a) {
     const int nr = min(16, lane_of(rk, x.i) - x.jb);
     return a.page_ids[lane_of(pst, x.i) + x.jb + min(lane & 15, nr - 1)];
   };
-  auto fetch = [&](const Pass &x, int id, Tile &v, float (&u)[NP][8]) __attribute__((always_inline)) {
+  auto fetch = [&](const Pass &x, int id, Tile &v) __attribute__((always_inline)) {
     v.load(a.pages, x.p, id, c0, a.N);
     // U of row lane % 16, ranks 8 (lane / 16 % 2) .. + 7 of the pass
     const int r = lane & 15, j0 = 8 * ((lane >> 4) & 1), nr = min(16, lane_of(rk, x.i) - x.jb);
@@ -769,10 +780,10 @@ __global__ __launch_bounds__(64) void terms_kernel(TermsArgs a) {
     const int at = uo + x.jb + j0;
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-      load8_tail(((kPair ? p : x.p) ? a.U[1] : a.U[0]) + (mine ? at : 0), min(8, mine ? total - at : total), u[p]);
+      load8_tail(((kPair ? p : x.p) ? a.U[1] : a.U[0]) + (mine ? at : 0), min(8, mine ? total - at : total), v.u[p]);
 #pragma unroll
       for (int q = 0; q < 8; ++q)
-        if (!mine || j0 + q >= nr) u[p][q] = 0.f;
+        if (!mine || j0 + q >= nr) v.u[p][q] = 0.f;
     }
   };
 
@@ -780,10 +791,9 @@ __global__ __launch_bounds__(64) void terms_kernel(TermsArgs a) {
   c.p = 0;
   run_at(c, 0);
   n1 = c;
-  Tile v, w;
-  float u[NP][8], un[NP][8];
+  Tile v;
   int id = ids(c);
-  fetch(c, id, v, u);
+  fetch(c, id, v);
   after(n1);
   if (n1.i < m) id = ids(n1);
   f32x4_t acc[Tile::NBLK];
@@ -791,22 +801,16 @@ __global__ __launch_bounds__(64) void terms_kernel(TermsArgs a) {
   for (int b = 0; b < Tile::NBLK; ++b) acc[b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   bool dropped = false;
   while (true) {
-    Pass n2 = n1;
+    dropped |= v.put(lds, min(16, lane_of(rk, c.i) - c.jb));
     const bool more = n1.i < m;
-    if (more) {
-      fetch(n1, id, w, un);
-      after(n2);
-      if (n2.i < m) id = ids(n2);
-    }
-    dropped |= v.add(lds, min(16, lane_of(rk, c.i) - c.jb), u, acc);
-    if (!more) break;
     c = n1;
-    n1 = n2;
-    v = w;
-#pragma unroll
-    for (int p = 0; p < NP; ++p)
-#pragma unroll
-      for (int q = 0; q < 8; ++q) u[p][q] = un[p][q];
+    if (more) {
+      fetch(c, id, v);
+      after(n1);
+      if (n1.i < m) id = ids(n1);
+    }
+    v.mul(lds, acc);
+    if (!more) break;
   }
   // through LDS, to lanes that hold 8 columns of a row
   float *stage = reinterpret_cast<float *>(lds);
