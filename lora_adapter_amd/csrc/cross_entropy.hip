@@ -250,11 +250,14 @@ __global__ __launch_bounds__(256) void ce_logits_f32_kernel(CeArgs c) {
   const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
   if (m0 >= M) return;
   const float *X = static_cast<const float *>(c.a.X), *W = static_cast<const float *>(c.a.W);
+  // the thread's two rows of X: the list is read once, not with every chunk's loads
+  int64_t x_row[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    x_row[i] = int64_t(c.w.rows[c.row0 + min(m0 + int(threadIdx.x) / 8 + 32 * i, M - 1)]) * d;
   const f32x16_t acc = tile_f32<false>(
       lds, 0, d,
-      [&](int r, int k) {
-        return *reinterpret_cast<const float4 *>(X + int64_t(c.w.rows[c.row0 + min(m0 + r, M - 1)]) * d + k);
-      },
+      [&](int r, int k) { return *reinterpret_cast<const float4 *>(X + (r < 32 ? x_row[0] : x_row[1]) + k); },
       [&](int r, int k) { return *reinterpret_cast<const float4 *>(W + int64_t(min(n0 + r, c.a.V - 1)) * d + k); });
   const int lane = threadIdx.x & 63;
 #pragma unroll
@@ -497,9 +500,9 @@ CeWs ce_layout(char *ws, int T, int V, int d, int dtype, bool grad) {
   w.part = reinterpret_cast<float2 *>(take(size_t(w.block) * size_t(w.pieces) * 8));
   if (grad) {
     const int64_t kt = w.lde / 64;
-    auto split = [&](int64_t tiles, int64_t fill) {
+    auto split = [&](int64_t tiles, int64_t fill, int64_t least) {
       int64_t n = fill / (tiles > 0 ? tiles : 1);
-      if (n > kt / 8) n = kt / 8;
+      if (n > kt / least) n = kt / least;
       return int(n < 1 ? 1 : n);
     };
     if (dtype == LORA_BF16) {
@@ -508,7 +511,7 @@ CeWs ce_layout(char *ws, int T, int V, int d, int dtype, bool grad) {
       double least = 0.0;
       for (int i = kBig; i <= kMid; ++i) {
         const int64_t tiles = tile_count(i, w.block, d);
-        const int n = split(tiles, 256);
+        const int n = split(tiles, 256, 8);
         const double rounds = double((tiles * n + 255) / 256) * double((kt + n - 1) / n);
         const double us = 0.17 * kTileShapes[i].cost * rounds + 2.0 * n * double(w.block) * d * 4.0 / 4e6;
         if (i == kBig || us < least) {
@@ -518,7 +521,7 @@ CeWs ce_layout(char *ws, int T, int V, int d, int dtype, bool grad) {
         }
       }
     } else {
-      w.splits = split(int64_t((w.block + 63) / 64) * (d / 64), 512);
+      w.splits = split(int64_t((w.block + 63) / 64) * (d / 64), 768, 4);   // several on a CU
     }
     w.e = take(size_t(w.block) * size_t(w.lde) * e);
     w.acc = reinterpret_cast<float *>(take(size_t(w.splits) * size_t(w.block) * size_t(d) * 4));

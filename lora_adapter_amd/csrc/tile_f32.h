@@ -14,8 +14,9 @@ struct F32Tile {
 
 // A 32 x 32 block of the tile for each of four waves: rows 32 (wave / 2), columns
 // 32 (wave % 2), as the MFMA's registers hold them.  K in chunks of 32 through
-// LDS, one barrier a chunk, the loads two chunks ahead: with few workgroups on a
-// CU one chunk's 0.4 us of MFMAs does not cover a load.  a(r, k) and b(r, k) give
+// LDS, one barrier (of LDS alone: the loads stay in flight) a chunk, the loads two
+// chunks ahead: with few workgroups on a CU one chunk's 0.4 us of MFMAs does not
+// cover a load.  a(r, k) and b(r, k) give
 // 4 values along k; with kBAcross b(c, k) gives row k's columns c .. c + 3.
 // k_end - k_begin is a multiple of 32.
 template <bool kBAcross, typename FA, typename FB>
@@ -57,20 +58,39 @@ __device__ __forceinline__ f32x16_t tile_f32(F32Tile &t, int k_begin, int k_end,
   load(1, k_begin + kF32K);
   put(0, 0);
   load(0, k_begin + 2 * kF32K);
-  __syncthreads();
-  for (int k0 = k_begin; k0 < k_end; k0 += 2 * kF32K) {
+  lds_bar();
+  // the chunk from kc, in stage s
+  auto chunk = [&](int s, int kc) __attribute__((always_inline)) {
+    // operands of 4 MFMAs at a time, the next four's reads under them
+    float xa[2][4], xb[2][4];
+    auto read = [&](int g) __attribute__((always_inline)) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int kc = k0 + s * kF32K;
-      if (kc >= k_end) break;
+      for (int q = 0; q < 4; ++q) {
+        xa[g & 1][q] = t.a[s][ra][8 * g + 2 * q + kh];
+        xb[g & 1][q] = t.b[s][rb][8 * g + 2 * q + kh];
+      }
+    };
+    read(0);
 #pragma unroll
-      for (int k = 0; k < kF32K; k += 2)
-        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(t.a[s][ra][k + kh], t.b[s][rb][k + kh], acc, 0, 0, 0);
-      put(s ^ 1, s ^ 1);
-      load(s ^ 1, kc + 3 * kF32K);
-      __syncthreads();
+    for (int g = 0; g < kF32K / 8; ++g) {
+      if (g + 1 < kF32K / 8) read(g + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(xa[g & 1][q], xb[g & 1][q], acc, 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    put(s ^ 1, s ^ 1);
+    load(s ^ 1, kc + 3 * kF32K);
+    lds_bar();
+  };
+  // (both chunks of a turn without a branch between them: past one the compiler
+  // would wait for every load)
+  int k0 = k_begin;
+  for (; k0 + kF32K < k_end; k0 += 2 * kF32K) {
+    chunk(0, k0);
+    chunk(1, k0 + kF32K);
   }
+  if (k0 < k_end) chunk(0, k0);
   return acc;
 }
 
