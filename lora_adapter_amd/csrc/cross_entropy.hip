@@ -250,6 +250,16 @@ __global__ __launch_bounds__(256) void ce_logits_f32_kernel(CeArgs c) {
   const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
   if (m0 >= M) return;
   const float *X = static_cast<const float *>(c.a.X), *W = static_cast<const float *>(c.a.W);
+  // ref and target of the tile's rows, as in ce_logits_kernel
+  __shared__ float s_ref[64];
+  __shared__ int s_y[64];
+  float ref = 0.f;
+  int y = -1;
+  if (threadIdx.x < 64) {
+    const int t = c.w.rows[c.row0 + min(m0 + int(threadIdx.x), M - 1)];
+    ref = ref_of(c.w.ly[t]);
+    y = c.a.targets[t];
+  }
   // the thread's two rows of X: the list is read once, not with every chunk's loads
   int64_t x_row[2];
 #pragma unroll
@@ -262,15 +272,18 @@ __global__ __launch_bounds__(256) void ce_logits_f32_kernel(CeArgs c) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int v = 0; v < 16; ++v) stage[f32_row(v)][f32_col()] = acc[v];
+  if (threadIdx.x < 64) {
+    s_ref[threadIdx.x] = ref;
+    s_y[threadIdx.x] = y;
+  }
   __syncthreads();
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const int rr = q * 32 + (threadIdx.x >> 3), lr = m0 + rr;
     const bool ok = lr < M;
-    const int t = c.w.rows[c.row0 + (ok ? lr : M - 1)];
     float x[8];
     Elem<float>::load8(&stage[rr][(lane & 7) * 8], x);
-    ce_store8<float>(c, x, lr, ok, n0 + (lane & 7) * 8, ref_of(c.w.ly[t]), c.a.targets[t]);
+    ce_store8<float>(c, x, lr, ok, n0 + (lane & 7) * 8, s_ref[rr], s_y[rr]);
   }
 }
 
@@ -427,16 +440,17 @@ __global__ __launch_bounds__(C::NT, 1) void ce_grad_kernel(CeArgs c) {
 __global__ __launch_bounds__(256) void ce_grad_f32_kernel(CeArgs c) {
   __shared__ F32Tile lds;
   const int M = block_rows(c), d = c.a.d;
-  const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
+  // (rows last: those past the list's end would leave their CUs' places empty)
+  const int m0 = blockIdx.z * 64, n0 = blockIdx.x * 64, z = blockIdx.y;
   if (m0 >= M) return;
   const float *e = static_cast<const float *>(c.w.e), *W = static_cast<const float *>(c.a.W);
   int k0, nk;
-  split_range(int(c.w.lde / 64), c.w.splits, blockIdx.z, k0, nk);
+  split_range(int(c.w.lde / 64), c.w.splits, z, k0, nk);
   const f32x16_t acc = tile_f32<true>(
       lds, k0, k0 + nk * 64,
       [&](int r, int k) { return *reinterpret_cast<const float4 *>(e + int64_t(min(m0 + r, M - 1)) * c.w.lde + k); },
       [&](int n, int k) { return *reinterpret_cast<const float4 *>(W + int64_t(min(k, c.a.V - 1)) * d + n0 + n); });
-  float *out = c.w.acc + int64_t(blockIdx.z) * c.w.block * d;
+  float *out = c.w.acc + int64_t(z) * c.w.block * d;
 #pragma unroll
   for (int v = 0; v < 16; ++v) {
     const int lr = m0 + f32_row(v);
@@ -574,7 +588,7 @@ hipError_t run(CeArgs c, hipStream_t s) {
           default: launch_grad<Mid>(c, rows, s);
         }
       } else {
-        hipLaunchKernelGGL(ce_grad_f32_kernel, dim3(unsigned(d / 64), unsigned((rows + 63) / 64), unsigned(c.w.splits)),
+        hipLaunchKernelGGL(ce_grad_f32_kernel, dim3(unsigned(d / 64), unsigned(c.w.splits), unsigned((rows + 63) / 64)),
                            dim3(256), 0, s, c);
       }
       hipLaunchKernelGGL(ce_finish_kernel<E>, dim3(unsigned(rows), unsigned((d + 2047) / 2048)), dim3(256), 0, s, c);
