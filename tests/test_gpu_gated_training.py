@@ -1,0 +1,281 @@
+"""The gated block, the cross entropy, their gradients, the adapters' gradients,
+the clipping and the orthogonalised update in a row, as a training step runs
+them; and single calls at sizes that take each tile shape and at rows past
+32-bit byte offsets."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from lora_adapter_amd import binding as B
+from oracle import training as R
+from tests import test_gpu_cross_entropy as CE
+from tests import test_gpu_gated as G
+from tests.gpu_training_cases import ACTS, CODE, DT, EPS, HALF, Block, f64, near, workspace
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    B.lib()
+
+
+class Step:
+    """One training step of a block's two adapted projections under a frozen head."""
+
+    def __init__(self, T, K, d, F, V, dtype, act="silu", seed=0, lo=1, hi=16):
+        self.b = b = Block(T, K, d, F, dtype, seed=seed, mask=True, lo=lo, hi=hi)
+        rng = np.random.default_rng(seed + 1)
+        dev = lambda a, t: torch.from_numpy(np.ascontiguousarray(a)).cuda().to(t)
+        self.act, self.V = act, V
+        self.head = dev(rng.standard_normal((V, F)) * F ** -0.5, DT[dtype])
+        y = rng.integers(0, V, size=T).astype(np.int32)
+        y[::4] = -1                                           # a prompt's tokens
+        self.y, self.w = dev(y, torch.int32), dev(0.5 + rng.random(T), torch.float32)
+        self.Wt = [w.t().contiguous() for w in b.W]
+        new = lambda *s: torch.zeros(*s, dtype=DT[dtype], device="cuda")
+        z = lambda *s: torch.zeros(*s, device="cuda")
+        self.H, self.g, self.u, self.dH, self.dg, self.du = (new(T, F) for _ in range(6))
+        self.dX, self.loss = new(T, d), z(T)
+        self.grads = [(z(b.P, d), z(b.P, F)) for _ in range(2)]
+        self.clipped = [(z(b.P, d), z(b.P, F)) for _ in range(2)]
+        self.momentum = [(z(b.P, d), z(b.P, F)) for _ in range(2)]
+        self.adapters = torch.arange(b.N, dtype=torch.int32, device="cuda")
+        self.norm = z(b.N + 1)
+        self.layers = B.GradLayers([(p, *g, *c) for p, g, c in zip(b.pools, self.grads, self.clipped)])
+        code = CODE[dtype]
+        self.ws_loss = workspace(B.lora_cross_entropy_workspace_bytes(T, V, F, code))
+        self.ws_gated = workspace(B.lora_gated_grad_workspace_bytes(T, K, d, F, b.R, code))
+        self.ws_grad = workspace(B.lora_grad_workspace_bytes(T, K, b.N, d, F, b.R, code))
+        self.ws_clip = workspace(B.lora_clip_grad_workspace_bytes(self.layers, b.N, b.R))
+        self.ws_orth = workspace(B.lora_orthogonal_step_workspace_bytes(b.N, b.R, d, F))
+
+    def gradients(self):
+        b = self.b
+        b.forward(self.act, self.H, self.g, self.u)
+        B.lora_cross_entropy(self.H, self.head, CODE[b.dtype], b.T, self.V, b.F, self.y, self.w, 1.0, self.loss,
+                             self.dH, self.ws_loss)
+        B.lora_gated_grad(self.dH, self.g, self.u, ACTS[self.act], *self.Wt, b.d_mask, b.keep, b.T, b.K, b.d_gates,
+                          *b.pools, b.plan, b.R, self.dg, self.du, self.dX, self.ws_gated)
+        for p, dY in enumerate((self.dg, self.du)):
+            B.lora_grad(b.X, b.d_mask, b.keep, dY, b.T, b.K, b.d_gates, b.pools[p], b.plan, b.ws[p], *self.grads[p],
+                        b.R, self.ws_grad)
+
+    def update(self):
+        b = self.b
+        B.lora_clip_grad(self.layers, self.adapters, b.N, b.R, 0.05, False, self.norm, self.ws_clip)
+        for p in range(2):
+            f = [B.FactorUpdate(pages, c, m, None, 0.02) for pages, c, m in
+                 zip((b.A[p], b.Bp[p]), self.clipped[p], self.momentum[p])]
+            B.lora_orthogonal_step(b.pools[p], self.adapters, b.N, b.R, *f, 0.9, False, 3, B.NS_COEF, 1e-7,
+                                   self.ws_orth)
+
+    def run(self):
+        self.gradients()
+        self.update()
+
+    def state(self):
+        return [*self.b.A, *self.b.Bp] + [m for pair in self.momentum for m in pair]
+
+    def outputs(self):
+        return [self.H, self.loss, self.dH, self.dg, self.du, self.dX, self.norm] + self.state()
+
+
+@pytest.mark.parametrize("T,K,d,F,V,dtype", [(24, 2, 64, 128, 97, "f32"), (150, 1, 128, 192, 300, "bf16")])
+def test_each_stage_against_64_bits(T, K, d, F, V, dtype):
+    s = Step(T, K, d, F, V, dtype, seed=3)
+    s.run()
+    torch.cuda.synchronize()
+    b = Block(T, K, d, F, dtype, seed=3, mask=True, lo=1, hi=16)       # the pages before the update
+    for got, (ref, tol), what in zip((s.H, s.g, s.u), G.expected(b, s.act), "Hgu"):
+        near(got, ref, tol, what)
+    X, W, y, w = f64(s.H), f64(s.head), s.y.cpu().numpy(), f64(s.w)
+    loss, dH, P = R.cross_entropy(X, W, y, w, 1.0)
+    tl, tx = CE.tolerances(X, W, y, w, 1.0, loss, dH, P, HALF[dtype])
+    near(s.loss, loss, tl, "loss")
+    near(s.dH, dH, tx, "dH")
+    (rg, tg), (ru, tu) = G.grad_tolerances(b, s.act, f64(s.g), f64(s.u), f64(s.dH))
+    near(s.dg, rg, tg, "d_gate")
+    near(s.du, ru, tu, "d_up")
+    near(s.dX, *G.expected_dx(b, f64(s.dg), f64(s.du), s.Wt), "dX")
+    host = [dict(rank=b.rank, page_start=b.start, page_ids=b.page_ids, n_pages=b.P, A=f64(a), B=f64(c))
+            for a, c in s.grads]
+    norm, out, _ = R.clip(host, list(range(b.N)), b.R, float(np.float32(0.05)), False)
+    near(s.norm, norm, np.abs(norm) * (2.0 ** -24 + 2.0 ** -40) + 1e-45, "norm")
+    assert (norm[:-1] > 0.05).any()
+    for o, c in zip(out, s.clipped):
+        for f, got in zip("AB", c):
+            pages = b.page_ids
+            near(got[pages.astype(np.int64)], o[f][pages], np.abs(o[f][pages]) * (2.0 ** -23 + 2.0 ** -40) + 2.0 ** -149, f)
+
+
+@pytest.mark.parametrize("act", list(ACTS))
+def test_gradients_are_the_differences_of_the_loss(act):
+    """float32: the adapters' gradients of the whole chain along a direction against
+    central differences of a 64-bit loss."""
+    T, K, d, F, V = 24, 2, 64, 128, 97
+    s = Step(T, K, d, F, V, "f32", act, seed=5)
+    b = s.b
+    s.gradients()
+    torch.cuda.synchronize()
+    X, W, head, w, y = f64(b.X), [f64(x) for x in b.W], f64(s.head), f64(s.w), s.y.cpu().numpy()
+    m = b.mask.astype(np.float64)
+    A, Bp = [f64(a) for a in b.A], [f64(x) for x in b.Bp]
+    rng = np.random.default_rng(9)
+    VA, VB = ([rng.standard_normal(x.shape) for x in q] for q in (A, Bp))
+
+    def forward(h):
+        y_ = []
+        for p in range(2):
+            o = X @ W[p].T
+            for t, pages, c in b.slots(p):
+                o[t] += (c * ((A[p] + h * VA[p])[pages] @ (X[t] * m[t]))) @ (Bp[p] + h * VB[p])[pages]
+            y_.append(o)
+        H = R.activation(act, y_[0])[0] * y_[1]
+        return y_[0], y_[1], H, R.cross_entropy(H, head, y, w, 1.0)
+
+    h = 1e-4
+    diff = (forward(h)[3][0].sum() - forward(-h)[3][0].sum()) / (2 * h)
+    got = sum((f64(ga) * VA[p]).sum() + (f64(gb) * VB[p]).sum() for p, (ga, gb) in enumerate(s.grads))
+    # The same chain of absolute values: a stage's sums of n terms are off by n 2^-24 of it, what
+    # they hand on by as much again, and the probabilities by the logits' error, (F + 8) 2^-24
+    # times at most `most`.  Slopes are at most 1.13, |act(g)| at most |g|.
+    g, u, H, (_, _, P) = forward(0.0)
+    most = (np.abs(H) @ np.abs(head).T).max()
+    listed = y >= 0
+    dHa = np.where(listed, w, 0)[:, None] * (P @ np.abs(head) + np.abs(head)[np.maximum(y, 0)])
+    size = 0.0
+    for p, da in enumerate((1.13 * dHa * np.abs(u), dHa * np.abs(g))):
+        for t, pages, c in b.slots(p):
+            z = np.abs(X[t] * m[t])
+            size += abs(c) * ((np.abs(A[p][pages]) @ z) @ (np.abs(VB[p][pages]) @ da[t]))
+            size += abs(c) * ((np.abs(Bp[p][pages]) @ da[t]) @ (np.abs(VA[p][pages]) @ z))
+    n = 2 * (d + F + V + b.R + T + 64) * (1 + most)
+    assert abs(got - diff) < n * EPS * size + 1e-6 * abs(diff)
+    assert abs(diff) > 1e-4 * size                      # the direction says something
+
+
+@pytest.mark.parametrize("T,K,d,F,V,dtype", [(5, 1, 64, 192, 130, "bf16"), (200, 2, 128, 320, 513, "bf16"),
+                                             (70, 2, 128, 192, 200, "f32")])
+def test_captured_steps_are_the_eager_ones(T, K, d, F, V, dtype):
+    """Three steps of a captured graph, the program's own work between them,
+    against three eager ones, bit for bit."""
+    s = Step(T, K, d, F, V, dtype, seed=8)
+    start = [t.clone() for t in s.state()]
+    s.run()                                              # (libraries and kernels loaded)
+    want = []
+    for t, o in zip(s.state(), start):
+        t.copy_(o)
+    for _ in range(3):
+        s.run()
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in s.outputs()])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.run()
+    for t, o in zip(s.state(), start):
+        t.copy_(o)
+    other = Step(T, K, d, F, V, dtype, seed=21)
+    for i in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(s.outputs(), want[i])), i
+        other.run()
+    assert not torch.equal(want[0][7], want[1][7])       # the pages moved
+
+
+# ---------------------------------------------------------------- tile shapes
+
+# (forward of a block) tiles of 128 x 128, 128 x 256, 192 x 256 and 256 x 256
+@pytest.mark.parametrize("T,F", [(130, 64), (200, 8256), (300, 11008), (500, 11008)])
+@pytest.mark.parametrize("K,d", [(1, 64), (2, 192)])
+def test_forward_tile_shapes(T, F, K, d):
+    G.check_forward(Block(T, K, d, F, seed=T + K, lo=0, hi=20, mask=K == 2), "silu")
+
+
+@pytest.mark.parametrize("T,V", [(100, 200), (200, 16500), (300, 22020), (500, 22020)])
+def test_cross_entropy_tile_shapes(T, V):
+    CE.check(*CE.make(T, V, 64, "bf16", seed=T, ignored=0.1))
+
+
+# ---------------------------------------------------------------- rows past 2^32 bytes
+
+FAR_T, FAR_D = 33000, 65600
+FAR_ROWS = [0, 1, 127, 16384, 32639, 32735, 32736, 32800, 32998, 32999]
+
+
+def far_rows(n, dtype=torch.bfloat16):
+    """[FAR_T][n], zero but for FAR_ROWS."""
+    x = torch.zeros(FAR_T, n, dtype=dtype, device="cuda")
+    x[FAR_ROWS] = torch.randn(len(FAR_ROWS), n, generator=torch.Generator("cuda").manual_seed(n), device="cuda").to(dtype)
+    return x
+
+
+class FarBlock(Block):
+    """A block over FAR_ROWS; the oracle sees those alone."""
+
+    def __init__(self, d, F):
+        super().__init__(len(FAR_ROWS), 1, d, F, seed=2, lo=1, hi=8, empty=False)
+        ids = torch.full((FAR_T, 1), -1, dtype=torch.int32, device="cuda")
+        ids[FAR_ROWS] = self.d_ids
+        self.far_ids, self.far_gates = ids, torch.ones(FAR_T, 1, device="cuda")
+        self.plan = workspace(B.lora_plan_bytes(FAR_T, 1, self.N))
+
+
+def test_forward_of_rows_past_32_bits():
+    b = FarBlock(FAR_D, 64)
+    X = far_rows(FAR_D)
+    b.X.copy_(X[FAR_ROWS])
+    H, g, u = (torch.full((FAR_T, 64), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    ws = [workspace(B.lora_apply_workspace_bytes(FAR_T, 1, FAR_D, 64, b.R, B.LORA_BF16)) for _ in range(2)]
+    B.lora_gated_forward(b.far_ids, b.far_gates, FAR_T, 1, X, *b.W, 0, H, g, u, None, 1.0, *b.pools, b.plan, *ws)
+    torch.cuda.synchronize()
+    for got, (ref, tol), what in zip((H, g, u), G.expected(b, "silu"), "Hgu"):
+        near(got[FAR_ROWS], ref, tol, what)
+        rest = torch.ones(FAR_T, dtype=torch.bool, device="cuda")
+        rest[FAR_ROWS] = False
+        assert not bool(got[rest].any())
+
+
+def test_gradient_of_rows_past_32_bits():
+    b = FarBlock(64, FAR_D)
+    dH, g, u = far_rows(FAR_D), far_rows(FAR_D), far_rows(FAR_D)
+    g.mul_(0.5)
+    W = [w.t().contiguous() for w in b.W]
+    dg, du = torch.empty_like(dH), torch.empty_like(dH)
+    dX = torch.full((FAR_T, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = workspace(B.lora_gated_grad_workspace_bytes(FAR_T, 1, 64, FAR_D, b.R, B.LORA_BF16))
+    B.lora_plan(b.far_ids, b.far_gates, FAR_T, 1, b.pools[0], b.plan)
+    B.lora_gated_grad(dH, g, u, 0, *W, None, 1.0, FAR_T, 1, b.far_gates, *b.pools, b.plan, b.R, dg, du, dX, ws)
+    torch.cuda.synchronize()
+    b.dH.copy_(dH[FAR_ROWS])
+    (rg, tg), (ru, tu) = G.grad_tolerances(b, "silu", f64(g[FAR_ROWS]), f64(u[FAR_ROWS]), f64(dH[FAR_ROWS]))
+    near(dg[FAR_ROWS], rg, tg, "d_gate")
+    near(du[FAR_ROWS], ru, tu, "d_up")
+    near(dX[FAR_ROWS], *G.expected_dx(b, f64(dg[FAR_ROWS]), f64(du[FAR_ROWS]), W), "dX")
+    rest = torch.ones(FAR_T, dtype=torch.bool, device="cuda")
+    rest[FAR_ROWS] = False
+    assert not bool(dX[rest].any())
+
+
+def test_cross_entropy_of_rows_past_32_bits():
+    V = 130
+    X = far_rows(FAR_D)
+    W = torch.randn(V, FAR_D, generator=torch.Generator("cuda").manual_seed(4), device="cuda").mul_(FAR_D ** -0.5).bfloat16()
+    y = torch.full((FAR_T,), -1, dtype=torch.int32, device="cuda")
+    y[FAR_ROWS] = torch.arange(len(FAR_ROWS), dtype=torch.int32, device="cuda") * 13
+    loss, dX = torch.full((FAR_T,), 7.0, device="cuda"), torch.full_like(X, 7.0)
+    ws = workspace(B.lora_cross_entropy_workspace_bytes(FAR_T, V, FAR_D, B.LORA_BF16))
+    B.lora_cross_entropy(X, W, B.LORA_BF16, FAR_T, V, FAR_D, y, None, 1.0, loss, dX, ws)
+    torch.cuda.synchronize()
+    Xd, Wd, yd = f64(X[FAR_ROWS]), f64(W), y[FAR_ROWS].cpu().numpy()
+    ref, rx, P = R.cross_entropy(Xd, Wd, yd, None, 1.0)
+    tl, tx = CE.tolerances(Xd, Wd, yd, None, 1.0, ref, rx, P, HALF["bf16"])
+    near(loss[FAR_ROWS], ref, tl, "loss")
+    near(dX[FAR_ROWS], rx, tx, "dX")
+    rest = torch.ones(FAR_T, dtype=torch.bool, device="cuda")
+    rest[FAR_ROWS] = False
+    assert not bool(loss[rest].any()) and not bool(dX[rest].any())
