@@ -662,8 +662,10 @@ int32_t lora_orthogonal_step(const lora_pool_desc *pool, const int32_t *adapters
  *   ws_gate, ws_up    a workspace of lora_apply_workspace_bytes each; each
  *                projection's U stays in its own, where lora_grad finds it.
  * Other arguments as for lora_apply.  No output may be another buffer of the
- * call.  lora_gated_forward = lora_plan then lora_gated_apply, as one call
- * with fewer launches (plan, U, H, pre_gate and pre_up are the same bit for bit).
+ * call; X, weights, outputs and workspaces are 16-byte aligned; widths up to
+ * 2^22.  lora_gated_forward = lora_plan then lora_gated_apply, as one call with
+ * fewer launches: up to some thousand tokens the plan is built beside the base
+ * products (plan, U, H, pre_gate and pre_up are the same bit for bit).
  * Errors: those of lora_apply and lora_forward. */
 #define LORA_ACT_SILU 0
 #define LORA_ACT_GELU 1
@@ -693,6 +695,7 @@ int32_t lora_gated_forward(const int32_t *ids, const float *gates, int32_t T, in
  *   forward; max_rank bounds every used adapter's rank (LORA_DEVERR_CAPACITY if
  *   not); d_gate, d_up [T][d_out] dtype, may be pre_gate, pre_up (in place); dX
  *   [T][d_in] dtype, or NULL.  ws >= lora_gated_grad_workspace_bytes(...).
+ *   16-byte aligned, keep_mask 8; widths up to 2^22.
  * Errors: INVALID_ARG, UNSUPPORTED, CAPACITY, DEVICE. */
 size_t lora_gated_grad_workspace_bytes(int32_t T, int32_t K, int32_t d_in, int32_t d_out,
                                        int32_t max_rank, int32_t dtype);
@@ -721,7 +724,7 @@ int32_t lora_gated_grad(const void *dH, const void *pre_gate, const void *pre_up
  *   ws >= lora_cross_entropy_workspace_bytes(..., dX != NULL): tokens are taken
  *   in blocks whose exponentials (dtype) take at most 512 MiB.
  * A logit of +infinity or NaN makes its token's loss and gradient NaN, and no
- * other token's.  At most 2^20 tokens and V of 2^22 (UNSUPPORTED).  Results are
+ * other token's.  At most 2^20 tokens, V and d of 2^22 (UNSUPPORTED).  Results are
  * deterministic.
  * Errors: INVALID_ARG (null, alignment, an output that is an input, sizes),
  * UNSUPPORTED, CAPACITY, DEVICE. */

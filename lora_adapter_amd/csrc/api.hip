@@ -1093,6 +1093,12 @@ bool outputs_apart(const void *const *out, int n_out, const void *const *in, int
   return true;
 }
 
+bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+bool aligned16(const void *p) { return aligned(p, 16); }
+
+// Rows of a weight tile, up to 256, are reached by 32-bit byte offsets.
+constexpr int32_t kMaxWidth = 1 << 22;
+
 struct GatedCall {
   ApplyWs w[2];
   GemmArgs g[2];
@@ -1121,10 +1127,15 @@ int32_t gated_args(const void *X, const void *W_gate_t, const void *W_up_t, int3
   if (st != LORA_OK) return st;
   if ((st = check_pair(gate, up)) != LORA_OK) return st;
   if (!plan || !activation_ok(activation) || !pre_gate != !pre_up) return LORA_ERR_INVALID_ARG;
+  if (gate->d_in > kMaxWidth || gate->d_out > kMaxWidth) return LORA_ERR_UNSUPPORTED;
   if (T == 0) return LORA_OK;
   if (!X || !W_gate_t || !W_up_t || !H || !gates || !ws_gate || !ws_up) return LORA_ERR_INVALID_ARG;
   const void *out[] = {H, pre_gate, pre_up, ws_gate, ws_up}, *in[] = {X, W_gate_t, W_up_t, plan};
   if (!outputs_apart(out, 5, in, 4)) return LORA_ERR_INVALID_ARG;
+  for (const void *p : {X, W_gate_t, W_up_t, static_cast<const void *>(H), static_cast<const void *>(pre_gate),
+                        static_cast<const void *>(pre_up), static_cast<const void *>(ws_gate),
+                        static_cast<const void *>(ws_up)})
+    if (!aligned16(p)) return LORA_ERR_INVALID_ARG;
   if ((st = base_args(X, W_gate_t, H, T, K, gate, plan, ws_gate, ws_gate_bytes, c.cfg, c.g[0])) != LORA_OK ||
       (st = base_args(X, W_up_t, H, T, K, up, plan, ws_up, ws_up_bytes, c.cfg, c.g[1])) != LORA_OK)
     return st;
@@ -1267,6 +1278,7 @@ size_t lora_gated_grad_workspace_bytes(int32_t T, int32_t K, int32_t d_in, int32
                                        int32_t max_rank, int32_t dtype) {
   if (check_batch(T, K) != LORA_OK || !dims_ok(d_in) || !dims_ok(d_out)) return 0;
   if (max_rank < 1 || max_rank > LORA_MAX_RANK || (dtype != LORA_F32 && dtype != LORA_BF16)) return 0;
+  if (d_in > kMaxWidth || d_out > kMaxWidth) return 0;
   return gated_grad_ws(T, K, d_in, d_out, max_rank, dtype).total;
 }
 
@@ -1281,11 +1293,16 @@ int32_t lora_gated_grad(const void *dH, const void *pre_gate, const void *pre_up
   if ((st = check_pair(gate, up)) != LORA_OK) return st;
   if (!plan || !activation_ok(activation) || max_rank < 1 || max_rank > LORA_MAX_RANK)
     return LORA_ERR_INVALID_ARG;
+  if (gate->d_in > kMaxWidth || gate->d_out > kMaxWidth) return LORA_ERR_UNSUPPORTED;
   if (T == 0) return LORA_OK;
   if (!dH || !pre_gate || !pre_up || !d_gate || !d_up) return LORA_ERR_INVALID_ARG;
   const void *out[] = {d_gate, d_up, dX, ws}, *in[] = {dH, W_gate, W_up, plan, keep_mask};
   if (!outputs_apart(out, 4, in, 5) || d_gate == pre_up || d_up == pre_gate) return LORA_ERR_INVALID_ARG;
   if (dX && (!W_gate || !W_up || !gates || !ws || dX == pre_gate || dX == pre_up)) return LORA_ERR_INVALID_ARG;
+  for (const void *p : {dH, pre_gate, pre_up, W_gate, W_up, static_cast<const void *>(d_gate),
+                        static_cast<const void *>(d_up), static_cast<const void *>(dX), static_cast<const void *>(ws)})
+    if (!aligned16(p)) return LORA_ERR_INVALID_ARG;
+  if (!aligned(keep_mask, 8)) return LORA_ERR_INVALID_ARG;
   const int32_t F = gate->d_out, d = gate->d_in, dtype = gate->dtype;
   const GatedGradWs w = gated_grad_ws(T, K, d, F, max_rank, dtype);
   if (dX && ws_bytes < w.total) return LORA_ERR_CAPACITY;
@@ -1339,11 +1356,9 @@ int32_t lora_gated_grad(const void *dH, const void *pre_gate, const void *pre_up
 
 namespace {
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
 int32_t check_entropy(int32_t T, int32_t V, int32_t d, int32_t dtype) {
   if (T < 0 || V < 1 || (dtype != LORA_F32 && dtype != LORA_BF16)) return LORA_ERR_INVALID_ARG;
-  if (T > kMaxPairs || V > (1 << 22) || !dims_ok(d)) return LORA_ERR_UNSUPPORTED;
+  if (T > kMaxPairs || V > (1 << 22) || !dims_ok(d) || d > kMaxWidth) return LORA_ERR_UNSUPPORTED;
   return LORA_OK;
 }
 

@@ -705,6 +705,8 @@ __device__ __forceinline__ void finish8(const TermsArgs &a, int64_t i, bool firs
   }
 }
 
+constexpr int kWindowRows = 32768;                      // of the grid's second dimension
+
 template <typename E, bool kSum>
 __global__ __launch_bounds__(64) void terms_kernel(TermsArgs a) {
   constexpr bool kPair = !kSum;
@@ -715,8 +717,7 @@ __global__ __launch_bounds__(64) void terms_kernel(TermsArgs a) {
   __shared__ __attribute__((aligned(16))) char lds[16 * SC * 4];
   static_assert(sizeof(lds) >= 4096, "a pass's page rows");
   const int P = a.hdr[LORA_PH_PAIRS], total = a.hdr[LORA_PH_RPAIRS], lane = threadIdx.x;
-  const int n_x = (a.N + COLS - 1) / COLS, window = int(blockIdx.x / unsigned(n_x));
-  const int c0 = int(blockIdx.x % unsigned(n_x)) * COLS;
+  const int window = int(blockIdx.z) * kWindowRows + int(blockIdx.y), c0 = int(blockIdx.x) * COLS;
   const bool lora_on = int64_t(total) <= a.u_cap;
   if (window >= a.windows) {
     // tokens without an active slot
@@ -1389,8 +1390,9 @@ hipError_t launch_terms(TermsArgs a, bool sum, int dtype, hipStream_t s) {
   const int64_t cols = (dtype == LORA_BF16 ? 128 : 64) / (sum ? 1 : 2), n_x = (a.N + cols - 1) / cols;
   a.windows = int((int64_t(a.M) * a.K + 15) / 16);
   for (a.k = 0; a.k < a.K; ++a.k) {
-    const int64_t idle = a.k == 0 ? (a.M + 15) / 16 : 0;
-    const dim3 grid(unsigned((a.windows + idle) * n_x)), block(64);
+    const int rows = a.windows + (a.k == 0 ? (a.M + 15) / 16 : 0);
+    const dim3 grid(unsigned(n_x), unsigned(rows < kWindowRows ? rows : kWindowRows),
+                    unsigned((rows + kWindowRows - 1) / kWindowRows)), block(64);
     if (dtype == LORA_BF16) {
       if (sum) hipLaunchKernelGGL((terms_kernel<uint16_t, true>), grid, block, 0, s, a);
       else hipLaunchKernelGGL((terms_kernel<uint16_t, false>), grid, block, 0, s, a);

@@ -196,9 +196,33 @@ def test_forward_tile_shapes(T, F, K, d):
     G.check_forward(Block(T, K, d, F, seed=T + K, lo=0, hi=20, mask=K == 2), "silu")
 
 
+def test_many_float32_tokens():
+    """More windows of 16 pairs than one dimension of a grid holds."""
+    T, d, F = 600000, 64, 64
+    b = Block(1000, 1, d, F, "f32", seed=12, mask=True)
+    n = T // b.T
+    ids, gates, mask = b.d_ids.repeat(n, 1), b.d_gates.repeat(n, 1), b.d_mask.repeat(n, 1)
+    X = b.X.repeat(n, 1)
+    plan = workspace(B.lora_plan_bytes(T, 1, b.N))
+    ws = [workspace(B.lora_apply_workspace_bytes(T, 1, d, F, b.R, B.LORA_F32)) for _ in range(2)]
+    H = torch.full((T, F), 7.0, device="cuda")
+    B.lora_gated_forward(ids, gates, T, 1, X, *b.W, 0, H, None, None, mask, b.keep, *b.pools, plan, *ws)
+    torch.cuda.synchronize()
+    ref, tol = G.expected(b, "silu")[0]
+    for i in (0, n // 2, n - 1):
+        near(H[i * b.T:(i + 1) * b.T], ref, tol, i)
+    assert torch.equal(H.view(n, b.T, F)[0].expand(n, -1, -1).reshape(T, F), H)
+
+
 @pytest.mark.parametrize("T,V", [(100, 200), (200, 16500), (300, 22020), (500, 22020)])
 def test_cross_entropy_tile_shapes(T, V):
     CE.check(*CE.make(T, V, 64, "bf16", seed=T, ignored=0.1))
+
+
+@pytest.mark.parametrize("T,N,dtype", [(200, 6000, "bf16"), (150, 1500, "f32")])
+def test_forward_of_more_adapters_than_fit_beside_the_product(T, N, dtype):
+    """The plan's tables of so many adapters do not fit the product's LDS: a launch of its own."""
+    G.check_forward(Block(T, 2, 64, 192, dtype, N=N, lo=0, hi=3, seed=N), "gelu")
 
 
 # ---------------------------------------------------------------- rows past 2^32 bytes

@@ -266,3 +266,40 @@ def test_binding_checks_shapes(B):
     layers = B.GradLayers([(pool, f(4, 128), f(4, 192))])
     with pytest.raises(ValueError):
         B.lora_clip_grad(layers, i, 2, 16, 1.0, False, f(2), ws, 0)
+
+
+def test_gated_alignment_and_widths(B):
+    """16 bytes for what is read and written by vectors, 8 for the mask; offsets of a
+    weight tile's rows fit 32 bits."""
+    L, r = B.lib(), ctypes.byref
+    INV, UNS = B.LORA_ERR_INVALID_ARG, B.LORA_ERR_UNSUPPORTED
+    names = ("X", "Wg", "Wu", "H", "pg", "pu", "wg", "wu")
+
+    def forward(pool=None, **off):
+        a = {n: (i + 1 << 16) + off.get(n, 0) for i, n in enumerate(names)}
+        p = pool or _pool(B)
+        return L.lora_gated_apply(a["X"], a["Wg"], a["Wu"], 0, a["H"], a["pg"], a["pu"], 4, 1, 1 << 12, None, 1.0, r(p),
+                                  r(p), 1 << 13, a["wg"], 0, a["wu"], 0, None)
+
+    for n in names:
+        for by in (2, 4, 8):
+            assert forward(**{n: by}) == INV, (n, by)
+    assert forward() == B.LORA_ERR_CAPACITY                          # all else in order
+    names2 = ("dH", "pg", "pu", "Wg", "Wu", "dg", "du", "dX", "ws", "mask")
+
+    def grad(pool=None, **off):
+        a = {n: (i + 1 << 16) + off.get(n, 0) for i, n in enumerate(names2)}
+        p = pool or _pool(B)
+        return L.lora_gated_grad(a["dH"], a["pg"], a["pu"], 0, a["Wg"], a["Wu"], a["mask"], 1.0, 4, 1, 1 << 12, r(p),
+                                 r(p), 1 << 13, 16, a["dg"], a["du"], a["dX"], a["ws"], 0, None)
+
+    for n in names2:
+        for by in (2, 4) if n == "mask" else (2, 4, 8):
+            assert grad(**{n: by}) == INV, (n, by)
+    assert grad() == B.LORA_ERR_CAPACITY
+    for kw in (dict(d_in=(1 << 22) + 64), dict(d_out=(1 << 22) + 64)):
+        assert forward(_pool(B, **kw)) == UNS and grad(_pool(B, **kw)) == UNS
+        w = dict(d_in=128, d_out=192)
+        w.update(kw)
+        assert B.lora_gated_grad_workspace_bytes(4, 1, w["d_in"], w["d_out"], 16, B.LORA_BF16) == 0
+    assert B.lora_cross_entropy_workspace_bytes(4, 100, (1 << 22) + 64, B.LORA_BF16) == 0
