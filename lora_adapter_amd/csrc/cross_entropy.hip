@@ -68,7 +68,7 @@ __device__ __forceinline__ bool ce_listed(const CeArgs &c, int t) {
 // Workgroup 0: the list of tokens that have a target and a weight.  Beside it,
 // one wave per token: the target's logit of a listed one (float64 sums: both
 // results hang on it), the zero loss and gradient of another.  (As launches one
-// after the other 48 us at 8192 tokens, as one 29.)
+// after the other 48 us at 8192 tokens, as one 31.)
 template <typename E>
 __global__ __launch_bounds__(1024) void ce_rows_kernel(CeArgs c) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, T = c.a.T;
@@ -194,12 +194,12 @@ __global__ __launch_bounds__(C::NT, 1) void ce_logits_kernel(CeArgs c) {
 #pragma unroll
   for (int i = 0; i < C::A_INS; ++i) {
     const int row = (wave * C::A_INS + i) * 8 + lrow;
-    src.ao.set(i, int64_t(c.w.rows[c.row0 + min(m0 + row, M - 1)]) * d + tswz(row, lane & 7) * 8);
+    src.ao.set(i, int64_t(c.w.rows[c.row0 + min(m0 + row, M - 1)]) * d + fswz(row, lane & 7) * 8);
   }
 #pragma unroll
   for (int i = 0; i < C::B_INS; ++i) {
     const int row = (wave * C::B_INS + i) * 8 + lrow;
-    src.bo[i] = (uint32_t(min(row, c.a.V - 1 - n0)) * uint32_t(d) + tswz(row, lane & 7) * 8) * 2;
+    src.bo[i] = (uint32_t(min(row, c.a.V - 1 - n0)) * uint32_t(d) + fswz(row, lane & 7) * 8) * 2;
   }
   // ref and target of the tile's rows, fetched under the K loop: as loads of
   // the epilogue they were a third of it
@@ -412,7 +412,7 @@ __global__ __launch_bounds__(C::NT, 1) void ce_grad_kernel(CeArgs c) {
 #pragma unroll
   for (int i = 0; i < C::A_INS; ++i) {
     const int row = (wave * C::A_INS + i) * 8 + (lane >> 3);
-    src.ao[i] = (uint32_t(min(row, M - 1 - m0)) * uint32_t(c.w.lde) + tswz(row, lane & 7) * 8) * 2;
+    src.ao[i] = (uint32_t(min(row, M - 1 - m0)) * uint32_t(c.w.lde) + fswz(row, lane & 7) * 8) * 2;
   }
 #pragma unroll
   for (int i = 0; i < C::B_INS; ++i) {

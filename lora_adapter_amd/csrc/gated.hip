@@ -9,9 +9,10 @@
 // holds 128 rows of each weight, 32 and 32 for each wave, so that a lane ends
 // up with g and u of the same element and X is read once.  The adapters' terms
 // join the accumulators as MFMA passes (gate and up in one pass), then
-// activation, product and the one rounding happen on the way out.  Smaller
-// batches take the split products of the single projections and an epilogue
-// that finishes both.
+// activation, product and the one rounding happen on the way out.  Batches of
+// some hundred tokens leave both base products in memory, and the launch of the
+// adapters' terms finishes them; up to 128 tokens take the split products of the
+// single projections and an epilogue that finishes both.
 #include "decode_tile.h"
 #include "plan_build.h"
 #include "shrink_units.h"
@@ -521,8 +522,9 @@ __device__ __forceinline__ bool any_slot(const int32_t *slot_pos, int t, int K) 
 // those without an active slot.
 // The products are MFMAs with the rows of other adapters zero, so that all runs
 // of a window share accumulators: with a branch for each row and rank row, or
-// every product on the vector units, the same launch took 270 us and 73, now
-// NEWTERMS.
+// every product on the vector units, that launch took 270 us and 73 without
+// finishing anything, as MFMAs 45; with its epilogue it takes 49 (57 with the next
+// pass's rows in registers instead of LDS: 138 of them instead of 99).
 // bf16 pages: U as hi | lo against the rows twice, as in add_segs; float32 pages:
 // v_mfma_f32_16x16x4_f32.
 template <typename E, bool kPair> struct TermTile;
@@ -873,13 +875,13 @@ struct GatedSrc {
 #pragma unroll
     for (int i = 0; i < C::A_INS; ++i) {
       const int row = (wave * C::A_INS + i) * 8 + (lane >> 3);
-      ao.set(i, int64_t(row_of(row)) * g.Kd + tswz(row, lane & 7) * 8);
+      ao.set(i, int64_t(row_of(row)) * g.Kd + fswz(row, lane & 7) * 8);
     }
 #pragma unroll
     for (int i = 0; i < C::B_INS; ++i) {
       const int row = (wave * C::B_INS + i) * 8 + (lane >> 3);
       const int of = (row >> 6) * 32 + (row & 31);        // of its weight
-      bo[i] = (uint32_t(min(of, g.N - 1 - n0)) * uint32_t(g.Kd) + tswz(row, lane & 7) * 8) * 2;
+      bo[i] = (uint32_t(min(of, g.N - 1 - n0)) * uint32_t(g.Kd) + fswz(row, lane & 7) * 8) * 2;
     }
   }
   __device__ __forceinline__ void copy(uint32_t lds, int kt, int i) const {
@@ -1037,8 +1039,9 @@ __global__ __launch_bounds__(256) void gated_decode_kernel(GemmArgs g0, GemmArgs
 // Decode epilogue: a workgroup per row and 512 columns, its waves the two
 // projections by halves of the pieces and of each slot's rank rows, joined
 // through LDS.  A row's rank rows come one batch after another, so that the
-// launch lasts as long as its longest chain: one wave for all four took 39 us
-// at 48 tokens of two adapters of ranks 8 .. 64 (4096 -> 11008).
+// launch lasts as long as its longest chain: at 48 tokens of two adapters of ranks
+// 8 .. 64 (4096 -> 11008) one wave for all four took 39 us, these 32, eight waves by
+// quarters 35; pages and pieces are some 140 MB.
 template <int kAct>
 __global__ __launch_bounds__(256) void gated_decode_epilogue_kernel(GatedArgs g) {
   __shared__ __attribute__((aligned(16))) float part[4][512];
@@ -1234,12 +1237,12 @@ __global__ __launch_bounds__(C::NT, 1) void gated_grad_x_tile_kernel(GatedGradXA
 #pragma unroll
   for (int i = 0; i < C::A_INS; ++i) {
     const int row = (wave * C::A_INS + i) * 8 + (lane >> 3);
-    src.ao.set(i, int64_t(rows[min(row, nrows - 1)]) * g.Kd + tswz(row, lane & 7) * 8);
+    src.ao.set(i, int64_t(rows[min(row, nrows - 1)]) * g.Kd + fswz(row, lane & 7) * 8);
   }
 #pragma unroll
   for (int i = 0; i < C::B_INS; ++i) {
     const int row = (wave * C::B_INS + i) * 8 + (lane >> 3);
-    src.bo[i] = (uint32_t(min(row, g.N - 1 - n0)) * uint32_t(g.Kd) + tswz(row, lane & 7) * 8) * 2;
+    src.bo[i] = (uint32_t(min(row, g.N - 1 - n0)) * uint32_t(g.Kd) + fswz(row, lane & 7) * 8) * 2;
   }
   const int4 sd0 = kSplit ? make_int4(-1, 0, 0, 0) : row_desc(g.ex, rows, nrows, 0);
   f32x4_t acc[C::TM][C::TN];
@@ -1500,7 +1503,9 @@ int gated_grad_x_splits(int T, int d_in, int d_out, int dtype) {
   int64_t tiles, want;
   if (dtype == LORA_BF16) {
     if (int64_t((T + 255) / 256) * ((d_in + 255) / 256) >= 192 || wide_rows(T, d_out)) return 0;
-    tiles = int64_t((T + 127) / 128) * ((d_in + 255) / 256);       // one on a CU
+    // 128 x 256, one on a CU: a K tile takes 0.97 us, of 192 x 256 1.5 and of 256 x 256
+    // 1.7, and smaller tiles divide the card better (600 tokens, 2240 wide: 41 us)
+    tiles = int64_t((T + 127) / 128) * ((d_in + 255) / 256);
     want = 256;
   } else {
     tiles = int64_t((T + 63) / 64) * (d_in / 64);                  // several on a CU
