@@ -28,6 +28,7 @@ namespace {
 
 constexpr int kSub = 64;                               // columns of one piece of a row
 constexpr size_t kBlockBytes = size_t(512) << 20;      // e of one block of tokens
+constexpr int kMaxSplits = 64;                         // whose sums one thread adds up
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kMaxExp = 64.f;                        // a piece's exponents over this are shifted
 
@@ -517,6 +518,7 @@ CeWs ce_layout(char *ws, int T, int V, int d, int dtype, bool grad) {
     auto split = [&](int64_t tiles, int64_t fill, int64_t least) {
       int64_t n = fill / (tiles > 0 ? tiles : 1);
       if (n > kt / least) n = kt / least;
+      if (n > kMaxSplits) n = kMaxSplits;
       return int(n < 1 ? 1 : n);
     };
     if (dtype == LORA_BF16) {
