@@ -67,9 +67,10 @@ __device__ __forceinline__ bool ce_listed(const CeArgs &c, int t) {
 }
 
 // Workgroup 0: the list of tokens that have a target and a weight.  Beside it,
-// one wave per token: the target's logit of a listed one (float64 sums: both
+// four waves per token: the target's logit of a listed one (float64 sums: both
 // results hang on it), the zero loss and gradient of another.  (As launches one
-// after the other 48 us at 8192 tokens, as one 31.)
+// after the other 48 us at 8192 tokens, as one 29; at 1024 tokens 6.6, 10 with a
+// wave per token.)
 template <typename E>
 __global__ __launch_bounds__(1024) void ce_rows_kernel(CeArgs c) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, T = c.a.T;
@@ -93,28 +94,35 @@ __global__ __launch_bounds__(1024) void ce_rows_kernel(CeArgs c) {
     if (tid == 1023) c.w.count[0] = at;
     return;
   }
-  const int t = (int(blockIdx.x) - 1) * 16 + wave, d = c.a.d;
-  if (t >= T) return;
-  if (!ce_listed(c, t)) {
-    if (lane == 0) c.a.loss[t] = c.a.targets[t] >= c.a.V ? __builtin_nanf("") : 0.f;
-    const float z[8] = {};
-    for (int i = lane * 8; c.a.dX && i < d; i += 512)
-      Cols<E, 8>::store(static_cast<E *>(c.a.dX) + int64_t(t) * d + i, z);
-    return;
-  }
-  const E *x = static_cast<const E *>(c.a.X) + int64_t(t) * d;
-  const E *w = static_cast<const E *>(c.a.W) + int64_t(c.a.targets[t]) * d;
+  // a quarter of the row for each of four waves
+  __shared__ double part[16];
+  const int t = (int(blockIdx.x) - 1) * 4 + (wave >> 2), q = wave & 3, d = c.a.d;
+  const bool listed = t < T && ce_listed(c, t);
   double sum = 0.0;
-  for (int i = lane * 8; i < d; i += 512) {
-    float xv[8], wv[8];
-    Elem<E>::load8(x + i, xv);
-    Elem<E>::load8(w + i, wv);
+  if (listed) {
+    const E *x = static_cast<const E *>(c.a.X) + int64_t(t) * d;
+    const E *w = static_cast<const E *>(c.a.W) + int64_t(c.a.targets[t]) * d;
+    for (int i = (q * 64 + lane) * 8; i < d; i += 2048) {
+      float xv[8], wv[8];
+      Elem<E>::load8(x + i, xv);
+      Elem<E>::load8(w + i, wv);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum = fma(double(xv[k]), double(wv[k]), sum);
+      for (int k = 0; k < 8; ++k) sum = fma(double(xv[k]), double(wv[k]), sum);
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+  } else if (t < T) {
+    if (q == 0 && lane == 0) c.a.loss[t] = c.a.targets[t] >= c.a.V ? __builtin_nanf("") : 0.f;
+    const float z[8] = {};
+    for (int i = (q * 64 + lane) * 8; c.a.dX && i < d; i += 2048)
+      Cols<E, 8>::store(static_cast<E *>(c.a.dX) + int64_t(t) * d + i, z);
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
-  if (lane == 0) c.w.ly[t] = sum * double(c.a.logit_scale) * 1.4426950408889634074;
+  if (lane == 0) part[wave] = sum;
+  __syncthreads();
+  if (listed && q == 0 && lane == 0) {
+    sum = (part[wave] + part[wave + 1]) + (part[wave + 2] + part[wave + 3]);
+    c.w.ly[t] = sum * double(c.a.logit_scale) * 1.4426950408889634074;
+  }
 }
 
 // ------------------------------------------------------------ first product
@@ -566,7 +574,7 @@ template <typename E>
 hipError_t run(CeArgs c, hipStream_t s) {
   constexpr bool bf = sizeof(E) == 2;
   const int T = c.a.T, V = c.a.V, d = c.a.d;
-  hipLaunchKernelGGL(ce_rows_kernel<E>, dim3(unsigned(1 + (T + 15) / 16)), dim3(1024), 0, s, c);
+  hipLaunchKernelGGL(ce_rows_kernel<E>, dim3(unsigned(1 + (T + 3) / 4)), dim3(1024), 0, s, c);
   for (int r0 = 0; r0 < T; r0 += c.w.block) {
     c.row0 = r0;
     const int rows = T - r0 < c.w.block ? T - r0 : c.w.block;
