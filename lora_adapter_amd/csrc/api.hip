@@ -1160,7 +1160,12 @@ int32_t gated_args(const void *X, const void *W_gate_t, const void *W_up_t, int3
   a.splits = gated_base_splits(T, a.N, a.Kd, gate->dtype, c.cfg.splits);
   TermsArgs &t = c.t;
   t = terms_args(pv, gate, T, K);
-  for (int p = 0; p < 2; ++p) t.sums[p] = a.sums[p] = c.g[p].partial;
+  for (int p = 0; p < 2; ++p) {
+    t.sums[p] = a.sums[p] = c.g[p].partial;
+    // the slots' terms behind, where the partials' room has them
+    if (K > 1 && K <= kTermSlots && a.splits + K <= c.cfg.splits)
+      t.slots[p] = a.sums[p] + int64_t(a.splits) * T * a.N;
+  }
   t.U[0] = a.ex.U; t.U[1] = a.U_up; t.u_cap = a.ex.u_cap;
   t.pages[0] = gate->b_pages; t.pages[1] = up->b_pages;
   t.N = a.N; t.splits = a.splits;
@@ -1254,10 +1259,10 @@ int32_t lora_gated_forward(const int32_t *ids, const float *gates, int32_t T, in
 namespace {
 
 // Workspace of the gated backward: [G of the gate][G of the up projection], and
-// where the product is split [the splits' sums].
+// where the product is split [the splits' sums][each slot's terms].
 struct GatedGradWs {
   int splits;
-  size_t g, sums, total;
+  size_t g, sums, slots, total;
 };
 
 GatedGradWs gated_grad_ws(int32_t T, int32_t K, int32_t d_in, int32_t d_out, int32_t max_rank, int32_t dtype) {
@@ -1266,7 +1271,8 @@ GatedGradWs gated_grad_ws(int32_t T, int32_t K, int32_t d_in, int32_t d_out, int
   w.g = align_up(size_t(T) * size_t(K) * size_t(max_rank) * sizeof(float) + 4);
   const size_t one = size_t(T) * size_t(d_in) * sizeof(float);
   w.sums = align_up(size_t(w.splits) * one);
-  w.total = 2 * w.g + w.sums;
+  w.slots = w.splits > 0 && K > 1 && K <= kTermSlots ? align_up(size_t(K) * one) : 0;
+  w.total = 2 * w.g + w.sums + w.slots;
   return w;
 }
 
@@ -1342,6 +1348,7 @@ int32_t lora_gated_grad(const void *dH, const void *pre_gate, const void *pre_up
   TermsArgs t = terms_args(pv, gate, T, K);
   if (w.splits) {
     t.sums[0] = a.sums = reinterpret_cast<float *>(base + 2 * w.g);
+    if (w.slots) t.slots[0] = reinterpret_cast<float *>(base + 2 * w.g + w.sums);
     t.U[0] = a.ex.U; t.U[1] = a.U_up; t.u_cap = a.ex.u_cap;
     t.pages[0] = gate->a_pages; t.pages[1] = up->a_pages;
     t.N = d; t.splits = w.splits;

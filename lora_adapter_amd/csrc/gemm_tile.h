@@ -49,12 +49,6 @@ __device__ __forceinline__ void store8_nt(uint16_t *p, const float v[8]) {
   w.w = f2bf2(v[6], v[7]);
   __builtin_nontemporal_store(w, reinterpret_cast<u32x4_t *>(p));
 }
-template <> struct Cols<float, 2> {
-  static __device__ __forceinline__ void load(const float *p, float v[2]) {
-    const float2 w = *reinterpret_cast<const float2 *>(p);
-    v[0] = w.x; v[1] = w.y;
-  }
-};
 template <> struct Cols<float, 8> {
   static __device__ __forceinline__ void load(const float *p, float v[8]) { Elem<float>::load8(p, v); }
   static __device__ __forceinline__ void store(float *p, const float v[8]) {

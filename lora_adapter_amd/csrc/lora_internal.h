@@ -497,6 +497,7 @@ struct TermsArgs {
   int64_t u_cap;
   const void *pages[2];     // [n_pages][N]
   float *sums[2];           // [splits][M][N]
+  float *slots[2];          // [K][M][N] for each slot's terms, or null (see launch_terms)
   int M, N, K, splits;
   int act;
   void *H, *pre_gate, *pre_up;
@@ -624,12 +625,13 @@ hipError_t launch_cross_entropy(const CrossEntropyArgs &a, int dtype, void *ws, 
 bool gated_whole(int64_t M, int64_t Kd, int dtype, bool fused);   // tiles that finish themselves
 hipError_t launch_gated(const GatedArgs &g, hipStream_t s);
 // Otherwise the base products, with the plan beside them if it fits (lds) ...
+constexpr int kTermSlots = 4;  // slots whose terms are kept apart, at most
 int gated_base_splits(int M, int N, int Kd, int dtype, int most);
 PlanLaunch gated_base_plan(const GatedArgs &g, int dtype, const int32_t *ids, const float *gates, int T, int K,
                            const PoolView &pool, int32_t *plan);
 hipError_t launch_gated_base(const GatedArgs &g, int dtype, const PlanArgs *plan, hipStream_t s);
 // ... and the rest; sum: dX
-hipError_t launch_terms(TermsArgs a, bool sum, int dtype, hipStream_t s);
+hipError_t launch_terms(const TermsArgs &a, bool sum, int dtype, hipStream_t s);
 // Decode: both products' partials, the per-slot shrinks and the plan; or, with
 // a plan, both products' partials.  Then both sums, both expands, activation and
 // product.

@@ -196,6 +196,17 @@ def test_forward_tile_shapes(T, F, K, d):
     G.check_forward(Block(T, K, d, F, seed=T + K, lo=0, hi=20, mask=K == 2), "silu")
 
 
+# slots whose terms are kept apart (up to 4, where the workspace has the room) and
+# slots taken one after another
+@pytest.mark.parametrize("T,K,d,F,dtype", [(200, 2, 1600, 448, "bf16"), (200, 4, 2688, 192, "bf16"), (150, 2, 64, 320, "bf16"),
+                                           (140, 5, 1600, 192, "bf16"), (70, 4, 576, 192, "f32"), (70, 8, 576, 192, "f32"),
+                                           (70, 2, 64, 192, "f32")])
+def test_slots_together_and_in_turn(T, K, d, F, dtype):
+    b = Block(T, K, d, F, dtype, seed=T + K, lo=0, hi=12, mask=True)
+    G.check_forward(b, "silu")
+    G.check_grad(b, "silu")
+
+
 def test_many_float32_tokens():
     """More windows of 16 pairs than one dimension of a grid holds."""
     T, d, F = 600000, 64, 64
