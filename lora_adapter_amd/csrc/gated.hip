@@ -1452,7 +1452,7 @@ hipError_t run_terms(TermsArgs a, hipStream_t s) {
 // With one slot a launch, which finishes; with several and room for their terms
 // two, that reads the pages once for all slots; else one for each slot
 // (600 tokens of top 2, 5824 -> 2240: 26 us in two launches, 45 slot by slot; 333
-// float32 tokens 16 and 21).
+// float32 tokens 16 and 21; with one slot, 700 tokens of 96 adapters, 60 and 49).
 hipError_t launch_terms(const TermsArgs &a, bool sum, int dtype, hipStream_t s) {
   if (dtype == LORA_BF16) return sum ? run_terms<uint16_t, true>(a, s) : run_terms<uint16_t, false>(a, s);
   return sum ? run_terms<float, true>(a, s) : run_terms<float, false>(a, s);
