@@ -314,3 +314,68 @@ def test_cross_entropy_of_rows_past_32_bits():
     rest = torch.ones(FAR_T, dtype=torch.bool, device="cuda")
     rest[FAR_ROWS] = False
     assert not bool(loss[rest].any()) and not bool(dX[rest].any())
+
+
+# ---------------------------------------------------------------- no room for U
+
+@pytest.mark.parametrize("T,K,d,F,dtype", [(5, 1, 128, 192, "bf16"), (200, 2, 1600, 448, "bf16"), (300, 1, 128, 448, "bf16"),
+                                           (4200, 1, 128, 1984, "bf16"), (70, 2, 576, 192, "f32")])
+@pytest.mark.parametrize("which", [0, 1])
+def test_without_room_for_u_the_base_alone(T, K, d, F, dtype, which):
+    """One projection's workspace too small for U, or max_rank below the ranks:
+    the plan says so and the results are the base products'."""
+    b = Block(T, K, d, F, dtype, seed=6, lo=12, hi=16, empty=False)
+    small = workspace(B.lora_apply_workspace_bytes(T, K, d, F, 1, CODE[dtype]))
+    full = [w.numel() for w in b.ws]
+    assert small.numel() < full[0]
+    b.ws[which] = small
+    H = b.out(F)
+    b.forward("silu", H.t)
+    torch.cuda.synchronize()
+    H.check()
+    assert int(b.plan.view(torch.int32)[B.PH_ERR]) & B.DEVERR_CAPACITY
+    pairs, b.ids = b.ids, np.full_like(b.ids, -1)
+    ref, tol = G.expected(b, "silu")[0]
+    near(H.t, ref, tol, "H")
+    b.ids = pairs
+    g, u = torch.randn_like(b.dH), torch.randn_like(b.dH)
+    W = [w.t().contiguous() for w in b.W]
+    B.lora_plan(b.d_ids, b.d_gates, T, K, b.pools[0], b.plan)
+    assert int(b.plan.view(torch.int32)[B.PH_ERR]) == 0
+    b.R = 1
+    dg, du, dx = G.run_grad(b, "silu", g, u, W)
+    assert int(b.plan.view(torch.int32)[B.PH_ERR]) & B.DEVERR_CAPACITY
+    b.ids = np.full_like(b.ids, -1)
+    near(dx, *G.expected_dx(b, f64(dg), f64(du), W), "dX")
+
+
+# ---------------------------------------------------------------- infinities and NaN in pages
+
+@pytest.mark.parametrize("T,K,d,F,dtype", [(5, 2, 128, 192, "bf16"), (150, 2, 64, 320, "bf16"), (200, 2, 1600, 448, "bf16"),
+                                           (4200, 2, 128, 1984, "bf16"), (70, 2, 576, 192, "f32"), (70, 5, 128, 192, "f32")])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_pages_that_are_not_finite_stay_with_their_rows(T, K, d, F, dtype, value):
+    """Another adapter's rows keep their bits; the adapter's own rows are what float
+    arithmetic makes of them, in g, u and dX."""
+    b = Block(T, K, d, F, dtype, seed=T + 1, lo=1, hi=12)
+    bad = 2
+    pages = torch.from_numpy(b.page_ids[b.start[bad]:b.start[bad + 1]].astype(np.int64)).cuda()
+    W = [w.t().contiguous() for w in b.W]
+    torch.manual_seed(T)
+    g0, u0 = torch.randn_like(b.dH), torch.randn_like(b.dH)
+
+    def run():
+        _, g, u = G.run_forward(b, "silu")
+        return g.clone(), u.clone(), G.run_grad(b, "silu", g0, u0, W)[2].clone()
+
+    clean = run()
+    for p in range(2):
+        b.Bp[p][pages[0], 5::7] = value
+        b.A[p][pages[-1], 3::11] = value
+    got = run()
+    own = torch.from_numpy(((b.ids == bad) & (b.gates != 0)).any(1)).cuda()
+    assert bool(own.any()) and bool((~own).any())
+    for a, c, what in zip(got, clean, ("g", "u", "dX")):
+        assert torch.equal(a[~own], c[~own]), what
+        # G = d.B is not finite for the adapter's pairs, and so is U = X.A: all its columns
+        assert not bool(torch.isfinite(a[own]).all(1).any()), what
