@@ -1197,7 +1197,7 @@ __global__ __launch_bounds__(256) void gated_base_f32_kernel(GatedArgs g, PlanAr
 template <typename E, int kAct>
 __global__ __launch_bounds__(256) void gated_act_grad_kernel(const E *dH, const E *pg, const E *pu, E *dg, E *du,
                                                              int64_t n8) {
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t i = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
   if (i >= n8) return;
   float h[8], g[8], u[8], a[8], b[8];
   Elem<E>::load8(dH + i * 8, h);
@@ -1386,8 +1386,10 @@ __global__ __launch_bounds__(256) void gated_grad_x_f32_kernel(GatedGradXArgs g)
 template <typename E>
 void launch_act_grad(const void *dH, const void *pg, const void *pu, int act, void *dg, void *du, int64_t n,
                      hipStream_t s) {
-  const int64_t n8 = n / 8;
-  const dim3 grid(unsigned((n8 + 255) / 256)), block(256);
+  // (a grid dimension holds less than 2^32 threads; a launch of more takes their number
+  // modulo 2^32 and reports nothing)
+  const int64_t n8 = n / 8, wgs = (n8 + 255) / 256, gx = wgs < (1 << 20) ? wgs : 1 << 20;
+  const dim3 grid(unsigned(gx), unsigned((wgs + gx - 1) / gx)), block(256);
   const E *h = static_cast<const E *>(dH), *g = static_cast<const E *>(pg), *u = static_cast<const E *>(pu);
   E *a = static_cast<E *>(dg), *b = static_cast<E *>(du);
   if (act == LORA_ACT_SILU)

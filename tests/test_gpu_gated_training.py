@@ -316,6 +316,34 @@ def test_cross_entropy_of_rows_past_32_bits():
     assert not bool(loss[rest].any()) and not bool(dX[rest].any())
 
 
+def test_more_elements_than_one_grid_dimension_has_threads():
+    """2^20 tokens of 32832: d_gate and d_up in place."""
+    T, F = 1 << 20, 32832
+    if torch.cuda.mem_get_info()[0] < 215 << 30:
+        pytest.skip("needs 215 GB of device memory")
+    b = Block(1, 1, 64, F, seed=3)
+    rows = [0, 524287, T // 2 + 3, T - 2, T - 1]
+    dH = torch.zeros(T, F, dtype=torch.bfloat16, device="cuda")
+    g, u = torch.ones_like(dH), torch.ones_like(dH)
+    for i, r in enumerate(rows):
+        for x in (dH, g, u):
+            x[r] = torch.randn(F, generator=torch.Generator("cuda").manual_seed(i), device="cuda").bfloat16()
+    was = [f64(x[rows]) for x in (g, u, dH)]
+    plan = workspace(B.lora_plan_bytes(T, 1, b.N))
+    B.lora_gated_grad(dH, g, u, 0, None, None, None, 1.0, T, 1, None, *b.pools, plan, b.R, g, u, None, None)
+    torch.cuda.synchronize()
+    (rg, tg), (ru, tu) = G.grad_tolerances(b, "silu", *was)
+    near(g[rows], rg, tg, "d_gate")
+    near(u[rows], ru, tu, "d_up")
+    # 0 . u . act'(1) and 0 . act(1) where dH is 0
+    for x in (g, u):
+        x[rows] = 0
+        for i in range(0, T, 1 << 16):
+            assert not bool(x[i:i + (1 << 16)].any()), i
+    del dH, g, u, x
+    torch.cuda.empty_cache()
+
+
 # ---------------------------------------------------------------- no room for U
 
 @pytest.mark.parametrize("T,K,d,F,dtype", [(5, 1, 128, 192, "bf16"), (200, 2, 1600, 448, "bf16"), (300, 1, 128, 448, "bf16"),
