@@ -742,8 +742,8 @@ int32_t lora_cross_entropy(const void *X, const void *W_t, int32_t dtype, int32_
  *   norm[m] = sqrt( sum over layers of |dA|^2 + |dB|^2, pages of adapters[m] )
  *   norm[M] = sqrt( sum_m norm[m]^2 )
  *   out = grad . min(1, max_norm / n),  n = together ? norm[M] : norm[m]
- * A norm that is not finite clips nothing: the gradients go through as they
- * are, and norm tells.
+ * A norm that is not finite, or that float32 does not hold (past 3.4e38: norm
+ * says infinity), clips nothing: the gradients go through as they are.
  *   layers    host array [n_layers]: a pool (its page table alone is read, and
  *             its widths) and float32 pages as lora_grad writes them, 16-byte
  *             aligned.  dA_out may be dA_pages (in place; rows whose factor is 1

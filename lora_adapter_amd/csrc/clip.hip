@@ -122,7 +122,8 @@ __global__ __launch_bounds__(kThreads) void clip_total_kernel(ClipArgs a) {
 // they are what the cache still holds.  With kPart each workgroup adds
 // the partials itself, its row's loads in flight; otherwise clip_norm_kernel
 // has.  The workgroups of an entry's first row write the norms.  A norm that is
-// not finite clips nothing: the gradients stay what they are, and the norm says so.
+// not finite, as the float that is written, clips nothing: the gradients stay what
+// they are, and the norm says so.
 template <bool kPart>
 __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipArgs a) {
   __shared__ double red[4];
@@ -147,7 +148,7 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipArgs a) {
     if (m == 0) a.norm[a.M] = float(sqrt(total));
   }
   const double n = sqrt(a.together ? total : square);
-  const float coef = n > double(a.max_norm) && n < double(INFINITY) ? float(double(a.max_norm) / n) : 1.f;
+  const float coef = n > double(a.max_norm) && float(n) < INFINITY ? float(double(a.max_norm) / n) : 1.f;
   if (l.out[f] == l.grad[f] && coef == 1.f) return;
   for (int j = y; j < r; j += Y) {
     const int64_t at = int64_t(l.page_ids[ps + j]) * d;

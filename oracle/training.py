@@ -74,8 +74,8 @@ def cross_entropy(X, W_t, targets, weights=None, scale: float = 1.0):
 
 def clip(layers, adapters, max_rank: int, max_norm: float, together: bool):
     """layers: dicts with rank, page_start, page_ids, n_pages, A, B (float64
-    pages).  Norms [M + 1], and the clipped pages (a new dict of A and B for
-    each layer; other pages as they were)."""
+    pages).  Norms [M + 1], infinite where float32 has no such number, and the
+    clipped pages (a new dict of A and B for each layer; other pages as they were)."""
     M = len(adapters)
     taken = []
     for l in layers:
@@ -98,6 +98,8 @@ def clip(layers, adapters, max_rank: int, max_norm: float, together: bool):
         for m, p in here.items():
             square[m] += (l["A"][p] ** 2).sum() + (l["B"][p] ** 2).sum()
     norm = np.sqrt(np.append(square, square.sum()))
+    with np.errstate(over="ignore"):
+        norm[np.isinf(norm.astype(np.float32))] = np.inf
     out = []
     for l, here in zip(layers, taken):
         o = {"A": l["A"].copy(), "B": l["B"].copy()}

@@ -112,6 +112,16 @@ def test_sizes_that_float32_squares_do_not_hold():
         L.check([0, 1, 2], 8, size * 0.5, True)
 
 
+def test_norms_past_float32():
+    """A norm that float32 does not hold is reported as infinite and clips nothing."""
+    L = Layers(2, 6, 1, 7, [(64, 64)], size=6.8e37, seed=4)
+    ads = [0, 1, 2, 3, 4, 5]
+    norm = R.clip(L.host, ads, 8, 5e37, False)[0]
+    assert np.isinf(norm[:-1]).any() and np.isfinite(norm[:-1]).any() and np.isinf(norm[-1])
+    L.check(ads, 8, 5e37, False)
+    L.check(ads, 8, 5e37, True)
+
+
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 def test_not_finite(value):
     """That adapter's gradients go through as they are; the others are clipped."""

@@ -303,3 +303,11 @@ def test_gated_alignment_and_widths(B):
         w.update(kw)
         assert B.lora_gated_grad_workspace_bytes(4, 1, w["d_in"], w["d_out"], 16, B.LORA_BF16) == 0
     assert B.lora_cross_entropy_workspace_bytes(4, 100, (1 << 22) + 64, B.LORA_BF16) == 0
+
+
+def test_clip_of_a_norm_that_float32_does_not_hold():
+    l = {"rank": [1, 1], "page_start": [0, 1, 2], "page_ids": [0, 1], "n_pages": 2,
+         "A": np.array([[3e38, 0], [3e38, 0]]), "B": np.array([[0, 3e38], [0, 1.0]])}
+    norm, out, _ = R.clip([l], [0, 1], 4, 1e38, False)
+    assert np.isinf(norm[0]) and norm[1] == 3e38 and np.isinf(norm[2])
+    assert np.array_equal(out[0]["A"][0], l["A"][0]) and np.allclose(out[0]["A"][1], [1e38, 0])
