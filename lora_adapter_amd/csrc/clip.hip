@@ -148,15 +148,19 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(ClipArgs a) {
     if (m == 0) a.norm[a.M] = float(sqrt(total));
   }
   const double n = sqrt(a.together ? total : square);
-  const float coef = n > double(a.max_norm) && float(n) < INFINITY ? float(double(a.max_norm) / n) : 1.f;
-  if (l.out[f] == l.grad[f] && coef == 1.f) return;
+  const bool clips = n > double(a.max_norm) && float(n) < INFINITY;
+  if (l.out[f] == l.grad[f] && !clips) return;
+  // the factor stays float64: it may be under float32's normal numbers, whose few bits
+  // (none under 2^-149) would be all that the results had
+  const double coef = clips ? double(a.max_norm) / n : 1.0;
   for (int j = y; j < r; j += Y) {
     const int64_t at = int64_t(l.page_ids[ps + j]) * d;
     for (int c = threadIdx.x * 4; c < d; c += kPieces * kStep) {
       if (j != y || c >= kPieces * kStep) load_pieces(l.grad[f] + at, c, d, v);
 #pragma unroll
       for (int u = 0; u < kPieces; ++u) {
-        v[u].x *= coef; v[u].y *= coef; v[u].z *= coef; v[u].w *= coef;
+        v[u].x = float(v[u].x * coef); v[u].y = float(v[u].y * coef);
+        v[u].z = float(v[u].z * coef); v[u].w = float(v[u].w * coef);
         if (c + u * kStep < d) *reinterpret_cast<float4 *>(l.out[f] + at + c + u * kStep) = v[u];
       }
     }

@@ -122,6 +122,14 @@ def test_norms_past_float32():
     L.check(ads, 8, 5e37, True)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_factors_that_float32_does_not_hold(in_place):
+    """max_norm / n below float32's normal numbers: the product is rounded once all the same."""
+    for size, top in ((1e30, 1e-11), (1e37, 1e-3), (1e30, 1e-20)):
+        L = Layers(2, 3, 2, 5, [(64, 64)], size=size, in_place=in_place)
+        L.check([0, 1, 2], 8, top, in_place)
+
+
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 def test_not_finite(value):
     """That adapter's gradients go through as they are; the others are clipped."""
