@@ -141,6 +141,17 @@ def test_not_finite(value):
     L.check([0, 1, 2], 8, 0.5, True)
 
 
+@pytest.mark.parametrize("n,M,together", [(7, 9, False), (7, 10, False), (7, 9, True), (7, 10, True), (7, 40, False),
+                                          (40, 60, False), (40, 60, True)])
+def test_partials_of_few_and_of_many(n, M, together):
+    """2016 and 2240 partials, on both sides of where the second pass's workgroups add
+    them; 8960 and 28800."""
+    L = Layers(n, M + 2, 1, 16, [(64, 128), (192, 64)], seed=M)
+    ads = [int(a) for a in np.random.default_rng(M).permutation(M + 2)[:M]]
+    ref = R.clip(L.host, ads, 16, 1.0, together)[0]
+    L.check(ads, 16, float(np.median(ref[:-1]) * (0.7 if together else 1.0)), together)
+
+
 def test_no_layers_and_no_adapters():
     L = Layers(1, 2, 1, 3, [(64, 64)])
     assert L.run([], 4, 1.0, True).tolist() == [0.0]
