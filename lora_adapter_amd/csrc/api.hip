@@ -1093,6 +1093,41 @@ bool outputs_apart(const void *const *out, int n_out, const void *const *in, int
   return true;
 }
 
+// The buffers of a call, to tell whether an output shares memory with another.
+struct Ranges {
+  struct {
+    uintptr_t at, end;
+  } r[40];
+  int n = 0;
+  void add(const void *p, size_t bytes) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    if (p && bytes) r[n++] = {at, at + bytes < at ? UINTPTR_MAX : at + bytes};
+  }
+  // What kernels read of a pool.
+  void add(const lora_pool_desc *p) {
+    const size_t e = p->dtype == LORA_BF16 ? 2 : 4, N = size_t(p->n_adapters), pages = size_t(p->n_pages);
+    add(p->rank, N * 4);
+    add(p->page_start, (N + 1) * 4);
+    add(p->page_ids, size_t(p->n_page_ids) * 4);
+    add(p->scale, N * 4);
+    add(p->a_pages, pages * size_t(p->d_in) * e);
+    add(p->b_pages, pages * size_t(p->d_out) * e);
+  }
+  bool apart(const Ranges &o) const {
+    for (int i = 0; i < n; ++i)
+      for (int j = 0; j < o.n; ++j)
+        if (r[i].at < o.r[j].end && o.r[j].at < r[i].end) return false;
+    return true;
+  }
+  // No two of them overlap.
+  bool apart() const {
+    for (int i = 0; i < n; ++i)
+      for (int j = 0; j < i; ++j)
+        if (r[i].at < r[j].end && r[j].at < r[i].end) return false;
+    return true;
+  }
+};
+
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool aligned16(const void *p) { return aligned(p, 16); }
 
@@ -1117,11 +1152,17 @@ TermsArgs terms_args(const PlanView &pv, const lora_pool_desc *pool, int32_t T, 
   return t;
 }
 
+// What a call may write of an apply workspace.
+size_t apply_ws_used(const void *ws, size_t ws_bytes, const ApplyWs &w, int32_t T, int32_t K) {
+  const size_t head = size_t(reinterpret_cast<const char *>(w.U) - static_cast<const char *>(ws));
+  return std::min(ws_bytes, head + size_t(T) * size_t(K) * LORA_MAX_RANK * sizeof(float));
+}
+
 // The checks of the gated forward (T > 0 from the workspaces on), and its
 // arguments.
-int32_t gated_args(const void *X, const void *W_gate_t, const void *W_up_t, int32_t activation,
+int32_t gated_args(const int32_t *ids, const void *X, const void *W_gate_t, const void *W_up_t, int32_t activation,
                    void *H, void *pre_gate, void *pre_up, int32_t T, int32_t K, const float *gates,
-                   const lora_pool_desc *gate, const lora_pool_desc *up, const void *plan,
+                   const uint8_t *keep_mask, const lora_pool_desc *gate, const lora_pool_desc *up, const void *plan,
                    void *ws_gate, size_t ws_gate_bytes, void *ws_up, size_t ws_up_bytes, GatedCall &c) {
   int32_t st = check_batch(T, K);
   if (st != LORA_OK) return st;
@@ -1136,11 +1177,28 @@ int32_t gated_args(const void *X, const void *W_gate_t, const void *W_up_t, int3
                         static_cast<const void *>(pre_up), static_cast<const void *>(ws_gate),
                         static_cast<const void *>(ws_up)})
     if (!aligned16(p)) return LORA_ERR_INVALID_ARG;
+  if (!aligned(keep_mask, 8)) return LORA_ERR_INVALID_ARG;
   if ((st = base_args(X, W_gate_t, H, T, K, gate, plan, ws_gate, ws_gate_bytes, c.cfg, c.g[0])) != LORA_OK ||
       (st = base_args(X, W_up_t, H, T, K, up, plan, ws_up, ws_up_bytes, c.cfg, c.g[1])) != LORA_OK)
     return st;
   c.w[0] = apply_layout(ws_gate, ws_gate_bytes, T, K, gate->d_in, gate->d_out, gate->dtype);
   c.w[1] = apply_layout(ws_up, ws_up_bytes, T, K, up->d_in, up->d_out, up->dtype);
+  const size_t e = gate->dtype == LORA_BF16 ? 2 : 4, TK = size_t(T) * size_t(K), F = size_t(gate->d_out), d = size_t(gate->d_in);
+  Ranges outs, ins;
+  for (const void *p : {static_cast<const void *>(H), static_cast<const void *>(pre_gate), static_cast<const void *>(pre_up)})
+    outs.add(p, size_t(T) * F * e);
+  outs.add(ws_gate, apply_ws_used(ws_gate, ws_gate_bytes, c.w[0], T, K));
+  outs.add(ws_up, apply_ws_used(ws_up, ws_up_bytes, c.w[1], T, K));
+  outs.add(plan, lora_plan_bytes(T, K, gate->n_adapters));
+  ins.add(X, size_t(T) * d * e);
+  ins.add(W_gate_t, F * d * e);
+  ins.add(W_up_t, F * d * e);
+  ins.add(ids, TK * sizeof(int32_t));
+  ins.add(gates, TK * sizeof(float));
+  ins.add(keep_mask, size_t(T) * d);
+  ins.add(gate);
+  ins.add(up);
+  if (!outs.apart() || !outs.apart(ins)) return LORA_ERR_INVALID_ARG;
   const PlanView pv = plan_view(plan, int64_t(T) * K, gate->n_adapters);
   GatedArgs &a = c.a;
   a = GatedArgs{};
@@ -1193,8 +1251,8 @@ int32_t lora_gated_apply(const void *X, const void *W_gate_t, const void *W_up_t
                          void *ws_gate, size_t ws_gate_bytes, void *ws_up, size_t ws_up_bytes,
                          void *stream) {
   GatedCall c;
-  const int32_t st = gated_args(X, W_gate_t, W_up_t, activation, H, pre_gate, pre_up, T, K, gates, gate, up,
-                                plan, ws_gate, ws_gate_bytes, ws_up, ws_up_bytes, c);
+  const int32_t st = gated_args(nullptr, X, W_gate_t, W_up_t, activation, H, pre_gate, pre_up, T, K, gates, keep_mask,
+                                gate, up, plan, ws_gate, ws_gate_bytes, ws_up, ws_up_bytes, c);
   if (st != LORA_OK || T == 0) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const PlanView pv = plan_view(plan, int64_t(T) * K, gate->n_adapters);
@@ -1216,7 +1274,7 @@ int32_t lora_gated_forward(const int32_t *ids, const float *gates, int32_t T, in
                            const lora_pool_desc *up, void *plan, size_t plan_bytes, void *ws_gate,
                            size_t ws_gate_bytes, void *ws_up, size_t ws_up_bytes, void *stream) {
   GatedCall c;
-  int32_t st = gated_args(X, W_gate_t, W_up_t, activation, H, pre_gate, pre_up, T, K, gates, gate, up, plan,
+  int32_t st = gated_args(ids, X, W_gate_t, W_up_t, activation, H, pre_gate, pre_up, T, K, gates, keep_mask, gate, up, plan,
                           ws_gate, ws_gate_bytes, ws_up, ws_up_bytes, c);
   if (st != LORA_OK) return st;
   if (plan_bytes < lora_plan_bytes(T, K, gate->n_adapters)) return LORA_ERR_CAPACITY;
@@ -1312,6 +1370,25 @@ int32_t lora_gated_grad(const void *dH, const void *pre_gate, const void *pre_up
   const int32_t F = gate->d_out, d = gate->d_in, dtype = gate->dtype;
   const GatedGradWs w = gated_grad_ws(T, K, d, F, max_rank, dtype);
   if (dX && ws_bytes < w.total) return LORA_ERR_CAPACITY;
+  const size_t e_size = dtype == LORA_BF16 ? 2 : 4, rows = size_t(T) * size_t(F) * e_size;
+  Ranges outs, ins;
+  outs.add(d_gate, rows);
+  outs.add(d_up, rows);
+  ins.add(dH, rows);
+  if (pre_gate != d_gate) ins.add(pre_gate, rows);      // in place, or apart
+  if (pre_up != d_up) ins.add(pre_up, rows);
+  if (dX) {
+    outs.add(dX, size_t(T) * size_t(d) * e_size);
+    outs.add(ws, w.total);
+    outs.add(plan, lora_plan_bytes(T, K, gate->n_adapters));
+    ins.add(W_gate, size_t(d) * size_t(F) * e_size);
+    ins.add(W_up, size_t(d) * size_t(F) * e_size);
+    ins.add(gates, size_t(T) * size_t(K) * sizeof(float));
+    ins.add(keep_mask, size_t(T) * size_t(d));
+    ins.add(gate);
+    ins.add(up);
+  }
+  if (!outs.apart() || !outs.apart(ins)) return LORA_ERR_INVALID_ARG;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = launch_gated_act_grad(dH, pre_gate, pre_up, activation, d_gate, d_up, int64_t(T) * F, dtype, s);
   if (e != hipSuccess || !dX) return dev(e);

@@ -309,3 +309,34 @@ def test_captured_and_beside_another_stream(T, F):
             step()
             torch.cuda.synchronize()
             assert all(torch.equal(o, r) for o, r in zip(outs, got)), k
+
+
+@pytest.mark.parametrize("T,F", [(3, 192), (200, 448), (4200, 1984)])
+def test_buffers_that_touch(T, F):
+    """All of a call's larger buffers one behind the other, without a byte between."""
+    b = Block(T, 2, 128, F, seed=9, mask=True)
+    ref = [t.clone() for t in run_forward(b, "silu")]
+    W = [w.t().contiguous() for w in b.W]
+    ref += [t.clone() for t in run_grad(b, "silu", ref[1], ref[2], W)]
+    one = torch.full((sum(t.numel() * t.element_size() for t in ref) + b.X.numel() * 2 + sum(w.numel() for w in b.ws)
+                      + b.plan.numel() + B.lora_gated_grad_workspace_bytes(T, 2, 128, F, b.R, B.LORA_BF16),), 0x77,
+                     dtype=torch.uint8, device="cuda")
+    at = 0
+
+    def take(n):
+        nonlocal at
+        at += n
+        return one[at - n:at]
+
+    rows = lambda n: take(2 * T * n).view(torch.bfloat16).view(T, n)
+    H, X, g, u = rows(F), rows(128), rows(F), rows(F)
+    X.copy_(b.X)
+    b.X = X
+    dg, ws, du, dX = rows(F), [take(w.numel()) for w in b.ws], rows(F), rows(128)
+    back = take(B.lora_gated_grad_workspace_bytes(T, 2, 128, F, b.R, B.LORA_BF16))
+    b.plan = take(b.plan.numel())
+    assert at == one.numel()
+    b.forward("silu", H, g, u, ws=ws)
+    B.lora_gated_grad(b.dH, g, u, 0, *W, b.d_mask, b.keep, T, 2, b.d_gates, *b.pools, b.plan, b.R, dg, du, dX, back)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip((H, g, u, dg, du, dX), ref))

@@ -311,3 +311,67 @@ def test_clip_of_a_norm_that_float32_does_not_hold():
     norm, out, _ = R.clip([l], [0, 1], 4, 1e38, False)
     assert np.isinf(norm[0]) and norm[1] == 3e38 and np.isinf(norm[2])
     assert np.array_equal(out[0]["A"][0], l["A"][0]) and np.allclose(out[0]["A"][1], [1e38, 0])
+
+
+SPOT = 1 << 26                 # buffers this far apart: none below reaches the next
+
+
+def _overlaps(call, outs, ins, extra=()):
+    """call(**{name: address}) at which two buffers overlap: INVALID_ARG, whichever way."""
+    names = list(outs) + list(ins)
+    at = {n: (i + 1) * SPOT for i, n in enumerate(names)}
+    for o, size in outs.items():
+        for n in names:
+            if n == o or (o, n) in extra or (n, o) in extra:
+                continue
+            other = outs.get(n) or ins[n]
+            # an output that begins inside the other, ends inside it, and its last 16 bytes
+            for where in (at[n] + (other - 1) // 16 * 16, at[n] + 16 - (size + 15) // 16 * 16, at[n]):
+                yield o, n, call(**{**at, o: where})
+
+
+def test_gated_buffers_that_overlap(B):
+    """Ranges, not starts alone; the mask, the gates, the ids and the pools among them."""
+    L, r, INV = B.lib(), ctypes.byref, B.LORA_ERR_INVALID_ARG
+    T, K, d, F, e, N, P = 160, 2, 128, 192, 2, 2, 4
+    n = B.lora_apply_workspace_bytes(T, K, d, F, 16, B.LORA_BF16)
+    tables = dict(rank=N * 4, page_start=N * 4 + 4, page_ids=12)
+    ins = dict(X=T * d * e, Wg=F * d * e, Wu=F * d * e, gates=T * K * 4, mask=T * d, **tables, ga=P * d * e, gb=P * F * e,
+               gs=N * 4, ua=P * d * e, ub=P * F * e, us=N * 4)
+    rows = T * F * e
+    pool = lambda a, p: _pool(B, a_pages=a[p + "a"], b_pages=a[p + "b"], scale=a[p + "s"], **{t: a[t] for t in tables})
+
+    def forward(kind, **a):
+        g, u = pool(a, "g"), pool(a, "u")
+        tail = (a["gates"], T, K, a["X"], a["Wg"], a["Wu"], 0, a["H"], a["pg"], a["pu"], a["mask"], 1.0, r(g), r(u),
+                a["plan"], BIG, a["wg"], n, a["wu"], n, None)
+        if kind == "forward":
+            return L.lora_gated_forward(a["ids"], *tail)
+        return L.lora_gated_apply(a["X"], a["Wg"], a["Wu"], 0, a["H"], a["pg"], a["pu"], T, K, a["gates"], a["mask"], 1.0,
+                                  r(g), r(u), a["plan"], a["wg"], n, a["wu"], n, None)
+
+    outs = dict(H=rows, pg=rows, pu=rows, wg=n, wu=n, plan=B.lora_plan_bytes(T, K, N))
+    for o, i, got in _overlaps(lambda **a: forward("forward", **a), outs, {**ins, "ids": T * K * 4}):
+        assert got == INV, (o, i)
+    for o, i, got in _overlaps(lambda **a: forward("apply", **a), outs, ins):
+        assert got == INV, (o, i)
+    at = {x: (i + 1) * SPOT for i, x in enumerate([*outs, *ins, "ids"])}
+    for by in (1, 2, 4):
+        assert forward("forward", **{**at, "mask": at["mask"] + by}) == INV
+        assert forward("apply", **{**at, "mask": at["mask"] + by}) == INV
+
+    nb = B.lora_gated_grad_workspace_bytes(T, K, d, F, 16, B.LORA_BF16)
+
+    def grad(**a):
+        g, u = pool(a, "g"), pool(a, "u")
+        return L.lora_gated_grad(a["dH"], a["pg"], a["pu"], 0, a["Wg"], a["Wu"], a["mask"], 1.0, T, K, a["gates"], r(g),
+                                 r(u), a["plan"], 16, a["dg"], a["du"], a["dX"], a["ws"], nb, None)
+
+    ins = dict(dH=rows, pg=rows, pu=rows, **{k: ins[k] for k in ins if k != "X"})
+    outs = dict(dg=rows, du=rows, dX=T * d * e, ws=nb, plan=outs["plan"])
+    for o, i, got in _overlaps(grad, outs, ins, extra=(("dg", "pg"), ("du", "pu"))):
+        assert got == INV, (o, i)
+    at = {x: (i + 1) * SPOT for i, x in enumerate([*outs, *ins])}
+    for o, i in (("dg", "pg"), ("du", "pu")):                        # in place, or apart
+        for by in (16, -16, rows - 16, 16 - rows):
+            assert grad(**{**at, o: at[i] + by}) == INV, (o, i, by)
