@@ -724,11 +724,12 @@ int32_t lora_gated_grad(const void *dH, const void *pre_gate, const void *pre_up
  *   loss [T] float32; dX [T][d] dtype, or NULL for the loss alone.
  *   ws >= lora_cross_entropy_workspace_bytes(..., dX != NULL): tokens are taken
  *   in blocks whose exponentials (dtype) take at most 512 MiB.
+ * No output or workspace overlaps another buffer of the call.
  * A logit of +infinity or NaN makes its token's loss and gradient NaN, and no
  * other token's.  At most 2^20 tokens, V and d of 2^22 (UNSUPPORTED).  Results are
  * deterministic.
- * Errors: INVALID_ARG (null, alignment, an output that is an input, sizes),
- * UNSUPPORTED, CAPACITY, DEVICE. */
+ * Errors: INVALID_ARG (null, alignment, overlap, sizes), UNSUPPORTED, CAPACITY,
+ * DEVICE. */
 size_t lora_cross_entropy_workspace_bytes(int32_t T, int32_t V, int32_t d, int32_t dtype,
                                           int32_t with_grad);
 int32_t lora_cross_entropy(const void *X, const void *W_t, int32_t dtype, int32_t T, int32_t V,

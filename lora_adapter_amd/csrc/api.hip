@@ -1468,7 +1468,18 @@ int32_t lora_cross_entropy(const void *X, const void *W_t, int32_t dtype, int32_
   if (!aligned16(X) || !aligned16(W_t) || !aligned16(dX) || !aligned16(ws)) return LORA_ERR_INVALID_ARG;
   const void *out[] = {loss, dX, ws}, *in[] = {X, W_t, targets, weights};
   if (!outputs_apart(out, 3, in, 4)) return LORA_ERR_INVALID_ARG;
-  if (ws_bytes < lora_cross_entropy_workspace_bytes(T, V, d, dtype, dX != nullptr)) return LORA_ERR_CAPACITY;
+  const size_t need = lora_cross_entropy_workspace_bytes(T, V, d, dtype, dX != nullptr);
+  if (ws_bytes < need) return LORA_ERR_CAPACITY;
+  const size_t row = size_t(d) * (dtype == LORA_BF16 ? 2 : 4);
+  Ranges outs, ins;
+  outs.add(loss, size_t(T) * sizeof(float));
+  outs.add(dX, size_t(T) * row);
+  outs.add(ws, need);
+  ins.add(X, size_t(T) * row);
+  ins.add(W_t, size_t(V) * row);
+  ins.add(targets, size_t(T) * sizeof(int32_t));
+  ins.add(weights, size_t(T) * sizeof(float));
+  if (!outs.apart() || !outs.apart(ins)) return LORA_ERR_INVALID_ARG;
   CrossEntropyArgs a{};
   a.X = X; a.W = W_t; a.T = T; a.V = V; a.d = d;
   a.targets = targets; a.weights = weights; a.logit_scale = logit_scale;

@@ -375,3 +375,19 @@ def test_gated_buffers_that_overlap(B):
     for o, i in (("dg", "pg"), ("du", "pu")):                        # in place, or apart
         for by in (16, -16, rows - 16, 16 - rows):
             assert grad(**{**at, o: at[i] + by}) == INV, (o, i, by)
+
+
+def test_cross_entropy_buffers_that_overlap(B):
+    T, V, d = 300, 500, 128
+    for grad in (True, False):
+        n = B.lora_cross_entropy_workspace_bytes(T, V, d, B.LORA_BF16, grad)
+        outs, ins = dict(loss=T * 4, dX=T * d * 2, ws=n), dict(X=T * d * 2, W=V * d * 2, y=T * 4, w=T * 4)
+        if not grad:
+            del outs["dX"]
+
+        def call(**a):
+            return B.lib().lora_cross_entropy(a["X"], a["W"], B.LORA_BF16, T, V, d, a["y"], a["w"], 1.0, a["loss"],
+                                              a.get("dX"), a["ws"], n, None)
+
+        for o, i, got in _overlaps(call, outs, ins):
+            assert got == B.LORA_ERR_INVALID_ARG, (o, i)
