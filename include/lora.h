@@ -756,8 +756,9 @@ int32_t lora_cross_entropy(const void *X, const void *W_t, int32_t dtype, int32_
  *             listed before is skipped (its norm gets nothing from that layer).
  *   max_norm > 0, INFINITY for the norms alone;  norm [M + 1] float32 device.
  * Squares and sums are float64, in a fixed order.  At most 16384 adapters and
- * 1024 layers (UNSUPPORTED).  No two outputs, and no output and another
- * gradient, may overlap.  ws >= lora_clip_grad_workspace_bytes(...).
+ * 1024 layers (UNSUPPORTED).  No two outputs (norm and ws among them), and no
+ * output and another gradient, the list or a page table, may overlap.
+ * ws >= lora_clip_grad_workspace_bytes(...), 8-byte aligned.
  * Errors: INVALID_ARG (null, alignment, overlap, sizes), UNSUPPORTED, CAPACITY,
  * DEVICE. */
 typedef struct {

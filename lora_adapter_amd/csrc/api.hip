@@ -1497,11 +1497,16 @@ constexpr int32_t kMaxClipLayers = 1024;
 
 struct Span {
   uintptr_t at, end;
-  int32_t id;          // 2 x layer + factor
+  int32_t id;          // gradients and what replaces them: 2 x layer + factor
 };
 
-// The outputs are apart from each other, and from every gradient but the one
-// they replace in place.
+Span span(const void *p, size_t bytes, int32_t id) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  return {at, at + bytes, id};
+}
+
+// The outputs are apart from each other, and from every input but the gradient
+// that they replace in place.
 bool spans_apart(Span *out, int n_out, const Span *in, int n_in) {
   std::sort(out, out + n_out, [](const Span &a, const Span &b) { return a.at < b.at; });
   for (int i = 1; i < n_out; ++i)
@@ -1533,9 +1538,14 @@ int32_t lora_clip_grad(const lora_grad_desc *layers, int32_t n_layers, const int
     return LORA_ERR_INVALID_ARG;
   if (max_rank < 1 || max_rank > LORA_MAX_RANK || !(max_norm > 0.f)) return LORA_ERR_INVALID_ARG;
   if (n_layers > kMaxClipLayers || M > kMaxOrthAdapters) return LORA_ERR_UNSUPPORTED;
+  if (!aligned(norm, sizeof(float)) || !aligned(ws, sizeof(double))) return LORA_ERR_INVALID_ARG;
   ClipLayer l[kMaxClipLayers];
-  Span outs[2 * kMaxClipLayers], ins[2 * kMaxClipLayers];
-  int n = 0;
+  Span outs[2 * kMaxClipLayers + 2], ins[5 * kMaxClipLayers + 1];
+  int n = 0, n_in = 0;
+  const size_t need = lora_clip_grad_workspace_bytes(n_layers, M, max_rank);
+  outs[n++] = span(norm, (size_t(M) + 1) * sizeof(float), -1);
+  outs[n++] = span(ws, need, -2);
+  if (M > 0) ins[n_in++] = span(adapters, size_t(M) * sizeof(int32_t), -3);
   for (int32_t i = 0; i < n_layers; ++i) {
     const lora_grad_desc &g = layers[i];
     const int32_t st = check_pool(&g.pool, false);
@@ -1550,14 +1560,16 @@ int32_t lora_clip_grad(const lora_grad_desc *layers, int32_t n_layers, const int
       if ((!in[f] || !out[f]) && !none) return LORA_ERR_INVALID_ARG;
       if (!aligned16(in[f]) || !aligned16(out[f])) return LORA_ERR_INVALID_ARG;
       const size_t bytes = size_t(g.pool.n_pages) * size_t(l[i].d[f]) * sizeof(float);
-      const uintptr_t a = reinterpret_cast<uintptr_t>(in[f]), b = reinterpret_cast<uintptr_t>(out[f]);
       if (bytes == 0) continue;
-      ins[n] = Span{a, a + bytes, 2 * i + f};
-      outs[n++] = Span{b, b + bytes, 2 * i + f};
+      ins[n_in++] = span(in[f], bytes, 2 * i + f);
+      outs[n++] = span(out[f], bytes, 2 * i + f);
     }
+    ins[n_in++] = span(g.pool.rank, size_t(g.pool.n_adapters) * sizeof(int32_t), -3);
+    ins[n_in++] = span(g.pool.page_start, (size_t(g.pool.n_adapters) + 1) * sizeof(int32_t), -3);
+    if (g.pool.n_page_ids > 0) ins[n_in++] = span(g.pool.page_ids, size_t(g.pool.n_page_ids) * sizeof(int32_t), -3);
   }
-  if (!spans_apart(outs, n, ins, n)) return LORA_ERR_INVALID_ARG;
-  if (ws_bytes < lora_clip_grad_workspace_bytes(n_layers, M, max_rank)) return LORA_ERR_CAPACITY;
+  if (!spans_apart(outs, n, ins, n_in)) return LORA_ERR_INVALID_ARG;
+  if (ws_bytes < need) return LORA_ERR_CAPACITY;
   ClipArgs a{};
   a.adapters = adapters; a.M = M; a.max_rank = max_rank; a.together = together ? 1 : 0;
   a.max_norm = max_norm; a.norm = norm;

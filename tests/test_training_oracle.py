@@ -391,3 +391,31 @@ def test_cross_entropy_buffers_that_overlap(B):
 
         for o, i, got in _overlaps(call, outs, ins):
             assert got == B.LORA_ERR_INVALID_ARG, (o, i)
+
+
+def test_clip_buffers_that_overlap(B):
+    """Outputs, norm and workspace with gradients, the list and the page tables."""
+    L, M, R, N, P = B.lib(), 3, 16, 2, 4
+    n = L.lora_clip_grad_workspace_bytes(2, M, R)
+    a_, b_ = P * 128 * 4, P * 192 * 4
+    tables = {f"{t}{i}": s for i in (0, 1) for t, s in (("rank", N * 4), ("page_start", N * 4 + 4), ("page_ids", 12))}
+    outs = dict(oa0=a_, ob0=b_, oa1=a_, ob1=b_, norm=4 * M + 4, ws=n)
+    ins = dict(a0=a_, b0=b_, a1=a_, b1=b_, ads=4 * M, **tables)
+
+    def call(**a):
+        layers = [B.GradDesc(_pool(B, **{t: a[f"{t}{i}"] for t in ("rank", "page_start", "page_ids")}), a[f"a{i}"],
+                             a[f"b{i}"], a[f"oa{i}"], a[f"ob{i}"]) for i in (0, 1)]
+        return L.lora_clip_grad((B.GradDesc * 2)(*layers), 2, a["ads"], M, R, 1.0, 0, a["norm"], a["ws"],
+                                a.get("n", n), None)
+
+    place = [(o, f"{f}{i}") for i in (0, 1) for f in "ab" for o in (f"o{f}{i}",)]
+    for o, i, got in _overlaps(call, outs, ins, extra=place):
+        assert got == B.LORA_ERR_INVALID_ARG, (o, i)
+    at = {x: (i + 1) * SPOT for i, x in enumerate([*outs, *ins])}
+    for o, i in place:                                               # in place, or apart
+        for by in (16, -16, ins[i] - 16):
+            assert call(**{**at, o: at[i] + by}) == B.LORA_ERR_INVALID_ARG, (o, i, by)
+    assert call(**at, n=n - 1) == B.LORA_ERR_CAPACITY
+    assert call(**{**at, **{o: at[i] for o, i in place}}, n=n - 1) == B.LORA_ERR_CAPACITY
+    for name, by in (("norm", 1), ("norm", 2), ("ws", 1), ("ws", 4)):
+        assert call(**{**at, name: at[name] + by}, n=n - 1) == B.LORA_ERR_INVALID_ARG, (name, by)
