@@ -707,11 +707,24 @@ def _check_rows(pool: Pool, T: int, **tensors):
             raise ValueError(f"{name}: expected contiguous [{T}][{width}] of {size}-byte elements, got {tuple(t.shape)}")
 
 
+def _check_values(size: int, n: int, **tensors):
+    """Contiguous, n elements of `size` bytes or more: name=tensor or None."""
+    for name, t in tensors.items():
+        if t is not None and (t.numel() < n or t.element_size() != size or not t.is_contiguous()):
+            raise ValueError(f"{name}: expected {n} contiguous elements of {size} bytes, got {tuple(t.shape)} of {t.dtype}")
+
+
+def _check_routing(pool: Pool, T: int, K: int, gates, keep_mask, ids=None):
+    _check_values(4, T * K, ids=ids, gates=gates)
+    _check_values(1, T * pool.d_in, keep_mask=keep_mask)
+
+
 def lora_gated_apply(X, W_gate_t, W_up_t, activation: int, H, pre_gate, pre_up, T: int, K: int, gates,
                      keep_mask, keep_scale: float, gate: Pool, up: Pool, plan, ws_gate, ws_up, stream=None):
     F = gate.d_out
     _check_rows(gate, T, X=(X, gate.d_in), H=(H, F), pre_gate=(pre_gate, F), pre_up=(pre_up, F))
     _check_rows(gate, F, W_gate_t=(W_gate_t, gate.d_in), W_up_t=(W_up_t, gate.d_in))
+    _check_routing(gate, T, K, gates, keep_mask)
     _check("lora_gated_apply", lib().lora_gated_apply(
         _ptr(X), _ptr(W_gate_t), _ptr(W_up_t), activation, _ptr(H), _ptr(pre_gate), _ptr(pre_up), T, K,
         _ptr(gates), _ptr(keep_mask), float(keep_scale), gate.ref, up.ref, _ptr(plan), _ptr(ws_gate),
@@ -723,6 +736,7 @@ def lora_gated_forward(ids, gates, T: int, K: int, X, W_gate_t, W_up_t, activati
     F = gate.d_out
     _check_rows(gate, T, X=(X, gate.d_in), H=(H, F), pre_gate=(pre_gate, F), pre_up=(pre_up, F))
     _check_rows(gate, F, W_gate_t=(W_gate_t, gate.d_in), W_up_t=(W_up_t, gate.d_in))
+    _check_routing(gate, T, K, gates, keep_mask, ids)
     _check("lora_gated_forward", lib().lora_gated_forward(
         _ptr(ids), _ptr(gates), T, K, _ptr(X), _ptr(W_gate_t), _ptr(W_up_t), activation, _ptr(H),
         _ptr(pre_gate), _ptr(pre_up), _ptr(keep_mask), float(keep_scale), gate.ref, up.ref, _ptr(plan),
@@ -739,6 +753,7 @@ def lora_gated_grad(dH, pre_gate, pre_up, activation: int, W_gate, W_up, keep_ma
     _check_rows(gate, T, dH=(dH, F), pre_gate=(pre_gate, F), pre_up=(pre_up, F), d_gate=(d_gate, F),
                 d_up=(d_up, F), dX=(dX, gate.d_in))
     _check_rows(gate, gate.d_in, W_gate=(W_gate, F), W_up=(W_up, F))
+    _check_routing(gate, T, K, gates, keep_mask)
     _check("lora_gated_grad", lib().lora_gated_grad(
         _ptr(dH), _ptr(pre_gate), _ptr(pre_up), activation, _ptr(W_gate), _ptr(W_up), _ptr(keep_mask),
         float(keep_scale), T, K, _ptr(gates), gate.ref, up.ref, _ptr(plan), max_rank, _ptr(d_gate),
@@ -789,6 +804,7 @@ def lora_clip_grad(layers: GradLayers, adapters, M: int, max_rank: int, max_norm
                    ws, stream=None):
     if norm.numel() != M + 1 or norm.element_size() != 4 or not norm.is_contiguous():
         raise ValueError(f"norm: expected {M + 1} contiguous float32, got {tuple(norm.shape)}")
+    _check_values(4, M, adapters=adapters)
     _check("lora_clip_grad", lib().lora_clip_grad(
         layers.desc, layers.n, _ptr(adapters), M, max_rank, float(max_norm), int(together), _ptr(norm), _ptr(ws),
         _size(ws), _stream(stream)))

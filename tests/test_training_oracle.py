@@ -419,3 +419,32 @@ def test_clip_buffers_that_overlap(B):
     assert call(**{**at, **{o: at[i] for o, i in place}}, n=n - 1) == B.LORA_ERR_CAPACITY
     for name, by in (("norm", 1), ("norm", 2), ("ws", 1), ("ws", 4)):
         assert call(**{**at, name: at[name] + by}, n=n - 1) == B.LORA_ERR_INVALID_ARG, (name, by)
+
+
+def test_binding_checks_routing_and_lists(B):
+    """ids, gates, the mask and the list of adapters: their sizes and elements."""
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    f32, u8 = lambda *s: torch.zeros(*s), lambda *s: torch.zeros(*s, dtype=torch.uint8)
+    T, K, d, F = 3, 2, 128, 192
+    pool = B.Pool(B.LORA_BF16, d, F, bf(4, d), bf(4, F), i32(2), i32(3), i32(2), f32(2))
+    ws = u8(64)
+    bad = [("ids", i32(T, 1)), ("ids", i32(T, K).long()), ("ids", i32(K, T).T), ("gates", f32(T)), ("gates", f32(T, K).double()),
+           ("gates", f32(T, K).half()), ("keep_mask", u8(T, d - 1)), ("keep_mask", f32(T, d)), ("keep_mask", u8(d, T).T)]
+    for name, t in bad:
+        a = {"ids": i32(T, K), "gates": f32(T, K), "keep_mask": u8(T, d), name: t}
+        with pytest.raises(ValueError, match=name):
+            B.lora_gated_forward(a["ids"], a["gates"], T, K, bf(T, d), bf(F, d), bf(F, d), 0, bf(T, F), None, None,
+                                 a["keep_mask"], 1.0, pool, pool, ws, ws, ws, 0)
+        if name == "ids":
+            continue
+        with pytest.raises(ValueError, match=name):
+            B.lora_gated_apply(bf(T, d), bf(F, d), bf(F, d), 0, bf(T, F), None, None, T, K, a["gates"], a["keep_mask"],
+                               1.0, pool, pool, ws, ws, ws, 0)
+        with pytest.raises(ValueError, match=name):
+            B.lora_gated_grad(bf(T, F), bf(T, F), bf(T, F), 0, bf(d, F), bf(d, F), a["keep_mask"], 1.0, T, K, a["gates"],
+                              pool, pool, ws, 16, bf(T, F), bf(T, F), bf(T, d), ws, 0)
+    layers = B.GradLayers([(pool, f32(4, d), f32(4, F))])
+    for ads in (i32(1), i32(2).long(), i32(4)[::2]):
+        with pytest.raises(ValueError, match="adapters"):
+            B.lora_clip_grad(layers, ads, 2, 16, 1.0, False, f32(3), ws, 0)
