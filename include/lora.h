@@ -723,7 +723,8 @@ int32_t lora_gated_grad(const void *dH, const void *pre_gate, const void *pre_up
  *   their X holds.  logit_scale is finite and not 0.
  *   loss [T] float32; dX [T][d] dtype, or NULL for the loss alone.
  *   ws >= lora_cross_entropy_workspace_bytes(..., dX != NULL): tokens are taken
- *   in blocks whose exponentials (dtype) take at most 512 MiB.
+ *   in blocks whose exponentials (dtype) and, with dX, whose sums (float32) take
+ *   at most 512 MiB each, of 256 tokens (float32: 64) at least.
  * No output or workspace overlaps another buffer of the call.
  * A logit of +infinity or NaN makes its token's loss and gradient NaN, and no
  * other token's.  At most 2^20 tokens, V and d of 2^22 (UNSUPPORTED).  Results are

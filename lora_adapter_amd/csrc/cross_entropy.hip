@@ -18,8 +18,10 @@
 // common reference to wait for, and the sums of each piece; a small one makes
 // S, the loss and the two coefficients of each row; the second product is
 // e.W, split along the vocabulary.  Memory is bounded by taking the tokens in
-// blocks (kBlockBytes of e).  Tokens without a target are left out before the
+// blocks (kBlockBytes of e, and of the float32 sums of dX).  Tokens without a target are left out before the
 // first product, by a list of the others.
+#include <algorithm>
+
 #include "tile_f32.h"
 #include "tile_loop.h"
 
@@ -27,7 +29,7 @@ namespace lora {
 namespace {
 
 constexpr int kSub = 64;                               // columns of one piece of a row
-constexpr size_t kBlockBytes = size_t(512) << 20;      // e of one block of tokens
+constexpr size_t kBlockBytes = size_t(512) << 20;      // e, and the sums of dX, of one block of tokens
 constexpr int kMaxSplits = 64;                         // whose sums one thread adds up
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kMaxExp = 64.f;                        // a piece's exponents over this are shifted
@@ -507,8 +509,10 @@ CeWs ce_layout(char *ws, int T, int V, int d, int dtype, bool grad) {
   const int tile = dtype == LORA_BF16 ? 256 : 64;
   w.lde = (int64_t(V) + 63) / 64 * 64;
   w.pieces = int(w.lde / kSub);
-  // rows of a block: as many as kBlockBytes hold, the blocks alike
-  int64_t most = int64_t(kBlockBytes / (size_t(w.lde) * e)) / tile * tile;
+  // rows of a block: as many as kBlockBytes hold of the exponentials and, with a gradient,
+  // of its float32 sums, the blocks alike.  (Several splits take 64 MiB of sums at most:
+  // they are for outputs of few tiles.)
+  int64_t most = int64_t(kBlockBytes / std::max(size_t(w.lde) * e, grad ? size_t(d) * 4 : 0)) / tile * tile;
   if (most < tile) most = tile;
   const int64_t blocks = (T + most - 1) / most;
   int64_t rows = blocks > 0 ? (T + blocks - 1) / blocks : 1;

@@ -205,6 +205,40 @@ def test_several_blocks_of_tokens():
     assert not bool(loss[gone].any()) and not bool(dX[gone].any())
 
 
+@pytest.mark.parametrize("dtype,T", [("bf16", 40000), ("f32", 33100)])
+def test_several_blocks_of_wide_tokens(dtype, T):
+    """A small vocabulary under wide states: the blocks hold the sums of dX; the
+    reference by torch in 64 bits on the GPU."""
+    V, d = 300, 4096
+    n = B.lora_cross_entropy_workspace_bytes(T, V, d, CODE[dtype])
+    assert n < T * d * 4 < 700 << 20
+    gen = torch.Generator("cuda").manual_seed(T)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    W = (r(V, d) * d ** -0.5).to(DT[dtype])
+    X, w = r(T, d).to(DT[dtype]), torch.rand(T, generator=gen, device="cuda") + 0.5
+    y = torch.randint(0, V, (T,), generator=gen, device="cuda", dtype=torch.int32)
+    y[torch.rand(T, generator=gen, device="cuda") < 0.1] = -1
+    loss, dX = run(X, W, y, w)
+    Wd, half = W.double(), HALF[dtype]
+    for t0 in (0, T // 2 - 500, T - 1000):
+        t = t0 + torch.nonzero(y[t0:t0 + 1000] >= 0)[:, 0]
+        k, c = torch.arange(t.numel(), device="cuda"), y[t].long()
+        L = X[t].double() @ Wd.t()
+        e = (d + 8) * EPS * (X[t].double().abs() @ Wd.abs().t()) + 2 * EPS * (L.abs() + L[k, c].abs()[:, None]) + 2.0 ** -22
+        P = torch.softmax(L, 1)
+        ref = -w[t].double() * torch.log_softmax(L, 1)[k, c]
+        Q = P.clone()
+        Q[k, c] = 0
+        shift = (Q * e).sum(1) + (V + 4) * EPS
+        assert bool(((loss[t].double() - ref).abs() <= 1.02 * w[t] * shift + 4 * EPS * ref.abs()).all())
+        g = w[t].double()[:, None] * (P @ Wd - Wd[c])
+        tol = 1.02 * w[t].double()[:, None] * ((Q * (e + half + (V + 8) * EPS + shift[:, None])) @ Wd.abs()
+                                               + (Q.sum(1) * (shift + e.max(1)[0] + half + (V + 8) * EPS))[:, None] * Wd[c].abs())
+        assert bool(((dX[t].double() - g).abs() <= tol + half * (g.abs() + tol)).all()), t0
+    gone = y < 0
+    assert not bool(loss[gone].any()) and not bool(dX[gone].any())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_gradient_is_the_differences_of_the_loss(dtype):
     X, W, y, w = make(20, 300, 64, "f32", ignored=0.2)

@@ -448,3 +448,13 @@ def test_binding_checks_routing_and_lists(B):
     for ads in (i32(1), i32(2).long(), i32(4)[::2]):
         with pytest.raises(ValueError, match="adapters"):
             B.lora_clip_grad(layers, ads, 2, 16, 1.0, False, f32(3), ws, 0)
+
+
+def test_cross_entropy_workspace_is_bounded(B):
+    """Exponentials and sums of a block of tokens, whichever are larger, and 20 bytes a token."""
+    for dtype in (B.LORA_BF16, B.LORA_F32):
+        for V, d in ((64, 4096), (1, 8192), (8192, 1024), (128256, 4096), (2000, 1024)):
+            n = B.lora_cross_entropy_workspace_bytes(1 << 20, V, d, dtype)
+            # e, sums, a sixteenth of e for the pieces' sums, 64 MiB of splits, lists
+            assert n < (512 << 20) * 2.07 + (64 << 20) + 24 * (1 << 20), (dtype, V, d, n)
+            assert B.lora_cross_entropy_workspace_bytes(1 << 20, V, d, dtype, False) < 80 << 20
