@@ -252,6 +252,23 @@ def test_gradient_is_the_differences_of_the_loss(dtype):
     assert np.all(np.abs((up - dn) / (2 * h) - along) <= f64(w) * (h * h * spread ** 3 + 4e-6 / h))
 
 
+def test_bf16_gradient_is_the_differences_of_a_64_bit_loss():
+    X, W, y, w = make(60, 300, 128, "bf16", seed=4, ignored=0.2)
+    Xd, Wd, yd, wd = f64(X), f64(W), y.cpu().numpy(), f64(w)
+    V = np.random.default_rng(5).standard_normal(Xd.shape)
+    dX = f64(run(X, W, y, w)[1])
+    h = 1e-4
+    up, dn = (R.cross_entropy(Xd + s * V, Wd, yd, wd)[0] for s in (h, -h))
+    along, (loss, ref, P) = (dX * V).sum(1), R.cross_entropy(Xd, Wd, yd, wd)
+    # dX by element as above; third derivatives of a log-sum-exp are at most the cube of the
+    # logits' spread along V; the losses' own 2^-52 over h
+    tol = (tolerances(Xd, Wd, yd, wd, 1.0, loss, ref, P, HALF["bf16"])[1] * np.abs(V)).sum(1)
+    spread = np.abs(V @ Wd.T).max(1)
+    assert np.all(np.abs((up - dn) / (2 * h) - along) <= tol + wd * (h * h * spread ** 3) + 1e-14 * (1 + loss) / h)
+    listed = yd >= 0
+    assert (np.abs(along[listed]) > 4 * tol[listed]).sum() > 10      # the directions say something
+
+
 def test_captured_and_beside_another_stream():
     X, W, y, w = make(300, 1100, 128, "bf16")
     ref = [t.clone() for t in run(X, W, y, w)]

@@ -319,6 +319,7 @@ def test_cross_entropy_of_rows_past_32_bits():
 def test_more_elements_than_one_grid_dimension_has_threads():
     """2^20 tokens of 32832: d_gate and d_up in place."""
     T, F = 1 << 20, 32832
+    torch.cuda.empty_cache()
     if torch.cuda.mem_get_info()[0] < 215 << 30:
         pytest.skip("needs 215 GB of device memory")
     b = Block(1, 1, 64, F, seed=3)
@@ -407,3 +408,96 @@ def test_pages_that_are_not_finite_stay_with_their_rows(T, K, d, F, dtype, value
         assert torch.equal(a[~own], c[~own]), what
         # G = d.B is not finite for the adapter's pairs, and so is U = X.A: all its columns
         assert not bool(torch.isfinite(a[own]).all(1).any()), what
+
+
+# ---------------------------------------------------------------- values that are not finite, by kind and place
+
+def signs(v, value):
+    """What v . value adds to a finite sum: an infinity's sign, NaN; 0 where |v| is too
+    near 0 for its sign to be known in float32."""
+    if np.isnan(value):
+        return np.full(v.shape, np.nan)
+    return np.sign(v) * np.sign(value)
+
+
+def check_kinds(got, clean, rows, cols, want, what):
+    """got equals clean bit for bit but at (rows, cols), where it is want . inf (NaN: NaN)."""
+    at = torch.zeros(got.shape, dtype=torch.bool, device="cuda")
+    at[torch.from_numpy(rows).cuda()[:, None], torch.from_numpy(cols).cuda()] = True
+    assert torch.equal(got[~at], clean[~at]), what
+    have = f64(got)[rows][:, cols]
+    want = np.broadcast_to(want[:, None], have.shape)
+    assert not np.isfinite(have).any(), what
+    nan = np.isnan(want)
+    assert np.isnan(have[nan]).all(), what
+    known = ~nan & (want != 0)
+    assert np.array_equal(have[known], want[known] * np.inf), what
+
+
+def own_rows(b, bad, p):
+    """The tokens with pairs of adapter `bad`, and those pairs' coefficients added up
+    (gates and scales are positive)."""
+    rows = np.flatnonzero(((b.ids == bad) & (b.gates != 0)).any(1))
+    c = (b.gates * (b.ids == bad)).sum(1)[rows] * float(b.scale[p][bad]) * b.keep
+    return rows, c
+
+
+VALUES = [float("inf"), float("-inf"), float("nan")]
+
+
+# one slot and several; decode, terms apart and in turn, tiles with ranks up to 16 and past it
+@pytest.mark.parametrize("T,K,d,F,dtype,hi", [(5, 1, 128, 192, "bf16", 12), (5, 2, 128, 192, "bf16", 40),
+                                              (150, 1, 64, 320, "bf16", 40), (200, 2, 1600, 448, "bf16", 12),
+                                              (140, 5, 1600, 192, "bf16", 20), (4200, 1, 128, 1984, "bf16", 12),
+                                              (4200, 1, 128, 1984, "bf16", 40), (4200, 2, 128, 1984, "bf16", 20),
+                                              (70, 1, 576, 192, "f32", 12), (70, 2, 576, 192, "f32", 40),
+                                              (70, 5, 128, 192, "f32", 20)])
+@pytest.mark.parametrize("value", VALUES)
+def test_b_pages_that_are_not_finite(T, K, d, F, dtype, hi, value):
+    b = Block(T, K, d, F, dtype, seed=T + hi, lo=max(1, hi - 6), hi=hi, N=4)
+    bad, cols = 2, np.arange(5, F, 37)
+    clean = [t.clone() for t in G.run_forward(b, "silu")]
+    j = int(b.rank[bad]) - 1
+    page = int(b.page_ids[b.start[bad] + j])
+    for p in range(2):
+        b.Bp[p][page, torch.from_numpy(cols).cuda()] = value
+    got = G.run_forward(b, "silu")
+    for p, what in enumerate("gu"):
+        rows, c = own_rows(b, bad, p)
+        assert 0 < rows.size < T
+        z, a = f64(b.X)[rows], f64(b.A[p])[page]
+        U = c * (z @ a)
+        U[np.abs(U) < (d + 8) * EPS * c * (np.abs(z) @ np.abs(a))] = 0
+        check_kinds(got[1 + p], clean[1 + p], rows, cols, signs(U, value), what)
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    keep[torch.from_numpy(rows).cuda()] = False
+    assert torch.equal(got[0][keep], clean[0][keep])
+
+
+# the split product with terms apart and in turn, whole tiles
+@pytest.mark.parametrize("T,K,d,F,dtype,hi", [(5, 1, 128, 192, "bf16", 12), (150, 2, 64, 320, "bf16", 40),
+                                              (200, 2, 1600, 448, "bf16", 12), (140, 5, 1600, 192, "bf16", 20),
+                                              (8200, 1, 1536, 64, "bf16", 12), (8200, 1, 1536, 64, "bf16", 40),
+                                              (12400, 2, 960, 64, "bf16", 20), (70, 1, 576, 192, "f32", 12),
+                                              (70, 2, 576, 192, "f32", 40), (70, 5, 128, 192, "f32", 20)])
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("value", VALUES)
+def test_a_pages_that_are_not_finite(T, K, d, F, dtype, hi, which, value):
+    b = Block(T, K, d, F, dtype, seed=T + hi, lo=max(1, hi - 6), hi=hi, N=4)
+    bad, cols = 2, np.arange(5, d, 37)
+    W = [w.t().contiguous() for w in b.W]
+    gen = torch.Generator("cuda").manual_seed(T)
+    g, u = (torch.randn(T, F, generator=gen, device="cuda").to(DT[dtype]) for _ in range(2))
+    B.lora_plan(b.d_ids, b.d_gates, T, K, b.pools[0], b.plan)
+    clean = [t.clone() for t in G.run_grad(b, "silu", g, u, W)]
+    j = int(b.rank[bad]) - 1
+    page = int(b.page_ids[b.start[bad] + j])
+    b.A[which][page, torch.from_numpy(cols).cuda()] = value
+    got = G.run_grad(b, "silu", g, u, W)
+    assert torch.equal(got[0], clean[0]) and torch.equal(got[1], clean[1])
+    rows, c = own_rows(b, bad, which)
+    assert 0 < rows.size < T
+    z, a = f64(got[which])[rows], f64(b.Bp[which])[page]
+    C = c * (z @ a)
+    C[np.abs(C) < (F + 8) * EPS * c * (np.abs(z) @ np.abs(a))] = 0
+    check_kinds(got[2], clean[2], rows, cols, signs(C, value), "dX")
