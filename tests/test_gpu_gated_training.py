@@ -501,3 +501,84 @@ def test_a_pages_that_are_not_finite(T, K, d, F, dtype, hi, which, value):
     C = c * (z @ a)
     C[np.abs(C) < (F + 8) * EPS * c * (np.abs(z) @ np.abs(a))] = 0
     check_kinds(got[2], clean[2], rows, cols, signs(C, value), "dX")
+
+
+# ---------------------------------------------------------------- the forward's whole tiles
+
+def whole(b):
+    """Whether the forward takes tiles that finish themselves: 256 or more of 256 x 256, and then
+    nothing lies before U in the workspace."""
+    return B.lora_apply_u_offset(b.T, b.K, b.d, b.F, CODE[b.dtype]) == 0
+
+
+@pytest.mark.parametrize("T,K,d,F,hi,runs", [(257, 1, 64, 32576, 16, False), (300, 2, 128, 32576, 16, False),
+                                             (500, 1, 64, 32576, 70, True), (400, 1, 192, 32576, 33, False),
+                                             (511, 3, 64, 32576, 40, True), (300, 8, 64, 32576, 12, False),
+                                             (3841, 1, 128, 3904, 16, True), (3900, 2, 64, 3904, 24, False)])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_forward_of_whole_tiles(T, K, d, F, hi, runs, act):
+    b = Block(T, K, d, F, seed=T + hi, lo=0, hi=hi, runs=runs, N=9, mask=T % 2 == 1)
+    assert whole(b)
+    G.check_forward(b, act, stored=act == "silu")
+
+
+@pytest.mark.parametrize("K,hi", [(1, 12), (1, 40), (2, 20)])
+@pytest.mark.parametrize("value", VALUES)
+def test_b_pages_that_are_not_finite_in_whole_tiles(K, hi, value):
+    b = Block(300, K, 64, 32576, seed=hi, lo=hi - 6, hi=hi, N=4)
+    assert whole(b)
+    test_b_pages_that_are_not_finite(300, K, 64, 32576, "bf16", hi, value)
+
+
+@pytest.mark.parametrize("K", [1, 2])
+def test_whole_tiles_of_plan_then_apply_and_captured(K):
+    """lora_gated_apply on lora_plan's plan, and a captured forward replayed beside other
+    work, against lora_gated_forward, bit for bit; U of both where lora_grad finds it."""
+    T, d, F = 300, 128, 32576
+    b = Block(T, K, d, F, seed=5, mask=True, hi=20)
+    assert whole(b)
+    one = [t.clone() for t in G.run_forward(b, "silu")]
+    n = 4 * int(B.lora_plan_header(b.plan)[B.PH_RPAIRS])
+    u = [w[:n].clone() for w in b.ws]
+    B.lora_plan(b.d_ids, b.d_gates, T, K, b.pools[0], b.plan)
+    H, g, up = b.out(F), b.out(F), b.out(F)
+    B.lora_gated_apply(b.X, *b.W, ACTS["silu"], H.t, g.t, up.t, T, K, b.d_gates, b.d_mask, b.keep, *b.pools, b.plan,
+                       *b.ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip((H.t, g.t, up.t), one))
+    assert all(torch.equal(x, w[:n]) for x, w in zip(u, b.ws))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.forward("silu", H.t, g.t, up.t)
+    other = Block(T, K, d, F, seed=6)
+    for _ in range(3):
+        for o in (H, g, up):
+            o.t.zero_()
+        G.run_forward(other, "gelu")
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip((H.t, g.t, up.t), one))
+
+
+def test_whole_tiles_of_tokens_without_adapters():
+    """Tokens without an active slot equal the base product's, wherever they lie; and all of them."""
+    b = Block(500, 1, 64, 32576, seed=2, N=5)
+    assert whole(b)
+    H = G.run_forward(b, "silu")[0].clone()
+    idle = torch.from_numpy(np.flatnonzero((b.ids[:, 0] < 0) | (b.rank[np.maximum(b.ids[:, 0], 0)] == 0))).cuda()
+    b.ids[:] = -1
+    b.d_ids.fill_(-1)
+    base = G.run_forward(b, "silu")[0]
+    assert idle.numel() > 20 and torch.equal(H[idle], base[idle])
+    G.check_forward(b, "silu")
+
+
+@pytest.mark.parametrize("which", [0, 1])
+def test_whole_tiles_without_room_for_u(which):
+    assert B.lora_apply_u_offset(300, 1, 64, 32576, B.LORA_BF16) == 0
+    b = Block(300, 1, 64, 32576, seed=6, lo=12, hi=16, empty=False)
+    b.ws[which] = workspace(B.lora_apply_workspace_bytes(300, 1, 64, 32576, 1, B.LORA_BF16))
+    H = G.run_forward(b, "silu")[0]
+    assert int(b.plan.view(torch.int32)[B.PH_ERR]) & B.DEVERR_CAPACITY
+    b.ids = np.full_like(b.ids, -1)
+    near(H, *G.expected(b, "silu")[0], "H")
