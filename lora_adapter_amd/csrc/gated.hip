@@ -75,7 +75,9 @@ constexpr int kTermLds = 4096;             // bytes of LDS per wave
 
 template <typename C>
 struct TileSegs {
-  int ps[C::BM], z[C::BM], lead[C::BM];    // page start (-1: none), U offset and list entry of each row
+  // page start (-1: none), rank, U offset and list entry of each row.  An adapter's
+  // pages are its page start and rank: two may share the start.
+  int ps[C::BM], rk[C::BM], z[C::BM], lead[C::BM];
   int l_ps[C::BM], l_r[C::BM], l_blocks[C::BM];
   int cnt[C::BM / 64], n;
 };
@@ -95,6 +97,7 @@ __device__ __forceinline__ void list_segs(TileSegs<C> &t, int4 sd) {
   lds_bar();                               // the last list is done with
   if (r < C::BM) {
     t.ps[r] = sd.x >= 0 ? sd.w : -1;
+    t.rk[r] = sd.y;
     t.z[r] = sd.z;
     t.l_blocks[r] = 0;
   }
@@ -103,9 +106,13 @@ __device__ __forceinline__ void list_segs(TileSegs<C> &t, int4 sd) {
   bool leads = false;
   if (r < C::BM && sd.x >= 0) {
     for (int i = 0; i < r; i += 4) {
-      const int4 v = *reinterpret_cast<const int4 *>(&t.ps[i]);
-      if (v.x == sd.w || v.y == sd.w || v.z == sd.w || v.w == sd.w) {
-        first = i + (v.x == sd.w ? 0 : v.y == sd.w ? 1 : v.z == sd.w ? 2 : 3);
+      const int4 v = *reinterpret_cast<const int4 *>(&t.ps[i]), q = *reinterpret_cast<const int4 *>(&t.rk[i]);
+      // (0: equal.  With && the compiler spills elsewhere in the tile of dX: 8192 tokens
+      // 1395 -> 1500 us)
+      const int m0 = (v.x ^ sd.w) | (q.x ^ sd.y), m1 = (v.y ^ sd.w) | (q.y ^ sd.y);
+      const int m2 = (v.z ^ sd.w) | (q.z ^ sd.y), m3 = (v.w ^ sd.w) | (q.w ^ sd.y);
+      if (m0 == 0 || m1 == 0 || m2 == 0 || m3 == 0) {
+        first = i + (m0 == 0 ? 0 : m1 == 0 ? 1 : m2 == 0 ? 2 : 3);
         break;
       }
     }
@@ -306,7 +313,7 @@ __device__ __forceinline__ unsigned add_segs(const Terms &e, const TileSegs<C> &
 template <bool kPair>
 struct TermCache {
   static constexpr int NF = kPair ? 4 : 8;
-  int key = -1;                            // first page id's place, or -1
+  int key = -1, rank = 0;                  // the adapter's page start, or -1, and rank
   bool dropped = false;                    // its values that are not finite were left out
   bf16x8_t b[NF];                          // kPair: gate 0, 1, up 0, 1; else gate 0 .. 3, up 0 .. 3
 };
@@ -339,6 +346,7 @@ __device__ __forceinline__ void load_terms(const Terms &e, char *lds, int at, in
   }
   t.dropped = __ballot(bad) != 0;
   t.key = at;
+  t.rank = nr;
   // B operand: lane (column lane % 16, rank rows 8 (lane / 16 % 2) .. + 7)
   constexpr int NB = kPair ? 2 : 4;        // blocks of a projection
   typedef __attribute__((address_space(3))) v4i16_t lds_v4;
@@ -421,7 +429,7 @@ __device__ __forceinline__ bool add_tile_terms(const Terms &e, const TileTerms<C
     pending &= ~__ballot(mine);
     bf16x8_t um[2] = {u[0], u[1]};
     if (!mine) um[0] = um[1] = bf16x8_t{};
-    if (t.key != kps) load_terms<kPair>(e, lds, kps, kr, c0, N, t);
+    if (t.key != kps || t.rank != kr) load_terms<kPair>(e, lds, kps, kr, c0, N, t);
     dropped |= t.dropped;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {

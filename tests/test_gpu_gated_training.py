@@ -582,3 +582,36 @@ def test_whole_tiles_without_room_for_u(which):
     assert int(b.plan.view(torch.int32)[B.PH_ERR]) & B.DEVERR_CAPACITY
     b.ids = np.full_like(b.ids, -1)
     near(H, *G.expected(b, "silu")[0], "H")
+
+
+# ---------------------------------------------------------------- adapters that share pages
+
+class NestedBlock(Block):
+    """The pages of adapter 0 are the first of adapter 2's, or the other way round (1, between
+    them, is no adapter: its page_start is not consistent, and no token names it); adapter 3
+    has some of them too."""
+
+    def __init__(self, T, K, d, F, dtype, r0, r2, seed):
+        top, low = max(r0, r2), min(r0, r2)
+        super().__init__(T, K, d, F, dtype, N=4, lo=top, hi=top, seed=seed, mask=True)
+        self.rank[:] = (r0, 1, r2, low)
+        self.start[:] = (0, r0, 0, r2, r2 + low)
+        self.ids[self.ids == 1] = 2
+        for t, a in ((self.d_rank, self.rank), (self.d_start, self.start), (self.d_ids, self.ids)):
+            t.copy_(torch.from_numpy(a))
+
+
+@pytest.mark.parametrize("T,K,d,F,dtype,r0,r2", [(5, 2, 128, 192, "bf16", 12, 5), (200, 2, 1600, 448, "bf16", 30, 7),
+                                                 (140, 5, 1600, 192, "bf16", 12, 5), (300, 1, 64, 32576, "bf16", 12, 9),
+                                                 (300, 1, 64, 32576, "bf16", 9, 12), (300, 1, 64, 32576, "bf16", 40, 33),
+                                                 (300, 2, 64, 32576, "bf16", 12, 5), (300, 2, 64, 32576, "bf16", 40, 9),
+                                                 (70, 2, 576, 192, "f32", 30, 7)])
+def test_forward_of_adapters_that_share_pages(T, K, d, F, dtype, r0, r2):
+    G.check_forward(NestedBlock(T, K, d, F, dtype, r0, r2, seed=T + r0), "silu")
+
+
+@pytest.mark.parametrize("T,K,d,F,dtype,r0,r2", [(5, 2, 128, 192, "bf16", 12, 5), (200, 2, 1600, 448, "bf16", 30, 7),
+                                                 (8200, 1, 1536, 64, "bf16", 9, 12), (8200, 1, 1536, 64, "bf16", 40, 33),
+                                                 (12400, 2, 960, 64, "bf16", 12, 5), (70, 2, 576, 192, "f32", 30, 7)])
+def test_gradient_of_adapters_that_share_pages(T, K, d, F, dtype, r0, r2):
+    G.check_grad(NestedBlock(T, K, d, F, dtype, r0, r2, seed=T + r0), "silu")
