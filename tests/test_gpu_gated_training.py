@@ -615,3 +615,36 @@ def test_forward_of_adapters_that_share_pages(T, K, d, F, dtype, r0, r2):
                                                  (12400, 2, 960, 64, "bf16", 12, 5), (70, 2, 576, 192, "f32", 30, 7)])
 def test_gradient_of_adapters_that_share_pages(T, K, d, F, dtype, r0, r2):
     G.check_grad(NestedBlock(T, K, d, F, dtype, r0, r2, seed=T + r0), "silu")
+
+
+# ---------------------------------------------------------------- the shrinks' forms
+
+# big segments (512 pairs or more, widths of multiples of 128) beside units in one launch or in two,
+# units whose rows stay in registers or not; sums of more than 4 and 8 splits
+@pytest.mark.parametrize("T,K,d,F,dtype,N", [(600, 1, 128, 128, "bf16", 3), (520, 2, 4096, 128, "bf16", 5),
+                                             (600, 1, 4224, 128, "bf16", 3), (530, 2, 6144, 128, "bf16", 30),
+                                             (600, 1, 6272, 128, "bf16", 3), (200, 1, 4160, 64, "bf16", 6),
+                                             (200, 1, 6208, 64, "bf16", 6), (5, 1, 9280, 128, "bf16", 3),
+                                             (100, 2, 6208, 192, "bf16", 6), (70, 1, 2112, 64, "f32", 4),
+                                             (70, 2, 1984, 128, "f32", 4)])
+@pytest.mark.parametrize("mask", [False, True])
+def test_forward_of_wide_rows(T, K, d, F, dtype, N, mask):
+    b = Block(T, K, d, F, dtype, N=N, seed=d, mask=mask, lo=0, hi=20)
+    G.check_forward(b, "silu")
+    # the same by a plan that is there: the shrinks of its order, at decode sizes too
+    one = [t.clone() for t in G.run_forward(b, "silu")]
+    B.lora_plan(b.d_ids, b.d_gates, T, K, b.pools[0], b.plan)
+    H, g, u = b.out(F), b.out(F), b.out(F)
+    B.lora_gated_apply(b.X, *b.W, ACTS["silu"], H.t, g.t, u.t, T, K, b.d_gates, b.d_mask, b.keep, *b.pools, b.plan, *b.ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x.t, y) for x, y in zip((H, g, u), one))
+
+
+@pytest.mark.parametrize("T,K,d,F,dtype,N", [(600, 1, 128, 128, "bf16", 3), (520, 2, 128, 4096, "bf16", 5),
+                                             (600, 1, 128, 4224, "bf16", 3), (530, 2, 128, 6144, "bf16", 30),
+                                             (600, 1, 128, 6272, "bf16", 3), (200, 1, 64, 4160, "bf16", 6),
+                                             (200, 1, 64, 6208, "bf16", 6), (8200, 1, 1536, 128, "bf16", 4),
+                                             (70, 1, 64, 2112, "f32", 4), (70, 2, 128, 1984, "f32", 4)])
+@pytest.mark.parametrize("mask", [False, True])
+def test_gradient_of_wide_rows(T, K, d, F, dtype, N, mask):
+    G.check_grad(Block(T, K, d, F, dtype, N=N, seed=F, mask=mask, lo=0, hi=20), "silu")
