@@ -717,7 +717,7 @@ int32_t lora_gated_grad(const void *dH, const void *pre_gate, const void *pre_up
  *   dX[t] = round( w[t] . logit_scale . (sum_v softmax(l)[v].W_t[v] - W_t[y[t]]) )
  *   X [T][d], W_t [V][d] dtype, 16-byte aligned; any V >= 1, d a multiple of 64;
  *   targets [T] int32: below 0 ignored.  V or more: the token's loss is NaN,
- *   and it is ignored otherwise.  weights [T] float32 or NULL (1 each): a mean
+ *   whatever its weight, and it is ignored otherwise.  weights [T] float32 or NULL (1 each): a mean
  *   over a job's tokens is 1 / their number; a weight of 0 ignores the token.
  *   Ignored tokens cost nothing, have a loss of 0 and a gradient of 0, whatever
  *   their X holds.  logit_scale is finite and not 0.
@@ -751,7 +751,8 @@ int32_t lora_cross_entropy(const void *X, const void *W_t, int32_t dtype, int32_
  *             its widths) and float32 pages as lora_grad writes them, 16-byte
  *             aligned.  dA_out may be dA_pages (in place; rows whose factor is 1
  *             are then not written) or other pages of the same layout; dB_out so.
- *             Pages of adapters that are not listed are neither read nor written.
+ *             Pages of adapters that are not listed are neither read nor written;
+ *             listed ones share no page with each other.
  *   adapters  [M] int32 device; in a layer, one that is out of range there, of
  *             rank 0 or above max_rank, with an inconsistent page table, or
  *             listed before is skipped (its norm gets nothing from that layer).

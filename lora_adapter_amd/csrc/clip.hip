@@ -180,7 +180,7 @@ int clip_rows(int n_layers, int M, int max_rank) {
 // its entry's itself, and one (or, with one norm for all, each) adds them all: 8
 // loads of a thread, below the launches between the passes.  7 layers of 1024 ->
 // 1024, a norm for each entry: 896 partials 10.5 us against 12.7 with the launches,
-// 1792 13.3 and 14.4, 3584 21.9 and 21.4, 28672 138 and 117.
+// 1792 13.3 and 14.4, 3584 21.9 and 21.4; of 1024 -> 2048, 28672 138 and 117.
 constexpr int64_t kOwnParts = 2048;
 
 }  // namespace

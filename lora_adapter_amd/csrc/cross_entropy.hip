@@ -14,12 +14,15 @@
 // (a whole number, so that putting the pieces on one shift later is exact).
 //
 // So the products run once each: the first launch of a block of tokens leaves
-// e in bf16 (float32 layers: float32), relative error 2^-9 of each term and no
-// common reference to wait for, and the sums of each piece; a small one makes
-// S, the loss and the two coefficients of each row; the second product is
-// e.W, split along the vocabulary.  Memory is bounded by taking the tokens in
-// blocks (kBlockBytes of e, and of the float32 sums of dX).  Tokens without a target are left out before the
-// first product, by a list of the others.
+// e in bf16 (float32 layers: float32), with no common reference to wait for, and
+// the sums of each piece; a small one makes S, the loss and the two coefficients
+// of each row; the second product is e.W, split along the vocabulary.  bf16 is what
+// its MFMAs take: each e is off by 2^-8 of itself at most and S is not, so that
+// dX is off by 2^-8 |w scale| sum over v != y of p_v |W_v| beside its own
+// rounding, as much where W_y and the likely rows are alike and the two sums
+// nearly cancel.  Memory is bounded by taking the tokens in blocks (kBlockBytes of
+// e, and of the float32 sums of dX).  Tokens without a target are left out before
+// the first product, by a list of the others.
 #include <algorithm>
 
 #include "tile_f32.h"

@@ -1202,6 +1202,10 @@ __global__ __launch_bounds__(256) void gated_base_f32_kernel(GatedArgs g, PlanAr
 }
 
 // ------------------------------------------------------------ backward
+// d_gate and d_up, rounded to the layer's type: they are outputs, and lora_grad, the
+// shrinks and dX's product all read them so, the MFMAs taking bf16 operands.  In dX
+// each term then carries that half step too (bf16, 600 tokens: dX is 2.3e-3 of its norm
+// from 64 bits, and 1.7e-3 with float32 ones, its own rounding).
 template <typename E, int kAct>
 __global__ __launch_bounds__(256) void gated_act_grad_kernel(const E *dH, const E *pg, const E *pu, E *dg, E *du,
                                                              int64_t n8) {
@@ -1476,7 +1480,7 @@ hipError_t launch_gated(const GatedArgs &g, hipStream_t s) {
   return hipGetLastError();
 }
 
-// With at most `most` splits: 512 float32 workgroups, at least 4 K tiles of 64 each.
+// With at most `most` splits: 768 float32 workgroups, at least 4 K tiles of 64 each.
 int gated_base_splits(int M, int N, int Kd, int dtype, int most) {
   if (dtype == LORA_BF16) return 1;
   const int64_t tiles = int64_t((M + 63) / 64) * (N / 32);

@@ -620,9 +620,9 @@ hipError_t launch_clip(const ClipLayer *layers, int n_layers, ClipArgs a, void *
 size_t cross_entropy_workspace_bytes(int T, int V, int d, int dtype, bool grad);
 hipError_t launch_cross_entropy(const CrossEntropyArgs &a, int dtype, void *ws, hipStream_t s);
 
-// More than decode: tiles of both projections, behind a launch of the adapters'
-// terms where a.term is given (float32 needs it).
-bool gated_whole(int64_t M, int64_t Kd, int dtype, bool fused);   // tiles that finish themselves
+// More than decode: tiles of both projections that add the adapters' terms and
+// finish by themselves.
+bool gated_whole(int64_t M, int64_t Kd, int dtype, bool fused);   // whether they are taken
 hipError_t launch_gated(const GatedArgs &g, hipStream_t s);
 // Otherwise the base products, with the plan beside them if it fits (lds) ...
 constexpr int kTermSlots = 4;  // slots whose terms are kept apart, at most

@@ -1,4 +1,4 @@
-// The K loop of a bf16 output tile over two LDS stages, for the products of
+// The K loop of a bf16 output tile over two to four LDS stages, for the products of
 // the gated block (two weights side by side, or two products added along K)
 // and of the cross entropy (weights read along their other axis).
 // Internal to liblora (gfx950 only).
