@@ -648,3 +648,32 @@ def test_forward_of_wide_rows(T, K, d, F, dtype, N, mask):
 @pytest.mark.parametrize("mask", [False, True])
 def test_gradient_of_wide_rows(T, K, d, F, dtype, N, mask):
     G.check_grad(Block(T, K, d, F, dtype, N=N, seed=F, mask=mask, lo=0, hi=20), "silu")
+
+
+# ---------------------------------------------------------------- ranks and pools at their ends
+
+@pytest.mark.parametrize("T,K,d,F,dtype,N,lo,hi", [(5, 2, 64, 192, "bf16", 3, 1000, 1024), (150, 2, 64, 192, "bf16", 3, 500, 1024),
+                                                   (200, 2, 1600, 448, "bf16", 1, 257, 257), (300, 1, 64, 32576, "bf16", 2, 200, 260),
+                                                   (300, 2, 64, 32576, "bf16", 1, 65, 65), (70, 2, 128, 192, "f32", 2, 700, 1024),
+                                                   (40, 8, 64, 64, "bf16", 1, 1, 1), (8200, 1, 1536, 64, "bf16", 3, 100, 130)])
+def test_large_ranks_and_one_adapter(T, K, d, F, dtype, N, lo, hi):
+    b = Block(T, K, d, F, dtype, N=N, lo=lo, hi=hi, seed=hi, mask=True)
+    if T < 8000:
+        G.check_forward(b, "silu")
+    if F < 10000:
+        G.check_grad(b, "silu")
+
+
+@pytest.mark.parametrize("T,d,F,dtype", [(5, 128, 192, "bf16"), (200, 128, 192, "bf16"), (300, 64, 32576, "bf16"),
+                                         (8200, 1536, 64, "bf16"), (70, 64, 64, "f32")])
+def test_pools_without_pages(T, d, F, dtype):
+    """Every rank 0 and no page at all: the base products."""
+    b = Block(T, 2, d, F, dtype, N=3, lo=0, hi=0, seed=T)
+    t = DT[dtype]
+    none = [torch.empty(0, n, dtype=t, device="cuda") for n in (d, F)]
+    b.pools = [B.Pool(CODE[dtype], d, F, *none, b.d_rank, b.d_start, b.d_page_ids[:0], p.tensors[5]) for p in b.pools]
+    assert b.pools[0].desc.n_pages == 0 and not b.pools[0].desc.a_pages
+    if T < 8000:
+        G.check_forward(b, "silu")
+    if F < 10000:
+        G.check_grad(b, "silu")
