@@ -205,38 +205,70 @@ def test_several_blocks_of_tokens():
     assert not bool(loss[gone].any()) and not bool(dX[gone].any())
 
 
-@pytest.mark.parametrize("dtype,T", [("bf16", 40000), ("f32", 33100)])
-def test_several_blocks_of_wide_tokens(dtype, T):
-    """A small vocabulary under wide states: the blocks hold the sums of dX; the
-    reference by torch in 64 bits on the GPU."""
-    V, d = 300, 4096
-    n = B.lora_cross_entropy_workspace_bytes(T, V, d, CODE[dtype])
-    assert n < T * d * 4 < 700 << 20
+def check_on_gpu(X, W, y, w, loss, dX, tokens):
+    """The tokens' results against torch in 64 bits on the GPU, bounds as in `tolerances`."""
+    dtype = "bf16" if X.dtype == torch.bfloat16 else "f32"
+    (_, d), V, Wd, half = X.shape, W.shape[0], W.double(), HALF[dtype]
+    t = tokens[y[tokens] >= 0]
+    k, c = torch.arange(t.numel(), device="cuda"), y[t].long()
+    L = X[t].double() @ Wd.t()
+    e = (d + 8) * EPS * (X[t].double().abs() @ Wd.abs().t()) + 2 * EPS * (L.abs() + L[k, c].abs()[:, None]) + 2.0 ** -22
+    P = torch.softmax(L, 1)
+    wt = w[t].double()
+    ref = -wt * torch.log_softmax(L, 1)[k, c]
+    g = wt[:, None] * (P @ Wd - Wd[c])
+    P[k, c] = 0
+    shift = (P * e).sum(1) + (V + 4) * EPS * P.sum(1)
+    assert bool(((loss[t].double() - ref).abs() <= 1.02 * wt * shift + 4 * EPS * ref.abs() + 1e-37).all())
+    rel = half + (V + 8) * EPS + shift
+    tol = (P * (e + rel[:, None])) @ Wd.abs() + (P.sum(1) * (shift + e.max(1)[0] + rel))[:, None] * Wd[c].abs()
+    tol = 1.02 * wt[:, None] * tol
+    assert bool(((dX[t].double() - g).abs() <= tol + half * (g.abs() + tol) + 1e-37).all())
+
+
+def made_on_gpu(T, V, d, dtype, ignored):
     gen = torch.Generator("cuda").manual_seed(T)
     r = lambda *s: torch.randn(*s, generator=gen, device="cuda")
-    W = (r(V, d) * d ** -0.5).to(DT[dtype])
-    X, w = r(T, d).to(DT[dtype]), torch.rand(T, generator=gen, device="cuda") + 0.5
+    u = lambda: torch.rand(T, generator=gen, device="cuda")
+    W, X = (r(V, d) * d ** -0.5).to(DT[dtype]), (2 * r(T, d)).to(DT[dtype])
     y = torch.randint(0, V, (T,), generator=gen, device="cuda", dtype=torch.int32)
-    y[torch.rand(T, generator=gen, device="cuda") < 0.1] = -1
+    y[u() < ignored] = -1
+    return X, W, y, u() + 0.5
+
+
+@pytest.mark.parametrize("dtype,T", [("bf16", 40000), ("f32", 33100)])
+def test_several_blocks_of_wide_tokens(dtype, T):
+    """A small vocabulary under wide states: the blocks hold the sums of dX."""
+    V, d = 300, 4096
+    assert B.lora_cross_entropy_workspace_bytes(T, V, d, CODE[dtype]) < T * d * 4 < 700 << 20
+    X, W, y, w = made_on_gpu(T, V, d, dtype, 0.1)
     loss, dX = run(X, W, y, w)
-    Wd, half = W.double(), HALF[dtype]
     for t0 in (0, T // 2 - 500, T - 1000):
-        t = t0 + torch.nonzero(y[t0:t0 + 1000] >= 0)[:, 0]
-        k, c = torch.arange(t.numel(), device="cuda"), y[t].long()
-        L = X[t].double() @ Wd.t()
-        e = (d + 8) * EPS * (X[t].double().abs() @ Wd.abs().t()) + 2 * EPS * (L.abs() + L[k, c].abs()[:, None]) + 2.0 ** -22
-        P = torch.softmax(L, 1)
-        ref = -w[t].double() * torch.log_softmax(L, 1)[k, c]
-        Q = P.clone()
-        Q[k, c] = 0
-        shift = (Q * e).sum(1) + (V + 4) * EPS
-        assert bool(((loss[t].double() - ref).abs() <= 1.02 * w[t] * shift + 4 * EPS * ref.abs()).all())
-        g = w[t].double()[:, None] * (P @ Wd - Wd[c])
-        tol = 1.02 * w[t].double()[:, None] * ((Q * (e + half + (V + 8) * EPS + shift[:, None])) @ Wd.abs()
-                                               + (Q.sum(1) * (shift + e.max(1)[0] + half + (V + 8) * EPS))[:, None] * Wd[c].abs())
-        assert bool(((dX[t].double() - g).abs() <= tol + half * (g.abs() + tol)).all()), t0
+        check_on_gpu(X, W, y, w, loss, dX, torch.arange(t0, t0 + 1000, device="cuda"))
     gone = y < 0
     assert not bool(loss[gone].any()) and not bool(dX[gone].any())
+
+
+@pytest.mark.parametrize("dtype,T,V", [("bf16", 300, 1 << 22), ("f32", 70, (1 << 22) - 5), ("bf16", 1 << 20, 3),
+                                       ("f32", 1 << 20, 67), ("bf16", 7, 131077)])
+def test_largest_vocabulary_and_most_tokens(dtype, T, V):
+    X, W, y, w = made_on_gpu(T, V, 64, dtype, 0.2)
+    loss, dX = run(X, W, y, w)
+    n = min(T, 1000, (1 << 27) // V)
+    for t0 in (0, (T - n) // 2, T - n):
+        check_on_gpu(X, W, y, w, loss, dX, torch.arange(t0, t0 + n, device="cuda"))
+    gone = y < 0
+    assert not bool(loss[gone].any()) and not bool(dX[gone].any())
+    torch.cuda.empty_cache()
+
+
+# tiles of 192 x 256 and 256 x 256 with many splits, few, and none; the last columns a quarter of a tile
+@pytest.mark.parametrize("T,V,d", [(130, 20011, 4160), (192, 20011, 8256), (700, 8003, 8256), (1150, 3001, 8256),
+                                   (700, 3001, 6208), (250, 32003, 6208), (1000, 8003, 6208), (2000, 1001, 6208)])
+def test_second_products_tile_shapes(T, V, d):
+    X, W, y, w = made_on_gpu(T, V, d, "bf16", 0.05)
+    loss, dX = run(X, W, y, w)
+    check_on_gpu(X, W, y, w, loss, dX, torch.arange(T, device="cuda"))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
