@@ -665,7 +665,9 @@ int32_t lora_orthogonal_step(const lora_pool_desc *pool, const int32_t *adapters
  * another buffer of the call; X, weights, outputs and workspaces are 16-byte
  * aligned, keep_mask 8; widths up to 2^22.  lora_gated_forward = lora_plan then lora_gated_apply, as one call with
  * fewer launches: up to some thousand tokens the plan is built beside the base
- * products (plan, U, H, pre_gate and pre_up are the same bit for bit).
+ * products (the plan's arrays listed at lora_plan, U, H, pre_gate and pre_up are
+ * the same bit for bit; its internal parts may differ, and every later call takes
+ * either).
  * Errors: those of lora_apply and lora_forward. */
 #define LORA_ACT_SILU 0
 #define LORA_ACT_GELU 1
