@@ -663,11 +663,11 @@ int32_t lora_orthogonal_step(const lora_pool_desc *pool, const int32_t *adapters
  *                projection's U stays in its own, where lora_grad finds it.
  * Other arguments as for lora_apply.  No output, workspace or plan may overlap
  * another buffer of the call; X, weights, outputs and workspaces are 16-byte
- * aligned, keep_mask 8; widths up to 2^22.  lora_gated_forward = lora_plan then lora_gated_apply, as one call with
- * fewer launches: up to some thousand tokens the plan is built beside the base
- * products (the plan's arrays listed at lora_plan, U, H, pre_gate and pre_up are
- * the same bit for bit; its internal parts may differ, and every later call takes
- * either).
+ * aligned, keep_mask 8; widths up to 2^22.
+ * lora_gated_forward = lora_plan then lora_gated_apply, as one call with fewer
+ * launches: up to some thousand tokens the plan is built beside the base products
+ * (the plan's arrays listed at lora_plan, U, H, pre_gate and pre_up are the same
+ * bit for bit; its internal parts may differ, and every later call takes either).
  * Errors: those of lora_apply and lora_forward. */
 #define LORA_ACT_SILU 0
 #define LORA_ACT_GELU 1
@@ -697,7 +697,7 @@ int32_t lora_gated_forward(const int32_t *ids, const float *gates, int32_t T, in
  *   forward; max_rank bounds every used adapter's rank (LORA_DEVERR_CAPACITY if
  *   not); d_gate, d_up [T][d_out] dtype, may be pre_gate, pre_up (in place); dX
  *   [T][d_in] dtype, or NULL.  ws >= lora_gated_grad_workspace_bytes(...).
- *   No output or workspace otherwise overlaps another buffer of the call.
+ *   No output, workspace or plan otherwise overlaps another buffer of the call.
  *   16-byte aligned, keep_mask 8; widths up to 2^22.
  * Errors: INVALID_ARG, UNSUPPORTED, CAPACITY, DEVICE. */
 size_t lora_gated_grad_workspace_bytes(int32_t T, int32_t K, int32_t d_in, int32_t d_out,
